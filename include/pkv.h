@@ -78,6 +78,9 @@ enum pkv_status {
 #define PKV_FLAG_OUT_RANGE 16  /* pkv_gather: a row beyond out_rows */
 #define PKV_FLAG_GROUP_RANGE 32 /* pkv_decode_attn_prefix: a group or prefix beyond its declared
                                    bound, or a member shorter than its group's prefix */
+#define PKV_FLAG_TOKEN_RANGE 64 /* pkv_verify_draft: a drafted token outside [0, vocab_size) or a
+                                   draft length outside [0, num_draft] */
+#define PKV_FLAG_NO_MASS 128    /* pkv_verify_draft: no probability to draw a token from */
 
 typedef struct {
     int32_t num_blocks;   /* physical blocks in each pool */
@@ -470,6 +473,161 @@ int pkv_decode_step_prefix(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_b
                            int64_t *slot_mapping_out, pkv_cache_desc cache, int32_t partition_blocks,
                            int32_t prefix_partition_blocks, void *workspace, size_t workspace_bytes,
                            int32_t *err_flag, pkv_stream_t stream);
+
+/*
+ * ---- rotary position embedding with the append -------------------------------------------------
+ * A model with rotary positions turns each query and key by its position's angles before attention;
+ * the cache holds turned keys.  These calls turn a step's queries and keys and write the keys and
+ * values into their slots in one pass.  A token at position P turns the element pairs j < R / 2 of
+ * every head of q and k_new by the angle P * inv_freq[j]:
+ *     a' = a cos - b sin,   b' = a sin + b cos,
+ * pair j being the elements (j, j + R / 2), or (2j, 2j + 1) with interleaved != 0; the elements from
+ * R = rotary_dim on are copied (R a multiple of 16, at most H; H a multiple of 16, at most 256).
+ * inv_freq double [R / 2] (device; any scaling of the frequencies is the caller's): the angle is
+ * reduced in 64 bits, so far positions lose nothing, and the rotation computed in fp32 and rounded
+ * once, to bf16 or to e4m3.  v_new is not turned.  q_out [tokens][N][H] receives the turned queries
+ * and may be q itself (in place), but not overlap it otherwise.  A token without a slot (below) is
+ * left out: nothing is written for it, q_out included.  q, k_new, v_new, q_out and the pools are
+ * 16-byte aligned (e4m3 pools 8-byte).
+ */
+
+/* Slots and positions given (prompts, any mixture of sequences): token i goes to slot_mapping[i]
+   (int64, negative: left out; beyond the pool: PKV_FLAG_SLOT_RANGE, left out) and sits at
+   positions[i] (int32).  Slots within one call must be distinct. */
+int pkv_rope_append(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                    const int32_t *positions, const double *inv_freq, int32_t rotary_dim,
+                    int32_t interleaved, const int64_t *slot_mapping, int32_t num_tokens,
+                    int32_t num_q_heads, pkv_bf16 *k_cache, pkv_bf16 *v_cache, pkv_bf16 *q_out,
+                    pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream);
+
+/* The same into e4m3 pools, quantized as pkv_append_fp8 does (the turned key straight from fp32). */
+int pkv_rope_append_fp8(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                        const int32_t *positions, const double *inv_freq, int32_t rotary_dim,
+                        int32_t interleaved, const float *k_scale, const float *v_scale,
+                        int32_t scale_block_stride, const int64_t *slot_mapping, int32_t num_tokens,
+                        int32_t num_q_heads, uint8_t *k_cache, uint8_t *v_cache, pkv_bf16 *q_out,
+                        pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream);
+
+/* The num_new (>= 1) newest tokens of each sequence (context_lens counts them, as in
+   pkv_decode_attn_multi; 1 is the ordinary decode step): token t of sequence b sits at position
+   ctx - num_new + t and goes to that position's slot, which slot_mapping_out int64 [num_seqs][num_new]
+   receives (the values and flags of pkv_slot_mapping_multi; -1: left out). */
+int pkv_rope_append_multi(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *context_lens, const double *inv_freq, int32_t rotary_dim,
+                          int32_t interleaved, int32_t num_seqs, int32_t num_new, int32_t num_q_heads,
+                          pkv_bf16 *k_cache, pkv_bf16 *v_cache, pkv_bf16 *q_out,
+                          int64_t *slot_mapping_out, pkv_cache_desc cache, int32_t *err_flag,
+                          pkv_stream_t stream);
+
+int pkv_rope_append_multi_fp8(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, const double *inv_freq, int32_t rotary_dim,
+                              int32_t interleaved, const float *k_scale, const float *v_scale,
+                              int32_t scale_block_stride, int32_t num_seqs, int32_t num_new,
+                              int32_t num_q_heads, uint8_t *k_cache, uint8_t *v_cache, pkv_bf16 *q_out,
+                              int64_t *slot_mapping_out, pkv_cache_desc cache, int32_t *err_flag,
+                              pkv_stream_t stream);
+
+/*
+ * ---- attention over selected blocks ------------------------------------------------------------
+ * A long context is attended to in part: a cheap upper bound says which blocks can hold large logits
+ * for this step's query, and attention reads those blocks alone.
+ */
+
+/* Bounds of the keys: key_bounds bf16 [num_blocks][K][2][H] (16-byte aligned), row 0 the minimum and
+   row 1 the maximum of each element over the block's tokens within the context.  One pair per physical
+   block, so blocks shared by sequences share it.  Rebuilds the bounds of every block that holds one of a
+   sequence's last num_new tokens from the keys in the cache: num_new = 1 (or the step's T) after a decode
+   step's append, at least the longest context after a prompt or a copy-on-write.  A NaN key makes its
+   element's bounds NaN.  H a multiple of 8 (e4m3: 16). */
+int pkv_key_bounds(const pkv_bf16 *k_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                   const int32_t *context_lens, int32_t num_seqs, int32_t num_new, pkv_bf16 *key_bounds,
+                   pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream);
+
+/* The same for an e4m3 pool: bounds of code * scale, rounded to the nearest bf16 (a bound may lie half a
+   bf16 step inside the keys it bounds). */
+int pkv_key_bounds_fp8(const uint8_t *k_cache, const float *k_scale, int32_t scale_block_stride,
+                       const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                       int32_t num_seqs, int32_t num_new, pkv_bf16 *key_bounds, pkv_cache_desc cache,
+                       int32_t *err_flag, pkv_stream_t stream);
+
+/* Workspace of pkv_select_blocks, 256-byte aligned and ZEROED BEFORE ITS FIRST USE (each call leaves its
+   counters at zero again; calls that share a workspace must not overlap on the GPU). */
+size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq);
+
+/* The blocks each (sequence, KV head) attends to.  score(b, kvh, j) = the largest, over the G query heads
+   of KV head kvh, of sum_h max(q_h lo_jh, q_h hi_jh): no q . k of block j exceeds it.  selected int32
+   [num_seqs][K][max_selected] receives logical block indices in ascending order: all of a sequence's blocks
+   if it has no more than max_selected; else its first first_blocks and last last_blocks blocks, which need
+   no bounds, and the best scored of the others, max_selected in all -- exactly those that the scores' real
+   values choose, ties to the lowest index (a NaN score counts as the largest).  Entries behind a sequence's
+   blocks are -1.  q bf16 [num_seqs][N][H] (16-byte aligned) as attention takes it, for a positive softmax
+   scale.  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE and scores -inf.  H in {64, 128},
+   G in {1, 2, 4, 8}, first_blocks + last_blocks <= max_selected. */
+int pkv_select_blocks(const pkv_bf16 *q, const pkv_bf16 *key_bounds, const int32_t *block_tables,
+                      int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                      int32_t num_q_heads, int32_t first_blocks, int32_t last_blocks, int32_t max_selected,
+                      int32_t *selected, pkv_cache_desc cache, void *workspace, size_t workspace_bytes,
+                      int32_t *err_flag, pkv_stream_t stream);
+
+/* Decode attention (one token per sequence) over selected blocks: the query heads of KV head kvh attend to
+   the tokens of the logical blocks selected[b][kvh][0 .. n), n = min(ceil(ctx / 16), max_selected), in any
+   order; entries from n on are not read.  An entry -1 is skipped; one outside the sequence's blocks, or whose
+   block id is outside the pool, is skipped and sets PKV_FLAG_BLOCK_RANGE; an entry that appears twice counts
+   twice.  Nothing to attend to gives out 0, lse -inf.  partition_blocks 0: one CTA per (sequence, KV head);
+   > 0: the list is cut into partitions of that many entries, max_partitions >= ceil(max_selected /
+   partition_blocks), G * max_partitions <= 8192, merged by log-sum-exp in the same launch, with a workspace of
+   pkv_splitk_workspace_bytes(num_seqs, N, H, max_partitions) bytes under its rules.  Other arguments and
+   alignments as pkv_decode_attn_splitk. */
+int pkv_decode_attn_blocks(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *selected, int32_t max_selected,
+                           int32_t num_seqs, int32_t num_q_heads, float scale, pkv_bf16 *out,
+                           float *lse_out, pkv_cache_desc cache, int32_t partition_blocks,
+                           int32_t max_partitions, void *workspace, size_t workspace_bytes,
+                           int32_t *err_flag, pkv_stream_t stream);
+
+/* The same over e4m3 pools (q 8-byte aligned), scales as in pkv_decode_attn_fp8. */
+int pkv_decode_attn_blocks_fp8(const pkv_bf16 *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                               const float *k_scale, const float *v_scale, int32_t scale_block_stride,
+                               const int32_t *block_tables, int32_t max_blocks_per_seq,
+                               const int32_t *context_lens, const int32_t *selected, int32_t max_selected,
+                               int32_t num_seqs, int32_t num_q_heads, float scale, pkv_bf16 *out,
+                               float *lse_out, pkv_cache_desc cache, int32_t partition_blocks,
+                               int32_t max_partitions, void *workspace, size_t workspace_bytes,
+                               int32_t *err_flag, pkv_stream_t stream);
+
+/*
+ * ---- verification of drafted tokens ------------------------------------------------------------
+ * What follows a multi-token step's attention ("Week 11. Inference", Step 3): the target model's
+ * probabilities at the T + 1 positions decide how many of the T = num_draft drafted tokens stand.
+ */
+
+/* Workspace of pkv_verify_draft, 256-byte aligned and ZEROED BEFORE ITS FIRST USE (as above). */
+size_t pkv_verify_workspace_bytes(int32_t num_seqs, int32_t vocab_size);
+
+/* Drafted token x_t = draft_tokens[b][t] stands while accept_u[b][t] * q_t(x_t) < p_t(x_t) (the products
+   exact); at the first refusal t the next token is drawn from max(p_t - q_t, 0), and where all stand from
+   p_T': the first index whose running sum of those weights exceeds sample_u[b] times their total (sums
+   exact to 2^-44, so the draw does not depend on how the work is split; a residual without mass, possible
+   only for rows that are no distributions, falls back to p_t).  target_probs [num_seqs][T + 1] rows of
+   target_stride elements, draft_probs [num_seqs][T] rows of draft_stride, fp32 (prob_bf16 = 0) or bf16;
+   rows hold vocab_size values in [0, 1] (others are clamped, NaN counts as 0) and need not be normalised.
+   draft_probs NULL: a draft without probabilities, q_t one-hot at x_t.  draft_lens int32 [num_seqs]
+   (nullable: T everywhere): the drafted tokens a sequence has, T' = draft_lens[b]; what lies behind them is
+   not read.  accept_u, sample_u in [0, 1).  num_accepted int32 [num_seqs]; tokens_out int32
+   [num_seqs][T + 1]: the accepted tokens, the drawn one, then -1.  context_lens / context_lens_out int32
+   [num_seqs] (both or neither; may be one array): a context that counts the T' drafted tokens becomes the
+   one that keeps the accepted ones, ctx - T' + num_accepted.  A drafted token outside the vocabulary is
+   refused and sets PKV_FLAG_TOKEN_RANGE; a row without mass gives token -1 and PKV_FLAG_NO_MASS.
+   vocab_size up to 2^19 - 1, num_draft 0 to 1024. */
+int pkv_verify_draft(const void *target_probs, int64_t target_stride, const void *draft_probs,
+                     int64_t draft_stride, int32_t prob_bf16, const int32_t *draft_tokens,
+                     const int32_t *draft_lens, const float *accept_u, const float *sample_u,
+                     int32_t num_seqs, int32_t num_draft, int32_t vocab_size, int32_t *num_accepted,
+                     int32_t *tokens_out, const int32_t *context_lens, int32_t *context_lens_out,
+                     void *workspace, size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
 
 /* Synchronise the stream, copy *err_flag to *host_value; PKV_ERR_RANGE if it is non-zero. */
 int pkv_read_err_flag(const int32_t *err_flag, int32_t *host_value, pkv_stream_t stream);

@@ -42,6 +42,8 @@ PKV_FLAG_CTX_RANGE = 4
 PKV_FLAG_TIMEOUT = 8
 PKV_FLAG_OUT_RANGE = 16
 PKV_FLAG_GROUP_RANGE = 32
+PKV_FLAG_TOKEN_RANGE = 64
+PKV_FLAG_NO_MASS = 128
 
 BLOCK_SIZE = 16
 
@@ -109,7 +111,7 @@ def _stream(stream):
 # The pools and the workspaces must be device memory (the pools are read by TMA).  Every other
 # argument may also be pinned (page-locked) host memory, which the kernels read and write in place
 # (on a GB300 over NVLink-C2C) -- a step's inputs and outputs need no copies then.
-_DEVICE_ONLY = ("k_cache", "v_cache", "workspace", "part_out", "part_lse")
+_DEVICE_ONLY = ("k_cache", "v_cache", "workspace", "part_out", "part_lse", "key_bounds", "k_scale", "v_scale")
 
 
 def _need(t, dtype, ndim, name):
@@ -679,3 +681,287 @@ def pkv_decode_attn_splitk_noalloc(q, k_cache, v_cache, block_tables, context_le
                                                float(scale), _ptr(out), _ptr(lse_out),
                                                cache_desc(k_cache), partition_blocks, max_partitions,
                                                _ptr(err_flag), _stream(stream))
+
+
+# ------------------------- the operators around a step's attention -------------------------
+# A step makes several of these calls and some run for a few microseconds, so their arguments are checked
+# in one expression per tensor; what it does not accept goes to _refuse, which names the fault (or accepts
+# pinned host memory).  Addresses go to ctypes as integers.
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(stream, dev: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _arg(t, dtype, shape, name: str, dev: int) -> int:
+    """The address of a contiguous tensor of this type and shape on the current device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, dtype, shape, name, dev)
+
+
+def _refuse(t, dtype, shape, name: str, dev: int) -> int:
+    _need(t, dtype, len(shape), name)  # not a tensor, another type, not contiguous, not on a GPU or pinned
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _maybe(t, dtype, shape, name: str, dev: int):
+    return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _shape(t, ndim: int, name: str):
+    """The shape of a tensor that sets the sizes of the others."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _scale_args(k_scale, v_scale, nb: int, K: int, dev: int):
+    """Addresses of the scales and their stride: 0 for [K], K for [num_blocks, K]."""
+    per_block = _shape(k_scale, k_scale.dim() if isinstance(k_scale, torch.Tensor) else 1, "k_scale")
+    shape = (nb, K) if len(per_block) == 2 else (K,)
+    return (_arg(k_scale, torch.float32, shape, "k_scale", dev), _arg(v_scale, torch.float32, shape, "v_scale", dev),
+            K if len(shape) == 2 else 0)
+
+
+_bf16, _u8, _i32, _i64, _f32 = torch.bfloat16, torch.uint8, torch.int32, torch.int64, torch.float32
+_FLAG = (1,)
+
+# ------------------------------ rotary positions with the append ------------------------------
+_lib.pkv_rope_append.argtypes = [_P, _P, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _P, _P, _P, CacheDesc, _P, _P]
+_lib.pkv_rope_append_fp8.argtypes = [_P, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P,
+                                     CacheDesc, _P, _P]
+_lib.pkv_rope_append_multi.argtypes = [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                       CacheDesc, _P, _P]
+_lib.pkv_rope_append_multi_fp8.argtypes = [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                                           _P, _P, _P, _P, CacheDesc, _P, _P]
+
+
+def _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, pool, lead: int, dev: int):
+    """(q, k_new, v_new, q_out, k_cache, v_cache, inv_freq) addresses, rotary_dim, N, cache descriptor."""
+    qs, cs = _shape(q, lead + 2, "q"), _shape(k_cache, 4, "k_cache")
+    nb, bs, K, H = cs
+    new = (*qs[:lead], K, H)
+    half = _shape(inv_freq, 1, "inv_freq")[0]
+    if qs[-1] != H:
+        raise ValueError("q [.., N, H] and the pools [num_blocks, 16, K, H] differ in head_dim")
+    qp, op = _arg(q, _bf16, qs, "q", dev), _arg(q_out, _bf16, qs, "q_out", dev)
+    if op != qp and abs(op - qp) < 2 * q.numel():
+        raise ValueError("q_out may be q itself, but not overlap it")
+    return (qp, _arg(k_new, _bf16, new, "k_new", dev), _arg(v_new, _bf16, new, "v_new", dev), op,
+            _arg(k_cache, pool, cs, "k_cache", dev), _arg(v_cache, pool, cs, "v_cache", dev),
+            _arg(inv_freq, torch.float64, (half,), "inv_freq", dev), 2 * half, qs[-2], CacheDesc(nb, bs, K, H))
+
+
+def pkv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache, v_cache, q_out,
+                    interleaved: bool = False, err_flag=None, stream=None) -> int:
+    """q, q_out [T, N, H], k_new, v_new [T, K, H] bf16; positions int32 [T]; slot_mapping int64 [T];
+    inv_freq float64 [rotary_dim / 2]: q turned into q_out (or in place), k_new turned and v_new
+    written into their slots."""
+    dev = _current_device()
+    qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _bf16, 1, dev)
+    n = q.shape[0]
+    return _lib.pkv_rope_append(qp, kp, vp, _arg(positions, _i32, (n,), "positions", dev), fp, R, interleaved,
+                                _arg(slot_mapping, _i64, (n,), "slot_mapping", dev), n, N, kc, vc, op, desc,
+                                _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_rope_append_fp8(q, k_new, v_new, positions, inv_freq, k_scale, v_scale, slot_mapping, k_cache, v_cache,
+                        q_out, interleaved: bool = False, err_flag=None, stream=None) -> int:
+    """pkv_rope_append into e4m3 pools (uint8) with scales [K] or [num_blocks, K]."""
+    dev = _current_device()
+    qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _u8, 1, dev)
+    ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
+    n = q.shape[0]
+    return _lib.pkv_rope_append_fp8(qp, kp, vp, _arg(positions, _i32, (n,), "positions", dev), fp, R, interleaved, ks,
+                                    vs, stride, _arg(slot_mapping, _i64, (n,), "slot_mapping", dev), n, N, kc, vc, op,
+                                    desc, _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def _table_args(block_tables, context_lens, B: int, dev: int):
+    width = _shape(block_tables, 2, "block_tables")[1]
+    return (_arg(block_tables, _i32, (B, width), "block_tables", dev), width,
+            _arg(context_lens, _i32, (B,), "context_lens", dev))
+
+
+def pkv_rope_append_multi(q, k_new, v_new, block_tables, context_lens, inv_freq, k_cache, v_cache, q_out,
+                          slot_mapping, interleaved: bool = False, err_flag=None, stream=None) -> int:
+    """The T newest tokens of each sequence: q, q_out bf16 [B, T, N, H]; k_new, v_new [B, T, K, H];
+    slot_mapping int64 [B, T] (written)."""
+    dev = _current_device()
+    qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _bf16, 2, dev)
+    B, T = q.shape[:2]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    return _lib.pkv_rope_append_multi(qp, kp, vp, tp, width, cp, fp, R, interleaved, B, T, N, kc, vc, op,
+                                      _arg(slot_mapping, _i64, (B, T), "slot_mapping", dev), desc,
+                                      _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_rope_append_multi_fp8(q, k_new, v_new, block_tables, context_lens, inv_freq, k_scale, v_scale, k_cache,
+                              v_cache, q_out, slot_mapping, interleaved: bool = False, err_flag=None,
+                              stream=None) -> int:
+    """pkv_rope_append_multi into e4m3 pools (uint8) with scales [K] or [num_blocks, K]."""
+    dev = _current_device()
+    qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _u8, 2, dev)
+    ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
+    B, T = q.shape[:2]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    return _lib.pkv_rope_append_multi_fp8(qp, kp, vp, tp, width, cp, fp, R, interleaved, ks, vs, stride, B, T, N, kc,
+                                          vc, op, _arg(slot_mapping, _i64, (B, T), "slot_mapping", dev), desc,
+                                          _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+# ------------------------------ attention over selected blocks --------------------------------
+_lib.pkv_key_bounds.argtypes = [_P, _P, _I32, _P, _I32, _I32, _P, CacheDesc, _P, _P]
+_lib.pkv_key_bounds_fp8.argtypes = [_P, _P, _I32, _P, _I32, _P, _I32, _I32, _P, CacheDesc, _P, _P]
+_lib.pkv_select_workspace_bytes.argtypes = [_I32, _I32, _I32]
+_lib.pkv_select_workspace_bytes.restype = ctypes.c_size_t
+_lib.pkv_select_blocks.argtypes = [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P, CacheDesc, _P,
+                                   ctypes.c_size_t, _P, _P]
+_lib.pkv_decode_attn_blocks.argtypes = [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P,
+                                        CacheDesc, _I32, _I32, _P, ctypes.c_size_t, _P, _P]
+_lib.pkv_decode_attn_blocks_fp8.argtypes = [_P, _P, _P, _P, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32,
+                                            ctypes.c_float, _P, _P, CacheDesc, _I32, _I32, _P, ctypes.c_size_t, _P,
+                                            _P]
+
+
+def _bounds_args(k_cache, pool, block_tables, context_lens, key_bounds, dev: int):
+    cs, B = _shape(k_cache, 4, "k_cache"), _shape(context_lens, 1, "context_lens")[0]
+    nb, bs, K, H = cs
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    return (_arg(k_cache, pool, cs, "k_cache", dev), tp, width, cp, B,
+            _arg(key_bounds, _bf16, (nb, K, 2, H), "key_bounds", dev), CacheDesc(nb, bs, K, H))
+
+
+def pkv_key_bounds(k_cache, block_tables, context_lens, num_new: int, key_bounds, err_flag=None, stream=None) -> int:
+    """key_bounds bf16 [num_blocks, K, 2, H]: minimum and maximum of the keys of every block that holds
+    one of a sequence's last num_new tokens."""
+    dev = _current_device()
+    kc, tp, width, cp, B, bp, desc = _bounds_args(k_cache, _bf16, block_tables, context_lens, key_bounds, dev)
+    return _lib.pkv_key_bounds(kc, tp, width, cp, B, num_new, bp, desc,
+                               _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_key_bounds_fp8(k_cache, k_scale, block_tables, context_lens, num_new: int, key_bounds, err_flag=None,
+                       stream=None) -> int:
+    """pkv_key_bounds of an e4m3 pool (uint8) with scales [K] or [num_blocks, K]."""
+    dev = _current_device()
+    kc, tp, width, cp, B, bp, desc = _bounds_args(k_cache, _u8, block_tables, context_lens, key_bounds, dev)
+    ks, _, stride = _scale_args(k_scale, k_scale, desc.num_blocks, desc.num_kv_heads, dev)
+    return _lib.pkv_key_bounds_fp8(kc, ks, stride, tp, width, cp, B, num_new, bp, desc,
+                                   _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_select_workspace_bytes(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int) -> int:
+    return int(_lib.pkv_select_workspace_bytes(num_seqs, num_kv_heads, max_blocks_per_seq))
+
+
+def pkv_select_blocks(q, key_bounds, block_tables, context_lens, selected, workspace, first_blocks: int = 1,
+                      last_blocks: int = 1, err_flag=None, stream=None) -> int:
+    """selected int32 [B, K, M]: the logical blocks each (sequence, KV head) attends to, ascending, -1
+    behind them.  workspace: pkv_select_workspace_bytes(B, K, max_blocks) bytes, zeroed before its
+    first use."""
+    dev = _current_device()
+    qs, (nb, K, _, H) = _shape(q, 3, "q"), _shape(key_bounds, 4, "key_bounds")
+    B, N, _ = qs
+    M, size = _shape(selected, 3, "selected")[2], _shape(workspace, 1, "workspace")[0]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    return _lib.pkv_select_blocks(_arg(q, _bf16, (B, N, H), "q", dev),
+                                  _arg(key_bounds, _bf16, (nb, K, 2, H), "key_bounds", dev), tp, width, cp, B, N,
+                                  first_blocks, last_blocks, M, _arg(selected, _i32, (B, K, M), "selected", dev),
+                                  CacheDesc(nb, BLOCK_SIZE, K, H), _arg(workspace, _u8, (size,), "workspace", dev),
+                                  size, _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def _blocks_args(q, k_cache, v_cache, pool, block_tables, context_lens, selected, out, lse_out, workspace, dev: int):
+    qs, cs = _shape(q, 3, "q"), _shape(k_cache, 4, "k_cache")
+    B, N, _ = qs
+    nb, bs, K, H = cs
+    M = _shape(selected, 3, "selected")[2]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    size = 0 if workspace is None else _shape(workspace, 1, "workspace")[0]
+    return (_arg(q, _bf16, (B, N, H), "q", dev), _arg(k_cache, pool, cs, "k_cache", dev),
+            _arg(v_cache, pool, cs, "v_cache", dev), tp, width, cp,
+            _arg(selected, _i32, (B, K, M), "selected", dev), M, B, N, _arg(out, _bf16, qs, "out", dev),
+            _maybe(lse_out, _f32, (B, N), "lse_out", dev), CacheDesc(nb, bs, K, H),
+            _maybe(workspace, _u8, (size,), "workspace", dev), size)
+
+
+def pkv_decode_attn_blocks(q, k_cache, v_cache, block_tables, context_lens, selected, scale: float, out,
+                           lse_out=None, partition_blocks: int = 0, max_partitions: int = 0, workspace=None,
+                           err_flag=None, stream=None) -> int:
+    """Decode attention of each KV head's query group over the logical blocks selected [B, K, M]."""
+    dev = _current_device()
+    qp, kc, vc, tp, width, cp, sp, M, B, N, op, lp, desc, ws, size = _blocks_args(
+        q, k_cache, v_cache, _bf16, block_tables, context_lens, selected, out, lse_out, workspace, dev)
+    return _lib.pkv_decode_attn_blocks(qp, kc, vc, tp, width, cp, sp, M, B, N, scale, op, lp, desc, partition_blocks,
+                                       max_partitions, ws, size, _maybe(err_flag, _i32, _FLAG, "err_flag", dev),
+                                       _launch(stream, dev))
+
+
+def pkv_decode_attn_blocks_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected,
+                               scale: float, out, lse_out=None, partition_blocks: int = 0, max_partitions: int = 0,
+                               workspace=None, err_flag=None, stream=None) -> int:
+    """pkv_decode_attn_blocks over e4m3 pools (uint8) with scales [K] or [num_blocks, K]."""
+    dev = _current_device()
+    qp, kc, vc, tp, width, cp, sp, M, B, N, op, lp, desc, ws, size = _blocks_args(
+        q, k_cache, v_cache, _u8, block_tables, context_lens, selected, out, lse_out, workspace, dev)
+    ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
+    return _lib.pkv_decode_attn_blocks_fp8(qp, kc, vc, ks, vs, stride, tp, width, cp, sp, M, B, N, scale, op, lp, desc,
+                                           partition_blocks, max_partitions, ws, size,
+                                           _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+# ------------------------------ verification of drafted tokens --------------------------------
+_lib.pkv_verify_workspace_bytes.argtypes = [_I32, _I32]
+_lib.pkv_verify_workspace_bytes.restype = ctypes.c_size_t
+_lib.pkv_verify_draft.argtypes = [_P, _I64, _P, _I64, _I32, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P,
+                                  ctypes.c_size_t, _P, _P]
+
+
+def pkv_verify_workspace_bytes(num_seqs: int, vocab_size: int) -> int:
+    return int(_lib.pkv_verify_workspace_bytes(num_seqs, vocab_size))
+
+
+def pkv_verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u, num_accepted, tokens_out,
+                     workspace, draft_lens=None, context_lens=None, context_lens_out=None,
+                     vocab_size: int | None = None, err_flag=None, stream=None) -> int:
+    """target_probs [B, T + 1, Vs], draft_probs [B, T, Vs'] (None: one-hot drafts), both float32 or bf16,
+    of which the first vocab_size columns count (default: all of target_probs'); draft_tokens int32 and
+    accept_u float32 [B, T]; sample_u float32 [B]; num_accepted int32 [B] and tokens_out int32 [B, T + 1]
+    (written); draft_lens, context_lens, context_lens_out int32 [B]."""
+    dev = _current_device()
+    B, rows, width = _shape(target_probs, 3, "target_probs")
+    T, dtype = rows - 1, target_probs.dtype
+    if dtype is not _f32 and dtype is not _bf16:
+        raise TypeError(f"target_probs must be float32 or bfloat16, got {dtype}")
+    V = width if vocab_size is None else int(vocab_size)
+    wide = V if draft_probs is None else _shape(draft_probs, 3, "draft_probs")[2]
+    if V > width or V > wide:
+        raise ValueError(f"vocab_size {V} exceeds the columns of target_probs or draft_probs")
+    size = _shape(workspace, 1, "workspace")[0]
+    return _lib.pkv_verify_draft(_arg(target_probs, dtype, (B, rows, width), "target_probs", dev), width,
+                                 _maybe(draft_probs, dtype, (B, T, wide), "draft_probs", dev), wide, dtype is _bf16,
+                                 _arg(draft_tokens, _i32, (B, T), "draft_tokens", dev),
+                                 _maybe(draft_lens, _i32, (B,), "draft_lens", dev),
+                                 _arg(accept_u, _f32, (B, T), "accept_u", dev),
+                                 _arg(sample_u, _f32, (B,), "sample_u", dev), B, T, V,
+                                 _arg(num_accepted, _i32, (B,), "num_accepted", dev),
+                                 _arg(tokens_out, _i32, (B, rows), "tokens_out", dev),
+                                 _maybe(context_lens, _i32, (B,), "context_lens", dev),
+                                 _maybe(context_lens_out, _i32, (B,), "context_lens_out", dev),
+                                 _arg(workspace, _u8, (size,), "workspace", dev), size,
+                                 _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))

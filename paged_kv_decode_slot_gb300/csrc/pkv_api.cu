@@ -10,6 +10,7 @@
 
 #include "pkv.h"
 #include "pkv_internal.h"
+#include "pkv_ops.h"
 
 #define PKV_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -1199,4 +1200,384 @@ PKV_EXPORT int pkv_decode_step_prefix(const pkv_bf16 *q, const pkv_bf16 *k_new, 
     return prefix_attention(a, group_starts, prefix_blocks, num_groups, max_group_size, max_prefix_blocks,
                             k_new, v_new, k_cache, v_cache, slot_mapping_out, out, lse_out, partition_blocks,
                             prefix_partition_blocks, workspace, workspace_bytes, stream);
+}
+
+// ---- rotary position embedding with the append ----------------------------------------------
+namespace {
+
+int check_scale_stride(int32_t stride, const pkv_cache_desc &d)
+{
+    return stride == 0 || stride == d.num_kv_heads ? PKV_OK : PKV_ERR_SHAPE;
+}
+
+// The part of a rotating append that does not depend on how its slots are given.
+int rope_append(pkv::RopeParams &p, bool interleaved, bool fp8, const pkv_cache_desc &d, int32_t num_q_heads,
+                int32_t rotary_dim, int64_t tokens, cudaStream_t stream)
+{
+    if (!p.q || !p.k_new || !p.v_new || !p.q_out || !p.k_cache || !p.v_cache || !p.inv_freq) return PKV_ERR_NULL;
+    if (fp8 && (!p.k_scale || !p.v_scale)) return PKV_ERR_NULL;
+    int st = check_copy_desc(d);
+    if (st != PKV_OK) return st;
+    if (num_q_heads <= 0 || rotary_dim <= 0 || rotary_dim > d.head_dim || tokens < 0) return PKV_ERR_SHAPE;
+    if (d.head_dim % 16 != 0 || d.head_dim > 256 || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (fp8 && check_scale_stride(p.scale_stride, d) != PKV_OK) return PKV_ERR_SHAPE;
+    // head offsets inside a token are 32-bit; the grid has one CTA per token
+    if (((int64_t)num_q_heads + 2 * (int64_t)d.num_kv_heads) * d.head_dim > INT32_MAX / 2 || tokens > INT32_MAX)
+        return PKV_ERR_SHAPE;
+    const uintptr_t pool = fp8 ? 8 : 16;
+    if (!aligned(p.q, 16) || !aligned(p.k_new, 16) || !aligned(p.v_new, 16) || !aligned(p.q_out, 16) ||
+        !aligned(p.k_cache, pool) || !aligned(p.v_cache, pool) || !aligned(p.inv_freq, 8) ||
+        !aligned(p.k_scale, 4) || !aligned(p.v_scale, 4) || !aligned(p.slots, 8) || !aligned(p.slots_out, 8))
+        return PKV_ERR_ALIGN;
+    if (tokens == 0) return PKV_OK;
+    p.R = rotary_dim;
+    p.n = tokens;
+    p.N = num_q_heads;
+    p.K = d.num_kv_heads;
+    p.H = d.head_dim;
+    p.num_blocks = d.num_blocks;
+    cudaError_t e = pkv::launch_rope_append(p, interleaved, fp8, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "rope append launch");
+}
+
+int rope_append_slots(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new, const int32_t *positions,
+                      const double *inv_freq, int32_t rotary_dim, int32_t interleaved, const float *k_scale,
+                      const float *v_scale, int32_t scale_stride, const int64_t *slot_mapping, int32_t num_tokens,
+                      int32_t num_q_heads, void *k_cache, void *v_cache, pkv_bf16 *q_out, const pkv_cache_desc &cache,
+                      int32_t *err_flag, bool fp8, cudaStream_t stream)
+{
+    if (!positions || !slot_mapping) return PKV_ERR_NULL;
+    pkv::RopeParams p{};
+    p.q = q, p.k_new = k_new, p.v_new = v_new, p.q_out = q_out;
+    p.k_cache = k_cache, p.v_cache = v_cache;
+    p.k_scale = k_scale, p.v_scale = v_scale, p.scale_stride = scale_stride;
+    p.inv_freq = inv_freq;
+    p.positions = positions, p.slots = slot_mapping;
+    p.err_flag = err_flag;
+    return rope_append(p, interleaved != 0, fp8, cache, num_q_heads, rotary_dim, num_tokens, stream);
+}
+
+int rope_append_tables(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new, const int32_t *block_tables,
+                       int32_t max_nb, const int32_t *context_lens, const double *inv_freq, int32_t rotary_dim,
+                       int32_t interleaved, const float *k_scale, const float *v_scale, int32_t scale_stride,
+                       int32_t num_seqs, int32_t num_new, int32_t num_q_heads, void *k_cache, void *v_cache,
+                       pkv_bf16 *q_out, int64_t *slot_mapping_out, const pkv_cache_desc &cache, int32_t *err_flag,
+                       bool fp8, cudaStream_t stream)
+{
+    if (!block_tables || !context_lens || !slot_mapping_out) return PKV_ERR_NULL;
+    if (num_seqs < 0 || num_new <= 0 || max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX) return PKV_ERR_SHAPE;
+    pkv::RopeParams p{};
+    p.q = q, p.k_new = k_new, p.v_new = v_new, p.q_out = q_out;
+    p.k_cache = k_cache, p.v_cache = v_cache;
+    p.k_scale = k_scale, p.v_scale = v_scale, p.scale_stride = scale_stride;
+    p.inv_freq = inv_freq;
+    p.block_tables = block_tables, p.context_lens = context_lens, p.max_nb = max_nb, p.T = num_new;
+    p.slots_out = slot_mapping_out;
+    p.err_flag = err_flag;
+    return rope_append(p, interleaved != 0, fp8, cache, num_q_heads, rotary_dim, (int64_t)num_seqs * num_new, stream);
+}
+
+}  // namespace
+
+PKV_EXPORT int pkv_rope_append(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                               const int32_t *positions, const double *inv_freq, int32_t rotary_dim,
+                               int32_t interleaved, const int64_t *slot_mapping, int32_t num_tokens,
+                               int32_t num_q_heads, pkv_bf16 *k_cache, pkv_bf16 *v_cache, pkv_bf16 *q_out,
+                               pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream)
+{
+    return rope_append_slots(q, k_new, v_new, positions, inv_freq, rotary_dim, interleaved, nullptr, nullptr, 0,
+                             slot_mapping, num_tokens, num_q_heads, k_cache, v_cache, q_out, cache, err_flag, false,
+                             stream);
+}
+
+PKV_EXPORT int pkv_rope_append_fp8(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                                   const int32_t *positions, const double *inv_freq, int32_t rotary_dim,
+                                   int32_t interleaved, const float *k_scale, const float *v_scale,
+                                   int32_t scale_block_stride, const int64_t *slot_mapping, int32_t num_tokens,
+                                   int32_t num_q_heads, uint8_t *k_cache, uint8_t *v_cache, pkv_bf16 *q_out,
+                                   pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream)
+{
+    return rope_append_slots(q, k_new, v_new, positions, inv_freq, rotary_dim, interleaved, k_scale, v_scale,
+                             scale_block_stride, slot_mapping, num_tokens, num_q_heads, k_cache, v_cache, q_out,
+                             cache, err_flag, true, stream);
+}
+
+PKV_EXPORT int pkv_rope_append_multi(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t *context_lens, const double *inv_freq, int32_t rotary_dim,
+                                     int32_t interleaved, int32_t num_seqs, int32_t num_new, int32_t num_q_heads,
+                                     pkv_bf16 *k_cache, pkv_bf16 *v_cache, pkv_bf16 *q_out,
+                                     int64_t *slot_mapping_out, pkv_cache_desc cache, int32_t *err_flag,
+                                     pkv_stream_t stream)
+{
+    return rope_append_tables(q, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, inv_freq, rotary_dim,
+                              interleaved, nullptr, nullptr, 0, num_seqs, num_new, num_q_heads, k_cache, v_cache,
+                              q_out, slot_mapping_out, cache, err_flag, false, stream);
+}
+
+PKV_EXPORT int pkv_rope_append_multi_fp8(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_bf16 *v_new,
+                                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t *context_lens, const double *inv_freq, int32_t rotary_dim,
+                                         int32_t interleaved, const float *k_scale, const float *v_scale,
+                                         int32_t scale_block_stride, int32_t num_seqs, int32_t num_new,
+                                         int32_t num_q_heads, uint8_t *k_cache, uint8_t *v_cache, pkv_bf16 *q_out,
+                                         int64_t *slot_mapping_out, pkv_cache_desc cache, int32_t *err_flag,
+                                         pkv_stream_t stream)
+{
+    return rope_append_tables(q, k_new, v_new, block_tables, max_blocks_per_seq, context_lens, inv_freq, rotary_dim,
+                              interleaved, k_scale, v_scale, scale_block_stride, num_seqs, num_new, num_q_heads,
+                              k_cache, v_cache, q_out, slot_mapping_out, cache, err_flag, true, stream);
+}
+
+// ---- attention over selected blocks ---------------------------------------------------------
+namespace {
+
+int key_bounds(const void *k_cache, const float *k_scale, int32_t scale_stride, const int32_t *block_tables,
+               int32_t max_nb, const int32_t *context_lens, int32_t num_seqs, int32_t num_new, pkv_bf16 *bounds,
+               const pkv_cache_desc &d, int32_t *err_flag, bool fp8, cudaStream_t stream)
+{
+    if (!k_cache || !block_tables || !context_lens || !bounds || (fp8 && !k_scale)) return PKV_ERR_NULL;
+    if (num_seqs < 0 || num_seqs > 65535 || num_new < 0 || max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX)
+        return PKV_ERR_SHAPE;
+    int st = check_copy_desc(d);
+    if (st != PKV_OK) return st;
+    if (fp8 && d.head_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (fp8 && check_scale_stride(scale_stride, d) != PKV_OK) return PKV_ERR_SHAPE;
+    if ((int64_t)d.num_kv_heads * d.head_dim > INT32_MAX / 16) return PKV_ERR_SHAPE;
+    if (!aligned(k_cache, 16) || !aligned(bounds, 16) || !aligned(k_scale, 4)) return PKV_ERR_ALIGN;
+    if (num_seqs == 0 || num_new == 0) return PKV_OK;
+    pkv::BoundsParams p{};
+    p.k_cache = k_cache;
+    p.k_scale = k_scale, p.scale_stride = scale_stride;
+    p.block_tables = block_tables, p.context_lens = context_lens;
+    p.max_nb = max_nb, p.B = num_seqs, p.K = d.num_kv_heads, p.H = d.head_dim;
+    p.num_blocks = d.num_blocks, p.num_new = num_new;
+    p.bounds = bounds;
+    p.err_flag = err_flag;
+    // num_new consecutive tokens touch at most this many blocks
+    const int span = (int)std::min<int64_t>(max_nb, ((int64_t)num_new + 14) / 16 + 1);
+    cudaError_t e = pkv::launch_key_bounds(p, fp8, span, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "key bounds launch");
+}
+
+// pkv_select_blocks' workspace: scores fp32 [B][K][max_nb], exact fp64 [B][K][max_nb], list int32
+// [B][K][max_nb], chunk maxima fp32 [B][K][chunks], counters int32 [B][K], each 256-byte aligned.
+struct SelectWs {
+    int64_t scores, exact, list, chunk_max, counters, end;
+    int32_t chunks;
+};
+
+SelectWs select_ws(int32_t B, int32_t K, int32_t max_nb)
+{
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    const int64_t units = (int64_t)B * K;
+    SelectWs w;
+    w.chunks = (max_nb + pkv::kSelectChunk - 1) / pkv::kSelectChunk;
+    w.scores = 0;
+    w.exact = up(w.scores + units * max_nb * 4);
+    w.list = up(w.exact + units * max_nb * 8);
+    w.chunk_max = up(w.list + units * max_nb * 4);
+    w.counters = up(w.chunk_max + units * w.chunks * 4);
+    w.end = w.counters + units * 4;
+    return w;
+}
+
+int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_selected, const float *k_scale,
+                     const float *v_scale, int32_t scale_stride, pkv_bf16 *out, float *lse_out,
+                     int32_t partition_blocks, int32_t max_partitions, void *workspace, size_t workspace_bytes,
+                     bool fp8, cudaStream_t stream)
+{
+    if (!out || !selected || (fp8 && (!k_scale || !v_scale))) return PKV_ERR_NULL;
+    int st = validate_attn(a);
+    if (st != PKV_OK) return st;
+    if (fp8) {
+        st = check_fp8_desc(a.d);
+        if (st != PKV_OK) return st;
+        if (check_scale_stride(scale_stride, a.d) != PKV_OK) return PKV_ERR_SHAPE;
+        if (!aligned(a.q, 8) || !aligned(k_scale, 4) || !aligned(v_scale, 4)) return PKV_ERR_ALIGN;
+    }
+    if (max_selected <= 0 || partition_blocks < 0) return PKV_ERR_SHAPE;
+    if (!aligned(out, 4) || !aligned(lse_out, 4) || !aligned(selected, 4)) return PKV_ERR_ALIGN;
+    SplitWs w{nullptr, nullptr, nullptr};
+    if (partition_blocks > 0) {
+        if (max_partitions <= 0 || (int64_t)max_partitions * partition_blocks < max_selected) return PKV_ERR_SHAPE;
+        // the unit's last CTA merges in its drained ring; a grid dimension has 65,535 blocks
+        if (!merge_in_kernel(a.N, a.d.num_kv_heads, max_partitions)) return PKV_ERR_UNSUPPORTED;
+        if (!workspace ||
+            workspace_bytes < pkv_splitk_workspace_bytes(a.B, a.N, a.d.head_dim, max_partitions))
+            return PKV_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return PKV_ERR_ALIGN;
+        w = split_ws(workspace, a.B, a.N, a.d.head_dim, max_partitions);
+    }
+    if (a.B == 0) return PKV_OK;
+    CUtensorMap tk, tv;
+    int tok_major = 0;
+    st = fp8 ? make_kv_maps_fp8(&tk, &tv, a.k_cache, a.v_cache, a.d)
+             : make_kv_maps(&tk, &tv, a.k_cache, a.v_cache, a.d, &tok_major);
+    if (st != PKV_OK) return st;
+    pkv::BlocksParams p{};
+    p.q = a.q;
+    p.block_tables = a.block_tables, p.context_lens = a.context_lens, p.selected = selected;
+    p.max_nb = a.max_nb, p.B = a.B, p.N = a.N, p.K = a.d.num_kv_heads, p.G = a.N / a.d.num_kv_heads;
+    p.M = max_selected, p.num_blocks = a.d.num_blocks;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.tok_major = tok_major;
+    p.part_blocks = partition_blocks > 0 ? partition_blocks : max_selected;
+    p.max_parts = partition_blocks > 0 ? max_partitions : 1;
+    p.k_scale = k_scale, p.v_scale = v_scale, p.scale_stride = scale_stride;
+    p.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    p.lse_out = lse_out;
+    p.part_out = w.part_out, p.part_lse = w.part_lse, p.counters = w.counters;
+    p.err_flag = a.err_flag;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    cudaError_t e = pkv::launch_attn_blocks(a.d.head_dim, fp8, tk, tv, p, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "selected blocks attention launch");
+}
+
+}  // namespace
+
+PKV_EXPORT int pkv_key_bounds(const pkv_bf16 *k_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, int32_t num_seqs, int32_t num_new, pkv_bf16 *bounds,
+                              pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream)
+{
+    return key_bounds(k_cache, nullptr, 0, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_new, bounds,
+                      cache, err_flag, false, stream);
+}
+
+PKV_EXPORT int pkv_key_bounds_fp8(const uint8_t *k_cache, const float *k_scale, int32_t scale_block_stride,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, int32_t num_seqs, int32_t num_new, pkv_bf16 *bounds,
+                                  pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream)
+{
+    return key_bounds(k_cache, k_scale, scale_block_stride, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                      num_new, bounds, cache, err_flag, true, stream);
+}
+
+PKV_EXPORT size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq)
+{
+    if (num_seqs < 0 || num_kv_heads < 0 || max_blocks_per_seq < 0) return 0;
+    return (size_t)select_ws(num_seqs, num_kv_heads, max_blocks_per_seq).end;
+}
+
+PKV_EXPORT int pkv_select_blocks(const pkv_bf16 *q, const pkv_bf16 *bounds, const int32_t *block_tables,
+                                 int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t first_blocks, int32_t last_blocks,
+                                 int32_t max_selected, int32_t *selected, pkv_cache_desc cache, void *workspace,
+                                 size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!q || !bounds || !block_tables || !context_lens || !selected) return PKV_ERR_NULL;
+    int st = check_attn_desc(cache, num_q_heads);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0 || num_seqs > 65535 || cache.num_kv_heads > 65535 || max_blocks_per_seq <= 0 ||
+        (int64_t)max_blocks_per_seq * 16 > INT32_MAX)
+        return PKV_ERR_SHAPE;
+    if (first_blocks < 0 || last_blocks < 0 || max_selected <= 0 ||
+        (int64_t)first_blocks + last_blocks > max_selected)
+        return PKV_ERR_SHAPE;
+    if (!workspace || workspace_bytes < pkv_select_workspace_bytes(num_seqs, cache.num_kv_heads, max_blocks_per_seq))
+        return PKV_ERR_WORKSPACE;
+    if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(selected, 4) || !aligned(workspace, 256))
+        return PKV_ERR_ALIGN;
+    if (num_seqs == 0) return PKV_OK;
+    const SelectWs w = select_ws(num_seqs, cache.num_kv_heads, max_blocks_per_seq);
+    char *base = static_cast<char *>(workspace);
+    pkv::SelectParams p{};
+    p.q = q, p.bounds = bounds;
+    p.block_tables = block_tables, p.context_lens = context_lens;
+    p.max_nb = max_blocks_per_seq, p.B = num_seqs, p.N = num_q_heads;
+    p.K = cache.num_kv_heads, p.G = num_q_heads / cache.num_kv_heads, p.num_blocks = cache.num_blocks;
+    p.first = first_blocks, p.last = last_blocks, p.M = max_selected;
+    p.selected = selected;
+    p.scores = reinterpret_cast<float *>(base + w.scores);
+    p.exact = reinterpret_cast<double *>(base + w.exact);
+    p.list = reinterpret_cast<int32_t *>(base + w.list);
+    p.chunk_max = reinterpret_cast<float *>(base + w.chunk_max);
+    p.counters = reinterpret_cast<int32_t *>(base + w.counters);
+    p.chunks = w.chunks;
+    p.err_flag = err_flag;
+    cudaError_t e = pkv::launch_select_blocks(p, cache.head_dim, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "block selection launch");
+}
+
+PKV_EXPORT int pkv_decode_attn_blocks(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+                                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t *context_lens, const int32_t *selected, int32_t max_selected,
+                                      int32_t num_seqs, int32_t num_q_heads, float scale, pkv_bf16 *out,
+                                      float *lse_out, pkv_cache_desc cache, int32_t partition_blocks,
+                                      int32_t max_partitions, void *workspace, size_t workspace_bytes,
+                                      int32_t *err_flag, pkv_stream_t stream)
+{
+    AttnArgs a{q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads, scale,
+               cache, err_flag};
+    return blocks_attention(a, selected, max_selected, nullptr, nullptr, 0, out, lse_out, partition_blocks,
+                            max_partitions, workspace, workspace_bytes, false, stream);
+}
+
+PKV_EXPORT int pkv_decode_attn_blocks_fp8(const pkv_bf16 *q, const uint8_t *k_cache, const uint8_t *v_cache,
+                                          const float *k_scale, const float *v_scale, int32_t scale_block_stride,
+                                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t *context_lens, const int32_t *selected, int32_t max_selected,
+                                          int32_t num_seqs, int32_t num_q_heads, float scale, pkv_bf16 *out,
+                                          float *lse_out, pkv_cache_desc cache, int32_t partition_blocks,
+                                          int32_t max_partitions, void *workspace, size_t workspace_bytes,
+                                          int32_t *err_flag, pkv_stream_t stream)
+{
+    AttnArgs a{q, reinterpret_cast<const pkv_bf16 *>(k_cache), reinterpret_cast<const pkv_bf16 *>(v_cache),
+               block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads, scale, cache, err_flag};
+    return blocks_attention(a, selected, max_selected, k_scale, v_scale, scale_block_stride, out, lse_out,
+                            partition_blocks, max_partitions, workspace, workspace_bytes, true, stream);
+}
+
+// ---- verification of drafted tokens ---------------------------------------------------------
+namespace {
+
+int32_t verify_chunks(int32_t vocab) { return (vocab + pkv::kVerifyChunk - 1) / pkv::kVerifyChunk; }
+
+// sums int64 [B][chunks], then (256-byte aligned) counters int32 [B]
+int64_t verify_counter_offset(int32_t B, int32_t vocab)
+{
+    return ((int64_t)B * verify_chunks(vocab) * 8 + 255) / 256 * 256;
+}
+
+}  // namespace
+
+PKV_EXPORT size_t pkv_verify_workspace_bytes(int32_t num_seqs, int32_t vocab_size)
+{
+    if (num_seqs < 0 || vocab_size < 0 || vocab_size >= (1 << 19)) return 0;
+    return (size_t)(verify_counter_offset(num_seqs, vocab_size) + (int64_t)num_seqs * 4);
+}
+
+PKV_EXPORT int pkv_verify_draft(const void *target_probs, int64_t target_stride, const void *draft_probs,
+                                int64_t draft_stride, int32_t prob_bf16, const int32_t *draft_tokens,
+                                const int32_t *draft_lens, const float *accept_u, const float *sample_u,
+                                int32_t num_seqs, int32_t num_draft, int32_t vocab_size, int32_t *num_accepted,
+                                int32_t *tokens_out, const int32_t *context_lens, int32_t *context_lens_out,
+                                void *workspace, size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!target_probs || !sample_u || !num_accepted || !tokens_out) return PKV_ERR_NULL;
+    if (num_draft > 0 && (!draft_tokens || !accept_u)) return PKV_ERR_NULL;
+    if ((context_lens == nullptr) != (context_lens_out == nullptr)) return PKV_ERR_NULL;
+    if (num_seqs < 0 || num_seqs > 65535 || num_draft < 0 || num_draft > 1024 || vocab_size <= 0)
+        return PKV_ERR_SHAPE;
+    if (vocab_size >= (1 << 19)) return PKV_ERR_UNSUPPORTED;  // the sums of clamped rows fit 63 bits
+    if (target_stride < vocab_size || (draft_probs && draft_stride < vocab_size)) return PKV_ERR_SHAPE;
+    const uintptr_t es = prob_bf16 ? 2 : 4;
+    if (!aligned(target_probs, es) || !aligned(draft_probs, es) || !aligned(workspace, 256)) return PKV_ERR_ALIGN;
+    if (!workspace || workspace_bytes < pkv_verify_workspace_bytes(num_seqs, vocab_size)) return PKV_ERR_WORKSPACE;
+    if (num_seqs == 0) return PKV_OK;
+    pkv::VerifyParams p{};
+    p.target = target_probs, p.draft = num_draft > 0 ? draft_probs : nullptr;
+    p.target_stride = target_stride, p.draft_stride = draft_stride;
+    p.tokens = draft_tokens, p.lens = draft_lens;
+    p.accept_u = accept_u, p.sample_u = sample_u;
+    p.B = num_seqs, p.T = num_draft, p.V = vocab_size;
+    p.accepted = num_accepted, p.out = tokens_out;
+    p.context_lens = context_lens, p.context_lens_out = context_lens_out;
+    p.sums = static_cast<long long *>(workspace);
+    p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) +
+                                             verify_counter_offset(num_seqs, vocab_size));
+    p.chunks = verify_chunks(vocab_size);
+    p.err_flag = err_flag;
+    cudaError_t e = pkv::launch_verify(p, prob_bf16 != 0, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "draft verification launch");
 }

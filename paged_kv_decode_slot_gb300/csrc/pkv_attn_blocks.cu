@@ -1,0 +1,347 @@
+// pkv_attn_blocks.cu - decode attention over selected blocks of a paged cache.
+//
+// Every (sequence, KV head) brings a list of logical blocks; its G query heads attend to the tokens of those
+// blocks alone.  The work is that of the dense kernel on a list in place of the table's leading blocks: TMA
+// loads of one (block, KV head) tile each, streamed by producer warps into a ring of shared-memory stages, and
+// consumer warps that keep an online softmax over the tiles they take (see pkv_attn.cu).  What differs:
+//  * a tile's block id takes two dependent loads (list entry, table entry), looked up 32 tiles ahead of use by
+//    the producer's lanes; the list's first entries are fetched before the sequence's length is there;
+//  * the tokens that count of a tile follow from its logical block, not from its place in the list: the
+//    producer leaves that number with the stage (0 for an entry to skip);
+//  * the running sum takes the 32-bit weights, so lse does not carry the rounding of the 16-bit weights that
+//    the product P V takes.
+// One CTA per (KV head, sequence, partition of the list); the last partition of a unit to finish merges.
+// Bound by memory: 32 H bytes of K and as many of V per tile and two bytes an element.
+#include "pkv_attn_common.cuh"
+#include "pkv_ops.h"
+
+namespace pkv {
+
+// One 16-token tile (the first `valid` tokens count) folded into a warp's state, bf16.
+template <int H>
+__device__ __forceinline__ void block_update(WarpAcc<H> &a, const uint32_t (&qf)[H / 16][2], uint32_t kt, uint32_t vt,
+                                             int valid, float sl2, int tok_major, int lane)
+{
+    constexpr int kKSteps = H / 16;
+    const int mi = lane >> 3, ri = lane & 7;
+    const int k_tok = ri + 8 * (mi & 1), k_hoff = 8 * (mi >> 1);
+    const int v_tok = ri + 8 * (mi >> 1), v_hoff = 8 * (mi & 1);
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < kKSteps; kk += 2) {
+        uint32_t a0[4], a1[4];
+        ldsm_x4(a0, kt + tile_chunk_offset<H>(k_tok, 16 * kk + k_hoff, tok_major));
+        ldsm_x4(a1, kt + tile_chunk_offset<H>(k_tok, 16 * kk + 16 + k_hoff, tok_major));
+        mma_bf16_16816(sa, a0, qf[kk][0], qf[kk][1]);
+        mma_bf16_16816(sb, a1, qf[kk + 1][0], qf[kk + 1][1]);
+    }
+    const int t0 = lane >> 2, t1 = t0 + 8;
+    const float x0 = t0 < valid ? (sa[0] + sb[0]) * sl2 : -INFINITY;
+    const float x1 = t0 < valid ? (sa[1] + sb[1]) * sl2 : -INFINITY;
+    const float x2 = t1 < valid ? (sa[2] + sb[2]) * sl2 : -INFINITY;
+    const float x3 = t1 < valid ? (sa[3] + sb[3]) * sl2 : -INFINITY;
+    float mA = fmaxf(x0, x2), mB = fmaxf(x1, x3);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+        mA = fmaxf(mA, __shfl_xor_sync(0xFFFFFFFFu, mA, off));
+        mB = fmaxf(mB, __shfl_xor_sync(0xFFFFFFFFu, mB, off));
+    }
+    const bool needA = mA > a.m[0] + kRescaleThreshold;
+    const bool needB = mB > a.m[1] + kRescaleThreshold;
+    if (__any_sync(0xFFFFFFFFu, needA || needB)) {
+        const float alphaA = needA ? exp2_sfu(a.m[0] - mA) : 1.f;
+        const float alphaB = needB ? exp2_sfu(a.m[1] - mB) : 1.f;
+        if (needA) a.m[0] = mA;
+        if (needB) a.m[1] = mB;
+        a.l[0] *= alphaA;
+        a.l[1] *= alphaB;
+#pragma unroll
+        for (int mt = 0; mt < kKSteps; ++mt) {
+            a.o[mt][0] *= alphaA;
+            a.o[mt][1] *= alphaB;
+            a.o[mt][2] *= alphaA;
+            a.o[mt][3] *= alphaB;
+        }
+    }
+    const float w0 = exp2_sfu(x0 - a.m[0]), w1 = exp2_sfu(x1 - a.m[1]);
+    const float w2 = exp2_sfu(x2 - a.m[0]), w3 = exp2_sfu(x3 - a.m[1]);
+    a.l[0] += w0 + w2;
+    a.l[1] += w1 + w3;
+    // the weights enter the product P V rounded to bf16 (off by 2^-9 at most, as the result's own rounding is)
+    const uint32_t pb0 = movmatrix_trans(pack_bf16x2(w0, w1));
+    const uint32_t pb1 = movmatrix_trans(pack_bf16x2(w2, w3));
+    const bool partial = valid < kBlockSize;
+    const int tc = (lane & 3) * 2;
+#pragma unroll
+    for (int mt = 0; mt < kKSteps; ++mt) {
+        uint32_t av[4];
+        ldsm_x4_trans(av, vt + tile_chunk_offset<H>(v_tok, 16 * mt + v_hoff, tok_major));
+        if (partial) {  // zero V of tokens past the context (they may be NaN)
+            const uint32_t lo = (tc < valid ? 0x0000FFFFu : 0u) | (tc + 1 < valid ? 0xFFFF0000u : 0u);
+            const uint32_t hi = (tc + 8 < valid ? 0x0000FFFFu : 0u) | (tc + 9 < valid ? 0xFFFF0000u : 0u);
+            av[0] &= lo;
+            av[1] &= lo;
+            av[2] &= hi;
+            av[3] &= hi;
+        }
+        mma_bf16_16816(a.o[mt], av, pb0, pb1);
+    }
+}
+
+// kFp8: e4m3 pools (H = 128).  Scales come per tile in both granularities (the producer fetches them with the
+// block id): the K scale multiplies the tile's logits, the V scale its weights relative to the largest seen
+// (VScaleRef, pkv_attn_common.cuh).
+template <int H, bool kFp8>
+__global__ void __launch_bounds__(kAttnThreads, PKV_CTAS_PER_SM)
+attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const BlocksParams p)
+{
+    constexpr int S = kFp8 ? kStagesFp8 : kStages;
+    using L = AttnLayout<H, S, kConsumerWarps, kProducers, kFp8 ? 1 : 2>;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
+    uint8_t *base = smem_raw + (base_u32 - raw_u32);
+
+    const int kvh = blockIdx.x, b = blockIdx.y, part = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.G;
+    const int begin = part * p.part_blocks;  // this CTA's entries of the list: [begin, end)
+    const int32_t *sel = p.selected + ((size_t)b * p.K + kvh) * p.M + begin;
+    const int pw = warp - kConsumerWarps;  // producer warp
+
+    int first_sel = -1;  // the producers' first list entries do not depend on the length
+    if (pw >= 0 && begin + pw + kProducers * lane < min(p.M, begin + p.part_blocks)) first_sel = __ldg(sel + pw + kProducers * lane);
+    int ctx = p.context_lens[b];
+    if (ctx < 0 || ctx > p.max_nb * kBlockSize) {
+        if (threadIdx.x == 0 && kvh == 0 && part == 0) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+        ctx = 0;
+    }
+    const int nb = (ctx + kBlockSize - 1) / kBlockSize;
+    const int entries = min(nb, p.M);  // a sequence has no more blocks to list
+    const int nparts = (entries + p.part_blocks - 1) / p.part_blocks;
+    const int n = min(entries - begin, p.part_blocks);
+    const size_t bn0 = (size_t)b * p.N + (size_t)kvh * G;
+    if (n <= 0) {
+        if (entries == 0 && part == 0) {
+            for (int idx = threadIdx.x; idx < G * H; idx += kAttnThreads) {
+                const int g = idx / H, h = idx - g * H;
+                p.out[(bn0 + g) * H + h] = __float2bfloat16_rn(0.f);
+                if (h == 0 && p.lse_out) p.lse_out[bn0 + g] = -INFINITY;
+            }
+        }
+        return;
+    }
+
+    const uint32_t bar_full = base_u32 + L::kBarOffset;
+    const uint32_t bar_empty = bar_full + 8 * S;
+    volatile int *valid_of = reinterpret_cast<volatile int *>(base + L::kMiscOffset);  // [S] tokens that count
+    volatile int *abort_flag = valid_of + S;
+    volatile int *issued_count = abort_flag + 1;  // [kProducers]
+    volatile float2 *stage_sc = reinterpret_cast<volatile float2 *>(base + L::kScaleOffset);
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int q = 0; q < kProducers; ++q) issued_count[q] = 0;
+        init_ring<S>(bar_full, bar_empty);
+    }
+    __syncthreads();
+
+    WarpAcc<H> acc;
+    VScaleRef vr{0.f, 0.f};
+
+    if (pw >= 0) {
+        // ------------------------------ producer warps ------------------------------
+        if (lane == 0 && pw == 0) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+        }
+        const int32_t *tbl = p.block_tables + (size_t)b * p.max_nb;
+        const int mine = n > pw ? (n - pw + kProducers - 1) / kProducers : 0;
+        // one tile per lane: its block id (-1: skipped), the tokens that count, its scales
+        struct Tile {
+            int bid, valid;
+            float ks, vs;
+        };
+        auto look_up = [&](int j) {
+            Tile t{-1, 0, 0.f, 0.f};
+            if (j < 0 || j >= nb) {
+                if (j != -1) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);  // -1: an entry left empty
+                return t;
+            }
+            const int bid = __ldg(tbl + j);
+            if (bid < 0 || bid >= p.num_blocks) {
+                set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                return t;
+            }
+            t.bid = bid;
+            t.valid = min(kBlockSize, ctx - j * kBlockSize);
+            if constexpr (kFp8) {
+                const size_t si = (size_t)bid * p.scale_stride + kvh;
+                t.ks = __ldg(p.k_scale + si);
+                t.vs = __ldg(p.v_scale + si);
+            }
+            return t;
+        };
+        Tile cur{-1, 0, 0.f, 0.f};
+        if (lane < mine) cur = look_up(first_sel);
+        int issued = 0;
+        bool aborted = false;
+        for (int k0 = 0; k0 < mine && !aborted; k0 += 32) {
+            Tile nxt{-1, 0, 0.f, 0.f};
+            if (k0 + 32 + lane < mine) nxt = look_up(__ldg(sel + pw + kProducers * (k0 + 32 + lane)));
+            const int cnt = min(32, mine - k0);
+            for (int k = 0; k < cnt; ++k) {
+                const int bid = __shfl_sync(0xFFFFFFFFu, cur.bid, k);
+                const int valid = __shfl_sync(0xFFFFFFFFu, cur.valid, k);
+                float2 sc = make_float2(0.f, 0.f);
+                if constexpr (kFp8) sc = make_float2(__shfl_sync(0xFFFFFFFFu, cur.ks, k), __shfl_sync(0xFFFFFFFFu, cur.vs, k));
+                bool ok = true;
+                if (lane == 0) {
+                    const int i = pw + kProducers * (k0 + k), s = i % S;
+                    const uint32_t bar = bar_full + 8 * s;
+                    if (i >= S && !mbar_wait_bounded(bar_empty + 8 * s, ((i / S) & 1) ^ 1, abort_flag, p.wait_ns)) {
+                        if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                    } else {
+                        valid_of[s] = valid;
+                        if constexpr (kFp8) stage_sc[s].x = sc.x, stage_sc[s].y = sc.y;
+                        if (valid > 0) {
+                            const uint32_t dst = base_u32 + s * L::kStageBytes;
+                            mbar_arrive_expect_tx(bar, L::kStageBytes);
+                            if constexpr (kFp8) {
+                                tma_load_4d(dst, &tm_k, bar, 0, kvh, 0, bid);
+                                tma_load_4d(dst + L::kTileBytes, &tm_v, bar, 0, kvh, 0, bid);
+                            } else if (p.tok_major) {
+                                tma_load_5d(dst, &tm_k, bar, 0, 0, kvh, 0, bid);
+                                tma_load_5d(dst + L::kTileBytes, &tm_v, bar, 0, 0, kvh, 0, bid);
+                            } else {
+                                tma_load_5d(dst, &tm_k, bar, 0, 0, 0, kvh, bid);
+                                tma_load_5d(dst + L::kTileBytes, &tm_v, bar, 0, 0, 0, kvh, bid);
+                            }
+                        } else {
+                            mbar_arrive(bar);
+                        }
+                        ++issued;
+                    }
+                }
+                if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+                    aborted = true;
+                    break;
+                }
+            }
+            cur = nxt;
+        }
+        if (lane == 0) issued_count[pw] = issued;
+    } else {
+        // ------------------------------ consumer warps ------------------------------
+        uint32_t qf[H / 16][2];
+        if constexpr (kFp8) load_q_frags_fp8<H>(qf, p.q, p.N, b, kvh, G, lane);
+        else load_q_frags<H>(qf, p.q, p.N, b, kvh, G, lane);
+        acc_reset<H>(acc);
+        for (int i = warp; i < n; i += kConsumerWarps) {
+            const int s = i % S;
+            // lanes may differ at the deadline: the warp agrees before its collective work
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_full + 8 * s, (i / S) & 1, abort_flag, p.wait_ns))) {
+                if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+                *abort_flag = 1;
+                break;
+            }
+            const int valid = valid_of[s];
+            if (valid > 0) {
+                const uint32_t kt = base_u32 + s * L::kStageBytes;
+                if constexpr (kFp8)
+                    tile_update_fp8<H, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2 * stage_sc[s].x, stage_sc[s].y, vr, lane);
+                else
+                    block_update<H>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2, p.tok_major, lane);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+        }
+    }
+
+    __syncthreads();
+    const bool aborted = *abort_flag != 0;
+    if (aborted) {
+        if (pw >= 0 && lane == 0) drain_ring<S, kProducers>(bar_full, pw, issued_count[pw]);
+        __syncthreads();
+        if (nparts <= 1) return;  // the unit's other partitions still count on this one: a void partial
+    }
+
+    // ------------------------- merge the consumer warps' states -------------------------
+    float *mo = reinterpret_cast<float *>(base);
+    float *mm = mo + kConsumerWarps * 8 * H;
+    float *ml = mm + kConsumerWarps * 8;
+    if (!aborted) {
+        if (warp < kConsumerWarps) {
+            if constexpr (kFp8) acc_scale_o<H>(acc, vr.v);
+            deposit<H, kFp8>(acc, mo, mm, ml, warp, lane);
+        }
+        __syncthreads();
+    }
+    for (int idx = threadIdx.x; idx < G * H; idx += kAttnThreads) {
+        const int g = idx / H, h = idx - g * H;
+        float val = __int_as_float(0x7FC00000), lse = __int_as_float(0x7FC00000);  // NaN: void
+        if (!aborted) combine<H>(mo, mm, ml, g, h, val, lse);
+        const size_t bn = bn0 + g;
+        if (nparts > 1) {
+            p.part_out[(bn * p.max_parts + part) * H + h] = val;
+            if (h == 0) p.part_lse[bn * p.max_parts + part] = lse;
+        } else {
+            p.out[bn * H + h] = __float2bfloat16_rn(val);
+            if (h == 0 && p.lse_out) p.lse_out[bn] = lse;
+        }
+    }
+    if (nparts <= 1) return;
+
+    // ----------------- log-sum-exp merge by the unit's last partition -----------------
+    __shared__ int last_one;
+    __syncthreads();
+    int32_t *count = p.counters + (size_t)b * p.K + kvh;
+    if (threadIdx.x == 0) last_one = atomic_add_acq_rel_gpu(count, 1) == nparts - 1;
+    __syncthreads();
+    if (!last_one) return;
+    float *wts = reinterpret_cast<float *>(base);                          // [G][nparts]
+    float *red = reinterpret_cast<float *>(base) + kInKernelMergeWeights;  // [kMergeWarps][8][H]
+    for (int idx = threadIdx.x; idx < G * nparts; idx += kAttnThreads) {
+        const int g = idx / nparts, q = idx - g * nparts;
+        wts[idx] = __ldcg(p.part_lse + (bn0 + g) * p.max_parts + q);
+    }
+    __syncthreads();
+    for (int g = warp; g < G; g += kAttnThreads / 32) {
+        const float lse = lse_merge_weights<true>(wts + g * nparts, nparts, wts + g * nparts, lane);
+        if (lane == 0 && p.lse_out) p.lse_out[bn0 + g] = lse;
+    }
+    __syncthreads();
+    merge_rows<H, 8>(wts, nparts, G, p.part_out + bn0 * p.max_parts * H, (size_t)p.max_parts * H, red, p.out + bn0 * H, H,
+                     threadIdx.x, kAttnThreads);
+    if (threadIdx.x == 0) *count = 0;  // ready for the next call
+}
+
+template <int H, bool kFp8>
+static cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, cudaStream_t stream)
+{
+    constexpr int smem = AttnLayout<H, kFp8 ? kStagesFp8 : kStages, kConsumerWarps, kProducers, kFp8 ? 1 : 2>::kAlloc;
+    static int ready[64] = {};  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready[dev] = 1;
+    }
+    attn_blocks_kernel<H, kFp8><<<dim3(p.K, p.B, p.max_parts), kAttnThreads, smem, stream>>>(tk, tv, p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p,
+                               cudaStream_t stream)
+{
+    if (fp8) return launch_t<128, true>(tk, tv, p, stream);
+    return H == 128 ? launch_t<128, false>(tk, tv, p, stream) : launch_t<64, false>(tk, tv, p, stream);
+}
+
+}  // namespace pkv

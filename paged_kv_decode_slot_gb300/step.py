@@ -120,6 +120,16 @@ def plan_attention(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int, nu
     return AttentionPlan("split", partition_blocks, count(max_blocks_per_seq, partition_blocks))
 
 
+def plan_blocks_attention(num_seqs: int, num_kv_heads: int, max_selected: int, num_sms: int) -> AttentionPlan:
+    """Partitions of the selected-block lists for pkv_decode_attn_blocks: one CTA per (sequence, KV
+    head) while those units cover the SMs and the lists are short, else partitions as
+    ``plan_attention`` sizes them for tables of that length."""
+    plan = plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False)
+    if plan.mode == "single":
+        return AttentionPlan("single", 0, 1)
+    return plan
+
+
 class DecodeStep:
     """State of one decode step over a paged cache: the pools and workspace on the GPU; q,
     k_new, v_new, block tables and context lengths on the GPU or in pinned host memory (then
