@@ -482,10 +482,10 @@ int pkv_decode_step_prefix(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_b
  * every head of q and k_new by the angle P * inv_freq[j]:
  *     a' = a cos - b sin,   b' = a sin + b cos,
  * pair j being the elements (j, j + R / 2), or (2j, 2j + 1) with interleaved != 0; the elements from
- * R = rotary_dim on are copied (R a multiple of 16, at most H; H a multiple of 16, at most 256).
+ * R = rotary_dim on are copied (R a multiple of 16, at most H; H in {64, 128}).
  * inv_freq double [R / 2] (device; any scaling of the frequencies is the caller's): the angle is
- * reduced in 64 bits, so far positions lose nothing, and the rotation computed in fp32 and rounded
- * once, to bf16 or to e4m3.  v_new is not turned.  q_out [tokens][N][H] receives the turned queries
+ * taken in 64 bits (off by less than 1e-6 at any position), and the rotation computed in fp32 and
+ * rounded once, to bf16 or to e4m3.  v_new is not turned.  q_out [tokens][N][H] receives the turned queries
  * and may be q itself (in place), but not overlap it otherwise.  A token without a slot (below) is
  * left out: nothing is written for it, q_out included.  q, k_new, v_new, q_out and the pools are
  * 16-byte aligned (e4m3 pools 8-byte).
@@ -552,8 +552,8 @@ int pkv_key_bounds_fp8(const uint8_t *k_cache, const float *k_scale, int32_t sca
                        int32_t num_seqs, int32_t num_new, pkv_bf16 *key_bounds, pkv_cache_desc cache,
                        int32_t *err_flag, pkv_stream_t stream);
 
-/* Workspace of pkv_select_blocks, 256-byte aligned and ZEROED BEFORE ITS FIRST USE (each call leaves its
-   counters at zero again; calls that share a workspace must not overlap on the GPU). */
+/* Workspace of pkv_select_blocks, 256-byte aligned; its contents do not matter between calls, but calls
+   that share a workspace must not overlap on the GPU. */
 size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq);
 
 /* The blocks each (sequence, KV head) attends to.  score(b, kvh, j) = the largest, over the G query heads

@@ -16,5 +16,6 @@ def __getattr__(name):
                                                     "check", "library", "max_partitions_for", "tapered_partitions_for", "IN_KERNEL_MERGE_WEIGHTS",
                                                     "split_attention_launches", "multi_attention_launches"):
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = value = getattr(binding, name)  # found without this function from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -872,8 +872,7 @@ def pkv_select_workspace_bytes(num_seqs: int, num_kv_heads: int, max_blocks_per_
 def pkv_select_blocks(q, key_bounds, block_tables, context_lens, selected, workspace, first_blocks: int = 1,
                       last_blocks: int = 1, err_flag=None, stream=None) -> int:
     """selected int32 [B, K, M]: the logical blocks each (sequence, KV head) attends to, ascending, -1
-    behind them.  workspace: pkv_select_workspace_bytes(B, K, max_blocks) bytes, zeroed before its
-    first use."""
+    behind them.  workspace: pkv_select_workspace_bytes(B, K, max_blocks) bytes."""
     dev = _current_device()
     qs, (nb, K, _, H) = _shape(q, 3, "q"), _shape(key_bounds, 4, "key_bounds")
     B, N, _ = qs

@@ -85,7 +85,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 // 64-element half (16 x 128 bytes): the tcgen05 column kernel lands the two halves of a K tile in
 // separate regions, so consecutive tiles form one operand of uniform row stride.
 CUresult encode_kv_map(CUtensorMap *map, const void *base, const pkv_cache_desc &d, int tok_major,
-                       int half_box = 0)
+                       int half_box = 0, CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
 {
     const cuuint64_t H = (cuuint64_t)d.head_dim, K = (cuuint64_t)d.num_kv_heads;
     const cuuint64_t halves = H / 64;
@@ -109,7 +109,7 @@ CUresult encode_kv_map(CUtensorMap *map, const void *base, const pkv_cache_desc 
     }
     return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims,
                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                       promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 int g_tok_major = -1;  // layout the driver accepted first (-1: not yet known)
@@ -122,7 +122,8 @@ std::atomic<int64_t> g_withhold_tile{-1};
 #endif
 
 int make_kv_maps(CUtensorMap *tk, CUtensorMap *tv, const void *k, const void *v,
-                 const pkv_cache_desc &d, int *tok_major)
+                 const pkv_cache_desc &d, int *tok_major,
+                 CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
 {
     if (!encode_fn()) {
         g_last_error = "cuTensorMapEncodeTiled is unavailable from the driver";
@@ -132,8 +133,8 @@ int make_kv_maps(CUtensorMap *tk, CUtensorMap *tv, const void *k, const void *v,
     const int first = g_tok_major < 0 ? 0 : g_tok_major;
     for (int attempt = 0; attempt < 2; ++attempt) {
         const int mode = attempt == 0 ? first : 1 - first;
-        CUresult rk = encode_kv_map(tk, k, d, mode);
-        CUresult rv = rk == CUDA_SUCCESS ? encode_kv_map(tv, v, d, mode) : rk;
+        CUresult rk = encode_kv_map(tk, k, d, mode, 0, promotion);
+        CUresult rv = rk == CUDA_SUCCESS ? encode_kv_map(tv, v, d, mode, 0, promotion) : rk;
         if (rk == CUDA_SUCCESS && rv == CUDA_SUCCESS) {
             g_tok_major = mode;
             *tok_major = mode;
@@ -493,8 +494,8 @@ namespace {
 
 // e4m3 pool [num_blocks][16][K][H] bytes, H = 128: dims (h, head, token, block) with monotone
 // strides; the box is one (block, head) tile, 16 rows of 128 bytes, 128B-swizzled.
-int make_kv_maps_fp8(CUtensorMap *tk, CUtensorMap *tv, const void *k, const void *v,
-                     const pkv_cache_desc &d)
+int make_kv_maps_fp8(CUtensorMap *tk, CUtensorMap *tv, const void *k, const void *v, const pkv_cache_desc &d,
+                     CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
 {
     if (!encode_fn()) {
         g_last_error = "cuTensorMapEncodeTiled is unavailable from the driver";
@@ -509,7 +510,7 @@ int make_kv_maps_fp8(CUtensorMap *tk, CUtensorMap *tv, const void *k, const void
         CUresult r = encode_fn()(t ? tv : tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                                  const_cast<void *>(t ? v : k), dims, strides, box, es,
                                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                                 promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) {
             g_last_error = "cuTensorMapEncodeTiled failed for the e4m3 pool (CUresult " +
                            std::to_string((int)r) + ")";
@@ -1219,10 +1220,10 @@ int rope_append(pkv::RopeParams &p, bool interleaved, bool fp8, const pkv_cache_
     int st = check_copy_desc(d);
     if (st != PKV_OK) return st;
     if (num_q_heads <= 0 || rotary_dim <= 0 || rotary_dim > d.head_dim || tokens < 0) return PKV_ERR_SHAPE;
-    if (d.head_dim % 16 != 0 || d.head_dim > 256 || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if ((d.head_dim != 64 && d.head_dim != 128) || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
     if (fp8 && check_scale_stride(p.scale_stride, d) != PKV_OK) return PKV_ERR_SHAPE;
-    // head offsets inside a token are 32-bit; the grid has one CTA per token
-    if (((int64_t)num_q_heads + 2 * (int64_t)d.num_kv_heads) * d.head_dim > INT32_MAX / 2 || tokens > INT32_MAX)
+    // offsets inside a token are 32-bit
+    if (((int64_t)num_q_heads + 2 * (int64_t)d.num_kv_heads) * d.head_dim > INT32_MAX / 2 || tokens > INT32_MAX / 2)
         return PKV_ERR_SHAPE;
     const uintptr_t pool = fp8 ? 8 : 16;
     if (!aligned(p.q, 16) || !aligned(p.k_new, 16) || !aligned(p.v_new, 16) || !aligned(p.q_out, 16) ||
@@ -1231,12 +1232,16 @@ int rope_append(pkv::RopeParams &p, bool interleaved, bool fp8, const pkv_cache_
         return PKV_ERR_ALIGN;
     if (tokens == 0) return PKV_OK;
     p.R = rotary_dim;
-    p.n = tokens;
+    p.n = (int32_t)tokens;
     p.N = num_q_heads;
     p.K = d.num_kv_heads;
     p.H = d.head_dim;
     p.num_blocks = d.num_blocks;
-    cudaError_t e = pkv::launch_rope_append(p, interleaved, fp8, stream);
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    int sms = 0;
+    st = sm_count(&sms);
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_rope_append(p, interleaved, fp8, sms, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "rope append launch");
 }
 
@@ -1361,10 +1366,10 @@ int key_bounds(const void *k_cache, const float *k_scale, int32_t scale_stride, 
 }
 
 // pkv_select_blocks' workspace: scores fp32 [B][K][max_nb], exact fp64 [B][K][max_nb], list int32
-// [B][K][max_nb], chunk maxima fp32 [B][K][chunks], counters int32 [B][K], each 256-byte aligned.
+// [B][K][max_nb], tile maxima fp32 [B][K][tiles], each 256-byte aligned.
 struct SelectWs {
-    int64_t scores, exact, list, chunk_max, counters, end;
-    int32_t chunks;
+    int64_t scores, exact, list, tile_max, end;
+    int32_t tiles;
 };
 
 SelectWs select_ws(int32_t B, int32_t K, int32_t max_nb)
@@ -1372,13 +1377,12 @@ SelectWs select_ws(int32_t B, int32_t K, int32_t max_nb)
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     const int64_t units = (int64_t)B * K;
     SelectWs w;
-    w.chunks = (max_nb + pkv::kSelectChunk - 1) / pkv::kSelectChunk;
+    w.tiles = (max_nb + 15) / 16;
     w.scores = 0;
     w.exact = up(w.scores + units * max_nb * 4);
     w.list = up(w.exact + units * max_nb * 8);
-    w.chunk_max = up(w.list + units * max_nb * 4);
-    w.counters = up(w.chunk_max + units * w.chunks * 4);
-    w.end = w.counters + units * 4;
+    w.tile_max = up(w.list + units * max_nb * 4);
+    w.end = w.tile_max + units * w.tiles * 4;
     return w;
 }
 
@@ -1412,8 +1416,12 @@ int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_sel
     if (a.B == 0) return PKV_OK;
     CUtensorMap tk, tv;
     int tok_major = 0;
-    st = fp8 ? make_kv_maps_fp8(&tk, &tv, a.k_cache, a.v_cache, a.d)
-             : make_kv_maps(&tk, &tv, a.k_cache, a.v_cache, a.d, &tok_major);
+    // Each KV head reads blocks of its own choice, so a token's row of the next head is not wanted: L2 fetches no more
+    // than the row of one head (128 bytes in e4m3 and at H = 64).
+    const CUtensorMapL2promotion promotion = fp8 || a.d.head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                                       : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    st = fp8 ? make_kv_maps_fp8(&tk, &tv, a.k_cache, a.v_cache, a.d, promotion)
+             : make_kv_maps(&tk, &tv, a.k_cache, a.v_cache, a.d, &tok_major, promotion);
     if (st != PKV_OK) return st;
     pkv::BlocksParams p{};
     p.q = a.q;
@@ -1491,11 +1499,13 @@ PKV_EXPORT int pkv_select_blocks(const pkv_bf16 *q, const pkv_bf16 *bounds, cons
     p.scores = reinterpret_cast<float *>(base + w.scores);
     p.exact = reinterpret_cast<double *>(base + w.exact);
     p.list = reinterpret_cast<int32_t *>(base + w.list);
-    p.chunk_max = reinterpret_cast<float *>(base + w.chunk_max);
-    p.counters = reinterpret_cast<int32_t *>(base + w.counters);
-    p.chunks = w.chunks;
+    p.tile_max = reinterpret_cast<float *>(base + w.tile_max);
+    p.tiles = w.tiles;
     p.err_flag = err_flag;
-    cudaError_t e = pkv::launch_select_blocks(p, cache.head_dim, stream);
+    int sms = 0;
+    st = sm_count(&sms);
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_select_blocks(p, cache.head_dim, sms, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "block selection launch");
 }
 
@@ -1531,12 +1541,11 @@ PKV_EXPORT int pkv_decode_attn_blocks_fp8(const pkv_bf16 *q, const uint8_t *k_ca
 // ---- verification of drafted tokens ---------------------------------------------------------
 namespace {
 
-int32_t verify_chunks(int32_t vocab) { return (vocab + pkv::kVerifyChunk - 1) / pkv::kVerifyChunk; }
-
-// sums int64 [B][chunks], then (256-byte aligned) counters int32 [B]
+// sums int64 [B][most runs], then (256-byte aligned) counters int32 [B]
 int64_t verify_counter_offset(int32_t B, int32_t vocab)
 {
-    return ((int64_t)B * verify_chunks(vocab) * 8 + 255) / 256 * 256;
+    const int64_t runs = ((int64_t)vocab + pkv::kVerifyRun - 1) / pkv::kVerifyRun;
+    return (B * runs * 8 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -1576,8 +1585,10 @@ PKV_EXPORT int pkv_verify_draft(const void *target_probs, int64_t target_stride,
     p.sums = static_cast<long long *>(workspace);
     p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) +
                                              verify_counter_offset(num_seqs, vocab_size));
-    p.chunks = verify_chunks(vocab_size);
     p.err_flag = err_flag;
-    cudaError_t e = pkv::launch_verify(p, prob_bf16 != 0, stream);
+    int sms = 0;
+    const int st = sm_count(&sms);
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_verify(p, prob_bf16 != 0, sms, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "draft verification launch");
 }

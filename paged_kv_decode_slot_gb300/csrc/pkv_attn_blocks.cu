@@ -97,6 +97,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                    const BlocksParams p)
 {
     constexpr int S = kFp8 ? kStagesFp8 : kStages;
+    constexpr int kBatch = S / kProducers / 2;
     using L = AttnLayout<H, S, kConsumerWarps, kProducers, kFp8 ? 1 : 2>;
 
     extern __shared__ uint8_t smem_raw[];
@@ -191,14 +192,16 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             Tile nxt{-1, 0, 0.f, 0.f};
             if (k0 + 32 + lane < mine) nxt = look_up(__ldg(sel + pw + kProducers * (k0 + 32 + lane)));
             const int cnt = min(32, mine - k0);
-            for (int k = 0; k < cnt; ++k) {
-                const int bid = __shfl_sync(0xFFFFFFFFu, cur.bid, k);
-                const int valid = __shfl_sync(0xFFFFFFFFu, cur.valid, k);
+            // kBatch tiles at a time, one per lane: half of this producer's stages, so that the other half stays in flight
+            for (int k = 0; k < cnt; k += kBatch) {
+                const int from = min(k + lane, 31);
+                const int bid = __shfl_sync(0xFFFFFFFFu, cur.bid, from);
+                const int valid = __shfl_sync(0xFFFFFFFFu, cur.valid, from);
                 float2 sc = make_float2(0.f, 0.f);
-                if constexpr (kFp8) sc = make_float2(__shfl_sync(0xFFFFFFFFu, cur.ks, k), __shfl_sync(0xFFFFFFFFu, cur.vs, k));
+                if constexpr (kFp8) sc = make_float2(__shfl_sync(0xFFFFFFFFu, cur.ks, from), __shfl_sync(0xFFFFFFFFu, cur.vs, from));
                 bool ok = true;
-                if (lane == 0) {
-                    const int i = pw + kProducers * (k0 + k), s = i % S;
+                if (lane < kBatch && k + lane < cnt) {
+                    const int i = pw + kProducers * (k0 + k + lane), s = i % S;
                     const uint32_t bar = bar_full + 8 * s;
                     if (i >= S && !mbar_wait_bounded(bar_empty + 8 * s, ((i / S) & 1) ^ 1, abort_flag, p.wait_ns)) {
                         if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
@@ -223,10 +226,12 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         } else {
                             mbar_arrive(bar);
                         }
-                        ++issued;
                     }
                 }
-                if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+                // the tiles issued so far are those before the first refused one; a refused wait ends the producer
+                const unsigned refused = __ballot_sync(0xFFFFFFFFu, !ok);
+                issued += refused ? __ffs(refused) - 1 : min(kBatch, cnt - k);
+                if (refused) {
                     aborted = true;
                     break;
                 }

@@ -33,13 +33,14 @@ struct RopeParams {
     const int32_t *context_lens;   // [B]
     int64_t *slots_out;            // [B][T]
     int32_t max_nb, T;
-    int64_t n;                     // tokens
+    int32_t n;                     // tokens
     int32_t N, K, H;
     int32_t num_blocks;
     int32_t *err_flag;
+    uint64_t wait_ns;
 };
 
-cudaError_t launch_rope_append(const RopeParams &p, bool interleaved, bool fp8, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams &p, bool interleaved, bool fp8, int sms, cudaStream_t stream);
 
 // Element-wise minimum and maximum of the keys of every block that holds one of a sequence's last
 // num_new tokens (pkv_select.cu): bounds [num_blocks][K][2][H].  span: blocks per sequence at most.
@@ -65,20 +66,17 @@ struct SelectParams {
     int32_t max_nb, B, N, K, G, num_blocks;
     int32_t first, last, M;
     int32_t *selected;             // [B][K][M]
-    // workspace (select_workspace): scores and exact sums by logical block, the list of the blocks
-    // whose scores cannot be told apart in 32 bits, the largest |bound| of each chunk, counters
+    // workspace: scores by logical block; sums in 64 bits and the list of the blocks whose scores cannot be
+    // told apart in 32 bits; the largest |bound| of each tile of 16 blocks
     float *scores;                 // [B][K][max_nb]
     double *exact;                 // [B][K][max_nb]
     int32_t *list;                 // [B][K][max_nb]
-    float *chunk_max;              // [B][K][chunks]
-    int32_t *counters;             // [B][K], zero between calls
-    int32_t chunks;                // chunks of kSelectChunk blocks that cover max_nb
+    float *tile_max;               // [B][K][tiles]
+    int32_t tiles;                 // tiles that cover max_nb blocks
     int32_t *err_flag;
 };
 
-constexpr int kSelectChunk = 128;  // logical blocks scored by one CTA
-
-cudaError_t launch_select_blocks(const SelectParams &p, int H, cudaStream_t stream);
+cudaError_t launch_select_blocks(const SelectParams &p, int H, int sms, cudaStream_t stream);
 
 // Decode attention over selected blocks (pkv_attn_blocks.cu).
 struct BlocksParams {
@@ -120,14 +118,14 @@ struct VerifyParams {
     int32_t *out;                  // [B][T + 1]
     const int32_t *context_lens;   // [B], nullable
     int32_t *context_lens_out;     // [B]
-    long long *sums;               // workspace [B][chunks]
+    long long *sums;               // workspace [B][runs]
     int32_t *counters;             // [B], zero between calls
-    int32_t chunks;
+    int32_t run;                   // entries of a warp's run (set by the launcher)
     int32_t *err_flag;
 };
 
-constexpr int kVerifyChunk = 4096;  // vocabulary entries summed by one CTA
+constexpr int kVerifyRun = 256;  // a run of the vocabulary summed by one warp is a multiple of this
 
-cudaError_t launch_verify(const VerifyParams &p, bool bf16, cudaStream_t stream);
+cudaError_t launch_verify(VerifyParams p, bool bf16, int sms, cudaStream_t stream);
 
 }  // namespace pkv

@@ -4,33 +4,65 @@
 // Token i at position P turns element pair (a, b) of a head by the angle P * inv_freq[j]:
 //     a' = a cos - b sin,   b' = a sin + b cos,   j < R / 2,
 // pair j being elements (j, j + R/2) or, interleaved, (2j, 2j + 1); elements from R on are copied.
-// q goes to q_out, k into its slot of the K pool, v unturned into its slot of the V pool: what the
-// separate rotation would write and the append read back never leaves the chip.
+// q goes to q_out, k into its slot of the K pool, v unturned into its slot of the V pool: what a
+// separate rotation would write and an append read back never leaves the chip.
 //
-// The angle.  P * inv_freq in 32 bits is off by whole radians for far positions, so turns =
-// P * inv_freq / (2 pi) and its distance to the nearest integer are taken in 64 bits (absolute error
-// below 2^-52 of the turns: 1e-7 of a turn at position 2^31), and only that distance is rounded to
-// 32 bits for sincospif.  The R / 2 angles of a token are computed once and shared by its N + K heads.
+// The angle.  P * inv_freq in 32 bits is off by whole radians for far positions.  Only the fraction of
+// a turn counts, so each frequency is taken once, in 64 bits, as a fraction of a turn per position in
+// units of 2^-64; the product with the position then wraps around a turn by itself, in integers.  The
+// fraction is off by 2^-54 turns (inv_freq's and 1/2pi's roundings) and the angle by P times that:
+// 10^-10 of a turn at position 10^6, 10^-7 at 2^31.  Its upper 32 bits go to sincospif.
 //
-// Bound by memory: a token moves (N + 2K) * H elements each way and computes 6 operations a pair.
-// One CTA per token: a thread's loads (two 16-byte vectors an item, up to kItems items) are issued
-// before the token's position, slot and angles are there, and need none of them.  A token whose slot
-// is negative is left out: nothing of its rows is written.
+// Bound by memory: a token moves (N + 2K) H elements each way and computes 6 operations a pair.  The work is cut into
+// units of kUnitHeads heads of one token (q's, then k's, then v's); a CTA takes every gridDim-th unit and streams
+// the units' rows through a ring in shared memory with bulk copies, so that the loads under way need no
+// registers and the arithmetic (the e4m3 form's quotients above all) has enough warps; results go straight to global
+// memory.  A token whose slot is negative is left out: nothing of its rows is written.
+//
+// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 34.8 us (5.8 TB/s, 85% of the measured
+// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 55 us (4.7 TB/s, 69%): bound by issue
+// slots (72% busy; the quotients are a third of the instructions).
 #include "pkv_device.cuh"
 #include "pkv_ops.h"
 
 namespace pkv {
 
-constexpr int kRopeThreads = 192;
-constexpr int kRopeItems = 2;  // items a thread holds at a time
+// Threads, heads of a unit, stages and CTAs per SM, measured on 8,192 tokens of 32 + 2 * 8 heads (bf16) and 5,001 of
+// 40 + 2 * 40 (e4m3): 256 / 64 / 2 / 4 34.8 and 55.0 us; 192 / 48 / 3 / 5 34.6 and 60.1 (three units a token instead
+// of two); 192 / 48 / 2 / 6 36.1 and 68.6; 128 / 32 / 3 / 8 46.2 and 64.2; 384 / 96 / 2 / 3 42.8 and 83.4.
+constexpr int kRopeThreads = 256;
+constexpr int kUnitHeads = 64;
+constexpr int kRopeStages = 2;
+constexpr int kRopeCtasPerSm = 4;
 constexpr double kInv2Pi = 0.15915494309189533577;
 
-__device__ __forceinline__ uint2 rope_quantize8(const float (&x)[8], float sc)
+// Eight values as e4m3 codes of x / scale, the quotient rounded to nearest in fp32 as the plain append takes it (the
+// input is the rotation's 32-bit result, so a turned key is rounded once to 8 bits).  Markstein's theorem (IBM J.
+// Res. Dev. 34, 1990): with r = 1 / scale rounded to nearest and y within an ulp of the quotient,
+// y + (x - y scale) r, both operations fused, is the quotient rounded to nearest.  r + s is the reciprocal to twice
+// the precision, so y = x r + x s is off by little more than half an ulp.  Nothing over- or underflows where it
+// matters: x is cut off at 512 scale (codes end at 448; NaN stays), quotients below 2^-11 are code 0 whatever their
+// last bits, and scales beyond 2^+-80 are brought nearer to 1 together with x.  Checking a plain x r against both
+// neighbouring codes and dividing where they differ measured 55 against 50 us on 5,001 tokens of 3 * 40 heads.
+__device__ __forceinline__ uint2 rope_quantize8(float (&x)[8], float sc)
 {
-    // e4m3(x / scale), the division rounded to nearest, as the plain append quantizes; x is the
-    // rotation's 32-bit result, so a rotated key is rounded once
-    auto q2 = [&](int i) -> uint32_t { return f32x2_to_e4m3x2(__fdiv_rn(x[i], sc), __fdiv_rn(x[i + 1], sc)); };
-    return make_uint2(q2(0) | (q2(2) << 16), q2(4) | (q2(6) << 16));
+    if (sc < 0x1p-80f || sc > 0x1p80f) {
+        const float k = sc < 1.f ? 0x1p100f : 0x1p-100f;
+        sc *= k;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= k;
+    }
+    const float r = __frcp_rn(sc), s = __fmaf_rn(-r, sc, 1.f) * r, most = 512.f * sc;
+    uint32_t c[4];
+    auto quotient = [&](float v) {
+        float w;
+        asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(w) : "f"(v), "f"(most));
+        const float y = __fmaf_rn(w, r, w * s);
+        return __fmaf_rn(__fmaf_rn(-y, sc, w), r, y);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(quotient(x[2 * i]), quotient(x[2 * i + 1]));
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 __device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8])
@@ -45,157 +77,248 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
                       pack_bf16x2(x[6], x[7]));
 }
 
-// Slot and position of token i; false: nothing is written for it.
-__device__ __forceinline__ bool rope_slot(const RopeParams &p, int64_t i, bool report, int64_t &slot, int &pos)
+// Slot and position of token i (slot < 0: nothing is written for it).
+__device__ __forceinline__ void rope_slot(const RopeParams &p, int i, bool report, int64_t &slot, int &pos)
 {
     if (!p.block_tables) {
         slot = p.slots[i];
         pos = p.positions[i];
         if (slot >= (int64_t)p.num_blocks * kBlockSize) {
             if (report) set_flag(p.err_flag, PKV_FLAG_SLOT_RANGE);
-            return false;
+            slot = -1;
         }
-        return slot >= 0;
+        return;
     }
-    const int b = (int)(i / p.T), t = (int)(i - (int64_t)b * p.T);
+    const int b = i / p.T, t = i - b * p.T;
     const int ctx = p.context_lens[b];
     slot = -1;
-    pos = ctx - p.T + t;
+    pos = 0;
     if (ctx > p.max_nb * kBlockSize) {
         if (report) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
-        pos = 0;
-    } else if (ctx > 0 && pos >= 0) {
+    } else if (ctx > 0 && t >= p.T - ctx) {
+        pos = ctx - p.T + t;
         const int blk = p.block_tables[(size_t)b * p.max_nb + pos / kBlockSize];
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (report) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-        } else {
-            slot = (int64_t)blk * kBlockSize + pos % kBlockSize;
-        }
+        if (blk >= 0 && blk < p.num_blocks) slot = (int64_t)blk * kBlockSize + pos % kBlockSize;
+        else if (report) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
     }
     if (report) p.slots_out[i] = slot;
-    return slot >= 0;
 }
 
-template <bool kInter, bool kFp8>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p)
+// 1-D bulk copy global -> this CTA's shared memory, counted on the mbarrier (16-byte addresses and size).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    extern __shared__ float2 cs[];  // [R / 2] (cos, sin)
-    const int64_t i = blockIdx.x;
-    const int per_head = p.H / 16, nq = p.N * per_head, nk = p.K * per_head;
-    const int items = nq + 2 * nk;
-    const int rot = p.R / 16;  // rotated items of a head; the others copy 16 neighbouring elements
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
-    // The two vectors of item x: rows of q, then k_new, then v_new.
-    auto offsets = [&](int x, int &o0, int &o1, bool &turned) {
-        const int c = x % per_head, head = x / per_head;
-        turned = x < nq + nk && c < rot;
-        o0 = head * p.H + (turned && !kInter ? 8 * c : 16 * c);
-        o1 = turned && !kInter ? o0 + p.R / 2 : o0 + 8;
+template <int H, bool kInter, bool kFp8>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kernel(const RopeParams p)
+{
+    constexpr int S = kRopeStages, kPerHead = H / 16;  // items (two 16-byte vectors) of a head
+    constexpr int kStageBytes = kUnitHeads * H * 2;
+    extern __shared__ __align__(128) uint8_t ring[];  // [S][kUnitHeads][H] bf16
+    // (cos, sin) of this unit's token and of the next one's, two pairs a vector: vector (e / 2) * kGroups + g holds
+    // pairs e, e + 1 of group g, so that neighbouring threads, who turn neighbouring groups, read neighbouring vectors.
+    // A group is what one thread reads in a row: 8 pairs, interleaved 4.
+    constexpr int kPairs = kInter ? 4 : 8, kGroups = H / 2 / kPairs;
+    __shared__ float4 cs[2][H / 4];
+    __shared__ int64_t slot_of[4];                    // of this unit and the two after it
+    __shared__ int pos_of[4];
+    __shared__ __align__(8) uint64_t full[S];
+    __shared__ int aborted;
+    const int tid = threadIdx.x;
+    const int heads = p.N + 2 * p.K;
+    const int rot = p.R / 16;  // turned items of a head; the others copy 16 neighbouring elements
+    // Units are (token, chunk of heads) pairs; from one to the next of this CTA's, gridDim.x units on, without a division.
+    const int chunks = (heads + kUnitHeads - 1) / kUnitHeads, per = (heads + chunks - 1) / chunks;
+    const int step_i = gridDim.x / chunks, step_c = gridDim.x - step_i * chunks;
+    struct Unit {
+        int i, chunk;
     };
-    auto source = [&](int x) {
-        return x < nq ? p.q + i * p.N * p.H
-                      : (x < nq + nk ? p.k_new + i * p.K * p.H - (int64_t)p.N * p.H
-                                     : p.v_new + i * p.K * p.H - (int64_t)(p.N + p.K) * p.H);
+    auto advance = [&](Unit &t) {
+        t.i += step_i;
+        t.chunk += step_c;
+        if (t.chunk >= chunks) t.chunk -= chunks, ++t.i;
     };
-    uint4 a[kRopeItems], b[kRopeItems];
-    auto load = [&](int x0) {
-#pragma unroll
-        for (int u = 0; u < kRopeItems; ++u) {
-            const int x = x0 + u * kRopeThreads;
-            if (x < items) {
-                int o0, o1;
-                bool turned;
-                offsets(x, o0, o1, turned);
-                const uint16_t *src = source(x);
-                a[u] = *reinterpret_cast<const uint4 *>(src + o0);
-                b[u] = *reinterpret_cast<const uint4 *>(src + o1);
-            }
+
+    // Rows of a unit: up to three runs of heads, of q, k_new and v_new.
+    auto load = [&](const Unit &t, int stage) {
+        const int h0 = t.chunk * per, h1 = min(heads, h0 + per);
+        const uint32_t bar = smem_u32(full + stage), dst = smem_u32(ring) + stage * kStageBytes;
+        mbar_arrive_expect_tx(bar, (uint32_t)(h1 - h0) * H * 2);
+        auto part = [&](const uint16_t *src, int from, int to) {  // heads [from, to) of all, src at head `from`
+            const int a = max(from, h0), b = min(to, h1);
+            if (a < b) bulk_load(dst + (a - h0) * H * 2, src + (int64_t)(a - from) * H, (uint32_t)(b - a) * H * 2, bar);
+        };
+        part(p.q + (int64_t)t.i * p.N * H, 0, p.N);
+        part(p.k_new + (int64_t)t.i * p.K * H, p.N, p.N + p.K);
+        part(p.v_new + (int64_t)t.i * p.K * H, p.N + p.K, heads);
+    };
+    const int first = blockIdx.x / chunks;
+    Unit now{first, (int)blockIdx.x - first * chunks}, ahead = now;  // ahead: the next unit to load
+    int copied = 0;  // units whose loads were issued (thread 0)
+    if (tid == 0) {
+        aborted = 0;
+        for (int s = 0; s < S; ++s) mbar_init(smem_u32(full + s), 1);
+        fence_barrier_init();
+        for (; copied < S && ahead.i < p.n; ++copied, advance(ahead)) load(ahead, copied);
+    }
+    unsigned long long freq = 0;  // turns per position in units of 2^-64, of pair tid
+    if (tid < p.R / 2) {
+        const double t = p.inv_freq[tid] * kInv2Pi;
+        freq = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);  // 1.0 saturates: 2^-64 of a turn off
+    }
+    // Slots and positions are loaded three units ahead by one thread and handed on two units ahead, the angles are
+    // computed one ahead, so that a unit's vectors wait for neither.
+    Unit asked = now;
+    int64_t slot = -1;
+    int pos = 0;
+    auto ask = [&]() {
+        slot = -1;
+        if (asked.i < p.n) rope_slot(p, asked.i, asked.chunk == 0, slot, pos);
+        advance(asked);
+    };
+    auto tell = [&](int k) { slot_of[k & 3] = slot, pos_of[k & 3] = pos; };
+    if (tid == 0) {
+        ask(), tell(0), ask(), tell(1), ask();
+    }
+    __syncthreads();  // the barriers exist, the first two slots are there
+    auto turn = [&](int k) {
+        if (tid < p.R / 2) {
+            const unsigned turns = (unsigned)((freq * (unsigned long long)(long long)pos_of[k & 3]) >> 32);
+            float s, c;
+            sincospif((float)(int)turns * 0x1p-31f, &s, &c);  // the nearer way round: within half a turn
+            const int g = tid / kPairs, e = tid % kPairs;
+            reinterpret_cast<float2 *>(cs[k & 1])[2 * ((e / 2) * kGroups + g) + (e & 1)] = make_float2(c, s);
         }
     };
-    load(threadIdx.x);
-
-    int64_t slot;
-    int pos;
-    if (!rope_slot(p, i, threadIdx.x == 0, slot, pos)) return;
-    for (int j = threadIdx.x; j < p.R / 2; j += kRopeThreads) {
-        const double turns = (double)pos * p.inv_freq[j] * kInv2Pi;
-        const float f = (float)(turns - rint(turns));
-        float s, c;
-        sincospif(2.f * f, &s, &c);
-        cs[j] = make_float2(c, s);
-    }
-    __syncthreads();
-
-    for (int x0 = threadIdx.x; x0 < items; x0 += kRopeItems * kRopeThreads) {
-        if (x0 != (int)threadIdx.x) load(x0);
+    // e4m3: the scales of this thread's items of a unit, loaded one unit ahead
+    constexpr int kRounds = kFp8 ? (kUnitHeads * kPerHead + kRopeThreads - 1) / kRopeThreads : 1;
+    float sc[kRounds], sc_next[kRounds];
+    auto scales = [&](const Unit &t, int64_t slot, float (&to)[kRounds]) {
+        if (!kFp8 || t.i >= p.n || slot < 0) return;
 #pragma unroll
-        for (int u = 0; u < kRopeItems; ++u) {
-            const int x = x0 + u * kRopeThreads;
-            if (x >= items) break;
-            int o0, o1;
-            bool turned;
-            offsets(x, o0, o1, turned);
-            float y0[8], y1[8];
-            unpack8(a[u], y0);
-            unpack8(b[u], y1);
-            if (turned) {
-                const float2 *w = cs + 8 * (x % per_head);
-                if (kInter) {  // pairs (2e, 2e + 1): the first four in y0, the others in y1
+        for (int r = 0; r < kRounds; ++r) {
+            const int kvh = t.chunk * per + (tid + r * kRopeThreads) / kPerHead - p.N;
+            if (kvh >= 0 && kvh < 2 * p.K)
+                to[r] = __ldg((kvh < p.K ? p.k_scale + kvh : p.v_scale + kvh - p.K) + (slot / kBlockSize) * p.scale_stride);
+        }
+    };
+    Unit next = now;
+    advance(next);
+    scales(now, slot_of[0], sc);
+    turn(0);
+    __syncthreads();  // the first angles are there
+
+    for (int k = 0;; ++k) {
+        if (tid == 0) tell(k + 2), ask();
+        scales(next, slot_of[(k + 1) & 3], sc_next);
+        turn(k + 1);
+        const int64_t at_slot = slot_of[k & 3];
+        const int h0 = now.chunk * per, items = (min(heads, h0 + per) - h0) * kPerHead;
+        const int stage = k % S;
+        const bool there = mbar_wait_bounded(smem_u32(full + stage), (uint32_t)(k / S) & 1, nullptr, p.wait_ns);
+        if (!there) aborted = 1;
+        if (there && at_slot >= 0) {
+            const uint8_t *src = ring + stage * kStageBytes;
+            const float4 *angles = cs[k & 1];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 w0 = w[e], w1 = w[e + 4];
-                        const float p0 = y0[2 * e], p1 = y0[2 * e + 1], r0 = y1[2 * e], r1 = y1[2 * e + 1];
-                        y0[2 * e] = p0 * w0.x - p1 * w0.y;
-                        y0[2 * e + 1] = p0 * w0.y + p1 * w0.x;
-                        y1[2 * e] = r0 * w1.x - r1 * w1.y;
-                        y1[2 * e + 1] = r0 * w1.y + r1 * w1.x;
-                    }
-                } else {
+            for (int r = 0; r < (kUnitHeads * kPerHead + kRopeThreads - 1) / kRopeThreads; ++r) {
+                const int x = tid + r * kRopeThreads;
+                if (x >= items) break;
+                const int c = x % kPerHead, head = h0 + x / kPerHead;
+                const bool is_v = head >= p.N + p.K, turned = !is_v && c < rot;
+                // an item's vectors lie half of the turned (or of the copied) elements apart, so that neighbouring
+                // threads read and write neighbouring vectors
+                const int from = turned || is_v ? 0 : p.R, width = turned ? p.R : H - from;
+                const int o0 = from + 8 * (turned || is_v ? c : c - rot), o1 = o0 + width / 2;
+                const uint4 a = *reinterpret_cast<const uint4 *>(src + ((x / kPerHead) * H + o0) * 2);
+                const uint4 b = *reinterpret_cast<const uint4 *>(src + ((x / kPerHead) * H + o1) * 2);
+                float y0[8], y1[8];
+                unpack8(a, y0);
+                unpack8(b, y1);
+                if (turned) {
+                    // group c, or interleaved, group c for one vector and R / 16 + c for the other
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float2 w0 = w[e];
-                        const float p0 = y0[e], p1 = y1[e];
-                        y0[e] = p0 * w0.x - p1 * w0.y;
-                        y1[e] = p0 * w0.y + p1 * w0.x;
+                        const float4 v = angles[((e % kPairs) / 2) * kGroups + (kInter && e >= 4 ? rot + c : c)];
+                        const float co = e & 1 ? v.z : v.x, si = e & 1 ? v.w : v.y;
+                        float &r0 = kInter ? (e < 4 ? y0[2 * (e & 3)] : y1[2 * (e & 3)]) : y0[e];
+                        float &r1 = kInter ? (e < 4 ? y0[2 * (e & 3) + 1] : y1[2 * (e & 3) + 1]) : y1[e];
+                        const float f0 = r0, f1 = r1;
+                        r0 = f0 * co - f1 * si;
+                        r1 = f0 * si + f1 * co;
                     }
                 }
-            }
-            if (x < nq) {
-                uint16_t *dst = p.q_out + i * p.N * p.H;
-                *reinterpret_cast<uint4 *>(dst + o0) = turned ? pack8(y0) : a[u];
-                *reinterpret_cast<uint4 *>(dst + o1) = turned ? pack8(y1) : b[u];
-                continue;
-            }
-            const bool is_v = x >= nq + nk;
-            const int64_t row = slot * p.K * p.H - (int64_t)(is_v ? p.N + p.K : p.N) * p.H;
-            void *pool = is_v ? p.v_cache : p.k_cache;
-            if (kFp8) {
-                const int kvh = x / per_head - (is_v ? p.N + p.K : p.N);
-                const float sc = (is_v ? p.v_scale : p.k_scale)[(slot / kBlockSize) * p.scale_stride + kvh];
-                uint8_t *dst = static_cast<uint8_t *>(pool) + row;
-                *reinterpret_cast<uint2 *>(dst + o0) = rope_quantize8(y0, sc);
-                *reinterpret_cast<uint2 *>(dst + o1) = rope_quantize8(y1, sc);
-            } else {
-                uint16_t *dst = static_cast<uint16_t *>(pool) + row;
-                *reinterpret_cast<uint4 *>(dst + o0) = turned ? pack8(y0) : a[u];
-                *reinterpret_cast<uint4 *>(dst + o1) = turned ? pack8(y1) : b[u];
+                const int kvh = head - p.N - (is_v ? p.K : 0);
+                if (kFp8 && head >= p.N) {
+                    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) + (at_slot * p.K + kvh) * H;
+                    *reinterpret_cast<uint2 *>(dst + o0) = rope_quantize8(y0, sc[kFp8 ? r : 0]);
+                    *reinterpret_cast<uint2 *>(dst + o1) = rope_quantize8(y1, sc[kFp8 ? r : 0]);
+                } else {
+                    uint16_t *dst = head < p.N ? p.q_out + ((int64_t)now.i * p.N + head) * H
+                                               : static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + (at_slot * p.K + kvh) * H;
+                    *reinterpret_cast<uint4 *>(dst + o0) = turned ? pack8(y0) : a;
+                    *reinterpret_cast<uint4 *>(dst + o1) = turned ? pack8(y1) : b;
+                }
             }
         }
+        __syncthreads();  // every thread is done with this unit's stage and the next unit's angles
+        if (aborted) {
+            if (tid == 0) {  // leave no copy in flight behind
+                set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+                for (int x = k; x < copied; ++x)
+                    mbar_wait_bounded(smem_u32(full + x % S), (uint32_t)(x / S) & 1, nullptr, kDrainLimitNs);
+            }
+            __syncthreads();
+            return;
+        }
+        if (tid == 0 && ahead.i < p.n) {
+            load(ahead, stage);
+            ++copied;
+            advance(ahead);
+        }
+        if (next.i >= p.n) return;
+        now = next;
+        advance(next);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) sc[r] = sc_next[r];
     }
 }
 
-cudaError_t launch_rope_append(const RopeParams &p, bool interleaved, bool fp8, cudaStream_t stream)
+template <int H, bool kInter, bool kFp8>
+static cudaError_t launch_k(const RopeParams &p, unsigned grid, cudaStream_t stream)
 {
-    const size_t smem = sizeof(float2) * (size_t)(p.R / 2);
-    const unsigned grid = (unsigned)p.n;
-    if (interleaved) {
-        if (fp8) rope_append_kernel<true, true><<<grid, kRopeThreads, smem, stream>>>(p);
-        else rope_append_kernel<true, false><<<grid, kRopeThreads, smem, stream>>>(p);
-    } else {
-        if (fp8) rope_append_kernel<false, true><<<grid, kRopeThreads, smem, stream>>>(p);
-        else rope_append_kernel<false, false><<<grid, kRopeThreads, smem, stream>>>(p);
+    constexpr int smem = kRopeStages * kUnitHeads * H * 2;
+    static int ready[64] = {};  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(rope_append_kernel<H, kInter, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready[dev] = 1;
     }
+    rope_append_kernel<H, kInter, kFp8><<<grid, kRopeThreads, smem, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int H>
+static cudaError_t launch_t(const RopeParams &p, bool interleaved, bool fp8, int sms, cudaStream_t stream)
+{
+    const int heads = p.N + 2 * p.K;
+    const int64_t units = (int64_t)p.n * ((heads + kUnitHeads - 1) / kUnitHeads), most = (int64_t)sms * kRopeCtasPerSm;
+    const unsigned grid = (unsigned)(units < most ? units : most);
+    if (interleaved) return fp8 ? launch_k<H, true, true>(p, grid, stream) : launch_k<H, true, false>(p, grid, stream);
+    return fp8 ? launch_k<H, false, true>(p, grid, stream) : launch_k<H, false, false>(p, grid, stream);
+}
+
+cudaError_t launch_rope_append(const RopeParams &p, bool interleaved, bool fp8, int sms, cudaStream_t stream)
+{
+    return p.H == 128 ? launch_t<128>(p, interleaved, fp8, sms, stream)
+                      : launch_t<64>(p, interleaved, fp8, sms, stream);
 }
 
 }  // namespace pkv

@@ -11,11 +11,15 @@
 // The operands need no rounding (min, max and the parts of q are bf16 numbers), so a score is off by the
 // order of its fp32 sums alone.
 //
+// Two launches, the second started early (programmatic serialization): scores into the workspace, then one CTA per
+// (sequence, KV head) chooses.
+//
 // Selection.  The first F and the last L blocks, and the best of the rest, M in all, in ascending order:
 // exactly those that the scores' real values choose, ties to the lowest index.  With eps bounding the
 // error of every score, t the k-th largest score: a block above t + 2 eps is in, one below t - 2 eps is out,
 // and if those between do not all fit, their sums are taken again in 64 bits and ranked.
 #include "pkv_device.cuh"
+#include "pkv_internal.h"
 #include "pkv_ops.h"
 
 namespace pkv {
@@ -147,11 +151,12 @@ cudaError_t launch_key_bounds(const BoundsParams &p, bool fp8, int span, cudaStr
 }
 
 // -------------------------------------- selection -------------------------------------------
-constexpr int kSelectThreads = 256;
-constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kMostWarps = 16;      // of a choosing CTA
 constexpr int kBins = 2048;         // bins of one narrowing pass
 constexpr int kRankMost = 256;      // undecided blocks ranked pairwise; more go through narrowing passes
-static_assert(kSelectChunk == 16 * kSelectWarps, "a warp scores 16 blocks");
+constexpr int kFew = 64;            // keys of one bin ranked pairwise
+constexpr int kKeep = 8192;         // scores the choosing CTA keeps in shared memory (131,072 tokens); longer
+                                    // contexts read them from L2 in every pass
 
 // Order-preserving maps to unsigned integers; NaN counts as +inf (such a block is attended to, so the NaN
 // shows in the output instead of being left out), and -0 as +0.
@@ -171,16 +176,18 @@ __device__ __forceinline__ unsigned long long order_key(double x)
 
 struct SelectShared {
     uint32_t hist[kBins];
-    uint32_t warp_sum[kSelectWarps + 1];
-    unsigned long long lo, hi;       // range of a narrowing pass
-    uint32_t above;        // keys above the chosen bin
-    uint32_t count;
-    float eps, q1;
+    uint32_t warp_sum[2][kMostWarps];
+    unsigned long long range[2][kMostWarps];
+    unsigned long long lo, hi;  // range of a narrowing pass
+    uint32_t above, inside;     // keys above the chosen bin, and in it
+    uint32_t few_n;
+    unsigned long long few[kFew];
+    float bound[2][kMostWarps];  // |q|_1 and the largest |bound|, by warp
     double exact[kRankMost];
-    int last_one;
 };
 
-// Exclusive prefix sum over the CTA of one value per thread; total gets the sum.
+// Sum and exclusive prefix sum over the CTA of one value per thread.
+template <int NT>
 __device__ __forceinline__ uint32_t block_exclusive(SelectShared &s, uint32_t v, uint32_t &total)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -191,12 +198,12 @@ __device__ __forceinline__ uint32_t block_exclusive(SelectShared &s, uint32_t v,
         if (lane >= off) inc += o;
     }
     __syncthreads();
-    if (lane == 31) s.warp_sum[warp] = inc;
+    if (lane == 31) s.warp_sum[0][warp] = inc;
     __syncthreads();
     uint32_t before = 0, sum = 0;
 #pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
-        const uint32_t x = s.warp_sum[w];
+    for (int w = 0; w < (NT / 32); ++w) {
+        const uint32_t x = s.warp_sum[0][w];
         before += w < warp ? x : 0u;
         sum += x;
     }
@@ -204,63 +211,87 @@ __device__ __forceinline__ uint32_t block_exclusive(SelectShared &s, uint32_t v,
     return before + inc - v;
 }
 
-// The k-th largest (k >= 1) of the n keys key(0..n-1), and the number of keys above it.  Narrowing passes:
-// the keys' range is cut into up to 2048 bins, the bin that holds the k-th becomes the range; a bin is
-// 2^shift keys wide, so a pass takes eleven bits off the range, whatever the keys are.  The first range is
-// that of the keys themselves: scores of one query lie within a few powers of two and spread over the
-// bins, so the shared-memory atomics seldom meet.
-template <typename Key, typename F>
-__device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F key, uint32_t &above)
+// The k-th largest (k >= 1) of the n keys key(0 .. n-1), whose smallest and largest are mn and mx over this
+// thread's share (any split over the CTA), and the number of keys above it.  Narrowing passes: the keys' range
+// is cut into up to 2048 bins and the bin that holds the k-th becomes the range; a bin is 2^shift keys
+// wide, so a pass takes eleven bits off the range whatever the keys are.  The first range is that of the keys
+// themselves: the scores of one query lie within a few powers of two and spread over the bins, so shared-memory
+// atomics seldom meet, and one pass nearly always leaves few enough keys to rank them pairwise.
+template <int NT, typename Key, typename F>
+__device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F key, Key mn, Key mx, uint32_t &above)
 {
     const int tid = threadIdx.x;
-    Key mn = ~Key(0), mx = 0;
-    for (int i = tid; i < n; i += kSelectThreads) {
-        const Key x = key(i);
-        mn = min(mn, x);
-        mx = max(mx, x);
-    }
+    constexpr int kMine = kBins / NT;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         mn = min(mn, (Key)__shfl_xor_sync(0xFFFFFFFFu, mn, off));
         mx = max(mx, (Key)__shfl_xor_sync(0xFFFFFFFFu, mx, off));
     }
     __syncthreads();
-    if (tid == 0) s.lo = ~0ull, s.hi = 0ull, s.above = 0u;
+    if ((tid & 31) == 0) s.range[0][tid >> 5] = mn, s.range[1][tid >> 5] = mx;
     __syncthreads();
-    if ((tid & 31) == 0) {
-        atomicMin(&s.lo, (unsigned long long)mn);
-        atomicMax(&s.hi, (unsigned long long)mx);
+    unsigned long long all_lo = s.range[0][0], all_hi = s.range[1][0];
+#pragma unroll
+    for (int w = 1; w < (NT / 32); ++w) {
+        all_lo = min(all_lo, s.range[0][w]);
+        all_hi = max(all_hi, s.range[1][w]);
     }
-    __syncthreads();
-    Key lo = (Key)s.lo, hi = (Key)s.hi;
-    uint32_t up = 0;  // keys above hi
+    Key lo = (Key)all_lo, hi = (Key)all_hi;
+    uint32_t up = 0, inside = (uint32_t)n;  // keys above hi, keys in [lo, hi]
     while (lo < hi) {
+        if (inside <= kFew) {
+            if (tid == 0) s.few_n = 0u;
+            __syncthreads();
+            for (int i = tid; i < n; i += NT) {
+                const Key x = key(i);
+                if (x >= lo && x <= hi) s.few[atomicAdd(&s.few_n, 1u)] = (unsigned long long)x;
+            }
+            __syncthreads();
+            if (tid < (int)inside) {
+                const Key x = (Key)s.few[tid];
+                uint32_t more = up, same = 0;
+                for (uint32_t o = 0; o < inside; ++o) {
+                    more += (Key)s.few[o] > x;
+                    same += (Key)s.few[o] == x;
+                }
+                if (more < k && more + same >= k) {  // equal keys write equal values
+                    s.lo = (unsigned long long)x;
+                    s.above = more;
+                }
+            }
+            __syncthreads();
+            lo = (Key)s.lo;
+            up = s.above;
+            break;
+        }
         const int bits = 64 - __clzll((long long)(unsigned long long)(hi - lo));
         const int shift = max(0, bits - 11);
-        for (int x = tid; x < kBins; x += kSelectThreads) s.hist[x] = 0u;
+#pragma unroll
+        for (int x = 0; x < kMine; ++x) s.hist[tid + x * NT] = 0u;
         __syncthreads();
-        for (int i = tid; i < n; i += kSelectThreads) {
+        for (int i = tid; i < n; i += NT) {
             const Key x = key(i);
             if (x >= lo && x <= hi) atomicAdd(&s.hist[(uint32_t)((x - lo) >> shift)], 1u);
         }
         __syncthreads();
-        // bins from the top: thread t holds bins [kBins - 8 (t + 1), kBins - 8 t)
-        uint32_t mine[kBins / kSelectThreads], sum = 0, total;
-        const int b0 = kBins - (kBins / kSelectThreads) * (tid + 1);
+        // bins from the top: thread t holds bins [kBins - kMine (t + 1), kBins - kMine t)
+        uint32_t mine[kMine], sum = 0, total;
+        const int b0 = kBins - kMine * (tid + 1);
 #pragma unroll
-        for (int x = 0; x < kBins / kSelectThreads; ++x) {
+        for (int x = 0; x < kMine; ++x) {
             mine[x] = s.hist[b0 + x];
             sum += mine[x];
         }
-        uint32_t before = up + block_exclusive(s, sum, total);
+        uint32_t before = up + block_exclusive<NT>(s, sum, total);
         if (before < k && before + sum >= k) {  // one thread: the k-th is in one of its bins
 #pragma unroll
-            for (int x = kBins / kSelectThreads - 1; x >= 0; --x) {
+            for (int x = kMine - 1; x >= 0; --x) {
                 if (before < k && before + mine[x] >= k) {
                     const unsigned long long from = (unsigned long long)lo + ((unsigned long long)(b0 + x) << shift);
                     s.lo = from;
                     s.hi = min((unsigned long long)hi, from + min((1ull << shift) - 1, ~from));  // no wrap at the top
                     s.above = before;
+                    s.inside = mine[x];
                 }
                 before += mine[x];
             }
@@ -269,6 +300,7 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
         lo = (Key)s.lo;
         hi = (Key)s.hi;
         up = s.above;
+        inside = s.inside;
         __syncthreads();
     }
     above = up;
@@ -281,18 +313,24 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
 template <int H>
 __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int kvh, int j, int lane)
 {
+    constexpr int E = H / 32;  // neighbouring elements of a lane
+    const double kInf = __longlong_as_double(0x7FF0000000000000ll);
     const int blk = __ldg(p.block_tables + (size_t)b * p.max_nb + j);
-    if (blk < 0 || blk >= p.num_blocks) return -__longlong_as_double(0x7FF0000000000000ll);
-    const uint16_t *lo = p.bounds + ((int64_t)blk * p.K + kvh) * 2 * H, *hi = lo + H;
-    const uint16_t *q = p.q + ((size_t)b * p.N + (size_t)kvh * p.G) * H;
-    double best = -__longlong_as_double(0x7FF0000000000000ll);
+    if (blk < 0 || blk >= p.num_blocks) return -kInf;
+    const uint16_t *row = p.bounds + ((int64_t)blk * p.K + kvh) * 2 * H + lane * E;
+    const uint16_t *q = p.q + ((size_t)b * p.N + (size_t)kvh * p.G) * H + lane * E;
+    float lo[E], hi[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) lo[e] = bf16_to_f32(row[e]), hi[e] = bf16_to_f32(row[H + e]);
+    double best = -kInf;
     bool nan = false;
+#pragma unroll 4
     for (int g = 0; g < p.G; ++g) {
         double sum = 0.0;
-        for (int h = lane; h < H; h += 32) {
-            const float x = bf16_to_f32(q[g * H + h]);
-            const float y = bf16_to_f32(x > 0.f ? hi[h] : lo[h]);
-            sum += (double)(x * y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float x = bf16_to_f32(q[g * H + e]);
+            sum += (double)(x * (x > 0.f ? hi[e] : lo[e]));
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
@@ -302,39 +340,68 @@ __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int 
     return nan ? __longlong_as_double(0x7FF8000000000000ll) : best;
 }
 
-// Writes the blocks j in [0, nb) with take(j) to dst in ascending order (at most `most`).  Each warp
-// counts, then writes, a contiguous run of blocks; take is called twice for each j.
-template <typename Take>
-__device__ __forceinline__ uint32_t compact(SelectShared &s, int nb, Take take, int32_t *dst, uint32_t most)
+// A warp's contiguous run of the blocks [0, nb): the runs in warp order are the blocks in ascending order.
+template <int NT>
+__device__ __forceinline__ void warp_run(int nb, int &begin, int &end)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = ((nb + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-    const int begin = min(nb, warp * per), end = min(nb, begin + per);
-    uint32_t n = 0;
-    for (int j0 = begin; j0 < end; j0 += 32)
-        n += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < end && take(j0 + lane)));
-    __syncthreads();
-    if (lane == 0) s.warp_sum[warp] = n;
-    __syncthreads();
-    uint32_t at = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
-        at += w < warp ? s.warp_sum[w] : 0u;
-        total += s.warp_sum[w];
-    }
+    const int per = ((nb + (NT / 32) - 1) / (NT / 32) + 31) / 32 * 32;
+    begin = min(nb, (int)(threadIdx.x >> 5) * per);
+    end = min(nb, begin + per);
+}
+
+// Writes the blocks j in [0, nb) with take(j) to dst in ascending order; before: those of the earlier warps' runs.
+template <int NT, typename Take>
+__device__ __forceinline__ void write_run(int nb, Take take, uint32_t before, int32_t *dst, uint32_t most)
+{
+    const int lane = threadIdx.x & 31;
+    int begin, end;
+    warp_run<NT>(nb, begin, end);
     for (int j0 = begin; j0 < end; j0 += 32) {
         const bool in = j0 + lane < end && take(j0 + lane);
         const unsigned m = __ballot_sync(0xFFFFFFFFu, in);
-        const uint32_t o = at + __popc(m & ((1u << lane) - 1u));
+        const uint32_t o = before + __popc(m & ((1u << lane) - 1u));
         if (in && o < most) dst[o] = j0 + lane;
-        at += __popc(m);
+        before += __popc(m);
     }
-    return min(total, most);
 }
 
-// The last CTA of a (sequence, KV head) chooses, from the scores that the chunks left.
-template <int H>
-__device__ __forceinline__ void choose(SelectShared &s, const SelectParams &p, int b, int kvh, int nb, int chunks)
+// Over the blocks [0, nb): how many a(j) and b(j) hold for, in all and in the runs of earlier warps.
+struct Counts {
+    uint32_t all_a, all_b, before_a, before_b;
+};
+
+template <int NT, typename A, typename B>
+__device__ __forceinline__ Counts count_runs(SelectShared &s, int nb, A a, B b)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int begin, end;
+    warp_run<NT>(nb, begin, end);
+    uint32_t na = 0, nbb = 0;
+    for (int j0 = begin; j0 < end; j0 += 32) {
+        const bool here = j0 + lane < end;
+        na += __popc(__ballot_sync(0xFFFFFFFFu, here && a(j0 + lane)));
+        nbb += __popc(__ballot_sync(0xFFFFFFFFu, here && b(j0 + lane)));
+    }
+    __syncthreads();
+    if (lane == 0) s.warp_sum[0][warp] = na, s.warp_sum[1][warp] = nbb;
+    __syncthreads();
+    Counts c{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < (NT / 32); ++w) {
+        const uint32_t x = s.warp_sum[0][w], y = s.warp_sum[1][w];
+        c.all_a += x;
+        c.all_b += y;
+        c.before_a += w < warp ? x : 0u;
+        c.before_b += w < warp ? y : 0u;
+    }
+    return c;
+}
+
+// The choice of one (sequence, KV head) from its scores.  q1: this warp's share of the largest |q|_1 over the
+// group's heads; kKept: the candidates' keys fit in keep (shared memory).
+template <int H, int NT, bool kKept>
+__device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const SelectParams &p, int b, int kvh, int nb,
+                                       float q1)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t unit = (size_t)b * p.K + kvh;
@@ -342,213 +409,390 @@ __device__ __forceinline__ void choose(SelectShared &s, const SelectParams &p, i
     int32_t *sel = p.selected + unit * p.M;
     const int first = p.first, n = nb - p.first - p.last;  // candidates: blocks first .. first + n - 1
     const uint32_t k = (uint32_t)(p.M - p.first - p.last);  // 0 <= k < n
+    auto middle = [&](int j) { return j >= first && j < first + n; };
+    if (k == 0) {
+        const Counts c = count_runs<NT>(s, nb, [&](int j) { return !middle(j); }, [](int) { return false; });
+        write_run<NT>(nb, [&](int j) { return !middle(j); }, c.before_a, sel, (uint32_t)p.M);
+        return;
+    }
 
-    // eps: 2^-14 |q|_1 max|bound|.  A product of depth 2H = 256 is 16 mma of 16 products each.  Each product is at
-    // most its part of S = |q|_1 max|bound|, no partial sum exceeds S, and an mma that keeps 23 bits below its
-    // largest term loses at most 2^-23 S for each of its 17 terms and once more at its end: 16 * 18 * 2^-23 S,
-    // and as much again for slack in what the documentation leaves open about the sum's rounding.
-    if (k > 0) {
-        float q1 = 0.f, mb = 0.f;
-        for (int g = warp; g < p.G; g += kSelectWarps) {
-            float x = 0.f;
-            for (int h = lane; h < H; h += 32) x += fabsf(bf16_to_f32(p.q[((size_t)b * p.N + (size_t)kvh * p.G + g) * H + h]));
+    // the scores, as keys; their range; |q|_1 and the largest |bound|
+    uint32_t mn = ~0u, mx = 0u;
+    auto load = [&](int i) { return order_key(__ldcg(scores + first + i)); };
+    {
+        constexpr int U = 8;  // loads in flight a thread
+        for (int i0 = tid; i0 < n; i0 += U * NT) {
+            uint32_t x[U];
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-            q1 = fmaxf(q1, x);
-        }
-        for (int c = tid; c < chunks; c += kSelectThreads) mb = fmaxf(mb, __ldcg(p.chunk_max + unit * p.chunks + c));
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * NT < n) x[u] = load(i0 + u * NT);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
-        if (tid == 0) s.q1 = 0.f, s.eps = 0.f;
-        __syncthreads();
-        if (lane == 0) {  // non-negative floats order like their bits
-            atomicMax(reinterpret_cast<int *>(&s.q1), __float_as_int(q1));
-            atomicMax(reinterpret_cast<int *>(&s.eps), __float_as_int(mb));
-        }
-        __syncthreads();
-        const float eps2 = 2.f * ldexpf(s.q1 * s.eps, -14);
-        auto key = [&](int i) { return order_key(__ldcg(scores + first + i)); };
-        uint32_t above;
-        const uint32_t kt = kth_largest<uint32_t>(s, n, k, key, above);
-        const float t = __uint_as_float(kt & 0x80000000u ? kt & 0x7FFFFFFFu : ~kt);
-        // bounds of the undecided scores, rounded outwards; both ends at t where eps2 is no number
-        const uint32_t kin = eps2 == eps2 ? max(kt, order_key(__fadd_ru(t, eps2))) : ~0u;
-        const uint32_t kout = eps2 == eps2 ? min(kt, order_key(__fadd_rd(t, -eps2))) : 0u;
-        auto score_key = [&](int j) { return order_key(__ldcg(scores + j)); };
-        auto middle = [&](int j) { return j >= first && j < first + n; };
-        uint32_t n_in = 0, n_amb = 0;
-        for (int i = tid; i < n; i += kSelectThreads) {
-            const uint32_t x = key(i);
-            n_in += x > kin;
-            n_amb += x <= kin && x >= kout;
-        }
-        uint32_t sum_in, sum_amb;
-        block_exclusive(s, n_in, sum_in);
-        block_exclusive(s, n_amb, sum_amb);
-        const uint32_t need = k - sum_in;
-        if (sum_amb > need) {
-            // more undecided blocks than places: rank them by their sums in 64 bits
-            int32_t *list = p.list + unit * p.max_nb;
-            compact(s, nb, [&](int j) { return middle(j) && score_key(j) <= kin && score_key(j) >= kout; }, list, sum_amb);
-            __syncthreads();
-            const int m = (int)sum_amb;
-            double *exact = m <= kRankMost ? s.exact : p.exact + unit * p.max_nb;
-            for (int a = warp; a < m; a += kSelectWarps) {
-                const double x = exact_score<H>(p, b, kvh, list[a], lane);
-                if (lane == 0) exact[a] = x;
-            }
-            __syncthreads();
-            if (m <= kRankMost) {
-                for (int a = tid; a < m; a += kSelectThreads) {
-                    const unsigned long long x = order_key(exact[a]);
-                    uint32_t rank = 0;  // the list ascends, so among equals the earlier one goes first
-                    for (int o = 0; o < m; ++o) {
-                        const unsigned long long y = order_key(exact[o]);
-                        rank += y > x || (y == x && o < a);
-                    }
-                    scores[list[a]] = rank < need ? INFINITY : -INFINITY;
-                }
-            } else {
-                uint32_t over;
-                const unsigned long long xt = kth_largest<unsigned long long>(s, m, need, [&](int a) { return order_key(exact[a]); }, over);
-                // of the sums equal to the need-th one, the first need - over in the list
-                uint32_t ties = need - over, run = 0;
-                for (int a0 = 0; a0 < m; a0 += kSelectThreads) {
-                    const int a = a0 + tid;
-                    const unsigned long long x = a < m ? order_key(exact[a]) : 0ull;
-                    const bool tie = a < m && x == xt;
-                    uint32_t total;
-                    const uint32_t before = run + block_exclusive(s, tie ? 1u : 0u, total);
-                    run += total;
-                    if (a < m) scores[list[a]] = x > xt || (tie && before < ties) ? INFINITY : -INFINITY;
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * NT;
+                if (i < n) {
+                    mn = min(mn, x[u]);
+                    mx = max(mx, x[u]);
+                    if constexpr (kKept) keep[first + i] = x[u];
                 }
             }
-            __syncthreads();
-            // decided: above the band, or raised to +inf
-            compact(s, nb, [&](int j) { return !middle(j) || score_key(j) > kin || __ldcg(scores + j) == INFINITY; }, sel, (uint32_t)p.M);
-        } else {
-            compact(s, nb, [&](int j) { return !middle(j) || score_key(j) >= kout; }, sel, (uint32_t)p.M);
+        }
+    }
+    float mb = 0.f;
+    for (int c = tid; c < (nb + 15) / 16; c += NT) mb = fmaxf(mb, __ldcg(p.tile_max + unit * p.tiles + c));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
+    if (lane == 0) s.bound[0][warp] = q1, s.bound[1][warp] = mb;  // read behind the barriers that follow
+    auto at = [&](int j) -> uint32_t {  // key of block j
+        if constexpr (kKept) return keep[j];
+        else return order_key(__ldcg(scores + j));
+    };
+    uint32_t above;
+    const uint32_t kt = kth_largest<NT, uint32_t>(s, n, k, [&](int i) { return at(first + i); }, mn, mx, above);
+    const float t = __uint_as_float(kt & 0x80000000u ? kt & 0x7FFFFFFFu : ~kt);
+    // eps: 2^-17 |q|_1 max|bound| = 2^-17 S.  A score is the sum of eight chains of at most two mma of 16 products.  No
+    // product and no partial sum of a chain exceeds the chain's part S' of S; an mma that keeps 23 bits below its
+    // largest term loses at most 2^-23 S' for each of its 17 terms and once more at its end, the three levels of fp32
+    // additions 2^-24 S each: (2 * 18 + 2) 2^-23 S, and over half as much again for slack in what the documentation
+    // leaves open about the rounding inside an mma.
+    float all_q = s.bound[0][0], all_b = s.bound[1][0];
+#pragma unroll
+    for (int w = 1; w < (NT / 32); ++w) {
+        all_q = fmaxf(all_q, s.bound[0][w]);
+        all_b = fmaxf(all_b, s.bound[1][w]);
+    }
+    const float eps2 = 2.f * ldexpf(all_q * all_b, -17);
+    // bounds of the undecided scores, rounded outwards; everything is undecided where eps2 is no number
+    const uint32_t kin = eps2 == eps2 ? max(kt, order_key(__fadd_ru(t, eps2))) : ~0u;
+    const uint32_t kout = eps2 == eps2 ? min(kt, order_key(__fadd_rd(t, -eps2))) : 0u;
+    const Counts c = count_runs<NT>(s, nb, [&](int j) { return !middle(j) || at(j) >= kout; },
+                                [&](int j) { return middle(j) && at(j) <= kin && at(j) >= kout; });
+    if (c.all_a == (uint32_t)p.M) {  // nothing left to decide
+        write_run<NT>(nb, [&](int j) { return !middle(j) || at(j) >= kout; }, c.before_a, sel, (uint32_t)p.M);
+        return;
+    }
+    // more undecided blocks than places: rank them by their sums in 64 bits
+    const uint32_t need = (uint32_t)p.M - (c.all_a - c.all_b);
+    const int m = (int)c.all_b;
+    int32_t *list = p.list + unit * p.max_nb;
+    write_run<NT>(nb, [&](int j) { return middle(j) && at(j) <= kin && at(j) >= kout; }, c.before_b, list, c.all_b);
+    __syncthreads();
+    double *exact = m <= kRankMost ? s.exact : p.exact + unit * p.max_nb;
+    for (int a = warp; a < m; a += (NT / 32)) {
+        const double x = exact_score<H>(p, b, kvh, list[a], lane);
+        if (lane == 0) exact[a] = x;
+    }
+    __syncthreads();
+    // a decided block's key becomes the largest or the smallest there is
+    auto decide = [&](int a, bool in) {
+        if constexpr (kKept) keep[list[a]] = in ? ~0u : 0u;
+        else scores[list[a]] = in ? INFINITY : -INFINITY;
+    };
+    if (m <= kRankMost) {
+        for (int a = tid; a < m; a += NT) {
+            const unsigned long long x = order_key(exact[a]);
+            uint32_t rank = 0;  // the list ascends, so among equals the earlier one goes first
+            for (int o = 0; o < m; ++o) {
+                const unsigned long long y = order_key(exact[o]);
+                rank += y > x || (y == x && o < a);
+            }
+            decide(a, rank < need);
         }
     } else {
-        compact(s, nb, [&](int j) { return j < first || j >= first + n; }, sel, (uint32_t)p.M);
+        unsigned long long lo = ~0ull, hi = 0ull;
+        for (int a = tid; a < m; a += NT) {
+            lo = min(lo, order_key(exact[a]));
+            hi = max(hi, order_key(exact[a]));
+        }
+        uint32_t over;
+        const unsigned long long xt =
+            kth_largest<NT, unsigned long long>(s, m, need, [&](int a) { return order_key(exact[a]); }, lo, hi, over);
+        // of the sums equal to the need-th one, the first need - over in the list
+        uint32_t run = 0;
+        for (int a0 = 0; a0 < m; a0 += NT) {
+            const int a = a0 + tid;
+            const unsigned long long x = a < m ? order_key(exact[a]) : 0ull;
+            const bool tie = a < m && x == xt;
+            uint32_t total;
+            const uint32_t before = run + block_exclusive<NT>(s, tie ? 1u : 0u, total);
+            run += total;
+            if (a < m) decide(a, x > xt || (tie && before < need - over));
+        }
+    }
+    __syncthreads();
+    // above the undecided ones, or decided in (+inf itself may be the top of the undecided range)
+    auto in = [&](int j) {
+        const uint32_t x = at(j);
+        return !middle(j) || x > kin || x == (kKept ? ~0u : order_key(INFINITY));
+    };
+    const Counts f = count_runs<NT>(s, nb, in, [](int) { return false; });
+    write_run<NT>(nb, in, f.before_a, sel, (uint32_t)p.M);
+}
+
+// ---------------------------------------- scores --------------------------------------------
+constexpr int kScoreThreads = 256;
+constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreStages = 3;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
+{
+    // 16 bytes, or 16 zeros where there is nothing to load
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Tiles of 16 blocks that sequence b is scored in: none where all its blocks are selected anyway.
+__device__ __forceinline__ int score_tiles(const SelectParams &p, int b)
+{
+    if (b >= p.B) return 0;
+    const int ctx = __ldg(p.context_lens + b);
+    if (ctx < 0 || ctx > p.max_nb * kBlockSize) return 0;
+    const int nb = (ctx + kBlockSize - 1) / kBlockSize;
+    return nb > p.M ? (nb + 15) / 16 : 0;
+}
+
+// A warp's place in the list of tiles, ordered (sequence, tile, KV head).
+struct TileAt {
+    int b, at, end;  // sequence, its entry tile * K + kvh, its tiles * K
+    __device__ __forceinline__ void skip(const SelectParams &p, int by)
+    {
+        at += by;
+        while (at >= end && b < p.B) {
+            at -= end;
+            end = score_tiles(p, ++b) * p.K;
+        }
+    }
+};
+
+// Each CTA takes a contiguous share of all tiles (they are counted at the start from the lengths, so ragged
+// batches and wide tables cost nothing), its warps in turn -- so that the heads of a block, next to each other
+// in memory, are read at about the same time -- and each warp streams its tiles through a ring of its own in
+// shared memory: a tile's bounds are 4 H bytes a block (8 KB at H = 128), copied asynchronously two tiles ahead, the
+// block ids one tile further ahead.  The product's depth may be taken in any order, so a lane's 16-byte vectors are its k indices:
+// each lane copies exactly what it reads back as mma fragments, and the ring needs no barrier.  Bound by memory:
+// eight warps with two tiles each in flight are 128 KB per SM.
+template <int H>
+__global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const SelectParams p)
+{
+    constexpr int V = H / 32;        // 16-byte vectors of a row that a lane holds
+    constexpr int kVecs = 4 * V;     // of a tile: two rows, lo and hi
+    constexpr int S = kScoreStages;
+    extern __shared__ uint4 ring[];  // [warps][S][kVecs][32]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = lane >> 2, m = lane & 3;
+    pdl_launch_dependents();  // the choosing grid may take its place; it waits for this one
+
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        int t = score_tiles(p, b0 + lane);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, off);
+        total += (int64_t)t * p.K;
+    }
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t begin = blockIdx.x * share, end = min(total, begin + share);
+    const int n = end - begin > warp ? (int)((end - begin - warp + kScoreWarps - 1) / kScoreWarps) : 0;
+    if (n == 0) return;
+    TileAt load_at{0, 0, 0};
+    {
+        int64_t before = 0;  // the sequence that holds entry `begin`
+        for (int b0 = 0;; b0 += 32) {
+            const int t = score_tiles(p, b0 + lane) * p.K;
+            int64_t inc = t;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+                if (lane >= off) inc += o;
+            }
+            const unsigned past = __ballot_sync(0xFFFFFFFFu, before + inc > begin);
+            if (past) {
+                const int at = __ffs(past) - 1;
+                load_at.b = b0 + at;
+                load_at.end = __shfl_sync(0xFFFFFFFFu, t, at);
+                load_at.at = (int)(begin - (before + __shfl_sync(0xFFFFFFFFu, inc, at) - load_at.end));
+                break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+        load_at.skip(p, warp);
+    }
+    TileAt use_at = load_at;
+
+    const uint32_t mine = smem_u32(ring + (warp * S * kVecs) * 32 + lane);
+    int blk[2];        // ids of the next tile to copy
+    uint32_t bad = 0;  // of each stage's two rows: the id is outside the pool
+    auto look_up = [&](const TileAt &at) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int j = (at.at / p.K) * 16 + r + 8 * x;
+            // forced blocks are selected without a score, and their bounds need not be up to date
+            const int nb = (__ldg(p.context_lens + at.b) + kBlockSize - 1) / kBlockSize;
+            blk[x] = j >= p.first && j < nb - p.last ? __ldg(p.block_tables + (size_t)at.b * p.max_nb + j) : -2;
+        }
+    };
+    auto copy = [&](const TileAt &at, int stage) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const bool there = blk[x] >= 0 && blk[x] < p.num_blocks;
+            const uint32_t bit = 1u << (2 * stage + x);
+            bad = there ? bad & ~bit : bad | bit;
+            if (!there && blk[x] != -2 && m == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+            const uint16_t *row = p.bounds + ((int64_t)(there ? blk[x] : 0) * p.K + at.at % p.K) * 2 * H + 8 * m;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    cp_async16(mine + ((stage * kVecs + (x * 2 + e) * V + i) * 32) * 16, row + e * H + 32 * i, there);
+        }
+    };
+    int copied = 0;
+    auto advance = [&]() {  // copy the next tile, look the one after it up
+        if (copied < n) {
+            copy(load_at, copied % S);
+            if (++copied < n) {
+                load_at.skip(p, kScoreWarps);
+                look_up(load_at);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(load_at);
+#pragma unroll
+    for (int x = 0; x < S - 1; ++x) advance();
+
+    int q_b = -1, q_kvh = -1, nb = 0;
+    uint32_t qf[2][V][4];  // fragments of min(q, 0) and max(q, 0)
+    for (int i = 0; i < n; ++i) {
+        advance();
+        const int tile = use_at.at / p.K, kvh = use_at.at - tile * p.K;
+        if (use_at.b != q_b || kvh != q_kvh) {
+            q_b = use_at.b, q_kvh = kvh;
+            nb = (__ldg(p.context_lens + q_b) + kBlockSize - 1) / kBlockSize;
+            const bool live = r < p.G;
+            const uint16_t *qrow = p.q + ((size_t)q_b * p.N + (size_t)q_kvh * p.G + (live ? r : 0)) * H + 8 * m;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * v)) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    qf[0][v][y] = min_bf16x2(xw[y], 0u);
+                    qf[1][v][y] = max_bf16x2(xw[y], 0u);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        const int stage = i % S;
+        const uint4 *src = ring + (size_t)((warp * S + stage) * kVecs) * 32 + lane;
+        float c[8][4] = {};  // eight chains of at most two products: short sums keep the error bound small
+        uint32_t big = 0u;  // packed max |bound|
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint4 x = src[(e * V + v) * 32], y = src[((2 + e) * V + v) * 32];
+                const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+                mma_bf16_16816(c[4 * e + 2 * (v & 1)], a0, qf[e][v][0], qf[e][v][1]);
+                mma_bf16_16816(c[4 * e + 2 * (v & 1) + 1], a1, qf[e][v][2], qf[e][v][3]);
+#pragma unroll
+                for (int y2 = 0; y2 < 4; ++y2) {
+                    big = max_bf16x2(big, a0[y2] & 0x7FFF7FFFu);
+                    big = max_bf16x2(big, a1[y2] & 0x7FFF7FFFu);
+                }
+            }
+        }
+        const size_t unit = (size_t)q_b * p.K + q_kvh;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            // this lane's columns are heads 2m and 2m + 1
+            auto sum = [&](int y) {
+                return ((c[0][y] + c[1][y]) + (c[2][y] + c[3][y])) + ((c[4][y] + c[5][y]) + (c[6][y] + c[7][y]));
+            };
+            const float s0 = sum(2 * x), s1 = sum(2 * x + 1);
+            float best = -INFINITY;
+            bool nan = false;
+            if (2 * m < p.G) best = s0, nan = s0 != s0;
+            if (2 * m + 1 < p.G) best = fmaxf(best, s1), nan |= s1 != s1;
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, off));
+            const unsigned nans = __ballot_sync(0xFFFFFFFFu, nan);
+            if ((nans >> (lane & ~3)) & 15u) best = __int_as_float(0x7FC00000);
+            if ((bad >> (2 * stage + x)) & 1u) best = -INFINITY;
+            const int j = tile * 16 + r + 8 * x;
+            if (m == 0 && j < nb) p.scores[unit * p.max_nb + j] = best;
+        }
+        float mb = fmaxf(bf16x2_lo(big), bf16x2_hi(big));
+        // a NaN bound: no bound on the error, every score is looked at in 64 bits
+        if (bf16x2_lo(big) != bf16x2_lo(big) || bf16x2_hi(big) != bf16x2_hi(big)) mb = INFINITY;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
+        if (lane == 0) p.tile_max[unit * p.tiles + tile] = mb;
+        if (i + 1 < n) use_at.skip(p, kScoreWarps);
     }
 }
 
-// Grid (chunks, K, B): 128 blocks of a (sequence, KV head) a CTA, 16 a warp, whose bounds (4 H bytes a block)
-// the warp loads straight into mma fragments -- the product's depth may be taken in any order, so a
-// lane's 16-byte vectors are its k indices -- with all its loads (8 KB at H = 128) in flight at once.
-template <int H>
-__global__ void __launch_bounds__(kSelectThreads, 2) select_blocks_kernel(const SelectParams p)
+template <int H, int NT>
+__global__ void __launch_bounds__(NT) choose_blocks_kernel(const SelectParams p)
 {
-    constexpr int V = H / 32;  // 16-byte vectors a lane holds of a row
     __shared__ SelectShared s;
-    const int chunk = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    extern __shared__ uint32_t keep[];  // [min(max_nb, kKeep)]
+    const int kvh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int ctx = p.context_lens[b];
     if (ctx < 0 || ctx > p.max_nb * kBlockSize) {
-        if (tid == 0 && kvh == 0 && chunk == 0) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+        if (tid == 0 && kvh == 0) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
         ctx = 0;
     }
     const int nb = (ctx + kBlockSize - 1) / kBlockSize;
-    const size_t unit = (size_t)b * p.K + kvh;
-    if (nb <= p.M) {  // every block is selected: no scores needed
-        if (chunk == 0)
-            for (int x = tid; x < p.M; x += kSelectThreads) p.selected[unit * p.M + x] = x < nb ? x : -1;
+    if (nb <= p.M) {  // every block is selected
+        int32_t *sel = p.selected + ((size_t)b * p.K + kvh) * p.M;
+        for (int x = tid; x < p.M; x += NT) sel[x] = x < nb ? x : -1;
         return;
     }
-    const int chunks = (nb + kSelectChunk - 1) / kSelectChunk;
-    if (chunk >= chunks) return;
-
-    const int r = lane >> 2, m = lane & 3;
-    const int j0 = chunk * kSelectChunk + warp * 16 + r;
-    const uint16_t *row[2];
+    float q1 = 0.f;
+    for (int g = warp; g < p.G; g += (NT / 32)) {
+        const uint16_t *q = p.q + ((size_t)b * p.N + (size_t)kvh * p.G + g) * H;
+        float x = 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int j = j0 + 8 * x;
-        row[x] = nullptr;
-        if (j >= p.first && j < nb - p.last) {  // the others are selected without a score
-            const int blk = __ldg(p.block_tables + (size_t)b * p.max_nb + j);
-            if (blk >= 0 && blk < p.num_blocks) row[x] = p.bounds + ((int64_t)blk * p.K + kvh) * 2 * H + 8 * m;
-            else if (m == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-        }
+        for (int h = 0; h < H; h += 32) x += fabsf(bf16_to_f32(q[h + lane]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+        q1 = fmaxf(q1, x);
     }
-    uint4 av[2][2][V];  // [row][lo, hi][vector]
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                av[x][e][i] = row[x] ? __ldg(reinterpret_cast<const uint4 *>(row[x] + e * H + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
-    const bool live = r < p.G;
-    const uint16_t *qrow = p.q + ((size_t)b * p.N + (size_t)kvh * p.G + (live ? r : 0)) * H + 8 * m;
-    uint4 qv[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        qv[i] = live ? __ldg(reinterpret_cast<const uint4 *>(qrow + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
-
-    float c[2][4] = {};
-    uint32_t big = 0u;  // packed max |bound|
-    const uint32_t zero = 0u;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t qw[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-            uint32_t bq[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) bq[w] = e ? max_bf16x2(qw[w], zero) : min_bf16x2(qw[w], zero);
-            const uint4 x = av[0][e][i], y = av[1][e][i];
-            const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-            mma_bf16_16816(c[0], a0, bq[0], bq[1]);
-            mma_bf16_16816(c[1], a1, bq[2], bq[3]);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                big = max_bf16x2(big, a0[w] & 0x7FFF7FFFu);
-                big = max_bf16x2(big, a1[w] & 0x7FFF7FFFu);
-            }
-        }
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        // this lane's columns are heads 2m and 2m + 1
-        const float s0 = c[0][2 * x] + c[1][2 * x], s1 = c[0][2 * x + 1] + c[1][2 * x + 1];
-        float best = -INFINITY;
-        bool nan = false;
-        if (2 * m < p.G) best = s0, nan = s0 != s0;
-        if (2 * m + 1 < p.G) best = fmaxf(best, s1), nan |= s1 != s1;
-#pragma unroll
-        for (int off = 1; off < 4; off <<= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, off));
-        const unsigned nans = __ballot_sync(0xFFFFFFFFu, nan);
-        const int j = j0 + 8 * x;
-        if (m == 0 && j < nb)
-            p.scores[unit * p.max_nb + j] = (nans >> (lane & ~3)) & 15u ? __int_as_float(0x7FC00000) : (row[x] ? best : -INFINITY);
-    }
-    float mb = fmaxf(bf16x2_lo(big), bf16x2_hi(big));
-    const bool mb_nan = bf16x2_lo(big) != bf16x2_lo(big) || bf16x2_hi(big) != bf16x2_hi(big);
-    if (mb_nan) mb = INFINITY;  // no bound on the error: every score is looked at in 64 bits
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
-    if (lane == 0) s.warp_sum[warp] = __float_as_uint(mb);
-    __syncthreads();  // every score of this CTA is written
-    if (tid == 0) {
-        uint32_t top = 0u;
-        for (int w = 0; w < kSelectWarps; ++w) top = max(top, s.warp_sum[w]);
-        p.chunk_max[unit * p.chunks + chunk] = __uint_as_float(top);
-        s.last_one = atomic_add_acq_rel_gpu(p.counters + unit, 1) == chunks - 1;
-    }
-    __syncthreads();
-    if (!s.last_one) return;
-    choose<H>(s, p, b, kvh, nb, chunks);
-    if (tid == 0) p.counters[unit] = 0;  // ready for the next call
+    pdl_wait_primary();  // the scores
+    if (nb <= kKeep) choose<H, NT, true>(s, keep, p, b, kvh, nb, q1);
+    else choose<H, NT, false>(s, keep, p, b, kvh, nb, q1);
 }
 
-cudaError_t launch_select_blocks(const SelectParams &p, int H, cudaStream_t stream)
+template <int H>
+static cudaError_t launch_select_t(const SelectParams &p, int sms, cudaStream_t stream)
 {
-    const dim3 grid(p.chunks, p.K, p.B);
-    if (H == 128) select_blocks_kernel<128><<<grid, kSelectThreads, 0, stream>>>(p);
-    else select_blocks_kernel<64><<<grid, kSelectThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    constexpr int smem = kScoreWarps * kScoreStages * (H / 8) * 32 * 16;
+    static int ready[64] = {};  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(score_blocks_kernel<H>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready[dev] = 1;
+    }
+    const int64_t most = ((int64_t)p.B * p.K * p.tiles + kScoreWarps - 1) / kScoreWarps;  // a tile per warp
+    const unsigned grid = (unsigned)(most < sms ? most : sms);
+    score_blocks_kernel<H><<<grid, kScoreThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    static_assert(sizeof(SelectShared) + sizeof(uint32_t) * kKeep <= 48 * 1024, "no opt-in to larger shared memory");
+    const size_t keep = sizeof(uint32_t) * (size_t)(p.max_nb < kKeep ? p.max_nb : kKeep);
+    const dim3 units(p.K, p.B);
+    // Threads of a choosing CTA: 256 where the batch's CTAs share the SMs (64 * 8 units of up to 2,048 blocks: 75.6 us
+    // for the whole selection, 80.5 with 512), 512 where there are fewer units than SMs (8 units of 2,048 blocks: 11.0,
+    // 11.7 with 256).
+    if ((int64_t)p.K * p.B < sms) return launch_kernel(choose_blocks_kernel<H, 512>, units, dim3(512), keep, stream, true, p);
+    return launch_kernel(choose_blocks_kernel<H, 256>, units, dim3(256), keep, stream, true, p);
+}
+
+cudaError_t launch_select_blocks(const SelectParams &p, int H, int sms, cudaStream_t stream)
+{
+    return H == 128 ? launch_select_t<128>(p, sms, stream) : launch_select_t<64>(p, sms, stream);
 }
 
 }  // namespace pkv

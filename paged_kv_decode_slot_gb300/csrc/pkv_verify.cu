@@ -12,9 +12,10 @@
 // p - q with its rounding error first), each summed exactly: four at a time in 32 bits, then as 64-bit integers
 // in units of 2^-44.  The sums do not depend on the order, and a weight is off by little more than 2^-45.
 //
-// Bound by memory: one row of p, and where a token was refused one row of q.  A CTA sums a chunk of 4,096
-// entries (whatever CTAs a sequence has, the rows are spread over the SMs); the last chunk to finish adds the
-// chunks' sums up, finds the chunk that the draw falls into and then the entry in it.
+// Bound by memory: one row of p, and where a token was refused one row of q.  A row is cut into one run of entries
+// per warp, runs of at least 256 entries and as many as keep about four CTAs per SM over the whole batch; the last
+// CTA of a sequence to finish adds the runs' sums up, finds the run that the draw falls into and the entry in it.
+// The acceptance is decided by every CTA for itself: a few loads against a second launch.
 #include "pkv_device.cuh"
 #include "pkv_ops.h"
 
@@ -22,8 +23,6 @@ namespace pkv {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kPerThread = kVerifyChunk / kVerifyThreads;
-static_assert(kPerThread == 16, "a thread's entries are four groups of four");
 
 __device__ __forceinline__ float prob_at(const float *row, int64_t i) { return __ldg(row + i); }
 __device__ __forceinline__ float prob_at(const uint16_t *row, int64_t i) { return bf16_to_f32(__ldg(row + i)); }
@@ -67,6 +66,14 @@ struct VerifyRow {  // the row that a sequence's next token is drawn from
 template <typename T>
 __device__ __forceinline__ VerifyRow<T> decide(const VerifyParams &p, int b, bool report)
 {
+    const int lane = threadIdx.x & 31;
+    // the first tokens and numbers do not depend on the draft's length: their loads go together with its
+    int x_first = -1;
+    float u_first = 0.f;
+    if (lane < p.T) {
+        x_first = p.tokens[(int64_t)b * p.T + lane];
+        u_first = p.accept_u[(int64_t)b * p.T + lane];
+    }
     int len = p.lens ? p.lens[b] : p.T;
     if (len < 0 || len > p.T) {
         if (report) set_flag(p.err_flag, PKV_FLAG_TOKEN_RANGE);
@@ -75,22 +82,21 @@ __device__ __forceinline__ VerifyRow<T> decide(const VerifyParams &p, int b, boo
     const T *target = static_cast<const T *>(p.target) + (int64_t)b * (p.T + 1) * p.target_stride;
     const T *draft = p.draft ? static_cast<const T *>(p.draft) + (int64_t)b * p.T * p.draft_stride : nullptr;
     // lane t looks at token t (a warp's worth at a time): the first refusal of the warp's
-    const int lane = threadIdx.x & 31;
     int n = len, hot = -1;
     for (int t0 = 0; t0 < len; t0 += 32) {
         const int t = t0 + lane;
         bool refuse = false;
         int x = -1;
         if (t < len) {
-            x = p.tokens[(int64_t)b * p.T + t];
+            x = t0 ? p.tokens[(int64_t)b * p.T + t] : x_first;
+            const float u = t0 ? p.accept_u[(int64_t)b * p.T + t] : u_first;
             refuse = true;
             if (x < 0 || x >= p.V) {
                 if (report) set_flag(p.err_flag, PKV_FLAG_TOKEN_RANGE);
             } else {
                 const float pt = clean(prob_at(target + (int64_t)t * p.target_stride, x));
                 const float qt = draft ? clean(prob_at(draft + (int64_t)t * p.draft_stride, x)) : 1.f;
-                // products of 24-bit numbers are exact in 64 bits
-                refuse = !((double)p.accept_u[(int64_t)b * p.T + t] * (double)qt < (double)pt);
+                refuse = !((double)u * (double)qt < (double)pt);  // products of 24-bit numbers are exact in 64 bits
             }
         }
         const unsigned m = __ballot_sync(0xFFFFFFFFu, refuse);
@@ -109,72 +115,114 @@ __device__ __forceinline__ VerifyRow<T> decide(const VerifyParams &p, int b, boo
     return row;
 }
 
-// A thread's 16 entries of chunk c as cleaned pairs.  kRuns: consecutive entries (running sums need the order);
-// otherwise vectors a CTA's width apart, so that a warp's loads are contiguous.  16-byte loads where the rows
-// allow them (a row of an odd vocabulary starts anywhere).
-template <typename T, bool kRuns>
-__device__ __forceinline__ int64_t entry_of(int c, int k)
-{
-    constexpr int E = 16 / sizeof(T);  // entries of a vector
-    const int64_t i0 = (int64_t)c * kVerifyChunk;
-    return kRuns ? i0 + threadIdx.x * kPerThread + k : i0 + ((k / E) * kVerifyThreads + (int)threadIdx.x) * E + k % E;
-}
+// Two 16-byte vectors of each row that a thread holds: as loaded, so that the next ones can be on their way while
+// these are summed.
+template <typename T>
+struct Pairs {
+    static constexpr int E = 16 / sizeof(T), kEntries = 2 * E;
+    uint4 p[2], q[2];
 
-template <bool kRuns, typename T>
-__device__ __forceinline__ void load16(const VerifyRow<T> &row, int c, int V, float (&p)[16], float (&q)[16])
-{
-    constexpr int E = 16 / sizeof(T);
-    auto fetch = [&](const T *src, float (&x)[16]) {
-        if ((c + 1) * (int64_t)kVerifyChunk <= V && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
-            uint4 v[16 / E];
-#pragma unroll
-            for (int k = 0; k < 16 / E; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(src + entry_of<T, kRuns>(c, E * k)));
-#pragma unroll
-            for (int k = 0; k < 16 / E; ++k) {
-                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (sizeof(T) == 4) {
-                        x[E * k + e] = clean(__uint_as_float(w[e]));
-                    } else {
-                        x[E * k + 2 * e] = clean(bf16x2_lo(w[e]));
-                        x[E * k + 2 * e + 1] = clean(bf16x2_hi(w[e]));
-                    }
-                }
-            }
+    __device__ static __forceinline__ float entry(const uint4 (&v)[2], int k)
+    {
+        const uint4 x = v[k / E];
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            return __uint_as_float(w[k % E]);
         } else {
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            return k & 1 ? bf16x2_hi(w[(k % E) / 2]) : bf16x2_lo(w[(k % E) / 2]);
+        }
+    }
+    // kVec: vector k holds the entries from i0 + k * step on, and the rows start on 16 bytes; the part of a vector
+    // behind `end` is left at zero.  Otherwise entry k of the thread is i0 + k * step (rows of an odd vocabulary
+    // start anywhere: with step 32 and lanes next to each other a warp's loads are contiguous all the same).
+    template <bool kVec>
+    __device__ __forceinline__ void load(const VerifyRow<T> &row, int64_t i0, int step, int64_t end)
+    {
+        auto fetch = [&](const T *src, uint4 (&v)[2]) {
+            if constexpr (kVec) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int64_t i = entry_of<T, kRuns>(c, k);
-                x[k] = i < V ? clean(prob_at(src, i)) : 0.f;
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t i = i0 + k * (int64_t)step;
+                    v[k] = i + E <= end ? __ldg(reinterpret_cast<const uint4 *>(src + i)) : make_uint4(0u, 0u, 0u, 0u);
+                    if (i < end && i + E > end) v[k] = cut(src, i, 1, end);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) v[k] = cut(src, i0 + k * E * (int64_t)step, step, end);
+            }
+        };
+        fetch(row.p, p);
+        if (row.q) fetch(row.q, q);
+        else q[0] = q[1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ static __forceinline__ uint4 cut(const T *src, int64_t i, int step, int64_t end)
+    {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (i + e * (int64_t)step < end) {
+                if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(__ldg(src + i + e * (int64_t)step));
+                else w[e / 2] |= (uint32_t)__ldg(src + i + e * (int64_t)step) << (16 * (e & 1));
             }
         }
-    };
-    fetch(row.p, p);
-    if (row.q) {
-        fetch(row.q, q);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) q[k] = entry_of<T, kRuns>(c, k) == row.hot ? 1.f : 0.f;
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    // units of 2^-44 of all entries; a one-hot draft's token is entry `hot` of this thread's (-1: elsewhere)
+    __device__ __forceinline__ long long units(int hot) const
+    {
+        long long sum = 0;
+#pragma unroll
+        for (int h = 0; h < kEntries / 4; ++h) {
+            WeightSum w;
+            w.clear();
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k) w.add(clean(entry(p, k)), k == hot ? 1.f : clean(entry(q, k)));
+            sum += w.units();
+        }
+        return sum;
+    }
+};
+
+// Which of the entries i0 + k of a thread (consecutive ones), or with vectors `step` apart, is the row's hot token.
+template <typename T>
+__device__ __forceinline__ int hot_entry(const VerifyRow<T> &row, int64_t i0, int step, bool vec)
+{
+    constexpr int E = Pairs<T>::E;
+    if (row.hot < 0) return -1;
+    const int64_t d = row.hot - i0;
+    if (d < 0) return -1;
+    if (!vec) return d % step == 0 && d / step < 2 * E ? (int)(d / step) : -1;
+    const int64_t k = d / step;
+    return k < 2 && d - k * step < E ? (int)(k * E + d - k * step) : -1;
 }
 
-// The sum of a thread's 16 entries of chunk c.
-template <bool kRuns, typename T>
-__device__ __forceinline__ long long thread_sum(const VerifyRow<T> &row, int c, int V)
+// The sum of this warp's run of entries [begin, end), on every lane.
+template <typename T, bool kVec>
+__device__ __forceinline__ long long run_sum_t(const VerifyRow<T> &row, int64_t begin, int64_t end)
 {
-    float p[16], q[16];
-    load16<kRuns>(row, c, V, p, q);
+    constexpr int E = Pairs<T>::E, kStride = 64 * E;  // entries of a warp's round
+    const int lane = threadIdx.x & 31;
+    const int64_t off = kVec ? lane * E : lane;
+    const int step = kVec ? 32 * E : 32;
     long long sum = 0;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        WeightSum w;
-        w.clear();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w.add(p[4 * h + k], q[4 * h + k]);
-        sum += w.units();
+    Pairs<T> next;
+    next.template load<kVec>(row, begin + off, step, end);
+    for (int64_t i = begin; i < end; i += kStride) {
+        const Pairs<T> now = next;
+        if (i + kStride < end) next.template load<kVec>(row, i + kStride + off, step, end);
+        sum += now.units(hot_entry(row, i + off, step, kVec));
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     return sum;
+}
+
+template <typename T>
+__device__ __forceinline__ long long run_sum(const VerifyRow<T> &row, int64_t begin, int64_t end)
+{
+    const bool even = (reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) % 16 == 0;
+    return even ? run_sum_t<T, true>(row, begin, end) : run_sum_t<T, false>(row, begin, end);
 }
 
 __device__ __forceinline__ long long block_sum(long long v, long long *warp_sums)
@@ -215,16 +263,19 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     __shared__ int found, last_one;
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     VerifyRow<T> row = decide<T>(p, b, c == 0 && tid < 32);
-    long long *sums = p.sums + (int64_t)b * p.chunks;
-    const long long mine = block_sum(thread_sum<false>(row, c, p.V), warp_sums);
-    if (tid == 0) {
-        sums[c] = mine;
-        last_one = atomic_add_acq_rel_gpu(p.counters + b, 1) == p.chunks - 1;
+    const int runs = (p.V + p.run - 1) / p.run;
+    long long *sums = p.sums + (int64_t)b * runs;
+    const int r = c * kVerifyWarps + (tid >> 5);  // this warp's run
+    if (r < runs) {
+        const long long mine = run_sum(row, (int64_t)r * p.run, min((int64_t)p.V, (int64_t)(r + 1) * p.run));
+        if ((tid & 31) == 0) sums[r] = mine;
     }
+    __syncthreads();
+    if (tid == 0) last_one = atomic_add_acq_rel_gpu(p.counters + b, 1) == (int)gridDim.x - 1;
     __syncthreads();
     if (!last_one) return;
 
-    // ---- the sequence's last CTA: total, chunk, entry ----
+    // ---- the sequence's last CTA: total, run, entry ----
     int token = -1;
     for (int pass = 0; pass < 2 && token < 0; ++pass) {
         if (pass) {
@@ -232,27 +283,29 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             if (!row.q && row.hot < 0) break;
             row.q = nullptr;
             row.hot = -1;
-            for (int x = 0; x < p.chunks; ++x) {
-                const long long v = block_sum(thread_sum<false>(row, x, p.V), warp_sums);
-                if (tid == 0) sums[x] = v;
+            for (int x = tid >> 5; x < runs; x += kVerifyWarps) {
+                const long long v = run_sum(row, (int64_t)x * p.run, min((int64_t)p.V, (int64_t)(x + 1) * p.run));
+                if ((tid & 31) == 0) sums[x] = v;
             }
             __syncthreads();
         }
         long long total = 0;
-        for (int x = tid; x < p.chunks; x += kVerifyThreads) total += __ldcg(sums + x);
+        for (int x = tid; x < runs; x += kVerifyThreads) total += __ldcg(sums + x);
         total = block_sum(total, warp_sums);
         if (total <= 0) continue;
-        // r in [0, 1): the running sum must exceed r * total, so the last entry with weight always does
-        const double r = fmin(fmax((double)p.sample_u[b], 0.0), 1.0 - 0x1p-53);
-        const double bar = r * (double)total;  // sums below 2^53 units are exact in 64 bits
+        // r < 1 and the running sum must exceed r * total, so the last entry with weight always does; sums below
+        // 2^53 units (rows that are no distributions may have more) are exact in 64 bits
+        const double bar = fmin(fmax((double)p.sample_u[b], 0.0), 1.0 - 0x1p-53) * (double)total;
+        // sums of [x0 + tid] or of entries: the thread whose running sum is the first above the bar reports
+        auto reaches = [&](long long upto, long long v) { return (double)upto > bar && (double)(upto - v) <= bar; };
         long long before = 0;
-        for (int x0 = 0; x0 < p.chunks; x0 += kVerifyThreads) {
+        for (int x0 = 0; x0 < runs; x0 += kVerifyThreads) {
             const int x = x0 + tid;
-            const long long v = x < p.chunks ? __ldcg(sums + x) : 0;
+            const long long v = x < runs ? __ldcg(sums + x) : 0;
             const long long upto = before + block_inclusive(v, warp_sums);
             if (tid == 0) found = -1;
             __syncthreads();
-            if ((double)upto > bar && (double)(upto - v) <= bar) {
+            if (reaches(upto, v)) {
                 found = x;
                 found_before = upto - v;
             }
@@ -260,31 +313,34 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             if (found >= 0) break;
             before += block_sum(v, warp_sums);
         }
-        const int at = found;
-        const long long base = found_before;
-        const long long w = thread_sum<true>(row, at, p.V);
-        const long long upto = base + block_inclusive(w, warp_sums);
-        if (tid == 0) found = -1;
-        __syncthreads();
-        if ((double)upto > bar && (double)(upto - w) <= bar) {
-            // this thread's entries, one by one
-            float pv[16], qv[16];
-            load16<true>(row, at, p.V, pv, qv);
-            long long run = upto - w;
-            int hit = -1;
+        const int64_t begin = (int64_t)found * p.run, end = min((int64_t)p.V, begin + p.run);
+        before = found_before;
+        constexpr int kMine = Pairs<T>::kEntries;  // consecutive entries of a thread
+        for (int64_t i = begin; i < end && token < 0; i += kMine * kVerifyThreads) {
+            Pairs<T> x;
+            x.template load<false>(row, i + tid * kMine, 1, end);
+            const int hot = hot_entry(row, i + tid * kMine, 1, false);
+            const long long v = x.units(hot);
+            const long long upto = before + block_inclusive(v, warp_sums);
+            if (tid == 0) found = -1;
+            __syncthreads();
+            if (reaches(upto, v)) {  // this thread's entries, one by one
+                long long run = upto - v;
+                int hit = -1;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                WeightSum one;
-                one.clear();
-                one.add(pv[k], qv[k]);
-                run += one.units();
-                if (hit < 0 && (double)run > bar) hit = (int)entry_of<T, true>(at, k);
+                for (int k = 0; k < kMine; ++k) {
+                    WeightSum one;
+                    one.clear();
+                    one.add(clean(x.entry(x.p, k)), k == hot ? 1.f : clean(x.entry(x.q, k)));
+                    run += one.units();
+                    if (hit < 0 && (double)run > bar) hit = (int)(i + tid * kMine + k);
+                }
+                found = hit;
             }
-            found = hit;
+            __syncthreads();
+            token = found;
+            before += block_sum(v, warp_sums);  // its barriers also keep `found` until all have read it
         }
-        __syncthreads();
-        token = found;
-        __syncthreads();
     }
     if (token < 0 && tid == 0) set_flag(p.err_flag, PKV_FLAG_NO_MASS);
     const int n = row.accepted;
@@ -300,9 +356,16 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     }
 }
 
-cudaError_t launch_verify(const VerifyParams &p, bool bf16, cudaStream_t stream)
+cudaError_t launch_verify(VerifyParams p, bool bf16, int sms, cudaStream_t stream)
 {
-    const dim3 grid(p.chunks, p.B);
+    // runs of at least kVerifyRun entries, CTAs enough for about four per SM
+    const int most = (p.V + kVerifyRun * kVerifyWarps - 1) / (kVerifyRun * kVerifyWarps);
+    const int want = (4 * sms + p.B - 1) / p.B;
+    const int ctas = want < most ? want : most;
+    const int per = (p.V + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
+    p.run = (per + kVerifyRun - 1) / kVerifyRun * kVerifyRun;
+    const int runs = (p.V + p.run - 1) / p.run;
+    const dim3 grid((runs + kVerifyWarps - 1) / kVerifyWarps, p.B);
     if (bf16) verify_kernel<uint16_t><<<grid, kVerifyThreads, 0, stream>>>(p);
     else verify_kernel<float><<<grid, kVerifyThreads, 0, stream>>>(p);
     return cudaGetLastError();
