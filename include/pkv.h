@@ -488,7 +488,7 @@ int pkv_decode_step_prefix(const pkv_bf16 *q, const pkv_bf16 *k_new, const pkv_b
  * rounded once, to bf16 or to e4m3.  v_new is not turned.  q_out [tokens][N][H] receives the turned queries
  * and may be q itself (in place), but not overlap it otherwise.  A token without a slot (below) is
  * left out: nothing is written for it, q_out included.  q, k_new, v_new, q_out and the pools are
- * 16-byte aligned (e4m3 pools 8-byte).
+ * 16-byte aligned (e4m3 pools 8-byte); q, k_new and v_new are device memory (bulk copies read them).
  */
 
 /* Slots and positions given (prompts, any mixture of sequences): token i goes to slot_mapping[i]

@@ -111,7 +111,7 @@ def _stream(stream):
 # The pools and the workspaces must be device memory (the pools are read by TMA).  Every other
 # argument may also be pinned (page-locked) host memory, which the kernels read and write in place
 # (on a GB300 over NVLink-C2C) -- a step's inputs and outputs need no copies then.
-_DEVICE_ONLY = ("k_cache", "v_cache", "workspace", "part_out", "part_lse", "key_bounds", "k_scale", "v_scale")
+_DEVICE_ONLY = ("k_cache", "v_cache", "workspace", "part_out", "part_lse")
 
 
 def _need(t, dtype, ndim, name):
@@ -686,9 +686,14 @@ def pkv_decode_attn_splitk_noalloc(q, k_cache, v_cache, block_tables, context_le
 # ------------------------- the operators around a step's attention -------------------------
 # A step makes several of these calls and some run for a few microseconds, so their arguments are checked
 # in one expression per tensor; what it does not accept goes to _refuse, which names the fault (or accepts
-# pinned host memory).  Addresses go to ctypes as integers.
+# pinned host memory).  Addresses go to ctypes as integers; empty tensors have none, so a call without tokens or
+# sequences ends in the binding.
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# Besides the pools and workspaces, what bulk copies read or every step reads again must be device memory.
+_DEVICE_ONLY_NEW = ("key_bounds", "k_scale", "v_scale", "q before the rotation", "k_new before the rotation", "v_new")
 
 
 def _launch(stream, dev: int) -> int:
@@ -708,6 +713,8 @@ def _arg(t, dtype, shape, name: str, dev: int) -> int:
 
 
 def _refuse(t, dtype, shape, name: str, dev: int) -> int:
+    if name in _DEVICE_ONLY_NEW and isinstance(t, torch.Tensor) and not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     _need(t, dtype, len(shape), name)  # not a tensor, another type, not contiguous, not on a GPU or pinned
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -758,10 +765,10 @@ def _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, pool, lead: i
     half = _shape(inv_freq, 1, "inv_freq")[0]
     if qs[-1] != H:
         raise ValueError("q [.., N, H] and the pools [num_blocks, 16, K, H] differ in head_dim")
-    qp, op = _arg(q, _bf16, qs, "q", dev), _arg(q_out, _bf16, qs, "q_out", dev)
+    qp, op = _arg(q, _bf16, qs, "q before the rotation", dev), _arg(q_out, _bf16, qs, "q_out", dev)
     if op != qp and abs(op - qp) < 2 * q.numel():
         raise ValueError("q_out may be q itself, but not overlap it")
-    return (qp, _arg(k_new, _bf16, new, "k_new", dev), _arg(v_new, _bf16, new, "v_new", dev), op,
+    return (qp, _arg(k_new, _bf16, new, "k_new before the rotation", dev), _arg(v_new, _bf16, new, "v_new", dev), op,
             _arg(k_cache, pool, cs, "k_cache", dev), _arg(v_cache, pool, cs, "v_cache", dev),
             _arg(inv_freq, torch.float64, (half,), "inv_freq", dev), 2 * half, qs[-2], CacheDesc(nb, bs, K, H))
 
@@ -774,6 +781,8 @@ def pkv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache,
     dev = _current_device()
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _bf16, 1, dev)
     n = q.shape[0]
+    if n == 0:
+        return PKV_OK
     return _lib.pkv_rope_append(qp, kp, vp, _arg(positions, _i32, (n,), "positions", dev), fp, R, interleaved,
                                 _arg(slot_mapping, _i64, (n,), "slot_mapping", dev), n, N, kc, vc, op, desc,
                                 _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
@@ -786,6 +795,8 @@ def pkv_rope_append_fp8(q, k_new, v_new, positions, inv_freq, k_scale, v_scale, 
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _u8, 1, dev)
     ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
     n = q.shape[0]
+    if n == 0:
+        return PKV_OK
     return _lib.pkv_rope_append_fp8(qp, kp, vp, _arg(positions, _i32, (n,), "positions", dev), fp, R, interleaved, ks,
                                     vs, stride, _arg(slot_mapping, _i64, (n,), "slot_mapping", dev), n, N, kc, vc, op,
                                     desc, _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
@@ -805,6 +816,8 @@ def pkv_rope_append_multi(q, k_new, v_new, block_tables, context_lens, inv_freq,
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _bf16, 2, dev)
     B, T = q.shape[:2]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    if B * T == 0:
+        return PKV_OK
     return _lib.pkv_rope_append_multi(qp, kp, vp, tp, width, cp, fp, R, interleaved, B, T, N, kc, vc, op,
                                       _arg(slot_mapping, _i64, (B, T), "slot_mapping", dev), desc,
                                       _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
@@ -819,6 +832,8 @@ def pkv_rope_append_multi_fp8(q, k_new, v_new, block_tables, context_lens, inv_f
     ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
     B, T = q.shape[:2]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    if B * T == 0:
+        return PKV_OK
     return _lib.pkv_rope_append_multi_fp8(qp, kp, vp, tp, width, cp, fp, R, interleaved, ks, vs, stride, B, T, N, kc,
                                           vc, op, _arg(slot_mapping, _i64, (B, T), "slot_mapping", dev), desc,
                                           _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
@@ -851,6 +866,8 @@ def pkv_key_bounds(k_cache, block_tables, context_lens, num_new: int, key_bounds
     one of a sequence's last num_new tokens."""
     dev = _current_device()
     kc, tp, width, cp, B, bp, desc = _bounds_args(k_cache, _bf16, block_tables, context_lens, key_bounds, dev)
+    if B == 0:
+        return PKV_OK
     return _lib.pkv_key_bounds(kc, tp, width, cp, B, num_new, bp, desc,
                                _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
 
@@ -861,6 +878,8 @@ def pkv_key_bounds_fp8(k_cache, k_scale, block_tables, context_lens, num_new: in
     dev = _current_device()
     kc, tp, width, cp, B, bp, desc = _bounds_args(k_cache, _u8, block_tables, context_lens, key_bounds, dev)
     ks, _, stride = _scale_args(k_scale, k_scale, desc.num_blocks, desc.num_kv_heads, dev)
+    if B == 0:
+        return PKV_OK
     return _lib.pkv_key_bounds_fp8(kc, ks, stride, tp, width, cp, B, num_new, bp, desc,
                                    _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
 
@@ -878,6 +897,8 @@ def pkv_select_blocks(q, key_bounds, block_tables, context_lens, selected, works
     B, N, _ = qs
     M, size = _shape(selected, 3, "selected")[2], _shape(workspace, 1, "workspace")[0]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    if B == 0:
+        return PKV_OK
     return _lib.pkv_select_blocks(_arg(q, _bf16, (B, N, H), "q", dev),
                                   _arg(key_bounds, _bf16, (nb, K, 2, H), "key_bounds", dev), tp, width, cp, B, N,
                                   first_blocks, last_blocks, M, _arg(selected, _i32, (B, K, M), "selected", dev),
@@ -906,6 +927,8 @@ def pkv_decode_attn_blocks(q, k_cache, v_cache, block_tables, context_lens, sele
     dev = _current_device()
     qp, kc, vc, tp, width, cp, sp, M, B, N, op, lp, desc, ws, size = _blocks_args(
         q, k_cache, v_cache, _bf16, block_tables, context_lens, selected, out, lse_out, workspace, dev)
+    if B == 0:
+        return PKV_OK
     return _lib.pkv_decode_attn_blocks(qp, kc, vc, tp, width, cp, sp, M, B, N, scale, op, lp, desc, partition_blocks,
                                        max_partitions, ws, size, _maybe(err_flag, _i32, _FLAG, "err_flag", dev),
                                        _launch(stream, dev))
@@ -919,6 +942,8 @@ def pkv_decode_attn_blocks_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     qp, kc, vc, tp, width, cp, sp, M, B, N, op, lp, desc, ws, size = _blocks_args(
         q, k_cache, v_cache, _u8, block_tables, context_lens, selected, out, lse_out, workspace, dev)
     ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
+    if B == 0:
+        return PKV_OK
     return _lib.pkv_decode_attn_blocks_fp8(qp, kc, vc, ks, vs, stride, tp, width, cp, sp, M, B, N, scale, op, lp, desc,
                                            partition_blocks, max_partitions, ws, size,
                                            _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
@@ -952,6 +977,8 @@ def pkv_verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u
     if V > width or V > wide:
         raise ValueError(f"vocab_size {V} exceeds the columns of target_probs or draft_probs")
     size = _shape(workspace, 1, "workspace")[0]
+    if B == 0:
+        return PKV_OK
     return _lib.pkv_verify_draft(_arg(target_probs, dtype, (B, rows, width), "target_probs", dev), width,
                                  _maybe(draft_probs, dtype, (B, T, wide), "draft_probs", dev), wide, dtype is _bf16,
                                  _arg(draft_tokens, _i32, (B, T), "draft_tokens", dev),

@@ -58,7 +58,7 @@ __device__ __forceinline__ uint2 rope_quantize8(float (&x)[8], float sc)
         float w;
         asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(w) : "f"(v), "f"(most));
         const float y = __fmaf_rn(w, r, w * s);
-        return __fmaf_rn(__fmaf_rn(-y, sc, w), r, y);
+        return copysignf(__fmaf_rn(__fmaf_rn(-y, sc, w), r, y), w);  // -0 / scale is -0
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(quotient(x[2 * i]), quotient(x[2 * i + 1]));

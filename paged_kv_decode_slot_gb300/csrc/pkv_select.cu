@@ -461,9 +461,11 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
         all_b = fmaxf(all_b, s.bound[1][w]);
     }
     const float eps2 = 2.f * ldexpf(all_q * all_b, -17);
-    // bounds of the undecided scores, rounded outwards; everything is undecided where eps2 is no number
-    const uint32_t kin = eps2 == eps2 ? max(kt, order_key(__fadd_ru(t, eps2))) : ~0u;
-    const uint32_t kout = eps2 == eps2 ? min(kt, order_key(__fadd_rd(t, -eps2))) : 0u;
+    // bounds of the undecided scores, rounded outwards; infinite bounds (0 times infinity in the products) leave every
+    // score undecided
+    const bool bounded = eps2 < INFINITY;
+    const uint32_t kin = bounded ? max(kt, order_key(__fadd_ru(t, eps2))) : ~0u;
+    const uint32_t kout = bounded ? min(kt, order_key(__fadd_rd(t, -eps2))) : 0u;
     const Counts c = count_runs<NT>(s, nb, [&](int j) { return !middle(j) || at(j) >= kout; },
                                 [&](int j) { return middle(j) && at(j) <= kin && at(j) >= kout; });
     if (c.all_a == (uint32_t)p.M) {  // nothing left to decide
@@ -617,7 +619,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     TileAt use_at = load_at;
 
     const uint32_t mine = smem_u32(ring + (warp * S * kVecs) * 32 + lane);
-    int blk[2];        // ids of the next tile to copy
+    int blk[2];        // ids of the next tile to copy, of the blocks that are scored
+    bool scored[2];
     uint32_t bad = 0;  // of each stage's two rows: the id is outside the pool
     auto look_up = [&](const TileAt &at) {
 #pragma unroll
@@ -625,7 +628,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
             const int j = (at.at / p.K) * 16 + r + 8 * x;
             // forced blocks are selected without a score, and their bounds need not be up to date
             const int nb = (__ldg(p.context_lens + at.b) + kBlockSize - 1) / kBlockSize;
-            blk[x] = j >= p.first && j < nb - p.last ? __ldg(p.block_tables + (size_t)at.b * p.max_nb + j) : -2;
+            scored[x] = j >= p.first && j < nb - p.last;
+            blk[x] = scored[x] ? __ldg(p.block_tables + (size_t)at.b * p.max_nb + j) : -1;
         }
     };
     auto copy = [&](const TileAt &at, int stage) {
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
             const bool there = blk[x] >= 0 && blk[x] < p.num_blocks;
             const uint32_t bit = 1u << (2 * stage + x);
             bad = there ? bad & ~bit : bad | bit;
-            if (!there && blk[x] != -2 && m == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+            if (!there && scored[x] && m == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
             const uint16_t *row = p.bounds + ((int64_t)(there ? blk[x] : 0) * p.K + at.at % p.K) * 2 * H + 8 * m;
 #pragma unroll
             for (int e = 0; e < 2; ++e)

@@ -463,6 +463,80 @@ class PrefixDecodeStep:
         return [getattr(self, n) for n in self.input_names()]
 
 
+class SparseDecodeStep:
+    """A decode step that attends to selected blocks only, over bf16 pools or (k_scale, v_scale given)
+    e4m3 ones: ``pkv_rope_append_multi`` turns the new token's query and key by its position and writes
+    its K/V into its slot, ``pkv_key_bounds`` brings the bounds of its block up to date,
+    ``pkv_select_blocks`` chooses at most ``max_selected`` blocks per (sequence, KV head) -- the first
+    ``first_blocks``, the last ``last_blocks`` and those whose bounds promise the largest logits -- and
+    ``pkv_decode_attn_blocks`` attends to them.  A sequence with no more blocks than that is attended
+    in full.  The new token's own block must be among the selected ones: ``last_blocks`` >= 1.
+
+    q [B, N, H] and k_new/v_new [B, K, H] bf16 before the rotation, in device memory; key_bounds bf16
+    [num_blocks, K, 2, H], up to date for the blocks of the context (after a prompt:
+    ``pkv_key_bounds`` with num_new = its length); inv_freq float64 [rotary_dim / 2]; pools, tables and
+    lengths as ``DecodeStep``.  q_turned, selected, slot_mapping, out and lse are written."""
+
+    def __init__(self, q, k_new, v_new, k_cache, v_cache, key_bounds, block_tables, context_lens, scale,
+                 inv_freq, max_selected: int, first_blocks: int = 1, last_blocks: int = 1,
+                 interleaved: bool = False, k_scale=None, v_scale=None, err_flag=None):
+        if last_blocks < 1:
+            raise ValueError("the new token's block has to be attended to: last_blocks >= 1")
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        self.q, self.k_new, self.v_new = q, k_new, v_new
+        self.k_cache, self.v_cache, self.key_bounds = k_cache, v_cache, key_bounds
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.block_tables, self.context_lens = block_tables, context_lens
+        self.scale, self.inv_freq, self.interleaved = float(scale), inv_freq, bool(interleaved)
+        self.first_blocks, self.last_blocks = int(first_blocks), int(last_blocks)
+        dev = k_cache.device
+        nseq, N, H = q.shape
+        K = k_cache.shape[2]
+        sms = torch.cuda.get_device_properties(dev).multi_processor_count
+        self.plan = plan_blocks_attention(nseq, K, max_selected, sms)
+        self.fused = True
+        self.q_turned = torch.empty_like(q)
+        self.slot_mapping = torch.empty(nseq, 1, dtype=torch.int64, device=dev)
+        self.selected = torch.empty(nseq, K, max_selected, dtype=torch.int32, device=dev)
+        self.out = torch.empty(nseq, N, H, dtype=q.dtype, device=dev)
+        self.lse = torch.empty(nseq, N, dtype=torch.float32, device=dev)
+        self.err_flag = err_flag
+        self.select_workspace = torch.empty(B.pkv_select_workspace_bytes(nseq, K, block_tables.shape[1]),
+                                            dtype=torch.uint8, device=dev)
+        self.workspace = None
+        if self.plan.mode == "split":
+            nbytes = B.pkv_splitk_workspace_bytes(nseq, N, H, self.plan.max_partitions)
+            self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+
+    def run(self, stream=None) -> None:
+        q, kn, vn = self.q.unsqueeze(1), self.k_new.unsqueeze(1), self.v_new.unsqueeze(1)
+        turned, tables, lens, err = self.q_turned.unsqueeze(1), self.block_tables, self.context_lens, self.err_flag
+        scales = () if self.k_scale is None else (self.k_scale, self.v_scale)
+        rope = B.pkv_rope_append_multi_fp8 if scales else B.pkv_rope_append_multi
+        B.check(rope(q, kn, vn, tables, lens, self.inv_freq, *scales, self.k_cache, self.v_cache, turned,
+                     self.slot_mapping, self.interleaved, err, stream))
+        if scales:
+            B.check(B.pkv_key_bounds_fp8(self.k_cache, self.k_scale, tables, lens, 1, self.key_bounds, err, stream))
+        else:
+            B.check(B.pkv_key_bounds(self.k_cache, tables, lens, 1, self.key_bounds, err, stream))
+        B.check(B.pkv_select_blocks(self.q_turned, self.key_bounds, tables, lens, self.selected,
+                                    self.select_workspace, self.first_blocks, self.last_blocks, err, stream))
+        attend = B.pkv_decode_attn_blocks_fp8 if scales else B.pkv_decode_attn_blocks
+        B.check(attend(self.q_turned, self.k_cache, self.v_cache, *scales, tables, lens, self.selected, self.scale,
+                       self.out, self.lse, self.plan.partition_blocks, self.plan.max_partitions, self.workspace,
+                       err, stream))
+
+    def launches_per_step(self) -> int:
+        return 5  # append, bounds, scores, choice, attention (its partitions merge in the same launch)
+
+    def input_names(self):
+        return ("q", "k_new", "v_new", "block_tables", "context_lens")
+
+    def inputs(self):
+        return [getattr(self, n) for n in self.input_names()]
+
+
 class LayerStack:
     """One decode step of a model with several attention layers: the same sequences (block tables
     and context lengths) in every layer, each layer with its own pools and its own q, k_new and
