@@ -1438,7 +1438,10 @@ int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_sel
     p.part_out = w.part_out, p.part_lse = w.part_lse, p.counters = w.counters;
     p.err_flag = a.err_flag;
     p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
-    cudaError_t e = pkv::launch_attn_blocks(a.d.head_dim, fp8, tk, tv, p, stream);
+    int sms = 0;
+    st = sm_count(&sms);
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_attn_blocks(a.d.head_dim, fp8, tk, tv, p, sms, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "selected blocks attention launch");
 }
 

@@ -91,14 +91,15 @@ __device__ __forceinline__ void block_update(WarpAcc<H> &a, const uint32_t (&qf)
 // kFp8: e4m3 pools (H = 128).  Scales come per tile in both granularities (the producer fetches them with the
 // block id): the K scale multiplies the tile's logits, the V scale its weights relative to the largest seen
 // (VScaleRef, pkv_attn_common.cuh).
-template <int H, bool kFp8>
-__global__ void __launch_bounds__(kAttnThreads, PKV_CTAS_PER_SM)
+template <int H, bool kFp8, int W>
+__global__ void __launch_bounds__((W + kProducers) * 32, W > 4 ? 2 : PKV_CTAS_PER_SM)
 attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const BlocksParams p)
 {
-    constexpr int S = kFp8 ? kStagesFp8 : kStages;
-    constexpr int kBatch = S / kProducers / 2;
-    using L = AttnLayout<H, S, kConsumerWarps, kProducers, kFp8 ? 1 : 2>;
+    constexpr int P = kProducers, S = kFp8 ? kStagesFp8 : (W > 4 ? 2 * kStages : kStages), kThreads = (W + P) * 32;
+    static_assert(S % W == 0, "a stage's tiles belong to one warp");
+    constexpr int kBatch = S / P / 2;
+    using L = AttnLayout<H, S, W, P, kFp8 ? 1 : 2>;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -110,10 +111,10 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int G = p.G;
     const int begin = part * p.part_blocks;  // this CTA's entries of the list: [begin, end)
     const int32_t *sel = p.selected + ((size_t)b * p.K + kvh) * p.M + begin;
-    const int pw = warp - kConsumerWarps;  // producer warp
+    const int pw = warp - W;  // producer warp
 
     int first_sel = -1;  // the producers' first list entries do not depend on the length
-    if (pw >= 0 && begin + pw + kProducers * lane < min(p.M, begin + p.part_blocks)) first_sel = __ldg(sel + pw + kProducers * lane);
+    if (pw >= 0 && begin + pw + P * lane < min(p.M, begin + p.part_blocks)) first_sel = __ldg(sel + pw + P * lane);
     int ctx = p.context_lens[b];
     if (ctx < 0 || ctx > p.max_nb * kBlockSize) {
         if (threadIdx.x == 0 && kvh == 0 && part == 0) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
@@ -126,7 +127,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const size_t bn0 = (size_t)b * p.N + (size_t)kvh * G;
     if (n <= 0) {
         if (entries == 0 && part == 0) {
-            for (int idx = threadIdx.x; idx < G * H; idx += kAttnThreads) {
+            for (int idx = threadIdx.x; idx < G * H; idx += kThreads) {
                 const int g = idx / H, h = idx - g * H;
                 p.out[(bn0 + g) * H + h] = __float2bfloat16_rn(0.f);
                 if (h == 0 && p.lse_out) p.lse_out[bn0 + g] = -INFINITY;
@@ -139,11 +140,11 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t bar_empty = bar_full + 8 * S;
     volatile int *valid_of = reinterpret_cast<volatile int *>(base + L::kMiscOffset);  // [S] tokens that count
     volatile int *abort_flag = valid_of + S;
-    volatile int *issued_count = abort_flag + 1;  // [kProducers]
+    volatile int *issued_count = abort_flag + 1;  // [P]
     volatile float2 *stage_sc = reinterpret_cast<volatile float2 *>(base + L::kScaleOffset);
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int q = 0; q < kProducers; ++q) issued_count[q] = 0;
+        for (int q = 0; q < P; ++q) issued_count[q] = 0;
         init_ring<S>(bar_full, bar_empty);
     }
     __syncthreads();
@@ -158,7 +159,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             prefetch_tensormap(&tm_v);
         }
         const int32_t *tbl = p.block_tables + (size_t)b * p.max_nb;
-        const int mine = n > pw ? (n - pw + kProducers - 1) / kProducers : 0;
+        const int mine = n > pw ? (n - pw + P - 1) / P : 0;
         // one tile per lane: its block id (-1: skipped), the tokens that count, its scales
         struct Tile {
             int bid, valid;
@@ -190,7 +191,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         bool aborted = false;
         for (int k0 = 0; k0 < mine && !aborted; k0 += 32) {
             Tile nxt{-1, 0, 0.f, 0.f};
-            if (k0 + 32 + lane < mine) nxt = look_up(__ldg(sel + pw + kProducers * (k0 + 32 + lane)));
+            if (k0 + 32 + lane < mine) nxt = look_up(__ldg(sel + pw + P * (k0 + 32 + lane)));
             const int cnt = min(32, mine - k0);
             // kBatch tiles at a time, one per lane: half of this producer's stages, so that the other half stays in flight
             for (int k = 0; k < cnt; k += kBatch) {
@@ -201,7 +202,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if constexpr (kFp8) sc = make_float2(__shfl_sync(0xFFFFFFFFu, cur.ks, from), __shfl_sync(0xFFFFFFFFu, cur.vs, from));
                 bool ok = true;
                 if (lane < kBatch && k + lane < cnt) {
-                    const int i = pw + kProducers * (k0 + k + lane), s = i % S;
+                    const int i = pw + P * (k0 + k + lane), s = i % S;
                     const uint32_t bar = bar_full + 8 * s;
                     if (i >= S && !mbar_wait_bounded(bar_empty + 8 * s, ((i / S) & 1) ^ 1, abort_flag, p.wait_ns)) {
                         if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
@@ -245,7 +246,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if constexpr (kFp8) load_q_frags_fp8<H>(qf, p.q, p.N, b, kvh, G, lane);
         else load_q_frags<H>(qf, p.q, p.N, b, kvh, G, lane);
         acc_reset<H>(acc);
-        for (int i = warp; i < n; i += kConsumerWarps) {
+        for (int i = warp; i < n; i += W) {
             const int s = i % S;
             // lanes may differ at the deadline: the warp agrees before its collective work
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_full + 8 * s, (i / S) & 1, abort_flag, p.wait_ns))) {
@@ -269,26 +270,26 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     __syncthreads();
     const bool aborted = *abort_flag != 0;
     if (aborted) {
-        if (pw >= 0 && lane == 0) drain_ring<S, kProducers>(bar_full, pw, issued_count[pw]);
+        if (pw >= 0 && lane == 0) drain_ring<S, P>(bar_full, pw, issued_count[pw]);
         __syncthreads();
         if (nparts <= 1) return;  // the unit's other partitions still count on this one: a void partial
     }
 
     // ------------------------- merge the consumer warps' states -------------------------
     float *mo = reinterpret_cast<float *>(base);
-    float *mm = mo + kConsumerWarps * 8 * H;
-    float *ml = mm + kConsumerWarps * 8;
+    float *mm = mo + W * 8 * H;
+    float *ml = mm + W * 8;
     if (!aborted) {
-        if (warp < kConsumerWarps) {
+        if (warp < W) {
             if constexpr (kFp8) acc_scale_o<H>(acc, vr.v);
             deposit<H, kFp8>(acc, mo, mm, ml, warp, lane);
         }
         __syncthreads();
     }
-    for (int idx = threadIdx.x; idx < G * H; idx += kAttnThreads) {
+    for (int idx = threadIdx.x; idx < G * H; idx += kThreads) {
         const int g = idx / H, h = idx - g * H;
         float val = __int_as_float(0x7FC00000), lse = __int_as_float(0x7FC00000);  // NaN: void
-        if (!aborted) combine<H>(mo, mm, ml, g, h, val, lse);
+        if (!aborted) combine<H, W>(mo, mm, ml, g, h, val, lse);
         const size_t bn = bn0 + g;
         if (nparts > 1) {
             p.part_out[(bn * p.max_parts + part) * H + h] = val;
@@ -309,44 +310,51 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (!last_one) return;
     float *wts = reinterpret_cast<float *>(base);                          // [G][nparts]
     float *red = reinterpret_cast<float *>(base) + kInKernelMergeWeights;  // [kMergeWarps][8][H]
-    for (int idx = threadIdx.x; idx < G * nparts; idx += kAttnThreads) {
+    for (int idx = threadIdx.x; idx < G * nparts; idx += kThreads) {
         const int g = idx / nparts, q = idx - g * nparts;
         wts[idx] = __ldcg(p.part_lse + (bn0 + g) * p.max_parts + q);
     }
     __syncthreads();
-    for (int g = warp; g < G; g += kAttnThreads / 32) {
+    for (int g = warp; g < G; g += kThreads / 32) {
         const float lse = lse_merge_weights<true>(wts + g * nparts, nparts, wts + g * nparts, lane);
         if (lane == 0 && p.lse_out) p.lse_out[bn0 + g] = lse;
     }
     __syncthreads();
     merge_rows<H, 8>(wts, nparts, G, p.part_out + bn0 * p.max_parts * H, (size_t)p.max_parts * H, red, p.out + bn0 * H, H,
-                     threadIdx.x, kAttnThreads);
+                     threadIdx.x, kThreads);
     if (threadIdx.x == 0) *count = 0;  // ready for the next call
 }
 
-template <int H, bool kFp8>
+template <int H, bool kFp8, int W>
 static cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, cudaStream_t stream)
 {
-    constexpr int smem = AttnLayout<H, kFp8 ? kStagesFp8 : kStages, kConsumerWarps, kProducers, kFp8 ? 1 : 2>::kAlloc;
+    constexpr int S = kFp8 ? kStagesFp8 : (W > 4 ? 2 * kStages : kStages);
+    constexpr int smem = AttnLayout<H, S, W, kProducers, kFp8 ? 1 : 2>::kAlloc;
     static int ready[64] = {};  // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         ready[dev] = 1;
     }
-    attn_blocks_kernel<H, kFp8><<<dim3(p.K, p.B, p.max_parts), kAttnThreads, smem, stream>>>(tk, tv, p);
+    attn_blocks_kernel<H, kFp8, W><<<dim3(p.K, p.B, p.max_parts), (W + kProducers) * 32, smem, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p,
+cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, int sms,
                                cudaStream_t stream)
 {
-    if (fp8) return launch_t<128, true>(tk, tv, p, stream);
-    return H == 128 ? launch_t<128, false>(tk, tv, p, stream) : launch_t<64, false>(tk, tv, p, stream);
+    // Eight consumer warps and sixteen stages instead of four and eight where one CTA takes a whole list: always in e4m3
+    // (64 * 8 lists of 128 blocks 63.6 -> 54.3 us), in bf16 -- whose sixteen stages leave room for one CTA per SM --
+    // while there is one list per SM at most (16 * 8 lists of 128: 30.4 -> 25.9; 64 * 8 lists: 85.4 and 86.0).  CTAs of
+    // a cut list are short and many: four warps (2 * 160 e4m3 parts of 125 blocks 46.3, with eight 52.4).
+    const bool wide = p.max_parts == 1 && (fp8 || (int64_t)p.B * p.K <= sms);
+    if (fp8) return wide ? launch_t<128, true, 8>(tk, tv, p, stream) : launch_t<128, true, 4>(tk, tv, p, stream);
+    if (H == 128) return wide ? launch_t<128, false, 8>(tk, tv, p, stream) : launch_t<128, false, 4>(tk, tv, p, stream);
+    return wide ? launch_t<64, false, 8>(tk, tv, p, stream) : launch_t<64, false, 4>(tk, tv, p, stream);
 }
 
 }  // namespace pkv

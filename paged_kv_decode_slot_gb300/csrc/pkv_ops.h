@@ -102,7 +102,7 @@ struct BlocksParams {
 };
 
 cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv,
-                               const BlocksParams &p, cudaStream_t stream);
+                               const BlocksParams &p, int sms, cudaStream_t stream);
 
 // Verification of drafted tokens (pkv_verify.cu).
 struct VerifyParams {

@@ -39,8 +39,8 @@ constexpr double kInv2Pi = 0.15915494309189533577;
 // Eight values as e4m3 codes of x / scale, the quotient rounded to nearest in fp32 as the plain append takes it (the
 // input is the rotation's 32-bit result, so a turned key is rounded once to 8 bits).  Markstein's theorem (IBM J.
 // Res. Dev. 34, 1990): with r = 1 / scale rounded to nearest and y within an ulp of the quotient,
-// y + (x - y scale) r, both operations fused, is the quotient rounded to nearest.  r + s is the reciprocal to twice
-// the precision, so y = x r + x s is off by little more than half an ulp.  Nothing over- or underflows where it
+// y + (x - y scale) r, both operations fused, is the quotient rounded to nearest.  r0 + s is the reciprocal to twice
+// the precision, so y = x r0 + x s is off by little more than half an ulp.  Nothing over- or underflows where it
 // matters: x is cut off at 512 scale (codes end at 448; NaN stays), quotients below 2^-11 are code 0 whatever their
 // last bits, and scales beyond 2^+-80 are brought nearer to 1 together with x.  Checking a plain x r against both
 // neighbouring codes and dividing where they differ measured 55 against 50 us on 5,001 tokens of 3 * 40 heads.
@@ -52,13 +52,14 @@ __device__ __forceinline__ uint2 rope_quantize8(float (&x)[8], float sc)
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= k;
     }
-    const float r = __frcp_rn(sc), s = __fmaf_rn(-r, sc, 1.f) * r, most = 512.f * sc;
+    const float r = __frcp_rn(sc), r0 = __frcp_rd(sc), s = __fmaf_rn(-r0, sc, 1.f) * r0;  // r0 + s is 1 / sc, s >= 0
+    const float most = 512.f * sc;
     uint32_t c[4];
-    auto quotient = [&](float v) {
+    auto quotient = [&](float v) {  // signs of zero included: w s has w's sign, and so has y
         float w;
         asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(w) : "f"(v), "f"(most));
-        const float y = __fmaf_rn(w, r, w * s);
-        return copysignf(__fmaf_rn(__fmaf_rn(-y, sc, w), r, y), w);  // -0 / scale is -0
+        const float y = __fmaf_rn(w, r0, w * s);
+        return __fmaf_rn(-__fmaf_rn(y, sc, -w), r, y);
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(quotient(x[2 * i]), quotient(x[2 * i + 1]));

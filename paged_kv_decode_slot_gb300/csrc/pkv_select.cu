@@ -152,7 +152,7 @@ cudaError_t launch_key_bounds(const BoundsParams &p, bool fp8, int span, cudaStr
 
 // -------------------------------------- selection -------------------------------------------
 constexpr int kMostWarps = 16;      // of a choosing CTA
-constexpr int kBins = 2048;         // bins of one narrowing pass
+constexpr int kBinBits = 9, kBins = 1 << kBinBits;  // bins of one narrowing pass
 constexpr int kRankMost = 256;      // undecided blocks ranked pairwise; more go through narrowing passes
 constexpr int kFew = 64;            // keys of one bin ranked pairwise
 constexpr int kKeep = 8192;         // scores the choosing CTA keeps in shared memory (131,072 tokens); longer
@@ -184,6 +184,8 @@ struct SelectShared {
     unsigned long long few[kFew];
     float bound[2][kMostWarps];  // |q|_1 and the largest |bound|, by warp
     double exact[kRankMost];
+    int32_t list[kRankMost];
+    uint32_t chosen[kRankMost];
 };
 
 // Sum and exclusive prefix sum over the CTA of one value per thread.
@@ -211,24 +213,41 @@ __device__ __forceinline__ uint32_t block_exclusive(SelectShared &s, uint32_t v,
     return before + inc - v;
 }
 
+template <typename Key>
+__device__ __forceinline__ void warp_range(Key &mn, Key &mx)
+{
+    if constexpr (sizeof(Key) == 4) {
+        mn = __reduce_min_sync(0xFFFFFFFFu, mn);
+        mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+    } else {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            mn = min(mn, (Key)__shfl_xor_sync(0xFFFFFFFFu, mn, off));
+            mx = max(mx, (Key)__shfl_xor_sync(0xFFFFFFFFu, mx, off));
+        }
+    }
+}
+
 // The k-th largest (k >= 1) of the n keys key(0 .. n-1), whose smallest and largest are mn and mx over this
 // thread's share (any split over the CTA), and the number of keys above it.  Narrowing passes: the keys' range
-// is cut into up to 2048 bins and the bin that holds the k-th becomes the range; a bin is 2^shift keys
-// wide, so a pass takes eleven bits off the range whatever the keys are.  The first range is that of the keys
+// is cut into up to 512 bins and the bin that holds the k-th becomes the range; a bin is 2^shift keys
+// wide, so a pass takes nine bits off the range whatever the keys are.  The first range is that of the keys
 // themselves: the scores of one query lie within a few powers of two and spread over the bins, so shared-memory
-// atomics seldom meet, and one pass nearly always leaves few enough keys to rank them pairwise.
+// atomics seldom meet, and one pass nearly always leaves few enough keys to rank them pairwise.  A thread only asks for
+// the keys i = tid mod NT; a barrier has to lie between this and whatever used s before.
 template <int NT, typename Key, typename F>
 __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F key, Key mn, Key mx, uint32_t &above)
 {
-    const int tid = threadIdx.x;
-    constexpr int kMine = kBins / NT;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kMine = kBins >= NT ? kBins / NT : 1;  // bins of a thread, of the first kBins / kMine threads
+    // from the top: thread t holds bins [kBins - kMine (t + 1), kBins - kMine t)
+    const int b0 = kBins - kMine * (tid + 1);
+    warp_range(mn, mx);
+    if (lane == 0) s.range[0][warp] = mn, s.range[1][warp] = mx;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        mn = min(mn, (Key)__shfl_xor_sync(0xFFFFFFFFu, mn, off));
-        mx = max(mx, (Key)__shfl_xor_sync(0xFFFFFFFFu, mx, off));
-    }
-    __syncthreads();
-    if ((tid & 31) == 0) s.range[0][tid >> 5] = mn, s.range[1][tid >> 5] = mx;
+    for (int x = 0; x < kMine; ++x)
+        if (b0 >= 0) s.hist[b0 + x] = 0u;
+    if (tid == 0) s.few_n = 0u;
     __syncthreads();
     unsigned long long all_lo = s.range[0][0], all_hi = s.range[1][0];
 #pragma unroll
@@ -238,51 +257,33 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
     }
     Key lo = (Key)all_lo, hi = (Key)all_hi;
     uint32_t up = 0, inside = (uint32_t)n;  // keys above hi, keys in [lo, hi]
-    while (lo < hi) {
-        if (inside <= kFew) {
-            if (tid == 0) s.few_n = 0u;
-            __syncthreads();
-            for (int i = tid; i < n; i += NT) {
-                const Key x = key(i);
-                if (x >= lo && x <= hi) s.few[atomicAdd(&s.few_n, 1u)] = (unsigned long long)x;
-            }
-            __syncthreads();
-            if (tid < (int)inside) {
-                const Key x = (Key)s.few[tid];
-                uint32_t more = up, same = 0;
-                for (uint32_t o = 0; o < inside; ++o) {
-                    more += (Key)s.few[o] > x;
-                    same += (Key)s.few[o] == x;
-                }
-                if (more < k && more + same >= k) {  // equal keys write equal values
-                    s.lo = (unsigned long long)x;
-                    s.above = more;
-                }
-            }
-            __syncthreads();
-            lo = (Key)s.lo;
-            up = s.above;
-            break;
-        }
+    while (lo < hi && inside > kFew) {
         const int bits = 64 - __clzll((long long)(unsigned long long)(hi - lo));
-        const int shift = max(0, bits - 11);
-#pragma unroll
-        for (int x = 0; x < kMine; ++x) s.hist[tid + x * NT] = 0u;
-        __syncthreads();
+        const int shift = max(0, bits - kBinBits);
+#pragma unroll 4
         for (int i = tid; i < n; i += NT) {
             const Key x = key(i);
             if (x >= lo && x <= hi) atomicAdd(&s.hist[(uint32_t)((x - lo) >> shift)], 1u);
         }
         __syncthreads();
-        // bins from the top: thread t holds bins [kBins - kMine (t + 1), kBins - kMine t)
-        uint32_t mine[kMine], sum = 0, total;
-        const int b0 = kBins - kMine * (tid + 1);
+        uint32_t mine[kMine], sum = 0;
 #pragma unroll
         for (int x = 0; x < kMine; ++x) {
-            mine[x] = s.hist[b0 + x];
+            mine[x] = b0 >= 0 ? s.hist[b0 + x] : 0u;
             sum += mine[x];
+            if (b0 >= 0) s.hist[b0 + x] = 0u;  // for another pass
         }
-        uint32_t before = up + block_exclusive<NT>(s, sum, total);
+        uint32_t inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+            if (lane >= off) inc += o;
+        }
+        if (lane == 31) s.warp_sum[0][warp] = inc;
+        __syncthreads();
+        uint32_t before = up + inc - sum;
+#pragma unroll
+        for (int w = 0; w < (NT / 32); ++w) before += w < warp ? s.warp_sum[0][w] : 0u;
         if (before < k && before + sum >= k) {  // one thread: the k-th is in one of its bins
 #pragma unroll
             for (int x = kMine - 1; x >= 0; --x) {
@@ -296,12 +297,36 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
                 before += mine[x];
             }
         }
-        __syncthreads();
+        __syncthreads();  // (the next write of lo, hi, above and inside lies behind another barrier)
         lo = (Key)s.lo;
         hi = (Key)s.hi;
         up = s.above;
         inside = s.inside;
+    }
+    if (lo < hi) {
+#pragma unroll 4
+        for (int i = tid; i < n; i += NT) {
+            const Key x = key(i);
+            if (x >= lo && x <= hi) s.few[atomicAdd(&s.few_n, 1u)] = (unsigned long long)x;
+        }
         __syncthreads();
+        if (tid < (int)inside) {
+            const Key x = (Key)s.few[tid];
+            uint32_t more = up, same = 0;
+#pragma unroll 4
+            for (uint32_t o = 0; o < inside; ++o) {
+                const Key y = (Key)s.few[o];
+                more += y > x;
+                same += y == x;
+            }
+            if (more < k && more + same >= k) {  // equal keys write equal values
+                s.lo = (unsigned long long)x;
+                s.above = more;
+            }
+        }
+        __syncthreads();
+        lo = (Key)s.lo;
+        up = s.above;
     }
     above = up;
     return lo;
@@ -349,52 +374,58 @@ __device__ __forceinline__ void warp_run(int nb, int &begin, int &end)
     end = min(nb, begin + per);
 }
 
-// Writes the blocks j in [0, nb) with take(j) to dst in ascending order; before: those of the earlier warps' runs.
-template <int NT, typename Take>
-__device__ __forceinline__ void write_run(int nb, Take take, uint32_t before, int32_t *dst, uint32_t most)
-{
-    const int lane = threadIdx.x & 31;
-    int begin, end;
-    warp_run<NT>(nb, begin, end);
-    for (int j0 = begin; j0 < end; j0 += 32) {
-        const bool in = j0 + lane < end && take(j0 + lane);
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, in);
-        const uint32_t o = before + __popc(m & ((1u << lane) - 1u));
-        if (in && o < most) dst[o] = j0 + lane;
-        before += __popc(m);
-    }
-}
-
-// Over the blocks [0, nb): how many a(j) and b(j) hold for, in all and in the runs of earlier warps.
+// Blocks [0, nb) by class(j), two bits: bit 0 and bit 1 are counted apart, in all and in the runs of earlier warps.
+// Lane i keeps what the warp's i-th 32 blocks answered.
 struct Counts {
-    uint32_t all_a, all_b, before_a, before_b;
+    uint32_t all[2], before[2], mask[2];
 };
 
-template <int NT, typename A, typename B>
-__device__ __forceinline__ Counts count_runs(SelectShared &s, int nb, A a, B b)
+template <int NT, typename Class>
+__device__ __forceinline__ Counts count_runs(SelectShared &s, int nb, Class cls)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int begin, end;
     warp_run<NT>(nb, begin, end);
-    uint32_t na = 0, nbb = 0;
+    Counts c{{0, 0}, {0, 0}, {0, 0}};
+    uint32_t n0 = 0, n1 = 0;
+#pragma unroll 4
     for (int j0 = begin; j0 < end; j0 += 32) {
-        const bool here = j0 + lane < end;
-        na += __popc(__ballot_sync(0xFFFFFFFFu, here && a(j0 + lane)));
-        nbb += __popc(__ballot_sync(0xFFFFFFFFu, here && b(j0 + lane)));
+        const int x = j0 + lane < end ? cls(j0 + lane) : 0;
+        const uint32_t m0 = __ballot_sync(0xFFFFFFFFu, x & 1), m1 = __ballot_sync(0xFFFFFFFFu, x & 2);
+        if (lane == (j0 - begin) / 32) c.mask[0] = m0, c.mask[1] = m1;
+        n0 += __popc(m0);
+        n1 += __popc(m1);
     }
     __syncthreads();
-    if (lane == 0) s.warp_sum[0][warp] = na, s.warp_sum[1][warp] = nbb;
+    if (lane == 0) s.warp_sum[0][warp] = n0, s.warp_sum[1][warp] = n1;
     __syncthreads();
-    Counts c{0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < (NT / 32); ++w) {
         const uint32_t x = s.warp_sum[0][w], y = s.warp_sum[1][w];
-        c.all_a += x;
-        c.all_b += y;
-        c.before_a += w < warp ? x : 0u;
-        c.before_b += w < warp ? y : 0u;
+        c.all[0] += x;
+        c.all[1] += y;
+        c.before[0] += w < warp ? x : 0u;
+        c.before[1] += w < warp ? y : 0u;
     }
     return c;
+}
+
+// Writes the blocks of [0, nb) whose class has `bit` to dst, ascending.  kMasks: there are at most 1,024 blocks a warp,
+// and what count_runs saw is still right.
+template <int NT, bool kMasks, typename Class>
+__device__ __forceinline__ void write_run(int nb, Class cls, int bit, const Counts &c, int32_t *dst, uint32_t most)
+{
+    const int lane = threadIdx.x & 31;
+    int begin, end;
+    warp_run<NT>(nb, begin, end);
+    uint32_t before = c.before[bit];
+    for (int j0 = begin; j0 < end; j0 += 32) {
+        const uint32_t m = kMasks ? __shfl_sync(0xFFFFFFFFu, c.mask[bit], (j0 - begin) / 32)
+                                  : __ballot_sync(0xFFFFFFFFu, j0 + lane < end && (cls(j0 + lane) >> bit & 1));
+        const uint32_t o = before + __popc(m & ((1u << lane) - 1u));
+        if ((m >> lane & 1u) && o < most) dst[o] = j0 + lane;
+        before += __popc(m);
+    }
 }
 
 // The choice of one (sequence, KV head) from its scores.  q1: this warp's share of the largest |q|_1 over the
@@ -411,18 +442,19 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     const uint32_t k = (uint32_t)(p.M - p.first - p.last);  // 0 <= k < n
     auto middle = [&](int j) { return j >= first && j < first + n; };
     if (k == 0) {
-        const Counts c = count_runs<NT>(s, nb, [&](int j) { return !middle(j); }, [](int) { return false; });
-        write_run<NT>(nb, [&](int j) { return !middle(j); }, c.before_a, sel, (uint32_t)p.M);
+        auto forced = [&](int j) { return middle(j) ? 0 : 1; };
+        write_run<NT, kKept>(nb, forced, 0, count_runs<NT>(s, nb, forced), sel, (uint32_t)p.M);
         return;
     }
 
-    // the scores, as keys; their range; |q|_1 and the largest |bound|
-    uint32_t mn = ~0u, mx = 0u;
-    auto load = [&](int i) { return order_key(__ldcg(scores + first + i)); };
+    // the scores, as keys; their range; |q|_1 and the largest |bound| (all loads on their way together)
+    uint32_t mn = ~0u, mx = 0u, mb = 0u;
+    for (int c = tid; c < (nb + 15) / 16; c += NT) mb = max(mb, __float_as_uint(__ldcg(p.tile_max + unit * p.tiles + c)));
+    auto load = [&](int i) { return __ldcg(scores + first + i); };
     {
         constexpr int U = 8;  // loads in flight a thread
         for (int i0 = tid; i0 < n; i0 += U * NT) {
-            uint32_t x[U];
+            float x[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (i0 + u * NT < n) x[u] = load(i0 + u * NT);
@@ -430,18 +462,16 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
             for (int u = 0; u < U; ++u) {
                 const int i = i0 + u * NT;
                 if (i < n) {
-                    mn = min(mn, x[u]);
-                    mx = max(mx, x[u]);
-                    if constexpr (kKept) keep[first + i] = x[u];
+                    const uint32_t y = order_key(x[u]);
+                    mn = min(mn, y);
+                    mx = max(mx, y);
+                    if constexpr (kKept) keep[first + i] = y;
                 }
             }
         }
     }
-    float mb = 0.f;
-    for (int c = tid; c < (nb + 15) / 16; c += NT) mb = fmaxf(mb, __ldcg(p.tile_max + unit * p.tiles + c));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
-    if (lane == 0) s.bound[0][warp] = q1, s.bound[1][warp] = mb;  // read behind the barriers that follow
+    mb = __reduce_max_sync(0xFFFFFFFFu, mb);  // non-negative numbers order like their bits
+    if (lane == 0) s.bound[0][warp] = q1, s.bound[1][warp] = __uint_as_float(mb);  // read behind the barriers that follow
     auto at = [&](int j) -> uint32_t {  // key of block j
         if constexpr (kKept) return keep[j];
         else return order_key(__ldcg(scores + j));
@@ -449,34 +479,39 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     uint32_t above;
     const uint32_t kt = kth_largest<NT, uint32_t>(s, n, k, [&](int i) { return at(first + i); }, mn, mx, above);
     const float t = __uint_as_float(kt & 0x80000000u ? kt & 0x7FFFFFFFu : ~kt);
-    // eps: 2^-17 |q|_1 max|bound| = 2^-17 S.  A score is the sum of eight chains of at most two mma of 16 products.  No
-    // product and no partial sum of a chain exceeds the chain's part S' of S; an mma that keeps 23 bits below its
-    // largest term loses at most 2^-23 S' for each of its 17 terms and once more at its end, the three levels of fp32
-    // additions 2^-24 S each: (2 * 18 + 2) 2^-23 S, and over half as much again for slack in what the documentation
-    // leaves open about the rounding inside an mma.
+    // eps: 2^-18 |q|_1 max|bound| = 2^-18 S.  A score is the fp32 sum of sixteen mma of 16 products each.  No product exceeds
+    // S and an mma's own sum its part S' of S; one that keeps 23 bits below its largest term loses at most 2^-23 S' for each
+    // of its 16 terms and once more at its end, and every addition after it 2^-24 S: (17 + 7.5) 2^-23 S, and a third as
+    // much again for slack in what the documentation leaves open about the rounding inside an mma.
     float all_q = s.bound[0][0], all_b = s.bound[1][0];
 #pragma unroll
     for (int w = 1; w < (NT / 32); ++w) {
         all_q = fmaxf(all_q, s.bound[0][w]);
         all_b = fmaxf(all_b, s.bound[1][w]);
     }
-    const float eps2 = 2.f * ldexpf(all_q * all_b, -17);
+    const float eps2 = 2.f * ldexpf(all_q * all_b, -18);
     // bounds of the undecided scores, rounded outwards; infinite bounds (0 times infinity in the products) leave every
     // score undecided
     const bool bounded = eps2 < INFINITY;
     const uint32_t kin = bounded ? max(kt, order_key(__fadd_ru(t, eps2))) : ~0u;
     const uint32_t kout = bounded ? min(kt, order_key(__fadd_rd(t, -eps2))) : 0u;
-    const Counts c = count_runs<NT>(s, nb, [&](int j) { return !middle(j) || at(j) >= kout; },
-                                [&](int j) { return middle(j) && at(j) <= kin && at(j) >= kout; });
-    if (c.all_a == (uint32_t)p.M) {  // nothing left to decide
-        write_run<NT>(nb, [&](int j) { return !middle(j) || at(j) >= kout; }, c.before_a, sel, (uint32_t)p.M);
+    // bit 0: forced or not below the undecided range; bit 1: undecided
+    auto cls = [&](int j) {
+        if (!middle(j)) return 1;
+        const uint32_t x = at(j);
+        return x < kout ? 0 : (x <= kin ? 3 : 1);
+    };
+    const Counts c = count_runs<NT>(s, nb, cls);
+    if (c.all[0] == (uint32_t)p.M) {  // nothing left to decide
+        write_run<NT, kKept>(nb, cls, 0, c, sel, (uint32_t)p.M);
         return;
     }
     // more undecided blocks than places: rank them by their sums in 64 bits
-    const uint32_t need = (uint32_t)p.M - (c.all_a - c.all_b);
-    const int m = (int)c.all_b;
-    int32_t *list = p.list + unit * p.max_nb;
-    write_run<NT>(nb, [&](int j) { return middle(j) && at(j) <= kin && at(j) >= kout; }, c.before_b, list, c.all_b);
+    const uint32_t need = (uint32_t)p.M - (c.all[0] - c.all[1]);
+    const int m = (int)c.all[1];
+    const bool few = kKept && m <= kRankMost;
+    int32_t *list = few ? s.list : p.list + unit * p.max_nb;
+    write_run<NT, kKept>(nb, cls, 1, c, list, c.all[1]);
     __syncthreads();
     double *exact = m <= kRankMost ? s.exact : p.exact + unit * p.max_nb;
     for (int a = warp; a < m; a += (NT / 32)) {
@@ -484,6 +519,36 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
         if (lane == 0) exact[a] = x;
     }
     __syncthreads();
+    if (few) {
+        for (int a = tid; a < m; a += NT) {
+            const unsigned long long x = order_key(exact[a]);
+            uint32_t rank = 0;  // the list ascends, so among equals the earlier one goes first
+            for (int o = 0; o < m; ++o) {
+                const unsigned long long y = order_key(exact[o]);
+                rank += y > x || (y == x && o < a);
+            }
+            s.chosen[a] = rank < need;
+        }
+        __syncthreads();
+        // the earlier warps' runs hold the list's first before[1] blocks
+        uint32_t lost = 0;
+        for (int a0 = 0; a0 < (int)c.before[1]; a0 += 32)
+            lost += __popc(__ballot_sync(0xFFFFFFFFu, a0 + lane < (int)c.before[1] && !s.chosen[a0 + lane]));
+        uint32_t at_list = c.before[1], before = c.before[0] - lost;
+        int begin, end;
+        warp_run<NT>(nb, begin, end);
+        for (int j0 = begin; j0 < end; j0 += 32) {
+            const uint32_t m0 = __shfl_sync(0xFFFFFFFFu, c.mask[0], (j0 - begin) / 32);
+            const uint32_t m1 = __shfl_sync(0xFFFFFFFFu, c.mask[1], (j0 - begin) / 32), below = (1u << lane) - 1u;
+            bool in = m0 >> lane & 1u;
+            if (m1 >> lane & 1u) in = s.chosen[at_list + __popc(m1 & below)] != 0;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
+            if (in) sel[before + __popc(mask & below)] = j0 + lane;
+            before += __popc(mask);
+            at_list += __popc(m1);
+        }
+        return;
+    }
     // a decided block's key becomes the largest or the smallest there is
     auto decide = [&](int a, bool in) {
         if constexpr (kKept) keep[list[a]] = in ? ~0u : 0u;
@@ -523,17 +588,16 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     __syncthreads();
     // above the undecided ones, or decided in (+inf itself may be the top of the undecided range)
     auto in = [&](int j) {
+        if (!middle(j)) return 1;
         const uint32_t x = at(j);
-        return !middle(j) || x > kin || x == (kKept ? ~0u : order_key(INFINITY));
+        return x > kin || x == (kKept ? ~0u : order_key(INFINITY)) ? 1 : 0;
     };
-    const Counts f = count_runs<NT>(s, nb, in, [](int) { return false; });
-    write_run<NT>(nb, in, f.before_a, sel, (uint32_t)p.M);
+    write_run<NT, kKept>(nb, in, 0, count_runs<NT>(s, nb, in), sel, (uint32_t)p.M);
 }
 
 // ---------------------------------------- scores --------------------------------------------
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreStages = 3;
+constexpr int kScoreWarps = 8, kScoreThreads = 32 * kScoreWarps;
+constexpr int kScoreStages = 2;  // three measured the same
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there)
 {
@@ -553,13 +617,20 @@ __device__ __forceinline__ int score_tiles(const SelectParams &p, int b)
 
 // A warp's place in the list of tiles, ordered (sequence, tile, KV head).
 struct TileAt {
-    int b, at, end;  // sequence, its entry tile * K + kvh, its tiles * K
-    __device__ __forceinline__ void skip(const SelectParams &p, int by)
+    int b, tile, kvh, tiles;
+    // kScoreWarps entries on, without a division: by_tile and by_kvh are kScoreWarps / K and the remainder
+    __device__ __forceinline__ void next(const SelectParams &p, int by_tile, int by_kvh)
     {
-        at += by;
-        while (at >= end && b < p.B) {
-            at -= end;
-            end = score_tiles(p, ++b) * p.K;
+        tile += by_tile;
+        kvh += by_kvh;
+        if (kvh >= p.K) kvh -= p.K, ++tile;
+        wrap(p);
+    }
+    __device__ __forceinline__ void wrap(const SelectParams &p)
+    {
+        while (tile >= tiles && b < p.B) {
+            tile -= tiles;
+            tiles = score_tiles(p, ++b);
         }
     }
 };
@@ -567,10 +638,10 @@ struct TileAt {
 // Each CTA takes a contiguous share of all tiles (they are counted at the start from the lengths, so ragged
 // batches and wide tables cost nothing), its warps in turn -- so that the heads of a block, next to each other
 // in memory, are read at about the same time -- and each warp streams its tiles through a ring of its own in
-// shared memory: a tile's bounds are 4 H bytes a block (8 KB at H = 128), copied asynchronously two tiles ahead, the
+// shared memory: a tile's bounds are 4 H bytes a block (8 KB at H = 128), copied asynchronously one tile ahead, the
 // block ids one tile further ahead.  The product's depth may be taken in any order, so a lane's 16-byte vectors are its k indices:
 // each lane copies exactly what it reads back as mma fragments, and the ring needs no barrier.  Bound by memory:
-// eight warps with two tiles each in flight are 128 KB per SM.
+// eight warps with a tile or two each in flight are 64 to 128 KB per SM.
 template <int H>
 __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const SelectParams p)
 {
@@ -593,12 +664,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     const int64_t begin = blockIdx.x * share, end = min(total, begin + share);
     const int n = end - begin > warp ? (int)((end - begin - warp + kScoreWarps - 1) / kScoreWarps) : 0;
     if (n == 0) return;
-    TileAt load_at{0, 0, 0};
+    TileAt load_at{0, 0, 0, 0};
+    const int by_tile = kScoreWarps / p.K, by_kvh = kScoreWarps - by_tile * p.K;
     {
         int64_t before = 0;  // the sequence that holds entry `begin`
         for (int b0 = 0;; b0 += 32) {
-            const int t = score_tiles(p, b0 + lane) * p.K;
-            int64_t inc = t;
+            const int t = score_tiles(p, b0 + lane);
+            int64_t inc = (int64_t)t * p.K;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
@@ -608,13 +680,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
             if (past) {
                 const int at = __ffs(past) - 1;
                 load_at.b = b0 + at;
-                load_at.end = __shfl_sync(0xFFFFFFFFu, t, at);
-                load_at.at = (int)(begin - (before + __shfl_sync(0xFFFFFFFFu, inc, at) - load_at.end));
+                load_at.tiles = __shfl_sync(0xFFFFFFFFu, t, at);
+                const int64_t entry = begin + warp - (before + __shfl_sync(0xFFFFFFFFu, inc, at) - (int64_t)load_at.tiles * p.K);
+                load_at.tile = (int)(entry / p.K);
+                load_at.kvh = (int)(entry - (int64_t)load_at.tile * p.K);
                 break;
             }
             before += __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
-        load_at.skip(p, warp);
+        load_at.wrap(p);
     }
     TileAt use_at = load_at;
 
@@ -625,7 +699,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     auto look_up = [&](const TileAt &at) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int j = (at.at / p.K) * 16 + r + 8 * x;
+            const int j = at.tile * 16 + r + 8 * x;
             // forced blocks are selected without a score, and their bounds need not be up to date
             const int nb = (__ldg(p.context_lens + at.b) + kBlockSize - 1) / kBlockSize;
             scored[x] = j >= p.first && j < nb - p.last;
@@ -639,7 +713,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
             const uint32_t bit = 1u << (2 * stage + x);
             bad = there ? bad & ~bit : bad | bit;
             if (!there && scored[x] && m == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-            const uint16_t *row = p.bounds + ((int64_t)(there ? blk[x] : 0) * p.K + at.at % p.K) * 2 * H + 8 * m;
+            const uint16_t *row = p.bounds + ((int64_t)(there ? blk[x] : 0) * p.K + at.kvh) * 2 * H + 8 * m;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -652,7 +726,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
         if (copied < n) {
             copy(load_at, copied % S);
             if (++copied < n) {
-                load_at.skip(p, kScoreWarps);
+                load_at.next(p, by_tile, by_kvh);
                 look_up(load_at);
             }
         }
@@ -666,7 +740,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     uint32_t qf[2][V][4];  // fragments of min(q, 0) and max(q, 0)
     for (int i = 0; i < n; ++i) {
         advance();
-        const int tile = use_at.at / p.K, kvh = use_at.at - tile * p.K;
+        const int tile = use_at.tile, kvh = use_at.kvh;
         if (use_at.b != q_b || kvh != q_kvh) {
             q_b = use_at.b, q_kvh = kvh;
             nb = (__ldg(p.context_lens + q_b) + kBlockSize - 1) / kBlockSize;
@@ -686,20 +760,24 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
         const int stage = i % S;
         const uint4 *src = ring + (size_t)((warp * S + stage) * kVecs) * 32 + lane;
-        float c[8][4] = {};  // eight chains of at most two products: short sums keep the error bound small
-        uint32_t big = 0u;  // packed max |bound|
+        float c[4] = {};
+        uint32_t big = 0u, small = 0u;  // packed largest upper and smallest lower bound: |bound| is at most the larger end
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const uint4 x = src[(e * V + v) * 32], y = src[((2 + e) * V + v) * 32];
                 const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-                mma_bf16_16816(c[4 * e + 2 * (v & 1)], a0, qf[e][v][0], qf[e][v][1]);
-                mma_bf16_16816(c[4 * e + 2 * (v & 1) + 1], a1, qf[e][v][2], qf[e][v][3]);
+                // every product's sum on its own, added up in fp32: the error bound of the scores stays small
+                float c0[4] = {}, c1[4] = {};
+                mma_bf16_16816(c0, a0, qf[e][v][0], qf[e][v][1]);
+                mma_bf16_16816(c1, a1, qf[e][v][2], qf[e][v][3]);
+#pragma unroll
+                for (int y2 = 0; y2 < 4; ++y2) c[y2] += c0[y2] + c1[y2];
 #pragma unroll
                 for (int y2 = 0; y2 < 4; ++y2) {
-                    big = max_bf16x2(big, a0[y2] & 0x7FFF7FFFu);
-                    big = max_bf16x2(big, a1[y2] & 0x7FFF7FFFu);
+                    if (e) big = max_bf16x2(max_bf16x2(big, a0[y2]), a1[y2]);
+                    else small = min_bf16x2(min_bf16x2(small, a0[y2]), a1[y2]);
                 }
             }
         }
@@ -707,10 +785,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             // this lane's columns are heads 2m and 2m + 1
-            auto sum = [&](int y) {
-                return ((c[0][y] + c[1][y]) + (c[2][y] + c[3][y])) + ((c[4][y] + c[5][y]) + (c[6][y] + c[7][y]));
-            };
-            const float s0 = sum(2 * x), s1 = sum(2 * x + 1);
+            const float s0 = c[2 * x], s1 = c[2 * x + 1];
             float best = -INFINITY;
             bool nan = false;
             if (2 * m < p.G) best = s0, nan = s0 != s0;
@@ -723,13 +798,12 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
             const int j = tile * 16 + r + 8 * x;
             if (m == 0 && j < nb) p.scores[unit * p.max_nb + j] = best;
         }
-        float mb = fmaxf(bf16x2_lo(big), bf16x2_hi(big));
-        // a NaN bound: no bound on the error, every score is looked at in 64 bits
-        if (bf16x2_lo(big) != bf16x2_lo(big) || bf16x2_hi(big) != bf16x2_hi(big)) mb = INFINITY;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, off));
+        big = max_bf16x2(big, small ^ 0x80008000u);  // NaN stays
+        // non-negative numbers order like their bits, NaN above all: no bound on the error then, nor with infinities
+        const uint32_t top = max(big & 0xFFFFu, big >> 16);
+        const float mb = __uint_as_float(min(__reduce_max_sync(0xFFFFFFFFu, top & 0x7FFFu) << 16, 0x7F800000u));
         if (lane == 0) p.tile_max[unit * p.tiles + tile] = mb;
-        if (i + 1 < n) use_at.skip(p, kScoreWarps);
+        if (i + 1 < n) use_at.next(p, by_tile, by_kvh);
     }
 }
 

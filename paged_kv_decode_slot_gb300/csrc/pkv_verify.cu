@@ -9,8 +9,8 @@
 // Exact sums.  Which token a draw falls on is decided where two running sums over a vocabulary of 10^5
 // entries differ by 10^-5 or less, and 32-bit sums, whose order depends on the split, would move those borders.
 // So every weight is split into a multiple of 2^-22 and a multiple of 2^-44 of what is left (the difference
-// p - q with its rounding error first), each summed exactly: four at a time in 32 bits, then as 64-bit integers
-// in units of 2^-44.  The sums do not depend on the order, and a weight is off by little more than 2^-45.
+// p - q with its rounding error first), each summed exactly, as integers.  The sums do not depend on the order, and a
+// weight is off by little more than 2^-45.
 //
 // Bound by memory: one row of p, and where a token was refused one row of q.  A row is cut into one run of entries
 // per warp, runs of at least 256 entries and as many as keep about four CTAs per SM over the whole batch; the last
@@ -30,28 +30,28 @@ __device__ __forceinline__ float prob_at(const uint16_t *row, int64_t i) { retur
 // Probabilities are numbers in [0, 1]: NaN and what is below count as 0, what is above as 1.
 __device__ __forceinline__ float clean(float x) { return __saturatef(x); }
 
-// Up to four weights, summed in their two parts, which fit the 24 bits of a float: a weight is at most 2^22
-// units of 2^-22, and what is left of it at most 2^-23 + 2^-25, below 2^22 units of 2^-44.
+// Sums of weights max(p - q, 0) in two parts, multiples of 2^-22 and of 2^-44.  Adding 3 (1.5 * 2^-21) to a number below
+// 1 (2^-22) rounds it to the last place there, 2^-22 (2^-44), and the sum's bit pattern counts those units: the patterns
+// are added up as integers, the constants' taken off at the end.  Exact up to 256 weights (2^22 units each at most).
 struct WeightSum {
-    float a, b;
-    __device__ __forceinline__ void clear() { a = b = 0.f; }
-    // max(p - q, 0) for cleaned p, q: d is the rounded difference, e what its rounding left (exact: p >= q)
+    static constexpr float kA = 3.f, kB = 3.f / 4194304.f;
+    int a = 0, b = 0;
+    // p cleaned; q only has to be cleaned from below: min(p, q) takes off what lies above p
     __device__ __forceinline__ void add(float p, float q)
     {
-        const float d0 = __fsub_rn(p, q);
-        const float e0 = __fsub_rn(__fsub_rn(p, d0), q);
-        const bool pos = d0 > 0.f;
-        const float d = pos ? d0 : 0.f, e = pos ? e0 : 0.f;
-        constexpr float kA = 3.f, kB = 3.f / 4194304.f;  // 1.5 * 2^1 and 1.5 * 2^-21: units 2^-22 and 2^-44
-        const float ha = __fsub_rn(__fadd_rn(d, kA), kA);
-        const float r = __fadd_rn(__fsub_rn(d, ha), e);
-        const float hb = __fsub_rn(__fadd_rn(r, kB), kB);
-        a = __fadd_rn(a, ha);
-        b = __fadd_rn(b, hb);
+        const float m = fminf(p, q);
+        const float d = __fsub_rn(p, m), e = __fsub_rn(__fsub_rn(p, d), m);  // p - m = d + e exactly (p >= m >= 0)
+        const float ta = __fadd_rn(d, kA);
+        const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(ta, kA)), e);
+        a += __float_as_int(ta);
+        b += __float_as_int(__fadd_rn(r, kB));
     }
-    __device__ __forceinline__ long long units() const
+    // in units of 2^-44, after n additions (integers wrap around and back)
+    __device__ __forceinline__ long long units(int n) const
     {
-        return ((long long)(int)(a * 4194304.f) << 22) + (long long)(int)(b * 17592186044416.f);
+        const int ua = (int)((unsigned)a - (unsigned)n * (unsigned)__float_as_int(kA));
+        const int ub = (int)((unsigned)b - (unsigned)n * (unsigned)__float_as_int(kB));
+        return ((long long)ua << 22) + ub;
     }
 };
 
@@ -168,19 +168,19 @@ struct Pairs {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __device__ static __forceinline__ float at_least_0(float x) { return fmaxf(x, 0.f); }  // NaN: 0
     // units of 2^-44 of all entries; a one-hot draft's token is entry `hot` of this thread's (-1: elsewhere)
     __device__ __forceinline__ long long units(int hot) const
     {
-        long long sum = 0;
+        WeightSum w;
+        if (hot < 0) {
 #pragma unroll
-        for (int h = 0; h < kEntries / 4; ++h) {
-            WeightSum w;
-            w.clear();
+            for (int k = 0; k < kEntries; ++k) w.add(clean(entry(p, k)), at_least_0(entry(q, k)));
+        } else {
 #pragma unroll
-            for (int k = 4 * h; k < 4 * h + 4; ++k) w.add(clean(entry(p, k)), k == hot ? 1.f : clean(entry(q, k)));
-            sum += w.units();
+            for (int k = 0; k < kEntries; ++k) w.add(clean(entry(p, k)), k == hot ? 1.f : 0.f);
         }
-        return sum;
+        return w.units(kEntries);
     }
 };
 
@@ -330,9 +330,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
 #pragma unroll
                 for (int k = 0; k < kMine; ++k) {
                     WeightSum one;
-                    one.clear();
-                    one.add(clean(x.entry(x.p, k)), k == hot ? 1.f : clean(x.entry(x.q, k)));
-                    run += one.units();
+                    one.add(clean(x.entry(x.p, k)), k == hot ? 1.f : x.at_least_0(x.entry(x.q, k)));
+                    run += one.units(1);
                     if (hit < 0 && (double)run > bar) hit = (int)(i + tid * kMine + k);
                 }
                 found = hit;

@@ -121,13 +121,16 @@ def plan_attention(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int, nu
 
 
 def plan_blocks_attention(num_seqs: int, num_kv_heads: int, max_selected: int, num_sms: int) -> AttentionPlan:
-    """Partitions of the selected-block lists for pkv_decode_attn_blocks: one CTA per (sequence, KV
-    head) while those units cover the SMs and the lists are short, else partitions as
-    ``plan_attention`` sizes them for tables of that length."""
-    plan = plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False)
-    if plan.mode == "single":
+    """Partitions of the selected-block lists for pkv_decode_attn_blocks.  Measured on GB300, us:
+      * (sequence, KV head) lists for more than half the SMs: one CTA a list (128 lists of 128 blocks
+        25.9, in 64-block partitions 28.1; of 250 blocks 44.5 and 46.9), up to 128 blocks a list where
+        there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 305, whole 344);
+      * fewer lists: partitions as ``plan_attention`` sizes them, about 512 CTAs of at least 8 blocks
+        (8 lists of 128: 8.3, whole 14.5)."""
+    units = num_seqs * num_kv_heads
+    if max_selected <= 8 or (num_sms < 2 * units and (units < num_sms or max_selected <= LONG_PARTITION_BLOCKS)):
         return AttentionPlan("single", 0, 1)
-    return plan
+    return plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False)
 
 
 class DecodeStep:
