@@ -727,6 +727,15 @@ def _maybe(t, dtype, shape, name: str, dev: int):
     return None if t is None else _arg(t, dtype, shape, name, dev)
 
 
+_arg_py, _maybe_py = _arg, _maybe
+try:  # the same check without the interpreter (csrc/tensor_args.cpp): 0.1 instead of 0.4 us an argument
+    from . import tensor_args as _tensor_args
+    _tensor_args.set_refuse(_refuse)
+    _arg, _maybe = _tensor_args.arg, _tensor_args.maybe
+except ImportError:
+    pass
+
+
 def _shape(t, ndim: int, name: str):
     """The shape of a tensor that sets the sizes of the others."""
     if not isinstance(t, torch.Tensor):

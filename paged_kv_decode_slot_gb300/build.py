@@ -1,10 +1,12 @@
-"""Build libpagedkv.so in-tree for sm_103a with nvcc (translation units compiled in parallel)."""
+"""Build libpagedkv.so in-tree for sm_103a with nvcc (translation units compiled in parallel), and the
+binding's argument check (a small Python extension) with g++."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,40 @@ SOURCES = ["pkv_api.cu", "pkv_attn.cu", "pkv_attn_cols.cu", "pkv_attn_tc.cu", "p
 HEADERS = ["pkv_device.cuh", "pkv_internal.h", "pkv_attn_common.cuh", "pkv_cols.cuh", "pkv_tcgen05.cuh",
            "pkv_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+
+
+ARGS_SOURCE = os.path.join(CSRC, "tensor_args.cpp")
+ARGS_PATH = os.path.join(PKG, "tensor_args.so")
+
+
+def start_tensor_args():
+    """Start compiling the binding's argument check if it is older than its source; None if there is nothing to
+    do.  It needs the headers of Python and torch; without them the binding checks in Python."""
+    if os.path.exists(ARGS_PATH) and os.path.getmtime(ARGS_PATH) >= os.path.getmtime(ARGS_SOURCE):
+        return None
+    import torch
+    base, python = os.path.dirname(torch.__file__), sysconfig.get_paths()["include"]
+    if not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
+        print("tensor_args is not built (no g++ or no Python.h): the binding checks its arguments in Python", file=sys.stderr)
+        return None
+    tmp = ARGS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I", python, ARGS_SOURCE, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def finish_tensor_args(started) -> None:
+    if started is None:
+        return
+    tmp, proc = started
+    text, _ = proc.communicate()
+    if proc.returncode == 0:
+        os.replace(tmp, ARGS_PATH)
+    else:
+        print("tensor_args is not built, the binding checks its arguments in Python:\n" + text.decode(errors="replace")[-2000:],
+              file=sys.stderr)
 
 
 def nvcc_path() -> str:
@@ -47,7 +83,9 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
     variant = out is not None
     out = out or LIB_PATH
     bdir = build_dir or BUILD_DIR
+    started = None if variant else start_tensor_args()
     if not force and not _stale(out):
+        finish_tensor_args(started)
         return out
     nvcc = nvcc_path()
     os.makedirs(bdir, exist_ok=True)
@@ -71,6 +109,7 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
         logs.append(text.decode(errors="replace"))
         if p.returncode != 0:
             failed.append(src)
+    finish_tensor_args(started)
     log_text = "".join(logs)
     with open(os.path.join(bdir, "compile.log"), "w") as f:
         f.write(log_text)

@@ -159,6 +159,7 @@ def test_binding_refuses_host_tensors_types_and_shapes(monkeypatch):
         B.pkv_rope_append(t(4, 8, 128), k, k, *rest)
     with pytest.raises(ValueError):                          # 2 dims
         B.pkv_rope_append(t(4, 64), k, k, *rest)
+    monkeypatch.setattr(B, "_arg", B._arg_py)                # (the compiled check does not take a stand-in for a GPU)
     with pytest.raises(ValueError, match="k_cache must be a CUDA tensor"):
         B.pkv_key_bounds(kc, t(3, 4, dtype=torch.int32).pin_memory() if torch.cuda.is_available() else _Cuda(3, 4, dtype=torch.int32),
                          _Cuda(3, dtype=torch.int32), 1, t(9, 2, 2, 64))
@@ -183,6 +184,8 @@ def test_binding_shapes_must_match(monkeypatch):
     from paged_kv_decode_slot_gb300 import binding as B
     monkeypatch.setattr(B, "_current_device", lambda: 0)
     monkeypatch.setattr(B, "_launch", lambda stream, dev: 0)
+    monkeypatch.setattr(B, "_arg", B._arg_py)                # (the compiled check does not take a stand-in for a GPU)
+    monkeypatch.setattr(B, "_maybe", B._maybe_py)
     c = lambda *shape, dtype=torch.bfloat16: _Cuda(*shape, dtype=dtype)
     i32 = torch.int32
     q, kc, bt, ctx = c(4, 8, 64), c(9, 16, 2, 64), c(4, 5, dtype=i32), c(4, dtype=i32)
@@ -214,6 +217,22 @@ def test_binding_shapes_must_match(monkeypatch):
         base = torch.zeros(5, 8, 64, dtype=torch.bfloat16).as_subclass(_Cuda)
         B.pkv_rope_append(base[:4], c(4, 2, 64), c(4, 2, 64), ctx, c(32, dtype=torch.float64), c(4, dtype=torch.int64),
                           kc, kc, base[1:])
+
+
+def test_compiled_argument_check_is_built_and_refuses_alike():
+    from paged_kv_decode_slot_gb300 import binding as B
+    from paged_kv_decode_slot_gb300.build import build_library
+    build_library()
+    from paged_kv_decode_slot_gb300 import tensor_args
+    x = torch.zeros(3, 4)
+    for check in (tensor_args.arg, B._arg_py):
+        for args, error in (((x, torch.float32, (3, 4), "x", 0), "x must be a CUDA tensor"), ((x, torch.int32, (3, 4), "x", 0), "torch.int32"),
+                            ((x, torch.float32, (3,), "x", 0), "1 dims"), ((None, torch.float32, (3,), "x", 0), "torch.Tensor")):
+            with pytest.raises((TypeError, ValueError), match=error):
+                check(*args)
+    assert tensor_args.maybe(None, torch.float32, (3,), "x", 0) is None
+    with pytest.raises(TypeError):
+        tensor_args.arg(x)
 
 
 def test_plan_blocks_attention():
