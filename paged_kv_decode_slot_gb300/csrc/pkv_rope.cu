@@ -19,63 +19,120 @@
 // registers and the arithmetic (the e4m3 form's quotients above all) has enough warps; results go straight to global
 // memory.  A token whose slot is negative is left out: nothing of its rows is written.
 //
-// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 34.8 us (5.8 TB/s, 85% of the measured
-// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 55 us (4.7 TB/s, 69%): bound by issue
-// slots (72% busy; the quotients are a third of the instructions).
+// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 34.4 us (5.9 TB/s, 86% of the measured
+// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 53.9 us (4.8 TB/s, 70%): bound by issue
+// slots (72% busy before fp32 operations went in pairs; the quotients are a third of the instructions).
 #include "pkv_device.cuh"
 #include "pkv_ops.h"
 
 namespace pkv {
 
 // Threads, heads of a unit, stages and CTAs per SM, measured on 8,192 tokens of 32 + 2 * 8 heads (bf16) and 5,001 of
-// 40 + 2 * 40 (e4m3): 256 / 64 / 2 / 4 34.8 and 55.0 us; 192 / 48 / 3 / 5 34.6 and 60.1 (three units a token instead
-// of two); 192 / 48 / 2 / 6 36.1 and 68.6; 128 / 32 / 3 / 8 46.2 and 64.2; 384 / 96 / 2 / 3 42.8 and 83.4.
+// 40 + 2 * 40 (e4m3) with an earlier form of the arithmetic: 256 / 64 / 2 / 4 34.8 and 55.0 us; 192 / 48 / 3 / 5 34.6 and
+// 60.1 (three units a token instead of two); 192 / 48 / 2 / 6 36.1 and 68.6; 128 / 32 / 3 / 8 46.2 and 64.2; 384 / 96 / 2 / 3
+// 42.8 and 83.4.
 constexpr int kRopeThreads = 256;
 constexpr int kUnitHeads = 64;
 constexpr int kRopeStages = 2;
 constexpr int kRopeCtasPerSm = 4;
 constexpr double kInv2Pi = 0.15915494309189533577;
 
-// Eight values as e4m3 codes of x / scale, the quotient rounded to nearest in fp32 as the plain append takes it (the
-// input is the rotation's 32-bit result, so a turned key is rounded once to 8 bits).  Markstein's theorem (IBM J.
-// Res. Dev. 34, 1990): with r = 1 / scale rounded to nearest and y within an ulp of the quotient,
-// y + (x - y scale) r, both operations fused, is the quotient rounded to nearest.  r0 + s is the reciprocal to twice
-// the precision, so y = x r0 + x s is off by little more than half an ulp.  Nothing over- or underflows where it
-// matters: x is cut off at 512 scale (codes end at 448; NaN stays), quotients below 2^-11 are code 0 whatever their
-// last bits, and scales beyond 2^+-80 are brought nearer to 1 together with x.  Checking a plain x r against both
-// neighbouring codes and dividing where they differ measured 55 against 50 us on 5,001 tokens of 3 * 40 heads.
-__device__ __forceinline__ uint2 rope_quantize8(float (&x)[8], float sc)
+// Two fp32 operations at a time (add, mul and fma on f32x2, sm_100 and later): the kernel is bound by issue slots.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi)
 {
-    if (sc < 0x1p-80f || sc > 0x1p80f) {
-        const float k = sc < 1.f ? 0x1p100f : 0x1p-100f;
-        sc *= k;
+    f32x2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 halves(f32x2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t codes(f32x2 v)
+{
+    const float2 r = halves(v);
+    return f32x2_to_e4m3x2(r.x, r.y);
+}
+
+// Eight values as e4m3 codes of x / scale, the quotient rounded to nearest in fp32 as the plain append takes it (the
+// input is the rotation's 32-bit result, so a turned key is rounded once to 8 bits).  x times a reciprocal made smaller,
+// and made larger, by 2^-21 lie to both sides of that quotient (five roundings of 2^-24 between them): where their codes
+// agree, they are the quotient's too (rounding is monotonic; zeros, infinities and NaN agree with themselves); only
+// where they differ is x divided.  The reciprocal of a scale outside [2^-100, 2^100] may over- or underflow: there
+// every x is divided.  (Correcting one product by its remainder, Markstein's way, measured 57.8 us against 53.9 on 5,001 tokens of 3 * 40 heads.)
+__device__ __forceinline__ uint2 rope_quantize8(const f32x2 (&x)[4], float sc)
+{
+    const float r = __frcp_rn(sc), r0 = r * (1.f - 0x1p-21f), r1 = r * (1.f + 0x1p-21f);
+    const f32x2 down = pair(r0, r0), up = pair(r1, r1);
+    uint32_t c[4], differ = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= k;
+    for (int i = 0; i < 4; ++i) {
+        c[i] = codes(mul2(x[i], down));
+        differ |= c[i] ^ codes(mul2(x[i], up));
     }
-    const float r = __frcp_rn(sc), r0 = __frcp_rd(sc), s = __fmaf_rn(-r0, sc, 1.f) * r0;  // r0 + s is 1 / sc, s >= 0
-    const float most = 512.f * sc;
-    uint32_t c[4];
-    auto quotient = [&](float v) {  // signs of zero included: w s has w's sign, and so has y
-        float w;
-        asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(w) : "f"(v), "f"(most));
-        const float y = __fmaf_rn(w, r0, w * s);
-        return __fmaf_rn(-__fmaf_rn(y, sc, -w), r, y);
-    };
+    if (differ || !(sc >= 0x1p-100f && sc <= 0x1p100f)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(quotient(x[2 * i]), quotient(x[2 * i + 1]));
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = halves(x[i]);
+            c[i] = f32x2_to_e4m3x2(__fdiv_rn(v.x, sc), __fdiv_rn(v.y, sc));
+        }
+    }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-__device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8])
+// A vector's words, unpacked: neighbouring elements of a word as one pair, or (kSplit) the lower elements of two
+// words as one pair and the upper ones as another, which is what interleaved pairs want.
+template <bool kSplit>
+__device__ __forceinline__ void unpack8(const uint4 v, f32x2 (&x)[4])
 {
-    x[0] = bf16x2_lo(v.x), x[1] = bf16x2_hi(v.x), x[2] = bf16x2_lo(v.y), x[3] = bf16x2_hi(v.y);
-    x[4] = bf16x2_lo(v.z), x[5] = bf16x2_hi(v.z), x[6] = bf16x2_lo(v.w), x[7] = bf16x2_hi(v.w);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kSplit) {
+            const uint32_t a = w[i & 2], b = w[(i & 2) + 1];
+            x[i] = i & 1 ? pair(bf16x2_hi(a), bf16x2_hi(b)) : pair(bf16x2_lo(a), bf16x2_lo(b));
+        } else {
+            x[i] = pair(bf16x2_lo(w[i]), bf16x2_hi(w[i]));
+        }
+    }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+// From the split order back to neighbouring elements.
+__device__ __forceinline__ void join8(f32x2 (&x)[4])
 {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float2 a = halves(x[i]), b = halves(x[i + 1]);
+        x[i] = pair(a.x, b.x);
+        x[i + 1] = pair(a.y, b.y);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const f32x2 (&x)[4])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = halves(x[i]);
+        w[i] = pack_bf16x2(v.x, v.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Slot and position of token i (slot < 0: nothing is written for it).
@@ -119,7 +176,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
     constexpr int S = kRopeStages, kPerHead = H / 16;  // items (two 16-byte vectors) of a head
     constexpr int kStageBytes = kUnitHeads * H * 2;
     extern __shared__ __align__(128) uint8_t ring[];  // [S][kUnitHeads][H] bf16
-    // (cos, sin) of this unit's token and of the next one's, two pairs a vector: vector (e / 2) * kGroups + g holds
+    // Cosines and sines of this unit's token and of the next one's: vector (e / 2) * kGroups + g holds (cos, cos, sin, sin) of
     // pairs e, e + 1 of group g, so that neighbouring threads, who turn neighbouring groups, read neighbouring vectors.
     // A group is what one thread reads in a row: 8 pairs, interleaved 4.
     constexpr int kPairs = kInter ? 4 : 8, kGroups = H / 2 / kPairs;
@@ -191,7 +248,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
             float s, c;
             sincospif((float)(int)turns * 0x1p-31f, &s, &c);  // the nearer way round: within half a turn
             const int g = tid / kPairs, e = tid % kPairs;
-            reinterpret_cast<float2 *>(cs[k & 1])[2 * ((e / 2) * kGroups + g) + (e & 1)] = make_float2(c, s);
+            float *to = reinterpret_cast<float *>(cs[k & 1]) + 4 * ((e / 2) * kGroups + g) + (e & 1);
+            to[0] = c;
+            to[2] = s;
         }
     };
     // e4m3: the scales of this thread's items of a unit, loaded one unit ahead
@@ -236,21 +295,28 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
                 const int o0 = from + 8 * (turned || is_v ? c : c - rot), o1 = o0 + width / 2;
                 const uint4 a = *reinterpret_cast<const uint4 *>(src + ((x / kPerHead) * H + o0) * 2);
                 const uint4 b = *reinterpret_cast<const uint4 *>(src + ((x / kPerHead) * H + o1) * 2);
-                float y0[8], y1[8];
-                unpack8(a, y0);
-                unpack8(b, y1);
+                f32x2 y0[4], y1[4];
                 if (turned) {
+                    unpack8<kInter>(a, y0);
+                    unpack8<kInter>(b, y1);
                     // group c, or interleaved, group c for one vector and R / 16 + c for the other
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 v = angles[((e % kPairs) / 2) * kGroups + (kInter && e >= 4 ? rot + c : c)];
-                        const float co = e & 1 ? v.z : v.x, si = e & 1 ? v.w : v.y;
-                        float &r0 = kInter ? (e < 4 ? y0[2 * (e & 3)] : y1[2 * (e & 3)]) : y0[e];
-                        float &r1 = kInter ? (e < 4 ? y0[2 * (e & 3) + 1] : y1[2 * (e & 3) + 1]) : y1[e];
-                        const float f0 = r0, f1 = r1;
-                        r0 = f0 * co - f1 * si;
-                        r1 = f0 * si + f1 * co;
+                    for (int e = 0; e < 4; ++e) {  // two pairs at a time
+                        const float4 v = angles[(kInter ? e & 1 : e) * kGroups + (kInter && e >= 2 ? rot + c : c)];
+                        const f32x2 co = pair(v.x, v.y), si = pair(v.z, v.w), minus = pair(-v.z, -v.w);
+                        f32x2 &r0 = kInter ? (e < 2 ? y0[2 * (e & 1)] : y1[2 * (e & 1)]) : y0[e];
+                        f32x2 &r1 = kInter ? (e < 2 ? y0[2 * (e & 1) + 1] : y1[2 * (e & 1) + 1]) : y1[e];
+                        const f32x2 f0 = r0, f1 = r1;
+                        r0 = fma2(f0, co, mul2(f1, minus));
+                        r1 = fma2(f0, si, mul2(f1, co));
                     }
+                    if constexpr (kInter) {
+                        join8(y0);
+                        join8(y1);
+                    }
+                } else if (kFp8 && head >= p.N) {
+                    unpack8<false>(a, y0);
+                    unpack8<false>(b, y1);
                 }
                 const int kvh = head - p.N - (is_v ? p.K : 0);
                 if (kFp8 && head >= p.N) {
