@@ -537,7 +537,8 @@ int pkv_rope_append_multi_fp8(const pkv_bf16 *q, const pkv_bf16 *k_new, const pk
 
 /* Bounds of the keys: key_bounds bf16 [num_blocks][K][2][H] (16-byte aligned), row 0 the minimum and
    row 1 the maximum of each element over the block's tokens within the context.  One pair per physical
-   block, so blocks shared by sequences share it.  Rebuilds the bounds of every block that holds one of a
+   block, so blocks shared by sequences share it (they are full in each of them; a partly filled one is
+   copied on write).  Rebuilds the bounds of every block that holds one of a
    sequence's last num_new tokens from the keys in the cache: num_new = 1 (or the step's T) after a decode
    step's append, at least the longest context after a prompt or a copy-on-write.  A NaN key makes its
    element's bounds NaN.  H a multiple of 8 (e4m3: 16). */
@@ -577,9 +578,12 @@ int pkv_select_blocks(const pkv_bf16 *q, const pkv_bf16 *key_bounds, const int32
    block id is outside the pool, is skipped and sets PKV_FLAG_BLOCK_RANGE; an entry that appears twice counts
    twice.  Nothing to attend to gives out 0, lse -inf.  partition_blocks 0: one CTA per (sequence, KV head);
    > 0: the list is cut into partitions of that many entries, max_partitions >= ceil(max_selected /
-   partition_blocks), G * max_partitions <= 8192, merged by log-sum-exp in the same launch, with a workspace of
-   pkv_splitk_workspace_bytes(num_seqs, N, H, max_partitions) bytes under its rules.  Other arguments and
-   alignments as pkv_decode_attn_splitk. */
+   partition_blocks), G * max_partitions <= 8192, merged by log-sum-exp in the same launch, with a workspace of at
+   least pkv_splitk_workspace_bytes(num_seqs, N, H, max_partitions) bytes, 256-byte aligned and ZEROED BEFORE ITS
+   FIRST USE: each call leaves its counters, at the end of the workspace_bytes it is given, at zero again.  A
+   workspace for a batch also serves fewer sequences (with the same N, H and max_partitions) if each call is given
+   all of it; it is not shared with other entry points unless zeroed in between, and calls that share it must not
+   overlap on the GPU.  Other arguments and alignments as pkv_decode_attn_splitk. */
 int pkv_decode_attn_blocks(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
                            const int32_t *block_tables, int32_t max_blocks_per_seq,
                            const int32_t *context_lens, const int32_t *selected, int32_t max_selected,
@@ -604,7 +608,10 @@ int pkv_decode_attn_blocks_fp8(const pkv_bf16 *q, const uint8_t *k_cache, const 
  * probabilities at the T + 1 positions decide how many of the T = num_draft drafted tokens stand.
  */
 
-/* Workspace of pkv_verify_draft, 256-byte aligned and ZEROED BEFORE ITS FIRST USE (as above). */
+/* Workspace of pkv_verify_draft, 256-byte aligned and ZEROED BEFORE ITS FIRST USE: each call leaves its counters,
+   at the end of the workspace_bytes it is given, at zero again.  A workspace for a batch also serves smaller ones
+   (fewer sequences, a smaller vocabulary) if each call is given all of it.  Calls that share a workspace must not
+   overlap on the GPU. */
 size_t pkv_verify_workspace_bytes(int32_t num_seqs, int32_t vocab_size);
 
 /* Drafted token x_t = draft_tokens[b][t] stands while accept_u[b][t] * q_t(x_t) < p_t(x_t) (the products

@@ -1386,6 +1386,12 @@ SelectWs select_ws(int32_t B, int32_t K, int32_t max_nb)
     return w;
 }
 
+// The last n int32 of a workspace (4-byte aligned).
+int32_t *tail_counters(void *workspace, size_t bytes, int64_t n)
+{
+    return reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + (bytes / 4 - (size_t)n) * 4);
+}
+
 int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_selected, const float *k_scale,
                      const float *v_scale, int32_t scale_stride, pkv_bf16 *out, float *lse_out,
                      int32_t partition_blocks, int32_t max_partitions, void *workspace, size_t workspace_bytes,
@@ -1404,7 +1410,8 @@ int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_sel
     if (!aligned(out, 4) || !aligned(lse_out, 4) || !aligned(selected, 4)) return PKV_ERR_ALIGN;
     SplitWs w{nullptr, nullptr, nullptr};
     if (partition_blocks > 0) {
-        if (max_partitions <= 0 || (int64_t)max_partitions * partition_blocks < max_selected) return PKV_ERR_SHAPE;
+        const int64_t covered = (int64_t)max_partitions * partition_blocks;
+        if (max_partitions <= 0 || covered < max_selected || covered > INT32_MAX) return PKV_ERR_SHAPE;
         // the unit's last CTA merges in its drained ring; a grid dimension has 65,535 blocks
         if (!merge_in_kernel(a.N, a.d.num_kv_heads, max_partitions)) return PKV_ERR_UNSUPPORTED;
         if (!workspace ||
@@ -1412,6 +1419,8 @@ int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_sel
             return PKV_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return PKV_ERR_ALIGN;
         w = split_ws(workspace, a.B, a.N, a.d.head_dim, max_partitions);
+        // The counters lie at the workspace's end, whatever the batch: partials of a smaller one never reach them.
+        w.counters = tail_counters(workspace, workspace_bytes, (int64_t)a.B * a.N);
     }
     if (a.B == 0) return PKV_OK;
     CUtensorMap tk, tv;
@@ -1544,7 +1553,7 @@ PKV_EXPORT int pkv_decode_attn_blocks_fp8(const pkv_bf16 *q, const uint8_t *k_ca
 // ---- verification of drafted tokens ---------------------------------------------------------
 namespace {
 
-// sums int64 [B][most runs], then (256-byte aligned) counters int32 [B]
+// sums int64 [B][most runs], then (256-byte aligned, and at the workspace's end) counters int32 [B]
 int64_t verify_counter_offset(int32_t B, int32_t vocab)
 {
     const int64_t runs = ((int64_t)vocab + pkv::kVerifyRun - 1) / pkv::kVerifyRun;
@@ -1586,8 +1595,7 @@ PKV_EXPORT int pkv_verify_draft(const void *target_probs, int64_t target_stride,
     p.accepted = num_accepted, p.out = tokens_out;
     p.context_lens = context_lens, p.context_lens_out = context_lens_out;
     p.sums = static_cast<long long *>(workspace);
-    p.counters = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) +
-                                             verify_counter_offset(num_seqs, vocab_size));
+    p.counters = tail_counters(workspace, workspace_bytes, num_seqs);
     p.err_flag = err_flag;
     int sms = 0;
     const int st = sm_count(&sms);

@@ -822,6 +822,7 @@ __global__ void __launch_bounds__(NT) choose_blocks_kernel(const SelectParams p)
     if (nb <= p.M) {  // every block is selected
         int32_t *sel = p.selected + ((size_t)b * p.K + kvh) * p.M;
         for (int x = tid; x < p.M; x += NT) sel[x] = x < nb ? x : -1;
+        pdl_wait_primary();  // whatever runs next on the stream finds the scoring grid done, too
         return;
     }
     float q1 = 0.f;

@@ -228,6 +228,21 @@ def test_repeats_on_another_stream_in_a_graph_and_long_lists(pkv):
     assert pkv.pkv_decode_attn_blocks(q[:0], k, v, tab[:0], ctx[:0], s[:0], c.scale, out[:0]) == pkv.PKV_OK
 
 
+def test_one_workspace_for_batches_of_every_size(pkv):
+    """A batch that shrinks and grows on the workspace of its largest size: the counters stay where no partial reaches."""
+    c = Case(19, [900, 640, 33, 0, 500, 480], 8, 2, 128)
+    sel = c.lists(40)
+    q, k, v, tab, ctx, s = bf16_dev(c.q), bf16_dev(c.k), bf16_dev(c.v), i32_dev(c.tab), i32_dev(c.ctx), torch.from_numpy(sel).cuda()
+    ws = torch.zeros(pkv.pkv_splitk_workspace_bytes(6, 8, 128, 7) + 12, dtype=torch.uint8, device="cuda")
+    first = None
+    for n in (6, 2, 1, 5, 6, 3, 6):
+        out, lse = torch.full_like(q[:n], float("nan")), torch.zeros(n, 8, device="cuda")
+        pkv.check(pkv.pkv_decode_attn_blocks(q[:n], k, v, tab[:n], ctx[:n], s[:n], c.scale, out, lse, 6, 7, ws))
+        first = out if first is None else first
+        assert torch.equal(out.view(torch.int16), first[:n].view(torch.int16))
+    c.check(first, None, sel, "shrinking batch")
+
+
 def test_blocks_past_four_gigabytes(pkv):
     nb = 70000                                                  # 70,000 x 16 x 8 x 128 x 2 bytes: 2.3 GB a pool, 4.6 in all
     c = Case(18, [640, 100], 16, 8, 128)

@@ -196,6 +196,18 @@ def test_the_sampled_tokens_follow_the_target(pkv):
     assert abs(acc.sum() - B * rate) <= 5.5 * math.sqrt(B * rate * (1 - rate))
 
 
+def test_one_workspace_for_batches_and_vocabularies_of_every_size(pkv):
+    B, T, V = 12, 2, 9000
+    p, q, tok, r = draw(10, B, T, V, torch.float32)
+    u, s = r.random((B, T)).astype(np.float32), r.random(B).astype(np.float32)
+    ws = torch.zeros(pkv.pkv_verify_workspace_bytes(B, V) + 5, dtype=torch.uint8, device="cuda")
+    for n, v in ((12, 9000), (1, 9000), (12, 300), (5, 8999), (12, 9000), (11, 17), (12, 9000)):
+        t = np.minimum(tok[:n], v - 1)
+        acc, out, _ = run(pkv, p[:n], q[:n], t, u[:n], s[:n], V=v, ws=ws)
+        want = R.verify(p[:n].double().cpu().numpy(), q[:n].double().cpu().numpy(), t, u[:n], s[:n], V=v)
+        assert np.array_equal(acc, want[0]) and np.array_equal(out, want[1])
+
+
 def test_repeats_on_one_workspace_another_stream_and_in_a_graph(pkv):
     B, T, V = 9, 4, 50001
     p, q, tok, r = draw(9, B, T, V, torch.float32)

@@ -116,6 +116,7 @@ def test_blocks_attention_refusals(lib):
     assert f(pb=2, parts=4) == -7 and f(B=4, pb=2, parts=4, ws=FAKE, size=need - 1) == -7
     assert f(pb=2, parts=4, ws=FAKE + 16, size=need) == -6
     assert f(pb=1, parts=2049, ws=FAKE, size=1 << 40) == -3   # 4 heads x 2,049 weights: more than the merge holds
+    assert f(pb=2 ** 31 - 1, parts=2, ws=FAKE, size=1 << 40) == -2   # more entries than 32 bits count
     assert f(kc=FAKE + 8) == -6 and f(out=FAKE + 2) == -6
     g = caller(lib.pkv_decode_attn_blocks_fp8, [("q", P, FAKE), ("kc", P, FAKE), ("vc", P, FAKE), ("ks", P, FAKE), ("vs", P, FAKE),
                ("stride", I, 0)] + args + [("d", Desc, Desc(64, 16, 2, 128))] + tail)
