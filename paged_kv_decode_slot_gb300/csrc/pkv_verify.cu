@@ -13,9 +13,15 @@
 // weight is off by little more than 2^-45.
 //
 // Bound by memory: one row of p, and where a token was refused one row of q.  A row is cut into one run of entries
-// per warp, runs of at least 256 entries and as many as keep about four CTAs per SM over the whole batch; the last
-// CTA of a sequence to finish adds the runs' sums up, finds the run that the draw falls into and the entry in it.
-// The acceptance is decided by every CTA for itself: a few loads against a second launch.
+// per warp, runs of at least 256 entries and as many as keep about four CTAs per SM over the whole batch, but no more
+// than 1,024 (their sums then go through shared memory in one step); the last CTA of a sequence to finish adds the runs'
+// sums up, finds the run that the draw falls into and the entry in it.  The acceptance is decided by every CTA for
+// itself: a few loads against a second launch.
+//
+// Measured: one sequence (three drafted tokens, 32,000 bf16 entries) 6.5 us, a chain of dependent loads (length, token,
+// probability, row, count, sums, entry); 64 sequences (four drafted tokens, 128,256 fp32 entries) 15.9 us, that chain
+// around one pass over 55 MB in about 8 us.  With a scan over the block for every step of the last CTA's search they took
+// 8.2 and 18.2 us.
 #include "pkv_device.cuh"
 #include "pkv_ops.h"
 
@@ -23,6 +29,7 @@ namespace pkv {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyRuns = 1024;  // runs of a row at most
 
 __device__ __forceinline__ float prob_at(const float *row, int64_t i) { return __ldg(row + i); }
 __device__ __forceinline__ float prob_at(const uint16_t *row, int64_t i) { return bf16_to_f32(__ldg(row + i)); }
@@ -59,7 +66,8 @@ template <typename T>
 struct VerifyRow {  // the row that a sequence's next token is drawn from
     const T *p, *q;  // q null: p alone
     int hot;         // one-hot draft refused: its token (else -1)
-    int accepted;
+    int accepted, len;
+    int token;       // lane t: drafted token t (t < 32)
 };
 
 // The acceptance of sequence b's drafted tokens.  Every CTA decides it for itself (gamma loads of each kind).
@@ -109,6 +117,8 @@ __device__ __forceinline__ VerifyRow<T> decide(const VerifyParams &p, int b, boo
     }
     VerifyRow<T> row;
     row.accepted = n;
+    row.len = len;
+    row.token = x_first;
     row.p = target + (int64_t)n * p.target_stride;
     row.q = draft && n < len ? draft + (int64_t)n * p.draft_stride : nullptr;
     row.hot = !draft && n < len ? hot : -1;
@@ -225,44 +235,88 @@ __device__ __forceinline__ long long run_sum(const VerifyRow<T> &row, int64_t be
     return even ? run_sum_t<T, true>(row, begin, end) : run_sum_t<T, false>(row, begin, end);
 }
 
-__device__ __forceinline__ long long block_sum(long long v, long long *warp_sums)
+__device__ __forceinline__ long long warp_inclusive(long long v)
 {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
-    __syncthreads();
-    long long sum = 0;
-#pragma unroll
-    for (int w = 0; w < kVerifyWarps; ++w) sum += warp_sums[w];
-    return sum;
-}
-
-// Inclusive prefix sums over the CTA.
-__device__ __forceinline__ long long block_inclusive(long long v, long long *warp_sums)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long o = __shfl_up_sync(0xFFFFFFFFu, v, off);
         if (lane >= off) v += o;
     }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kVerifyWarps; ++w) v += w < warp ? warp_sums[w] : 0;
     return v;
+}
+
+// A sequence's last CTA: the token drawn from the row, -1 where the row has no mass.  sums: the runs' sums in shared
+// memory; every warp looks for the run by itself (no barriers), all threads together for the entry in it.
+template <typename T>
+__device__ __forceinline__ int draw(const VerifyRow<T> &row, const VerifyParams &p, int runs, float sample, const long long *sums,
+                                    long long *warp_sums, int *found)
+{
+    constexpr int kMine = Pairs<T>::kEntries;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // lane's share: per consecutive runs
+    const int per = (runs + 31) / 32;
+    long long mine = 0;
+    for (int x = lane * per; x < min(runs, (lane + 1) * per); ++x) mine += sums[x];
+    const long long upto = warp_inclusive(mine), total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    if (total <= 0) return -1;
+    // the running sum has to exceed r * total, r < 1, so the last entry with weight always does; running sums are whole
+    // numbers, so they exceed it where they exceed its floor (below 2^53 units, as those of probabilities are, exact)
+    const long long bar = (long long)floor(fmin(fmax((double)sample, 0.0), 1.0 - 0x1p-53) * (double)total);
+    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, upto > bar)) - 1;
+    long long base = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+    int run = owner * per;
+    for (; base + sums[run] <= bar; ++run) base += sums[run];
+    // entries of the run, consecutive ones for each thread
+    const int64_t begin = (int64_t)run * p.run, end = min((int64_t)p.V, begin + p.run);
+    for (int64_t i0 = begin; i0 < end; i0 += kMine * kVerifyThreads) {
+        const int each = (int)min((int64_t)kMine, (end - i0 + kVerifyThreads - 1) / kVerifyThreads);
+        const int64_t i = i0 + (int64_t)tid * each, stop = min(end, i + each);
+        Pairs<T> x;
+        x.template load<false>(row, i, 1, stop);
+        const int hot = hot_entry(row, i, 1, false);
+        const long long w = x.units(hot < each ? hot : -1), inc = warp_inclusive(w);
+        if (lane == 31) warp_sums[warp] = inc;
+        if (tid == 0) *found = -1;
+        __syncthreads();
+        long long after = base + inc, all = 0;
+#pragma unroll
+        for (int y = 0; y < kVerifyWarps; ++y) {
+            after += y < warp ? warp_sums[y] : 0;
+            all += warp_sums[y];
+        }
+        if (after > bar && after - w <= bar) {  // one thread: its entries one by one
+            long long at = after - w;
+            int hit = -1;
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+                WeightSum one;
+                one.add(clean(x.entry(x.p, k)), k == hot ? 1.f : x.at_least_0(x.entry(x.q, k)));
+                at += one.units(1);
+                if (hit < 0 && at > bar) hit = (int)(i + k);
+            }
+            *found = hit;
+        }
+        __syncthreads();
+        const int token = *found;
+        __syncthreads();
+        if (token >= 0) return token;
+        base += all;
+    }
+    return -1;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p)
 {
+    __shared__ long long all_sums[kVerifyRuns];
     __shared__ long long warp_sums[kVerifyWarps];
-    __shared__ long long found_before;
     __shared__ int found, last_one;
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     VerifyRow<T> row = decide<T>(p, b, c == 0 && tid < 32);
+    // what the last CTA needs besides the sums: loaded before it is known to be the last
+    const float sample = p.sample_u[b];
+    const int ctx = p.context_lens ? p.context_lens[b] : 0;
     const int runs = (p.V + p.run - 1) / p.run;
     long long *sums = p.sums + (int64_t)b * runs;
     const int r = c * kVerifyWarps + (tid >> 5);  // this warp's run
@@ -275,92 +329,42 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     __syncthreads();
     if (!last_one) return;
 
-    // ---- the sequence's last CTA: total, run, entry ----
-    int token = -1;
-    for (int pass = 0; pass < 2 && token < 0; ++pass) {
-        if (pass) {
-            // no residual mass (p nowhere above q): the token is drawn from p itself
-            if (!row.q && row.hot < 0) break;
-            row.q = nullptr;
-            row.hot = -1;
-            for (int x = tid >> 5; x < runs; x += kVerifyWarps) {
-                const long long v = run_sum(row, (int64_t)x * p.run, min((int64_t)p.V, (int64_t)(x + 1) * p.run));
-                if ((tid & 31) == 0) sums[x] = v;
-            }
-            __syncthreads();
+    for (int x = tid; x < runs; x += kVerifyThreads) all_sums[x] = __ldcg(sums + x);
+    __syncthreads();
+    int token = draw(row, p, runs, sample, all_sums, warp_sums, &found);
+    if (token < 0 && (row.q || row.hot >= 0)) {
+        // no residual mass (p nowhere above q): the token is drawn from p itself
+        row.q = nullptr;
+        row.hot = -1;
+        __syncthreads();
+        for (int x = tid >> 5; x < runs; x += kVerifyWarps) {
+            const long long v = run_sum(row, (int64_t)x * p.run, min((int64_t)p.V, (int64_t)(x + 1) * p.run));
+            if ((tid & 31) == 0) all_sums[x] = v;
         }
-        long long total = 0;
-        for (int x = tid; x < runs; x += kVerifyThreads) total += __ldcg(sums + x);
-        total = block_sum(total, warp_sums);
-        if (total <= 0) continue;
-        // r < 1 and the running sum must exceed r * total, so the last entry with weight always does; sums below
-        // 2^53 units (rows that are no distributions may have more) are exact in 64 bits
-        const double bar = fmin(fmax((double)p.sample_u[b], 0.0), 1.0 - 0x1p-53) * (double)total;
-        // sums of [x0 + tid] or of entries: the thread whose running sum is the first above the bar reports
-        auto reaches = [&](long long upto, long long v) { return (double)upto > bar && (double)(upto - v) <= bar; };
-        long long before = 0;
-        for (int x0 = 0; x0 < runs; x0 += kVerifyThreads) {
-            const int x = x0 + tid;
-            const long long v = x < runs ? __ldcg(sums + x) : 0;
-            const long long upto = before + block_inclusive(v, warp_sums);
-            if (tid == 0) found = -1;
-            __syncthreads();
-            if (reaches(upto, v)) {
-                found = x;
-                found_before = upto - v;
-            }
-            __syncthreads();
-            if (found >= 0) break;
-            before += block_sum(v, warp_sums);
-        }
-        const int64_t begin = (int64_t)found * p.run, end = min((int64_t)p.V, begin + p.run);
-        before = found_before;
-        constexpr int kMine = Pairs<T>::kEntries;  // consecutive entries of a thread
-        for (int64_t i = begin; i < end && token < 0; i += kMine * kVerifyThreads) {
-            Pairs<T> x;
-            x.template load<false>(row, i + tid * kMine, 1, end);
-            const int hot = hot_entry(row, i + tid * kMine, 1, false);
-            const long long v = x.units(hot);
-            const long long upto = before + block_inclusive(v, warp_sums);
-            if (tid == 0) found = -1;
-            __syncthreads();
-            if (reaches(upto, v)) {  // this thread's entries, one by one
-                long long run = upto - v;
-                int hit = -1;
-#pragma unroll
-                for (int k = 0; k < kMine; ++k) {
-                    WeightSum one;
-                    one.add(clean(x.entry(x.p, k)), k == hot ? 1.f : x.at_least_0(x.entry(x.q, k)));
-                    run += one.units(1);
-                    if (hit < 0 && (double)run > bar) hit = (int)(i + tid * kMine + k);
-                }
-                found = hit;
-            }
-            __syncthreads();
-            token = found;
-            before += block_sum(v, warp_sums);  // its barriers also keep `found` until all have read it
-        }
+        __syncthreads();
+        token = draw(row, p, runs, sample, all_sums, warp_sums, &found);
     }
     if (token < 0 && tid == 0) set_flag(p.err_flag, PKV_FLAG_NO_MASS);
     const int n = row.accepted;
-    for (int t = tid; t <= p.T; t += kVerifyThreads)
-        p.out[(int64_t)b * (p.T + 1) + t] = t < n ? p.tokens[(int64_t)b * p.T + t] : (t == n ? token : -1);
+    for (int t = tid; t <= p.T; t += kVerifyThreads) {
+        int x = token;
+        if (t < n) x = t < 32 ? row.token : p.tokens[(int64_t)b * p.T + t];
+        p.out[(int64_t)b * (p.T + 1) + t] = t <= n ? x : -1;
+    }
     if (tid == 0) {
         p.accepted[b] = n;
-        if (p.context_lens) {
-            const int len = p.lens ? min(max(p.lens[b], 0), p.T) : p.T;
-            p.context_lens_out[b] = p.context_lens[b] - len + n;
-        }
+        if (p.context_lens) p.context_lens_out[b] = ctx - row.len + n;
         p.counters[b] = 0;  // ready for the next call
     }
 }
 
 cudaError_t launch_verify(VerifyParams p, bool bf16, int sms, cudaStream_t stream)
 {
-    // runs of at least kVerifyRun entries, CTAs enough for about four per SM
+    // runs of at least kVerifyRun entries, at most kVerifyRuns of them, CTAs enough for about four per SM
     const int most = (p.V + kVerifyRun * kVerifyWarps - 1) / (kVerifyRun * kVerifyWarps);
     const int want = (4 * sms + p.B - 1) / p.B;
-    const int ctas = want < most ? want : most;
+    int ctas = want < most ? want : most;
+    if (ctas > kVerifyRuns / kVerifyWarps) ctas = kVerifyRuns / kVerifyWarps;
     const int per = (p.V + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
     p.run = (per + kVerifyRun - 1) / kVerifyRun * kVerifyRun;
     const int runs = (p.V + p.run - 1) / p.run;

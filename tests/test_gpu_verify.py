@@ -66,6 +66,17 @@ def test_matches_the_definition(pkv, B, T, V, onehot, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("B,T,V", [(700, 1, 40001), (1, 2, 300001), (2, 1, 524287)])
+def test_runs_of_many_entries_and_rows_of_many_runs(pkv, B, T, V, dtype):
+    """One CTA a row, so that the draw goes through a run in several steps; rows cut into as many runs as there may be."""
+    p, q, tok, r = draw(B + T + V, B, T, V, dtype)
+    u, s = r.random((B, T)).astype(np.float32), r.random(B).astype(np.float32)
+    acc, out, _ = run(pkv, p, q, tok, u, s)
+    want = R.verify(p.double().cpu().numpy(), q.double().cpu().numpy(), tok, u, s)
+    assert np.array_equal(acc, want[0]) and np.array_equal(out, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 def test_ragged_drafts_padded_rows_and_shorter_contexts(pkv, dtype):
     """Draft lengths from 0 to T, rows wider than the vocabulary (with values that must not count), contexts kept."""
     B, T, V = 40, 5, 1001
