@@ -64,7 +64,7 @@ __device__ __forceinline__ bool bounds_block(const BoundsParams &p, int &blk, in
         return false;
     }
     const int j = max(0, ctx - p.num_new) / kBlockSize + blockIdx.x;
-    if (j * kBlockSize >= ctx) return false;
+    if (j >= (ctx + kBlockSize - 1) / kBlockSize) return false;
     blk = p.block_tables[(size_t)b * p.max_nb + j];
     if (blk < 0 || blk >= p.num_blocks) {
         if (threadIdx.x == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
@@ -332,8 +332,8 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
     return lo;
 }
 
-// The sum over h of max(q lo, q hi) in 64 bits, the largest over the group's heads (products of two bf16
-// numbers are exact in 32 bits), by one warp: every lane's order and the shuffles' are the same for
+// The sum over h of max(q lo, q hi) in 64 bits, the largest over the group's heads (in 32 bits products of bf16
+// numbers may over- or underflow; here they are exact), by one warp: every lane's order and the shuffles' are the same for
 // every block, so equal blocks get equal sums.
 template <int H>
 __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int kvh, int j, int lane)
@@ -355,7 +355,7 @@ __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int 
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float x = bf16_to_f32(q[g * H + e]);
-            sum += (double)(x * (x > 0.f ? hi[e] : lo[e]));
+            sum += (double)x * (double)(x > 0.f ? hi[e] : lo[e]);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
@@ -482,14 +482,16 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     // eps: 2^-18 |q|_1 max|bound| = 2^-18 S.  A score is the fp32 sum of sixteen mma of 16 products each.  No product exceeds
     // S and an mma's own sum its part S' of S; one that keeps 23 bits below its largest term loses at most 2^-23 S' for each
     // of its 16 terms and once more at its end, and every addition after it 2^-24 S: (17 + 7.5) 2^-23 S, and a third as
-    // much again for slack in what the documentation leaves open about the rounding inside an mma.
+    // much again for slack in what the documentation leaves open about the rounding inside an mma.  Products and sums that
+    // underflow are off by 2^-126 each at most, 2^-117 for all of a score's: 2^-111 has the same slack and changes nothing
+    // for scores of ordinary size.  Where products may overflow, S does.
     float all_q = s.bound[0][0], all_b = s.bound[1][0];
 #pragma unroll
     for (int w = 1; w < (NT / 32); ++w) {
         all_q = fmaxf(all_q, s.bound[0][w]);
         all_b = fmaxf(all_b, s.bound[1][w]);
     }
-    const float eps2 = 2.f * ldexpf(all_q * all_b, -18);
+    const float eps2 = 2.f * (ldexpf(all_q * all_b, -18) + 0x1p-111f);
     // bounds of the undecided scores, rounded outwards; infinite bounds (0 times infinity in the products) leave every
     // score undecided
     const bool bounded = eps2 < INFINITY;

@@ -126,6 +126,16 @@ def test_selection_of_long_contexts(pkv, nb, M):
     check(pkv, q, bounds, tab, ctx, M, 1, 2)
 
 
+@pytest.mark.parametrize("eq,eb", [(-70, -65), (-60, -60), (-120, -10), (70, 66), (100, 27)])
+def test_scores_that_leave_the_range_of_32_bits(pkv, eq, eb):
+    """Products and sums that under- or overflow in 32 bits: the choice is that of the real values all the same."""
+    ctx = [16 * 300, 16 * 40 + 1]
+    q, bounds, tab, _ = case(eq + eb + 400, ctx, 4, 2, 64)
+    q, bounds = R.to_bf16(R.bf16_values(q) * 2.0 ** eq), R.to_bf16(R.bf16_values(bounds) * 2.0 ** eb)
+    assert np.isfinite(R.bf16_values(q)).all() and np.isfinite(R.bf16_values(bounds)).all()
+    check(pkv, q, bounds, tab, ctx, 20, 1, 1)
+
+
 def test_ties_go_to_the_lowest_index(pkv):
     """Equal blocks, a query of zeros, and equal scores of different blocks."""
     ctx = [16 * 700, 16 * 90, 16 * 20]
