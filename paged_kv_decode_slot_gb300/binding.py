@@ -728,11 +728,15 @@ def _maybe(t, dtype, shape, name: str, dev: int):
 
 
 _arg_py, _maybe_py = _arg, _maybe
+_calls = None
 try:  # the same check without the interpreter (csrc/tensor_args.cpp): 0.1 instead of 0.4 us an argument
     from . import tensor_args as _tensor_args
     _tensor_args.set_refuse(_refuse)
     _arg, _maybe = _tensor_args.arg, _tensor_args.maybe
-except ImportError:
+    # and whole calls: they return None for what is not plain, which the forms below then take or refuse
+    _tensor_args.use_library(_lib._handle, lambda stream, dev: _launch(stream, dev))
+    _calls = _tensor_args
+except (ImportError, AttributeError):  # not built, or by an older source
     pass
 
 
@@ -788,6 +792,11 @@ def pkv_rope_append(q, k_new, v_new, positions, inv_freq, slot_mapping, k_cache,
     inv_freq float64 [rotary_dim / 2]: q turned into q_out (or in place), k_new turned and v_new
     written into their slots."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.rope_append(q, k_new, v_new, positions, inv_freq, k_cache, v_cache, q_out, slot_mapping, interleaved,
+                                    err_flag, stream, dev)
+        if status is not None:
+            return status
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _bf16, 1, dev)
     n = q.shape[0]
     if n == 0:
@@ -801,6 +810,11 @@ def pkv_rope_append_fp8(q, k_new, v_new, positions, inv_freq, k_scale, v_scale, 
                         q_out, interleaved: bool = False, err_flag=None, stream=None) -> int:
     """pkv_rope_append into e4m3 pools (uint8) with scales [K] or [num_blocks, K]."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.rope_append_fp8(q, k_new, v_new, positions, inv_freq, k_scale, v_scale, k_cache, v_cache, q_out,
+                                        slot_mapping, interleaved, err_flag, stream, dev)
+        if status is not None:
+            return status
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _u8, 1, dev)
     ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
     n = q.shape[0]
@@ -822,6 +836,11 @@ def pkv_rope_append_multi(q, k_new, v_new, block_tables, context_lens, inv_freq,
     """The T newest tokens of each sequence: q, q_out bf16 [B, T, N, H]; k_new, v_new [B, T, K, H];
     slot_mapping int64 [B, T] (written)."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.rope_append_multi(q, k_new, v_new, block_tables, context_lens, inv_freq, k_cache, v_cache, q_out,
+                                          slot_mapping, interleaved, err_flag, stream, dev)
+        if status is not None:
+            return status
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _bf16, 2, dev)
     B, T = q.shape[:2]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
@@ -837,6 +856,11 @@ def pkv_rope_append_multi_fp8(q, k_new, v_new, block_tables, context_lens, inv_f
                               stream=None) -> int:
     """pkv_rope_append_multi into e4m3 pools (uint8) with scales [K] or [num_blocks, K]."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.rope_append_multi_fp8(q, k_new, v_new, block_tables, context_lens, inv_freq, k_scale, v_scale,
+                                              k_cache, v_cache, q_out, slot_mapping, interleaved, err_flag, stream, dev)
+        if status is not None:
+            return status
     qp, kp, vp, op, kc, vc, fp, R, N, desc = _rope_args(q, k_new, v_new, inv_freq, k_cache, v_cache, q_out, _u8, 2, dev)
     ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
     B, T = q.shape[:2]
@@ -874,6 +898,10 @@ def pkv_key_bounds(k_cache, block_tables, context_lens, num_new: int, key_bounds
     """key_bounds bf16 [num_blocks, K, 2, H]: minimum and maximum of the keys of every block that holds
     one of a sequence's last num_new tokens."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.key_bounds(k_cache, block_tables, context_lens, num_new, key_bounds, err_flag, stream, dev)
+        if status is not None:
+            return status
     kc, tp, width, cp, B, bp, desc = _bounds_args(k_cache, _bf16, block_tables, context_lens, key_bounds, dev)
     if B == 0:
         return PKV_OK
@@ -885,6 +913,10 @@ def pkv_key_bounds_fp8(k_cache, k_scale, block_tables, context_lens, num_new: in
                        stream=None) -> int:
     """pkv_key_bounds of an e4m3 pool (uint8) with scales [K] or [num_blocks, K]."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.key_bounds_fp8(k_cache, k_scale, block_tables, context_lens, num_new, key_bounds, err_flag, stream, dev)
+        if status is not None:
+            return status
     kc, tp, width, cp, B, bp, desc = _bounds_args(k_cache, _u8, block_tables, context_lens, key_bounds, dev)
     ks, _, stride = _scale_args(k_scale, k_scale, desc.num_blocks, desc.num_kv_heads, dev)
     if B == 0:
@@ -902,6 +934,11 @@ def pkv_select_blocks(q, key_bounds, block_tables, context_lens, selected, works
     """selected int32 [B, K, M]: the logical blocks each (sequence, KV head) attends to, ascending, -1
     behind them.  workspace: pkv_select_workspace_bytes(B, K, max_blocks) bytes."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.select_blocks(q, key_bounds, block_tables, context_lens, selected, workspace, first_blocks,
+                                      last_blocks, err_flag, BLOCK_SIZE, stream, dev)
+        if status is not None:
+            return status
     qs, (nb, K, _, H) = _shape(q, 3, "q"), _shape(key_bounds, 4, "key_bounds")
     B, N, _ = qs
     M, size = _shape(selected, 3, "selected")[2], _shape(workspace, 1, "workspace")[0]
@@ -934,6 +971,11 @@ def pkv_decode_attn_blocks(q, k_cache, v_cache, block_tables, context_lens, sele
                            err_flag=None, stream=None) -> int:
     """Decode attention of each KV head's query group over the logical blocks selected [B, K, M]."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.decode_attn_blocks(q, k_cache, v_cache, block_tables, context_lens, selected, scale, out, lse_out,
+                                           partition_blocks, max_partitions, workspace, err_flag, stream, dev)
+        if status is not None:
+            return status
     qp, kc, vc, tp, width, cp, sp, M, B, N, op, lp, desc, ws, size = _blocks_args(
         q, k_cache, v_cache, _bf16, block_tables, context_lens, selected, out, lse_out, workspace, dev)
     if B == 0:
@@ -948,6 +990,12 @@ def pkv_decode_attn_blocks_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
                                workspace=None, err_flag=None, stream=None) -> int:
     """pkv_decode_attn_blocks over e4m3 pools (uint8) with scales [K] or [num_blocks, K]."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.decode_attn_blocks_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, selected,
+                                               scale, out, lse_out, partition_blocks, max_partitions, workspace,
+                                               err_flag, stream, dev)
+        if status is not None:
+            return status
     qp, kc, vc, tp, width, cp, sp, M, B, N, op, lp, desc, ws, size = _blocks_args(
         q, k_cache, v_cache, _u8, block_tables, context_lens, selected, out, lse_out, workspace, dev)
     ks, vs, stride = _scale_args(k_scale, v_scale, desc.num_blocks, desc.num_kv_heads, dev)
@@ -977,6 +1025,11 @@ def pkv_verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u
     accept_u float32 [B, T]; sample_u float32 [B]; num_accepted int32 [B] and tokens_out int32 [B, T + 1]
     (written); draft_lens, context_lens, context_lens_out int32 [B]."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u, num_accepted, tokens_out,
+                                     workspace, draft_lens, context_lens, context_lens_out, vocab_size, err_flag, stream, dev)
+        if status is not None:
+            return status
     B, rows, width = _shape(target_probs, 3, "target_probs")
     T, dtype = rows - 1, target_probs.dtype
     if dtype is not _f32 and dtype is not _bf16:

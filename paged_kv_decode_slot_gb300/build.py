@@ -28,7 +28,8 @@ ARGS_PATH = os.path.join(PKG, "tensor_args.so")
 def start_tensor_args():
     """Start compiling the binding's argument check if it is older than its source; None if there is nothing to
     do.  It needs the headers of Python and torch; without them the binding checks in Python."""
-    if os.path.exists(ARGS_PATH) and os.path.getmtime(ARGS_PATH) >= os.path.getmtime(ARGS_SOURCE):
+    if os.path.exists(ARGS_PATH) and os.path.getmtime(ARGS_PATH) >= max(
+            os.path.getmtime(f) for f in (ARGS_SOURCE, os.path.join(INCLUDE, "pkv.h"))):
         return None
     import torch
     base, python = os.path.dirname(torch.__file__), sysconfig.get_paths()["include"]
@@ -38,8 +39,8 @@ def start_tensor_args():
     tmp = ARGS_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(base, "include"),
-           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I", python, ARGS_SOURCE, "-o", tmp,
-           "-L", os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I", python, "-I", INCLUDE, ARGS_SOURCE,
+           "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-ldl"]
     return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 

@@ -121,6 +121,45 @@ def test_sparse_decode_steps(pkv, kv, graph):
         assert full.any() and not full.all()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_calls_made_by_the_extension_and_from_python_are_alike(pkv, kv, monkeypatch):
+    """Plain arguments go through the compiled calls, every one of them; without the extension the results are the same bits."""
+    from paged_kv_decode_slot_gb300 import binding as B
+    from paged_kv_decode_slot_gb300.step import SparseDecodeStep
+    assert B._calls is not None
+    taken = {}
+
+    class Recorder:
+        def __getattr__(self, name):
+            def call(*args):
+                status = getattr(compiled, name)(*args)
+                taken.setdefault(name, []).append(status)
+                return status
+            return call
+    compiled, results = B._calls, []
+    for calls in (Recorder(), None):
+        monkeypatch.setattr(B, "_calls", calls)
+        s = Serving(pkv, 3, [300, 20], 20, kv)
+        q, k, v = (bf16_dev(R.to_bf16(s.r.standard_normal((s.B, h, H)))) for h in (N, K, K))
+        scales = dict(k_scale=s.scales[0], v_scale=s.scales[1]) if s.scales else {}
+        step = SparseDecodeStep(q, k, v, s.kc, s.vc, s.bounds, s.tables, i32_dev(s.lens + 1), 0.1, s.inv, 9, err_flag=s.err, **scales)
+        step.run(torch.cuda.current_stream())
+        p = torch.softmax(torch.from_numpy(s.r.standard_normal((s.B, 3, 77))).cuda(), -1).float()
+        tok, u = torch.zeros(s.B, 2, dtype=torch.int32, device="cuda"), torch.from_numpy(s.r.random((s.B, 2)).astype(np.float32)).cuda()
+        acc, out = torch.empty(s.B, dtype=torch.int32, device="cuda"), torch.empty(s.B, 3, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(pkv.pkv_verify_workspace_bytes(s.B, 77), dtype=torch.uint8, device="cuda")
+        for V in (None, 70):
+            pkv.check(pkv.pkv_verify_draft(p, None, tok, u, u[:, 0].contiguous(), acc, out, ws, vocab_size=V))
+        assert pkv.pkv_read_err_flag(s.err) == (pkv.PKV_OK, 0)
+        results.append([t.cpu().view(torch.uint8) for t in (s.kc, s.vc, s.bounds, step.q_turned, step.slot_mapping, step.selected, step.out,
+                                                           step.lse, acc, out)])
+    fp8 = "" if kv == "bf16" else "_fp8"
+    assert sorted(taken) == sorted(["rope_append" + fp8, "rope_append_multi" + fp8, "key_bounds" + fp8, "select_blocks",
+                                    "decode_attn_blocks" + fp8, "verify_draft"])
+    assert all(x == 0 for seen in taken.values() for x in seen)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_speculative_steps_over_one_cache(pkv):
     """T drafted tokens and the one before them: rotating append, multi-token attention, verification against the target's
     probabilities, and the next step from the context that remains -- refused tokens' slots are written over."""

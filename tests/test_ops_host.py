@@ -236,6 +236,26 @@ def test_compiled_argument_check_is_built_and_refuses_alike():
         tensor_args.arg(x)
 
 
+def test_compiled_calls_leave_what_is_not_plain_to_the_binding():
+    """Host tensors, other types, missing arguments and sizes that do not fit: None, and nothing is called."""
+    from paged_kv_decode_slot_gb300 import binding as B
+    from paged_kv_decode_slot_gb300.build import build_library
+    build_library()
+    from paged_kv_decode_slot_gb300 import tensor_args
+    assert B._calls is tensor_args
+    counts = dict(rope_append=13, rope_append_fp8=15, rope_append_multi=14, rope_append_multi_fp8=16, key_bounds=8, key_bounds_fp8=9,
+                  select_blocks=12, decode_attn_blocks=15, decode_attn_blocks_fp8=17, verify_draft=15)
+    t = torch.zeros(2, 3, 64, dtype=torch.bfloat16)
+    for name, n in counts.items():
+        f = getattr(tensor_args, name)
+        for args in ((), (t,) * n, (None,) * n, (t,) * (n - 1) + (0,), (t,) * (n - 2) + (None, 0), (1,) * n, (1 << 80,) * n, ("x",) * (n + 1)):
+            assert f(*args) is None, (name, len(args))
+    with pytest.raises(TypeError):
+        tensor_args.use_library(0)
+    with pytest.raises(ImportError):
+        tensor_args.use_library(ctypes.CDLL(None)._handle, B._launch)
+
+
 def test_plan_blocks_attention():
     from paged_kv_decode_slot_gb300.step import plan_blocks_attention as plan
     p = plan(64, 8, 128, 152)
