@@ -113,6 +113,21 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int32_t *sel = p.selected + ((size_t)b * p.K + kvh) * p.M + begin;
     const int pw = warp - W;  // producer warp
 
+    const uint32_t bar_full = base_u32 + L::kBarOffset;
+    const uint32_t bar_empty = bar_full + 8 * S;
+    volatile int *valid_of = reinterpret_cast<volatile int *>(base + L::kMiscOffset);  // [S] tokens that count
+    volatile int *abort_flag = valid_of + S;
+    volatile int *issued_count = abort_flag + 1;  // [P]
+    volatile float2 *stage_sc = reinterpret_cast<volatile float2 *>(base + L::kScaleOffset);
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        *abort_flag = 0;
+        for (int q = 0; q < P; ++q) issued_count[q] = 0;
+        init_ring<S>(bar_full, bar_empty);
+    }
+    pdl_wait_primary();  // launched early: nothing is read or written before the launch ahead is done
+    pdl_launch_dependents();
     int first_sel = -1;  // the producers' first list entries do not depend on the length
     if (pw >= 0 && begin + pw + P * lane < min(p.M, begin + p.part_blocks)) first_sel = __ldg(sel + pw + P * lane);
     int ctx = p.context_lens[b];
@@ -136,17 +151,6 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         return;
     }
 
-    const uint32_t bar_full = base_u32 + L::kBarOffset;
-    const uint32_t bar_empty = bar_full + 8 * S;
-    volatile int *valid_of = reinterpret_cast<volatile int *>(base + L::kMiscOffset);  // [S] tokens that count
-    volatile int *abort_flag = valid_of + S;
-    volatile int *issued_count = abort_flag + 1;  // [P]
-    volatile float2 *stage_sc = reinterpret_cast<volatile float2 *>(base + L::kScaleOffset);
-    if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        for (int q = 0; q < P; ++q) issued_count[q] = 0;
-        init_ring<S>(bar_full, bar_empty);
-    }
     __syncthreads();
 
     WarpAcc<H> acc;
@@ -154,10 +158,6 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
     if (pw >= 0) {
         // ------------------------------ producer warps ------------------------------
-        if (lane == 0 && pw == 0) {
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-        }
         const int32_t *tbl = p.block_tables + (size_t)b * p.max_nb;
         const int mine = n > pw ? (n - pw + P - 1) / P : 0;
         // one tile per lane: its block id (-1: skipped), the tokens that count, its scales
@@ -340,8 +340,8 @@ static cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const 
         if (e != cudaSuccess) return e;
         ready[dev] = 1;
     }
-    attn_blocks_kernel<H, kFp8, W><<<dim3(p.K, p.B, p.max_parts), (W + kProducers) * 32, smem, stream>>>(tk, tv, p);
-    return cudaGetLastError();
+    return launch_kernel(attn_blocks_kernel<H, kFp8, W>, dim3(p.K, p.B, p.max_parts), dim3((W + kProducers) * 32), smem, stream, true,
+                         tk, tv, p);
 }
 
 cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, int sms,

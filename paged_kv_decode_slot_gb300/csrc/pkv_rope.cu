@@ -23,6 +23,7 @@
 // copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 53.9 us (4.8 TB/s, 70%): bound by issue
 // slots (72% busy before fp32 operations went in pairs; the quotients are a third of the instructions).
 #include "pkv_device.cuh"
+#include "pkv_internal.h"
 #include "pkv_ops.h"
 
 namespace pkv {
@@ -220,6 +221,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
         aborted = 0;
         for (int s = 0; s < S; ++s) mbar_init(smem_u32(full + s), 1);
         fence_barrier_init();
+    }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (tid == 0) {
         for (; copied < S && ahead.i < p.n; ++copied, advance(ahead)) load(ahead, copied);
     }
     unsigned long long freq = 0;  // turns per position in units of 2^-64, of pair tid
@@ -368,8 +373,7 @@ static cudaError_t launch_k(const RopeParams &p, unsigned grid, cudaStream_t str
         if (e != cudaSuccess) return e;
         ready[dev] = 1;
     }
-    rope_append_kernel<H, kInter, kFp8><<<grid, kRopeThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(rope_append_kernel<H, kInter, kFp8>, dim3(grid), dim3(kRopeThreads), smem, stream, true, p);
 }
 
 template <int H>

@@ -76,6 +76,8 @@ __device__ __forceinline__ bool bounds_block(const BoundsParams &p, int &blk, in
 
 __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const BoundsParams p)
 {
+    pdl_wait_primary();
+    pdl_launch_dependents();
     int blk, rows;
     if (!bounds_block(p, blk, rows)) return;
     const int vecs = p.K * p.H / 8;  // 16-byte columns of a token row
@@ -103,6 +105,8 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_kernel(const Bounds
 // step inside the key it bounds.
 __global__ void __launch_bounds__(kBoundsThreads) key_bounds_fp8_kernel(const BoundsParams p)
 {
+    pdl_wait_primary();
+    pdl_launch_dependents();
     int blk, rows;
     if (!bounds_block(p, blk, rows)) return;
     const int vecs = p.K * p.H / 16;
@@ -145,9 +149,7 @@ __global__ void __launch_bounds__(kBoundsThreads) key_bounds_fp8_kernel(const Bo
 cudaError_t launch_key_bounds(const BoundsParams &p, bool fp8, int span, cudaStream_t stream)
 {
     const dim3 grid(span, p.B);
-    if (fp8) key_bounds_fp8_kernel<<<grid, kBoundsThreads, 0, stream>>>(p);
-    else key_bounds_kernel<<<grid, kBoundsThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(fp8 ? key_bounds_fp8_kernel : key_bounds_kernel, grid, dim3(kBoundsThreads), 0, stream, true, p);
 }
 
 // -------------------------------------- selection -------------------------------------------
@@ -653,7 +655,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     extern __shared__ uint4 ring[];  // [warps][S][kVecs][32]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, m = lane & 3;
-    pdl_launch_dependents();  // the choosing grid may take its place; it waits for this one
+    pdl_wait_primary();
+    pdl_launch_dependents();  // the choosing grid may take its place; it waits for this one before it reads scores
 
     int64_t total = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -838,6 +841,7 @@ __global__ void __launch_bounds__(NT) choose_blocks_kernel(const SelectParams p)
         q1 = fmaxf(q1, x);
     }
     pdl_wait_primary();  // the scores
+    pdl_launch_dependents();
     if (nb <= kKeep) choose<H, NT, true>(s, keep, p, b, kvh, nb, q1);
     else choose<H, NT, false>(s, keep, p, b, kvh, nb, q1);
 }
@@ -858,8 +862,7 @@ static cudaError_t launch_select_t(const SelectParams &p, int sms, cudaStream_t 
     }
     const int64_t most = ((int64_t)p.B * p.K * p.tiles + kScoreWarps - 1) / kScoreWarps;  // a tile per warp
     const unsigned grid = (unsigned)(most < sms ? most : sms);
-    score_blocks_kernel<H><<<grid, kScoreThreads, smem, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_kernel(score_blocks_kernel<H>, dim3(grid), dim3(kScoreThreads), smem, stream, true, p);
     if (e != cudaSuccess) return e;
     static_assert(sizeof(SelectShared) + sizeof(uint32_t) * kKeep <= 48 * 1024, "no opt-in to larger shared memory");
     const size_t keep = sizeof(uint32_t) * (size_t)(p.max_nb < kKeep ? p.max_nb : kKeep);

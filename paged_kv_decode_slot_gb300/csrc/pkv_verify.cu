@@ -23,6 +23,7 @@
 // around one pass over 55 MB in about 8 us.  With a scan over the block for every step of the last CTA's search they took
 // 8.2 and 18.2 us.
 #include "pkv_device.cuh"
+#include "pkv_internal.h"
 #include "pkv_ops.h"
 
 namespace pkv {
@@ -313,6 +314,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     __shared__ long long warp_sums[kVerifyWarps];
     __shared__ int found, last_one;
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    pdl_wait_primary();
+    pdl_launch_dependents();
     VerifyRow<T> row = decide<T>(p, b, c == 0 && tid < 32);
     // what the last CTA needs besides the sums: loaded before it is known to be the last
     const float sample = p.sample_u[b];
@@ -369,9 +372,7 @@ cudaError_t launch_verify(VerifyParams p, bool bf16, int sms, cudaStream_t strea
     p.run = (per + kVerifyRun - 1) / kVerifyRun * kVerifyRun;
     const int runs = (p.V + p.run - 1) / p.run;
     const dim3 grid((runs + kVerifyWarps - 1) / kVerifyWarps, p.B);
-    if (bf16) verify_kernel<uint16_t><<<grid, kVerifyThreads, 0, stream>>>(p);
-    else verify_kernel<float><<<grid, kVerifyThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_kernel(bf16 ? verify_kernel<uint16_t> : verify_kernel<float>, grid, dim3(kVerifyThreads), 0, stream, true, p);
 }
 
 }  // namespace pkv

@@ -160,6 +160,59 @@ def test_calls_made_by_the_extension_and_from_python_are_alike(pkv, kv, monkeypa
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_launches_behind_copies_other_streams_and_each_other(pkv, kv):
+    """The launches start early behind whatever is ahead of them and wait for it: new inputs written by copies (from the host
+    too), by kernels and on another stream just before a step, eager and captured, many steps without a pause."""
+    from paged_kv_decode_slot_gb300.step import SparseDecodeStep
+    steps, M, ctx0 = 24, 6, [200, 90, 17]
+    r = np.random.default_rng(5)
+    news = [[R.to_bf16(r.standard_normal((len(ctx0), h, H))) for h in (N, K, K)] for _ in range(steps)]
+    pinned = [[bf16_dev(x).cpu().pin_memory() for x in new] for new in news]
+    outs = []
+    for mode in ("one by one", "behind each other", "captured"):
+        s = Serving(pkv, 4, ctx0, steps + 1, kv)
+        q, k, v = (torch.zeros(s.B, h, H, dtype=torch.bfloat16, device="cuda") for h in (N, K, K))
+        lens = i32_dev(s.lens)
+        kept = torch.zeros(steps, s.B, N, H, dtype=torch.bfloat16, device="cuda")
+        scales = dict(k_scale=s.scales[0], v_scale=s.scales[1]) if s.scales else {}
+        step = SparseDecodeStep(q, k, v, s.kc, s.vc, s.bounds, s.tables, lens, 0.1, s.inv, M, err_flag=s.err, **scales)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+
+        def one(i):
+            here = torch.cuda.current_stream()
+            side.wait_stream(here)
+            q.copy_(pinned[i][0], non_blocking=True)           # a copy right ahead of the first launch
+            with torch.cuda.stream(side):
+                k.copy_(pinned[i][1], non_blocking=True)
+                v.copy_(pinned[i][2], non_blocking=True)
+            lens.add_(1)
+            here.wait_stream(side)                             # ahead of it: two streams
+            step.run()
+            kept[i].copy_(step.out)
+
+        if mode == "captured":
+            g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.graph(g, stream=st):
+                for i in range(steps):
+                    one(i)
+            assert int(lens[0]) == ctx0[0]
+            g.replay()
+        else:
+            for i in range(steps):
+                one(i)
+                if mode == "one by one":
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert pkv.pkv_read_err_flag(s.err) == (pkv.PKV_OK, 0)
+        outs.append((kept.clone(), s.kc.clone(), s.bounds.clone()))
+    for other in outs[1:]:
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs[0], other))
+    assert all(bool((outs[0][0][i] != outs[0][0][i + 1]).any()) for i in range(steps - 1))
+
+
 def test_speculative_steps_over_one_cache(pkv):
     """T drafted tokens and the one before them: rotating append, multi-token attention, verification against the target's
     probabilities, and the next step from the context that remains -- refused tokens' slots are written over."""
