@@ -10,12 +10,15 @@
 //    producer leaves that number with the stage (0 for an entry to skip);
 //  * the running sum takes the 32-bit weights, so lse does not carry the rounding of the 16-bit weights that
 //    the product P V takes.
-// One CTA per (KV head, sequence, partition of the list); the last partition of a unit to finish merges.
+// One CTA per (KV head, sequence, partition of the list); a list's partitions are one cluster, which joins their partial
+// results in its shared memory, or (many of them) the last to finish joins them from the workspace.
 // Bound by memory: 32 H bytes of K and as many of V per tile and two bytes an element.
 #include "pkv_attn_common.cuh"
 #include "pkv_ops.h"
 
 namespace pkv {
+
+constexpr int kClusterMost = 16;  // partitions of a list that are one cluster, at most (beyond 8 by the device's leave)
 
 // One 16-token tile (the first `valid` tokens count) folded into a warp's state, bf16.
 template <int H>
@@ -91,7 +94,23 @@ __device__ __forceinline__ void block_update(WarpAcc<H> &a, const uint32_t (&qf)
 // kFp8: e4m3 pools (H = 128).  Scales come per tile in both granularities (the producer fetches them with the
 // block id): the K scale multiplies the tile's logits, the V scale its weights relative to the largest seen
 // (VScaleRef, pkv_attn_common.cuh).
-template <int H, bool kFp8, int W>
+// Another CTA's shared memory (the address of the same place in this one's, and its rank in the cluster).
+__device__ __forceinline__ float load_cluster(uint32_t at, int rank)
+{
+    uint32_t there;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int H, bool kFp8, int W, bool kCluster>
 __global__ void __launch_bounds__((W + kProducers) * 32, W > 4 ? 2 : PKV_CTAS_PER_SM)
 attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const BlocksParams p)
@@ -272,13 +291,15 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (aborted) {
         if (pw >= 0 && lane == 0) drain_ring<S, P>(bar_full, pw, issued_count[pw]);
         __syncthreads();
-        if (nparts <= 1) return;  // the unit's other partitions still count on this one: a void partial
+        if (nparts <= 1) return;  // the list's other partitions still count on this one: a void partial
     }
 
     // ------------------------- merge the consumer warps' states -------------------------
     float *mo = reinterpret_cast<float *>(base);
     float *mm = mo + W * 8 * H;
     float *ml = mm + W * 8;
+    float *mine = ml + W * 8;  // kCluster: this partition's [G][H], lse [8]
+    static_assert((W * 8 * (H + 2) + 8 * (H + 1)) * 4 <= L::kPipeBytes, "the drained ring holds the states and the partial");
     if (!aborted) {
         if (warp < W) {
             if constexpr (kFp8) acc_scale_o<H>(acc, vr.v);
@@ -291,7 +312,10 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         float val = __int_as_float(0x7FC00000), lse = __int_as_float(0x7FC00000);  // NaN: void
         if (!aborted) combine<H, W>(mo, mm, ml, g, h, val, lse);
         const size_t bn = bn0 + g;
-        if (nparts > 1) {
+        if (kCluster && nparts > 1) {
+            mine[idx] = val;
+            if (h == 0) mine[8 * H + g] = lse;
+        } else if (nparts > 1) {
             p.part_out[(bn * p.max_parts + part) * H + h] = val;
             if (h == 0) p.part_lse[bn * p.max_parts + part] = lse;
         } else {
@@ -300,6 +324,40 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
     }
     if (nparts <= 1) return;
+    if constexpr (kCluster) {
+        // the list's partitions are one cluster: each reads all partials where they are and writes its part of the rows
+        cluster_sync();
+        const uint32_t at = smem_u32(mine);
+        for (int idx = part * kThreads + threadIdx.x; idx < G * H; idx += nparts * kThreads) {
+            const int g = idx / H;
+            float lse[kClusterMost], v[kClusterMost], M = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < kClusterMost; ++q) {
+                if (q >= nparts) break;
+                lse[q] = load_cluster(at + (8 * H + g) * 4, q);
+                v[q] = load_cluster(at + idx * 4, q);
+            }
+            bool none = true;  // no keys at all
+#pragma unroll
+            for (int q = 0; q < kClusterMost; ++q) {
+                if (q >= nparts) break;
+                M = fmaxf(M, lse[q]);
+                none &= lse[q] == -INFINITY;
+            }
+            float sum = 0.f, val = 0.f;
+#pragma unroll
+            for (int q = 0; q < kClusterMost; ++q) {
+                if (q >= nparts) break;
+                const float w = none ? 0.f : expf(lse[q] - M);  // (a void partial's NaN stays)
+                sum += w;
+                val += w * v[q];
+            }
+            p.out[bn0 * H + idx] = __float2bfloat16_rn(none ? 0.f : val / sum);
+            if (idx == g * H && p.lse_out) p.lse_out[bn0 + g] = none ? -INFINITY : M + logf(sum);
+        }
+        cluster_sync();  // no partition leaves before all have been read
+        return;
+    }
 
     // ----------------- log-sum-exp merge by the unit's last partition -----------------
     __shared__ int last_one;
@@ -325,7 +383,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (threadIdx.x == 0) *count = 0;  // ready for the next call
 }
 
-template <int H, bool kFp8, int W>
+template <int H, bool kFp8, int W, bool kCluster>
 static cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, cudaStream_t stream)
 {
     constexpr int S = kFp8 ? kStagesFp8 : (W > 4 ? 2 * kStages : kStages);
@@ -336,12 +394,25 @@ static cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8, W, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (kCluster) e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8, W, kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         ready[dev] = 1;
     }
-    return launch_kernel(attn_blocks_kernel<H, kFp8, W>, dim3(p.K, p.B, p.max_parts), dim3((W + kProducers) * 32), smem, stream, true,
-                         tk, tv, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.K, p.B, p.max_parts);
+    cfg.blockDim = dim3((W + kProducers) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {1, 1, (unsigned)p.max_parts};
+    cfg.attrs = attr;
+    cfg.numAttrs = kCluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, attn_blocks_kernel<H, kFp8, W, kCluster>, tk, tv, p);
 }
 
 cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, int sms,
@@ -352,9 +423,19 @@ cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUt
     // while there is one list per SM at most (16 * 8 lists of 128: 30.4 -> 25.9; 64 * 8 lists: 85.4 and 86.0).  CTAs of
     // a cut list are short and many: four warps (2 * 160 e4m3 parts of 125 blocks 46.3, with eight 52.4).
     const bool wide = p.max_parts == 1 && (fp8 || (int64_t)p.B * p.K <= sms);
-    if (fp8) return wide ? launch_t<128, true, 8>(tk, tv, p, stream) : launch_t<128, true, 4>(tk, tv, p, stream);
-    if (H == 128) return wide ? launch_t<128, false, 8>(tk, tv, p, stream) : launch_t<128, false, 4>(tk, tv, p, stream);
-    return wide ? launch_t<64, false, 8>(tk, tv, p, stream) : launch_t<64, false, 4>(tk, tv, p, stream);
+    // A list's partitions as one cluster, which joins their partials in shared memory, where they all run at once (8 lists of
+    // 128 in 16-block partitions 6.3 us, through the workspace 8.5; 64 lists of 250 in 42-block ones 25.7) or are two (512
+    // lists of 128 84.3 and 86.6); larger clusters start late in a grid of several waves (512 lists in 16-block ones 108, not
+    // as clusters 96).
+    const bool cluster = p.max_parts > 1 && p.max_parts <= kClusterMost &&
+                         (p.max_parts == 2 || (int64_t)p.B * p.K * p.max_parts <= (int64_t)PKV_CTAS_PER_SM * sms);
+    if (cluster) {
+        if (fp8) return launch_t<128, true, 4, true>(tk, tv, p, stream);
+        return H == 128 ? launch_t<128, false, 4, true>(tk, tv, p, stream) : launch_t<64, false, 4, true>(tk, tv, p, stream);
+    }
+    if (fp8) return wide ? launch_t<128, true, 8, false>(tk, tv, p, stream) : launch_t<128, true, 4, false>(tk, tv, p, stream);
+    if (H == 128) return wide ? launch_t<128, false, 8, false>(tk, tv, p, stream) : launch_t<128, false, 4, false>(tk, tv, p, stream);
+    return wide ? launch_t<64, false, 8, false>(tk, tv, p, stream) : launch_t<64, false, 4, false>(tk, tv, p, stream);
 }
 
 }  // namespace pkv

@@ -122,15 +122,23 @@ def plan_attention(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int, nu
 
 def plan_blocks_attention(num_seqs: int, num_kv_heads: int, max_selected: int, num_sms: int) -> AttentionPlan:
     """Partitions of the selected-block lists for pkv_decode_attn_blocks.  Measured on GB300, us:
-      * (sequence, KV head) lists for more than half the SMs: one CTA a list (128 lists of 128 blocks
-        25.9, in 64-block partitions 28.1; of 250 blocks 44.5 and 46.9), up to 128 blocks a list where
-        there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 305, whole 344);
-      * fewer lists: partitions as ``plan_attention`` sizes them, about 512 CTAs of at least 8 blocks
-        (8 lists of 128: 8.3, whole 14.5)."""
+      * (sequence, KV head) lists that leave room for four partitions or more each in one wave of three CTAs
+        per SM: as many as fit, up to 12 (16 for lists beyond 256 blocks) and of 4 blocks at least; they merge
+        inside a cluster (8 lists of 128: 6.0, whole 13.1; 64 lists of 250: 25.7, whole 32.4; 96 of 250: 35.2
+        and 36.7; 8 of 1,024: 18.8);
+      * a handful of very long lists: partitions as ``plan_attention`` sizes them, which merge through the
+        workspace (2 lists of 1,024 blocks: 11.8, as clusters of 16 13.0);
+      * more lists: one CTA a list (128 lists of 128 blocks 25.1, in halves 26.3), up to 128 blocks a list
+        where there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 305, whole 344)."""
     units = num_seqs * num_kv_heads
-    if max_selected <= 8 or (num_sms < 2 * units and (units < num_sms or max_selected <= LONG_PARTITION_BLOCKS)):
+    room = 3 * num_sms // units if units > 0 else 0
+    if max_selected <= 8 or (room < 4 and (units < num_sms or max_selected <= LONG_PARTITION_BLOCKS)):
         return AttentionPlan("single", 0, 1)
-    return plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False)
+    if room < 4 or (units < 8 and max_selected > 512):
+        return plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False)
+    most = min(room, 12 if max_selected <= 256 else 16)
+    partition_blocks = max(4, -(-max_selected // most))
+    return AttentionPlan("split", partition_blocks, B.max_partitions_for(max_selected, partition_blocks))
 
 
 class DecodeStep:

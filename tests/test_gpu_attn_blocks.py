@@ -177,6 +177,26 @@ def test_entries_out_of_range_twice_and_behind_the_blocks(pkv, pb):
     assert np.all(out_f64(out) == 0) and bool(torch.isneginf(lse).all())
 
 
+@pytest.mark.parametrize("kv,N,K,H", [("bf16", 8, 1, 128), ("bf16", 6, 3, 64), ("e4m3_block", 8, 2, 128)])
+@pytest.mark.parametrize("parts", [2, 3, 8, 9, 15, 16, 17, 40])
+def test_partitions_that_merge_in_clusters_and_through_the_workspace(pkv, kv, N, K, H, parts):
+    """Lists in two to sixteen partitions (a cluster each) and more, lists that end in any of them, some without a key."""
+    M = 3 * parts - 1
+    c = Case(parts + N, [16 * n for n in range(0, M + 4, max(1, M // 7))] + [16 * M - 3, 1, 17], N, K, H, kv)
+    sel = c.lists(M, holes=True)
+    sel[0], sel[-3, :, :3], sel[-3, :, 6:9] = -1, -1, -1
+    c.poison(sel)
+    c.check(*c.run(pkv, sel, 3), sel, f"{parts} partitions")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3_head"])
+@pytest.mark.parametrize("parts", [1, 2, 3, 5])
+def test_more_partitions_than_run_at_once(pkv, kv, parts):
+    c = Case(21 + parts, [int(x) for x in np.random.default_rng(parts).integers(0, 16 * 11, 90)], 8, 8, 128, kv)
+    sel = c.lists(10)
+    c.check(*c.run(pkv, sel, -(-10 // parts)), sel, f"{parts} partitions of {90 * 8} lists")
+
+
 @pytest.mark.parametrize("pb", [0, 3])
 def test_nothing_selected(pkv, pb):
     c = Case(14, [100, 3, 0], 4, 2, 64)
