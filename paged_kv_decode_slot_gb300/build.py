@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["pkv_api.cu", "pkv_attn.cu", "pkv_attn_cols.cu", "pkv_attn_tc.cu", "pkv_cache_ops.cu",
            "pkv_rope.cu", "pkv_select.cu", "pkv_attn_blocks.cu", "pkv_verify.cu"]
 HEADERS = ["pkv_device.cuh", "pkv_internal.h", "pkv_attn_common.cuh", "pkv_cols.cuh", "pkv_tcgen05.cuh",
-           "pkv_ops.h"]
+           "pkv_cluster.cuh", "pkv_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

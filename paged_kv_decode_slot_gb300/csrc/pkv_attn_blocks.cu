@@ -14,6 +14,7 @@
 // results in its shared memory, or (many of them) the last to finish joins them from the workspace.
 // Bound by memory: 32 H bytes of K and as many of V per tile and two bytes an element.
 #include "pkv_attn_common.cuh"
+#include "pkv_cluster.cuh"
 #include "pkv_ops.h"
 
 namespace pkv {
@@ -94,22 +95,6 @@ __device__ __forceinline__ void block_update(WarpAcc<H> &a, const uint32_t (&qf)
 // kFp8: e4m3 pools (H = 128).  Scales come per tile in both granularities (the producer fetches them with the
 // block id): the K scale multiplies the tile's logits, the V scale its weights relative to the largest seen
 // (VScaleRef, pkv_attn_common.cuh).
-// Another CTA's shared memory (the address of the same place in this one's, and its rank in the cluster).
-__device__ __forceinline__ float load_cluster(uint32_t at, int rank)
-{
-    uint32_t there;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 template <int H, bool kFp8, int W, bool kCluster>
 __global__ void __launch_bounds__((W + kProducers) * 32, W > 4 ? 2 : PKV_CTAS_PER_SM)
 attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -334,8 +319,8 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
             for (int q = 0; q < kClusterMost; ++q) {
                 if (q >= nparts) break;
-                lse[q] = load_cluster(at + (8 * H + g) * 4, q);
-                v[q] = load_cluster(at + idx * 4, q);
+                lse[q] = load_cluster<float>(at + (8 * H + g) * 4, q);
+                v[q] = load_cluster<float>(at + idx * 4, q);
             }
             bool none = true;  // no keys at all
 #pragma unroll
@@ -396,23 +381,12 @@ static cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const 
     if (!ready[dev]) {
         e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8, W, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        if (kCluster) e = cudaFuncSetAttribute(attn_blocks_kernel<H, kFp8, W, kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (kCluster) e = allow_wide_clusters(attn_blocks_kernel<H, kFp8, W, kCluster>);
         if (e != cudaSuccess) return e;
         ready[dev] = 1;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.K, p.B, p.max_parts);
-    cfg.blockDim = dim3((W + kProducers) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {1, 1, (unsigned)p.max_parts};
-    cfg.attrs = attr;
-    cfg.numAttrs = kCluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_blocks_kernel<H, kFp8, W, kCluster>, tk, tv, p);
+    return launch_clusters(attn_blocks_kernel<H, kFp8, W, kCluster>, dim3(p.K, p.B, p.max_parts), dim3((W + kProducers) * 32),
+                           dim3(1, 1, kCluster ? p.max_parts : 1), smem, stream, tk, tv, p);
 }
 
 cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv, const BlocksParams &p, int sms,

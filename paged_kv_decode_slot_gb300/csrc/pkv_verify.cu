@@ -13,15 +13,16 @@
 // weight is off by little more than 2^-45.
 //
 // Bound by memory: one row of p, and where a token was refused one row of q.  A row is cut into one run of entries
-// per warp, runs of at least 256 entries and as many as keep about four CTAs per SM over the whole batch, but no more
-// than 1,024 (their sums then go through shared memory in one step); the last CTA of a sequence to finish adds the runs'
-// sums up, finds the run that the draw falls into and the entry in it.  The acceptance is decided by every CTA for
-// itself: a few loads against a second launch.
+// per warp, runs of at least 256 entries; the acceptance is decided by every CTA for itself (a few loads against a second
+// launch).  A few sequences take one cluster each, whose first CTA reads the runs' sums in the others' shared memory; many
+// take as many CTAs as are about four per SM over the whole batch (1,024 runs a row at most), and the last CTA of a
+// sequence to finish takes the sums from the workspace.  It adds them up, finds the run that the draw falls into and the
+// entry in it.
 //
-// Measured: one sequence (three drafted tokens, 32,000 bf16 entries) 6.5 us, a chain of dependent loads (length, token,
-// probability, row, count, sums, entry); 64 sequences (four drafted tokens, 128,256 fp32 entries) 15.9 us, that chain
-// around one pass over 55 MB in about 8 us.  With a scan over the block for every step of the last CTA's search they took
-// 8.2 and 18.2 us.
+// Measured: one sequence (three drafted tokens, 32,000 bf16 entries) 5.7 us, a chain of dependent loads (length, token,
+// probability, row, sums, entry); 64 sequences (four drafted tokens, 128,256 fp32 entries) 15.4 us, that chain around one
+// pass over 55 MB in about 8 us.
+#include "pkv_cluster.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_ops.h"
@@ -31,6 +32,8 @@ namespace pkv {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyRuns = 1024;  // runs of a row at most
+constexpr int kClusterCtas = 16;   // of a cluster at most
+constexpr int kClusterShare = 16384;  // entries of one of its CTAs at most
 
 __device__ __forceinline__ float prob_at(const float *row, int64_t i) { return __ldg(row + i); }
 __device__ __forceinline__ float prob_at(const uint16_t *row, int64_t i) { return bf16_to_f32(__ldg(row + i)); }
@@ -307,10 +310,11 @@ __device__ __forceinline__ int draw(const VerifyRow<T> &row, const VerifyParams 
     return -1;
 }
 
-template <typename T>
+template <typename T, bool kCluster>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p)
 {
-    __shared__ long long all_sums[kVerifyRuns];
+    __shared__ long long all_sums[kCluster ? kClusterCtas * kVerifyWarps : kVerifyRuns];
+    __shared__ long long my_sums[kVerifyWarps];
     __shared__ long long warp_sums[kVerifyWarps];
     __shared__ int found, last_one;
     const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
@@ -323,16 +327,26 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const int runs = (p.V + p.run - 1) / p.run;
     long long *sums = p.sums + (int64_t)b * runs;
     const int r = c * kVerifyWarps + (tid >> 5);  // this warp's run
-    if (r < runs) {
-        const long long mine = run_sum(row, (int64_t)r * p.run, min((int64_t)p.V, (int64_t)(r + 1) * p.run));
-        if ((tid & 31) == 0) sums[r] = mine;
+    long long mine = 0;
+    if (r < runs) mine = run_sum(row, (int64_t)r * p.run, min((int64_t)p.V, (int64_t)(r + 1) * p.run));
+    if constexpr (kCluster) {
+        // a sequence's CTAs are one cluster: the first draws, and reads the others' sums where they are
+        if ((tid & 31) == 0) my_sums[tid >> 5] = mine;
+        cluster_sync();
+        if (c == 0 && tid < runs) all_sums[tid] = load_cluster<long long>(smem_u32(my_sums + tid % kVerifyWarps), tid / kVerifyWarps);
+        cluster_arrive();  // the others may leave
+        if (c != 0) {
+            cluster_wait();
+            return;
+        }
+    } else {
+        if ((tid & 31) == 0 && r < runs) sums[r] = mine;
+        __syncthreads();
+        if (tid == 0) last_one = atomic_add_acq_rel_gpu(p.counters + b, 1) == (int)gridDim.x - 1;
+        __syncthreads();
+        if (!last_one) return;
+        for (int x = tid; x < runs; x += kVerifyThreads) all_sums[x] = __ldcg(sums + x);
     }
-    __syncthreads();
-    if (tid == 0) last_one = atomic_add_acq_rel_gpu(p.counters + b, 1) == (int)gridDim.x - 1;
-    __syncthreads();
-    if (!last_one) return;
-
-    for (int x = tid; x < runs; x += kVerifyThreads) all_sums[x] = __ldcg(sums + x);
     __syncthreads();
     int token = draw(row, p, runs, sample, all_sums, warp_sums, &found);
     if (token < 0 && (row.q || row.hot >= 0)) {
@@ -357,7 +371,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     if (tid == 0) {
         p.accepted[b] = n;
         if (p.context_lens) p.context_lens_out[b] = ctx - row.len + n;
-        p.counters[b] = 0;  // ready for the next call
+        if constexpr (!kCluster) p.counters[b] = 0;  // ready for the next call
+    }
+    if constexpr (kCluster) {
+        __syncwarp();
+        cluster_wait();
     }
 }
 
@@ -368,11 +386,32 @@ cudaError_t launch_verify(VerifyParams p, bool bf16, int sms, cudaStream_t strea
     const int want = (4 * sms + p.B - 1) / p.B;
     int ctas = want < most ? want : most;
     if (ctas > kVerifyRuns / kVerifyWarps) ctas = kVerifyRuns / kVerifyWarps;
+    // A cluster per sequence where that is one CTA per SM at most and 16,384 entries a CTA: 1 sequence of 128,256 entries 5.8 us,
+    // through the workspace (63 CTAs) 7.5; 4: 6.2 and 9.4; 16: 8.7 and 9.5; 64 of 32,000: 7.9 and 9.4; but 32 of 128,256, 4
+    // CTAs each, 15.9 and 11.2, and clusters in a grid of several CTAs per SM start late: 64 of 128,256 20.9 and 15.4.
+    const int cap = sms / p.B < kClusterCtas ? sms / p.B : kClusterCtas;
+    const bool clusters = cap > 0 && (p.V + cap - 1) / cap <= kClusterShare;
+    if (clusters && ctas > cap) ctas = cap;
     const int per = (p.V + ctas * kVerifyWarps - 1) / (ctas * kVerifyWarps);
     p.run = (per + kVerifyRun - 1) / kVerifyRun * kVerifyRun;
     const int runs = (p.V + p.run - 1) / p.run;
-    const dim3 grid((runs + kVerifyWarps - 1) / kVerifyWarps, p.B);
-    return launch_kernel(bf16 ? verify_kernel<uint16_t> : verify_kernel<float>, grid, dim3(kVerifyThreads), 0, stream, true, p);
+    const dim3 grid((runs + kVerifyWarps - 1) / kVerifyWarps, p.B), one(1, 1, 1);
+    if (clusters || grid.x == 1) {
+        static bool ready[64] = {};  // per device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (!ready[dev]) {
+            e = allow_wide_clusters(verify_kernel<uint16_t, true>);
+            if (e == cudaSuccess) e = allow_wide_clusters(verify_kernel<float, true>);
+            if (e != cudaSuccess) return e;
+            ready[dev] = true;
+        }
+        return launch_clusters(bf16 ? verify_kernel<uint16_t, true> : verify_kernel<float, true>, grid, dim3(kVerifyThreads),
+                               dim3(grid.x, 1, 1), 0, stream, p);
+    }
+    return launch_clusters(bf16 ? verify_kernel<uint16_t, false> : verify_kernel<float, false>, grid, dim3(kVerifyThreads), one, 0, stream, p);
 }
 
 }  // namespace pkv

@@ -247,3 +247,29 @@ def test_repeats_on_one_workspace_another_stream_and_in_a_graph(pkv):
         assert np.array_equal(a[0], acc.cpu().numpy()) and np.array_equal(a[1], out.cpu().numpy())
     e = torch.empty(0, dtype=torch.int32, device="cuda")
     assert pkv.pkv_verify_draft(p[:0], q[:0], args[0][:0], args[1][:0], args[2][:0], e, out[:0], ws) == pkv.PKV_OK
+
+
+def test_a_batch_that_shrinks_between_clusters_and_the_workspace(pkv):
+    """Forty long rows share out through the workspace, a few of them in clusters: calls in turn on one workspace, repeated
+    and captured, give the same tokens and leave the counters at zero."""
+    B, T, V = 40, 1, 70001
+    p, q, tok, r = draw(31, B, T, V, torch.float32)
+    u, s = r.random((B, T)).astype(np.float32), r.random(B).astype(np.float32)
+    want = R.verify(p.double().cpu().numpy(), q.double().cpu().numpy(), tok, u, s)
+    ws = torch.zeros(pkv.pkv_verify_workspace_bytes(B, V), dtype=torch.uint8, device="cuda")
+    for n in (40, 3, 40, 1, 9, 39, 40):
+        acc, out, _ = run(pkv, p[:n], q[:n], tok[:n], u[:n], s[:n], ws=ws)
+        assert np.array_equal(acc, want[0][:n]) and np.array_equal(out, want[1][:n])
+        assert int(ws[-4 * B:].view(torch.int32).abs().sum()) == 0, "the counters are not back at zero"
+    args = (dev(tok, torch.int32), dev(u, torch.float32), dev(s, torch.float32))
+    acc, out = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, T + 1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            pkv.check(pkv.pkv_verify_draft(p, q, *args, acc, out, ws))
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(acc.cpu().numpy(), want[0]) and np.array_equal(out.cpu().numpy(), want[1])
