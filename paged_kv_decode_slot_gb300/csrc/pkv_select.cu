@@ -334,37 +334,108 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
     return lo;
 }
 
-// The sum over h of max(q lo, q hi) in 64 bits, the largest over the group's heads (in 32 bits products of bf16
-// numbers may over- or underflow; here they are exact), by one warp: every lane's order and the shuffles' are the same for
-// every block, so equal blocks get equal sums.
-template <int H>
+// The sum over h of max(q lo, q hi), the largest over the group's heads, by one warp: `best` holds the heads' sums so far.
+// In 64-bit floating point (in 32 bits products of bf16 numbers may over- or underflow; here they are exact).  The order of
+// the sum is the same for every block, so equal blocks get equal sums.
+template <int E>
+__device__ __forceinline__ double head_sum(const float (&x)[E], const float (&lo)[E], const float (&hi)[E])
+{
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum += (double)x[e] * (double)(x[e] > 0.f ? hi[e] : lo[e]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+    return sum;
+}
+
+// The score of block j, exact but for one rounding to 64 bits.  fp64 units are few on this chip (a block's products took
+// 3 us through them), so the products, scaled below 1 by powers of two, are added up as integers: adding 3 rounds a number
+// below 1 to a multiple of 2^-22 in the sum's bits, the rest goes the same way at 2^-44 and 2^-66.  A product has 16 bits,
+// so what is lost is below 2^-66 of the largest possible one.  kHold: the queries are held in registers and on their way
+// while the block is looked up (1.2 us less for a CTA that has registers to spare).
+template <int H, bool kHold>
 __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int kvh, int j, int lane)
 {
     constexpr int E = H / 32;  // neighbouring elements of a lane
+    constexpr float kA = 3.f, kB = 3.f / (1 << 22), kC = kB / (1 << 22);
     const double kInf = __longlong_as_double(0x7FF0000000000000ll);
     const int blk = __ldg(p.block_tables + (size_t)b * p.max_nb + j);
+    const uint16_t *q = p.q + ((size_t)b * p.N + (size_t)kvh * p.G) * H + lane * E;
+    uint16_t held[kHold ? 8 : 1][E];
+    unsigned top_b = 0, top_q = 0;
+    if constexpr (kHold) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                held[g][e] = g < p.G ? q[g * H + e] : 0;
+                top_q = max(top_q, held[g][e] & 0x7FFFu);
+            }
+    }
     if (blk < 0 || blk >= p.num_blocks) return -kInf;
     const uint16_t *row = p.bounds + ((int64_t)blk * p.K + kvh) * 2 * H + lane * E;
-    const uint16_t *q = p.q + ((size_t)b * p.N + (size_t)kvh * p.G) * H + lane * E;
     float lo[E], hi[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) lo[e] = bf16_to_f32(row[e]), hi[e] = bf16_to_f32(row[H + e]);
+    for (int e = 0; e < E; ++e) {
+        const unsigned l = row[e], h = row[H + e];
+        lo[e] = bf16_to_f32((uint16_t)l), hi[e] = bf16_to_f32((uint16_t)h);
+        top_b = max(top_b, max(l & 0x7FFFu, h & 0x7FFFu));
+    }
+    if constexpr (!kHold) {
+#pragma unroll 4
+        for (int g = 0; g < p.G; ++g)
+#pragma unroll
+            for (int e = 0; e < E; ++e) top_q = max(top_q, q[g * H + e] & 0x7FFFu);
+    }
+    const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, top_b) >> 7), eq = (int)(__reduce_max_sync(0xFFFFFFFFu, top_q) >> 7);
     double best = -kInf;
     bool nan = false;
-#pragma unroll 4
-    for (int g = 0; g < p.G; ++g) {
-        double sum = 0.0;
+    if (eb >= 253 || eq >= 253) {  // infinities, NaN and numbers whose scale is out of range
+#pragma unroll 1
+        for (int g = 0; g < p.G; ++g) {
+            float y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = bf16_to_f32(q[g * H + e]);
+            const double sum = head_sum<E>(y, lo, hi);
+            nan |= sum != sum;
+            best = sum > best ? sum : best;
+        }
+        return nan ? __longlong_as_double(0x7FF8000000000000ll) : best;
+    }
+    const float fb = __uint_as_float((unsigned)(253 - eb) << 23), fq = __uint_as_float((unsigned)(253 - eq) << 23);
+#pragma unroll
+    for (int e = 0; e < E; ++e) lo[e] *= fb, hi[e] *= fb;
+    unsigned mine[3] = {0, 0, 0};  // lane g keeps head g's sums
+#pragma unroll(kHold ? 8 : 2)
+    for (int g = 0; g < (kHold ? 8 : p.G); ++g) {
+        if (g >= p.G) break;
+        unsigned a = 0, s1 = 0, s2 = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float x = bf16_to_f32(q[g * H + e]);
-            sum += (double)x * (double)(x > 0.f ? hi[e] : lo[e]);
+            const float x = bf16_to_f32(kHold ? held[kHold ? g : 0][e] : q[g * H + e]), y = (x * fq) * (x > 0.f ? hi[e] : lo[e]);
+            const float t = __fadd_rn(y, kA), r = __fsub_rn(y, __fsub_rn(t, kA));
+            const float t1 = __fadd_rn(r, kB), r1 = __fsub_rn(r, __fsub_rn(t1, kB));
+            a += __float_as_uint(t);
+            s1 += __float_as_uint(t1);
+            s2 += __float_as_uint(__fadd_rn(r1, kC));
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-        nan |= sum != sum;
-        best = sum > best ? sum : best;
+        a = __reduce_add_sync(0xFFFFFFFFu, a);
+        s1 = __reduce_add_sync(0xFFFFFFFFu, s1);
+        s2 = __reduce_add_sync(0xFFFFFFFFu, s2);
+        if (lane == g) mine[0] = a, mine[1] = s1, mine[2] = s2;
     }
-    return nan ? __longlong_as_double(0x7FF8000000000000ll) : best;
+    // the constants' bits off again: counts of 2^-22, 2^-44 and 2^-66
+    const int ua = (int)(mine[0] - H * __float_as_uint(kA)), ub = (int)(mine[1] - H * __float_as_uint(kB)),
+              uc = (int)(mine[2] - H * __float_as_uint(kC));
+    const double unit = __longlong_as_double((long long)(1023 + eb + eq - 252 - 44) << 52);  // 2^-44 of the scales' product
+    double sum = fma((double)uc, unit * 0x1p-22, (double)(((long long)ua << 22) + ub) * unit);
+    if (lane >= p.G) sum = -kInf;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) {
+        const double o = __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+        sum = o > sum ? o : sum;
+    }
+    return __shfl_sync(0xFFFFFFFFu, sum, 0);
 }
 
 // A warp's contiguous run of the blocks [0, nb): the runs in warp order are the blocks in ascending order.
@@ -519,7 +590,7 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     __syncthreads();
     double *exact = m <= kRankMost ? s.exact : p.exact + unit * p.max_nb;
     for (int a = warp; a < m; a += (NT / 32)) {
-        const double x = exact_score<H>(p, b, kvh, list[a], lane);
+        const double x = exact_score<H, (NT > 256)>(p, b, kvh, list[a], lane);
         if (lane == 0) exact[a] = x;
     }
     __syncthreads();
@@ -813,7 +884,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
 }
 
 template <int H, int NT>
-__global__ void __launch_bounds__(NT) choose_blocks_kernel(const SelectParams p)
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 : 4) choose_blocks_kernel(const SelectParams p)
 {
     __shared__ SelectShared s;
     extern __shared__ uint32_t keep[];  // [min(max_nb, kKeep)]

@@ -126,6 +126,21 @@ def test_selection_of_long_contexts(pkv, nb, M):
     check(pkv, q, bounds, tab, ctx, M, 1, 2)
 
 
+@pytest.mark.parametrize("N,H", [(1, 64), (4, 128), (8, 128)])
+@pytest.mark.parametrize("step", [-20, -30, -47, -55])
+def test_scores_that_differ_far_below_32_bits(pkv, N, H, step):
+    """score_j = 1 + k_j 2^step with k a permutation: equal in 32 bits, told apart by the sums that follow."""
+    nb, M = 250, 30
+    r = np.random.default_rng(N - step)
+    tab, pool = R.tables(r, [16 * nb])
+    q, bounds = np.zeros((1, N, H)), np.zeros((pool, 1, 2, H))
+    q[0, :, 3], q[0, :, H - 2] = 1.0, 2.0 ** (step // 2)
+    q[0, :-1, 3] = 0.5                                          # the last head decides
+    bounds[:, :, :, 3] = 1.0
+    bounds[tab[0], 0, :, H - 2] = (r.permutation(nb) * 2.0 ** (step - step // 2))[:, None]
+    check(pkv, R.to_bf16(q), R.to_bf16(bounds), tab, [16 * nb], M, 1, 1)
+
+
 @pytest.mark.parametrize("eq,eb", [(-70, -65), (-60, -60), (-120, -10), (70, 66), (100, 27)])
 def test_scores_that_leave_the_range_of_32_bits(pkv, eq, eb):
     """Products and sums that under- or overflow in 32 bits: the choice is that of the real values all the same."""
