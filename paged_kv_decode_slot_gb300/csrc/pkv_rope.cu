@@ -19,9 +19,10 @@
 // registers and the arithmetic (the e4m3 form's quotients above all) has enough warps; results go straight to global
 // memory.  A token whose slot is negative is left out: nothing of its rows is written.
 //
-// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 34.4 us (5.9 TB/s, 86% of the measured
-// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 53.9 us (4.8 TB/s, 70%): bound by issue
-// slots (72% busy before fp32 operations went in pairs; the quotients are a third of the instructions).
+// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 33.5 us (6.0 TB/s, 88% of the measured
+// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 52.9 us (4.8 TB/s, 71%): bound by issue
+// slots (68% busy; the check of the quotients takes 8 us; 28 of 32 lanes are busy, and an order of the items that puts
+// turned and copied ones into warps of their own took 55.9).  64 decode tokens: 2.8 us, a launch and four dependent loads.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_ops.h"

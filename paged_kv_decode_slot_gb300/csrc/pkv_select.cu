@@ -12,12 +12,14 @@
 // order of its fp32 sums alone.
 //
 // Two launches, the second started early (programmatic serialization): scores into the workspace, then one CTA per
-// (sequence, KV head) chooses.
+// (sequence, KV head) chooses.  64 sequences of 8K to 32K tokens, 8 KV heads, 128 blocks each: 69 us, of which the scores,
+// bound by memory, 57 for 336 MB (5.9 TB/s, 87% of the measured copy bandwidth); one sequence of 32K tokens: 8.5 us, the
+// latency of a tile's loads (3.5) and of the choice's barriers and passes over shared memory (5).
 //
 // Selection.  The first F and the last L blocks, and the best of the rest, M in all, in ascending order:
 // exactly those that the scores' real values choose, ties to the lowest index.  With eps bounding the
 // error of every score, t the k-th largest score: a block above t + 2 eps is in, one below t - 2 eps is out,
-// and if those between do not all fit, their sums are taken again in 64 bits and ranked.
+// and if those between do not all fit, their sums are taken again, as integers (exact_score), and ranked.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_ops.h"
@@ -27,7 +29,8 @@ namespace pkv {
 // ------------------------------------- key bounds -----------------------------------------
 // One CTA per block that holds new tokens, one thread per 16-byte column of its [K][H] rows: all 16 rows are
 // loaded at once (independent loads), rows past the context are left out.  One pass over the keys,
-// bound by memory.
+// bound by memory: 16 prompts of 512 to 8,192 tokens (8 heads of 128, 161 MB) 27.2 us, 5.9 TB/s, 87% of the measured copy
+// bandwidth; the newest block of 64 sequences in e4m3 2.4 us, a launch and two dependent loads.
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)
 {
     const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
@@ -348,8 +351,8 @@ __device__ __forceinline__ double head_sum(const float (&x)[E], const float (&lo
     return sum;
 }
 
-// The score of block j, exact but for one rounding to 64 bits.  fp64 units are few on this chip (a block's products took
-// 3 us through them), so the products, scaled below 1 by powers of two, are added up as integers: adding 3 rounds a number
+// The score of block j, exact but for one rounding to 64 bits.  fp64 units are few on this chip (through them this
+// step took 5 us of a choice, so it takes 1.5), so the products, scaled below 1 by powers of two, are added up as integers: adding 3 rounds a number
 // below 1 to a multiple of 2^-22 in the sum's bits, the rest goes the same way at 2^-44 and 2^-66.  A product has 16 bits,
 // so what is lost is below 2^-66 of the largest possible one.  kHold: the queries are held in registers and on their way
 // while the block is looked up (1.2 us less for a CTA that has registers to spare).
