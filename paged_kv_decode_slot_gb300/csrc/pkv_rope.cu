@@ -77,7 +77,8 @@ __device__ __forceinline__ uint32_t codes(f32x2 v)
 // and made larger, by 2^-21 lie to both sides of that quotient (five roundings of 2^-24 between them): where their codes
 // agree, they are the quotient's too (rounding is monotonic; zeros, infinities and NaN agree with themselves); only
 // where they differ is x divided.  The reciprocal of a scale outside [2^-100, 2^100] may over- or underflow: there
-// every x is divided.  (Correcting one product by its remainder, Markstein's way, measured 57.8 us against 53.9 on 5,001 tokens of 3 * 40 heads.)
+// every x is divided.  (Correcting one product by its remainder, Markstein's way, measured 57.8 us against 53.9 on 5,001
+// tokens of 3 * 40 heads.)
 __device__ __forceinline__ uint2 rope_quantize8(const f32x2 (&x)[4], float sc)
 {
     const float r = __frcp_rn(sc), r0 = r * (1.f - 0x1p-21f), r1 = r * (1.f + 0x1p-21f);
@@ -263,12 +264,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
     constexpr int kRounds = kFp8 ? (kUnitHeads * kPerHead + kRopeThreads - 1) / kRopeThreads : 1;
     float sc[kRounds], sc_next[kRounds];
     auto scales = [&](const Unit &t, int64_t slot, float (&to)[kRounds]) {
-        if (!kFp8 || t.i >= p.n || slot < 0) return;
+        if constexpr (kFp8) {
+            if (t.i >= p.n || slot < 0) return;
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int kvh = t.chunk * per + (tid + r * kRopeThreads) / kPerHead - p.N;
-            if (kvh >= 0 && kvh < 2 * p.K)
-                to[r] = __ldg((kvh < p.K ? p.k_scale + kvh : p.v_scale + kvh - p.K) + (slot / kBlockSize) * p.scale_stride);
+            for (int r = 0; r < kRounds; ++r) {
+                const int kvh = t.chunk * per + (tid + r * kRopeThreads) / kPerHead - p.N;
+                if (kvh >= 0 && kvh < 2 * p.K)
+                    to[r] = __ldg((kvh < p.K ? p.k_scale + kvh : p.v_scale + kvh - p.K) + (slot / kBlockSize) * p.scale_stride);
+            }
         }
     };
     Unit next = now;

@@ -351,11 +351,11 @@ __device__ __forceinline__ double head_sum(const float (&x)[E], const float (&lo
     return sum;
 }
 
-// The score of block j, exact but for one rounding to 64 bits.  fp64 units are few on this chip (through them this
-// step took 5 us of a choice, so it takes 1.5), so the products, scaled below 1 by powers of two, are added up as integers: adding 3 rounds a number
-// below 1 to a multiple of 2^-22 in the sum's bits, the rest goes the same way at 2^-44 and 2^-66.  A product has 16 bits,
-// so what is lost is below 2^-66 of the largest possible one.  kHold: the queries are held in registers and on their way
-// while the block is looked up (1.2 us less for a CTA that has registers to spare).
+// The score of block j, exact but for one rounding to 64 bits.  fp64 units are few on this chip (through them this step took
+// 5 us of a choice, so it takes 1.5), so the products, scaled below 1 by powers of two, are added up as integers: adding 3
+// rounds a number below 1 to a multiple of 2^-22 in the sum's bits, the rest goes the same way at 2^-44 and 2^-66.  A product
+// has 16 bits, so what is lost is below 2^-66 of the largest possible one.  kHold: the queries are held in registers and on
+// their way while the block is looked up (1.2 us less for a CTA that has registers to spare).
 template <int H, bool kHold>
 __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int kvh, int j, int lane)
 {

@@ -18,27 +18,39 @@ namespace {
 
 PyObject *g_refuse = nullptr;  // binding._refuse(t, dtype, shape, name, dev): raises, or accepts pinned host memory
 
-// arg(t, dtype, shape, name, dev) -> the address of a contiguous tensor of this type and shape on CUDA device dev
+// The address of a contiguous tensor of this type and shape on CUDA device dev; null: something is not as asked, or Python's
+// error is set.  Tensors without memory (fake ones) throw.
+void *plain(PyObject *const *a)
+{
+    if (!THPVariable_Check(a[0]) || !THPDtype_Check(a[1]) || !PyTuple_Check(a[2])) return nullptr;
+    const at::Tensor &t = THPVariable_Unpack(a[0]);
+    const long dev = PyLong_AsLong(a[4]);
+    if (dev == -1 && PyErr_Occurred()) return nullptr;
+    const auto sizes = t.sizes();
+    bool same = t.scalar_type() == reinterpret_cast<THPDtype *>(a[1])->scalar_type && t.is_cuda() && t.get_device() == dev &&
+                PyTuple_GET_SIZE(a[2]) == (Py_ssize_t)sizes.size() && t.is_contiguous();
+    for (size_t i = 0; same && i < sizes.size(); ++i) {
+        const long long s = PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], i));
+        if (s == -1 && PyErr_Occurred()) return nullptr;
+        same = s == sizes[i];
+    }
+    return same ? t.data_ptr() : nullptr;
+}
+
+// arg(t, dtype, shape, name, dev) -> that address; what is not as asked goes to the binding
 PyObject *arg(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     if (n != 5) {
         PyErr_SetString(PyExc_TypeError, "arg(t, dtype, shape, name, dev)");
         return nullptr;
     }
-    if (THPVariable_Check(a[0]) && THPDtype_Check(a[1]) && PyTuple_Check(a[2])) {
-        const at::Tensor &t = THPVariable_Unpack(a[0]);
-        const long dev = PyLong_AsLong(a[4]);
-        if (dev == -1 && PyErr_Occurred()) return nullptr;
-        const auto sizes = t.sizes();
-        bool same = t.scalar_type() == reinterpret_cast<THPDtype *>(a[1])->scalar_type && t.is_cuda() &&
-                    t.get_device() == dev && PyTuple_GET_SIZE(a[2]) == (Py_ssize_t)sizes.size() && t.is_contiguous();
-        for (size_t i = 0; same && i < sizes.size(); ++i) {
-            const long long s = PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], i));
-            if (s == -1 && PyErr_Occurred()) return nullptr;
-            same = s == sizes[i];
-        }
-        if (same) return PyLong_FromVoidPtr(t.data_ptr());
+    void *at = nullptr;
+    try {
+        at = plain(a);
+    } catch (...) {  // nothing may pass the interpreter; it meets the same in the binding, and says so
     }
+    if (at) return PyLong_FromVoidPtr(at);
+    if (PyErr_Occurred()) return nullptr;
     if (!g_refuse) {
         PyErr_SetString(PyExc_RuntimeError, "set_refuse was not called");
         return nullptr;
@@ -165,7 +177,9 @@ struct Call {
             ok &= d->v == sizes[i] && (d->v <= INT32_MAX || shape.size() == 1);
             ++i;
         }
-        return static_cast<T *>(t.data_ptr());
+        T *at = static_cast<T *>(t.data_ptr());
+        ok &= at != nullptr;
+        return at;
     }
     template <typename T = void>
     T *maybe(at::ScalarType type, std::initializer_list<Dim *> shape)
@@ -359,21 +373,32 @@ PyObject *verify_draft(PyObject *, PyObject *const *a, Py_ssize_t n)
                   out, ctx, ctx_out, ws, (size_t)size.v, err, stream);
 }
 
+// A whole call; a tensor that throws (a fake one has no address) is not plain.
+template <PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *whole(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    try {
+        return f(self, a, n);
+    } catch (...) {
+        Py_RETURN_NONE;
+    }
+}
+
 #define PKV_METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     PKV_METHOD("arg", arg),
     PKV_METHOD("maybe", maybe),
     PKV_METHOD("use_library", use_library),
-    PKV_METHOD("rope_append", (rope<false, false>)),
-    PKV_METHOD("rope_append_fp8", (rope<true, false>)),
-    PKV_METHOD("rope_append_multi", (rope<false, true>)),
-    PKV_METHOD("rope_append_multi_fp8", (rope<true, true>)),
-    PKV_METHOD("key_bounds", key_bounds<false>),
-    PKV_METHOD("key_bounds_fp8", key_bounds<true>),
-    PKV_METHOD("select_blocks", select_blocks),
-    PKV_METHOD("decode_attn_blocks", decode_attn_blocks<false>),
-    PKV_METHOD("decode_attn_blocks_fp8", decode_attn_blocks<true>),
-    PKV_METHOD("verify_draft", verify_draft),
+    PKV_METHOD("rope_append", (whole<rope<false, false>>)),
+    PKV_METHOD("rope_append_fp8", (whole<rope<true, false>>)),
+    PKV_METHOD("rope_append_multi", (whole<rope<false, true>>)),
+    PKV_METHOD("rope_append_multi_fp8", (whole<rope<true, true>>)),
+    PKV_METHOD("key_bounds", whole<key_bounds<false>>),
+    PKV_METHOD("key_bounds_fp8", whole<key_bounds<true>>),
+    PKV_METHOD("select_blocks", whole<select_blocks>),
+    PKV_METHOD("decode_attn_blocks", whole<decode_attn_blocks<false>>),
+    PKV_METHOD("decode_attn_blocks_fp8", whole<decode_attn_blocks<true>>),
+    PKV_METHOD("verify_draft", whole<verify_draft>),
     {"set_refuse", set_refuse, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

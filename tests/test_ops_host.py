@@ -256,6 +256,29 @@ def test_compiled_calls_leave_what_is_not_plain_to_the_binding():
         tensor_args.use_library(ctypes.CDLL(None)._handle, B._launch)
 
 
+@pytest.mark.filterwarnings("ignore")
+def test_compiled_calls_and_tensors_without_memory():
+    """Fake tensors that say they are on the GPU: no address, no exception past the interpreter."""
+    from paged_kv_decode_slot_gb300.build import build_library
+    build_library()
+    from paged_kv_decode_slot_gb300 import tensor_args
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        c = lambda *shape, dtype=torch.bfloat16: torch.empty(*shape, dtype=dtype, device="cuda")
+        kc, tables, lens, bounds = c(9, 16, 2, 64), c(3, 4, dtype=torch.int32), c(3, dtype=torch.int32), c(9, 2, 2, 64)
+        q, sel, ws, out = c(3, 8, 64), c(3, 2, 5, dtype=torch.int32), c(512, dtype=torch.uint8), c(3, 8, 64)
+        p, tok, u = c(3, 3, 10), c(3, 2, dtype=torch.int32), c(3, 2, dtype=torch.float32)
+        assert kc.is_cuda
+        assert tensor_args.key_bounds(kc, tables, lens, 1, bounds, None, None, 0) is None
+        assert tensor_args.select_blocks(q, bounds, tables, lens, sel, ws, 1, 1, None, 16, None, 0) is None
+        assert tensor_args.decode_attn_blocks(q, kc, kc, tables, lens, sel, 1.0, out, None, 0, 0, None, None, None, 0) is None
+        assert tensor_args.verify_draft(p, None, tok, u, u[:, 0].contiguous(), lens, c(3, 3, dtype=torch.int32), ws, None, None, None,
+                                        None, None, None, 0) is None
+        inv, new, slots = c(32, dtype=torch.float64), c(3, 1, 2, 64), c(3, 1, dtype=torch.int64)
+        assert tensor_args.rope_append_multi(c(3, 1, 8, 64), new, new, tables, lens, inv, kc, kc, c(3, 1, 8, 64), slots, False, None,
+                                             None, 0) is None
+
+
 def test_plan_blocks_attention():
     from paged_kv_decode_slot_gb300.step import plan_blocks_attention as plan
     p = plan(64, 8, 128, 152)
