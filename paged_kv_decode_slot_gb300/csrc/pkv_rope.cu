@@ -20,9 +20,9 @@
 // memory.  A token whose slot is negative is left out: nothing of its rows is written.
 //
 // Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 33.5 us (6.0 TB/s, 88% of the measured
-// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 52.9 us (4.8 TB/s, 71%): bound by issue
-// slots (68% busy; the check of the quotients takes 8 us; 28 of 32 lanes are busy, and an order of the items that puts
-// turned and copied ones into warps of their own took 55.9).  64 decode tokens: 2.8 us, a launch and four dependent loads.
+// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 50.7 us (5.0 TB/s, 74%): bound by issue
+// slots (68% busy; the check of the quotients takes 7 us; 28 of 32 lanes are busy, and an order of the items that put
+// turned and copied ones into warps of their own cost 3 us).  64 decode tokens: 2.8 us, a launch and four dependent loads.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_ops.h"
@@ -72,31 +72,46 @@ __device__ __forceinline__ uint32_t codes(f32x2 v)
     return f32x2_to_e4m3x2(r.x, r.y);
 }
 
-// Eight values as e4m3 codes of x / scale, the quotient rounded to nearest in fp32 as the plain append takes it (the
-// input is the rotation's 32-bit result, so a turned key is rounded once to 8 bits).  x times a reciprocal made smaller,
-// and made larger, by 2^-21 lie to both sides of that quotient (five roundings of 2^-24 between them): where their codes
-// agree, they are the quotient's too (rounding is monotonic; zeros, infinities and NaN agree with themselves); only
-// where they differ is x divided.  The reciprocal of a scale outside [2^-100, 2^100] may over- or underflow: there
-// every x is divided.  (Correcting one product by its remainder, Markstein's way, measured 57.8 us against 53.9 on 5,001
-// tokens of 3 * 40 heads.)
-__device__ __forceinline__ uint2 rope_quantize8(const f32x2 (&x)[4], float sc)
+// A scale's reciprocal, made smaller and made larger by 2^-21.
+struct Reciprocal {
+    f32x2 down, up;
+    float scale;
+    bool plain;  // the scale is in [2^-100, 2^100]
+};
+
+__device__ __forceinline__ Reciprocal reciprocal(float scale)
 {
-    const float r = __frcp_rn(sc), r0 = r * (1.f - 0x1p-21f), r1 = r * (1.f + 0x1p-21f);
-    const f32x2 down = pair(r0, r0), up = pair(r1, r1);
-    uint32_t c[4], differ = 0u;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));  // off by 2^-23 at most
+    const float r0 = r * (1.f - 0x1p-21f), r1 = r * (1.f + 0x1p-21f);
+    return Reciprocal{pair(r0, r0), pair(r1, r1), scale, scale >= 0x1p-100f && scale <= 0x1p100f};
+}
+
+// Two times eight values as e4m3 codes of x / scale, the quotient rounded to nearest in fp32 as the plain append takes it (the
+// input is the rotation's 32-bit result, so a turned key is rounded once to 8 bits).  x times a reciprocal made smaller,
+// and made larger, by 2^-21 lie to both sides of that quotient (five units of 2^-24 between them: two for the reciprocal, one
+// for each product and for the quotient's rounding): where their codes agree, they are the quotient's too (rounding is
+// monotonic; zeros, infinities and NaN agree with themselves); only where they differ is x divided.  The reciprocal of a
+// scale outside [2^-100, 2^100] may over- or underflow: there every x is divided.  (Correcting one product by its remainder,
+// Markstein's way, measured 57.8 us against 53.9 on 5,001 tokens of 3 * 40 heads.)
+__device__ __forceinline__ void rope_quantize(const f32x2 (&x)[4], const f32x2 (&y)[4], const Reciprocal &by, uint2 &cx, uint2 &cy)
+{
+    uint32_t c[8], differ = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        c[i] = codes(mul2(x[i], down));
-        differ |= c[i] ^ codes(mul2(x[i], up));
+    for (int i = 0; i < 8; ++i) {
+        const f32x2 v = i < 4 ? x[i % 4] : y[i % 4];
+        c[i] = codes(mul2(v, by.down));
+        differ |= c[i] ^ codes(mul2(v, by.up));
     }
-    if (differ || !(sc >= 0x1p-100f && sc <= 0x1p100f)) {
+    if (differ || !by.plain) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = halves(x[i]);
-            c[i] = f32x2_to_e4m3x2(__fdiv_rn(v.x, sc), __fdiv_rn(v.y, sc));
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = halves(i < 4 ? x[i % 4] : y[i % 4]);
+            c[i] = f32x2_to_e4m3x2(__fdiv_rn(v.x, by.scale), __fdiv_rn(v.y, by.scale));
         }
     }
-    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    cx = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    cy = make_uint2(c[4] | (c[5] << 16), c[6] | (c[7] << 16));
 }
 
 // A vector's words, unpacked: neighbouring elements of a word as one pair, or (kSplit) the lower elements of two
@@ -270,7 +285,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
             for (int r = 0; r < kRounds; ++r) {
                 const int kvh = t.chunk * per + (tid + r * kRopeThreads) / kPerHead - p.N;
                 if (kvh >= 0 && kvh < 2 * p.K)
-                    to[r] = __ldg((kvh < p.K ? p.k_scale + kvh : p.v_scale + kvh - p.K) + (slot / kBlockSize) * p.scale_stride);
+                    to[r] = __ldg((kvh < p.K ? p.k_scale + kvh : p.v_scale + kvh - p.K) + (int64_t)((uint64_t)slot / kBlockSize) * p.scale_stride);
             }
         }
     };
@@ -292,6 +307,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
         if (there && at_slot >= 0) {
             const uint8_t *src = ring + stage * kStageBytes;
             const float4 *angles = cs[k & 1];
+            uint16_t *q_row = p.q_out + (int64_t)now.i * p.N * H;
+            const int64_t row_off = at_slot * p.K * H;
 #pragma unroll
             for (int r = 0; r < (kUnitHeads * kPerHead + kRopeThreads - 1) / kRopeThreads; ++r) {
                 const int x = tid + r * kRopeThreads;
@@ -327,14 +344,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtasPerSm) rope_append_kern
                     unpack8<false>(a, y0);
                     unpack8<false>(b, y1);
                 }
-                const int kvh = head - p.N - (is_v ? p.K : 0);
+                const int at = (head - p.N - (is_v ? p.K : 0)) * H;
                 if (kFp8 && head >= p.N) {
-                    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) + (at_slot * p.K + kvh) * H;
-                    *reinterpret_cast<uint2 *>(dst + o0) = rope_quantize8(y0, sc[kFp8 ? r : 0]);
-                    *reinterpret_cast<uint2 *>(dst + o1) = rope_quantize8(y1, sc[kFp8 ? r : 0]);
+                    uint8_t *dst = static_cast<uint8_t *>(is_v ? p.v_cache : p.k_cache) + row_off + at;
+                    uint2 c0, c1;
+                    rope_quantize(y0, y1, reciprocal(sc[kFp8 ? r : 0]), c0, c1);
+                    *reinterpret_cast<uint2 *>(dst + o0) = c0;
+                    *reinterpret_cast<uint2 *>(dst + o1) = c1;
                 } else {
-                    uint16_t *dst = head < p.N ? p.q_out + ((int64_t)now.i * p.N + head) * H
-                                               : static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + (at_slot * p.K + kvh) * H;
+                    uint16_t *dst = head < p.N ? q_row + head * H : static_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + row_off + at;
                     *reinterpret_cast<uint4 *>(dst + o0) = turned ? pack8(y0) : a;
                     *reinterpret_cast<uint4 *>(dst + o1) = turned ? pack8(y1) : b;
                 }
