@@ -204,6 +204,27 @@ def test_e4m3_quotients_of_extreme_values(pkv, scale):
     assert torch.equal(kc[..., 64:][~nan[..., 64:]], kc2[..., 64:][~nan[..., 64:]])
 
 
+def test_e4m3_codes_of_every_bf16_value_over_many_scales(pkv):
+    """All 65,536 bit patterns over 96 scales (mantissas of zeros, of ones, next to powers of two, random; exponents from 2^-102
+    to 2^102): the codes of pkv_append_fp8, which divides."""
+    K, H, n = 96, 128, 512
+    r = np.random.default_rng(6)
+    mant = np.concatenate([[0, 1, 0x7FFFFF, 0x7FFFFE, 0x400000, 0x3FFFFF, 0x2AAAAA, 0x555555], r.integers(0, 1 << 23, K - 8)])
+    expo = np.concatenate([np.repeat(127, 8), r.integers(25, 230, 8), r.integers(100, 140, K - 16)])
+    sc = torch.from_numpy((expo.astype(np.uint32) << 23 | mant.astype(np.uint32)).view(np.float32)).cuda()
+    bits = np.arange(65536, dtype=np.uint16).reshape(n, 1, H)
+    kv = bf16_dev(np.ascontiguousarray(np.broadcast_to(bits, (n, K, H))))
+    pools = [torch.zeros(n // 16, 16, K, H, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    slots = torch.arange(n, dtype=torch.int64, device="cuda")
+    pkv.check(pkv.pkv_append_fp8(kv, kv, sc, sc, slots, pools[0], pools[1]))
+    q = torch.zeros(n, 1, H, dtype=torch.bfloat16, device="cuda")
+    pkv.check(pkv.pkv_rope_append_fp8(q, kv, kv, i32_dev(np.zeros(n)), torch.ones(8, dtype=torch.float64, device="cuda"), sc, sc, slots,
+                                      pools[2], pools[3], q))
+    nan = (pools[1] & 0x7F) == 0x7F
+    assert torch.equal((pools[3] & 0x7F) == 0x7F, nan) and torch.equal(pools[3][~nan], pools[1][~nan])
+    assert torch.equal(pools[2][..., 16:][~nan[..., 16:]], pools[0][..., 16:][~nan[..., 16:]])
+
+
 def test_bad_slots_tables_and_lengths_are_flagged_and_left_out(pkv):
     c = Case(6, 20, 4, 2, 64, 64, False)
     q, k, v, pos, f = c.dev()
