@@ -197,6 +197,15 @@ def test_more_partitions_than_run_at_once(pkv, kv, parts):
     c.check(*c.run(pkv, sel, -(-10 // parts)), sel, f"{parts} partitions of {90 * 8} lists")
 
 
+@pytest.mark.parametrize("kv,H", [("bf16", 64), ("bf16", 128), ("e4m3_block", 128)])
+@pytest.mark.parametrize("B", [18, 20, 37, 40, 55, 59])
+def test_whole_lists_around_what_runs_at_once(pkv, kv, H, B):
+    """Eight lists a sequence: about one, two and three for each SM, where the number of warps a list changes."""
+    c = Case(B + H, [int(x) for x in np.random.default_rng(B).integers(0, 16 * 22, B)], 8, 8, H, kv)
+    sel = c.lists(20)
+    c.check(*c.run(pkv, sel), sel, f"{B * 8} lists")
+
+
 @pytest.mark.parametrize("pb", [0, 3])
 def test_nothing_selected(pkv, pb):
     c = Case(14, [100, 3, 0], 4, 2, 64)
