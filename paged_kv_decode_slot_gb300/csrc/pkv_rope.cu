@@ -20,7 +20,7 @@
 // memory.  A token whose slot is negative is left out: nothing of its rows is written.
 //
 // Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 33.5 us (6.0 TB/s, 88% of the measured
-// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 50.7 us (5.0 TB/s, 74%): bound by issue
+// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 50.5 us (5.1 TB/s, 75%): bound by issue
 // slots (68% busy; the check of the quotients takes 7 us; 28 of 32 lanes are busy, and an order of the items that put
 // turned and copied ones into warps of their own cost 3 us).  64 decode tokens: 2.8 us, a launch and four dependent loads.
 #include "pkv_device.cuh"
