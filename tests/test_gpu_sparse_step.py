@@ -213,6 +213,57 @@ def test_launches_behind_copies_other_streams_and_each_other(pkv, kv):
     assert all(bool((outs[0][0][i] != outs[0][0][i + 1]).any()) for i in range(steps - 1))
 
 
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
+def test_two_streams_at_once(pkv, graph):
+    """Two batches' steps and verifications side by side on two streams (clusters, persistent grids and early launches of both
+    share the SMs), many times: the results of one after the other."""
+    from paged_kv_decode_slot_gb300.step import SparseDecodeStep
+    work = []
+    for seed, prompts, kv in ((6, [900, 300, 77], "bf16"), (7, [2000], "e4m3")):
+        s = Serving(pkv, seed, prompts, 2, kv)
+        q, k, v = (bf16_dev(R.to_bf16(s.r.standard_normal((s.B, h, H)))) for h in (N, K, K))
+        scales = dict(k_scale=s.scales[0], v_scale=s.scales[1]) if s.scales else {}
+        step = SparseDecodeStep(q, k, v, s.kc, s.vc, s.bounds, s.tables, i32_dev(s.lens + 1), 0.1, s.inv, 40, err_flag=s.err, **scales)
+        p = torch.softmax(torch.from_numpy(s.r.standard_normal((s.B, 4, 60001))).cuda().float() * 3, -1)
+        d = torch.softmax(torch.from_numpy(s.r.standard_normal((s.B, 3, 60001))).cuda().float() * 3, -1)
+        tok = d.argmax(-1).int()
+        u, sam = torch.from_numpy(s.r.random((s.B, 3)).astype(np.float32)).cuda(), torch.from_numpy(s.r.random(s.B).astype(np.float32)).cuda()
+        acc, out = torch.empty(s.B, dtype=torch.int32, device="cuda"), torch.empty(s.B, 4, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(pkv.pkv_verify_workspace_bytes(s.B, 60001), dtype=torch.uint8, device="cuda")
+
+        def run(step=step, args=(p, d, tok, u, sam, acc, out, ws)):
+            step.run()
+            pkv.check(pkv.pkv_verify_draft(*args))
+        run()
+        torch.cuda.synchronize()
+        results = (step.out, step.lse, step.selected, s.kc, s.vc, acc, out)
+        work.append((run, results, [t.clone() for t in results], torch.cuda.Stream(), s.err))
+    if graph:
+        graphs = []
+        for run, _, _, st, _ in work:
+            g = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g, stream=st):
+                for _ in range(5):
+                    run()
+            graphs.append(g)
+        eager = work                                            # (it holds the tensors that the graphs read)
+        work = [(g.replay, *w[1:]) for g, w in zip(graphs, eager)]
+    for _ in range(4):
+        for _, results, _, _, _ in work:
+            for t in results[:3] + results[5:]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for run, _, _, st, _ in work:
+                with torch.cuda.stream(st):
+                    run()
+        torch.cuda.synchronize()
+        for _, results, want, _, err in work:
+            assert pkv.pkv_read_err_flag(err) == (pkv.PKV_OK, 0)
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(results, want))
+
+
 def test_speculative_steps_over_one_cache(pkv):
     """T drafted tokens and the one before them: rotating append, multi-token attention, verification against the target's
     probabilities, and the next step from the context that remains -- refused tokens' slots are written over."""
