@@ -8,14 +8,15 @@
 //    the producer's lanes; the list's first entries are fetched before the sequence's length is there;
 //  * the tokens that count of a tile follow from its logical block, not from its place in the list: the
 //    producer leaves that number with the stage (0 for an entry to skip);
-//  * the running sum takes the 32-bit weights, so lse does not carry the rounding of the 16-bit weights that
-//    the product P V takes.
+//  * the weights enter the product P V as pairs of 16-bit numbers and the running sum takes them in fp32 (kPairs in
+//    pkv_attn_common.cuh), so that neither the output nor lse carries a rounding of the weights to 16 bits: with one
+//    16-bit weight each, 64 sequences took 86.1 us instead of 87.9 and the e4m3 batch below 44.6 instead of 46.7.
 // One CTA per (KV head, sequence, partition of the list); a list's partitions are one cluster, which joins their partial
 // results in its shared memory, or (many of them) the last to finish joins them from the workspace.
 // Bound by memory: 32 H bytes of K and as many of V per tile and two bytes an element.  64 sequences of 512 to 8,192 tokens,
-// up to 128 blocks for each of 8 KV heads, 498 MB: 86 us (5.8 TB/s, 85% of the measured copy bandwidth); 20 sequences of 250
-// e4m3 blocks, 165 MB: 45 us, 320 CTAs on 152 SMs (38 of 125, as many tiles in even numbers: 35); one sequence of 128 blocks:
-// 6.5 us, the chain of length, list, table, tiles and merge.
+// up to 128 blocks for each of 8 KV heads, 498 MB: 88 us (5.7 TB/s, 83% of the measured copy bandwidth); 20 sequences of 250
+// e4m3 blocks, 165 MB: 47 us, 320 CTAs on 152 SMs; one sequence of 128 blocks:
+// 6.8 us, the chain of length, list, table, tiles and merge.
 #include "pkv_attn_common.cuh"
 #include "pkv_cluster.cuh"
 #include "pkv_ops.h"
@@ -23,77 +24,6 @@
 namespace pkv {
 
 constexpr int kClusterMost = 16;  // partitions of a list that are one cluster, at most (beyond 8 by the device's leave)
-
-// One 16-token tile (the first `valid` tokens count) folded into a warp's state, bf16.
-template <int H>
-__device__ __forceinline__ void block_update(WarpAcc<H> &a, const uint32_t (&qf)[H / 16][2], uint32_t kt, uint32_t vt,
-                                             int valid, float sl2, int tok_major, int lane)
-{
-    constexpr int kKSteps = H / 16;
-    const int mi = lane >> 3, ri = lane & 7;
-    const int k_tok = ri + 8 * (mi & 1), k_hoff = 8 * (mi >> 1);
-    const int v_tok = ri + 8 * (mi >> 1), v_hoff = 8 * (mi & 1);
-    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kk = 0; kk < kKSteps; kk += 2) {
-        uint32_t a0[4], a1[4];
-        ldsm_x4(a0, kt + tile_chunk_offset<H>(k_tok, 16 * kk + k_hoff, tok_major));
-        ldsm_x4(a1, kt + tile_chunk_offset<H>(k_tok, 16 * kk + 16 + k_hoff, tok_major));
-        mma_bf16_16816(sa, a0, qf[kk][0], qf[kk][1]);
-        mma_bf16_16816(sb, a1, qf[kk + 1][0], qf[kk + 1][1]);
-    }
-    const int t0 = lane >> 2, t1 = t0 + 8;
-    const float x0 = t0 < valid ? (sa[0] + sb[0]) * sl2 : -INFINITY;
-    const float x1 = t0 < valid ? (sa[1] + sb[1]) * sl2 : -INFINITY;
-    const float x2 = t1 < valid ? (sa[2] + sb[2]) * sl2 : -INFINITY;
-    const float x3 = t1 < valid ? (sa[3] + sb[3]) * sl2 : -INFINITY;
-    float mA = fmaxf(x0, x2), mB = fmaxf(x1, x3);
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-        mA = fmaxf(mA, __shfl_xor_sync(0xFFFFFFFFu, mA, off));
-        mB = fmaxf(mB, __shfl_xor_sync(0xFFFFFFFFu, mB, off));
-    }
-    const bool needA = mA > a.m[0] + kRescaleThreshold;
-    const bool needB = mB > a.m[1] + kRescaleThreshold;
-    if (__any_sync(0xFFFFFFFFu, needA || needB)) {
-        const float alphaA = needA ? exp2_sfu(a.m[0] - mA) : 1.f;
-        const float alphaB = needB ? exp2_sfu(a.m[1] - mB) : 1.f;
-        if (needA) a.m[0] = mA;
-        if (needB) a.m[1] = mB;
-        a.l[0] *= alphaA;
-        a.l[1] *= alphaB;
-#pragma unroll
-        for (int mt = 0; mt < kKSteps; ++mt) {
-            a.o[mt][0] *= alphaA;
-            a.o[mt][1] *= alphaB;
-            a.o[mt][2] *= alphaA;
-            a.o[mt][3] *= alphaB;
-        }
-    }
-    const float w0 = exp2_sfu(x0 - a.m[0]), w1 = exp2_sfu(x1 - a.m[1]);
-    const float w2 = exp2_sfu(x2 - a.m[0]), w3 = exp2_sfu(x3 - a.m[1]);
-    a.l[0] += w0 + w2;
-    a.l[1] += w1 + w3;
-    // the weights enter the product P V rounded to bf16 (off by 2^-9 at most, as the result's own rounding is)
-    const uint32_t pb0 = movmatrix_trans(pack_bf16x2(w0, w1));
-    const uint32_t pb1 = movmatrix_trans(pack_bf16x2(w2, w3));
-    const bool partial = valid < kBlockSize;
-    const int tc = (lane & 3) * 2;
-#pragma unroll
-    for (int mt = 0; mt < kKSteps; ++mt) {
-        uint32_t av[4];
-        ldsm_x4_trans(av, vt + tile_chunk_offset<H>(v_tok, 16 * mt + v_hoff, tok_major));
-        if (partial) {  // zero V of tokens past the context (they may be NaN)
-            const uint32_t lo = (tc < valid ? 0x0000FFFFu : 0u) | (tc + 1 < valid ? 0xFFFF0000u : 0u);
-            const uint32_t hi = (tc + 8 < valid ? 0x0000FFFFu : 0u) | (tc + 9 < valid ? 0xFFFF0000u : 0u);
-            av[0] &= lo;
-            av[1] &= lo;
-            av[2] &= hi;
-            av[3] &= hi;
-        }
-        mma_bf16_16816(a.o[mt], av, pb0, pb1);
-    }
-}
 
 // kFp8: e4m3 pools (H = 128).  Scales come per tile in both granularities (the producer fetches them with the
 // block id): the K scale multiplies the tile's logits, the V scale its weights relative to the largest seen
@@ -265,9 +195,9 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (valid > 0) {
                 const uint32_t kt = base_u32 + s * L::kStageBytes;
                 if constexpr (kFp8)
-                    tile_update_fp8<H, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2 * stage_sc[s].x, stage_sc[s].y, vr, lane);
+                    tile_update_fp8<H, true, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2 * stage_sc[s].x, stage_sc[s].y, vr, lane);
                 else
-                    block_update<H>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2, p.tok_major, lane);
+                    tile_update<H, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2, p.tok_major, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_empty + 8 * s);

@@ -128,8 +128,12 @@ __device__ __forceinline__ void load_q_frags(uint32_t (&qf)[H / 16][2], const ui
     }
 }
 
-// One 16-token tile (the first `valid` tokens count) folded into a warp's state.
-template <int H>
+// One 16-token tile (the first `valid` tokens count) folded into a warp's state.  The product P V takes
+// the softmax weights as bf16; the running sum takes what the product took, so that the average
+// is exactly normalised.  kPairs: each weight enters the product as two bf16 numbers, the rounded weight
+// and what the rounding left (two matrix instructions instead of one; what is lost is 2^-16 of the
+// weight), and the sum takes the fp32 weights.
+template <int H, bool kPairs = false>
 __device__ __forceinline__ void tile_update(WarpAcc<H> &a, const uint32_t (&qf)[H / 16][2],
                                             uint32_t kt, uint32_t vt, int valid, float sl2,
                                             int tok_major, int lane)
@@ -178,10 +182,20 @@ __device__ __forceinline__ void tile_update(WarpAcc<H> &a, const uint32_t (&qf)[
             a.o[mt][3] *= alphaB;
         }
     }
-    const uint32_t p01 = pack_bf16x2(exp2_sfu(x0 - a.m[0]), exp2_sfu(x1 - a.m[1]));
-    const uint32_t p23 = pack_bf16x2(exp2_sfu(x2 - a.m[0]), exp2_sfu(x3 - a.m[1]));
-    a.l[0] += bf16x2_lo(p01) + bf16x2_lo(p23);  // sums of the rounded weights
-    a.l[1] += bf16x2_hi(p01) + bf16x2_hi(p23);
+    const float w0 = exp2_sfu(x0 - a.m[0]), w1 = exp2_sfu(x1 - a.m[1]);
+    const float w2 = exp2_sfu(x2 - a.m[0]), w3 = exp2_sfu(x3 - a.m[1]);
+    const uint32_t p01 = pack_bf16x2(w0, w1);
+    const uint32_t p23 = pack_bf16x2(w2, w3);
+    uint32_t rest0 = 0u, rest1 = 0u;
+    if constexpr (kPairs) {
+        a.l[0] += w0 + w2;
+        a.l[1] += w1 + w3;
+        rest0 = movmatrix_trans(pack_bf16x2(w0 - bf16x2_lo(p01), w1 - bf16x2_hi(p01)));
+        rest1 = movmatrix_trans(pack_bf16x2(w2 - bf16x2_lo(p23), w3 - bf16x2_hi(p23)));
+    } else {
+        a.l[0] += bf16x2_lo(p01) + bf16x2_lo(p23);  // sums of the rounded weights
+        a.l[1] += bf16x2_hi(p01) + bf16x2_hi(p23);
+    }
     const uint32_t pb0 = movmatrix_trans(p01);    // P^T rows tok 0-7 -> B fragment
     const uint32_t pb1 = movmatrix_trans(p23);    // tok 8-15
 
@@ -203,6 +217,7 @@ __device__ __forceinline__ void tile_update(WarpAcc<H> &a, const uint32_t (&qf)[
             av[3] &= lo1 | hi1;
         }
         mma_bf16_16816(a.o[mt], av, pb0, pb1);
+        if constexpr (kPairs) mma_bf16_16816(a.o[mt], av, rest0, rest1);
     }
 }
 
@@ -252,8 +267,10 @@ struct VScaleRef {
 
 // One 16-token e4m3 tile folded into a warp's state (the codes only: the tile's K scale is folded
 // into sl2).  kBS: per-(block, head) scales -- the tile's V scale vs_t enters through vr (above);
-// otherwise the head's V scale multiplies the output at the end and vs_t / vr are unused.
-template <int H, bool kBS = false>
+// otherwise the head's V scale multiplies the output at the end and vs_t / vr are unused.  kPairs: each
+// weight enters the product P V as two f16 numbers, the rounded weight and what the rounding left (what is
+// lost is 2^-22 of the weight, or 2^-25 of the largest weights' unit), as in tile_update.
+template <int H, bool kBS = false, bool kPairs = false>
 __device__ __forceinline__ void tile_update_fp8(WarpAcc<H> &a, const uint32_t (&qf)[H / 16][2],
                                                 uint32_t kt, uint32_t vt, int valid, float sl2, float vs_t,
                                                 VScaleRef &vr, int lane)
@@ -328,7 +345,12 @@ __device__ __forceinline__ void tile_update_fp8(WarpAcc<H> &a, const uint32_t (&
     const float vsr = kBS ? vs_t * vr.inv : 1.f;  // <= 1 (+ rounding)
     const uint32_t p01 = pack_f16x2(w0 * vsr, w1 * vsr);
     const uint32_t p23 = pack_f16x2(w2 * vsr, w3 * vsr);
-    if constexpr (kBS) {
+    uint32_t rest0 = 0u, rest1 = 0u;
+    if constexpr (kPairs) {
+        rest0 = movmatrix_trans(pack_f16x2(w0 * vsr - f16x2_lo(p01), w1 * vsr - f16x2_hi(p01)));
+        rest1 = movmatrix_trans(pack_f16x2(w2 * vsr - f16x2_lo(p23), w3 * vsr - f16x2_hi(p23)));
+    }
+    if constexpr (kBS || kPairs) {
         a.l[0] += w0 + w2;
         a.l[1] += w1 + w3;
     } else {  // sums of the rounded weights: the weighted average is exactly normalised
@@ -371,6 +393,7 @@ __device__ __forceinline__ void tile_update_fp8(WarpAcc<H> &a, const uint32_t (&
                 av[3] &= lo1 | hi1;
             }
             mma_f16_16816(a.o[mt + hf], av, pb0, pb1);
+            if constexpr (kPairs) mma_f16_16816(a.o[mt + hf], av, rest0, rest1);
         }
     }
 }
