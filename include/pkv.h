@@ -226,7 +226,7 @@ int pkv_append_fp8(const pkv_bf16 *k_new, const pkv_bf16 *v_new, const float *k_
 /* Decode attention over e4m3 pools: partition_blocks 0 = single pass (workspace unused),
    > 0 = partitions as in pkv_decode_attn_splitk (tapered under the same conditions) + log-sum-exp
    merge, with its workspace.
-   q 8-byte aligned. */
+   q 8-byte aligned and held in f16: elements below 2^-14 lose bits, those from 65,520 on become infinite. */
 int pkv_decode_attn_fp8(const pkv_bf16 *q, const uint8_t *k_cache, const uint8_t *v_cache,
                         const float *k_scale, const float *v_scale, int32_t scale_block_stride,
                         const int32_t *block_tables,
@@ -592,7 +592,9 @@ int pkv_decode_attn_blocks(const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv
                            int32_t max_partitions, void *workspace, size_t workspace_bytes,
                            int32_t *err_flag, pkv_stream_t stream);
 
-/* The same over e4m3 pools (q 8-byte aligned), scales as in pkv_decode_attn_fp8. */
+/* The same over e4m3 pools (q 8-byte aligned), scales as in pkv_decode_attn_fp8.  Queries may be of any magnitude.
+   Weights are held relative to the largest V scale of a list: where the blocks that matter have V scales 2^k times
+   smaller than that one, they are off by 2^(k - 25) of themselves. */
 int pkv_decode_attn_blocks_fp8(const pkv_bf16 *q, const uint8_t *k_cache, const uint8_t *v_cache,
                                const float *k_scale, const float *v_scale, int32_t scale_block_stride,
                                const int32_t *block_tables, int32_t max_blocks_per_seq,

@@ -180,7 +180,8 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     } else {
         // ------------------------------ consumer warps ------------------------------
         uint32_t qf[H / 16][2];
-        if constexpr (kFp8) load_q_frags_fp8<H>(qf, p.q, p.N, b, kvh, G, lane);
+        float2 back;
+        if constexpr (kFp8) back = load_q_frags_fp8_scaled<H>(qf, p.q, p.N, b, kvh, G, lane);
         else load_q_frags<H>(qf, p.q, p.N, b, kvh, G, lane);
         acc_reset<H>(acc);
         for (int i = warp; i < n; i += W) {
@@ -195,7 +196,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (valid > 0) {
                 const uint32_t kt = base_u32 + s * L::kStageBytes;
                 if constexpr (kFp8)
-                    tile_update_fp8<H, true, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2 * stage_sc[s].x, stage_sc[s].y, vr, lane);
+                    tile_update_fp8<H, true, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2 * stage_sc[s].x, stage_sc[s].y, vr, lane, back);
                 else
                     tile_update<H, true>(acc, qf, kt, kt + L::kTileBytes, valid, p.scale_log2, p.tok_major, lane);
             }

@@ -253,6 +253,36 @@ __device__ __forceinline__ void load_q_frags_fp8(uint32_t (&qf)[H / 16][2], cons
     }
 }
 
+// The same with every query row scaled by a power of two that takes its largest element to [2^14, 2^15), so that no
+// bf16 query leaves f16's range: elements down to 2^-28 of the row's largest stay exact, smaller ones are off
+// by 2^-39 of it at most.  Returns what takes the row's logits back, for this lane's two columns.
+template <int H>
+__device__ __forceinline__ float2 load_q_frags_fp8_scaled(uint32_t (&qf)[H / 16][2], const uint16_t *q, int N,
+                                                          int b, int kvh, int G, int lane)
+{
+    const int g_row = lane >> 2, m = lane & 3;
+    const bool live = g_row < G;
+    const uint16_t *qrow = q + ((size_t)b * N + (size_t)kvh * G + (live ? g_row : 0)) * H;
+    uint32_t top = 0u;
+#pragma unroll
+    for (int kk = 0; kk < H / 16; ++kk) {
+        const uint2 v = live ? __ldg(reinterpret_cast<const uint2 *>(qrow + 16 * kk + 4 * m)) : make_uint2(0u, 0u);
+        qf[kk][0] = v.x;
+        qf[kk][1] = v.y;
+        top = max(top, max(max(v.x & 0x7FFFu, v.x >> 16 & 0x7FFFu), max(v.y & 0x7FFFu, v.y >> 16 & 0x7FFFu)));
+    }
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));  // the row's other lanes
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const uint32_t e = min(268u - (top >> 7), 253u);  // exponent field of the factor, 2^126 at most
+    const float f = __uint_as_float(e << 23), back = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int kk = 0; kk < H / 16; ++kk)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) qf[kk][i] = pack_f16x2(bf16x2_lo(qf[kk][i]) * f, bf16x2_hi(qf[kk][i]) * f);
+    const int c0 = 4 * (2 * (lane & 3));  // a lane of the row of this lane's first column
+    return make_float2(__shfl_sync(0xFFFFFFFFu, back, c0), __shfl_sync(0xFFFFFFFFu, back, c0 + 4));
+}
+
 // Reference V scale of a warp's e4m3 tiles with one scale per (physical block, KV head).  The
 // warp's O holds sum_t w_t (vs_t / v) code_t, so its output is O * v / l.  v is the largest V scale
 // the warp has seen (0 before its first tile): when a tile's scale exceeds it, O is rescaled by
@@ -269,11 +299,12 @@ struct VScaleRef {
 // into sl2).  kBS: per-(block, head) scales -- the tile's V scale vs_t enters through vr (above);
 // otherwise the head's V scale multiplies the output at the end and vs_t / vr are unused.  kPairs: each
 // weight enters the product P V as two f16 numbers, the rounded weight and what the rounding left (what is
-// lost is 2^-22 of the weight, or 2^-25 of the largest weights' unit), as in tile_update.
+// lost is 2^-22 of the weight, or 2^-25 of the largest weights' unit), as in tile_update, and the queries'
+// rows were scaled (load_q_frags_fp8_scaled): `back` takes the columns' logits back.
 template <int H, bool kBS = false, bool kPairs = false>
 __device__ __forceinline__ void tile_update_fp8(WarpAcc<H> &a, const uint32_t (&qf)[H / 16][2],
                                                 uint32_t kt, uint32_t vt, int valid, float sl2, float vs_t,
-                                                VScaleRef &vr, int lane)
+                                                VScaleRef &vr, int lane, float2 back = make_float2(1.f, 1.f))
 {
     constexpr int kKSteps = H / 16;
     const int mi = lane >> 3, ri = lane & 7;
@@ -304,11 +335,17 @@ __device__ __forceinline__ void tile_update_fp8(WarpAcc<H> &a, const uint32_t (&
         mma_f16_16816(sa, a0, qf[kk][0], qf[kk][1]);
         mma_f16_16816(sb, a1, qf[kk + 1][0], qf[kk + 1][1]);
     }
+    float s4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s4[i] = sa[i] + sb[i];
+        if constexpr (kPairs) s4[i] *= i & 1 ? back.y : back.x;  // before the scales: what overflows here is beyond fp32 itself
+    }
     const int t0 = lane >> 2, t1 = t0 + 8;
-    const float x0 = t0 < valid ? (sa[0] + sb[0]) * sl2 : -INFINITY;
-    const float x1 = t0 < valid ? (sa[1] + sb[1]) * sl2 : -INFINITY;
-    const float x2 = t1 < valid ? (sa[2] + sb[2]) * sl2 : -INFINITY;
-    const float x3 = t1 < valid ? (sa[3] + sb[3]) * sl2 : -INFINITY;
+    const float x0 = t0 < valid ? s4[0] * sl2 : -INFINITY;
+    const float x1 = t0 < valid ? s4[1] * sl2 : -INFINITY;
+    const float x2 = t1 < valid ? s4[2] * sl2 : -INFINITY;
+    const float x3 = t1 < valid ? s4[3] * sl2 : -INFINITY;
     float mA = fmaxf(x0, x2), mB = fmaxf(x1, x3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {

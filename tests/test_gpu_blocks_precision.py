@@ -110,3 +110,21 @@ def test_the_average_of_a_constant_is_that_constant(pkv, kv, N, K, H, pb):
     c.v = np.broadcast_to(row, c.v.shape).copy()
     out, _ = c.run(pkv, pb)
     assert np.array_equal(out, np.broadcast_to(np.repeat(want, N // K, 0), out.shape))
+
+
+@pytest.mark.parametrize("kv,power", [(kv, p) for kv in ("e4m3_head", "e4m3_block") for p in (-120, -100, -30, -14, 15, 16, 40, 100, 120)] +
+                         [("bf16", p) for p in (-100, 16, 100)])
+def test_queries_of_any_magnitude(pkv, kv, power):
+    """Queries of 2^power under a softmax scale of 2^-power, whose logits are ordinary; and one head of a group whose logits are
+    2^power times the others', which attends to its largest logits alone, or to all tokens alike (K scales are powers of
+    two there: logits are equal, or apart by 2^-8 of themselves)."""
+    c = Case(power + 200, kv, 8, 2, 128, unit=2.0 ** power)
+    c.scale = 2.0 ** -power
+    check(c, *c.run(pkv, 0))
+    c = Case(power + 300, kv, 8, 2, 128)
+    q = R.bf16_values(c.q)
+    q[:, 3] *= 2.0 ** power
+    c.q = R.to_bf16(q)
+    if c.scales:
+        c.scales = ((2.0 ** np.round(np.log2(c.scales[0]))).astype(np.float32), c.scales[1])
+    check(c, *c.run(pkv, 2))
