@@ -561,8 +561,8 @@ size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_
    of KV head kvh, of sum_h max(q_h lo_jh, q_h hi_jh): no q . k of block j exceeds it.  selected int32
    [num_seqs][K][max_selected] receives logical block indices in ascending order: all of a sequence's blocks
    if it has no more than max_selected; else its first first_blocks and last last_blocks blocks, which need
-   no bounds, and the best scored of the others, max_selected in all -- exactly those that the scores' real
-   values choose, ties to the lowest index (a NaN score counts as the largest).  Entries behind a sequence's
+   no bounds, and the best scored of the others, max_selected in all -- exactly those that the scores choose,
+   each its real value rounded once to 64 bits, ties to the lowest index (a NaN score counts as the largest).  Entries behind a sequence's
    blocks are -1.  q bf16 [num_seqs][N][H] (16-byte aligned) as attention takes it, for a positive softmax
    scale.  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE and scores -inf.  H in {64, 128},
    G in {1, 2, 4, 8}, first_blocks + last_blocks <= max_selected. */

@@ -12,14 +12,16 @@
 // order of its fp32 sums alone.
 //
 // Two launches, the second started early (programmatic serialization): scores into the workspace, then one CTA per
-// (sequence, KV head) chooses.  64 sequences of 8K to 32K tokens, 8 KV heads, 128 blocks each: 69 us, of which the scores,
-// bound by memory, 57 for 336 MB (5.9 TB/s, 87% of the measured copy bandwidth); one sequence of 32K tokens: 8.5 us, the
-// latency of a tile's loads (3.5) and of the choice's barriers and passes over shared memory (5).
+// (sequence, KV head) chooses.  64 sequences of 8K to 32K tokens, 8 KV heads, 128 blocks each: 70 us, of which the scores,
+// bound by memory, 57 for 336 MB (5.9 TB/s, 87% of the measured copy bandwidth); one sequence of 32K tokens: 9.0 us, the
+// latency of a tile's loads (3.5) and of the choice's barriers and passes over shared memory (5.5).
 //
 // Selection.  The first F and the last L blocks, and the best of the rest, M in all, in ascending order:
-// exactly those that the scores' real values choose, ties to the lowest index.  With eps bounding the
+// exactly those that the scores' real values choose, rounded once to 64 bits, ties to the lowest index.  With eps bounding the
 // error of every score, t the k-th largest score: a block above t + 2 eps is in, one below t - 2 eps is out,
-// and if those between do not all fit, their sums are taken again, as integers (exact_score), and ranked.
+// and if those between do not all fit, their sums are taken again, as integers (exact_score), and ranked.  Operands whose
+// magnitudes lie more than 2^50 apart within a group and a block take a longer sum (wide_score): if every block of one sequence
+// of 32K tokens has to, the selection takes 0.7 ms, of 64 such sequences 2.4 ms.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_ops.h"
@@ -337,24 +339,95 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
     return lo;
 }
 
-// The sum over h of max(q lo, q hi), the largest over the group's heads, by one warp: `best` holds the heads' sums so far.
-// In 64-bit floating point (in 32 bits products of bf16 numbers may over- or underflow; here they are exact).  The order of
-// the sum is the same for every block, so equal blocks get equal sums.
+// The sum over a warp of m[e] 2^(at[e] - 266), |m| < 2^16, 0 <= at <= 506, rounded once to 64 bits (to nearest, ties to even).
+// In digits of 16 bits from the lowest one that any term reaches: the terms' parts of a digit are added up as integers, what
+// is beyond 16 bits is carried on, and the last 80 bits are kept with a note of what fell off below them.
 template <int E>
-__device__ __forceinline__ double head_sum(const float (&x)[E], const float (&lo)[E], const float (&hi)[E])
+__device__ __forceinline__ double exact_sum(const int (&m)[E], const int (&at)[E])
 {
-    double sum = 0.0;
+    int from = 512, to = 0, sign = 1;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum += (double)x[e] * (double)(x[e] > 0.f ? hi[e] : lo[e]);
+    for (int e = 0; e < E; ++e)
+        if (m[e]) from = min(from, at[e]), to = max(to, at[e]);
+    from = __reduce_min_sync(0xFFFFFFFFu, from) >> 4;
+    to = (__reduce_max_sync(0xFFFFFFFFu, to) >> 4) + 2;  // 16 bits of the terms, 7 of their number
+    unsigned long long window = 0, best = 0;  // the last four digits; as they were at the highest digit that is not 0
+    unsigned under = 0, best_under = 0;       // the digit below them
+    bool lost, best_lost = false;             // anything below that one
+    int top = -1;
+    for (;;) {
+        int carry = 0;
+        lost = false, window = 0, under = 0, top = -1;
+        for (int i = from; i <= to; ++i) {
+            int part = carry;
+            int mine = 0;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-    return sum;
+            for (int e = 0; e < E; ++e) {
+                const int v = sign * m[e] * (1 << (at[e] & 15)), w = at[e] >> 4;  // below 2^31
+                mine += w == i ? v & 0xFFFF : (w + 1 == i ? v >> 16 : 0);
+            }
+            part += __reduce_add_sync(0xFFFFFFFFu, mine);
+            const unsigned digit = part & 0xFFFF;
+            carry = part >> 16;
+            lost |= under != 0;
+            under = (unsigned)window & 0xFFFFu;
+            window = window >> 16 | (unsigned long long)digit << 48;
+            if (digit) best = window, best_under = under, best_lost = lost, top = i;
+        }
+        if (carry >= 0) break;
+        sign = -1;  // a negative sum: once more with the signs turned round
+    }
+    if (top < 0) return 0.0;
+    const int lead = __clzll((long long)best);  // below 16
+    const unsigned long long r =
+        best << lead | best_under >> (16 - lead) | (unsigned long long)(best_lost || (best_under << lead & 0xFFFFu));
+    const double unit = __longlong_as_double((long long)(1023 + 16 * (top - 3) - lead - 266) << 52);
+    return (sign < 0 ? -unit : unit) * __ull2double_rn(r);
 }
 
-// The score of block j, exact but for one rounding to 64 bits.  fp64 units are few on this chip (through them this step took
+// A block's score, rounded once to 64 bits, whatever its operands: q [G][H] and the block's two rows of bounds, at this lane's
+// elements.  Head by head; infinities and NaN go through 64-bit floating point, where nothing finite changes the outcome.
+// Seldom needed, so a call of its own.
+template <int H>
+__device__ __noinline__ double wide_score(const uint16_t *q, const uint16_t *row, int G)
+{
+    constexpr int E = H / 32;
+    double best = -__longlong_as_double(0x7FF0000000000000ll);
+    bool nan = false;
+    for (int g = 0; g < G; ++g) {
+        int m[E], at[E];
+        uint16_t x[E], b[E];
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            x[e] = q[g * H + e];
+            b[e] = row[(bf16_to_f32(x[e]) > 0.f ? H : 0) + e];
+            const int ex = x[e] >> 7 & 255, eb = b[e] >> 7 & 255;
+            odd |= ex == 255 || eb == 255;
+            const int v = ((x[e] & 127) | (ex ? 128 : 0)) * ((b[e] & 127) | (eb ? 128 : 0));
+            m[e] = (x[e] ^ b[e]) >> 15 ? -v : v;
+            at[e] = max(ex, 1) + max(eb, 1) - 2;  // q is its mantissa times 2^(ex - 134), and so is the bound
+        }
+        double sum = 0.0;
+        if (__any_sync(0xFFFFFFFFu, odd)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum += (double)bf16_to_f32(x[e]) * (double)bf16_to_f32(b[e]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+        } else {
+            sum = exact_sum<E>(m, at);
+        }
+        nan |= sum != sum;
+        best = sum > best ? sum : best;
+    }
+    return nan ? __longlong_as_double(0x7FF8000000000000ll) : best;
+}
+
+// The score of block j, rounded once to 64 bits.  fp64 units are few on this chip (through them this step took
 // 5 us of a choice, so it takes 1.5), so the products, scaled below 1 by powers of two, are added up as integers: adding 3
 // rounds a number below 1 to a multiple of 2^-22 in the sum's bits, the rest goes the same way at 2^-44 and 2^-66.  A product
-// has 16 bits, so what is lost is below 2^-66 of the largest possible one.  kHold: the queries are held in registers and on
+// has 16 bits, so nothing is lost where the smallest operands are within 2^50 of the largest, in the exponents of the group's
+// queries and of the block's bounds together; other blocks take wide_score.  kHold: the queries are held in registers and on
 // their way while the block is looked up (1.2 us less for a CTA that has registers to spare).
 template <int H, bool kHold>
 __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int kvh, int j, int lane)
@@ -365,14 +438,18 @@ __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int 
     const int blk = __ldg(p.block_tables + (size_t)b * p.max_nb + j);
     const uint16_t *q = p.q + ((size_t)b * p.N + (size_t)kvh * p.G) * H + lane * E;
     uint16_t held[kHold ? 8 : 1][E];
-    unsigned top_b = 0, top_q = 0;
+    unsigned top_b = 0, top_q = 0, low_b = ~0u, low_q = ~0u;  // largest, and smallest but 0 (less 1)
+    auto range = [](unsigned x, unsigned &top, unsigned &low) {
+        top = max(top, x & 0x7FFFu);
+        low = min(low, (x & 0x7FFFu) - 1u);
+    };
     if constexpr (kHold) {
 #pragma unroll
         for (int g = 0; g < 8; ++g)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 held[g][e] = g < p.G ? q[g * H + e] : 0;
-                top_q = max(top_q, held[g][e] & 0x7FFFu);
+                range(held[g][e], top_q, low_q);
             }
     }
     if (blk < 0 || blk >= p.num_blocks) return -kInf;
@@ -382,29 +459,19 @@ __device__ __forceinline__ double exact_score(const SelectParams &p, int b, int 
     for (int e = 0; e < E; ++e) {
         const unsigned l = row[e], h = row[H + e];
         lo[e] = bf16_to_f32((uint16_t)l), hi[e] = bf16_to_f32((uint16_t)h);
-        top_b = max(top_b, max(l & 0x7FFFu, h & 0x7FFFu));
+        range(l, top_b, low_b);
+        range(h, top_b, low_b);
     }
     if constexpr (!kHold) {
 #pragma unroll 4
         for (int g = 0; g < p.G; ++g)
 #pragma unroll
-            for (int e = 0; e < E; ++e) top_q = max(top_q, q[g * H + e] & 0x7FFFu);
+            for (int e = 0; e < E; ++e) range(q[g * H + e], top_q, low_q);
     }
     const int eb = (int)(__reduce_max_sync(0xFFFFFFFFu, top_b) >> 7), eq = (int)(__reduce_max_sync(0xFFFFFFFFu, top_q) >> 7);
-    double best = -kInf;
-    bool nan = false;
-    if (eb >= 253 || eq >= 253) {  // infinities, NaN and numbers whose scale is out of range
-#pragma unroll 1
-        for (int g = 0; g < p.G; ++g) {
-            float y[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) y[e] = bf16_to_f32(q[g * H + e]);
-            const double sum = head_sum<E>(y, lo, hi);
-            nan |= sum != sum;
-            best = sum > best ? sum : best;
-        }
-        return nan ? __longlong_as_double(0x7FF8000000000000ll) : best;
-    }
+    const int sb = (int)(__reduce_min_sync(0xFFFFFFFFu, low_b) + 1u >> 7), sq = (int)(__reduce_min_sync(0xFFFFFFFFu, low_q) + 1u >> 7);
+    // infinities, NaN and numbers whose scale is out of range; products whose last bit lies below 2^-66
+    if (eb >= 253 || eq >= 253 || (eb - max(sb, 1)) + (eq - max(sq, 1)) > 50) return wide_score<H>(q, row, p.G);
     const float fb = __uint_as_float((unsigned)(253 - eb) << 23), fq = __uint_as_float((unsigned)(253 - eq) << 23);
 #pragma unroll
     for (int e = 0; e < E; ++e) lo[e] *= fb, hi[e] *= fb;
