@@ -46,7 +46,7 @@ __device__ __forceinline__ float clean(float x) { return __saturatef(x); }
 // are added up as integers, the constants' taken off at the end.  Exact up to 256 weights (2^22 units each at most).
 struct WeightSum {
     static constexpr float kA = 3.f, kB = 3.f / 4194304.f;
-    int a = 0, b = 0;
+    unsigned a = 0, b = 0;
     // p cleaned; q only has to be cleaned from below: min(p, q) takes off what lies above p
     __device__ __forceinline__ void add(float p, float q)
     {
@@ -54,14 +54,14 @@ struct WeightSum {
         const float d = __fsub_rn(p, m), e = __fsub_rn(__fsub_rn(p, d), m);  // p - m = d + e exactly (p >= m >= 0)
         const float ta = __fadd_rn(d, kA);
         const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(ta, kA)), e);
-        a += __float_as_int(ta);
-        b += __float_as_int(__fadd_rn(r, kB));
+        a += __float_as_uint(ta);
+        b += __float_as_uint(__fadd_rn(r, kB));
     }
-    // in units of 2^-44, after n additions (integers wrap around and back)
+    // in units of 2^-44, after n additions (the counts wrap around and back)
     __device__ __forceinline__ long long units(int n) const
     {
-        const int ua = (int)((unsigned)a - (unsigned)n * (unsigned)__float_as_int(kA));
-        const int ub = (int)((unsigned)b - (unsigned)n * (unsigned)__float_as_int(kB));
+        const int ua = (int)(a - n * __float_as_uint(kA));
+        const int ub = (int)(b - n * __float_as_uint(kB));
         return ((long long)ua << 22) + ub;
     }
 };
