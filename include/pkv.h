@@ -618,9 +618,10 @@ size_t pkv_verify_workspace_bytes(int32_t num_seqs, int32_t vocab_size);
 
 /* Drafted token x_t = draft_tokens[b][t] stands while accept_u[b][t] * q_t(x_t) < p_t(x_t) (the products
    exact); at the first refusal t the next token is drawn from max(p_t - q_t, 0), and where all stand from
-   p_T': the first index whose running sum of those weights exceeds sample_u[b] times their total (sums
-   exact to 2^-44, so the draw does not depend on how the work is split; a residual without mass, possible
-   only for rows that are no distributions, falls back to p_t).  target_probs [num_seqs][T + 1] rows of
+   p_T': the first index whose running sum of those weights exceeds sample_u[b] times their total (weights
+   rounded to multiples of 2^-44, or of 2^-44 of the power of two above the row's largest one where they add up
+   to less than 2^-8, which takes longer; sums of them exact, so the draw does not depend on how the work is
+   split; a residual that is zero everywhere, possible only for rows that are no distributions, falls back to p_t).  target_probs [num_seqs][T + 1] rows of
    target_stride elements, draft_probs [num_seqs][T] rows of draft_stride, fp32 (prob_bf16 = 0) or bf16;
    rows hold vocab_size values in [0, 1] (others are clamped, NaN counts as 0) and need not be normalised.
    draft_probs NULL: a draft without probabilities, q_t one-hot at x_t.  draft_lens int32 [num_seqs]

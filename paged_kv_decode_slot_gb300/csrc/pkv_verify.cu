@@ -10,7 +10,8 @@
 // entries differ by 10^-5 or less, and 32-bit sums, whose order depends on the split, would move those borders.
 // So every weight is split into a multiple of 2^-22 and a multiple of 2^-44 of what is left (the difference
 // p - q with its rounding error first), each summed exactly, as integers.  The sums do not depend on the order, and a
-// weight is off by little more than 2^-45.
+// weight is off by little more than 2^-45.  Where a row's weights add up to less than 2^-8 that may be much of them: the
+// sequence's last CTA then scales the largest weight to [1/2, 1), sums the row once more and draws from that (draw_small).
 //
 // Bound by memory: one row of p, and where a token was refused one row of q.  A row is cut into one run of entries
 // per warp, runs of at least 256 entries; the acceptance is decided by every CTA for itself (a few loads against a second
@@ -20,7 +21,7 @@
 // entry in it.
 //
 // Measured: one sequence (three drafted tokens, 32,000 bf16 entries) 5.7 us, a chain of dependent loads (length, token,
-// probability, row, sums, entry); 64 sequences (four drafted tokens, 128,256 fp32 entries) 15.4 us, that chain around one
+// probability, row, sums, entry); 64 sequences (four drafted tokens, 128,256 fp32 entries) 15.7 us, that chain around one
 // pass over 55 MB in about 8 us.
 #include "pkv_cluster.cuh"
 #include "pkv_device.cuh"
@@ -48,10 +49,13 @@ struct WeightSum {
     static constexpr float kA = 3.f, kB = 3.f / 4194304.f;
     unsigned a = 0, b = 0;
     // p cleaned; q only has to be cleaned from below: min(p, q) takes off what lies above p
-    __device__ __forceinline__ void add(float p, float q)
+    __device__ __forceinline__ void add(float p, float q) { add(p, q, [](float x) { return x; }); }
+    template <typename Scale>
+    __device__ __forceinline__ void add(float p, float q, Scale scale)
     {
         const float m = fminf(p, q);
-        const float d = __fsub_rn(p, m), e = __fsub_rn(__fsub_rn(p, d), m);  // p - m = d + e exactly (p >= m >= 0)
+        float d = __fsub_rn(p, m), e = __fsub_rn(__fsub_rn(p, d), m);  // p - m = d + e exactly (p >= m >= 0)
+        d = scale(d), e = scale(e);
         const float ta = __fadd_rn(d, kA);
         const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(ta, kA)), e);
         a += __float_as_uint(ta);
@@ -250,27 +254,114 @@ __device__ __forceinline__ long long warp_inclusive(long long v)
     return v;
 }
 
-// A sequence's last CTA: the token drawn from the row, -1 where the row has no mass.  sums: the runs' sums in shared
-// memory; every warp looks for the run by itself (no barriers), all threads together for the entry in it.
-template <typename T>
-__device__ __forceinline__ int draw(const VerifyRow<T> &row, const VerifyParams &p, int runs, float sample, const long long *sums,
-                                    long long *warp_sums, int *found)
+// The run that a draw falls into, from the runs' sums in shared memory, for every warp by itself (no barriers).
+struct Place {
+    long long total, bar;  // the row's weights; the draw falls on the first entry whose running sum exceeds bar
+    long long base;        // sum of the runs before this one
+    int run;
+};
+
+// least: no place is looked for where the total is below it (1 at least).
+__device__ __forceinline__ Place find_run(const long long *sums, int runs, float sample, long long least)
 {
-    constexpr int kMine = Pairs<T>::kEntries;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int lane = threadIdx.x & 31;
     // lane's share: per consecutive runs
     const int per = (runs + 31) / 32;
     long long mine = 0;
     for (int x = lane * per; x < min(runs, (lane + 1) * per); ++x) mine += sums[x];
-    const long long upto = warp_inclusive(mine), total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    if (total <= 0) return -1;
+    const long long upto = warp_inclusive(mine);
+    Place at{__shfl_sync(0xFFFFFFFFu, upto, 31), 0, 0, 0};
+    if (at.total < least) return at;
     // the running sum has to exceed r * total, r < 1, so the last entry with weight always does; running sums are whole
     // numbers, so they exceed it where they exceed its floor (below 2^53 units, as those of probabilities are, exact)
-    const long long bar = (long long)floor(fmin(fmax((double)sample, 0.0), 1.0 - 0x1p-53) * (double)total);
-    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, upto > bar)) - 1;
-    long long base = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
-    int run = owner * per;
-    for (; base + sums[run] <= bar; ++run) base += sums[run];
+    at.bar = (long long)floor(fmin(fmax((double)sample, 0.0), 1.0 - 0x1p-53) * (double)at.total);
+    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, upto > at.bar)) - 1;
+    at.base = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+    at.run = owner * per;
+    for (; at.base + sums[at.run] <= at.bar; ++at.run) at.base += sums[at.run];
+    return at;
+}
+
+// Rows whose weights add up to less than 2^-8, where units of 2^-44 are too coarse (they lose a small weight, or all of
+// them): the weights are scaled by a power of two that takes the largest to [1/2, 1) and summed again, run by run into sums
+// and then entry by entry.  All threads call it; -1 where no entry has any weight.  A draw meets such a row about as often
+// as its mass says, so the kernel's registers come first: a call of its own, one entry a thread at a time (a row of 128,256
+// fp32 entries 157 us, 64 of them 215; 32,000 30 us).
+template <typename T>
+__device__ __noinline__ int draw_small(const VerifyRow<T> &row, const VerifyParams &p, int runs, float sample, long long *sums,
+                                       long long *warp_sums, int *found)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto prob = [&](int64_t i) { return clean(prob_at(row.p, i)); };
+    auto other = [&](int64_t i) { return row.q ? fmaxf(prob_at(row.q, i), 0.f) : (i == row.hot ? 1.f : 0.f); };
+    float top = 0.f;
+    for (int64_t i = tid; i < p.V; i += kVerifyThreads) {
+        const float x = prob(i);
+        top = fmaxf(top, __fsub_rn(x, fminf(x, other(i))));
+    }
+    const unsigned bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));  // non-negative numbers order like their bits
+    __syncthreads();
+    if (lane == 0) warp_sums[warp] = bits;
+    __syncthreads();
+    unsigned most = 0;
+#pragma unroll
+    for (int w = 0; w < kVerifyWarps; ++w) most = max(most, (unsigned)warp_sums[w]);
+    if (most == 0) return -1;
+    // 2^up takes the largest weight, 2^-149 at least, to [1/2, 1); in two factors, for it may be 2^148
+    const int up = (most >> 23 ? 126 - (int)(most >> 23) : 117 + __clz((int)most));
+    const float f0 = __uint_as_float((unsigned)(127 + min(up, 100)) << 23), f1 = __uint_as_float((unsigned)(127 + up - min(up, 100)) << 23);
+    auto weight = [&](int64_t i, int64_t end) -> long long {
+        if (i >= end) return 0;
+        WeightSum one;
+        one.add(prob(i), other(i), [&](float x) { return __fmul_rn(__fmul_rn(x, f0), f1); });
+        return one.units(1);
+    };
+    for (int x = warp; x < runs; x += kVerifyWarps) {
+        const int64_t begin = (int64_t)x * p.run, end = min((int64_t)p.V, begin + p.run);
+        long long sum = 0;
+        for (int64_t i = begin; i < end; i += 32) sum += weight(i + lane, end);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) sums[x] = sum;
+    }
+    __syncthreads();
+    Place at = find_run(sums, runs, sample, 1);
+    const int64_t begin = (int64_t)at.run * p.run, end = min((int64_t)p.V, begin + p.run);
+    for (int64_t i0 = begin; i0 < end; i0 += kVerifyThreads) {
+        const long long w = weight(i0 + tid, end), inc = warp_inclusive(w);
+        if (lane == 31) warp_sums[warp] = inc;
+        if (tid == 0) *found = -1;
+        __syncthreads();
+        long long after = at.base + inc, all = 0;
+#pragma unroll
+        for (int y = 0; y < kVerifyWarps; ++y) {
+            after += y < warp ? warp_sums[y] : 0;
+            all += warp_sums[y];
+        }
+        if (after > at.bar && after - w <= at.bar) *found = (int)(i0 + tid);  // one thread
+        __syncthreads();
+        const int token = *found;
+        __syncthreads();
+        if (token >= 0) return token;
+        at.base += all;
+    }
+    return -1;
+}
+
+// A sequence's last CTA: the token drawn from the row, -1 where the row has no mass.  sums: the runs' sums in shared
+// memory; all threads look together for the entry in the run.
+template <typename T>
+__device__ __forceinline__ int draw(const VerifyRow<T> &row, const VerifyParams &p, int runs, float sample, long long *sums,
+                                    long long *warp_sums, int *found)
+{
+    constexpr int kMine = Pairs<T>::kEntries;
+    constexpr long long kSmall = 1ll << 36;  // 2^-8
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Place at_run = find_run(sums, runs, sample, kSmall);
+    if (at_run.total < kSmall) return draw_small(row, p, runs, sample, sums, warp_sums, found);
+    const long long bar = at_run.bar;
+    long long base = at_run.base;
+    const int run = at_run.run;
     // entries of the run, consecutive ones for each thread
     const int64_t begin = (int64_t)run * p.run, end = min((int64_t)p.V, begin + p.run);
     for (int64_t i0 = begin; i0 < end; i0 += kMine * kVerifyThreads) {
