@@ -1447,6 +1447,9 @@ int blocks_attention(const AttnArgs &a, const int32_t *selected, int32_t max_sel
     p.part_out = w.part_out, p.part_lse = w.part_lse, p.counters = w.counters;
     p.err_flag = a.err_flag;
     p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+#ifdef PKV_TEST_HOOKS
+    p.withhold_tile = g_withhold_tile.load(std::memory_order_relaxed);
+#endif
     int sms = 0;
     st = sm_count(&sms);
     if (st != PKV_OK) return st;

@@ -36,6 +36,7 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     constexpr int P = kProducers, S = kFp8 ? kStagesFp8 : (W > 4 ? 2 * kStages : kStages), kThreads = (W + P) * 32;
     static_assert(S % W == 0, "a stage's tiles belong to one warp");
     constexpr int kBatch = S / P / 2;
+    static_assert(S == 2 * P * kBatch, "a producer's stages are two batches");
     using L = AttnLayout<H, S, W, P, kFp8 ? 1 : 2>;
 
     extern __shared__ uint8_t smem_raw[];
@@ -148,7 +149,9 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     } else {
                         valid_of[s] = valid;
                         if constexpr (kFp8) stage_sc[s].x = sc.x, stage_sc[s].y = sc.y;
-                        if (valid > 0) {
+                        if (PKV_TILE_WITHHELD(p, i)) {
+                            // test builds: never loaded, never signalled
+                        } else if (valid > 0) {
                             const uint32_t dst = base_u32 + s * L::kStageBytes;
                             mbar_arrive_expect_tx(bar, L::kStageBytes);
                             if constexpr (kFp8) {
@@ -166,13 +169,21 @@ attn_blocks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         }
                     }
                 }
-                // the tiles issued so far are those before the first refused one; a refused wait ends the producer
-                const unsigned refused = __ballot_sync(0xFFFFFFFFu, !ok);
-                issued += refused ? __ffs(refused) - 1 : min(kBatch, cnt - k);
-                if (refused) {
+                if (__any_sync(0xFFFFFFFFu, !ok)) {
+                    // A refused wait ends the producer.  Lanes before and behind it may have issued their tiles, so each of
+                    // the producer's stages is waited for by a lane: for this batch's tile if it was issued, else for the
+                    // tile that had the stage before.
+                    if (lane < 2 * kBatch) {
+                        const bool now = lane < kBatch && k + lane < cnt && ok;
+                        const int last = k0 + k + lane - (now ? 0 : 2 * kBatch), i = pw + P * last;
+                        if (last >= 0) mbar_wait_bounded(bar_full + 8 * (i % S), (i / S) & 1, nullptr, kDrainLimitNs);
+                    }
+                    __syncwarp();
+                    issued = 0;  // nothing is left to drain
                     aborted = true;
                     break;
                 }
+                issued += min(kBatch, cnt - k);
             }
             cur = nxt;
         }

@@ -99,6 +99,9 @@ struct BlocksParams {
     int32_t *counters;             // [B][K], zero between calls
     int32_t *err_flag;
     uint64_t wait_ns;
+#ifdef PKV_TEST_HOOKS
+    int64_t withhold_tile;         // pkv_debug_withhold_tile: -1, or a tile no CTA loads
+#endif
 };
 
 cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUtensorMap &tv,
