@@ -31,11 +31,15 @@ def start_tensor_args():
     if os.path.exists(ARGS_PATH) and os.path.getmtime(ARGS_PATH) >= max(
             os.path.getmtime(f) for f in (ARGS_SOURCE, os.path.join(INCLUDE, "pkv.h"))):
         return None
-    import torch
-    base, python = os.path.dirname(torch.__file__), sysconfig.get_paths()["include"]
-    if not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
-        print("tensor_args is not built (no g++ or no Python.h): the binding checks its arguments in Python", file=sys.stderr)
+    python = sysconfig.get_paths()["include"]
+    try:  # the library itself needs neither of them
+        import torch
+    except ImportError:
+        torch = None
+    if torch is None or not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
+        print("tensor_args is not built (no torch, no g++ or no Python.h): the binding checks its arguments in Python", file=sys.stderr)
         return None
+    base = os.path.dirname(torch.__file__)
     tmp = ARGS_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(base, "include"),
@@ -84,11 +88,12 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
     variant = out is not None
     out = out or LIB_PATH
     bdir = build_dir or BUILD_DIR
+    fresh = not force and not _stale(out)
+    nvcc = None if fresh else nvcc_path()
     started = None if variant else start_tensor_args()
-    if not force and not _stale(out):
+    if fresh:
         finish_tensor_args(started)
         return out
-    nvcc = nvcc_path()
     os.makedirs(bdir, exist_ok=True)
     common = [nvcc, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC, *[f"-D{d}" for d in defines]]
