@@ -731,12 +731,15 @@ _arg_py, _maybe_py = _arg, _maybe
 _calls = None
 try:  # the same check without the interpreter (csrc/tensor_args.cpp): 0.1 instead of 0.4 us an argument
     from . import tensor_args as _tensor_args
+    from .build import args_built_for as _args_built_for
+    if _tensor_args.built_for != _args_built_for(torch):
+        raise ImportError("tensor_args was built for another Python or torch: " + _tensor_args.built_for)
     _tensor_args.set_refuse(_refuse)
     _arg, _maybe = _tensor_args.arg, _tensor_args.maybe
     # and whole calls: they return None for what is not plain, which the forms below then take or refuse
     _tensor_args.use_library(_lib._handle, lambda stream, dev: _launch(stream, dev))
     _calls = _tensor_args
-except (ImportError, AttributeError):  # not built, or by an older source
+except (ImportError, AttributeError):  # not built, by an older source, or for other headers
     pass
 
 

@@ -22,39 +22,48 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
 ARGS_SOURCE = os.path.join(CSRC, "tensor_args.cpp")
-ARGS_PATH = os.path.join(PKG, "tensor_args.so")
+ARGS_PATH = os.path.join(PKG, "tensor_args" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
-def start_tensor_args():
-    """Start compiling the binding's argument check if it is older than its source; None if there is nothing to
-    do.  It needs the headers of Python and torch; without them the binding checks in Python."""
-    if os.path.exists(ARGS_PATH) and os.path.getmtime(ARGS_PATH) >= max(
-            os.path.getmtime(f) for f in (ARGS_SOURCE, os.path.join(INCLUDE, "pkv.h"))):
-        return None
+def args_built_for(torch) -> str:
+    """The interpreter and the torch whose layouts are compiled into the binding's argument check: it is used with no others."""
+    return (f"python {sys.version.split()[0]} {sysconfig.get_config_var('EXT_SUFFIX')}, torch {torch.__version__} "
+            f"{torch.version.git_version}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def start_tensor_args(force: bool = False):
+    """Start compiling the binding's argument check if it is older than its source or was built for another Python or
+    torch; None if there is nothing to do.  It needs the headers of both; without them the binding checks in Python."""
     python = sysconfig.get_paths()["include"]
     try:  # the library itself needs neither of them
         import torch
     except ImportError:
         torch = None
+    stamp = ARGS_PATH + ".for"
+    if not force and torch is not None and os.path.exists(ARGS_PATH) and os.path.exists(stamp) and open(stamp).read() == args_built_for(
+            torch) and os.path.getmtime(ARGS_PATH) >= max(os.path.getmtime(f) for f in (ARGS_SOURCE, os.path.join(INCLUDE, "pkv.h"))):
+        return None
     if torch is None or not shutil.which("g++") or not os.path.exists(os.path.join(python, "Python.h")):
         print("tensor_args is not built (no torch, no g++ or no Python.h): the binding checks its arguments in Python", file=sys.stderr)
         return None
     base = os.path.dirname(torch.__file__)
     tmp = ARGS_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(base, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DBUILT_FOR="{args_built_for(torch)}"', "-I", os.path.join(base, "include"),
            "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I", python, "-I", INCLUDE, ARGS_SOURCE,
            "-o", tmp, "-L", os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-ldl"]
-    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    return tmp, args_built_for(torch), subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 
 def finish_tensor_args(started) -> None:
     if started is None:
         return
-    tmp, proc = started
+    tmp, built_for, proc = started
     text, _ = proc.communicate()
     if proc.returncode == 0:
         os.replace(tmp, ARGS_PATH)
+        with open(ARGS_PATH + ".for", "w") as f:
+            f.write(built_for)
     else:
         print("tensor_args is not built, the binding checks its arguments in Python:\n" + text.decode(errors="replace")[-2000:],
               file=sys.stderr)
@@ -90,7 +99,7 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
     bdir = build_dir or BUILD_DIR
     fresh = not force and not _stale(out)
     nvcc = None if fresh else nvcc_path()
-    started = None if variant else start_tensor_args()
+    started = None if variant else start_tensor_args(force)
     if fresh:
         finish_tensor_args(started)
         return out

@@ -407,4 +407,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "tensor_args", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_tensor_args() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit_tensor_args()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) != 0) Py_CLEAR(m);  // the binding compares it with what runs
+    return m;
+}

@@ -35,3 +35,57 @@ def test_the_library_builds_without_torch(tmp_path):
     r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH, str(tmp_path)], cwd=ROOT, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "BUILT" in r.stdout, r.stderr[-2000:]
     assert "tensor_args is not built (no torch" in r.stderr
+
+
+def test_the_extension_is_built_for_this_python_and_torch(tmp_path, monkeypatch):
+    """It is built again where its source, Python or torch changed since, or where that is asked for; not otherwise."""
+    import torch
+    from paged_kv_decode_slot_gb300 import build
+    started = []
+
+    class Compiler:
+        returncode = 0
+
+        def __init__(self, cmd, **kw):
+            started.append(cmd)
+            open(cmd[cmd.index("-o") + 1], "wb").close()
+
+        def communicate(self):
+            return b"", None
+    monkeypatch.setattr(build.subprocess, "Popen", Compiler)
+    monkeypatch.setattr(build, "ARGS_PATH", str(tmp_path / "tensor_args.so"))
+
+    def builds(force=False):
+        before = len(started)
+        build.finish_tensor_args(build.start_tensor_args(force))
+        return len(started) > before
+    assert builds() and not builds() and builds(force=True) and not builds()
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert builds() and not builds()
+    assert any("99.0" in arg for arg in started[-1])
+    monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    assert builds() and not builds()
+    monkeypatch.setattr(sys, "version", "4.0.0 (elsewhere)")
+    assert builds() and not builds()
+    source = os.path.getmtime(build.ARGS_SOURCE)
+    os.utime(tmp_path / "tensor_args.so", (source - 9, source - 9))
+    assert builds() and not builds()
+
+
+ANOTHER_TORCH = """
+from paged_kv_decode_slot_gb300 import build
+build.build_library()
+from paged_kv_decode_slot_gb300 import tensor_args
+real = build.args_built_for
+import torch
+assert tensor_args.built_for == real(torch)
+build.args_built_for = lambda torch: real(torch) + " of another day"
+from paged_kv_decode_slot_gb300 import binding
+assert binding._calls is None and binding._arg is binding._arg_py and binding._maybe is binding._maybe_py
+print("PYTHON")
+"""
+
+
+def test_an_extension_built_for_others_is_not_used():
+    r = subprocess.run([sys.executable, "-c", ANOTHER_TORCH], cwd=ROOT, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and "PYTHON" in r.stdout, r.stderr[-2000:]
