@@ -11,11 +11,16 @@ ImportError (there is no fallback path).
 """
 
 
+_binding = None
+
+
 def __getattr__(name):
+    global _binding
     if name.startswith(("pkv_", "PKV_")) or name in ("BLOCK_SIZE", "CacheDesc", "PkvError", "cache_desc",
                                                     "check", "library", "max_partitions_for", "tapered_partitions_for", "IN_KERNEL_MERGE_WEIGHTS",
                                                     "split_attention_launches", "multi_attention_launches"):
-        from . import binding
-        globals()[name] = value = getattr(binding, name)  # found without this function from now on
-        return value
+        if _binding is None:  # an import statement takes longer than the call it is for
+            from . import binding
+            _binding = binding
+        return getattr(_binding, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -89,3 +89,17 @@ print("PYTHON")
 def test_an_extension_built_for_others_is_not_used():
     r = subprocess.run([sys.executable, "-c", ANOTHER_TORCH], cwd=ROOT, capture_output=True, text=True, timeout=900)
     assert r.returncode == 0 and "PYTHON" in r.stdout, r.stderr[-2000:]
+
+
+def test_the_package_gives_what_the_binding_has_now(monkeypatch):
+    """An entry point replaced in the binding (a wrapper, a stand-in) is seen through the package, used before or not."""
+    from paged_kv_decode_slot_gb300.build import build_library
+    build_library()
+    import paged_kv_decode_slot_gb300 as pkv
+    from paged_kv_decode_slot_gb300 import binding
+    before = pkv.pkv_verify_draft
+    assert before is binding.pkv_verify_draft
+    monkeypatch.setattr(binding, "pkv_verify_draft", len)
+    assert pkv.pkv_verify_draft is len
+    monkeypatch.undo()
+    assert pkv.pkv_verify_draft is before
