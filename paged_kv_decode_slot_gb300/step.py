@@ -129,15 +129,19 @@ def plan_blocks_attention(num_seqs: int, num_kv_heads: int, max_selected: int, n
       * a handful of very long lists: partitions as ``plan_attention`` sizes them, which merge through the
         workspace (2 lists of 1,024 blocks: 11.8, as clusters of 16 13.0);
       * more lists: one CTA a list (128 lists of 128 blocks 25.1, in halves 26.3), up to 128 blocks a list
-        where there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 305, whole 344)."""
+        where there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 305, whole 344).
+    A list is cut into no more partitions than the in-kernel merge takes for eight query heads a KV head (it has no
+    other): 1,024, so lists of more than 131,072 blocks get longer ones."""
     units = num_seqs * num_kv_heads
     room = 3 * num_sms // units if units > 0 else 0
     if max_selected <= 8 or (room < 4 and (units < num_sms or max_selected <= LONG_PARTITION_BLOCKS)):
         return AttentionPlan("single", 0, 1)
     if room < 4 or (units < 8 and max_selected > 512):
-        return plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False)
-    most = min(room, 12 if max_selected <= 256 else 16)
-    partition_blocks = max(4, -(-max_selected // most))
+        partition_blocks = plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False).partition_blocks
+        partition_blocks = max(partition_blocks, -(-max_selected * 8 // B.IN_KERNEL_MERGE_WEIGHTS))
+    else:
+        most = min(room, 12 if max_selected <= 256 else 16)
+        partition_blocks = max(4, -(-max_selected // most))
     return AttentionPlan("split", partition_blocks, B.max_partitions_for(max_selected, partition_blocks))
 
 

@@ -103,3 +103,18 @@ def test_the_package_gives_what_the_binding_has_now(monkeypatch):
     assert pkv.pkv_verify_draft is len
     monkeypatch.undo()
     assert pkv.pkv_verify_draft is before
+
+
+def test_plans_of_any_list_are_calls_that_the_library_takes():
+    """Partitions of selected-block lists cover them and fit the merge for every group of query heads that attention takes."""
+    from paged_kv_decode_slot_gb300.build import build_library
+    build_library()
+    from paged_kv_decode_slot_gb300 import binding
+    from paged_kv_decode_slot_gb300.step import plan_blocks_attention
+    for seqs in (1, 2, 5, 8, 20, 64, 1000, 65535):
+        for heads in (1, 2, 8, 40):
+            for most in (1, 8, 9, 128, 250, 513, 1000, 16384, 131072, 131073, 1 << 20, 1 << 26):
+                p = plan_blocks_attention(seqs, heads, most, 152)
+                if p.mode == "split":
+                    assert p.partition_blocks * p.max_partitions >= most > p.partition_blocks * (p.max_partitions - 1)
+                    assert 8 * p.max_partitions <= binding.IN_KERNEL_MERGE_WEIGHTS, (seqs, heads, most)
