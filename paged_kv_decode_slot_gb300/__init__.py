@@ -11,16 +11,29 @@ ImportError (there is no fallback path).
 """
 
 
-_binding = None
+import types
+
+_OTHERS = ("BLOCK_SIZE", "CacheDesc", "PkvError", "cache_desc", "check", "library", "max_partitions_for",
+           "tapered_partitions_for", "IN_KERNEL_MERGE_WEIGHTS", "split_attention_launches", "multi_attention_launches")
+
+
+class _Binding(types.ModuleType):
+    """The binding, once it is loaded: a name that is replaced in it is replaced here too."""
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name in globals() and _of_the_binding(name):
+            globals()[name] = value
+
+
+def _of_the_binding(name):
+    return name.startswith(("pkv_", "PKV_")) or name in _OTHERS
 
 
 def __getattr__(name):
-    global _binding
-    if name.startswith(("pkv_", "PKV_")) or name in ("BLOCK_SIZE", "CacheDesc", "PkvError", "cache_desc",
-                                                    "check", "library", "max_partitions_for", "tapered_partitions_for", "IN_KERNEL_MERGE_WEIGHTS",
-                                                    "split_attention_launches", "multi_attention_launches"):
-        if _binding is None:  # an import statement takes longer than the call it is for
-            from . import binding
-            _binding = binding
-        return getattr(_binding, name)
+    if _of_the_binding(name):
+        from . import binding
+        binding.__class__ = _Binding
+        globals()[name] = value = getattr(binding, name)  # found without this function from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

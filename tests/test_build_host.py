@@ -103,6 +103,10 @@ def test_the_package_gives_what_the_binding_has_now(monkeypatch):
     assert pkv.pkv_verify_draft is len
     monkeypatch.undo()
     assert pkv.pkv_verify_draft is before
+    monkeypatch.setattr(binding, "_f32", binding._f32)          # what the package does not offer stays the binding's
+    assert not hasattr(pkv, "_f32") and not hasattr(pkv, "pkv_nothing")
+    from paged_kv_decode_slot_gb300 import step                 # another module's names are its own
+    assert pkv.step is step and not hasattr(pkv, "SparseDecodeStep")
 
 
 def test_plans_of_any_list_are_calls_that_the_library_takes():
