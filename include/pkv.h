@@ -558,7 +558,8 @@ int pkv_key_bounds_fp8(const uint8_t *k_cache, const float *k_scale, int32_t sca
 size_t pkv_select_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq);
 
 /* The blocks each (sequence, KV head) attends to.  score(b, kvh, j) = the largest, over the G query heads
-   of KV head kvh, of sum_h max(q_h lo_jh, q_h hi_jh): no q . k of block j exceeds it.  selected int32
+   of KV head kvh, of sum_h max(q_h lo_jh, q_h hi_jh): no q . k of block j exceeds it (bounds of an e4m3 pool are
+   rounded to the nearest: there by no more than 1/254 of sum_h |q_h| times the bound's magnitude).  selected int32
    [num_seqs][K][max_selected] receives logical block indices in ascending order: all of a sequence's blocks
    if it has no more than max_selected; else its first first_blocks and last last_blocks blocks, which need
    no bounds, and the best scored of the others, max_selected in all -- exactly those that the scores choose,

@@ -109,3 +109,30 @@ def test_finite_scores_beside_infinite_ones_and_at_the_ends_of_the_range(pkv):
     q[..., 9] = 0.0
     check(pkv, q, bounds, tab, CTX, 12)
     check(pkv, q, bounds, tab, CTX, 60)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_no_logit_exceeds_its_blocks_score(pkv, kv):
+    """Scores of the bounds that the library wrote against the keys' products: bf16 bounds bound them; e4m3 bounds, half a step
+    of bf16 and a rounding to fp32 off, up to 1/254 of sum |q| |bound|."""
+    r = np.random.default_rng(5)
+    K, H, ctx = 2, 128, [16 * 40, 333]
+    tab, pool = R.tables(r, ctx)
+    bounds = torch.zeros(pool, K, 2, H, dtype=torch.bfloat16, device="cuda")
+    if kv == "bf16":
+        k = R.to_bf16(r.standard_normal((pool, 16, K, H)))
+        keys = R.bf16_values(k)
+        pkv.check(pkv.pkv_key_bounds(bf16_dev(k), i32_dev(tab), i32_dev(ctx), 640, bounds))
+    else:
+        k = (r.integers(0, 0x70, (pool, 16, K, H)) | r.integers(0, 2, (pool, 16, K, H)) << 7).astype(np.uint8)
+        scale = r.uniform(0.01, 0.1, (pool, K)).astype(np.float32)
+        keys = R.e4m3_table()[k] * scale.astype(np.float64)[:, None, :, None]
+        pkv.check(pkv.pkv_key_bounds_fp8(torch.from_numpy(k).cuda(), torch.from_numpy(scale).cuda(), i32_dev(tab), i32_dev(ctx), 640, bounds))
+    box, q = bounds.double().cpu().numpy(), R.bf16_values(R.to_bf16(r.standard_normal((K, 3, H))))
+    for b, c in enumerate(ctx):
+        for j in range(-(-c // 16)):
+            rows, (lo, hi) = keys[tab[b, j], :min(16, c - 16 * j)], box[tab[b, j]].transpose(1, 0, 2)
+            for h in range(K):
+                score = np.where(q[h] > 0, q[h] * hi[h], q[h] * lo[h]).sum(-1)
+                slack = 1e-12 if kv == "bf16" else (np.abs(q[h]) * np.where(q[h] > 0, np.abs(hi[h]), np.abs(lo[h]))).sum(-1) / 254
+                assert np.all((rows[:, h] @ q[h].T).max(0) <= score + slack)
