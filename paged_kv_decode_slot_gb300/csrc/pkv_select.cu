@@ -242,6 +242,8 @@ __device__ __forceinline__ void warp_range(Key &mn, Key &mx)
 // themselves: the scores of one query lie within a few powers of two and spread over the bins, so shared-memory
 // atomics seldom meet, and one pass nearly always leaves few enough keys to rank them pairwise.  A thread only asks for
 // the keys i = tid mod NT; a barrier has to lie between this and whatever used s before.
+// Keys that change on the way (another stream writing the workspace, against the rules) make the result meaningless, but
+// the passes are counted, places are checked and the call ends.
 template <int NT, typename Key, typename F>
 __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F key, Key mn, Key mx, uint32_t &above)
 {
@@ -264,7 +266,8 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
     }
     Key lo = (Key)all_lo, hi = (Key)all_hi;
     uint32_t up = 0, inside = (uint32_t)n;  // keys above hi, keys in [lo, hi]
-    while (lo < hi && inside > kFew) {
+    constexpr int kPasses = (8 * (int)sizeof(Key) + kBinBits - 1) / kBinBits;
+    for (int pass = 0; pass < kPasses && lo < hi && inside > kFew; ++pass) {
         const int bits = 64 - __clzll((long long)(unsigned long long)(hi - lo));
         const int shift = max(0, bits - kBinBits);
 #pragma unroll 4
@@ -314,9 +317,13 @@ __device__ __forceinline__ Key kth_largest(SelectShared &s, int n, uint32_t k, F
 #pragma unroll 4
         for (int i = tid; i < n; i += NT) {
             const Key x = key(i);
-            if (x >= lo && x <= hi) s.few[atomicAdd(&s.few_n, 1u)] = (unsigned long long)x;
+            if (x >= lo && x <= hi) {
+                const uint32_t at = atomicAdd(&s.few_n, 1u);
+                if (at < kFew) s.few[at] = (unsigned long long)x;
+            }
         }
         __syncthreads();
+        inside = min(inside, (uint32_t)kFew);
         if (tid < (int)inside) {
             const Key x = (Key)s.few[tid];
             uint32_t more = up, same = 0;
@@ -355,7 +362,7 @@ __device__ __forceinline__ double exact_sum(const int (&m)[E], const int (&at)[E
     unsigned under = 0, best_under = 0;       // the digit below them
     bool lost, best_lost = false;             // anything below that one
     int top = -1;
-    for (;;) {
+    for (int turn = 0; turn < 2; ++turn) {
         int carry = 0;
         lost = false, window = 0, under = 0, top = -1;
         for (int i = from; i <= to; ++i) {
@@ -375,7 +382,7 @@ __device__ __forceinline__ double exact_sum(const int (&m)[E], const int (&at)[E
             if (digit) best = window, best_under = under, best_lost = lost, top = i;
         }
         if (carry >= 0) break;
-        sign = -1;  // a negative sum: once more with the signs turned round
+        if (turn == 0) sign = -1;  // a negative sum: once more with the signs turned round
     }
     if (top < 0) return 0.0;
     const int lead = __clzll((long long)best);  // below 16
@@ -659,8 +666,9 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     write_run<NT, kKept>(nb, cls, 1, c, list, c.all[1]);
     __syncthreads();
     double *exact = m <= kRankMost ? s.exact : p.exact + unit * p.max_nb;
+    auto listed = [&](int a) { return min(max(list[a], 0), nb - 1); };  // (a list in the workspace is not taken on trust)
     for (int a = warp; a < m; a += (NT / 32)) {
-        const double x = exact_score<H, (NT > 256)>(p, b, kvh, list[a], lane);
+        const double x = exact_score<H, (NT > 256)>(p, b, kvh, listed(a), lane);
         if (lane == 0) exact[a] = x;
     }
     __syncthreads();
@@ -696,8 +704,8 @@ __device__ __forceinline__ void choose(SelectShared &s, uint32_t *keep, const Se
     }
     // a decided block's key becomes the largest or the smallest there is
     auto decide = [&](int a, bool in) {
-        if constexpr (kKept) keep[list[a]] = in ? ~0u : 0u;
-        else scores[list[a]] = in ? INFINITY : -INFINITY;
+        if constexpr (kKept) keep[listed(a)] = in ? ~0u : 0u;
+        else scores[listed(a)] = in ? INFINITY : -INFINITY;
     };
     if (m <= kRankMost) {
         for (int a = tid; a < m; a += NT) {
@@ -760,7 +768,13 @@ __device__ __forceinline__ int score_tiles(const SelectParams &p, int b)
     return nb > p.M ? (nb + 15) / 16 : 0;
 }
 
-// A warp's place in the list of tiles, ordered (sequence, tile, KV head).
+// Blocks of a sequence that the table has room for.
+__device__ __forceinline__ int score_blocks(const SelectParams &p, int b)
+{
+    return min((__ldg(p.context_lens + b) + kBlockSize - 1) / kBlockSize, p.max_nb);
+}
+
+// A warp's place in the list of tiles, ordered (sequence, tile, KV head); b = p.B behind the last one.
 struct TileAt {
     int b, tile, kvh, tiles;
     // kScoreWarps entries on, without a division: by_tile and by_kvh are kScoreWarps / K and the remainder
@@ -810,11 +824,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     const int64_t begin = blockIdx.x * share, end = min(total, begin + share);
     const int n = end - begin > warp ? (int)((end - begin - warp + kScoreWarps - 1) / kScoreWarps) : 0;
     if (n == 0) return;
-    TileAt load_at{0, 0, 0, 0};
+    TileAt load_at{p.B, 0, 0, 0};
     const int by_tile = kScoreWarps / p.K, by_kvh = kScoreWarps - by_tile * p.K;
     {
         int64_t before = 0;  // the sequence that holds entry `begin`
-        for (int b0 = 0;; b0 += 32) {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int t = score_tiles(p, b0 + lane);
             int64_t inc = (int64_t)t * p.K;
 #pragma unroll
@@ -843,11 +857,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     bool scored[2];
     uint32_t bad = 0;  // of each stage's two rows: the id is outside the pool
     auto look_up = [&](const TileAt &at) {
+        const int nb = at.b < p.B ? score_blocks(p, at.b) : 0;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int j = at.tile * 16 + r + 8 * x;
             // forced blocks are selected without a score, and their bounds need not be up to date
-            const int nb = (__ldg(p.context_lens + at.b) + kBlockSize - 1) / kBlockSize;
             scored[x] = j >= p.first && j < nb - p.last;
             blk[x] = scored[x] ? __ldg(p.block_tables + (size_t)at.b * p.max_nb + j) : -1;
         }
@@ -886,10 +900,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
     uint32_t qf[2][V][4];  // fragments of min(q, 0) and max(q, 0)
     for (int i = 0; i < n; ++i) {
         advance();
+        if (use_at.b >= p.B) break;  // (lengths that changed since they were counted)
         const int tile = use_at.tile, kvh = use_at.kvh;
         if (use_at.b != q_b || kvh != q_kvh) {
             q_b = use_at.b, q_kvh = kvh;
-            nb = (__ldg(p.context_lens + q_b) + kBlockSize - 1) / kBlockSize;
+            nb = score_blocks(p, q_b);
             const bool live = r < p.G;
             const uint16_t *qrow = p.q + ((size_t)q_b * p.N + (size_t)q_kvh * p.G + (live ? r : 0)) * H + 8 * m;
 #pragma unroll
@@ -951,6 +966,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const Se
         if (lane == 0) p.tile_max[unit * p.tiles + tile] = mb;
         if (i + 1 < n) use_at.next(p, by_tile, by_kvh);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int H, int NT>
@@ -959,12 +975,17 @@ __global__ void __launch_bounds__(NT, NT > 256 ? 1 : 4) choose_blocks_kernel(con
     __shared__ SelectShared s;
     extern __shared__ uint32_t keep[];  // [min(max_nb, kKeep)]
     const int kvh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int ctx = p.context_lens[b];
-    if (ctx < 0 || ctx > p.max_nb * kBlockSize) {
-        if (tid == 0 && kvh == 0) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
-        ctx = 0;
+    __shared__ int blocks;
+    if (tid == 0) {  // one thread's word for all, as the CTA's barriers depend on it
+        int ctx = p.context_lens[b];
+        if (ctx < 0 || ctx > p.max_nb * kBlockSize) {
+            if (kvh == 0) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+            ctx = 0;
+        }
+        blocks = (ctx + kBlockSize - 1) / kBlockSize;
     }
-    const int nb = (ctx + kBlockSize - 1) / kBlockSize;
+    __syncthreads();
+    const int nb = blocks;
     if (nb <= p.M) {  // every block is selected
         int32_t *sel = p.selected + ((size_t)b * p.K + kvh) * p.M;
         for (int x = tid; x < p.M; x += NT) sel[x] = x < nb ? x : -1;
