@@ -346,11 +346,13 @@ cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUt
     const int64_t lists = (int64_t)p.B * p.K;
     const bool wide = p.max_parts == 1 && (fp8 || H == 64 ? lists <= 2 * sms || lists > 3 * sms : lists <= sms);
     // A list's partitions as one cluster, which joins their partials in shared memory, where they all run at once (8 lists of
-    // 128 in 16-block partitions 6.3 us, through the workspace 8.5; 64 lists of 250 in 42-block ones 25.7) or are two (512
-    // lists of 128 84.3 and 86.6); larger clusters start late in a grid of several waves (512 lists in 16-block ones 108, not
-    // as clusters 96).
+    // 128 in 11-block partitions 6.7 us, through the workspace 8.4; 64 lists of 250 in 42-block ones 26.5 and 28.7) or are two
+    // (512 lists of 128 94.3 and 96.8); larger clusters start late in a grid of several waves (512 lists in 16-block ones 122, not
+    // as clusters 106).  A cluster's CTAs share a group of SMs, so not all of three CTAs per SM are to be had: of 456, 435 to 456
+    // in clusters of up to 6, 396 to 432 in ones of up to 12, 336 to 390 in ones of up to 16.
+    const int fit = p.max_parts <= 6 ? 95 : (p.max_parts <= 12 ? 86 : 73);  // per cent
     const bool cluster = p.max_parts > 1 && p.max_parts <= kClusterMost &&
-                         (p.max_parts == 2 || (int64_t)p.B * p.K * p.max_parts <= (int64_t)PKV_CTAS_PER_SM * sms);
+                         (p.max_parts == 2 || lists * p.max_parts * 100 <= (int64_t)PKV_CTAS_PER_SM * sms * fit);
     if (cluster) {
         if (fp8) return launch_t<128, true, 4, true>(tk, tv, p, stream);
         return H == 128 ? launch_t<128, false, 4, true>(tk, tv, p, stream) : launch_t<64, false, 4, true>(tk, tv, p, stream);

@@ -123,13 +123,15 @@ def plan_attention(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int, nu
 def plan_blocks_attention(num_seqs: int, num_kv_heads: int, max_selected: int, num_sms: int) -> AttentionPlan:
     """Partitions of the selected-block lists for pkv_decode_attn_blocks.  Measured on GB300, us:
       * (sequence, KV head) lists that leave room for four partitions or more each in one wave of three CTAs
-        per SM: as many as fit, up to 12 (16 for lists beyond 256 blocks) and of 4 blocks at least; they merge
-        inside a cluster (8 lists of 128: 6.0, whole 13.1; 64 lists of 250: 25.7, whole 32.4; 96 of 250: 35.2
-        and 36.7; 8 of 1,024: 18.8);
+        per SM: as many as run at once, up to 12 (16 for lists beyond 256 blocks) and of 4 blocks at least; they
+        merge inside a cluster (8 lists of 128: 6.7, whole 14.8; 64 lists of 250 in 6: 25.7, whole 33.9; 96 of 250
+        in 4: 34.8 and 37.0; 8 of 1,024: 20.4).  A cluster's CTAs share a group of SMs, so fewer fit than three per SM:
+        of 456, 435 to 456 in clusters of up to 6, 396 to 432 up to 12, 336 to 390 up to 16; clusters beyond
+        that wait for a second wave (64 lists of 250 in 7: 34.5, 40 in 11: 26.5, in 9: 18.7);
       * a handful of very long lists: partitions as ``plan_attention`` sizes them, which merge through the
-        workspace (2 lists of 1,024 blocks: 11.8, as clusters of 16 13.0);
-      * more lists: one CTA a list (128 lists of 128 blocks 25.1, in halves 26.3), up to 128 blocks a list
-        where there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 305, whole 344).
+        workspace (2 lists of 4,096 blocks: 38.2, as clusters of 16 56.0; of 1,024 16.0 either way);
+      * more lists: one CTA a list (128 lists of 128 blocks 25.8, in halves 27.2), up to 128 blocks a list
+        where there are as many lists as SMs; longer ones in 128-block partitions (512 lists of 500: 315, whole 364).
     A list is cut into no more partitions than the in-kernel merge takes for eight query heads a KV head (it has no
     other): 1,024, so lists of more than 131,072 blocks get longer ones."""
     units = num_seqs * num_kv_heads
@@ -140,7 +142,8 @@ def plan_blocks_attention(num_seqs: int, num_kv_heads: int, max_selected: int, n
         partition_blocks = plan_attention(num_seqs, num_kv_heads, max_selected, num_sms, taper=False).partition_blocks
         partition_blocks = max(partition_blocks, -(-max_selected * 8 // B.IN_KERNEL_MERGE_WEIGHTS))
     else:
-        most = min(room, 12 if max_selected <= 256 else 16)
+        most = max(n for n in range(2, min(room, 12 if max_selected <= 256 else 16) + 1)
+                   if units * n * 100 <= 3 * num_sms * (95 if n <= 6 else 86 if n <= 12 else 73) or n == 2)
         partition_blocks = max(4, -(-max_selected // most))
     return AttentionPlan("split", partition_blocks, B.max_partitions_for(max_selected, partition_blocks))
 

@@ -122,3 +122,15 @@ def test_plans_of_any_list_are_calls_that_the_library_takes():
                 if p.mode == "split":
                     assert p.partition_blocks * p.max_partitions >= most > p.partition_blocks * (p.max_partitions - 1)
                     assert 8 * p.max_partitions <= binding.IN_KERNEL_MERGE_WEIGHTS, (seqs, heads, most)
+
+
+def test_clusters_of_a_plan_run_at_once():
+    """CTAs of three per SM that fit in clusters of a size on 152 SMs (cudaOccupancyMaxActiveClusters on a GB300)."""
+    from paged_kv_decode_slot_gb300.build import build_library
+    build_library()
+    from paged_kv_decode_slot_gb300.step import plan_blocks_attention
+    fit = {1: 456, 2: 228, 3: 148, 4: 110, 5: 87, 6: 74, 7: 59, 8: 51, 9: 46, 10: 43, 11: 36, 12: 36, 13: 28, 14: 26, 15: 26, 16: 21}
+    for units in range(1, 115):
+        for most in (9, 40, 128, 250, 257, 500, 512):
+            p = plan_blocks_attention(units, 1, most, 152)
+            assert p.mode == "split" and fit[p.max_partitions] >= units, (units, most, p)
