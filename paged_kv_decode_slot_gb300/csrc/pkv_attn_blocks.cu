@@ -339,10 +339,10 @@ cudaError_t launch_attn_blocks(int H, bool fp8, const CUtensorMap &tk, const CUt
 {
     // Eight consumer warps and sixteen stages instead of four (and eight in bf16) where one CTA takes a whole list.  Tiles of
     // 4 KB (e4m3, H = 64) leave room for two such CTAs per SM, or three of four warps: four only where all lists then run at
-    // once and otherwise would not (64 * 8 e4m3 lists of 128 blocks 63.6 -> 54.3 us, bf16 H = 64 62.6 -> 50.0; but 46 * 8 lists
-    // 48.4 with eight, 42.2 with four, and 43.8 and 35.9).  Tiles of 8 KB leave room for one: while there is one list per SM
-    // at most (16 * 8 lists of 128: 30.4 -> 25.9; 64 * 8 lists: 85.4 and 86.0).  CTAs of a cut list are short and many: four
-    // warps (2 * 160 e4m3 parts of 125 blocks 46.3, with eight 52.4).
+    // once and otherwise would not (64 * 8 e4m3 lists of 128 blocks 74.1 -> 58.4 us, bf16 H = 64 63.4 -> 50.5; but 46 * 8 lists
+    // 49.1 with eight, 46.1 with four, and 44.5 and 36.1).  Tiles of 8 KB leave room for one: while there is one list per SM
+    // at most (16 * 8 lists of 128: 31.2 -> 25.6; 64 * 8 lists: 99.7 and 98.0).  CTAs of a cut list are short and many: four
+    // warps (2 * 160 e4m3 parts of 125 blocks 46.1, with eight 51.9).
     const int64_t lists = (int64_t)p.B * p.K;
     const bool wide = p.max_parts == 1 && (fp8 || H == 64 ? lists <= 2 * sms || lists > 3 * sms : lists <= sms);
     // A list's partitions as one cluster, which joins their partials in shared memory, where they all run at once (8 lists of

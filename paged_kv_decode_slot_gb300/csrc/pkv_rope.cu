@@ -19,10 +19,13 @@
 // registers and the arithmetic (the e4m3 form's quotients above all) has enough warps; results go straight to global
 // memory.  A token whose slot is negative is left out: nothing of its rows is written.
 //
-// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 33.5 us (6.0 TB/s, 88% of the measured
-// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 50.5 us (5.1 TB/s, 75%): bound by issue
-// slots (68% busy; the check of the quotients takes 7 us; 28 of 32 lanes are busy, and an order of the items that put
-// turned and copied ones into warps of their own cost 3 us).  64 decode tokens: 2.8 us, a launch and four dependent loads.
+// Measured: 8,192 tokens of 32 query and 8 KV heads of 128 in bf16, 201 MB, 33.6 us (6.0 TB/s, 88% of the measured
+// copy bandwidth); 5,001 tokens of 40 and 40 into e4m3, interleaved, 256 MB, 50.7 us (5.0 TB/s, 74%): neither DRAM (50%
+// in a cold run) nor the issue slots (67%) are full, warps wait most for the CTA's barrier at the end of each unit (the check
+// of the quotients takes 7 us; 28 of 32 lanes are busy, and an order of the items that put turned and copied ones into
+// warps of their own cost 3 us).  64 decode tokens: 2.8 us, a launch and four dependent loads.  A unit holds heads of one
+// token only, so few heads leave most threads and most of a stage empty: 8,192 tokens of 4 and 1 heads, 25 MB, 17.6 us
+// (21% of the copy bandwidth), of 8 and 2 21.4.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_ops.h"
@@ -32,14 +35,15 @@ namespace pkv {
 // Threads, heads of a unit, stages and CTAs per SM, measured on 8,192 tokens of 32 + 2 * 8 heads (bf16) and 5,001 of
 // 40 + 2 * 40 (e4m3) with an earlier form of the arithmetic: 256 / 64 / 2 / 4 34.8 and 55.0 us; 192 / 48 / 3 / 5 34.6 and
 // 60.1 (three units a token instead of two); 192 / 48 / 2 / 6 36.1 and 68.6; 128 / 32 / 3 / 8 46.2 and 64.2; 384 / 96 / 2 / 3
-// 42.8 and 83.4.
+// 42.8 and 83.4.  (48 and 120 heads are what they were chosen on.)
 constexpr int kRopeThreads = 256;
 constexpr int kUnitHeads = 64;
 constexpr int kRopeStages = 2;
 constexpr int kRopeCtasPerSm = 4;
 constexpr double kInv2Pi = 0.15915494309189533577;
 
-// Two fp32 operations at a time (add, mul and fma on f32x2, sm_100 and later): the kernel is bound by issue slots.
+// Two fp32 operations at a time (add, mul and fma on f32x2, sm_100 and later): the e4m3 form
+// took 57.8 us with single ones, 53.9 with pairs.
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair(float lo, float hi)
 {

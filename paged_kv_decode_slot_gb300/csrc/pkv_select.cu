@@ -12,8 +12,8 @@
 // order of its fp32 sums alone.
 //
 // Two launches, the second started early (programmatic serialization): scores into the workspace, then one CTA per
-// (sequence, KV head) chooses.  64 sequences of 8K to 32K tokens, 8 KV heads, 128 blocks each: 70 us, of which the scores,
-// bound by memory, 57 for 336 MB (5.9 TB/s, 87% of the measured copy bandwidth); one sequence of 32K tokens: 9.0 us, the
+// (sequence, KV head) chooses.  64 sequences of 8K to 32K tokens, 8 KV heads, 128 blocks each: 71 us, of which the scores,
+// bound by memory, 57 for 336 MB (5.9 TB/s, 87% of the measured copy bandwidth); one sequence of 32K tokens: 9.1 us, the
 // latency of a tile's loads (3.5) and of the choice's barriers and passes over shared memory (5.5).
 //
 // Selection.  The first F and the last L blocks, and the best of the rest, M in all, in ascending order:
@@ -32,7 +32,9 @@ namespace pkv {
 // One CTA per block that holds new tokens, one thread per 16-byte column of its [K][H] rows: all 16 rows are
 // loaded at once (independent loads), rows past the context are left out.  One pass over the keys,
 // bound by memory: 16 prompts of 512 to 8,192 tokens (8 heads of 128, 161 MB) 27.2 us, 5.9 TB/s, 87% of the measured copy
-// bandwidth; the newest block of 64 sequences in e4m3 2.4 us, a launch and two dependent loads.
+// bandwidth; the newest block of 64 sequences in e4m3 2.4 us, a launch and two dependent loads.  Threads without a column
+// idle: half of them in e4m3 (the same prompts 23.5 us, 56%), seven in eight for one head of 128 in bf16 (9.0 us for an eighth of
+// the bytes, 33%; e4m3 10.3).
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b)
 {
     const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
@@ -800,7 +802,9 @@ struct TileAt {
 // shared memory: a tile's bounds are 4 H bytes a block (8 KB at H = 128), copied asynchronously one tile ahead, the
 // block ids one tile further ahead.  The product's depth may be taken in any order, so a lane's 16-byte vectors are its k indices:
 // each lane copies exactly what it reads back as mma fragments, and the ring needs no barrier.  Bound by memory:
-// eight warps with a tile or two each in flight are 64 to 128 KB per SM.
+// eight warps with a tile or two each in flight are 64 to 128 KB per SM.  A warp whose tiles are all of one head (K divides 8)
+// loads its queries once a sequence, others with every tile: 64 sequences of 8K to 32K tokens take 43 us with 4 heads, 50
+// with 5, 71 with 8 and 86 with 10, 57, 62, 70 and 72% of the copy bandwidth.
 template <int H>
 __global__ void __launch_bounds__(kScoreThreads, 1) score_blocks_kernel(const SelectParams p)
 {
@@ -1029,9 +1033,9 @@ static cudaError_t launch_select_t(const SelectParams &p, int sms, cudaStream_t 
     static_assert(sizeof(SelectShared) + sizeof(uint32_t) * kKeep <= 48 * 1024, "no opt-in to larger shared memory");
     const size_t keep = sizeof(uint32_t) * (size_t)(p.max_nb < kKeep ? p.max_nb : kKeep);
     const dim3 units(p.K, p.B);
-    // Threads of a choosing CTA: 256 where the batch's CTAs share the SMs (64 * 8 units of up to 2,048 blocks: 75.6 us
-    // for the whole selection, 80.5 with 512), 512 where there are fewer units than SMs (8 units of 2,048 blocks: 11.0,
-    // 11.7 with 256).
+    // Threads of a choosing CTA: 256 where the batch's CTAs share the SMs (64 * 8 units of up to 2,048 blocks: 70.2 us
+    // for the whole selection, 82.4 with 512), 512 where there are fewer units than SMs (18 * 8 units of up to 2,048: 28.4,
+    // 30.2 with 256; 8 * 8 of 2,048 23.3 and 25.6; 8 of 2,048 alike).
     if ((int64_t)p.K * p.B < sms) return launch_kernel(choose_blocks_kernel<H, 512>, units, dim3(512), keep, stream, true, p);
     return launch_kernel(choose_blocks_kernel<H, 256>, units, dim3(256), keep, stream, true, p);
 }

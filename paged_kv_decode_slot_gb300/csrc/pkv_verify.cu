@@ -20,7 +20,7 @@
 // sequence to finish takes the sums from the workspace.  It adds them up, finds the run that the draw falls into and the
 // entry in it.
 //
-// Measured: one sequence (three drafted tokens, 32,000 bf16 entries) 5.7 us, a chain of dependent loads (length, token,
+// Measured: one sequence (three drafted tokens, 32,000 bf16 entries) 5.7 us (5.6 to 5.8), a chain of dependent loads (length, token,
 // probability, row, sums, entry); 64 sequences (four drafted tokens, 128,256 fp32 entries) 15.7 us, that chain around one
 // pass over 55 MB in about 8 us.
 #include "pkv_cluster.cuh"
@@ -477,9 +477,9 @@ cudaError_t launch_verify(VerifyParams p, bool bf16, int sms, cudaStream_t strea
     const int want = (4 * sms + p.B - 1) / p.B;
     int ctas = want < most ? want : most;
     if (ctas > kVerifyRuns / kVerifyWarps) ctas = kVerifyRuns / kVerifyWarps;
-    // A cluster per sequence where that is one CTA per SM at most and 16,384 entries a CTA: 1 sequence of 128,256 entries 5.8 us,
-    // through the workspace (63 CTAs) 7.5; 4: 6.2 and 9.4; 16: 8.7 and 9.5; 64 of 32,000: 7.9 and 9.4; but 32 of 128,256, 4
-    // CTAs each, 15.9 and 11.2, and clusters in a grid of several CTAs per SM start late: 64 of 128,256 20.9 and 15.4.
+    // A cluster per sequence where that is one CTA per SM at most and 16,384 entries a CTA: 1 sequence of 128,256 entries 5.9 us,
+    // through the workspace (63 CTAs) 7.5; 4: 6.3 and 9.1; 16: 8.6 and 9.4; 64 of 32,000: 7.9 and 9.5; but 32 of 128,256, 4
+    // CTAs each, 15.4 and 11.1, 64, 2 CTAs each, 30.6 and 15.8.
     const int cap = sms / p.B < kClusterCtas ? sms / p.B : kClusterCtas;
     const bool clusters = cap > 0 && (p.V + cap - 1) / cap <= kClusterShare;
     if (clusters && ctas > cap) ctas = cap;

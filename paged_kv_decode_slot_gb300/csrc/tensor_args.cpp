@@ -1,6 +1,6 @@
 // tensor_args.cpp - the binding's work per call in C++, as a Python extension: a step makes several calls of ten tensors
 // each, some for a few microseconds of GPU work, and the interpreter's attribute look-ups and foreign call take longer than
-// the launch (a rotating append of 64 tokens takes 3.2 us on the GPU; its call 8.9 us of a Grace core with each argument
+// the launch (a rotating append of 64 tokens takes 2.8 us on the GPU; its call 8.9 us of a Grace core with each argument
 // checked here but the call made from Python, 3.8 us made here).  arg() and maybe() check one tensor; the functions further
 // down check a whole call and make it if nothing about it is special, else they return None and binding.py's own form of the
 // call names the fault (or takes what is allowed but rare: pinned host memory, calls without tokens).  Nothing here
