@@ -42,8 +42,8 @@ constexpr int kRopeStages = 2;
 constexpr int kRopeCtasPerSm = 4;
 constexpr double kInv2Pi = 0.15915494309189533577;
 
-// Two fp32 operations at a time (add, mul and fma on f32x2, sm_100 and later): the e4m3 form
-// took 57.8 us with single ones, 53.9 with pairs.
+// Two fp32 operations at a time (add, mul and fma on f32x2, sm_100 and later): with the
+// quotients checked from both sides, they took the e4m3 form from 57.8 us to 53.9.
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair(float lo, float hi)
 {
