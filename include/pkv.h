@@ -81,6 +81,9 @@ enum pkv_status {
 #define PKV_FLAG_TOKEN_RANGE 64 /* pkv_verify_draft: a drafted token outside [0, vocab_size) or a
                                    draft length outside [0, num_draft] */
 #define PKV_FLAG_NO_MASS 128    /* pkv_verify_draft: no probability to draw a token from */
+#define PKV_FLAG_SEQ_RANGE 256  /* pkv_fork_sequences: a parent outside [-1, num_seqs) */
+#define PKV_FLAG_REF_RANGE 512  /* a block whose reference count and the table rows that hold it disagree */
+#define PKV_FLAG_NO_BLOCKS 1024 /* pkv_extend_sequences: too few free blocks for every sequence */
 
 typedef struct {
     int32_t num_blocks;   /* physical blocks in each pool */
@@ -639,6 +642,114 @@ int pkv_verify_draft(const void *target_probs, int64_t target_stride, const void
                      int32_t num_seqs, int32_t num_draft, int32_t vocab_size, int32_t *num_accepted,
                      int32_t *tokens_out, const int32_t *context_lens, int32_t *context_lens_out,
                      void *workspace, size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
+
+/*
+ * ---- a latent cache -------------------------------------------------------------------------------
+ * Keys and values of all heads from one shared row a token: 512 elements of a latent vector, then 64 of a rotary key.
+ * A head's own key and value projections are absorbed into its query before attention and applied to its output
+ * after (the caller's products), so that decode attention runs in the latent space itself: the row is every head's
+ * key, its first 512 elements are every head's value, and a cached token is 1,152 bytes whatever the number of heads.
+ * latent_cache bf16 [num_blocks][16][576], 16-byte aligned device memory; its pkv_cache_desc has num_kv_heads 1 and
+ * head_dim 576.  Other widths, and e4m3 latents, are not supported.
+ */
+#define PKV_LATENT_DIM 512
+#define PKV_LATENT_ROPE 64
+
+/* New tokens into the cache.  kv_new bf16 [num_tokens][576]: a token's latent vector and its rotary key as the model's
+   projection gives them.  The latent vector c is normed, c norm_weight / sqrt(mean(c^2) + eps) (norm_weight bf16 [512];
+   NULL: copied as it is), the key turned by the angles positions[i] * inv_freq[j] of its 32 pairs (inv_freq double [32];
+   pairs (j, j + 32), or (2j, 2j + 1) with interleaved != 0; angles as in pkv_rope_append), both written into the row of
+   slot_mapping[i] (negative: the token is left out; beyond the pool: PKV_FLAG_SLOT_RANGE, left out).  The rotary parts of
+   the token's queries, q_rope bf16 with element (i, n, j) at i * q_rope_token_stride + n * q_rope_head_stride + j (strides
+   in elements, multiples of 8), are turned by the same angles into elements 512 .. 575 of every head of q bf16
+   [num_tokens][N][576], whose other elements are not touched; q_rope may be those elements themselves (in place), but
+   not overlap them otherwise.  A token that is left out writes nothing, q included.  Computed in fp32, rounded once.  Slots
+   within one call must be distinct.  kv_new, q_rope, norm_weight, latent_cache and q are 16-byte aligned. */
+int pkv_latent_append(const pkv_bf16 *kv_new, const pkv_bf16 *q_rope, int64_t q_rope_token_stride,
+                      int64_t q_rope_head_stride, const int32_t *positions, const double *inv_freq, int32_t interleaved,
+                      const pkv_bf16 *norm_weight, float eps, const int64_t *slot_mapping, int32_t num_tokens,
+                      int32_t num_q_heads, pkv_bf16 *latent_cache, pkv_bf16 *q, pkv_cache_desc cache, int32_t *err_flag,
+                      pkv_stream_t stream);
+
+/* The num_new newest tokens of each sequence (token t of sequence b is row b * num_new + t of kv_new, q_rope and q): slots
+   and positions from the tables and lengths, as pkv_rope_append_multi; slot_mapping_out int64 [num_seqs][num_new]. */
+int pkv_latent_append_multi(const pkv_bf16 *kv_new, const pkv_bf16 *q_rope, int64_t q_rope_token_stride,
+                            int64_t q_rope_head_stride, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                            const int32_t *context_lens, const double *inv_freq, int32_t interleaved,
+                            const pkv_bf16 *norm_weight, float eps, int32_t num_seqs, int32_t num_new, int32_t num_q_heads,
+                            pkv_bf16 *latent_cache, pkv_bf16 *q, int64_t *slot_mapping_out, pkv_cache_desc cache,
+                            int32_t *err_flag, pkv_stream_t stream);
+
+/* Workspace of pkv_decode_attn_latent, 256-byte aligned device memory; its contents do not matter between calls, but
+   calls that share one must not overlap on the GPU (two captured graphs that share one must not run at once).  One made for a
+   batch serves every smaller num_seqs with the same num_new and N. */
+size_t pkv_latent_workspace_bytes(int32_t num_seqs, int32_t num_new, int32_t num_q_heads);
+
+/* Decode attention over a latent cache, the num_new (1..64) newest tokens of each sequence, already appended (context_lens
+   counts them): row c_j of the cache,  s_j = scale q . c_j (576 elements),  out = sum_j softmax(s)_j c_j[:512], token t over
+   the tokens [0, ctx - num_new + t] (no visible key: out 0, lse -inf).  q bf16 [num_seqs][num_new][N][576], 16-byte aligned
+   device memory; out bf16 [num_seqs][num_new][N][512] (4-byte aligned); lse_out float [num_seqs][num_new][N], natural
+   log, nullable.  Any N.  The tiles of all sequences are dealt out evenly over the GPU, whatever the lengths: which parts a
+   sequence is cut into, and so the last bits of its result, depend on the other sequences of the batch.  Softmax weights
+   are rounded to bf16 before they multiply the values (they sum to one as rounded).  Two launches (the second joins what
+   was cut).  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left out. */
+int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, int32_t num_new,
+                           int32_t num_q_heads, float scale, pkv_bf16 *out, float *lse_out, pkv_cache_desc cache,
+                           void *workspace, size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
+
+/*
+ * ---- the life of a cache's blocks -----------------------------------------------------------------
+ * ("Optimización de la inferencia", "Página Atención": pages anywhere in memory, shared ones copied on write.)  The state
+ * of the sequences: block_tables int32 [num_seqs][max_blocks_per_seq], context_lens int32 [num_seqs], and ref_counts
+ * int32 [num_blocks], for every physical block the number of table rows that hold it (entries j < ceil(ctx / 16) of a row
+ * count, those behind are not looked at).  A block with count 0 is free.  The calls below keep the counts; all results are
+ * exact and follow from the arguments alone.  Where counts and tables disagree the result is void: disagreements that
+ * a call meets set PKV_FLAG_REF_RANGE, nothing outside the given arrays is touched.  Blocks are blocks of every layer's
+ * pools (of any kind: K and V, e4m3, latent); what has to be copied is told as pairs for pkv_copy_blocks_pools.
+ */
+
+/* Row b of a new batch takes over row parents[b] of the old one, or (-1) starts empty: forks (several rows with one
+   parent share all its blocks), beams that choose their parents anew, sequences that end (rows that are nobody's parent
+   give their blocks back) and moves of rows, in one call.  parents int32 [num_seqs_out], each in [-1, num_seqs) (others:
+   PKV_FLAG_SEQ_RANGE, row starts empty).  block_tables_out int32 [num_seqs_out][max_blocks_per_seq] (entries behind a
+   row's blocks -1) and context_lens_out int32 [num_seqs_out] must not overlap the old ones; ref_counts is brought up to
+   date in place.  A context outside [0, 16 max_blocks_per_seq] sets PKV_FLAG_CTX_RANGE and counts as 0. */
+int pkv_fork_sequences(const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                       int32_t num_seqs, const int32_t *parents, int32_t num_seqs_out, int32_t *ref_counts,
+                       int32_t num_blocks, int32_t *block_tables_out, int32_t *context_lens_out, int32_t *err_flag,
+                       pkv_stream_t stream);
+
+/* Workspace of pkv_extend_sequences and pkv_compact_blocks, 4-byte aligned; its contents do not matter between calls,
+   calls that share one must not overlap on the GPU. */
+size_t pkv_blocks_workspace_bytes(int32_t num_blocks);
+
+/* Every row b grows by num_new[b] >= 0 tokens: context_lens[b] += num_new[b], with the blocks that takes.  In the order of
+   rows, and of positions within a row, fresh blocks are the free ones in ascending order.  A row whose last block is
+   partly filled writes into it: where other rows hold that block too, the row's entry becomes a fresh block and
+   copies[b] (int32 [num_seqs][2]) = (old, new), to be copied before the new tokens are written; otherwise copies[b] =
+   (-1, -1).  (Rows that share it and grow in one call are taken in order: the last holder keeps the block.)  Once a row needs
+   more blocks than are left, it and all growing rows behind it stay as they are and PKV_FLAG_NO_BLOCKS is set.  A negative
+   num_new, or a row that would outgrow its table, sets PKV_FLAG_CTX_RANGE and that row stays as it is. */
+int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *num_new,
+                         int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks, int32_t *copies, void *workspace,
+                         size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
+
+/* Moves blocks towards the front of the pool: the highest used id to the lowest free one, the next highest to the next
+   lowest, while that lies below it, at most max_moves times (num_blocks / 2 always suffices: then the used blocks are the
+   first ones).  moves int32 [max_moves][2] = (from, to), (-1, -1) behind the last; num_moves int32 [1].  Tables and counts
+   are rewritten at once; pkv_copy_blocks_pools with the moves has to follow before anything reads the pools. */
+int pkv_compact_blocks(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                       int32_t *ref_counts, int32_t num_blocks, int32_t *moves, int32_t max_moves, int32_t *num_moves,
+                       void *workspace, size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
+
+/* pkv_copy_blocks in many pools at once: in each of the num_pools (1..256) pools of num_blocks blocks of block_bytes bytes
+   (a multiple of 16), block src_dst[2i + 1] becomes a copy of block src_dst[2i]; a pair (-1, -1) is skipped.  pools is a
+   host array of device addresses, 16-byte aligned, read before the call returns.  Pairs run concurrently: no
+   destination may be another pair's source or destination.  Other ids outside the pool set PKV_FLAG_BLOCK_RANGE, that pair is
+   skipped. */
+int pkv_copy_blocks_pools(void *const *pools, int32_t num_pools, int64_t block_bytes, int32_t num_blocks,
+                          const int32_t *src_dst, int32_t num_pairs, int32_t *err_flag, pkv_stream_t stream);
 
 /* Synchronise the stream, copy *err_flag to *host_value; PKV_ERR_RANGE if it is non-zero. */
 int pkv_read_err_flag(const int32_t *err_flag, int32_t *host_value, pkv_stream_t stream);

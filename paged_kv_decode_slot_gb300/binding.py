@@ -44,8 +44,13 @@ PKV_FLAG_OUT_RANGE = 16
 PKV_FLAG_GROUP_RANGE = 32
 PKV_FLAG_TOKEN_RANGE = 64
 PKV_FLAG_NO_MASS = 128
+PKV_FLAG_SEQ_RANGE = 256
+PKV_FLAG_REF_RANGE = 512
+PKV_FLAG_NO_BLOCKS = 1024
 
 BLOCK_SIZE = 16
+PKV_LATENT_DIM = 512
+PKV_LATENT_ROPE = 64
 
 
 class CacheDesc(ctypes.Structure):
@@ -693,7 +698,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 # Besides the pools and workspaces, what bulk copies read or every step reads again must be device memory.
-_DEVICE_ONLY_NEW = ("key_bounds", "k_scale", "v_scale", "q before the rotation", "k_new before the rotation", "v_new")
+_DEVICE_ONLY_NEW = ("key_bounds", "k_scale", "v_scale", "q before the rotation", "k_new before the rotation", "v_new",
+                    "latent_cache", "q of the latent rows", "ref_counts")
 
 
 def _launch(stream, dev: int) -> int:
@@ -1056,3 +1062,187 @@ def pkv_verify_draft(target_probs, draft_probs, draft_tokens, accept_u, sample_u
                                  _maybe(context_lens_out, _i32, (B,), "context_lens_out", dev),
                                  _arg(workspace, _u8, (size,), "workspace", dev), size,
                                  _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+# --------------------------------------- a latent cache ----------------------------------------
+_lib.pkv_latent_append.argtypes = [_P, _P, _I64, _I64, _P, _P, _I32, _P, ctypes.c_float, _P, _I32, _I32, _P, _P, CacheDesc,
+                                   _P, _P]
+_lib.pkv_latent_append_multi.argtypes = [_P, _P, _I64, _I64, _P, _I32, _P, _P, _I32, _P, ctypes.c_float, _I32, _I32, _I32,
+                                         _P, _P, _P, CacheDesc, _P, _P]
+_lib.pkv_latent_workspace_bytes.argtypes = [_I32, _I32, _I32]
+_lib.pkv_latent_workspace_bytes.restype = ctypes.c_size_t
+_lib.pkv_decode_attn_latent.argtypes = [_P, _P, _P, _I32, _P, _I32, _I32, _I32, ctypes.c_float, _P, _P, CacheDesc, _P,
+                                        ctypes.c_size_t, _P, _P]
+_LATENT_ROW = PKV_LATENT_DIM + PKV_LATENT_ROPE
+
+
+def _latent_cache(latent_cache, dev: int):
+    """Address and descriptor of a latent cache [num_blocks, 16, 576]."""
+    cs = _shape(latent_cache, 3, "latent_cache")
+    if tuple(cs[1:]) != (BLOCK_SIZE, _LATENT_ROW):
+        raise ValueError(f"latent_cache must be [num_blocks, {BLOCK_SIZE}, {_LATENT_ROW}], got {list(cs)}")
+    return _arg(latent_cache, _bf16, cs, "latent_cache", dev), CacheDesc(cs[0], BLOCK_SIZE, 1, _LATENT_ROW)
+
+
+def _latent_rows(kv_new, q_rope, q, lead, dev: int):
+    """(kv_new, q_rope, its token and head strides, q) of tokens [*lead], and the number of heads."""
+    N = _shape(q, len(lead) + 2, "q")[-2]
+    if not isinstance(q_rope, torch.Tensor):
+        raise TypeError("q_rope must be a torch.Tensor")
+    if tuple(q_rope.shape) != (*lead, N, PKV_LATENT_ROPE):
+        raise ValueError(f"q_rope must be {[*lead, N, PKV_LATENT_ROPE]}, got {list(q_rope.shape)}")
+    st = q_rope.stride()
+    if st[-1] != 1 or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):
+        raise ValueError("q_rope's elements must be contiguous, and its tokens one stride apart")
+    if q_rope.dtype is not _bf16:
+        raise TypeError(f"q_rope must be {_bf16}, got {q_rope.dtype}")
+    if not q_rope.is_cuda and not q_rope.is_pinned():
+        raise ValueError("q_rope must be a CUDA tensor or pinned host memory")
+    if q_rope.is_cuda and q_rope.get_device() != dev:
+        raise ValueError(f"q_rope is on cuda:{q_rope.get_device()}, but the current device is cuda:{dev}")
+    token = st[len(lead) - 1]
+    if len(lead) == 2 and lead[1] == 1:
+        token = st[0]
+    return (_arg(kv_new, _bf16, (*lead, _LATENT_ROW), "kv_new", dev), q_rope.data_ptr(), token, st[-2],
+            _arg(q, _bf16, (*lead, N, _LATENT_ROW), "q", dev), N)
+
+
+def pkv_latent_append(kv_new, q_rope, positions, inv_freq, slot_mapping, latent_cache, q, norm_weight=None,
+                      eps: float = 1e-6, interleaved: bool = False, err_flag=None, stream=None) -> int:
+    """kv_new bf16 [T, 576] (latent vector, rotary key) normed, turned and written into the rows of slot_mapping int64 [T]
+    of latent_cache bf16 [num_blocks, 16, 576]; q_rope bf16 [T, N, 64] (any token and head strides) turned into
+    q [T, N, 576][..., 512:].  positions int32 [T], inv_freq float64 [32], norm_weight bf16 [512] or None."""
+    dev = _current_device()
+    n = _shape(kv_new, 2, "kv_new")[0]
+    cp, desc = _latent_cache(latent_cache, dev)
+    kp, rp, token, head, qp, N = _latent_rows(kv_new, q_rope, q, (n,), dev)
+    if n == 0:
+        return PKV_OK
+    return _lib.pkv_latent_append(kp, rp, token, head, _arg(positions, _i32, (n,), "positions", dev),
+                                  _arg(inv_freq, torch.float64, (PKV_LATENT_ROPE // 2,), "inv_freq", dev), interleaved,
+                                  _maybe(norm_weight, _bf16, (PKV_LATENT_DIM,), "norm_weight", dev), eps,
+                                  _arg(slot_mapping, _i64, (n,), "slot_mapping", dev), n, N, cp, qp, desc,
+                                  _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_latent_append_multi(kv_new, q_rope, block_tables, context_lens, inv_freq, latent_cache, q, slot_mapping,
+                            norm_weight=None, eps: float = 1e-6, interleaved: bool = False, err_flag=None,
+                            stream=None) -> int:
+    """pkv_latent_append of the T newest tokens of each sequence: kv_new [B, T, 576], q_rope [B, T, N, 64],
+    q [B, T, N, 576]; slot_mapping int64 [B, T] (written)."""
+    dev = _current_device()
+    B, T = _shape(kv_new, 3, "kv_new")[:2]
+    cp, desc = _latent_cache(latent_cache, dev)
+    kp, rp, token, head, qp, N = _latent_rows(kv_new, q_rope, q, (B, T), dev)
+    tp, width, lp = _table_args(block_tables, context_lens, B, dev)
+    if B * T == 0:
+        return PKV_OK
+    return _lib.pkv_latent_append_multi(kp, rp, token, head, tp, width, lp,
+                                        _arg(inv_freq, torch.float64, (PKV_LATENT_ROPE // 2,), "inv_freq", dev), interleaved,
+                                        _maybe(norm_weight, _bf16, (PKV_LATENT_DIM,), "norm_weight", dev), eps, B, T, N, cp,
+                                        qp, _arg(slot_mapping, _i64, (B, T), "slot_mapping", dev), desc,
+                                        _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_latent_workspace_bytes(num_seqs: int, num_new: int, num_q_heads: int) -> int:
+    return int(_lib.pkv_latent_workspace_bytes(num_seqs, num_new, num_q_heads))
+
+
+def pkv_decode_attn_latent(q, latent_cache, block_tables, context_lens, scale: float, out, lse_out=None, workspace=None,
+                           err_flag=None, stream=None) -> int:
+    """Decode attention of the T newest tokens of each sequence over a latent cache: q bf16 [B, T, N, 576], out bf16
+    [B, T, N, 512], lse_out float32 [B, T, N]; workspace: pkv_latent_workspace_bytes(B, T, N) bytes."""
+    dev = _current_device()
+    B, T, N, _ = qs = _shape(q, 4, "q")
+    cp, desc = _latent_cache(latent_cache, dev)
+    tp, width, lp = _table_args(block_tables, context_lens, B, dev)
+    size = 0 if workspace is None else _shape(workspace, 1, "workspace")[0]
+    if B == 0:
+        return PKV_OK
+    return _lib.pkv_decode_attn_latent(_arg(q, _bf16, (B, T, N, _LATENT_ROW), "q of the latent rows", dev), cp, tp, width, lp,
+                                       B, T, N, scale, _arg(out, _bf16, (B, T, N, PKV_LATENT_DIM), "out", dev),
+                                       _maybe(lse_out, _f32, (B, T, N), "lse_out", dev), desc,
+                                       _maybe(workspace, _u8, (size,), "workspace", dev), size,
+                                       _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+# ------------------------------- the life of a cache's blocks ----------------------------------
+_lib.pkv_fork_sequences.argtypes = [_P, _I32, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _P]
+_lib.pkv_blocks_workspace_bytes.argtypes = [_I32]
+_lib.pkv_blocks_workspace_bytes.restype = ctypes.c_size_t
+_lib.pkv_extend_sequences.argtypes = [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.pkv_compact_blocks.argtypes = [_P, _I32, _P, _I32, _P, _I32, _P, _I32, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.pkv_copy_blocks_pools.argtypes = [_P, _I32, _I64, _I32, _P, _I32, _P, _P]
+
+
+def pkv_fork_sequences(block_tables, context_lens, parents, ref_counts, block_tables_out, context_lens_out, err_flag=None,
+                       stream=None) -> int:
+    """Row b of block_tables_out [B', W] and context_lens_out [B'] becomes row parents[b] of the old ones [B, W], [B], or
+    empty (-1); ref_counts int32 [num_blocks] follows."""
+    dev = _current_device()
+    B, R = _shape(context_lens, 1, "context_lens")[0], _shape(parents, 1, "parents")[0]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    nb = _shape(ref_counts, 1, "ref_counts")[0]
+    if B + R == 0:
+        return PKV_OK
+    return _lib.pkv_fork_sequences(tp, width, cp, B, _arg(parents, _i32, (R,), "parents", dev), R,
+                                   _arg(ref_counts, _i32, (nb,), "ref_counts", dev), nb,
+                                   _arg(block_tables_out, _i32, (R, width), "block_tables_out", dev),
+                                   _arg(context_lens_out, _i32, (R,), "context_lens_out", dev),
+                                   _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_blocks_workspace_bytes(num_blocks: int) -> int:
+    return int(_lib.pkv_blocks_workspace_bytes(num_blocks))
+
+
+def pkv_extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag=None,
+                         stream=None) -> int:
+    """Row b grows by num_new[b] tokens: block_tables [B, W], context_lens [B] and ref_counts [num_blocks] in place,
+    copies int32 [B, 2] (written): the copy on write of each row, or (-1, -1).  workspace:
+    pkv_blocks_workspace_bytes(num_blocks) bytes."""
+    dev = _current_device()
+    B, nb = _shape(context_lens, 1, "context_lens")[0], _shape(ref_counts, 1, "ref_counts")[0]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    size = _shape(workspace, 1, "workspace")[0]
+    if B == 0:
+        return PKV_OK
+    return _lib.pkv_extend_sequences(tp, width, cp, _arg(num_new, _i32, (B,), "num_new", dev), B,
+                                     _arg(ref_counts, _i32, (nb,), "ref_counts", dev), nb,
+                                     _arg(copies, _i32, (B, 2), "copies", dev), _arg(workspace, _u8, (size,), "workspace", dev),
+                                     size, _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves, workspace, err_flag=None,
+                       stream=None) -> int:
+    """Blocks moved towards the front: moves int32 [max_moves, 2] and num_moves int32 [1] (written), block_tables [B, W]
+    and ref_counts [num_blocks] in place.  workspace: pkv_blocks_workspace_bytes(num_blocks) bytes."""
+    dev = _current_device()
+    B, nb = _shape(context_lens, 1, "context_lens")[0], _shape(ref_counts, 1, "ref_counts")[0]
+    tp, width, cp = _table_args(block_tables, context_lens, B, dev)
+    size, most = _shape(workspace, 1, "workspace")[0], _shape(moves, 2, "moves")[0]
+    return _lib.pkv_compact_blocks(tp, width, cp, B, _arg(ref_counts, _i32, (nb,), "ref_counts", dev), nb,
+                                   _arg(moves, _i32, (most, 2), "moves", dev), most,
+                                   _arg(num_moves, _i32, _FLAG, "num_moves", dev),
+                                   _arg(workspace, _u8, (size,), "workspace", dev), size,
+                                   _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+
+
+def pkv_copy_blocks_pools(pools, src_dst, err_flag=None, stream=None) -> int:
+    """Block src_dst[i, 1] of every pool [num_blocks, ...] (of one shape and type) becomes a copy of block src_dst[i, 0];
+    (-1, -1) is skipped."""
+    dev = _current_device()
+    pools = list(pools)
+    if not pools:
+        raise ValueError("pools is empty")
+    first = pools[0]
+    shape = _shape(first, first.dim() if isinstance(first, torch.Tensor) else 1, "k_cache")
+    if len(shape) < 2 or shape[0] < 1:
+        raise ValueError("a pool must be [num_blocks, ...]")
+    where = (ctypes.c_void_p * len(pools))(*[_arg(p, first.dtype, shape, "k_cache", dev) for p in pools])
+    n = _shape(src_dst, 2, "src_dst")[0]
+    if n == 0:
+        return PKV_OK
+    return _lib.pkv_copy_blocks_pools(where, len(pools), first.numel() // shape[0] * first.element_size(), shape[0],
+                                      _arg(src_dst, _i32, (n, 2), "src_dst", dev), n,
+                                      _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))

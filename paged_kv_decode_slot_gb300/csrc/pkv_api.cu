@@ -10,7 +10,9 @@
 
 #include "pkv.h"
 #include "pkv_internal.h"
+#include "pkv_latent.h"
 #include "pkv_ops.h"
+#include "pkv_sequences.h"
 
 #define PKV_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -688,6 +690,279 @@ PKV_EXPORT int pkv_gather(const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
                                        cache.num_kv_heads, cache.head_dim, k_out, v_out, out_rows,
                                        err_flag, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "gather launch");
+}
+
+// ---- a latent cache -----------------------------------------------------------------------------
+namespace {
+
+constexpr int kLatentRow = pkv::kLatentDim + pkv::kLatentRope;
+
+int check_latent_desc(const pkv_cache_desc &d)
+{
+    if (d.block_size != 16) return PKV_ERR_UNSUPPORTED;
+    if (d.num_blocks <= 0 || d.num_kv_heads <= 0 || d.head_dim <= 0) return PKV_ERR_SHAPE;
+    return d.num_kv_heads == 1 && d.head_dim == kLatentRow ? PKV_OK : PKV_ERR_UNSUPPORTED;
+}
+
+int latent_append(pkv::LatentAppendParams &p, bool interleaved, const pkv_cache_desc &d, int32_t num_q_heads, int64_t tokens,
+                  cudaStream_t stream)
+{
+    if (!p.kv_new || !p.q_rope || !p.q || !p.cache || !p.inv_freq) return PKV_ERR_NULL;
+    int st = check_latent_desc(d);
+    if (st != PKV_OK) return st;
+    if (num_q_heads <= 0 || tokens < 0 || !(p.eps >= 0.f)) return PKV_ERR_SHAPE;
+    // warps of the grid, and offsets inside a token, are 32-bit
+    if (tokens > INT32_MAX / 2 || num_q_heads > INT32_MAX / 2048 || tokens * (num_q_heads / 32 + 1) > INT32_MAX) return PKV_ERR_SHAPE;
+    if (p.q_rope_token < 0 || p.q_rope_head < 0) return PKV_ERR_SHAPE;
+    if (p.q_rope_token % 8 != 0 || p.q_rope_head % 8 != 0 || !aligned(p.kv_new, 16) || !aligned(p.q_rope, 16) ||
+        !aligned(p.q, 16) || !aligned(p.cache, 16) || !aligned(p.norm_weight, 16) || !aligned(p.inv_freq, 8) ||
+        !aligned(p.slots, 8) || !aligned(p.slots_out, 8))
+        return PKV_ERR_ALIGN;
+    if (tokens == 0) return PKV_OK;
+    p.n = (int32_t)tokens;
+    p.N = num_q_heads;
+    p.num_blocks = d.num_blocks;
+    cudaError_t e = pkv::launch_latent_append(p, interleaved, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "latent append launch");
+}
+
+// Bytes of the three parts of the attention's workspace, each 256-byte aligned.
+struct LatentWorkspace {
+    size_t lse_at, parts_at, bytes;
+};
+LatentWorkspace latent_workspace(int64_t num_seqs, const pkv::LatentPlan &plan)
+{
+    const size_t rows = 2 * (size_t)pkv::kLatentMaxClusters * plan.cta_rows;
+    auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    LatentWorkspace w;
+    w.lse_at = up(rows * pkv::kLatentDim * 4);
+    w.parts_at = w.lse_at + up(rows * 4);
+    w.bytes = w.parts_at + up((size_t)num_seqs * plan.chunks * sizeof(int2));
+    return w;
+}
+
+int check_latent_sizes(int32_t num_seqs, int32_t num_new, int32_t num_q_heads)
+{
+    if (num_seqs < 0 || num_new <= 0 || num_q_heads <= 0) return PKV_ERR_SHAPE;
+    if (num_new > 64) return PKV_ERR_UNSUPPORTED;
+    // rows of the batch are a coordinate of the queries' tensor map
+    if ((int64_t)num_new * num_q_heads > INT32_MAX / 2 || (int64_t)num_seqs * num_new * num_q_heads > INT32_MAX / 2) return PKV_ERR_SHAPE;
+    return PKV_OK;
+}
+
+// The cache as (64 elements, token, chunk of 64 elements, block), one block's rows of one chunk a box; the queries as
+// (64 elements, row, chunk), a CTA's rows a box.  Both land as rows of 128 bytes, 128-byte swizzled.
+int make_latent_maps(CUtensorMap *tc, CUtensorMap *tq, const void *cache, int32_t num_blocks, const void *q, int64_t rows,
+                     int cta_rows)
+{
+    if (!encode_fn()) {
+        g_last_error = "cuTensorMapEncodeTiled is unavailable from the driver";
+        return PKV_ERR_CUDA;
+    }
+    const cuuint64_t row = kLatentRow * 2;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    const cuuint64_t cd[4] = {64, 16, (cuuint64_t)kLatentRow / 64, (cuuint64_t)num_blocks}, cs[3] = {row, 128, 16 * row};
+    const cuuint32_t cb[4] = {64, 16, 1, 1};
+    CUresult r = encode_fn()(tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(cache), cd, cs, cb, es,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) {
+        const cuuint64_t qd[3] = {64, (cuuint64_t)rows, (cuuint64_t)kLatentRow / 64}, qs[2] = {row, 128};
+        const cuuint32_t qb[3] = {64, (cuuint32_t)cta_rows, 1};
+        r = encode_fn()(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), qd, qs, qb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    if (r == CUDA_SUCCESS) return PKV_OK;
+    g_last_error = "cuTensorMapEncodeTiled failed (CUresult " + std::to_string((int)r) + ")";
+    return PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+PKV_EXPORT int pkv_latent_append(const pkv_bf16 *kv_new, const pkv_bf16 *q_rope, int64_t q_rope_token_stride,
+                                 int64_t q_rope_head_stride, const int32_t *positions, const double *inv_freq,
+                                 int32_t interleaved, const pkv_bf16 *norm_weight, float eps, const int64_t *slot_mapping,
+                                 int32_t num_tokens, int32_t num_q_heads, pkv_bf16 *latent_cache, pkv_bf16 *q,
+                                 pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!positions || !slot_mapping) return PKV_ERR_NULL;
+    pkv::LatentAppendParams p{};
+    p.kv_new = kv_new, p.q_rope = q_rope, p.q_rope_token = q_rope_token_stride, p.q_rope_head = q_rope_head_stride;
+    p.q = q, p.norm_weight = norm_weight, p.eps = eps, p.inv_freq = inv_freq;
+    p.positions = positions, p.slots = slot_mapping;
+    p.cache = latent_cache, p.err_flag = err_flag;
+    return latent_append(p, interleaved != 0, cache, num_q_heads, num_tokens, stream);
+}
+
+PKV_EXPORT int pkv_latent_append_multi(const pkv_bf16 *kv_new, const pkv_bf16 *q_rope, int64_t q_rope_token_stride,
+                                       int64_t q_rope_head_stride, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *context_lens, const double *inv_freq, int32_t interleaved,
+                                       const pkv_bf16 *norm_weight, float eps, int32_t num_seqs, int32_t num_new,
+                                       int32_t num_q_heads, pkv_bf16 *latent_cache, pkv_bf16 *q, int64_t *slot_mapping_out,
+                                       pkv_cache_desc cache, int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!block_tables || !context_lens || !slot_mapping_out) return PKV_ERR_NULL;
+    if (num_seqs < 0 || num_new <= 0 || max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * 16 > INT32_MAX) return PKV_ERR_SHAPE;
+    pkv::LatentAppendParams p{};
+    p.kv_new = kv_new, p.q_rope = q_rope, p.q_rope_token = q_rope_token_stride, p.q_rope_head = q_rope_head_stride;
+    p.q = q, p.norm_weight = norm_weight, p.eps = eps, p.inv_freq = inv_freq;
+    p.block_tables = block_tables, p.context_lens = context_lens, p.max_nb = max_blocks_per_seq, p.T = num_new;
+    p.slots_out = slot_mapping_out;
+    p.cache = latent_cache, p.err_flag = err_flag;
+    return latent_append(p, interleaved != 0, cache, num_q_heads, (int64_t)num_seqs * num_new, stream);
+}
+
+PKV_EXPORT size_t pkv_latent_workspace_bytes(int32_t num_seqs, int32_t num_new, int32_t num_q_heads)
+{
+    if (check_latent_sizes(num_seqs, num_new, num_q_heads) != PKV_OK) return 0;
+    return latent_workspace(num_seqs, pkv::latent_plan((int64_t)num_new * num_q_heads)).bytes;
+}
+
+PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, const int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                      int32_t num_new, int32_t num_q_heads, float scale, pkv_bf16 *out, float *lse_out,
+                                      pkv_cache_desc cache, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                      pkv_stream_t stream)
+{
+    if (!q || !latent_cache || !block_tables || !context_lens || !out) return PKV_ERR_NULL;
+    int st = check_latent_desc(cache);
+    if (st == PKV_OK) st = check_latent_sizes(num_seqs, num_new, num_q_heads);
+    if (st != PKV_OK) return st;
+    if (max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * 16 > INT32_MAX) return PKV_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(out, 4) || !aligned(lse_out, 4)) return PKV_ERR_ALIGN;
+    const pkv::LatentPlan plan = pkv::latent_plan((int64_t)num_new * num_q_heads);
+    const LatentWorkspace w = latent_workspace(num_seqs, plan);
+    if (!workspace || workspace_bytes < w.bytes) return PKV_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PKV_ERR_ALIGN;
+    if (num_seqs == 0) return PKV_OK;
+    pkv::LatentAttnParams p{};
+    p.block_tables = block_tables, p.context_lens = context_lens, p.max_nb = max_blocks_per_seq;
+    p.B = num_seqs, p.N = num_q_heads, p.T = num_new, p.num_blocks = cache.num_blocks;
+    p.rows = num_new * num_q_heads, p.chunks = (int32_t)plan.chunks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = reinterpret_cast<__nv_bfloat16 *>(out), p.lse_out = lse_out;
+    char *ws = static_cast<char *>(workspace);
+    p.part_out = reinterpret_cast<float *>(ws);
+    p.part_lse = reinterpret_cast<float *>(ws + w.lse_at);
+    p.unit_parts = reinterpret_cast<int2 *>(ws + w.parts_at);
+    p.err_flag = err_flag;
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+#ifdef PKV_TEST_HOOKS
+    p.withhold_tile = g_withhold_tile.load(std::memory_order_relaxed);
+#endif
+    CUtensorMap tc, tq;
+    st = make_latent_maps(&tc, &tq, latent_cache, cache.num_blocks, q, (int64_t)num_seqs * p.rows, plan.cta_rows);
+    if (st != PKV_OK) return st;
+    int sms = 0;
+    st = sm_count(&sms);
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_latent_attn(tc, tq, p, plan, sms, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "latent attention launch");
+}
+
+// ---- the life of a cache's blocks -----------------------------------------------------------------
+namespace {
+
+int check_sequences(int32_t max_nb, int32_t num_seqs, int32_t num_blocks)
+{
+    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * 2048 || num_seqs < 0 || num_blocks <= 0) return PKV_ERR_SHAPE;
+    return PKV_OK;
+}
+
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+}  // namespace
+
+PKV_EXPORT int pkv_fork_sequences(const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                  int32_t num_seqs, const int32_t *parents, int32_t num_seqs_out, int32_t *ref_counts,
+                                  int32_t num_blocks, int32_t *block_tables_out, int32_t *context_lens_out,
+                                  int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!block_tables || !context_lens || !parents || !ref_counts || !block_tables_out || !context_lens_out) return PKV_ERR_NULL;
+    int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
+    if (st != PKV_OK) return st;
+    if (num_seqs_out < 0 || (int64_t)num_seqs + num_seqs_out > INT32_MAX) return PKV_ERR_SHAPE;
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(parents, 4) || !aligned(ref_counts, 4) ||
+        !aligned(block_tables_out, 4) || !aligned(context_lens_out, 4))
+        return PKV_ERR_ALIGN;
+    const int64_t row = 4 * (int64_t)max_blocks_per_seq;
+    if (overlap(block_tables, row * num_seqs, block_tables_out, row * num_seqs_out) ||
+        overlap(context_lens, 4 * (int64_t)num_seqs, context_lens_out, 4 * (int64_t)num_seqs_out))
+        return PKV_ERR_SHAPE;
+    if (num_seqs + num_seqs_out == 0) return PKV_OK;
+    pkv::ForkParams p{block_tables, context_lens, parents, max_blocks_per_seq, num_seqs, num_seqs_out, num_blocks, ref_counts,
+                      block_tables_out, context_lens_out, err_flag};
+    cudaError_t e = pkv::launch_fork_sequences(p, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "fork launch");
+}
+
+PKV_EXPORT size_t pkv_blocks_workspace_bytes(int32_t num_blocks) { return num_blocks > 0 ? 4 * (size_t)num_blocks : 0; }
+
+PKV_EXPORT int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens,
+                                    const int32_t *num_new, int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks,
+                                    int32_t *copies, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                    pkv_stream_t stream)
+{
+    if (!block_tables || !context_lens || !num_new || !ref_counts || !copies) return PKV_ERR_NULL;
+    int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
+    if (st != PKV_OK) return st;
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(num_new, 4) || !aligned(ref_counts, 4) ||
+        !aligned(copies, 4))
+        return PKV_ERR_ALIGN;
+    if (!workspace || workspace_bytes < pkv_blocks_workspace_bytes(num_blocks)) return PKV_ERR_WORKSPACE;
+    if (!aligned(workspace, 4)) return PKV_ERR_ALIGN;
+    if (num_seqs == 0) return PKV_OK;
+    pkv::ExtendParams p{block_tables, context_lens, num_new, max_blocks_per_seq, num_seqs, num_blocks, ref_counts, copies,
+                        static_cast<int32_t *>(workspace), err_flag};
+    cudaError_t e = pkv::launch_extend_sequences(p, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "extend launch");
+}
+
+PKV_EXPORT int pkv_compact_blocks(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                  int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks, int32_t *moves,
+                                  int32_t max_moves, int32_t *num_moves, void *workspace, size_t workspace_bytes,
+                                  int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!block_tables || !context_lens || !ref_counts || !moves || !num_moves) return PKV_ERR_NULL;
+    int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
+    if (st != PKV_OK) return st;
+    if (max_moves <= 0) return PKV_ERR_SHAPE;
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(ref_counts, 4) || !aligned(moves, 4) ||
+        !aligned(num_moves, 4))
+        return PKV_ERR_ALIGN;
+    if (!workspace || workspace_bytes < pkv_blocks_workspace_bytes(num_blocks)) return PKV_ERR_WORKSPACE;
+    if (!aligned(workspace, 4)) return PKV_ERR_ALIGN;
+    pkv::CompactParams p{block_tables, context_lens, max_blocks_per_seq, num_seqs, num_blocks, ref_counts, moves, max_moves,
+                         num_moves, static_cast<int32_t *>(workspace), err_flag};
+    cudaError_t e = pkv::launch_compact_blocks(p, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "compact launch");
+}
+
+PKV_EXPORT int pkv_copy_blocks_pools(void *const *pools, int32_t num_pools, int64_t block_bytes, int32_t num_blocks,
+                                     const int32_t *src_dst, int32_t num_pairs, int32_t *err_flag, pkv_stream_t stream)
+{
+    if (!pools || !src_dst) return PKV_ERR_NULL;
+    if (num_pools <= 0 || num_blocks <= 0 || num_pairs < 0 || block_bytes <= 0) return PKV_ERR_SHAPE;
+    if (num_pools > pkv::kMaxCopyPools || block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (!aligned(src_dst, 4)) return PKV_ERR_ALIGN;
+    pkv::CopyPoolsParams p;
+    for (int i = 0; i < num_pools; ++i) {
+        if (!pools[i]) return PKV_ERR_NULL;
+        if (!aligned(pools[i], 16)) return PKV_ERR_ALIGN;
+        p.pools[i] = pools[i];
+    }
+    if (num_pairs == 0) return PKV_OK;
+    p.src_dst = src_dst, p.num_pools = num_pools, p.pairs = num_pairs, p.num_blocks = num_blocks;
+    p.vectors = block_bytes / 16, p.err_flag = err_flag;
+    int sms = 0;
+    const int st = sm_count(&sms);
+    if (st != PKV_OK) return st;
+    cudaError_t e = pkv::launch_copy_pools(p, sms, stream);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "copy launch");
 }
 
 PKV_EXPORT int pkv_read_err_flag(const int32_t *err_flag, int32_t *host_value, pkv_stream_t stream)

@@ -1,0 +1,80 @@
+// pkv_latent.h - kernel parameter blocks and launchers of the latent cache: its append and its decode attention (not part
+// of the public C ABI).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace pkv {
+
+constexpr int kLatentDim = 512;   // the latent vector of a token
+constexpr int kLatentRope = 64;   // its rotary key
+constexpr int kLatentMaxClusters = 152;
+
+// How the (token, head) rows of a sequence are dealt to CTAs: chunks of ctas * cta_rows rows, ctas CTAs as a cluster.
+struct LatentPlan {
+    int cta_rows, ctas;
+    int64_t chunks;
+    int chunk_rows() const { return cta_rows * ctas; }
+};
+// The narrowest of 16, 32 and 64 rows a CTA that holds a sequence's rows: products cost their tokens and, less, their
+// rows, and what queries leave free of shared memory takes loads ahead.  From 65 rows on pairs of CTAs.
+inline LatentPlan latent_plan(int64_t rows)
+{
+    LatentPlan p;
+    p.cta_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.ctas = rows > 64 ? 2 : 1;
+    p.chunks = (rows + p.chunk_rows() - 1) / p.chunk_rows();
+    return p;
+}
+
+struct LatentAttnParams {
+    const int32_t *block_tables;   // [B][max_nb]
+    const int32_t *context_lens;   // [B]
+    int32_t max_nb, B, N, T, num_blocks;
+    int32_t rows;                  // T * N
+    int32_t chunks;                // chunks of rows a sequence
+    int32_t clusters;              // clusters of the grid (set by the launcher)
+    float scale_log2;
+    __nv_bfloat16 *out;            // [B][T][N][512]
+    float *lse_out;                // [B][T][N], nullable
+    // workspace: two parts a cluster of chunk rows each, and of each (sequence, chunk) its first cluster and its parts
+    float *part_out;               // [2 clusters][chunk rows][512]
+    float *part_lse;               // [2 clusters][chunk rows], log2
+    int2 *unit_parts;              // [B][chunks]
+    int32_t *err_flag;
+    uint64_t wait_ns;
+#ifdef PKV_TEST_HOOKS
+    int64_t withhold_tile;         // pkv_debug_withhold_tile: -1, or a tile no CTA loads
+#endif
+};
+
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
+                               int sms, cudaStream_t stream);
+
+// Norm and rotation of new tokens' rows with their append, and rotation of their queries (pkv_latent_append.cu).
+struct LatentAppendParams {
+    const uint16_t *kv_new;        // [n][576]
+    const uint16_t *q_rope;        // [n][N][64], strides below
+    int64_t q_rope_token, q_rope_head;
+    uint16_t *q;                   // [n][N][576]: elements 512 .. of a head are written
+    const uint16_t *norm_weight;   // [512], nullable: latents are copied
+    float eps;
+    const double *inv_freq;        // [32] radians per position
+    const int32_t *positions;      // [n]
+    const int64_t *slots;          // [n]
+    const int32_t *block_tables;   // [B][max_nb], else
+    const int32_t *context_lens;   // [B]
+    int64_t *slots_out;            // [B][T]
+    int32_t max_nb, T;
+    int32_t n, N, num_blocks;
+    uint16_t *cache;               // [num_blocks][16][576]
+    int32_t *err_flag;
+};
+
+cudaError_t launch_latent_append(const LatentAppendParams &p, bool interleaved, cudaStream_t stream);
+
+}  // namespace pkv

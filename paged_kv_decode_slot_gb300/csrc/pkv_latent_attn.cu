@@ -1,0 +1,871 @@
+// pkv_latent_attn.cu - decode attention over a paged latent cache: one row of 576 elements a token, of which all 576
+// are every head's key and the first 512 every head's value (the heads' own key and value projections are absorbed into
+// the queries before and applied to the outputs after).
+//     s[r][j] = scale q[r] . c[j],  out[r] = sum_j softmax(s[r])_j c[j][:512],  r a (token, head) row of a sequence.
+//
+// All rows share the keys, so the contraction is dense: with 128 rows 2 * 1088 * 128 operations for 1,152 bytes, 242 a
+// byte, about what the chip has for one byte of DRAM.  Hence the tcgen05 tensor cores, and both products transposed:
+//     S^T[128 tokens x R] = C[128 x 576] . Q^T        A: the tile's rows as they lie (K-major), B: the queries
+//     O^T[512 x R]       += C^T[512 x 128] . P^T      A: the same rows read MN-major (four M = 128 products), B: P
+// so that R = 16, 32 or 64 query rows a CTA is the N of the products, not a padded M: the 512 x R accumulator takes 4 R
+// of the 512 tensor-memory columns, where 128 rows x 512 would take them all.  More rows than 64 take a cluster of two
+// CTAs, 64 rows each: every piece of the cache is fetched by one of the two and multicast to both.
+//
+// The cache streams through a ring of 16 KB pieces, first as keys (128 tokens x 64 elements, nine a tile), then, from
+// L2, as values (64 tokens x 128 elements, eight a tile): a whole 128-token tile (147 KB) beside 64 queries (74 KB)
+// would leave nothing to load ahead into.  A box of a load is one block's 16 rows x 64 elements.
+//
+// The work is dealt out evenly: the tiles of all (sequence, chunk of rows) units in a row, cut into as many equal runs as
+// clusters run at once.  A unit that one cluster holds whole is written out directly; of one that is cut each part goes
+// to the workspace, at most two a cluster, and a second launch joins them by their log-sum-exp.
+//
+// CTA = 10 warps: 0-7 softmax (warp w: tokens 32 (w % 4) .. + 31, one a thread; half w / 4 of the rows), 8 issues the MMAs,
+// 9 the loads.  QK^T of tile i + 1 is issued before P V of tile i, so the tensor cores work through the softmax of tile i.
+// The running maxima move only when a logit exceeds them by 2^8 (checked with one barrier vote a tile); the sums stay in
+// the threads' registers, a part for each token lane, until the end.
+#include <float.h>
+
+#include "pkv_cluster.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "pkv_latent.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+
+constexpr int kLatChunks = (kLatentDim + kLatentRope) / 64;   // 64-element chunks of a row
+constexpr int kLatTile = 128;                                 // tokens of a tile
+constexpr int kLatTileBlocks = kLatTile / kBlockSize;
+constexpr int kLatStage = 16384;                              // bytes of a ring stage
+constexpr int kLatBox = kBlockSize * 128;                     // bytes of one block's 64-element rows
+constexpr int kLatSoftmaxWarps = 8, kLatMmaWarp = 8, kLatLoadWarp = 9;
+constexpr int kLatThreads = 320;
+constexpr float kLatRescale = 8.f;                            // log2 of how far a logit may exceed the running maximum
+
+// R: query rows of a CTA.  Two: the CTA is one of a cluster of two.
+template <int R, bool Two>
+struct LatentLayout {
+    static_assert(R == 16 || R == 32 || R == 64, "rows of a CTA");
+    static constexpr int kQChunk = R * 128;              // 64 elements of R queries, K-major, 128-byte swizzle
+    static constexpr int kQBytes = kLatChunks * kQChunk;
+    static constexpr int kPLine = R * 2;                 // bytes of one token's weights: a swizzle atom's row
+    static constexpr int kPBytes = kLatTile * kPLine;
+    static constexpr int kStages = R == 64 ? 8 : R == 32 ? 11 : 12;
+    static constexpr int kQOffset = 0;
+    static constexpr int kPOffset = kQBytes;
+    static constexpr int kRingOffset = kPOffset + ((kPBytes + 1023) & ~1023);
+    static constexpr int kBarOffset = kRingOffset + kStages * kLatStage;
+    // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, fin
+    static constexpr int kBars = 2 * kStages + 7;
+    static constexpr int kMiscOffset = kBarOffset + kBars * 8;
+    static constexpr int kStageWords = (2 * kStages + 3) & ~3;  // what follows is read in vectors of four words
+    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, issued, spare */ + kStageWords /* bytes */ +
+                                  R /* limits */ + R /* maxima */ + R /* factors */ + 4 * R /* of four warps */;
+    static constexpr int kAlloc = ((kMiscOffset + 15) & ~15) + kWords * 4 + 1024;
+    static_assert(kQBytes % 1024 == 0 && kRingOffset % 1024 == 0, "swizzle atoms are aligned");
+    static_assert(kAlloc + (kLatThreads + 4) * 8 <= 227 * 1024, "shared memory of a CTA");
+    static constexpr uint32_t kCols = R == 64 ? 512 : R == 32 ? 256 : 128;  // tensor memory: O^T 4 R, S^T 2 R
+};
+
+// ---- dealing out the tiles ----------------------------------------------------------------------
+// A unit's share of the work: its tiles and, as much as one tile, its queries, statistics and outputs.
+constexpr int kLatUnitCost = 1;
+
+__device__ __forceinline__ int latent_ctx(const LatentAttnParams &p, int b)
+{
+    const int ctx = __ldg(p.context_lens + b);
+    return ctx < 0 || ctx > p.max_nb * kBlockSize ? 0 : ctx;
+}
+__device__ __forceinline__ int latent_cost(int ctx) { return ctx > 0 ? (ctx + kLatTile - 1) / kLatTile + kLatUnitCost : 0; }
+
+// Tiles [t0, t1) of unit (b, chunk), which starts at `start` in the row of all units.
+struct LatentSegment {
+    int b, chunk, ctx, t0, t1, tiles;
+    int64_t start;
+    bool whole;
+};
+
+struct LatentWalk {
+    int64_t lo, hi, start;
+    int b, chunk;
+    __device__ __forceinline__ bool next(const LatentAttnParams &p, LatentSegment &s)
+    {
+        while (start < hi && b < p.B) {
+            const int ctx = latent_ctx(p, b), cost = latent_cost(ctx);
+            const int64_t at = start;
+            const int ub = b, uc = chunk;
+            start += cost;
+            if (++chunk == p.chunks || cost == 0) chunk = 0, ++b;
+            if (cost == 0) continue;
+            const int x0 = (int)max((int64_t)0, lo - at), x1 = (int)min((int64_t)cost, hi - at);
+            s.t0 = max(0, x0 - kLatUnitCost), s.t1 = max(0, x1 - kLatUnitCost);
+            if (s.t0 >= s.t1) continue;
+            s.b = ub, s.chunk = uc, s.ctx = ctx, s.tiles = cost - kLatUnitCost, s.start = at;
+            s.whole = s.t0 == 0 && s.t1 == s.tiles;
+            return true;
+        }
+        return false;
+    }
+};
+
+// This cluster's run of the work, the same in every thread; false: nothing to do.  `sums` holds kLatThreads + 4 64-bit
+// words of shared memory.  Every thread calls it.
+__device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cluster, int64_t *sums, LatentWalk &w, int64_t &total,
+                                            int &clusters)
+{
+    const int tid = threadIdx.x, per = (p.B + kLatThreads - 1) / kLatThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int64_t cost = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int ctx = __ldg(p.context_lens + b);
+        if (cluster == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+        cost += latent_cost(latent_ctx(p, b));
+    }
+    sums[tid] = cost;
+    __syncthreads();
+    if (tid < 32) {  // exclusive scan by one warp, ten entries a lane
+        constexpr int kPer = kLatThreads / 32;
+        int64_t mine = 0;
+        for (int k = 0; k < kPer; ++k) mine += sums[tid * kPer + k];
+        int64_t before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (tid >= o) before += up;
+        }
+        if (tid == 31) sums[kLatThreads] = before;
+        before -= mine;
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t v = sums[tid * kPer + k];
+            sums[tid * kPer + k] = before;
+            before += v;
+        }
+    }
+    __syncthreads();
+    const int64_t all = sums[kLatThreads];
+    total = all * p.chunks;
+    // no more runs than units and tiles: a run then holds at least one of them
+    clusters = (int)min((int64_t)p.clusters, total);
+    if (cluster >= clusters) return false;
+    w.lo = total * cluster / clusters;
+    w.hi = total * (cluster + 1) / clusters;
+    int64_t at = sums[tid] * p.chunks;
+    if (at <= w.lo && w.lo < (sums[tid] + cost) * p.chunks) {
+        for (int b = b0; b < b1; ++b) {
+            const int c = latent_cost(latent_ctx(p, b));
+            if (w.lo < at + (int64_t)c * p.chunks) {
+                const int chunk = (int)((w.lo - at) / c);
+                sums[kLatThreads + 1] = b;
+                sums[kLatThreads + 2] = chunk;
+                sums[kLatThreads + 3] = at + (int64_t)chunk * c;
+                break;
+            }
+            at += (int64_t)c * p.chunks;
+        }
+    }
+    __syncthreads();
+    w.b = (int)sums[kLatThreads + 1];
+    w.chunk = (int)sums[kLatThreads + 2];
+    w.start = sums[kLatThreads + 3];
+    return true;
+}
+
+// ---- small pieces -------------------------------------------------------------------------------
+// Descriptor of P^T as an MN-major operand of R elements a row: the swizzle is as wide as the row.
+template <int R>
+__device__ __forceinline__ uint64_t latent_p_desc(uint32_t addr)
+{
+    constexpr uint64_t kMode = R == 64 ? 2 : R == 32 ? 4 : 6;
+    constexpr uint32_t kGroup = 8 * R * 2;  // eight tokens
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kGroup >> 4) << 16) | ((uint64_t)(kGroup >> 4) << 32) | (1ull << 46) |
+           (kMode << 61);
+}
+
+// Where 16-byte unit u of token t's weights lies.
+template <int R>
+__device__ __forceinline__ uint32_t latent_p_at(int t, int u)
+{
+    const int x = R == 64 ? t & 7 : R == 32 ? (t >> 1) & 3 : (t >> 2) & 1;
+    return (uint32_t)(t * (R * 2) + ((u ^ x) << 4));
+}
+
+__device__ __forceinline__ void tma_load_4d_multicast(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                                      int c3, uint16_t ctas)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(ctas)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// tc_commit that arrives at the same barrier of both CTAs of the cluster.
+__device__ __forceinline__ void tc_commit_both(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// C columns of a warp's 32 lanes (C = 8, 16 or 32).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+template <int C>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&x)[C])
+{
+    if constexpr (C == 8) {
+        uint32_t r[8];
+        tmem_ld8(taddr, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = __uint_as_float(r[c]);
+    } else {
+        uint32_t r[C / 16][16];
+#pragma unroll
+        for (int k = 0; k < C / 16; ++k) tmem_ld16(taddr + 16 * k, r[k]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = __uint_as_float(r[c / 16][c % 16]);
+    }
+}
+template <int C>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&x)[C])
+{
+    if constexpr (C == 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) r[c] = __float_as_uint(x[c]);
+        tmem_st8(taddr, r);
+    } else {
+#pragma unroll
+        for (int k = 0; k < C / 16; ++k) {
+            uint32_t r[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(x[16 * k + c]);
+            tmem_st16(taddr + 16 * k, r);
+        }
+    }
+}
+
+// Reduce column c of a warp's 32 lanes for C columns at once; lane l receives column l % C.  x is used up.
+template <int C, typename Op>
+__device__ __forceinline__ float reduce_columns(float (&x)[C], int lane, Op op)
+{
+#pragma unroll
+    for (int o = C / 2; o >= 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float give = up ? x[j] : x[j + o], keep = up ? x[j + o] : x[j];
+            x[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+        }
+    }
+    float v = x[0];
+#pragma unroll
+    for (int o = C; o < 32; o <<= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// Barrier of the four warps of one half of the rows (128 threads), and the same with a vote.
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ bool half_any(int half, bool v)
+{
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(1 + half), "r"((int)v)
+        : "memory");
+    return r != 0;
+}
+
+template <int R, bool Two>
+__global__ void __launch_bounds__(kLatThreads, 1)
+latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q, const LatentAttnParams p)
+{
+    using L = LatentLayout<R, Two>;
+    constexpr int S = L::kStages;
+    constexpr int CW = R / 2;  // rows (columns of S^T) of a softmax thread
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t sums[kLatThreads + 4];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const mem = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = Two ? (int)cluster_rank() : 0;
+    const int cluster = Two ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    LatentWalk walk;
+    int64_t total;
+    int clusters;
+    if (!latent_deal(p, cluster, sums, walk, total, clusters)) return;  // both CTAs of a cluster alike
+
+    const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
+    const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * S, bar_qfull = bar_empty + 8 * S,
+                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_fin = bar_pv + 8;
+    volatile int *const tile_mask = reinterpret_cast<volatile int *>(mem + ((L::kMiscOffset + 15) & ~15));  // [4], by tile % 4
+    volatile int *const abort_flag = tile_mask + 4;
+    volatile uint32_t *const tmem_slot = reinterpret_cast<volatile uint32_t *>(tile_mask + 5);
+    volatile int *const issued = tile_mask + 6;
+    volatile int *const own_bytes = tile_mask + 8;        // [S]: of a stage's last load, what this CTA fetches
+    volatile int *const all_bytes = own_bytes + S;        // [S]: and what both fetch
+    int *const limit = const_cast<int *>(own_bytes + L::kStageWords);                     // [R] tokens a row sees
+    float *const top = reinterpret_cast<float *>(limit + R);                     // [R] running maxima (log2)
+    float *const factor = top + R;                                               // [R]
+    float *const quarters = factor + R;                                          // [4][R]
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        *issued = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, Two ? 2 : 1);
+        }
+        mbar_init(bar_qfull, 1);
+        mbar_init(bar_qfree, 1);
+        mbar_init(bar_s, 1);
+        mbar_init(bar_s + 8, 1);
+        mbar_init(bar_p, kLatSoftmaxWarps);
+        mbar_init(bar_pv, 1);
+        mbar_init(bar_fin, 1);
+        fence_barrier_init();
+    }
+    if (warp == kLatMmaWarp) {
+        tmem_alloc(smem_u32((const void *)tmem_slot), L::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if constexpr (Two) cluster_sync();  // the other CTA's barriers exist
+    const uint32_t tm_o = *tmem_slot, tm_s = tm_o + 4 * R;
+
+    auto give_up = [&]() {
+        if (lane == 0 && !*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+        *abort_flag = 1;
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns));
+    };
+
+    uint32_t q_loads = 0;  // segments whose queries were asked for (the loading warp)
+    if (warp == kLatLoadWarp) {
+        // ------------------------------ loads ------------------------------
+        if (lane == 0) {
+            prefetch_tensormap(&tm_c);
+            prefetch_tensormap(&tm_q);
+        }
+        int n = 0;           // stages filled so far
+        uint32_t g = 0;      // tiles so far
+        bool ok = true, withheld = false;
+        // One stage: a box per lane.  mine: this lane loads (block, chunk) to `at` in the stage.
+        auto fill = [&](bool mine, uint32_t at, int chunk, int block, int bytes_all, int bytes_own) {
+            const int s = n % S;
+            if (n >= S) ok = wait(bar_empty + 8 * s, (uint32_t)((n / S) & 1) ^ 1u);
+            if (!ok) return;
+            const uint32_t bar = bar_full + 8 * s;
+            if (lane == 0) {
+                if constexpr (Two) own_bytes[s] = bytes_own, all_bytes[s] = bytes_all;
+                mbar_arrive_expect_tx(bar, (uint32_t)bytes_all);
+            }
+            __syncwarp();
+            if (mine) {
+                const uint32_t dst = ring + s * kLatStage + at;
+                if constexpr (Two) tma_load_4d_multicast(dst, &tm_c, bar, 0, 0, chunk, block, 3);
+                else tma_load_4d(dst, &tm_c, bar, 0, 0, chunk, block);
+            }
+            ++n;
+        };
+        // V: 64 tokens (blocks 4 h ..) x 128 elements; lane: element half lane / 4, block lane % 4
+        auto fill_v = [&](int ids, uint32_t mask, int nblk) {
+            for (int h = 0; h < 2 && ok; ++h) {
+                if (4 * h >= nblk) break;
+                const int there = __popc(mask & (0xFu << (4 * h)));
+                const int half = lane >> 2, j = 4 * h + (lane & 3);
+                const int id = __shfl_sync(0xFFFFFFFFu, ids, j & 7);
+                const bool mine = lane < 8 && ((mask >> j) & 1u) && (!Two || half == rank);
+#pragma unroll 1
+                for (int m = 0; m < 4 && ok; ++m)
+                    fill(mine, (uint32_t)(half * (kLatStage / 2) + (lane & 3) * kLatBox), 2 * m + half, id, 2 * there * kLatBox,
+                         there * kLatBox);
+            }
+        };
+        LatentSegment sg;
+        while (ok && walk.next(p, sg)) {
+            // the queries, once the last unit's are no longer needed
+            if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
+            if (!ok) break;
+            const int64_t row = (int64_t)sg.b * p.rows + sg.chunk * (Two ? 2 * R : R) + rank * R;
+            if (lane == 0) mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
+            __syncwarp();
+            if (lane < kLatChunks) tma_load_3d(q_u32 + lane * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, lane);
+            ++q_loads;
+            const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
+            const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
+            auto ids_of = [&](int t) {
+                const int j = t * kLatTileBlocks + lane;
+                return lane < kLatTileBlocks && j < nb ? __ldg(tbl + j) : -1;
+            };
+            int next = ids_of(sg.t0), prev = -1;
+            uint32_t prev_mask = 0;
+            int prev_nblk = 0;
+            for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
+                const int ids = next;
+                if (t + 1 < sg.t1) next = ids_of(t + 1);
+                const int nblk = min(kLatTileBlocks, nb - t * kLatTileBlocks);
+                const bool good = lane < nblk && ids >= 0 && ids < p.num_blocks;
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+                if (mask != (1u << nblk) - 1u && lane == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                if (lane == 0) tile_mask[g & 3] = (int)mask;
+                // (published by the arrival of this tile's first stage)
+                __syncwarp();
+                const uint32_t half_mask = Two ? mask & (0xFu << (4 * rank)) : mask;
+                if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
+                    withheld = true, ok = false;
+                    break;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kLatChunks && ok; ++c)
+                    fill(lane < 8 && ((half_mask >> lane) & 1u), (uint32_t)(lane * kLatBox), c, ids, __popc(mask) * kLatBox,
+                         __popc(half_mask) * kLatBox);
+                if (t > sg.t0 && ok) fill_v(prev, prev_mask, prev_nblk);
+                prev = ids, prev_mask = mask, prev_nblk = nblk;
+            }
+            if (ok) fill_v(prev, prev_mask, prev_nblk);
+        }
+        if (!ok && !withheld) give_up();
+        if (lane == 0) *issued = n;
+        // every stage released, by both CTAs: nothing is on its way into this CTA's barriers any more
+        for (int k = max(0, n - S); k < n && ok; ++k) ok = wait(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
+        if (!ok && !withheld) give_up();
+    } else if (warp == kLatMmaWarp) {
+        // ------------------------------ MMAs ------------------------------
+        constexpr uint32_t kIdS = idesc_bf16_f32(128, R, 0, 0), kIdO = idesc_bf16_f32(128, R, 1, 1);
+        int n = 0;
+        uint32_t g = 0, unit = 0;
+        bool ok = true, started = false;
+        auto release = [&](int s) {
+            if constexpr (Two) tc_commit_both(bar_empty + 8 * s);
+            else tc_commit(bar_empty + 8 * s);
+        };
+        // P V of tile number gt, whose last block (if tail > 0) holds `tail` tokens
+        auto pv = [&](uint32_t gt, int nblk, int tail) {
+            ok = wait(bar_p, gt & 1);
+            if (!ok) return;
+            const uint32_t mask = (uint32_t)tile_mask[gt & 3];
+            const int first = __ffs(mask) - 1;
+            for (int h = 0; h < 2 && ok; ++h) {
+                if (4 * h >= nblk) break;
+#pragma unroll 1
+                for (int m = 0; m < 4 && ok; ++m, ++n) {
+                    const int s = n % S;
+                    ok = wait(bar_full + 8 * s, (uint32_t)((n / S) & 1));
+                    if (!ok) break;
+                    const uint32_t st = ring + s * kLatStage;
+                    if (tail > 0 && (nblk - 1) / 4 == h && ((mask >> (nblk - 1)) & 1u)) {
+                        // rows behind the sequence's end may hold anything: their weights are zero, but 0 x NaN is NaN
+                        const uint32_t blk = st + ((nblk - 1) & 3) * kLatBox;
+                        for (int x = lane; x < 2 * (kBlockSize - tail) * 8; x += 32) {
+                            const int d = x & 1, u = (x >> 1) & 7, row = tail + (x >> 4);
+                            st_shared_v4(blk + d * (kLatStage / 2) + row * 128 + u * 16, make_uint4(0u, 0u, 0u, 0u));
+                        }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int blk = 4 * h + j;
+                            if ((mask >> blk) & 1u)
+                                tc_mma_ss(tm_o + m * R, smem_desc_sw128(st + j * kLatBox, kLatStage / 2, 1024),
+                                          latent_p_desc<R>(p_u32 + blk * kBlockSize * L::kPLine), kIdO, started || blk > first);
+                        }
+                        release(s);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (ok && mask) started = true;
+            if (ok && lane == 0) tc_commit(bar_pv);
+            __syncwarp();
+        };
+        LatentSegment sg;
+        while (ok && walk.next(p, sg)) {
+            ok = wait(bar_qfull, unit & 1);
+            ++unit;
+            started = false;
+            const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
+            auto blocks = [&](int t) { return min(kLatTileBlocks, nb - t * kLatTileBlocks); };
+            auto tail = [&](int t) { return t + 1 == sg.tiles ? sg.ctx % kBlockSize : 0; };
+            for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
+                const uint32_t d = tm_s + R * (g & 1);
+#pragma unroll 1
+                for (int c = 0; c < kLatChunks && ok; ++c, ++n) {
+                    const int s = n % S;
+                    ok = wait(bar_full + 8 * s, (uint32_t)((n / S) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t a = ring + s * kLatStage, b = q_u32 + c * L::kQChunk;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_ss(d, smem_desc_sw128(a + 32 * k, 16, 1024), smem_desc_sw128(b + 32 * k, 16, 1024), kIdS, c + k > 0);
+                        release(s);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (lane == 0) {
+                    tc_commit(bar_s + 8 * (g & 1));
+                    if (t + 1 == sg.t1) tc_commit(bar_qfree);
+                }
+                __syncwarp();
+                if (t > sg.t0) pv(g - 1, blocks(t - 1), tail(t - 1));
+            }
+            if (ok) pv(g - 1, blocks(sg.t1 - 1), tail(sg.t1 - 1));
+        }
+        if (!ok) give_up();
+    } else {
+        // ------------------------------ softmax and outputs ------------------------------
+        const int quarter = warp & 3, half = warp >> 2, tok = 32 * quarter + lane, c0 = half * CW;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const int col = lane & (CW - 1);  // the column this lane holds after a reduction
+        uint32_t g = 0;
+        bool ok = true;
+        LatentSegment sg;
+        while (ok && walk.next(p, sg)) {
+            const int row0 = sg.chunk * (Two ? 2 * R : R) + rank * R;  // first row of this CTA within the sequence
+            const int nrows = min(R, p.rows - row0);
+            if (threadIdx.x == 0 && rank == 0 && sg.t0 == 0) {
+                // for the joining launch: the first cluster of the unit's parts, and how many there are
+                const int64_t last = sg.start + sg.tiles + kLatUnitCost - 1;
+                const int parts = sg.whole ? 1 : (int)(((last + 1) * clusters - 1) / total) - cluster + 1;
+                p.unit_parts[(int64_t)sg.b * p.chunks + sg.chunk] = make_int2(cluster, parts);
+            }
+            if (quarter == 0 && lane < CW) {
+                const int r = row0 + c0 + lane;
+                limit[c0 + lane] = c0 + lane < nrows ? sg.ctx - p.T + r / p.N + 1 : 0;
+                top[c0 + lane] = -FLT_MAX;
+            }
+            half_sync(half);
+            float l[CW];
+#pragma unroll
+            for (int c = 0; c < CW; ++c) l[c] = 0.f;
+            // The barriers below count all four warps of a half, so a warp whose wait gave up leaves only where
+            // all four agree on it, at the votes that open a tile and the outputs.
+            bool left = false;
+            for (int t = sg.t0; t < sg.t1; ++t, ++g) {
+                if (ok) ok = wait(bar_s + 8 * (g & 1), (g >> 1) & 1);
+                if (!ok) give_up();
+                left = half_any(half, !ok);
+                if (left) break;
+                tc_fence_after();
+                float x[CW];
+                tmem_load<CW>(lanes + tm_s + R * (g & 1) + c0, x);
+                const int at = t * kLatTile + tok;
+                const bool here = at < sg.ctx && (((uint32_t)tile_mask[g & 3] >> (tok / kBlockSize)) & 1u);
+                if (sg.ctx - p.T + 1 >= (t + 1) * kLatTile) {  // every row sees the whole tile
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) x[c] = here ? x[c] * p.scale_log2 : -INFINITY;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) x[c] = here && at < limit[c0 + c] ? x[c] * p.scale_log2 : -INFINITY;
+                }
+                float m[CW];
+                auto load_top = [&]() {
+#pragma unroll
+                    for (int c = 0; c < CW; c += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(top + c0 + c);
+                        m[c] = v.x, m[c + 1] = v.y, m[c + 2] = v.z, m[c + 3] = v.w;
+                    }
+                };
+                load_top();
+                float over = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < CW; ++c) over = fmaxf(over, x[c] - m[c]);
+                const bool raise = half_any(half, over > kLatRescale);
+                if (g > 0) ok = wait(bar_pv, (g - 1) & 1);  // P and O^T are free
+                if (!ok) give_up();
+                if (raise) {
+                    float v[CW];
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) v[c] = x[c];
+                    const float w = reduce_columns<CW>(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < CW) quarters[quarter * R + c0 + lane] = w;
+                    half_sync(half);
+                    if (quarter == 0 && lane < CW) {
+                        const float *f = quarters + c0 + lane;
+                        const float hi = fmaxf(fmaxf(f[0], f[R]), fmaxf(f[2 * R], f[3 * R])), old = top[c0 + lane];
+                        const bool up = hi > old + kLatRescale || (old == -FLT_MAX && hi > old);
+                        factor[c0 + lane] = up ? exp2_sfu(old - hi) : 1.f;
+                        if (up) top[c0 + lane] = hi;
+                    }
+                    half_sync(half);
+                    load_top();
+                    float f[CW];
+#pragma unroll
+                    for (int c = 0; c < CW; c += 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(factor + c0 + c);
+                        f[c] = u.x, f[c + 1] = u.y, f[c + 2] = u.z, f[c + 3] = u.w;
+                    }
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) l[c] *= f[c];
+                    if (t > sg.t0) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int mb = 0; mb < 4; ++mb) {
+                            tmem_load<CW>(lanes + tm_o + mb * R + c0, v);
+#pragma unroll
+                            for (int c = 0; c < CW; ++c) v[c] *= f[c];
+                            tmem_store<CW>(lanes + tm_o + mb * R + c0, v);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // weights: rounded to bf16 for the product, summed as they are
+#pragma unroll
+                for (int u = 0; u < CW / 8; ++u) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 8 * u + 2 * k;
+                        const float a = exp2_sfu(x[c] - m[c]), b = exp2_sfu(x[c + 1] - m[c + 1]);
+                        w[k] = pack_bf16x2(a, b);
+                        l[c] += a;
+                        l[c + 1] += b;
+                    }
+                    st_shared_v4(p_u32 + latent_p_at<R>(tok, c0 / 8 + u), make_uint4(w[0], w[1], w[2], w[3]));
+                }
+                fence_proxy_async_shared();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(bar_p);
+            }
+            if (!left) {
+                if (ok) ok = wait(bar_pv, (g - 1) & 1);
+                left = half_any(half, !ok);
+            }
+            if (left) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // sums over the tokens: of the warp, then of the four warps
+            const float sum = reduce_columns<CW>(l, lane, [](float a, float b) { return a + b; });
+            if (lane < CW) quarters[quarter * R + c0 + lane] = sum;
+            half_sync(half);
+            const float *f = quarters + c0 + col;
+            const float all = (f[0] + f[R]) + (f[2 * R] + f[3 * R]), hi = top[c0 + col];
+            const bool seen = hi != -FLT_MAX;
+            const int64_t part = (int64_t)(2 * cluster + (sg.t0 == 0)) * (Two ? 2 * R : R) + rank * R;  // rows of the workspace
+            if (quarter == 0 && lane < CW && c0 + lane < nrows) {
+                const float lse2 = seen ? hi + log2f(all) : -INFINITY;
+                const int64_t row = (int64_t)sg.b * p.rows + row0 + c0 + lane;
+                if (!sg.whole) p.part_lse[part + c0 + lane] = lse2;
+                else if (p.lse_out) p.lse_out[row] = lse2 * 0.69314718055994530942f;
+            }
+            if (quarter == 0 && lane < CW) factor[c0 + lane] = seen ? 1.f / all : 0.f;
+            half_sync(half);
+            float inv[CW];
+#pragma unroll
+            for (int c = 0; c < CW; ++c) inv[c] = factor[c0 + c];
+#pragma unroll 1
+            for (int mb = 0; mb < 4; ++mb) {
+                float o[CW];
+                tmem_load<CW>(lanes + tm_o + mb * R + c0, o);
+                const int h = mb * 128 + 32 * quarter + lane;
+#pragma unroll
+                for (int c = 0; c < CW; ++c) {
+                    if (c0 + c >= nrows) break;
+                    const float v = inv[c] == 0.f ? 0.f : o[c] * inv[c];
+                    if (sg.whole) p.out[((int64_t)sg.b * p.rows + row0 + c0 + c) * kLatentDim + h] = __float2bfloat16_rn(v);
+                    else p.part_out[(part + c0 + c) * kLatentDim + h] = v;
+                }
+            }
+            tc_fence_before();
+            half_sync(half);  // limits, maxima and factors are read
+        }
+        if (!ok) give_up();
+    }
+
+    // ------------------------------ teardown ------------------------------
+    __syncthreads();
+    if constexpr (Two) cluster_sync();  // neither CTA issues anything any more
+    const bool bad = *abort_flag != 0;
+    bool peer_bad = false;
+    if constexpr (Two) peer_bad = __float_as_int(load_cluster<float>(smem_u32((const void *)abort_flag), rank ^ 1)) != 0;
+    if (bad || peer_bad) {
+        if (warp == kLatMmaWarp) {
+            // every MMA this CTA issued completes before its tensor memory is released
+            if (lane == 0) tc_commit(bar_fin);
+            __syncwarp();
+            mbar_wait_bounded(bar_fin, 0u, nullptr, kDrainLimitNs);
+        }
+        if (warp == kLatLoadWarp && lane == 0) {
+            // Every copy on its way lands before this CTA leaves.  Where one CTA filled a stage and the other did not
+            // follow, the barrier is told to expect what was sent and no more.
+            const int mine = *issued;
+            int theirs = mine;
+            if constexpr (Two) theirs = __float_as_int(load_cluster<float>(smem_u32((const void *)issued), rank ^ 1));
+            const int most = max(mine, theirs);
+            for (int k = max(0, most - S); k < most; ++k) {
+                const int s = k % S;
+                const uint32_t bar = bar_full + 8 * s;
+                if constexpr (Two) {
+                    if (k >= theirs) {
+                        const uint32_t missing = (uint32_t)(all_bytes[s] - own_bytes[s]);
+                        if (missing)
+                            asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(missing)
+                                         : "memory");
+                    } else if (k >= mine) {
+                        mbar_arrive_expect_tx(bar, (uint32_t)__float_as_int(load_cluster<float>(smem_u32((const void *)(own_bytes + s)), rank ^ 1)));
+                    }
+                }
+                mbar_wait_bounded(bar, (uint32_t)((k / S) & 1), nullptr, kDrainLimitNs);
+            }
+            if (q_loads > 0) mbar_wait_bounded(bar_qfull, (q_loads - 1) & 1, nullptr, kDrainLimitNs);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (Two) cluster_sync();
+    if (warp == kLatMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tm_o, L::kCols);
+    }
+}
+
+// ---- joining the parts of units that were cut -----------------------------------------------------
+// One CTA per row at a time, four elements a thread: out = sum_p e^(lse_p - lse) out_p, as in the other merges of partial
+// softmaxes.  It also writes the rows of sequences without tokens, which no cluster has.
+constexpr int kLatJoinThreads = kLatentDim / 4;
+
+__global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const LatentAttnParams p, int chunk_rows, int64_t all_rows)
+{
+    __shared__ float weight[kLatentMaxClusters];
+    __shared__ float total_lse;
+    const int tid = threadIdx.x;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    for (int64_t row = blockIdx.x; row < all_rows; row += gridDim.x) {
+        const int b = (int)(row / p.rows), r = (int)(row - (int64_t)b * p.rows);
+        const int chunk = r / chunk_rows, cr = r - chunk * chunk_rows;
+        uint2 *out = reinterpret_cast<uint2 *>(p.out + row * kLatentDim) + tid;
+        if (latent_ctx(p, b) <= 0) {
+            // (out is 4-byte aligned)
+            uint32_t *o = reinterpret_cast<uint32_t *>(out);
+            o[0] = 0u, o[1] = 0u;
+            if (tid == 0 && p.lse_out) p.lse_out[row] = -INFINITY;
+            continue;
+        }
+        const int2 info = p.unit_parts[(int64_t)b * p.chunks + chunk];
+        const int first = max(0, min(info.x, p.clusters - 1)), parts = max(0, min(info.y, p.clusters - first));
+        if (parts <= 1) continue;
+        // part k of the unit lies in the last part of the first cluster and in the first parts of those behind it
+        auto place = [&](int k) { return (int64_t)(2 * (first + k) + (k == 0)) * chunk_rows + cr; };
+        __syncthreads();  // the last row's weights are read
+        if (tid < 32) {
+            float hi = -INFINITY;
+            for (int k = tid; k < parts; k += 32) hi = fmaxf(hi, weight[k] = __ldcg(p.part_lse + place(k)));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+            float sum = 0.f;
+            const float m = hi == -INFINITY ? 0.f : hi;
+            for (int k = tid; k < parts; k += 32) sum += weight[k] = exp2f(weight[k] - m);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            const float inv = sum > 0.f ? 1.f / sum : sum;  // no key seen: 0; NaN stays
+            for (int k = tid; k < parts; k += 32) weight[k] *= inv;
+            if (tid == 0) total_lse = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+        }
+        __syncthreads();
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float w = weight[k];
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_out + place(k) * kLatentDim) + tid);
+            acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+        }
+        uint32_t *o = reinterpret_cast<uint32_t *>(out);
+        o[0] = pack_bf16x2(acc.x, acc.y), o[1] = pack_bf16x2(acc.z, acc.w);
+        if (tid == 0 && p.lse_out) p.lse_out[row] = total_lse;
+    }
+}
+
+template <int R, bool Two>
+static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, LatentAttnParams p, int sms, cudaStream_t stream)
+{
+    using L = LatentLayout<R, Two>;
+    constexpr int kCtas = Two ? 2 : 1;
+    static int most[64] = {};  // per device: clusters that run at once
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!most[dev]) {
+        e = cudaFuncSetAttribute(latent_attn_kernel<R, Two>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if (e != cudaSuccess) return e;
+        int n = sms;
+        if constexpr (Two) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * sms), cfg.blockDim = dim3(kLatThreads), cfg.dynamicSmemBytes = L::kAlloc;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim = {2, 1, 1};
+            cfg.attrs = attr, cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<R, Two>, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        most[dev] = max(1, min(n, kLatentMaxClusters / kCtas));
+    }
+    // no more clusters than there can be tiles
+    const int64_t tiles = (int64_t)p.B * p.chunks * (((int64_t)p.max_nb + kLatTileBlocks - 1) / kLatTileBlocks);
+    p.clusters = (int)min((int64_t)most[dev], tiles);
+    e = launch_clusters(latent_attn_kernel<R, Two>, dim3(p.clusters * kCtas), dim3(kLatThreads), dim3(kCtas, 1, 1), L::kAlloc,
+                        stream, tc, tq, p);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)p.B * p.rows;
+    return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p,
+                         kCtas * R, rows);
+}
+
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
+                               int sms, cudaStream_t stream)
+{
+    if (plan.ctas == 2) return latent_attn_t<64, true>(tc, tq, p, sms, stream);
+    if (plan.cta_rows == 64) return latent_attn_t<64, false>(tc, tq, p, sms, stream);
+    if (plan.cta_rows == 32) return latent_attn_t<32, false>(tc, tq, p, sms, stream);
+    return latent_attn_t<16, false>(tc, tq, p, sms, stream);
+}
+
+}  // namespace pkv
