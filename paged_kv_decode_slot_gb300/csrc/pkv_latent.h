@@ -52,8 +52,8 @@ struct LatentAttnParams {
 #endif
 };
 
-cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
-                               int sms, cudaStream_t stream);
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tv, const CUtensorMap &tq, const LatentAttnParams &p,
+                               const LatentPlan &plan, int sms, cudaStream_t stream);
 
 // Norm and rotation of new tokens' rows with their append, and rotation of their queries (pkv_latent_append.cu).
 struct LatentAppendParams {

@@ -38,8 +38,8 @@ constexpr int kLatTile = 128;                                 // tokens of a til
 constexpr int kLatTileBlocks = kLatTile / kBlockSize;
 constexpr int kLatStage = 16384;                              // bytes of a ring stage
 constexpr int kLatBox = kBlockSize * 128;                     // bytes of one block's 64-element rows
-constexpr int kLatSoftmaxWarps = 8, kLatMmaWarp = 8, kLatLoadWarp = 9;
-constexpr int kLatThreads = 320;
+constexpr int kLatSoftmaxWarps = 8, kLatMmaWarp = 8, kLatLoadWarp = 9, kLatLoaders = 2, kLatTailWarp = 11;
+constexpr int kLatThreads = 384;
 constexpr float kLatRescale = 8.f;                            // log2 of how far a logit may exceed the running maximum
 
 // R: query rows of a CTA.  Two: the CTA is one of a cluster of two.
@@ -55,11 +55,11 @@ struct LatentLayout {
     static constexpr int kPOffset = kQBytes;
     static constexpr int kRingOffset = kPOffset + ((kPBytes + 1023) & ~1023);
     static constexpr int kBarOffset = kRingOffset + kStages * kLatStage;
-    // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, fin
-    static constexpr int kBars = 2 * kStages + 7;
+    // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, tail[2], fin
+    static constexpr int kBars = 2 * kStages + 9;
     static constexpr int kMiscOffset = kBarOffset + kBars * 8;
     static constexpr int kStageWords = (2 * kStages + 3) & ~3;  // what follows is read in vectors of four words
-    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, issued, spare */ + kStageWords /* bytes */ +
+    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, issued[2] */ + kStageWords /* bytes */ +
                                   R /* limits */ + R /* maxima */ + R /* factors */ + 4 * R /* of four warps */;
     static constexpr int kAlloc = ((kMiscOffset + 15) & ~15) + kWords * 4 + 1024;
     static_assert(kQBytes % 1024 == 0 && kRingOffset % 1024 == 0, "swizzle atoms are aligned");
@@ -168,6 +168,16 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int clust
     w.chunk = (int)sums[kLatThreads + 2];
     w.start = sums[kLatThreads + 3];
     return true;
+}
+
+// mbar_wait_bounded with the clock read late: %globaltimer takes 0.4 us to read, as long as a stage of the ring is in use, so
+// the first tries (each suspends the thread for a while) go without it.
+__device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
+{
+#pragma unroll 1
+    for (int it = 0; it < 64; ++it)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, abort, limit_ns);
 }
 
 // ---- small pieces -------------------------------------------------------------------------------
@@ -307,9 +317,29 @@ __device__ __forceinline__ bool half_any(int half, bool v)
     return r != 0;
 }
 
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// A place in the ring: stage s, and the parity of its uses.
+template <int S>
+struct RingPlace {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == S) s = 0, parity ^= 1u;
+    }
+};
+
 template <int R, bool Two>
 __global__ void __launch_bounds__(kLatThreads, 1)
-latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q, const LatentAttnParams p)
+latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_q, const LatentAttnParams p)
 {
     using L = LatentLayout<R, Two>;
     constexpr int S = L::kStages;
@@ -331,11 +361,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 
     const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
     const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * S, bar_qfull = bar_empty + 8 * S,
-                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_fin = bar_pv + 8;
+                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_tail = bar_pv + 8, bar_fin = bar_tail + 16;
     volatile int *const tile_mask = reinterpret_cast<volatile int *>(mem + ((L::kMiscOffset + 15) & ~15));  // [4], by tile % 4
     volatile int *const abort_flag = tile_mask + 4;
     volatile uint32_t *const tmem_slot = reinterpret_cast<volatile uint32_t *>(tile_mask + 5);
-    volatile int *const issued = tile_mask + 6;
+    volatile int *const issued = tile_mask + 6;           // [kLatLoaders]: stages before this one were filled
     volatile int *const own_bytes = tile_mask + 8;        // [S]: of a stage's last load, what this CTA fetches
     volatile int *const all_bytes = own_bytes + S;        // [S]: and what both fetch
     int *const limit = const_cast<int *>(own_bytes + L::kStageWords);                     // [R] tokens a row sees
@@ -345,7 +375,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        *issued = 0;
+        issued[0] = issued[1] = 0;
         for (int s = 0; s < S; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, Two ? 2 : 1);
@@ -356,6 +386,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         mbar_init(bar_s + 8, 1);
         mbar_init(bar_p, kLatSoftmaxWarps);
         mbar_init(bar_pv, 1);
+        mbar_init(bar_tail, 1);
+        mbar_init(bar_tail + 8, 1);
         mbar_init(bar_fin, 1);
         fence_barrier_init();
     }
@@ -374,61 +406,67 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         *abort_flag = 1;
     };
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns));
+        return __all_sync(0xFFFFFFFFu, latent_wait(bar, parity, abort_flag, p.wait_ns));
     };
 
-    uint32_t q_loads = 0;  // segments whose queries were asked for (the loading warp)
-    if (warp == kLatLoadWarp) {
+    auto wait_one = [&](uint32_t bar, uint32_t parity) { return latent_wait(bar, parity, abort_flag, p.wait_ns); };
+
+    uint32_t q_loads = 0;  // segments whose queries were asked for (the first loading warp)
+    if (warp >= kLatLoadWarp && warp < kLatLoadWarp + kLatLoaders) {
         // ------------------------------ loads ------------------------------
-        if (lane == 0) {
+        // The two warps take turns, a stage each; a lane issues a block's box.
+        const int me = warp - kLatLoadWarp;
+        if (lane == 0 && me == 0) {
             prefetch_tensormap(&tm_c);
+            prefetch_tensormap(&tm_v);
             prefetch_tensormap(&tm_q);
         }
-        int n = 0;           // stages filled so far
+        int n = 0;           // stages so far
+        RingPlace<S> at;
         uint32_t g = 0;      // tiles so far
         bool ok = true, withheld = false;
-        // One stage: a box per lane.  mine: this lane loads (block, chunk) to `at` in the stage.
-        auto fill = [&](bool mine, uint32_t at, int chunk, int block, int bytes_all, int bytes_own) {
-            const int s = n % S;
-            if (n >= S) ok = wait(bar_empty + 8 * s, (uint32_t)((n / S) & 1) ^ 1u);
-            if (!ok) return;
-            const uint32_t bar = bar_full + 8 * s;
-            if (lane == 0) {
-                if constexpr (Two) own_bytes[s] = bytes_own, all_bytes[s] = bytes_all;
-                mbar_arrive_expect_tx(bar, (uint32_t)bytes_all);
+        auto turn = [&]() { return (n & 1) == me; };
+        auto step = [&]() { ++n, at.next(); };
+        // The stage's barrier, told what to expect, once the stage is free.
+        auto open = [&](int bytes_all, int bytes_own) {
+            if (n >= S) ok = wait(bar_empty + 8 * at.s, at.parity ^ 1u);
+            if (ok && lane == 0) {
+                if constexpr (Two) own_bytes[at.s] = bytes_own, all_bytes[at.s] = bytes_all;
+                mbar_arrive_expect_tx(bar_full + 8 * at.s, (uint32_t)bytes_all);
             }
             __syncwarp();
-            if (mine) {
-                const uint32_t dst = ring + s * kLatStage + at;
-                if constexpr (Two) tma_load_4d_multicast(dst, &tm_c, bar, 0, 0, chunk, block, 3);
-                else tma_load_4d(dst, &tm_c, bar, 0, 0, chunk, block);
-            }
-            ++n;
         };
-        // V: 64 tokens (blocks 4 h ..) x 128 elements; lane: element half lane / 4, block lane % 4
+        // V: 64 tokens (four blocks) x 128 elements (two chunks a box)
         auto fill_v = [&](int ids, uint32_t mask, int nblk) {
-            for (int h = 0; h < 2 && ok; ++h) {
-                if (4 * h >= nblk) break;
-                const int there = __popc(mask & (0xFu << (4 * h)));
-                const int half = lane >> 2, j = 4 * h + (lane & 3);
-                const int id = __shfl_sync(0xFFFFFFFFu, ids, j & 7);
-                const bool mine = lane < 8 && ((mask >> j) & 1u) && (!Two || half == rank);
+            for (int h = 0; h < 2 && 4 * h < nblk; ++h) {
+                const uint32_t m4 = (mask >> (4 * h)) & 0xFu, own = Two ? m4 & (3u << (2 * rank)) : m4;
+                const int id = __shfl_sync(0xFFFFFFFFu, ids, (4 * h + lane) & 7);
+                const bool mine = lane < 4 && ((own >> lane) & 1u);
 #pragma unroll 1
-                for (int m = 0; m < 4 && ok; ++m)
-                    fill(mine, (uint32_t)(half * (kLatStage / 2) + (lane & 3) * kLatBox), 2 * m + half, id, 2 * there * kLatBox,
-                         there * kLatBox);
+                for (int m = 0; m < 4 && ok; ++m, step()) {
+                    if (!turn()) continue;
+                    open(2 * kLatBox * __popc(m4), 2 * kLatBox * __popc(own));
+                    if (!ok) return;
+                    if (mine) {
+                        const uint32_t dst = ring + at.s * kLatStage + lane * 2 * kLatBox, bar = bar_full + 8 * at.s;
+                        if constexpr (Two) tma_load_4d_multicast(dst, &tm_v, bar, 0, 0, 2 * m, id, 3);
+                        else tma_load_4d(dst, &tm_v, bar, 0, 0, 2 * m, id);
+                    }
+                }
             }
         };
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
-            // the queries, once the last unit's are no longer needed
-            if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
-            if (!ok) break;
-            const int64_t row = (int64_t)sg.b * p.rows + sg.chunk * (Two ? 2 * R : R) + rank * R;
-            if (lane == 0) mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
-            __syncwarp();
-            if (lane < kLatChunks) tma_load_3d(q_u32 + lane * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, lane);
-            ++q_loads;
+            if (me == 0) {
+                // the queries, once the last unit's are no longer needed
+                if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
+                if (!ok) break;
+                const int64_t row = (int64_t)sg.b * p.rows + sg.chunk * (Two ? 2 * R : R) + rank * R;
+                if (lane == 0) mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
+                __syncwarp();
+                if (lane < kLatChunks) tma_load_3d(q_u32 + lane * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, lane);
+                ++q_loads;
+            }
             const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
             const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
             auto ids_of = [&](int t) {
@@ -443,118 +481,154 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 if (t + 1 < sg.t1) next = ids_of(t + 1);
                 const int nblk = min(kLatTileBlocks, nb - t * kLatTileBlocks);
                 const bool good = lane < nblk && ids >= 0 && ids < p.num_blocks;
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
-                if (mask != (1u << nblk) - 1u && lane == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-                if (lane == 0) tile_mask[g & 3] = (int)mask;
-                // (published by the arrival of this tile's first stage)
-                __syncwarp();
-                const uint32_t half_mask = Two ? mask & (0xFu << (4 * rank)) : mask;
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good), own = Two ? mask & (0xFu << (4 * rank)) : mask;
+                if (lane == 0) {
+                    if (mask != (1u << nblk) - 1u) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                    tile_mask[g & 3] = (int)mask;  // both warps write it, each before it fills a stage of the tile
+                }
                 if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
                     withheld = true, ok = false;
                     break;
                 }
+                const bool mine = lane < 8 && ((own >> lane) & 1u);
 #pragma unroll 1
-                for (int c = 0; c < kLatChunks && ok; ++c)
-                    fill(lane < 8 && ((half_mask >> lane) & 1u), (uint32_t)(lane * kLatBox), c, ids, __popc(mask) * kLatBox,
-                         __popc(half_mask) * kLatBox);
+                for (int c = 0; c < kLatChunks && ok; ++c, step()) {
+                    if (!turn()) continue;
+                    open(kLatBox * __popc(mask), kLatBox * __popc(own));
+                    if (!ok) break;
+                    if (mine) {
+                        const uint32_t dst = ring + at.s * kLatStage + lane * kLatBox, bar = bar_full + 8 * at.s;
+                        if constexpr (Two) tma_load_4d_multicast(dst, &tm_c, bar, 0, 0, c, ids, 3);
+                        else tma_load_4d(dst, &tm_c, bar, 0, 0, c, ids);
+                    }
+                }
                 if (t > sg.t0 && ok) fill_v(prev, prev_mask, prev_nblk);
                 prev = ids, prev_mask = mask, prev_nblk = nblk;
             }
             if (ok) fill_v(prev, prev_mask, prev_nblk);
         }
         if (!ok && !withheld) give_up();
-        if (lane == 0) *issued = n;
+        if (lane == 0) issued[me] = n;
         // every stage released, by both CTAs: nothing is on its way into this CTA's barriers any more
-        for (int k = max(0, n - S); k < n && ok; ++k) ok = wait(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
+        for (int k = max(0, n - S); k < n && ok; ++k)
+            if ((k & 1) == me) ok = wait(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
         if (!ok && !withheld) give_up();
-    } else if (warp == kLatMmaWarp) {
-        // ------------------------------ MMAs ------------------------------
-        constexpr uint32_t kIdS = idesc_bf16_f32(128, R, 0, 0), kIdO = idesc_bf16_f32(128, R, 1, 1);
+    } else if (warp == kLatTailWarp) {
+        // ---------------- rows behind a sequence's end ----------------
+        // They may hold anything, and 0 x NaN is NaN: they are zeroed before P V reads them, when the MMA warp asks for it
+        // (asked and answered in turn, so that neither can be a use of the stage ahead of the other).
         int n = 0;
-        uint32_t g = 0, unit = 0;
-        bool ok = true, started = false;
-        auto release = [&](int s) {
-            if constexpr (Two) tc_commit_both(bar_empty + 8 * s);
-            else tc_commit(bar_empty + 8 * s);
-        };
-        // P V of tile number gt, whose last block (if tail > 0) holds `tail` tokens
-        auto pv = [&](uint32_t gt, int nblk, int tail) {
-            ok = wait(bar_p, gt & 1);
-            if (!ok) return;
-            const uint32_t mask = (uint32_t)tile_mask[gt & 3];
-            const int first = __ffs(mask) - 1;
-            for (int h = 0; h < 2 && ok; ++h) {
-                if (4 * h >= nblk) break;
-#pragma unroll 1
-                for (int m = 0; m < 4 && ok; ++m, ++n) {
-                    const int s = n % S;
-                    ok = wait(bar_full + 8 * s, (uint32_t)((n / S) & 1));
-                    if (!ok) break;
-                    const uint32_t st = ring + s * kLatStage;
-                    if (tail > 0 && (nblk - 1) / 4 == h && ((mask >> (nblk - 1)) & 1u)) {
-                        // rows behind the sequence's end may hold anything: their weights are zero, but 0 x NaN is NaN
-                        const uint32_t blk = st + ((nblk - 1) & 3) * kLatBox;
-                        for (int x = lane; x < 2 * (kBlockSize - tail) * 8; x += 32) {
-                            const int d = x & 1, u = (x >> 1) & 7, row = tail + (x >> 4);
-                            st_shared_v4(blk + d * (kLatStage / 2) + row * 128 + u * 16, make_uint4(0u, 0u, 0u, 0u));
-                        }
-                        fence_proxy_async_shared();
-                        __syncwarp();
-                    }
-                    tc_fence_after();
-                    if (lane == 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int blk = 4 * h + j;
-                            if ((mask >> blk) & 1u)
-                                tc_mma_ss(tm_o + m * R, smem_desc_sw128(st + j * kLatBox, kLatStage / 2, 1024),
-                                          latent_p_desc<R>(p_u32 + blk * kBlockSize * L::kPLine), kIdO, started || blk > first);
-                        }
-                        release(s);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (ok && mask) started = true;
-            if (ok && lane == 0) tc_commit(bar_pv);
-            __syncwarp();
-        };
+        uint32_t asked = 0;
+        bool ok = true;
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
-            ok = wait(bar_qfull, unit & 1);
-            ++unit;
-            started = false;
-            const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
-            auto blocks = [&](int t) { return min(kLatTileBlocks, nb - t * kLatTileBlocks); };
-            auto tail = [&](int t) { return t + 1 == sg.tiles ? sg.ctx % kBlockSize : 0; };
-            for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
-                const uint32_t d = tm_s + R * (g & 1);
-#pragma unroll 1
-                for (int c = 0; c < kLatChunks && ok; ++c, ++n) {
-                    const int s = n % S;
-                    ok = wait(bar_full + 8 * s, (uint32_t)((n / S) & 1));
+            const int count = sg.t1 - sg.t0, tail = sg.ctx % kBlockSize;
+            int last = 8;  // stages of the last tile's values
+            if (sg.t1 == sg.tiles) {
+                const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize - (sg.tiles - 1) * kLatTileBlocks;
+                last = nblk > 4 ? 8 : 4;
+                const int first = n + kLatChunks * count + 8 * (count - 1) + last - 4;
+                for (int k = first; k < first + 4 && tail > 0 && ok; ++k) {
+                    ok = wait(bar_tail, asked++ & 1);
                     if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t a = ring + s * kLatStage, b = q_u32 + c * L::kQChunk;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_ss(d, smem_desc_sw128(a + 32 * k, 16, 1024), smem_desc_sw128(b + 32 * k, 16, 1024), kIdS, c + k > 0);
-                        release(s);
+                    const uint32_t blk = ring + (k % S) * kLatStage + ((nblk - 1) & 3) * 2 * kLatBox;
+                    for (int x = lane; x < 2 * (kBlockSize - tail) * 8; x += 32) {
+                        const int d = x & 1, u = (x >> 1) & 7, row = tail + (x >> 4);
+                        st_shared_v4(blk + d * kLatBox + row * 128 + u * 16, make_uint4(0u, 0u, 0u, 0u));
                     }
+                    fence_proxy_async_shared();
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_tail + 8);
                 }
-                if (!ok) break;
-                if (lane == 0) {
-                    tc_commit(bar_s + 8 * (g & 1));
-                    if (t + 1 == sg.t1) tc_commit(bar_qfree);
-                }
-                __syncwarp();
-                if (t > sg.t0) pv(g - 1, blocks(t - 1), tail(t - 1));
             }
-            if (ok) pv(g - 1, blocks(sg.t1 - 1), tail(sg.t1 - 1));
+            n += kLatChunks * count + 8 * (count - 1) + last;
         }
         if (!ok) give_up();
+    } else if (warp == kLatMmaWarp) {
+        // ------------------------------ MMAs: one thread ------------------------------
+        if (elect_one()) {
+            constexpr uint32_t kIdS = idesc_bf16_f32(128, R, 0, 0), kIdO = idesc_bf16_f32(128, R, 1, 1);
+            // descriptors: an address moves the low word alone
+            const uint64_t k_desc = smem_desc_sw128(ring, 16, 1024), q_desc = smem_desc_sw128(q_u32, 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(ring, kLatBox, 1024), p_desc = latent_p_desc<R>(p_u32);
+            RingPlace<S> at;
+            uint32_t g = 0, unit = 0, tails = 0;
+            bool ok = true, started = false;
+            auto release = [&](int s) {
+                if constexpr (Two) tc_commit_both(bar_empty + 8 * s);
+                else tc_commit(bar_empty + 8 * s);
+            };
+            // P V of tile number gt; has_tail: its last block's end is zeroed first
+            auto pv = [&](uint32_t gt, int nblk, bool has_tail) {
+                ok = wait_one(bar_p, gt & 1);
+                if (!ok) return;
+                const uint32_t mask = (uint32_t)tile_mask[gt & 3];
+                const int first = __ffs(mask) - 1;
+                for (int h = 0; h < 2 && 4 * h < nblk; ++h) {
+                    const bool here = has_tail && (nblk - 1) / 4 == h;
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m, at.next()) {
+                        ok = wait_one(bar_full + 8 * at.s, at.parity);
+                        if (ok && here) {
+                            mbar_arrive(bar_tail);
+                            ok = wait_one(bar_tail + 8, tails++ & 1);
+                        }
+                        if (!ok) return;
+                        tc_fence_after();
+                        const uint64_t a = v_desc + (uint32_t)(at.s * (kLatStage >> 4)), b = p_desc + (uint32_t)((4 * h * kBlockSize * L::kPLine) >> 4);
+                        const uint32_t d = tm_o + m * R;
+                        if (mask == 0xFFu) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tc_mma_ss(d, a + j * (2 * kLatBox >> 4), b + j * (kBlockSize * L::kPLine >> 4), kIdO,
+                                          started || h > 0 || j > 0);
+                        } else {
+#pragma unroll 1
+                            for (int j = 0; j < 4; ++j)
+                                if ((mask >> (4 * h + j)) & 1u)
+                                    tc_mma_ss(d, a + j * (2 * kLatBox >> 4), b + j * (kBlockSize * L::kPLine >> 4), kIdO,
+                                              started || 4 * h + j > first);
+                        }
+                        release(at.s);
+                    }
+                }
+                if (mask) started = true;
+                tc_commit(bar_pv);
+            };
+            LatentSegment sg;
+            while (ok && walk.next(p, sg)) {
+                ok = wait_one(bar_qfull, unit & 1);
+                ++unit;
+                started = false;
+                const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
+                auto pv_tile = [&](uint32_t gt, int t) {
+                    pv(gt, min(kLatTileBlocks, nb - t * kLatTileBlocks), t + 1 == sg.tiles && sg.ctx % kBlockSize > 0);
+                };
+                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
+                    const uint32_t d = tm_s + R * (g & 1);
+#pragma unroll 1
+                    for (int c = 0; c < kLatChunks; ++c, at.next()) {
+                        ok = wait_one(bar_full + 8 * at.s, at.parity);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t a = k_desc + (uint32_t)(at.s * (kLatStage >> 4)), b = q_desc + (uint32_t)(c * (L::kQChunk >> 4));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tc_mma_ss(d, a + 2 * k, b + 2 * k, kIdS, c + k > 0);
+                        release(at.s);
+                    }
+                    if (!ok) break;
+                    tc_commit(bar_s + 8 * (g & 1));
+                    if (t + 1 == sg.t1) tc_commit(bar_qfree);
+                    if (t > sg.t0) pv_tile(g - 1, t - 1);
+                }
+                if (ok) pv_tile(g - 1, sg.t1 - 1);
+            }
+            if (!ok) {
+                if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+                *abort_flag = 1;
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------ softmax and outputs ------------------------------
         const int quarter = warp & 3, half = warp >> 2, tok = 32 * quarter + lane, c0 = half * CW;
@@ -614,8 +688,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 #pragma unroll
                 for (int c = 0; c < CW; ++c) over = fmaxf(over, x[c] - m[c]);
                 const bool raise = half_any(half, over > kLatRescale);
-                if (g > 0) ok = wait(bar_pv, (g - 1) & 1);  // P and O^T are free
-                if (!ok) give_up();
                 if (raise) {
                     float v[CW];
 #pragma unroll
@@ -632,40 +704,33 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     }
                     half_sync(half);
                     load_top();
-                    float f[CW];
-#pragma unroll
-                    for (int c = 0; c < CW; c += 4) {
-                        const float4 u = *reinterpret_cast<const float4 *>(factor + c0 + c);
-                        f[c] = u.x, f[c + 1] = u.y, f[c + 2] = u.z, f[c + 3] = u.w;
-                    }
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) l[c] *= f[c];
-                    if (t > sg.t0) {
-                        tc_fence_after();
+                    if (g > 0) ok = wait(bar_pv, (g - 1) & 1);
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int mb = 0; mb < 4; ++mb) {
-                            tmem_load<CW>(lanes + tm_o + mb * R + c0, v);
+                    for (int mb = 0; mb < 4 && t > sg.t0; ++mb) {
+                        tmem_load<CW>(lanes + tm_o + mb * R + c0, v);
 #pragma unroll
-                            for (int c = 0; c < CW; ++c) v[c] *= f[c];
-                            tmem_store<CW>(lanes + tm_o + mb * R + c0, v);
-                        }
-                        tmem_st_wait();
+                        for (int c = 0; c < CW; ++c) v[c] *= factor[c0 + c];
+                        tmem_store<CW>(lanes + tm_o + mb * R + c0, v);
                     }
+                    tmem_st_wait();
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) l[c] *= factor[c0 + c];
                 }
                 // weights: rounded to bf16 for the product, summed as they are
+                uint32_t w[CW / 2];
 #pragma unroll
-                for (int u = 0; u < CW / 8; ++u) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = 8 * u + 2 * k;
-                        const float a = exp2_sfu(x[c] - m[c]), b = exp2_sfu(x[c + 1] - m[c + 1]);
-                        w[k] = pack_bf16x2(a, b);
-                        l[c] += a;
-                        l[c + 1] += b;
-                    }
-                    st_shared_v4(p_u32 + latent_p_at<R>(tok, c0 / 8 + u), make_uint4(w[0], w[1], w[2], w[3]));
+                for (int c = 0; c < CW; c += 2) {
+                    const float a = exp2_sfu(x[c] - m[c]), b = exp2_sfu(x[c + 1] - m[c + 1]);
+                    w[c / 2] = pack_bf16x2(a, b);
+                    l[c] += a;
+                    l[c + 1] += b;
                 }
+                if (g > 0) ok = wait(bar_pv, (g - 1) & 1) && ok;  // the last tile's weights are no longer needed
+                if (!ok) give_up();
+#pragma unroll
+                for (int u = 0; u < CW / 8; ++u)
+                    st_shared_v4(p_u32 + latent_p_at<R>(tok, c0 / 8 + u), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
                 fence_proxy_async_shared();
                 tc_fence_before();
                 __syncwarp();
@@ -734,20 +799,26 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         if (warp == kLatLoadWarp && lane == 0) {
             // Every copy on its way lands before this CTA leaves.  Where one CTA filled a stage and the other did not
             // follow, the barrier is told to expect what was sent and no more.
-            const int mine = *issued;
-            int theirs = mine;
-            if constexpr (Two) theirs = __float_as_int(load_cluster<float>(smem_u32((const void *)issued), rank ^ 1));
-            const int most = max(mine, theirs);
-            for (int k = max(0, most - S); k < most; ++k) {
+            int mine[kLatLoaders], theirs[kLatLoaders], most = 0;
+            for (int w = 0; w < kLatLoaders; ++w) {
+                mine[w] = theirs[w] = issued[w];
+                if constexpr (Two) theirs[w] = __float_as_int(load_cluster<float>(smem_u32((const void *)(issued + w)), rank ^ 1));
+                most = max(most, max(mine[w], theirs[w]));
+            }
+            uint32_t seen = 0;  // stages whose last use was looked at
+            for (int k = most - 1; k >= 0 && k >= most - 2 * S; --k) {
                 const int s = k % S;
+                const bool own = k < mine[k & 1], other = k < theirs[k & 1];
+                if (((seen >> s) & 1u) || (!own && !other)) continue;
+                seen |= 1u << s;
                 const uint32_t bar = bar_full + 8 * s;
                 if constexpr (Two) {
-                    if (k >= theirs) {
+                    if (!other) {
                         const uint32_t missing = (uint32_t)(all_bytes[s] - own_bytes[s]);
                         if (missing)
                             asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(missing)
                                          : "memory");
-                    } else if (k >= mine) {
+                    } else if (!own) {
                         mbar_arrive_expect_tx(bar, (uint32_t)__float_as_int(load_cluster<float>(smem_u32((const void *)(own_bytes + s)), rank ^ 1)));
                     }
                 }
@@ -823,7 +894,7 @@ __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const Late
 }
 
 template <int R, bool Two>
-static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, LatentAttnParams p, int sms, cudaStream_t stream)
+static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tv, const CUtensorMap &tq, LatentAttnParams p, int sms, cudaStream_t stream)
 {
     using L = LatentLayout<R, Two>;
     constexpr int kCtas = Two ? 2 : 1;
@@ -852,20 +923,20 @@ static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, L
     const int64_t tiles = (int64_t)p.B * p.chunks * (((int64_t)p.max_nb + kLatTileBlocks - 1) / kLatTileBlocks);
     p.clusters = (int)min((int64_t)most[dev], tiles);
     e = launch_clusters(latent_attn_kernel<R, Two>, dim3(p.clusters * kCtas), dim3(kLatThreads), dim3(kCtas, 1, 1), L::kAlloc,
-                        stream, tc, tq, p);
+                        stream, tc, tv, tq, p);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.B * p.rows;
     return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p,
                          kCtas * R, rows);
 }
 
-cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tv, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
                                int sms, cudaStream_t stream)
 {
-    if (plan.ctas == 2) return latent_attn_t<64, true>(tc, tq, p, sms, stream);
-    if (plan.cta_rows == 64) return latent_attn_t<64, false>(tc, tq, p, sms, stream);
-    if (plan.cta_rows == 32) return latent_attn_t<32, false>(tc, tq, p, sms, stream);
-    return latent_attn_t<16, false>(tc, tq, p, sms, stream);
+    if (plan.ctas == 2) return latent_attn_t<64, true>(tc, tv, tq, p, sms, stream);
+    if (plan.cta_rows == 64) return latent_attn_t<64, false>(tc, tv, tq, p, sms, stream);
+    if (plan.cta_rows == 32) return latent_attn_t<32, false>(tc, tv, tq, p, sms, stream);
+    return latent_attn_t<16, false>(tc, tv, tq, p, sms, stream);
 }
 
 }  // namespace pkv
