@@ -732,7 +732,7 @@ struct LatentWorkspace {
 };
 LatentWorkspace latent_workspace(int64_t num_seqs, const pkv::LatentPlan &plan)
 {
-    const size_t rows = 2 * (size_t)pkv::kLatentMaxClusters * plan.cta_rows;
+    const size_t rows = 2 * (size_t)pkv::kLatentMaxCtas * plan.cta_rows;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     LatentWorkspace w;
     w.lse_at = up(rows * pkv::kLatentDim * 4);
@@ -750,28 +750,24 @@ int check_latent_sizes(int32_t num_seqs, int32_t num_new, int32_t num_q_heads)
     return PKV_OK;
 }
 
-// The cache as (64 elements, token, chunk of 64 elements, block), one block's rows of one chunk (as keys) or two (as
-// values) a box; the queries as (64 elements, row, chunk), a CTA's rows a box.  All land as rows of 128 bytes, 128-byte
-// swizzled.
-int make_latent_maps(CUtensorMap *tc, CUtensorMap *tv, CUtensorMap *tq, const void *cache, int32_t num_blocks, const void *q, int64_t rows,
+// The cache as (64 elements, 8 tokens, chunk of 64 elements, half of a block, block), a block a box; the queries as
+// (64 elements, row, chunk), a CTA's rows a box.  Both land as rows of 128 bytes, 128-byte swizzled.
+int make_latent_maps(CUtensorMap *tc, CUtensorMap *tq, const void *cache, int32_t num_blocks, const void *q, int64_t rows,
                      int cta_rows)
 {
     if (!encode_fn()) {
         g_last_error = "cuTensorMapEncodeTiled is unavailable from the driver";
         return PKV_ERR_CUDA;
     }
-    const cuuint64_t row = kLatentRow * 2;
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    const cuuint64_t cd[4] = {64, 16, (cuuint64_t)kLatentRow / 64, (cuuint64_t)num_blocks}, cs[3] = {row, 128, 16 * row};
-    CUresult r = CUDA_SUCCESS;
-    for (int chunks = 1; chunks <= 2 && r == CUDA_SUCCESS; ++chunks) {
-        const cuuint32_t cb[4] = {64, 16, (cuuint32_t)chunks, 1};
-        r = encode_fn()(chunks == 1 ? tc : tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(cache), cd, cs, cb, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    }
+    const cuuint64_t row = kLatentRow * 2, chunks = kLatentRow / 64;
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    const cuuint64_t cd[5] = {64, 8, chunks, 2, (cuuint64_t)num_blocks}, cs[4] = {row, 128, 8 * row, 16 * row};
+    const cuuint32_t cb[5] = {64, 8, (cuuint32_t)chunks, 2, 1};
+    CUresult r = encode_fn()(tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(cache), cd, cs, cb, es,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) {
-        const cuuint64_t qd[3] = {64, (cuuint64_t)rows, (cuuint64_t)kLatentRow / 64}, qs[2] = {row, 128};
+        const cuuint64_t qd[3] = {64, (cuuint64_t)rows, chunks}, qs[2] = {row, 128};
         const cuuint32_t qb[3] = {64, (cuuint32_t)cta_rows, 1};
         r = encode_fn()(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), qd, qs, qb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -854,13 +850,13 @@ PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_
 #ifdef PKV_TEST_HOOKS
     p.withhold_tile = g_withhold_tile.load(std::memory_order_relaxed);
 #endif
-    CUtensorMap tc, tv, tq;
-    st = make_latent_maps(&tc, &tv, &tq, latent_cache, cache.num_blocks, q, (int64_t)num_seqs * p.rows, plan.cta_rows);
+    CUtensorMap tc, tq;
+    st = make_latent_maps(&tc, &tq, latent_cache, cache.num_blocks, q, (int64_t)num_seqs * p.rows, plan.cta_rows);
     if (st != PKV_OK) return st;
     int sms = 0;
     st = sm_count(&sms);
     if (st != PKV_OK) return st;
-    cudaError_t e = pkv::launch_latent_attn(tc, tv, tq, p, plan, sms, stream);
+    cudaError_t e = pkv::launch_latent_attn(tc, tq, p, plan, sms, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "latent attention launch");
 }
 

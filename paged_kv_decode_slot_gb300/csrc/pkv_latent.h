@@ -12,22 +12,20 @@ namespace pkv {
 
 constexpr int kLatentDim = 512;   // the latent vector of a token
 constexpr int kLatentRope = 64;   // its rotary key
-constexpr int kLatentMaxClusters = 152;
+constexpr int kLatentMaxCtas = 152;
 
-// How the (token, head) rows of a sequence are dealt to CTAs: chunks of ctas * cta_rows rows, ctas CTAs as a cluster.
+// How the (token, head) rows of a sequence are dealt to CTAs: chunks of cta_rows rows.
 struct LatentPlan {
-    int cta_rows, ctas;
+    int cta_rows;
     int64_t chunks;
-    int chunk_rows() const { return cta_rows * ctas; }
 };
-// The narrowest of 16, 32 and 64 rows a CTA that holds a sequence's rows: products cost their tokens and, less, their
-// rows, and what queries leave free of shared memory takes loads ahead.  From 65 rows on pairs of CTAs.
+// The narrowest of 16, 32 and 64 rows a CTA that holds a sequence's rows (the products cost their tokens and, less, their
+// rows; what the queries leave free of shared memory takes loads ahead).
 inline LatentPlan latent_plan(int64_t rows)
 {
     LatentPlan p;
     p.cta_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.ctas = rows > 64 ? 2 : 1;
-    p.chunks = (rows + p.chunk_rows() - 1) / p.chunk_rows();
+    p.chunks = (rows + p.cta_rows - 1) / p.cta_rows;
     return p;
 }
 
@@ -37,13 +35,13 @@ struct LatentAttnParams {
     int32_t max_nb, B, N, T, num_blocks;
     int32_t rows;                  // T * N
     int32_t chunks;                // chunks of rows a sequence
-    int32_t clusters;              // clusters of the grid (set by the launcher)
+    int32_t ctas;                  // CTAs of the grid (set by the launcher)
     float scale_log2;
     __nv_bfloat16 *out;            // [B][T][N][512]
     float *lse_out;                // [B][T][N], nullable
-    // workspace: two parts a cluster of chunk rows each, and of each (sequence, chunk) its first cluster and its parts
-    float *part_out;               // [2 clusters][chunk rows][512]
-    float *part_lse;               // [2 clusters][chunk rows], log2
+    // workspace: two parts a CTA of cta_rows rows each, and of each (sequence, chunk) its first CTA and its parts
+    float *part_out;               // [2 ctas][cta_rows][512]
+    float *part_lse;               // [2 ctas][cta_rows], log2
     int2 *unit_parts;              // [B][chunks]
     int32_t *err_flag;
     uint64_t wait_ns;
@@ -52,8 +50,8 @@ struct LatentAttnParams {
 #endif
 };
 
-cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tv, const CUtensorMap &tq, const LatentAttnParams &p,
-                               const LatentPlan &plan, int sms, cudaStream_t stream);
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
+                               int sms, cudaStream_t stream);
 
 // Norm and rotation of new tokens' rows with their append, and rotation of their queries (pkv_latent_append.cu).
 struct LatentAppendParams {

@@ -5,27 +5,25 @@
 //
 // All rows share the keys, so the contraction is dense: with 128 rows 2 * 1088 * 128 operations for 1,152 bytes, 242 a
 // byte, about what the chip has for one byte of DRAM.  Hence the tcgen05 tensor cores, and both products transposed:
-//     S^T[128 tokens x R] = C[128 x 576] . Q^T        A: the tile's rows as they lie (K-major), B: the queries
-//     O^T[512 x R]       += C^T[512 x 128] . P^T      A: the same rows read MN-major (four M = 128 products), B: P
+//     S^T[64 tokens x R]  = C[64 x 576] . Q^T       A: the tile's rows as they lie (K-major), B: the queries
+//     O^T[512 x R]       += C^T[512 x 64] . P^T     A: the same bytes read MN-major (four M = 128 products), B: P
 // so that R = 16, 32 or 64 query rows a CTA is the N of the products, not a padded M: the 512 x R accumulator takes 4 R
-// of the 512 tensor-memory columns, where 128 rows x 512 would take them all.  More rows than 64 take a cluster of two
-// CTAs, 64 rows each: every piece of the cache is fetched by one of the two and multicast to both.
+// of the 512 tensor-memory columns, and a tile is loaded once and read as keys and as values where it lies.
 //
-// The cache streams through a ring of 16 KB pieces, first as keys (128 tokens x 64 elements, nine a tile), then, from
-// L2, as values (64 tokens x 128 elements, eight a tile): a whole 128-token tile (147 KB) beside 64 queries (74 KB)
-// would leave nothing to load ahead into.  A box of a load is one block's 16 rows x 64 elements.
+// A block of 16 tokens is one TMA load of 18 KB, a box of (64 elements, 8 tokens, 9 chunks of elements, 2 halves): it
+// lands as [half][chunk][8 rows][128 bytes], swizzle atoms of 8 rows, so that the 8-row groups of consecutive blocks lie
+// 9,216 bytes apart throughout and a tile of several blocks is one operand in either reading.
 //
 // The work is dealt out evenly: the tiles of all (sequence, chunk of rows) units in a row, cut into as many equal runs as
-// clusters run at once.  A unit that one cluster holds whole is written out directly; of one that is cut each part goes
-// to the workspace, at most two a cluster, and a second launch joins them by their log-sum-exp.
+// CTAs run at once.  A unit that one CTA holds whole is written out directly; of one that is cut each part goes to the
+// workspace, at most two a CTA, and a second launch joins them by their log-sum-exp.
 //
-// CTA = 10 warps: 0-7 softmax (warp w: tokens 32 (w % 4) .. + 31, one a thread; half w / 4 of the rows), 8 issues the MMAs,
-// 9 the loads.  QK^T of tile i + 1 is issued before P V of tile i, so the tensor cores work through the softmax of tile i.
-// The running maxima move only when a logit exceeds them by 2^8 (checked with one barrier vote a tile); the sums stay in
-// the threads' registers, a part for each token lane, until the end.
+// CTA = 11 warps: 0-7 softmax (warp w: block w % 4 of the tile, a token a lane; half w / 4 of the rows), 8 issues the MMAs,
+// 9 the loads, 10 zeroes what lies behind a sequence's end.  QK^T of tile i + 1 is issued before P V of tile i, so the tensor
+// cores work through the softmax of tile i.  The running maxima move only when a logit exceeds them by 2^8 (found with one
+// barrier vote a tile); the sums stay in the threads' registers, a part for each token lane, until the end.
 #include <float.h>
 
-#include "pkv_cluster.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_latent.h"
@@ -34,49 +32,56 @@
 namespace pkv {
 
 constexpr int kLatChunks = (kLatentDim + kLatentRope) / 64;   // 64-element chunks of a row
-constexpr int kLatTile = 128;                                 // tokens of a tile
-constexpr int kLatTileBlocks = kLatTile / kBlockSize;
-constexpr int kLatStage = 16384;                              // bytes of a ring stage
-constexpr int kLatBox = kBlockSize * 128;                     // bytes of one block's 64-element rows
-constexpr int kLatSoftmaxWarps = 8, kLatMmaWarp = 8, kLatLoadWarp = 9, kLatLoaders = 2, kLatTailWarp = 11;
-constexpr int kLatThreads = 384;
+constexpr int kLatGroup = kLatChunks * 1024;                  // bytes of eight tokens: an atom per chunk
+constexpr int kLatBlock = 2 * kLatGroup;                      // and of a block
+constexpr int kLatSoftmaxWarps = 8, kLatMmaWarp = 8, kLatLoadWarp = 9, kLatTailWarp = 10;
+constexpr int kLatThreads = 352;
 constexpr float kLatRescale = 8.f;                            // log2 of how far a logit may exceed the running maximum
 
-// R: query rows of a CTA.  Two: the CTA is one of a cluster of two.
-template <int R, bool Two>
+// R: query rows of a CTA.
+template <int R>
 struct LatentLayout {
     static_assert(R == 16 || R == 32 || R == 64, "rows of a CTA");
+    static constexpr int kBlocks = R == 64 ? 4 : 3;      // blocks of a tile (M = 64: at most four)
+    static constexpr int kSlots = R == 64 ? 2 : 3;       // tiles in shared memory
+    static constexpr int kTile = kBlocks * kBlockSize;   // tokens of a tile
+    static constexpr int kRing = kSlots * kBlocks;
     static constexpr int kQChunk = R * 128;              // 64 elements of R queries, K-major, 128-byte swizzle
     static constexpr int kQBytes = kLatChunks * kQChunk;
     static constexpr int kPLine = R * 2;                 // bytes of one token's weights: a swizzle atom's row
-    static constexpr int kPBytes = kLatTile * kPLine;
-    static constexpr int kStages = R == 64 ? 8 : R == 32 ? 11 : 12;
-    static constexpr int kQOffset = 0;
-    static constexpr int kPOffset = kQBytes;
-    static constexpr int kRingOffset = kPOffset + ((kPBytes + 1023) & ~1023);
-    static constexpr int kBarOffset = kRingOffset + kStages * kLatStage;
-    // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, tail[2], fin
-    static constexpr int kBars = 2 * kStages + 9;
-    static constexpr int kMiscOffset = kBarOffset + kBars * 8;
-    static constexpr int kStageWords = (2 * kStages + 3) & ~3;  // what follows is read in vectors of four words
-    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, issued[2] */ + kStageWords /* bytes */ +
-                                  R /* limits */ + R /* maxima */ + R /* factors */ + 4 * R /* of four warps */;
-    static constexpr int kAlloc = ((kMiscOffset + 15) & ~15) + kWords * 4 + 1024;
-    static_assert(kQBytes % 1024 == 0 && kRingOffset % 1024 == 0, "swizzle atoms are aligned");
-    static_assert(kAlloc + (kLatThreads + 4) * 8 <= 227 * 1024, "shared memory of a CTA");
+    static constexpr int kPBytes = kTile * kPLine;
+    static constexpr int kRingOffset = 0;
+    static constexpr int kQOffset = kRing * kLatBlock;
+    static constexpr int kPOffset = kQOffset + kQBytes;
+    static constexpr int kBarOffset = kPOffset + ((kPBytes + 1023) & ~1023);
+    // full[slots], empty[ring], q_full, q_free, s_full[2], p_ready, pv_done, tail[2], fin
+    static constexpr int kBars = kSlots + kRing + 9;
+    static constexpr int kMiscOffset = (kBarOffset + kBars * 8 + 15) & ~15;
+    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, - */ + 2 * 4 /* a slot's bytes */ + R /* limits */ +
+                                  R /* maxima */ + R /* factors */ + 4 * R /* of four warps */;
+    static constexpr int kBytes = kMiscOffset + kWords * 4;
+    static constexpr int kAlloc = kBytes + 1024;  // room to align the window
+    static_assert(kQOffset % 1024 == 0 && kPOffset % 1024 == 0 && kSlots <= 4, "swizzle atoms are aligned");
+    static_assert((kSlots - 1) * kBlocks * kLatBlock + 8 * kLatGroup <= kBytes, "M = 64 rows from any slot on lie inside the window");
+    static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
     static constexpr uint32_t kCols = R == 64 ? 512 : R == 32 ? 256 : 128;  // tensor memory: O^T 4 R, S^T 2 R
 };
 
 // ---- dealing out the tiles ----------------------------------------------------------------------
-// A unit's share of the work: its tiles and, as much as one tile, its queries, statistics and outputs.
-constexpr int kLatUnitCost = 1;
+// A unit's share of the work: its tiles and, as much as this many, its queries, statistics and outputs.
+constexpr int kLatUnitCost = 2;
 
 __device__ __forceinline__ int latent_ctx(const LatentAttnParams &p, int b)
 {
     const int ctx = __ldg(p.context_lens + b);
     return ctx < 0 || ctx > p.max_nb * kBlockSize ? 0 : ctx;
 }
-__device__ __forceinline__ int latent_cost(int ctx) { return ctx > 0 ? (ctx + kLatTile - 1) / kLatTile + kLatUnitCost : 0; }
+template <int R>
+__device__ __forceinline__ int latent_cost(int ctx)
+{
+    constexpr int kTile = LatentLayout<R>::kTile;
+    return ctx > 0 ? (ctx + kTile - 1) / kTile + kLatUnitCost : 0;
+}
 
 // Tiles [t0, t1) of unit (b, chunk), which starts at `start` in the row of all units.
 struct LatentSegment {
@@ -85,13 +90,14 @@ struct LatentSegment {
     bool whole;
 };
 
+template <int R>
 struct LatentWalk {
     int64_t lo, hi, start;
     int b, chunk;
     __device__ __forceinline__ bool next(const LatentAttnParams &p, LatentSegment &s)
     {
         while (start < hi && b < p.B) {
-            const int ctx = latent_ctx(p, b), cost = latent_cost(ctx);
+            const int ctx = latent_ctx(p, b), cost = latent_cost<R>(ctx);
             const int64_t at = start;
             const int ub = b, uc = chunk;
             start += cost;
@@ -108,18 +114,19 @@ struct LatentWalk {
     }
 };
 
-// This cluster's run of the work, the same in every thread; false: nothing to do.  `sums` holds kLatThreads + 4 64-bit
+// This CTA's run of the work, the same in every thread; false: nothing to do.  `sums` holds kLatThreads + 4 64-bit
 // words of shared memory.  Every thread calls it.
-__device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cluster, int64_t *sums, LatentWalk &w, int64_t &total,
-                                            int &clusters)
+template <int R>
+__device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, int64_t *sums, LatentWalk<R> &w, int64_t &total,
+                                            int &ctas)
 {
     const int tid = threadIdx.x, per = (p.B + kLatThreads - 1) / kLatThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t cost = 0;
     for (int b = b0; b < b1; ++b) {
         const int ctx = __ldg(p.context_lens + b);
-        if (cluster == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
-        cost += latent_cost(latent_ctx(p, b));
+        if (cta == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+        cost += latent_cost<R>(latent_ctx(p, b));
     }
     sums[tid] = cost;
     __syncthreads();
@@ -145,14 +152,14 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int clust
     const int64_t all = sums[kLatThreads];
     total = all * p.chunks;
     // no more runs than units and tiles: a run then holds at least one of them
-    clusters = (int)min((int64_t)p.clusters, total);
-    if (cluster >= clusters) return false;
-    w.lo = total * cluster / clusters;
-    w.hi = total * (cluster + 1) / clusters;
+    ctas = (int)min((int64_t)p.ctas, total);
+    if (cta >= ctas) return false;
+    w.lo = total * cta / ctas;
+    w.hi = total * (cta + 1) / ctas;
     int64_t at = sums[tid] * p.chunks;
     if (at <= w.lo && w.lo < (sums[tid] + cost) * p.chunks) {
         for (int b = b0; b < b1; ++b) {
-            const int c = latent_cost(latent_ctx(p, b));
+            const int c = latent_cost<R>(latent_ctx(p, b));
             if (w.lo < at + (int64_t)c * p.chunks) {
                 const int chunk = (int)((w.lo - at) / c);
                 sums[kLatThreads + 1] = b;
@@ -199,16 +206,6 @@ __device__ __forceinline__ uint32_t latent_p_at(int t, int u)
     return (uint32_t)(t * (R * 2) + ((u ^ x) << 4));
 }
 
-__device__ __forceinline__ void tma_load_4d_multicast(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
-                                                      int c3, uint16_t ctas)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(ctas)
-        : "memory");
-}
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
 {
     asm volatile(
@@ -216,22 +213,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
-}
-
-// tc_commit that arrives at the same barrier of both CTAs of the cluster.
-__device__ __forceinline__ void tc_commit_both(uint32_t bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
 }
 
 // C columns of a warp's 32 lanes (C = 8, 16 or 32).
@@ -325,70 +306,42 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// A place in the ring: stage s, and the parity of its uses.
-template <int S>
-struct RingPlace {
-    int s = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next()
-    {
-        if (++s == S) s = 0, parity ^= 1u;
-    }
-};
-
-template <int R, bool Two>
+template <int R>
 __global__ void __launch_bounds__(kLatThreads, 1)
-latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ CUtensorMap tm_q, const LatentAttnParams p)
+latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q, const LatentAttnParams p)
 {
-    using L = LatentLayout<R, Two>;
-    constexpr int S = L::kStages;
+    using L = LatentLayout<R>;
+    constexpr int NB = L::kBlocks, NS = L::kSlots, kRing = L::kRing;
     constexpr int CW = R / 2;  // rows (columns of S^T) of a softmax thread
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t sums[kLatThreads + 4];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const mem = smem_raw + (base - raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = Two ? (int)cluster_rank() : 0;
-    const int cluster = Two ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     pdl_wait_primary();
     pdl_launch_dependents();
-    LatentWalk walk;
+    LatentWalk<R> walk;
     int64_t total;
-    int clusters;
-    if (!latent_deal(p, cluster, sums, walk, total, clusters)) return;  // both CTAs of a cluster alike
+    int ctas;
+    // (the sums lie where the first tiles will)
+    if (!latent_deal<R>(p, cta, reinterpret_cast<int64_t *>(mem), walk, total, ctas)) return;
 
     const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
-    const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * S, bar_qfull = bar_empty + 8 * S,
-                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_tail = bar_pv + 8, bar_fin = bar_tail + 16;
-    volatile int *const tile_mask = reinterpret_cast<volatile int *>(mem + ((L::kMiscOffset + 15) & ~15));  // [4], by tile % 4
+    const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * NS, bar_qfull = bar_empty + 8 * kRing,
+                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_tail = bar_pv + 8,
+                   bar_fin = bar_tail + 16;
+    volatile int *const tile_mask = reinterpret_cast<volatile int *>(mem + L::kMiscOffset);  // [4], by tile % 4: blocks there
     volatile int *const abort_flag = tile_mask + 4;
     volatile uint32_t *const tmem_slot = reinterpret_cast<volatile uint32_t *>(tile_mask + 5);
-    volatile int *const issued = tile_mask + 6;           // [kLatLoaders]: stages before this one were filled
-    volatile int *const own_bytes = tile_mask + 8;        // [S]: of a stage's last load, what this CTA fetches
-    volatile int *const all_bytes = own_bytes + S;        // [S]: and what both fetch
-    int *const limit = const_cast<int *>(own_bytes + L::kStageWords);                     // [R] tokens a row sees
+    int *const limit = const_cast<int *>(tile_mask + 16);                        // [R] tokens a row sees
     float *const top = reinterpret_cast<float *>(limit + R);                     // [R] running maxima (log2)
     float *const factor = top + R;                                               // [R]
     float *const quarters = factor + R;                                          // [4][R]
 
+    __syncthreads();  // the sums are read
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        issued[0] = issued[1] = 0;
-        for (int s = 0; s < S; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, Two ? 2 : 1);
-        }
-        mbar_init(bar_qfull, 1);
-        mbar_init(bar_qfree, 1);
-        mbar_init(bar_s, 1);
-        mbar_init(bar_s + 8, 1);
-        mbar_init(bar_p, kLatSoftmaxWarps);
-        mbar_init(bar_pv, 1);
-        mbar_init(bar_tail, 1);
-        mbar_init(bar_tail + 8, 1);
-        mbar_init(bar_fin, 1);
+        for (int s = 0; s < NS + kRing + 9; ++s) mbar_init(bar_full + 8 * s, s == NS + kRing + 4 ? kLatSoftmaxWarps : 1);
         fence_barrier_init();
     }
     if (warp == kLatMmaWarp) {
@@ -398,230 +351,159 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if constexpr (Two) cluster_sync();  // the other CTA's barriers exist
     const uint32_t tm_o = *tmem_slot, tm_s = tm_o + 4 * R;
 
     auto give_up = [&]() {
         if (lane == 0 && !*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
         *abort_flag = 1;
     };
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, latent_wait(bar, parity, abort_flag, p.wait_ns));
-    };
-
     auto wait_one = [&](uint32_t bar, uint32_t parity) { return latent_wait(bar, parity, abort_flag, p.wait_ns); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)); };
 
-    uint32_t q_loads = 0;  // segments whose queries were asked for (the first loading warp)
-    if (warp >= kLatLoadWarp && warp < kLatLoadWarp + kLatLoaders) {
+    // of the loading warp: tiles begun, bytes of the last one that were not asked for, segments whose queries were
+    uint32_t g_loads = 0, missing = 0, q_loads = 0;
+    bool issuer = false;  // of the MMA warp: the thread that issues (and so the one whose MMAs a commit speaks of)
+    if (warp == kLatLoadWarp) {
         // ------------------------------ loads ------------------------------
-        // The two warps take turns, a stage each; a lane issues a block's box.
-        const int me = warp - kLatLoadWarp;
-        if (lane == 0 && me == 0) {
+        if (lane == 0) {
             prefetch_tensormap(&tm_c);
-            prefetch_tensormap(&tm_v);
             prefetch_tensormap(&tm_q);
         }
-        int n = 0;           // stages so far
-        RingPlace<S> at;
-        uint32_t g = 0;      // tiles so far
         bool ok = true, withheld = false;
-        auto turn = [&]() { return (n & 1) == me; };
-        auto step = [&]() { ++n, at.next(); };
-        // The stage's barrier, told what to expect, once the stage is free.
-        auto open = [&](int bytes_all, int bytes_own) {
-            if (n >= S) ok = wait(bar_empty + 8 * at.s, at.parity ^ 1u);
-            if (ok && lane == 0) {
-                if constexpr (Two) own_bytes[at.s] = bytes_own, all_bytes[at.s] = bytes_all;
-                mbar_arrive_expect_tx(bar_full + 8 * at.s, (uint32_t)bytes_all);
-            }
-            __syncwarp();
-        };
-        // V: 64 tokens (four blocks) x 128 elements (two chunks a box)
-        auto fill_v = [&](int ids, uint32_t mask, int nblk) {
-            for (int h = 0; h < 2 && 4 * h < nblk; ++h) {
-                const uint32_t m4 = (mask >> (4 * h)) & 0xFu, own = Two ? m4 & (3u << (2 * rank)) : m4;
-                const int id = __shfl_sync(0xFFFFFFFFu, ids, (4 * h + lane) & 7);
-                const bool mine = lane < 4 && ((own >> lane) & 1u);
-#pragma unroll 1
-                for (int m = 0; m < 4 && ok; ++m, step()) {
-                    if (!turn()) continue;
-                    open(2 * kLatBox * __popc(m4), 2 * kLatBox * __popc(own));
-                    if (!ok) return;
-                    if (mine) {
-                        const uint32_t dst = ring + at.s * kLatStage + lane * 2 * kLatBox, bar = bar_full + 8 * at.s;
-                        if constexpr (Two) tma_load_4d_multicast(dst, &tm_v, bar, 0, 0, 2 * m, id, 3);
-                        else tma_load_4d(dst, &tm_v, bar, 0, 0, 2 * m, id);
-                    }
-                }
-            }
-        };
+        int slot = 0;
+        uint32_t parity = 0;  // of the slot's uses
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
-            if (me == 0) {
-                // the queries, once the last unit's are no longer needed
-                if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
-                if (!ok) break;
-                const int64_t row = (int64_t)sg.b * p.rows + sg.chunk * (Two ? 2 * R : R) + rank * R;
-                if (lane == 0) mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
-                __syncwarp();
-                if (lane < kLatChunks) tma_load_3d(q_u32 + lane * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, lane);
-                ++q_loads;
-            }
+            // the queries, once the last unit's are no longer needed
+            if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
+            if (!ok) break;
+            const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * R;
+            if (lane == 0) mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
+            __syncwarp();
+            if (lane < kLatChunks) tma_load_3d(q_u32 + lane * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, lane);
+            ++q_loads;
             const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
             const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
             auto ids_of = [&](int t) {
-                const int j = t * kLatTileBlocks + lane;
-                return lane < kLatTileBlocks && j < nb ? __ldg(tbl + j) : -1;
+                const int j = t * NB + lane;
+                return lane < NB && t < sg.t1 && j < nb ? __ldg(tbl + j) : -1;
             };
-            int next = ids_of(sg.t0), prev = -1;
-            uint32_t prev_mask = 0;
-            int prev_nblk = 0;
-            for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
+            int next = ids_of(sg.t0);
+            for (int t = sg.t0; t < sg.t1 && ok; ++t) {
                 const int ids = next;
-                if (t + 1 < sg.t1) next = ids_of(t + 1);
-                const int nblk = min(kLatTileBlocks, nb - t * kLatTileBlocks);
-                const bool good = lane < nblk && ids >= 0 && ids < p.num_blocks;
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good), own = Two ? mask & (0xFu << (4 * rank)) : mask;
-                if (lane == 0) {
-                    if (mask != (1u << nblk) - 1u) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-                    tile_mask[g & 3] = (int)mask;  // both warps write it, each before it fills a stage of the tile
-                }
+                next = ids_of(t + 1);
+                const int nblk = min(NB, nb - t * NB);
+                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < nblk && ids >= 0 && ids < p.num_blocks);
                 if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
                     withheld = true, ok = false;
                     break;
                 }
-                const bool mine = lane < 8 && ((own >> lane) & 1u);
+                const uint32_t bar = bar_full + 8 * slot;
+                const bool used = g_loads >= NS;
 #pragma unroll 1
-                for (int c = 0; c < kLatChunks && ok; ++c, step()) {
-                    if (!turn()) continue;
-                    open(kLatBox * __popc(mask), kLatBox * __popc(own));
+                for (int j = 0; j < NB; ++j) {
+                    if (used) ok = wait(bar_empty + 8 * (slot * NB + j), parity ^ 1u);
                     if (!ok) break;
-                    if (mine) {
-                        const uint32_t dst = ring + at.s * kLatStage + lane * kLatBox, bar = bar_full + 8 * at.s;
-                        if constexpr (Two) tma_load_4d_multicast(dst, &tm_c, bar, 0, 0, c, ids, 3);
-                        else tma_load_4d(dst, &tm_c, bar, 0, 0, c, ids);
+                    const int id = __shfl_sync(0xFFFFFFFFu, ids, j);
+                    if (j == 0) missing = (uint32_t)__popc(mask) * kLatBlock, ++g_loads;
+                    if (lane == 0) {
+                        if (j == 0) {
+                            if (mask != (1u << nblk) - 1u) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                            tile_mask[(g_loads - 1) & 3] = (int)mask;
+                            mbar_arrive_expect_tx(bar, missing);
+                        }
+                        if ((mask >> j) & 1u) tma_load_5d(ring + (slot * NB + j) * kLatBlock, &tm_c, bar, 0, 0, 0, 0, id);
                     }
+                    if ((mask >> j) & 1u) missing -= kLatBlock;
+                    __syncwarp();
                 }
-                if (t > sg.t0 && ok) fill_v(prev, prev_mask, prev_nblk);
-                prev = ids, prev_mask = mask, prev_nblk = nblk;
+                if (++slot == NS) slot = 0, parity ^= 1u;
             }
-            if (ok) fill_v(prev, prev_mask, prev_nblk);
         }
-        if (!ok && !withheld) give_up();
-        if (lane == 0) issued[me] = n;
-        // every stage released, by both CTAs: nothing is on its way into this CTA's barriers any more
-        for (int k = max(0, n - S); k < n && ok; ++k)
-            if ((k & 1) == me) ok = wait(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
         if (!ok && !withheld) give_up();
     } else if (warp == kLatTailWarp) {
         // ---------------- rows behind a sequence's end ----------------
         // They may hold anything, and 0 x NaN is NaN: they are zeroed before P V reads them, when the MMA warp asks for it
-        // (asked and answered in turn, so that neither can be a use of the stage ahead of the other).
-        int n = 0;
-        uint32_t asked = 0;
+        // (asked and answered in turn, so that neither can be a use of the slot ahead of the other).
+        uint32_t g = 0, asked = 0;
         bool ok = true;
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
-            const int count = sg.t1 - sg.t0, tail = sg.ctx % kBlockSize;
-            int last = 8;  // stages of the last tile's values
-            if (sg.t1 == sg.tiles) {
-                const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize - (sg.tiles - 1) * kLatTileBlocks;
-                last = nblk > 4 ? 8 : 4;
-                const int first = n + kLatChunks * count + 8 * (count - 1) + last - 4;
-                for (int k = first; k < first + 4 && tail > 0 && ok; ++k) {
-                    ok = wait(bar_tail, asked++ & 1);
-                    if (!ok) break;
-                    const uint32_t blk = ring + (k % S) * kLatStage + ((nblk - 1) & 3) * 2 * kLatBox;
-                    for (int x = lane; x < 2 * (kBlockSize - tail) * 8; x += 32) {
-                        const int d = x & 1, u = (x >> 1) & 7, row = tail + (x >> 4);
-                        st_shared_v4(blk + d * kLatBox + row * 128 + u * 16, make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_tail + 8);
-                }
+            g += sg.t1 - sg.t0;
+            const int tail = sg.ctx % kBlockSize;
+            if (sg.t1 != sg.tiles || tail == 0) continue;
+            ok = wait(bar_tail, asked++ & 1);
+            if (!ok) break;
+            const int j = (sg.ctx / kBlockSize) - (sg.tiles - 1) * NB;
+            const uint32_t blk = ring + ((int)((g - 1) % NS) * NB + j) * kLatBlock;
+            // 16-byte units of the values' eight chunks
+            for (int x = lane; x < (kBlockSize - tail) * 64; x += 32) {
+                const int u = x & 63, row = tail + (x >> 6);
+                st_shared_v4(blk + (row >> 3) * kLatGroup + (u >> 3) * 1024 + (row & 7) * 128 + (u & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
             }
-            n += kLatChunks * count + 8 * (count - 1) + last;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tail + 8);
         }
         if (!ok) give_up();
     } else if (warp == kLatMmaWarp) {
         // ------------------------------ MMAs: one thread ------------------------------
-        if (elect_one()) {
-            constexpr uint32_t kIdS = idesc_bf16_f32(128, R, 0, 0), kIdO = idesc_bf16_f32(128, R, 1, 1);
+        // (whole warps at these waits and issues took 700 clocks for what takes one thread 150)
+        issuer = elect_one();
+        if (issuer) {
+            constexpr uint32_t kIdS = idesc_bf16_f32(64, R, 0, 0), kIdO = idesc_bf16_f32(128, R, 1, 1);
             // descriptors: an address moves the low word alone
-            const uint64_t k_desc = smem_desc_sw128(ring, 16, 1024), q_desc = smem_desc_sw128(q_u32, 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(ring, kLatBox, 1024), p_desc = latent_p_desc<R>(p_u32);
-            RingPlace<S> at;
-            uint32_t g = 0, unit = 0, tails = 0;
+            const uint64_t k_desc = smem_desc_sw128(ring, 16, kLatGroup), q_desc = smem_desc_sw128(q_u32, 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(ring, 1024, kLatGroup), p_desc = latent_p_desc<R>(p_u32);
+            uint32_t g = 0, unit = 0, tails = 0, parity = 0;
+            int slot = 0, pv_slot = 0;
             bool ok = true, started = false;
-            auto release = [&](int s) {
-                if constexpr (Two) tc_commit_both(bar_empty + 8 * s);
-                else tc_commit(bar_empty + 8 * s);
-            };
             // P V of tile number gt; has_tail: its last block's end is zeroed first
-            auto pv = [&](uint32_t gt, int nblk, bool has_tail) {
+            auto pv = [&](uint32_t gt, bool has_tail) {
                 ok = wait_one(bar_p, gt & 1);
-                if (!ok) return;
-                const uint32_t mask = (uint32_t)tile_mask[gt & 3];
-                const int first = __ffs(mask) - 1;
-                for (int h = 0; h < 2 && 4 * h < nblk; ++h) {
-                    const bool here = has_tail && (nblk - 1) / 4 == h;
-#pragma unroll 1
-                    for (int m = 0; m < 4; ++m, at.next()) {
-                        ok = wait_one(bar_full + 8 * at.s, at.parity);
-                        if (ok && here) {
-                            mbar_arrive(bar_tail);
-                            ok = wait_one(bar_tail + 8, tails++ & 1);
-                        }
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint64_t a = v_desc + (uint32_t)(at.s * (kLatStage >> 4)), b = p_desc + (uint32_t)((4 * h * kBlockSize * L::kPLine) >> 4);
-                        const uint32_t d = tm_o + m * R;
-                        if (mask == 0xFFu) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                tc_mma_ss(d, a + j * (2 * kLatBox >> 4), b + j * (kBlockSize * L::kPLine >> 4), kIdO,
-                                          started || h > 0 || j > 0);
-                        } else {
-#pragma unroll 1
-                            for (int j = 0; j < 4; ++j)
-                                if ((mask >> (4 * h + j)) & 1u)
-                                    tc_mma_ss(d, a + j * (2 * kLatBox >> 4), b + j * (kBlockSize * L::kPLine >> 4), kIdO,
-                                              started || 4 * h + j > first);
-                        }
-                        release(at.s);
-                    }
+                if (ok && has_tail) {
+                    mbar_arrive(bar_tail);
+                    ok = wait_one(bar_tail + 8, tails++ & 1);
                 }
-                if (mask) started = true;
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t mask = (uint32_t)tile_mask[gt & 3];
+#pragma unroll 1
+                for (int j = 0; j < NB; ++j) {
+                    const int blk = pv_slot * NB + j;
+                    if ((mask >> j) & 1u) {
+                        const uint64_t a = v_desc + (uint32_t)(blk * (kLatBlock >> 4)), b = p_desc + (uint32_t)(j * (kBlockSize * L::kPLine >> 4));
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) tc_mma_ss(tm_o + m * R, a + m * (2048 >> 4), b, kIdO, started);
+                        started = true;
+                    }
+                    tc_commit(bar_empty + 8 * blk);
+                }
                 tc_commit(bar_pv);
+                if (++pv_slot == NS) pv_slot = 0;
             };
             LatentSegment sg;
             while (ok && walk.next(p, sg)) {
                 ok = wait_one(bar_qfull, unit & 1);
                 ++unit;
-                started = false;
-                const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
-                auto pv_tile = [&](uint32_t gt, int t) {
-                    pv(gt, min(kLatTileBlocks, nb - t * kLatTileBlocks), t + 1 == sg.tiles && sg.ctx % kBlockSize > 0);
-                };
                 for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
-                    const uint32_t d = tm_s + R * (g & 1);
-#pragma unroll 1
-                    for (int c = 0; c < kLatChunks; ++c, at.next()) {
-                        ok = wait_one(bar_full + 8 * at.s, at.parity);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t a = k_desc + (uint32_t)(at.s * (kLatStage >> 4)), b = q_desc + (uint32_t)(c * (L::kQChunk >> 4));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) tc_mma_ss(d, a + 2 * k, b + 2 * k, kIdS, c + k > 0);
-                        release(at.s);
-                    }
+                    ok = wait_one(bar_full + 8 * slot, parity);
                     if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tm_s + R * (g & 1);
+                    const uint64_t a = k_desc + (uint32_t)(slot * NB * (kLatBlock >> 4));
+#pragma unroll
+                    for (int c = 0; c < kLatChunks; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_ss(d, a + c * (1024 >> 4) + 2 * k, q_desc + c * (L::kQChunk >> 4) + 2 * k, kIdS, c + k > 0);
                     tc_commit(bar_s + 8 * (g & 1));
+                    if (++slot == NS) slot = 0, parity ^= 1u;
                     if (t + 1 == sg.t1) tc_commit(bar_qfree);
-                    if (t > sg.t0) pv_tile(g - 1, t - 1);
+                    if (t > sg.t0) pv(g - 1, false);
+                    else started = false;
                 }
-                if (ok) pv_tile(g - 1, sg.t1 - 1);
+                if (ok) pv(g - 1, sg.t1 == sg.tiles && sg.ctx % kBlockSize > 0);
             }
             if (!ok) {
                 if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
@@ -631,20 +513,22 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         __syncwarp();
     } else {
         // ------------------------------ softmax and outputs ------------------------------
-        const int quarter = warp & 3, half = warp >> 2, tok = 32 * quarter + lane, c0 = half * CW;
+        // S^T has M = 64: its rows 16 q .. lie in tensor-memory lanes 32 q .. 32 q + 15
+        const int quarter = warp & 3, half = warp >> 2, tok = 16 * quarter + lane, c0 = half * CW;
+        const bool token = lane < 16 && quarter < NB;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const int col = lane & (CW - 1);  // the column this lane holds after a reduction
         uint32_t g = 0;
         bool ok = true;
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
-            const int row0 = sg.chunk * (Two ? 2 * R : R) + rank * R;  // first row of this CTA within the sequence
+            const int row0 = sg.chunk * R;  // first row of this unit within the sequence
             const int nrows = min(R, p.rows - row0);
-            if (threadIdx.x == 0 && rank == 0 && sg.t0 == 0) {
-                // for the joining launch: the first cluster of the unit's parts, and how many there are
+            if (threadIdx.x == 0 && sg.t0 == 0) {
+                // for the joining launch: the first CTA of the unit's parts, and how many there are
                 const int64_t last = sg.start + sg.tiles + kLatUnitCost - 1;
-                const int parts = sg.whole ? 1 : (int)(((last + 1) * clusters - 1) / total) - cluster + 1;
-                p.unit_parts[(int64_t)sg.b * p.chunks + sg.chunk] = make_int2(cluster, parts);
+                const int parts = sg.whole ? 1 : (int)(((last + 1) * ctas - 1) / total) - cta + 1;
+                p.unit_parts[(int64_t)sg.b * p.chunks + sg.chunk] = make_int2(cta, parts);
             }
             if (quarter == 0 && lane < CW) {
                 const int r = row0 + c0 + lane;
@@ -666,9 +550,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 tc_fence_after();
                 float x[CW];
                 tmem_load<CW>(lanes + tm_s + R * (g & 1) + c0, x);
-                const int at = t * kLatTile + tok;
-                const bool here = at < sg.ctx && (((uint32_t)tile_mask[g & 3] >> (tok / kBlockSize)) & 1u);
-                if (sg.ctx - p.T + 1 >= (t + 1) * kLatTile) {  // every row sees the whole tile
+                const int at = t * L::kTile + tok;
+                const bool here = token && at < sg.ctx && (((uint32_t)tile_mask[g & 3] >> quarter) & 1u);
+                if (sg.ctx - p.T + 1 >= (t + 1) * L::kTile) {  // every row sees the whole tile
 #pragma unroll
                     for (int c = 0; c < CW; ++c) x[c] = here ? x[c] * p.scale_log2 : -INFINITY;
                 } else {
@@ -730,7 +614,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 if (!ok) give_up();
 #pragma unroll
                 for (int u = 0; u < CW / 8; ++u)
-                    st_shared_v4(p_u32 + latent_p_at<R>(tok, c0 / 8 + u), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
+                    if (token) st_shared_v4(p_u32 + latent_p_at<R>(tok, c0 / 8 + u), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
                 fence_proxy_async_shared();
                 tc_fence_before();
                 __syncwarp();
@@ -752,7 +636,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             const float *f = quarters + c0 + col;
             const float all = (f[0] + f[R]) + (f[2 * R] + f[3 * R]), hi = top[c0 + col];
             const bool seen = hi != -FLT_MAX;
-            const int64_t part = (int64_t)(2 * cluster + (sg.t0 == 0)) * (Two ? 2 * R : R) + rank * R;  // rows of the workspace
+            const int64_t part = (int64_t)(2 * cta + (sg.t0 == 0)) * R;  // rows of the workspace
             if (quarter == 0 && lane < CW && c0 + lane < nrows) {
                 const float lse2 = seen ? hi + log2f(all) : -INFINITY;
                 const int64_t row = (int64_t)sg.b * p.rows + row0 + c0 + lane;
@@ -785,51 +669,25 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 
     // ------------------------------ teardown ------------------------------
     __syncthreads();
-    if constexpr (Two) cluster_sync();  // neither CTA issues anything any more
-    const bool bad = *abort_flag != 0;
-    bool peer_bad = false;
-    if constexpr (Two) peer_bad = __float_as_int(load_cluster<float>(smem_u32((const void *)abort_flag), rank ^ 1)) != 0;
-    if (bad || peer_bad) {
+    if (*abort_flag) {
         if (warp == kLatMmaWarp) {
             // every MMA this CTA issued completes before its tensor memory is released
-            if (lane == 0) tc_commit(bar_fin);
+            if (issuer) tc_commit(bar_fin);
             __syncwarp();
             mbar_wait_bounded(bar_fin, 0u, nullptr, kDrainLimitNs);
         }
         if (warp == kLatLoadWarp && lane == 0) {
-            // Every copy on its way lands before this CTA leaves.  Where one CTA filled a stage and the other did not
-            // follow, the barrier is told to expect what was sent and no more.
-            int mine[kLatLoaders], theirs[kLatLoaders], most = 0;
-            for (int w = 0; w < kLatLoaders; ++w) {
-                mine[w] = theirs[w] = issued[w];
-                if constexpr (Two) theirs[w] = __float_as_int(load_cluster<float>(smem_u32((const void *)(issued + w)), rank ^ 1));
-                most = max(most, max(mine[w], theirs[w]));
-            }
-            uint32_t seen = 0;  // stages whose last use was looked at
-            for (int k = most - 1; k >= 0 && k >= most - 2 * S; --k) {
-                const int s = k % S;
-                const bool own = k < mine[k & 1], other = k < theirs[k & 1];
-                if (((seen >> s) & 1u) || (!own && !other)) continue;
-                seen |= 1u << s;
-                const uint32_t bar = bar_full + 8 * s;
-                if constexpr (Two) {
-                    if (!other) {
-                        const uint32_t missing = (uint32_t)(all_bytes[s] - own_bytes[s]);
-                        if (missing)
-                            asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(missing)
-                                         : "memory");
-                    } else if (!own) {
-                        mbar_arrive_expect_tx(bar, (uint32_t)__float_as_int(load_cluster<float>(smem_u32((const void *)(own_bytes + s)), rank ^ 1)));
-                    }
-                }
-                mbar_wait_bounded(bar, (uint32_t)((k / S) & 1), nullptr, kDrainLimitNs);
-            }
+            // every copy on its way lands before this CTA leaves; what the last tile still expects was never asked for
+            if (missing)
+                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar_full + 8 * ((g_loads - 1) % NS)), "r"(missing)
+                             : "memory");
+            for (uint32_t k = g_loads > NS ? g_loads - NS : 0; k < g_loads; ++k)
+                mbar_wait_bounded(bar_full + 8 * (k % NS), (k / NS) & 1, nullptr, kDrainLimitNs);
             if (q_loads > 0) mbar_wait_bounded(bar_qfull, (q_loads - 1) & 1, nullptr, kDrainLimitNs);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (Two) cluster_sync();
     if (warp == kLatMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tm_o, L::kCols);
@@ -838,12 +696,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 
 // ---- joining the parts of units that were cut -----------------------------------------------------
 // One CTA per row at a time, four elements a thread: out = sum_p e^(lse_p - lse) out_p, as in the other merges of partial
-// softmaxes.  It also writes the rows of sequences without tokens, which no cluster has.
+// softmaxes.  It also writes the rows of sequences without tokens, which no CTA has.
 constexpr int kLatJoinThreads = kLatentDim / 4;
 
 __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const LatentAttnParams p, int chunk_rows, int64_t all_rows)
 {
-    __shared__ float weight[kLatentMaxClusters];
+    __shared__ float weight[kLatentMaxCtas];
     __shared__ float total_lse;
     const int tid = threadIdx.x;
     pdl_wait_primary();
@@ -860,9 +718,9 @@ __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const Late
             continue;
         }
         const int2 info = p.unit_parts[(int64_t)b * p.chunks + chunk];
-        const int first = max(0, min(info.x, p.clusters - 1)), parts = max(0, min(info.y, p.clusters - first));
+        const int first = max(0, min(info.x, p.ctas - 1)), parts = max(0, min(info.y, p.ctas - first));
         if (parts <= 1) continue;
-        // part k of the unit lies in the last part of the first cluster and in the first parts of those behind it
+        // part k of the unit lies in the last part of the first CTA and in the first parts of those behind it
         auto place = [&](int k) { return (int64_t)(2 * (first + k) + (k == 0)) * chunk_rows + cr; };
         __syncthreads();  // the last row's weights are read
         if (tid < 32) {
@@ -893,50 +751,36 @@ __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const Late
     }
 }
 
-template <int R, bool Two>
-static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tv, const CUtensorMap &tq, LatentAttnParams p, int sms, cudaStream_t stream)
+template <int R>
+static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, LatentAttnParams p, int sms, cudaStream_t stream)
 {
-    using L = LatentLayout<R, Two>;
-    constexpr int kCtas = Two ? 2 : 1;
-    static int most[64] = {};  // per device: clusters that run at once
+    using L = LatentLayout<R>;
+    static int ready[64] = {};  // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!most[dev]) {
-        e = cudaFuncSetAttribute(latent_attn_kernel<R, Two>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(latent_attn_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
         if (e != cudaSuccess) return e;
-        int n = sms;
-        if constexpr (Two) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(2 * sms), cfg.blockDim = dim3(kLatThreads), cfg.dynamicSmemBytes = L::kAlloc;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim = {2, 1, 1};
-            cfg.attrs = attr, cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, latent_attn_kernel<R, Two>, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-        most[dev] = max(1, min(n, kLatentMaxClusters / kCtas));
+        ready[dev] = 1;
     }
-    // no more clusters than there can be tiles
-    const int64_t tiles = (int64_t)p.B * p.chunks * (((int64_t)p.max_nb + kLatTileBlocks - 1) / kLatTileBlocks);
-    p.clusters = (int)min((int64_t)most[dev], tiles);
-    e = launch_clusters(latent_attn_kernel<R, Two>, dim3(p.clusters * kCtas), dim3(kLatThreads), dim3(kCtas, 1, 1), L::kAlloc,
-                        stream, tc, tv, tq, p);
+    // no more CTAs than there can be tiles
+    const int64_t tiles = (int64_t)p.B * p.chunks * (((int64_t)p.max_nb + L::kBlocks - 1) / L::kBlocks);
+    p.ctas = (int)min((int64_t)min(sms, kLatentMaxCtas), tiles);
+    e = launch_kernel(latent_attn_kernel<R>, dim3(p.ctas), dim3(kLatThreads), L::kAlloc, stream, true, tc, tq, p);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.B * p.rows;
-    return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p,
-                         kCtas * R, rows);
+    return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p, R,
+                         rows);
 }
 
-cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tv, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
                                int sms, cudaStream_t stream)
 {
-    if (plan.ctas == 2) return latent_attn_t<64, true>(tc, tv, tq, p, sms, stream);
-    if (plan.cta_rows == 64) return latent_attn_t<64, false>(tc, tv, tq, p, sms, stream);
-    if (plan.cta_rows == 32) return latent_attn_t<32, false>(tc, tv, tq, p, sms, stream);
-    return latent_attn_t<16, false>(tc, tv, tq, p, sms, stream);
+    if (plan.cta_rows == 64) return latent_attn_t<64>(tc, tq, p, sms, stream);
+    if (plan.cta_rows == 32) return latent_attn_t<32>(tc, tq, p, sms, stream);
+    return latent_attn_t<16>(tc, tq, p, sms, stream);
 }
 
 }  // namespace pkv
