@@ -688,7 +688,7 @@ size_t pkv_latent_workspace_bytes(int32_t num_seqs, int32_t num_new, int32_t num
 /* Decode attention over a latent cache, the num_new (1..64) newest tokens of each sequence, already appended (context_lens
    counts them): row c_j of the cache,  s_j = scale q . c_j (576 elements),  out = sum_j softmax(s)_j c_j[:512], token t over
    the tokens [0, ctx - num_new + t] (no visible key: out 0, lse -inf).  q bf16 [num_seqs][num_new][N][576], 16-byte aligned
-   device memory; out bf16 [num_seqs][num_new][N][512] (4-byte aligned); lse_out float [num_seqs][num_new][N], natural
+   device memory; out bf16 [num_seqs][num_new][N][512] (16-byte aligned); lse_out float [num_seqs][num_new][N], natural
    log, nullable.  Any N.  The tiles of all sequences are dealt out evenly over the GPU, whatever the lengths: which parts a
    sequence is cut into, and so the last bits of its result, depend on the other sequences of the batch.  Softmax weights
    are rounded to bf16 before they multiply the values (they sum to one as rounded).  Two launches (the second joins what

@@ -16,9 +16,11 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["pkv_api.cu", "pkv_attn.cu", "pkv_attn_cols.cu", "pkv_attn_tc.cu", "pkv_cache_ops.cu",
            "pkv_rope.cu", "pkv_select.cu", "pkv_attn_blocks.cu", "pkv_verify.cu",
-           "pkv_latent_append.cu", "pkv_latent_attn.cu", "pkv_sequences.cu"]
+           "pkv_latent_append.cu", "pkv_latent_attn.cu", "pkv_latent_pair.cu",
+           "pkv_sequences.cu"]
 HEADERS = ["pkv_device.cuh", "pkv_internal.h", "pkv_attn_common.cuh", "pkv_cols.cuh", "pkv_tcgen05.cuh",
-           "pkv_cluster.cuh", "pkv_ops.h", "pkv_latent.h", "pkv_sequences.h"]
+           "pkv_cluster.cuh", "pkv_ops.h", "pkv_latent.h",
+           "pkv_latent.cuh", "pkv_sequences.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

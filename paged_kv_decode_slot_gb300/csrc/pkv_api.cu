@@ -732,7 +732,7 @@ struct LatentWorkspace {
 };
 LatentWorkspace latent_workspace(int64_t num_seqs, const pkv::LatentPlan &plan)
 {
-    const size_t rows = 2 * (size_t)pkv::kLatentMaxCtas * plan.cta_rows;
+    const size_t rows = 2 * (size_t)(pkv::kLatentMaxCtas / plan.ctas()) * plan.chunk_rows;
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
     LatentWorkspace w;
     w.lse_at = up(rows * pkv::kLatentDim * 4);
@@ -750,31 +750,25 @@ int check_latent_sizes(int32_t num_seqs, int32_t num_new, int32_t num_q_heads)
     return PKV_OK;
 }
 
-// The cache as (64 elements, 8 tokens, chunk of 64 elements, half of a block, block), a block a box; the queries as
-// (64 elements, row, chunk), a CTA's rows a box.  Both land as rows of 128 bytes, 128-byte swizzled.
-int make_latent_maps(CUtensorMap *tc, CUtensorMap *tq, const void *cache, int32_t num_blocks, const void *q, int64_t rows,
-                     int cta_rows)
+// The cache as (64 elements, 8 tokens, chunk of 64 elements, half of a block, block), `chunks` chunks of a block a box; the
+// queries as (64 elements, row, chunk), `rows` rows of a chunk a box.  Both land as rows of 128 bytes, 128-byte swizzled.
+CUresult encode_latent_map(CUtensorMap *map, const void *cache, int32_t num_blocks, int chunks)
 {
-    if (!encode_fn()) {
-        g_last_error = "cuTensorMapEncodeTiled is unavailable from the driver";
-        return PKV_ERR_CUDA;
-    }
-    const cuuint64_t row = kLatentRow * 2, chunks = kLatentRow / 64;
+    const cuuint64_t row = kLatentRow * 2;
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    const cuuint64_t cd[5] = {64, 8, chunks, 2, (cuuint64_t)num_blocks}, cs[4] = {row, 128, 8 * row, 16 * row};
-    const cuuint32_t cb[5] = {64, 8, (cuuint32_t)chunks, 2, 1};
-    CUresult r = encode_fn()(tc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(cache), cd, cs, cb, es,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r == CUDA_SUCCESS) {
-        const cuuint64_t qd[3] = {64, (cuuint64_t)rows, chunks}, qs[2] = {row, 128};
-        const cuuint32_t qb[3] = {64, (cuuint32_t)cta_rows, 1};
-        r = encode_fn()(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), qd, qs, qb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    }
-    if (r == CUDA_SUCCESS) return PKV_OK;
-    g_last_error = "cuTensorMapEncodeTiled failed (CUresult " + std::to_string((int)r) + ")";
-    return PKV_ERR_CUDA;
+    const cuuint64_t d[5] = {64, 8, kLatentRow / 64, 2, (cuuint64_t)num_blocks}, s[4] = {row, 128, 8 * row, 16 * row};
+    const cuuint32_t b[5] = {64, 8, (cuuint32_t)chunks, 2, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(cache), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+CUresult encode_latent_queries(CUtensorMap *map, const void *q, int64_t all_rows, int rows)
+{
+    const cuuint64_t row = kLatentRow * 2;
+    const cuuint32_t es[3] = {1, 1, 1};
+    const cuuint64_t d[3] = {64, (cuuint64_t)all_rows, kLatentRow / 64}, s[2] = {row, 128};
+    const cuuint32_t b[3] = {64, (cuuint32_t)rows, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace
@@ -829,7 +823,7 @@ PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_
     if (st == PKV_OK) st = check_latent_sizes(num_seqs, num_new, num_q_heads);
     if (st != PKV_OK) return st;
     if (max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * 16 > INT32_MAX) return PKV_ERR_SHAPE;
-    if (!aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(out, 4) || !aligned(lse_out, 4)) return PKV_ERR_ALIGN;
+    if (!aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(out, 16) || !aligned(lse_out, 4)) return PKV_ERR_ALIGN;
     const pkv::LatentPlan plan = pkv::latent_plan((int64_t)num_new * num_q_heads);
     const LatentWorkspace w = latent_workspace(num_seqs, plan);
     if (!workspace || workspace_bytes < w.bytes) return PKV_ERR_WORKSPACE;
@@ -850,13 +844,29 @@ PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_
 #ifdef PKV_TEST_HOOKS
     p.withhold_tile = g_withhold_tile.load(std::memory_order_relaxed);
 #endif
-    CUtensorMap tc, tq;
-    st = make_latent_maps(&tc, &tq, latent_cache, cache.num_blocks, q, (int64_t)num_seqs * p.rows, plan.cta_rows);
-    if (st != PKV_OK) return st;
     int sms = 0;
     st = sm_count(&sms);
     if (st != PKV_OK) return st;
-    cudaError_t e = pkv::launch_latent_attn(tc, tq, p, plan, sms, stream);
+    if (!encode_fn()) {
+        g_last_error = "cuTensorMapEncodeTiled is unavailable from the driver";
+        return PKV_ERR_CUDA;
+    }
+    const int64_t all_rows = (int64_t)num_seqs * p.rows;
+    pkv::LatentPairMaps m;
+    CUresult r = encode_latent_queries(&m.queries, q, all_rows, plan.chunk_rows / plan.ctas());
+    if (plan.ctas() == 1) {
+        if (r == CUDA_SUCCESS) r = encode_latent_map(&m.keys, latent_cache, cache.num_blocks, kLatentRow / 64);
+    } else {
+        if (r == CUDA_SUCCESS) r = encode_latent_map(&m.keys, latent_cache, cache.num_blocks, 2);
+        if (r == CUDA_SUCCESS) r = encode_latent_map(&m.rope, latent_cache, cache.num_blocks, 1);
+        if (r == CUDA_SUCCESS) r = encode_latent_map(&m.values, latent_cache, cache.num_blocks, 4);
+    }
+    if (r != CUDA_SUCCESS) {
+        g_last_error = "cuTensorMapEncodeTiled failed (CUresult " + std::to_string((int)r) + ")";
+        return PKV_ERR_CUDA;
+    }
+    cudaError_t e = plan.ctas() == 1 ? pkv::launch_latent_attn(m.keys, m.queries, p, plan.chunk_rows, sms, stream)
+                                     : pkv::launch_latent_pair(m, p, sms, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "latent attention launch");
 }
 

@@ -1,0 +1,172 @@
+// pkv_latent.cuh - what the two kernels of attention over a latent cache share: how the tiles of a batch are dealt out,
+// waits, and the like.
+#pragma once
+
+#include <float.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "pkv_latent.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+
+constexpr int kLatChunks = (kLatentDim + kLatentRope) / 64;   // 64-element chunks of a row
+constexpr float kLatRescale = 8.f;                            // log2 of how far a logit may exceed the running maximum
+
+// ---- dealing out the tiles ----------------------------------------------------------------------
+// A unit's share of the work: its tiles and, as much as this many, its queries, statistics and outputs.
+template <int kTile>
+__device__ __forceinline__ constexpr int latent_unit_cost()
+{
+    return kTile >= 128 ? 1 : 3;
+}
+
+__device__ __forceinline__ int latent_ctx(const LatentAttnParams &p, int b)
+{
+    const int ctx = __ldg(p.context_lens + b);
+    return ctx < 0 || ctx > p.max_nb * kBlockSize ? 0 : ctx;
+}
+template <int kTile>
+__device__ __forceinline__ int latent_cost(int ctx)
+{
+    return ctx > 0 ? (ctx + kTile - 1) / kTile + latent_unit_cost<kTile>() : 0;
+}
+
+// Tiles [t0, t1) of unit (b, chunk), which starts at `start` in the row of all units.
+struct LatentSegment {
+    int b, chunk, ctx, t0, t1, tiles;
+    int64_t start;
+    bool whole;
+};
+
+template <int kTile>
+struct LatentWalk {
+    int64_t lo, hi, start;
+    int b, chunk;
+    __device__ __forceinline__ bool next(const LatentAttnParams &p, LatentSegment &s)
+    {
+        while (start < hi && b < p.B) {
+            const int ctx = latent_ctx(p, b), cost = latent_cost<kTile>(ctx);
+            const int64_t at = start;
+            const int ub = b, uc = chunk;
+            start += cost;
+            if (++chunk == p.chunks || cost == 0) chunk = 0, ++b;
+            if (cost == 0) continue;
+            const int x0 = (int)max((int64_t)0, lo - at), x1 = (int)min((int64_t)cost, hi - at);
+            s.t0 = max(0, x0 - latent_unit_cost<kTile>()), s.t1 = max(0, x1 - latent_unit_cost<kTile>());
+            if (s.t0 >= s.t1) continue;
+            s.b = ub, s.chunk = uc, s.ctx = ctx, s.tiles = cost - latent_unit_cost<kTile>(), s.start = at;
+            s.whole = s.t0 == 0 && s.t1 == s.tiles;
+            return true;
+        }
+        return false;
+    }
+};
+
+// This CTA's (or cluster's: `cta` of p.ctas) run of the work, the same in every thread; false: nothing to do.  `sums` holds kThreads + 4 64-bit
+// words of shared memory.  Every thread calls it.
+template <int kTile, int kThreads>
+__device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, int64_t *sums, LatentWalk<kTile> &w, int64_t &total,
+                                            int &ctas)
+{
+    const int tid = threadIdx.x, per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int64_t cost = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int ctx = __ldg(p.context_lens + b);
+        if (cta == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+        cost += latent_cost<kTile>(latent_ctx(p, b));
+    }
+    sums[tid] = cost;
+    __syncthreads();
+    if (tid < 32) {  // exclusive scan by one warp, ten entries a lane
+        constexpr int kPer = kThreads / 32;
+        int64_t mine = 0;
+        for (int k = 0; k < kPer; ++k) mine += sums[tid * kPer + k];
+        int64_t before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (tid >= o) before += up;
+        }
+        if (tid == 31) sums[kThreads] = before;
+        before -= mine;
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t v = sums[tid * kPer + k];
+            sums[tid * kPer + k] = before;
+            before += v;
+        }
+    }
+    __syncthreads();
+    const int64_t all = sums[kThreads];
+    total = all * p.chunks;
+    // no more runs than units and tiles: a run then holds at least one of them
+    ctas = (int)min((int64_t)p.ctas, total);
+    if (cta >= ctas) return false;
+    w.lo = total * cta / ctas;
+    w.hi = total * (cta + 1) / ctas;
+    int64_t at = sums[tid] * p.chunks;
+    if (at <= w.lo && w.lo < (sums[tid] + cost) * p.chunks) {
+        for (int b = b0; b < b1; ++b) {
+            const int c = latent_cost<kTile>(latent_ctx(p, b));
+            if (w.lo < at + (int64_t)c * p.chunks) {
+                const int chunk = (int)((w.lo - at) / c);
+                sums[kThreads + 1] = b;
+                sums[kThreads + 2] = chunk;
+                sums[kThreads + 3] = at + (int64_t)chunk * c;
+                break;
+            }
+            at += (int64_t)c * p.chunks;
+        }
+    }
+    __syncthreads();
+    w.b = (int)sums[kThreads + 1];
+    w.chunk = (int)sums[kThreads + 2];
+    w.start = sums[kThreads + 3];
+    return true;
+}
+
+// mbar_wait_bounded with the clock read late: %globaltimer takes 0.4 us to read, as long as a stage of the ring is in use, so
+// the first tries (each suspends the thread for a while) go without it.
+__device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
+{
+#pragma unroll 1
+    for (int it = 0; it < 64; ++it)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, abort, limit_ns);
+}
+
+// ---- small pieces -------------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// Barrier of four softmax warps that share rows (128 threads; `half` 0 or 1), and the same with a vote.
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ bool half_any(int half, bool v)
+{
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(1 + half), "r"((int)v)
+        : "memory");
+    return r != 0;
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+}  // namespace pkv

@@ -14,18 +14,19 @@ constexpr int kLatentDim = 512;   // the latent vector of a token
 constexpr int kLatentRope = 64;   // its rotary key
 constexpr int kLatentMaxCtas = 152;
 
-// How the (token, head) rows of a sequence are dealt to CTAs: chunks of cta_rows rows.
+// How the (token, head) rows of a sequence are dealt out: chunks of chunk_rows rows, to a CTA (16 or 32) or to a pair of
+// CTAs (128, 64 each).
 struct LatentPlan {
-    int cta_rows;
+    int chunk_rows;
     int64_t chunks;
+    int ctas() const { return chunk_rows == 128 ? 2 : 1; }
 };
-// The narrowest of 16, 32 and 64 rows a CTA that holds a sequence's rows (the products cost their tokens and, less, their
-// rows; what the queries leave free of shared memory takes loads ahead).
+// The narrowest that holds a sequence's rows.
 inline LatentPlan latent_plan(int64_t rows)
 {
     LatentPlan p;
-    p.cta_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.chunks = (rows + p.cta_rows - 1) / p.cta_rows;
+    p.chunk_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+    p.chunks = (rows + p.chunk_rows - 1) / p.chunk_rows;
     return p;
 }
 
@@ -35,13 +36,13 @@ struct LatentAttnParams {
     int32_t max_nb, B, N, T, num_blocks;
     int32_t rows;                  // T * N
     int32_t chunks;                // chunks of rows a sequence
-    int32_t ctas;                  // CTAs of the grid (set by the launcher)
+    int32_t ctas;                  // CTAs, or pairs of them, of the grid (set by the launcher)
     float scale_log2;
     __nv_bfloat16 *out;            // [B][T][N][512]
     float *lse_out;                // [B][T][N], nullable
-    // workspace: two parts a CTA of cta_rows rows each, and of each (sequence, chunk) its first CTA and its parts
-    float *part_out;               // [2 ctas][cta_rows][512]
-    float *part_lse;               // [2 ctas][cta_rows], log2
+    // workspace: two parts a CTA (or pair), and of each (sequence, chunk) its first CTA and how many there are
+    float *part_out;               // [2 ctas][chunk_rows][512]
+    float *part_lse;               // [2 ctas][chunk_rows], log2
     int2 *unit_parts;              // [B][chunks]
     int32_t *err_flag;
     uint64_t wait_ns;
@@ -50,8 +51,14 @@ struct LatentAttnParams {
 #endif
 };
 
-cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
-                               int sms, cudaStream_t stream);
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, int cta_rows, int sms,
+                               cudaStream_t stream);
+// Maps of the cache with boxes of a block's two chunks (keys), one chunk (the rotary key) and four chunks (values).
+struct LatentPairMaps {
+    CUtensorMap keys, rope, values, queries;
+};
+cudaError_t launch_latent_pair(const LatentPairMaps &maps, const LatentAttnParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_latent_join(const LatentAttnParams &p, int chunk_rows, int sms, cudaStream_t stream);
 
 // Norm and rotation of new tokens' rows with their append, and rotation of their queries (pkv_latent_append.cu).
 struct LatentAppendParams {

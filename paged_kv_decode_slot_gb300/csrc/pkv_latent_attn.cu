@@ -3,11 +3,12 @@
 // the queries before and applied to the outputs after).
 //     s[r][j] = scale q[r] . c[j],  out[r] = sum_j softmax(s[r])_j c[j][:512],  r a (token, head) row of a sequence.
 //
-// All rows share the keys, so the contraction is dense: with 128 rows 2 * 1088 * 128 operations for 1,152 bytes, 242 a
-// byte, about what the chip has for one byte of DRAM.  Hence the tcgen05 tensor cores, and both products transposed:
+// This is the kernel for sequences of at most 32 rows (few heads, as one of several GPUs has them); more rows take
+// pkv_latent_pair.cu.  All rows share the keys, so that even here the contraction is dense (35 operations a byte with 16 rows)
+// and goes to the tcgen05 tensor cores, both products transposed:
 //     S^T[64 tokens x R]  = C[64 x 576] . Q^T       A: the tile's rows as they lie (K-major), B: the queries
 //     O^T[512 x R]       += C^T[512 x 64] . P^T     A: the same bytes read MN-major (four M = 128 products), B: P
-// so that R = 16, 32 or 64 query rows a CTA is the N of the products, not a padded M: the 512 x R accumulator takes 4 R
+// so that R = 16 or 32 query rows a CTA is the N of the products, not a padded M: the 512 x R accumulator takes 4 R
 // of the 512 tensor-memory columns, and a tile is loaded once and read as keys and as values where it lies.
 //
 // A block of 16 tokens is one TMA load of 18 KB, a box of (64 elements, 8 tokens, 9 chunks of elements, 2 halves): it
@@ -22,28 +23,21 @@
 // 9 the loads, 10 zeroes what lies behind a sequence's end.  QK^T of tile i + 1 is issued before P V of tile i, so the tensor
 // cores work through the softmax of tile i.  The running maxima move only when a logit exceeds them by 2^8 (found with one
 // barrier vote a tile); the sums stay in the threads' registers, a part for each token lane, until the end.
-#include <float.h>
-
-#include "pkv_device.cuh"
-#include "pkv_internal.h"
-#include "pkv_latent.h"
-#include "pkv_tcgen05.cuh"
+#include "pkv_latent.cuh"
 
 namespace pkv {
 
-constexpr int kLatChunks = (kLatentDim + kLatentRope) / 64;   // 64-element chunks of a row
 constexpr int kLatGroup = kLatChunks * 1024;                  // bytes of eight tokens: an atom per chunk
 constexpr int kLatBlock = 2 * kLatGroup;                      // and of a block
 constexpr int kLatSoftmaxWarps = 8, kLatMmaWarp = 8, kLatLoadWarp = 9, kLatTailWarp = 10;
 constexpr int kLatThreads = 352;
-constexpr float kLatRescale = 8.f;                            // log2 of how far a logit may exceed the running maximum
 
 // R: query rows of a CTA.
 template <int R>
 struct LatentLayout {
-    static_assert(R == 16 || R == 32 || R == 64, "rows of a CTA");
-    static constexpr int kBlocks = R == 64 ? 4 : 3;      // blocks of a tile (M = 64: at most four)
-    static constexpr int kSlots = R == 64 ? 2 : 3;       // tiles in shared memory
+    static_assert(R == 16 || R == 32, "rows of a CTA");
+    static constexpr int kBlocks = 3;                    // blocks of a tile (M = 64: at most four)
+    static constexpr int kSlots = 3;                     // tiles in shared memory
     static constexpr int kTile = kBlocks * kBlockSize;   // tokens of a tile
     static constexpr int kRing = kSlots * kBlocks;
     static constexpr int kQChunk = R * 128;              // 64 elements of R queries, K-major, 128-byte swizzle
@@ -64,135 +58,15 @@ struct LatentLayout {
     static_assert(kQOffset % 1024 == 0 && kPOffset % 1024 == 0 && kSlots <= 4, "swizzle atoms are aligned");
     static_assert((kSlots - 1) * kBlocks * kLatBlock + 8 * kLatGroup <= kBytes, "M = 64 rows from any slot on lie inside the window");
     static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
-    static constexpr uint32_t kCols = R == 64 ? 512 : R == 32 ? 256 : 128;  // tensor memory: O^T 4 R, S^T 2 R
+    static constexpr uint32_t kCols = R == 32 ? 256 : 128;  // tensor memory: O^T 4 R, S^T 2 R
 };
-
-// ---- dealing out the tiles ----------------------------------------------------------------------
-// A unit's share of the work: its tiles and, as much as this many, its queries, statistics and outputs.
-constexpr int kLatUnitCost = 2;
-
-__device__ __forceinline__ int latent_ctx(const LatentAttnParams &p, int b)
-{
-    const int ctx = __ldg(p.context_lens + b);
-    return ctx < 0 || ctx > p.max_nb * kBlockSize ? 0 : ctx;
-}
-template <int R>
-__device__ __forceinline__ int latent_cost(int ctx)
-{
-    constexpr int kTile = LatentLayout<R>::kTile;
-    return ctx > 0 ? (ctx + kTile - 1) / kTile + kLatUnitCost : 0;
-}
-
-// Tiles [t0, t1) of unit (b, chunk), which starts at `start` in the row of all units.
-struct LatentSegment {
-    int b, chunk, ctx, t0, t1, tiles;
-    int64_t start;
-    bool whole;
-};
-
-template <int R>
-struct LatentWalk {
-    int64_t lo, hi, start;
-    int b, chunk;
-    __device__ __forceinline__ bool next(const LatentAttnParams &p, LatentSegment &s)
-    {
-        while (start < hi && b < p.B) {
-            const int ctx = latent_ctx(p, b), cost = latent_cost<R>(ctx);
-            const int64_t at = start;
-            const int ub = b, uc = chunk;
-            start += cost;
-            if (++chunk == p.chunks || cost == 0) chunk = 0, ++b;
-            if (cost == 0) continue;
-            const int x0 = (int)max((int64_t)0, lo - at), x1 = (int)min((int64_t)cost, hi - at);
-            s.t0 = max(0, x0 - kLatUnitCost), s.t1 = max(0, x1 - kLatUnitCost);
-            if (s.t0 >= s.t1) continue;
-            s.b = ub, s.chunk = uc, s.ctx = ctx, s.tiles = cost - kLatUnitCost, s.start = at;
-            s.whole = s.t0 == 0 && s.t1 == s.tiles;
-            return true;
-        }
-        return false;
-    }
-};
-
-// This CTA's run of the work, the same in every thread; false: nothing to do.  `sums` holds kLatThreads + 4 64-bit
-// words of shared memory.  Every thread calls it.
-template <int R>
-__device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, int64_t *sums, LatentWalk<R> &w, int64_t &total,
-                                            int &ctas)
-{
-    const int tid = threadIdx.x, per = (p.B + kLatThreads - 1) / kLatThreads;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int64_t cost = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int ctx = __ldg(p.context_lens + b);
-        if (cta == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
-        cost += latent_cost<R>(latent_ctx(p, b));
-    }
-    sums[tid] = cost;
-    __syncthreads();
-    if (tid < 32) {  // exclusive scan by one warp, ten entries a lane
-        constexpr int kPer = kLatThreads / 32;
-        int64_t mine = 0;
-        for (int k = 0; k < kPer; ++k) mine += sums[tid * kPer + k];
-        int64_t before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, before, o);
-            if (tid >= o) before += up;
-        }
-        if (tid == 31) sums[kLatThreads] = before;
-        before -= mine;
-        for (int k = 0; k < kPer; ++k) {
-            const int64_t v = sums[tid * kPer + k];
-            sums[tid * kPer + k] = before;
-            before += v;
-        }
-    }
-    __syncthreads();
-    const int64_t all = sums[kLatThreads];
-    total = all * p.chunks;
-    // no more runs than units and tiles: a run then holds at least one of them
-    ctas = (int)min((int64_t)p.ctas, total);
-    if (cta >= ctas) return false;
-    w.lo = total * cta / ctas;
-    w.hi = total * (cta + 1) / ctas;
-    int64_t at = sums[tid] * p.chunks;
-    if (at <= w.lo && w.lo < (sums[tid] + cost) * p.chunks) {
-        for (int b = b0; b < b1; ++b) {
-            const int c = latent_cost<R>(latent_ctx(p, b));
-            if (w.lo < at + (int64_t)c * p.chunks) {
-                const int chunk = (int)((w.lo - at) / c);
-                sums[kLatThreads + 1] = b;
-                sums[kLatThreads + 2] = chunk;
-                sums[kLatThreads + 3] = at + (int64_t)chunk * c;
-                break;
-            }
-            at += (int64_t)c * p.chunks;
-        }
-    }
-    __syncthreads();
-    w.b = (int)sums[kLatThreads + 1];
-    w.chunk = (int)sums[kLatThreads + 2];
-    w.start = sums[kLatThreads + 3];
-    return true;
-}
-
-// mbar_wait_bounded with the clock read late: %globaltimer takes 0.4 us to read, as long as a stage of the ring is in use, so
-// the first tries (each suspends the thread for a while) go without it.
-__device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
-{
-#pragma unroll 1
-    for (int it = 0; it < 64; ++it)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_bounded(bar, parity, abort, limit_ns);
-}
 
 // ---- small pieces -------------------------------------------------------------------------------
 // Descriptor of P^T as an MN-major operand of R elements a row: the swizzle is as wide as the row.
 template <int R>
 __device__ __forceinline__ uint64_t latent_p_desc(uint32_t addr)
 {
-    constexpr uint64_t kMode = R == 64 ? 2 : R == 32 ? 4 : 6;
+    constexpr uint64_t kMode = R == 32 ? 4 : 6;
     constexpr uint32_t kGroup = 8 * R * 2;  // eight tokens
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kGroup >> 4) << 16) | ((uint64_t)(kGroup >> 4) << 32) | (1ull << 46) |
            (kMode << 61);
@@ -202,17 +76,8 @@ __device__ __forceinline__ uint64_t latent_p_desc(uint32_t addr)
 template <int R>
 __device__ __forceinline__ uint32_t latent_p_at(int t, int u)
 {
-    const int x = R == 64 ? t & 7 : R == 32 ? (t >> 1) & 3 : (t >> 2) & 1;
+    const int x = R == 32 ? (t >> 1) & 3 : (t >> 2) & 1;
     return (uint32_t)(t * (R * 2) + ((u ^ x) << 4));
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
 }
 
 // C columns of a warp's 32 lanes (C = 8, 16 or 32).
@@ -284,28 +149,6 @@ __device__ __forceinline__ float reduce_columns(float (&x)[C], int lane, Op op)
     return v;
 }
 
-// Barrier of the four warps of one half of the rows (128 threads), and the same with a vote.
-__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
-__device__ __forceinline__ bool half_any(int half, bool v)
-{
-    int r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %2, 0;\n\t"
-        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(1 + half), "r"((int)v)
-        : "memory");
-    return r != 0;
-}
-
-// One thread of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 template <int R>
 __global__ void __launch_bounds__(kLatThreads, 1)
 latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_q, const LatentAttnParams p)
@@ -320,11 +163,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 
     pdl_wait_primary();
     pdl_launch_dependents();
-    LatentWalk<R> walk;
+    LatentWalk<L::kTile> walk;
     int64_t total;
     int ctas;
     // (the sums lie where the first tiles will)
-    if (!latent_deal<R>(p, cta, reinterpret_cast<int64_t *>(mem), walk, total, ctas)) return;
+    if (!latent_deal<L::kTile, kLatThreads>(p, cta, reinterpret_cast<int64_t *>(mem), walk, total, ctas)) return;
 
     const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
     const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * NS, bar_qfull = bar_empty + 8 * kRing,
@@ -526,7 +369,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             const int nrows = min(R, p.rows - row0);
             if (threadIdx.x == 0 && sg.t0 == 0) {
                 // for the joining launch: the first CTA of the unit's parts, and how many there are
-                const int64_t last = sg.start + sg.tiles + kLatUnitCost - 1;
+                const int64_t last = sg.start + sg.tiles + latent_unit_cost<L::kTile>() - 1;
                 const int parts = sg.whole ? 1 : (int)(((last + 1) * ctas - 1) / total) - cta + 1;
                 p.unit_parts[(int64_t)sg.b * p.chunks + sg.chunk] = make_int2(cta, parts);
             }
@@ -751,6 +594,13 @@ __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const Late
     }
 }
 
+cudaError_t launch_latent_join(const LatentAttnParams &p, int chunk_rows, int sms, cudaStream_t stream)
+{
+    const int64_t rows = (int64_t)p.B * p.rows;
+    return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p,
+                         chunk_rows, rows);
+}
+
 template <int R>
 static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, LatentAttnParams p, int sms, cudaStream_t stream)
 {
@@ -769,18 +619,13 @@ static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, L
     const int64_t tiles = (int64_t)p.B * p.chunks * (((int64_t)p.max_nb + L::kBlocks - 1) / L::kBlocks);
     p.ctas = (int)min((int64_t)min(sms, kLatentMaxCtas), tiles);
     e = launch_kernel(latent_attn_kernel<R>, dim3(p.ctas), dim3(kLatThreads), L::kAlloc, stream, true, tc, tq, p);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)p.B * p.rows;
-    return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p, R,
-                         rows);
+    return e != cudaSuccess ? e : launch_latent_join(p, R, sms, stream);
 }
 
-cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, const LatentPlan &plan,
-                               int sms, cudaStream_t stream)
+cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, int cta_rows, int sms,
+                               cudaStream_t stream)
 {
-    if (plan.cta_rows == 64) return latent_attn_t<64>(tc, tq, p, sms, stream);
-    if (plan.cta_rows == 32) return latent_attn_t<32>(tc, tq, p, sms, stream);
-    return latent_attn_t<16>(tc, tq, p, sms, stream);
+    return cta_rows == 32 ? latent_attn_t<32>(tc, tq, p, sms, stream) : latent_attn_t<16>(tc, tq, p, sms, stream);
 }
 
 }  // namespace pkv
