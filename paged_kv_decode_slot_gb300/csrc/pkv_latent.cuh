@@ -127,14 +127,19 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, 
     return true;
 }
 
-// mbar_wait_bounded with the clock read late: %globaltimer takes 0.4 us to read, as long as a stage of the ring is in use, so
-// the first tries (each suspends the thread for a while) go without it.
-__device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
+// mbar_wait_bounded in two parts.  What is met on every stage of a pipeline stays short: with the loop in line a wait for a
+// barrier that was ready took 220 clocks, with the call behind the first try 50.  And %globaltimer takes 0.4 us to read, as
+// long as a stage is in use, so the first tries (each suspends the thread for a while) go without it.
+static __device__ __noinline__ bool latent_wait_on(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
 {
 #pragma unroll 1
     for (int it = 0; it < 64; ++it)
         if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_bounded(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
+{
+    return mbar_try_wait(bar, parity) || latent_wait_on(bar, parity, abort, limit_ns);
 }
 
 // ---- small pieces -------------------------------------------------------------------------------

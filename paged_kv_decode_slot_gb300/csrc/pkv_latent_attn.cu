@@ -203,67 +203,75 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     auto wait_one = [&](uint32_t bar, uint32_t parity) { return latent_wait(bar, parity, abort_flag, p.wait_ns); };
     auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)); };
 
-    // of the loading warp: tiles begun, bytes of the last one that were not asked for, segments whose queries were
+    bool issuer = false;  // of the loading and the MMA warp: the thread that issues
+    // of the loading thread: tiles begun, bytes of the last one that were not asked for, segments whose queries were
     uint32_t g_loads = 0, missing = 0, q_loads = 0;
-    bool issuer = false;  // of the MMA warp: the thread that issues (and so the one whose MMAs a commit speaks of)
     if (warp == kLatLoadWarp) {
-        // ------------------------------ loads ------------------------------
-        if (lane == 0) {
+        // ------------------------------ loads: one thread ------------------------------
+        issuer = elect_one();
+        if (issuer) {
             prefetch_tensormap(&tm_c);
             prefetch_tensormap(&tm_q);
-        }
-        bool ok = true, withheld = false;
-        int slot = 0;
-        uint32_t parity = 0;  // of the slot's uses
-        LatentSegment sg;
-        while (ok && walk.next(p, sg)) {
-            // the queries, once the last unit's are no longer needed
-            if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
-            if (!ok) break;
-            const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * R;
-            if (lane == 0) mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
-            __syncwarp();
-            if (lane < kLatChunks) tma_load_3d(q_u32 + lane * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, lane);
-            ++q_loads;
-            const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
-            const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
-            auto ids_of = [&](int t) {
-                const int j = t * NB + lane;
-                return lane < NB && t < sg.t1 && j < nb ? __ldg(tbl + j) : -1;
-            };
-            int next = ids_of(sg.t0);
-            for (int t = sg.t0; t < sg.t1 && ok; ++t) {
-                const int ids = next;
-                next = ids_of(t + 1);
-                const int nblk = min(NB, nb - t * NB);
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < nblk && ids >= 0 && ids < p.num_blocks);
-                if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
-                    withheld = true, ok = false;
-                    break;
-                }
-                const uint32_t bar = bar_full + 8 * slot;
-                const bool used = g_loads >= NS;
-#pragma unroll 1
-                for (int j = 0; j < NB; ++j) {
-                    if (used) ok = wait(bar_empty + 8 * (slot * NB + j), parity ^ 1u);
-                    if (!ok) break;
-                    const int id = __shfl_sync(0xFFFFFFFFu, ids, j);
-                    if (j == 0) missing = (uint32_t)__popc(mask) * kLatBlock, ++g_loads;
-                    if (lane == 0) {
+            bool ok = true, withheld = false;
+            int slot = 0;
+            uint32_t parity = 0;  // of the slot's uses
+            LatentSegment sg;
+            while (ok && walk.next(p, sg)) {
+                // the queries, once the last unit's are no longer needed
+                if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
+                if (!ok) break;
+                const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * R;
+                mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
+                for (int c = 0; c < kLatChunks; ++c) tma_load_3d(q_u32 + c * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, c);
+                ++q_loads;
+                const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
+                const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
+                int next[NB];
+                auto ids_of = [&](int t) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) next[k] = t < sg.t1 && t * NB + k < nb ? __ldg(tbl + t * NB + k) : -1;
+                };
+                ids_of(sg.t0);
+                for (int t = sg.t0; t < sg.t1 && ok; ++t) {
+                    const int nblk = min(NB, nb - t * NB);
+                    int ids[NB];
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        ids[k] = next[k];
+                        mask |= (uint32_t)(ids[k] >= 0 && ids[k] < p.num_blocks) << k;
+                    }
+                    ids_of(t + 1);
+                    if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
+                        withheld = true, ok = false;
+                        break;
+                    }
+                    if (mask != (1u << nblk) - 1u) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                    const uint32_t bar = bar_full + 8 * slot;
+                    const bool used = g_loads >= NS;
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        if (ok && used) ok = wait_one(bar_empty + 8 * (slot * NB + j), parity ^ 1u);
+                        if (!ok) continue;
                         if (j == 0) {
-                            if (mask != (1u << nblk) - 1u) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-                            tile_mask[(g_loads - 1) & 3] = (int)mask;
+                            missing = (uint32_t)__popc(mask) * kLatBlock;
+                            tile_mask[g_loads++ & 3] = (int)mask;
                             mbar_arrive_expect_tx(bar, missing);
                         }
-                        if ((mask >> j) & 1u) tma_load_5d(ring + (slot * NB + j) * kLatBlock, &tm_c, bar, 0, 0, 0, 0, id);
+                        if ((mask >> j) & 1u) {
+                            tma_load_5d(ring + (slot * NB + j) * kLatBlock, &tm_c, bar, 0, 0, 0, 0, ids[j]);
+                            missing -= kLatBlock;
+                        }
                     }
-                    if ((mask >> j) & 1u) missing -= kLatBlock;
-                    __syncwarp();
+                    if (++slot == NS) slot = 0, parity ^= 1u;
                 }
-                if (++slot == NS) slot = 0, parity ^= 1u;
+            }
+            if (!ok && !withheld) {
+                if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+                *abort_flag = 1;
             }
         }
-        if (!ok && !withheld) give_up();
+        __syncwarp();
     } else if (warp == kLatTailWarp) {
         // ---------------- rows behind a sequence's end ----------------
         // They may hold anything, and 0 x NaN is NaN: they are zeroed before P V reads them, when the MMA warp asks for it
@@ -519,7 +527,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             __syncwarp();
             mbar_wait_bounded(bar_fin, 0u, nullptr, kDrainLimitNs);
         }
-        if (warp == kLatLoadWarp && lane == 0) {
+        if (warp == kLatLoadWarp && issuer) {
             // every copy on its way lands before this CTA leaves; what the last tile still expects was never asked for
             if (missing)
                 asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar_full + 8 * ((g_loads - 1) % NS)), "r"(missing)

@@ -91,38 +91,11 @@ __device__ __forceinline__ uint32_t pair_at(uint32_t at, int rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
     return there;
 }
+// (what the arrival speaks of was fenced for the asynchronous proxy, which is who reads it)
 __device__ __forceinline__ void pair_arrive(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-__device__ __forceinline__ bool pair_try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-// latent_wait, seeing what the other CTA released.
-__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, const volatile int *abort, uint64_t limit_ns)
-{
-#pragma unroll 1
-    for (int it = 0; it < 64; ++it)
-        if (pair_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (pair_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0u) {
-            if (abort && *abort) return false;
-            if (globaltimer_ns() - t0 > limit_ns) return false;
-        }
-    }
-}
-
 // TMA loads into this CTA's shared memory, counted on a barrier of the cluster.
 __device__ __forceinline__ void pair_load_5d(uint32_t dst, const CUtensorMap *map, uint32_t cluster_bar, int c0, int c1, int c2, int c3,
                                              int c4)
@@ -214,101 +187,114 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
         if (lane == 0 && !*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
         *abort_flag = 1;
     };
-    auto wait_one = [&](uint32_t bar, uint32_t parity) { return pair_wait(bar, parity, abort_flag, p.wait_ns); };
+    auto wait_one = [&](uint32_t bar, uint32_t parity) { return latent_wait(bar, parity, abort_flag, p.wait_ns); };
     auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)); };
     bool issuer = false;  // the thread that issues the MMAs (a commit speaks of its thread's)
 
     if (warp == kPairLoadWarp) {
-        // ------------------------------ loads ------------------------------
-        if (lane == 0) {
+        // ------------------------------ loads: one thread ------------------------------
+        if (elect_one()) {
             prefetch_tensormap(&maps.keys);
             prefetch_tensormap(&maps.rope);
             prefetch_tensormap(&maps.values);
             prefetch_tensormap(&maps.queries);
-        }
-        int n = 0;           // stages so far
-        uint32_t g = 0, q_loads = 0;
-        bool ok = true, withheld = false;
-        // Stage n, once it is free; the first CTA's barrier is told what both will send.
-        auto open = [&](int bytes_all, int bytes_own) {
-            const int s = n % S;
-            if (n >= S) ok = wait(bar_empty + 8 * s, (uint32_t)(((n / S) & 1) ^ 1));
-            if (ok && lane == 0) {
+            const uint32_t full_there = pair_at(bar_full, 0), qfull_there = pair_at(bar_qfull, 0);
+            int n = 0;           // stages so far
+            uint32_t g = 0, q_loads = 0;
+            bool ok = true, withheld = false;
+            // Stage n, once it is free; the first CTA's barrier is told what both will send.
+            auto open = [&](int bytes_all, int bytes_own) {
+                const int s = n % S;
+                if (n >= S) ok = wait_one(bar_empty + 8 * s, (uint32_t)(((n / S) & 1) ^ 1));
+                if (!ok) return;
                 sent[s] = bytes_own, use[s] = n + 1;
                 if (rank == 0) {
                     want[s] = bytes_all;
                     mbar_arrive_expect_tx(bar_full + 8 * s, (uint32_t)bytes_all);
                 }
-            }
-            __syncwarp();
-        };
-        auto fill_v = [&](int ids, uint32_t mask, int nblk) {
-#pragma unroll 1
-            for (int v = 0; v < 4 && 2 * v < nblk; ++v, ++n) {
-                const uint32_t two = (mask >> (2 * v)) & 3u;
-                const int id = __shfl_sync(0xFFFFFFFFu, ids, (2 * v + lane) & 7);
-                open(2 * __popc(two) * 8192, __popc(two) * 8192);
-                if (!ok) return;
-                if (lane < 2 && ((two >> lane) & 1u))
-                    pair_load_5d(ring + (n % S) * L::kStage + lane * 8192, &maps.values, pair_at(bar_full + 8 * (n % S), 0), 0, 0, 4 * rank, 0, id);
-            }
-        };
-        LatentSegment sg;
-        while (ok && walk.next(p, sg)) {
-            // the queries, once the last unit's are no longer needed
-            if (q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
-            if (!ok) break;
-            const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * 128 + rank * L::kRows;
-            ++q_loads;
-            if (lane == 0) {
-                *q_asked = (int)q_loads;
-                if (rank == 0) mbar_arrive_expect_tx(bar_qfull, 2 * L::kQBytes);
-            }
-            __syncwarp();
-            if (lane < kLatChunks) pair_load_3d(q_u32 + lane * L::kQChunk, &maps.queries, pair_at(bar_qfull, 0), 0, (int)row, lane);
-            const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
-            const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
-            auto ids_of = [&](int t) {
-                const int j = t * L::kBlocks + lane;
-                return lane < L::kBlocks && t < sg.t1 && j < nb ? __ldg(tbl + j) : -1;
             };
-            int next = ids_of(sg.t0), prev = -1, prev_nblk = 0;
+            int prev[L::kBlocks];
             uint32_t prev_mask = 0;
-            for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
-                const int ids = next;
-                next = ids_of(t + 1);
-                const int nblk = min(L::kBlocks, nb - t * L::kBlocks);
-                const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lane < nblk && ids >= 0 && ids < p.num_blocks);
-                if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
-                    withheld = true, ok = false;
-                    break;
+            auto fill_v = [&](int nblk) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    if (2 * v >= nblk) break;
+                    const uint32_t two = (prev_mask >> (2 * v)) & 3u;
+                    open(2 * __popc(two) * 8192, __popc(two) * 8192);
+                    if (!ok) return;
+                    const uint32_t dst = ring + (n % S) * L::kStage, bar = full_there + 8 * (n % S);
+                    if (two & 1u) pair_load_5d(dst, &maps.values, bar, 0, 0, 4 * rank, 0, prev[2 * v]);
+                    if (two & 2u) pair_load_5d(dst + 8192, &maps.values, bar, 0, 0, 4 * rank, 0, prev[2 * v + 1]);
+                    ++n;
                 }
-                if (lane == 0) {
+            };
+            LatentSegment sg;
+            while (ok && walk.next(p, sg)) {
+                // the queries, once the last unit's are no longer needed
+                if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
+                if (!ok) break;
+                const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * 128 + rank * L::kRows;
+                *q_asked = (int)++q_loads;
+                if (rank == 0) mbar_arrive_expect_tx(bar_qfull, 2 * L::kQBytes);
+                for (int c = 0; c < kLatChunks; ++c) pair_load_3d(q_u32 + c * L::kQChunk, &maps.queries, qfull_there, 0, (int)row, c);
+                const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
+                const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
+                int next[L::kBlocks];
+                auto ids_of = [&](int t) {
+#pragma unroll
+                    for (int k = 0; k < L::kBlocks; ++k) {
+                        const int j = t * L::kBlocks + k;
+                        next[k] = t < sg.t1 && j < nb ? __ldg(tbl + j) : -1;
+                    }
+                };
+                ids_of(sg.t0);
+                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
+                    const int nblk = min(L::kBlocks, nb - t * L::kBlocks);
+                    int ids[L::kBlocks];
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int k = 0; k < L::kBlocks; ++k) {
+                        ids[k] = next[k];
+                        mask |= (uint32_t)(ids[k] >= 0 && ids[k] < p.num_blocks) << k;
+                    }
+                    ids_of(t + 1);
+                    if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
+                        withheld = true, ok = false;
+                        break;
+                    }
                     if (mask != (1u << nblk) - 1u && rank == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
                     tile_mask[g & 3] = (int)mask;
-                }
-                const uint32_t own = (mask >> (4 * rank)) & 0xFu;
-                const int id = __shfl_sync(0xFFFFFFFFu, ids, (4 * rank + lane) & 7);
-                const bool mine = lane < 4 && ((own >> lane) & 1u);
+                    const uint32_t own = (mask >> (4 * rank)) & 0xFu;
+                    int mine[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mine[k] = rank ? ids[4 + k] : ids[k];
 #pragma unroll 1
-                for (int c = 0; c < 5; ++c, ++n) {
-                    const int bytes = c < 4 ? 4096 : 2048;
-                    open(__popc(mask) * bytes, __popc(own) * bytes);
-                    if (!ok) break;
-                    if (mine)
-                        pair_load_5d(ring + (n % S) * L::kStage + lane * bytes, c < 4 ? &maps.keys : &maps.rope, pair_at(bar_full + 8 * (n % S), 0),
-                                     0, 0, 2 * c, 0, id);
+                    for (int c = 0; c < 5; ++c, ++n) {
+                        const int bytes = c < 4 ? 4096 : 2048;
+                        open(__popc(mask) * bytes, __popc(own) * bytes);
+                        if (!ok) break;
+                        const CUtensorMap *const map = c < 4 ? &maps.keys : &maps.rope;
+                        const uint32_t dst = ring + (n % S) * L::kStage, bar = full_there + 8 * (n % S);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if ((own >> k) & 1u) pair_load_5d(dst + k * bytes, map, bar, 0, 0, 2 * c, 0, mine[k]);
+                    }
+                    if (t > sg.t0 && ok) fill_v(L::kBlocks);
+                    prev_mask = mask;
+#pragma unroll
+                    for (int k = 0; k < L::kBlocks; ++k) prev[k] = ids[k];
                 }
-                if (t > sg.t0 && ok) fill_v(prev, prev_mask, prev_nblk);
-                prev = ids, prev_mask = mask, prev_nblk = nblk;
+                if (ok) fill_v(min(L::kBlocks, nb - (sg.t1 - 1) * L::kBlocks));
             }
-            if (ok) fill_v(prev, prev_mask, prev_nblk);
+            // every stage and the queries released: no arrival is on its way into this CTA any more
+            for (int k = max(0, n - S); k < n && ok; ++k) ok = wait_one(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
+            if (ok && q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
+            if (!ok && !withheld) {
+                if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+                *abort_flag = 1;
+            }
         }
-        if (!ok && !withheld) give_up();
-        // every stage and the queries released: no arrival is on its way into this CTA any more
-        for (int k = max(0, n - S); k < n && ok; ++k) ok = wait(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
-        if (ok && q_loads > 0) ok = wait(bar_qfree, (q_loads - 1) & 1);
-        if (!ok && !withheld) give_up();
+        __syncwarp();
     } else if (warp == kPairTailWarp) {
         // ---------------- rows behind a sequence's end ----------------
         // They may hold anything, and 0 x NaN is NaN: both CTAs zero them before P V reads them, when the MMA thread asks for it
