@@ -730,7 +730,8 @@ size_t pkv_blocks_workspace_bytes(int32_t num_blocks);
    copies[b] (int32 [num_seqs][2]) = (old, new), to be copied before the new tokens are written; otherwise copies[b] =
    (-1, -1).  (Rows that share it and grow in one call are taken in order: the last holder keeps the block.)  Once a row needs
    more blocks than are left, it and all growing rows behind it stay as they are and PKV_FLAG_NO_BLOCKS is set.  A negative
-   num_new, or a row that would outgrow its table, sets PKV_FLAG_CTX_RANGE and that row stays as it is. */
+   num_new, a context outside [0, 16 max_blocks_per_seq], or a row that would outgrow its table, sets PKV_FLAG_CTX_RANGE and that
+   row stays as it is. */
 int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *num_new,
                          int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks, int32_t *copies, void *workspace,
                          size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);

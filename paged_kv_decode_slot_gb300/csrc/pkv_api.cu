@@ -892,7 +892,9 @@ PKV_EXPORT int pkv_fork_sequences(const int32_t *block_tables, int32_t max_block
                                   int32_t num_blocks, int32_t *block_tables_out, int32_t *context_lens_out,
                                   int32_t *err_flag, pkv_stream_t stream)
 {
-    if (!block_tables || !context_lens || !parents || !ref_counts || !block_tables_out || !context_lens_out) return PKV_ERR_NULL;
+    if ((num_seqs != 0 && (!block_tables || !context_lens)) || !ref_counts ||
+        (num_seqs_out != 0 && (!parents || !block_tables_out || !context_lens_out)))
+        return PKV_ERR_NULL;
     int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
     if (st != PKV_OK) return st;
     if (num_seqs_out < 0 || (int64_t)num_seqs + num_seqs_out > INT32_MAX) return PKV_ERR_SHAPE;
@@ -937,7 +939,7 @@ PKV_EXPORT int pkv_compact_blocks(int32_t *block_tables, int32_t max_blocks_per_
                                   int32_t max_moves, int32_t *num_moves, void *workspace, size_t workspace_bytes,
                                   int32_t *err_flag, pkv_stream_t stream)
 {
-    if (!block_tables || !context_lens || !ref_counts || !moves || !num_moves) return PKV_ERR_NULL;
+    if ((num_seqs != 0 && (!block_tables || !context_lens)) || !ref_counts || !moves || !num_moves) return PKV_ERR_NULL;
     int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
     if (st != PKV_OK) return st;
     if (max_moves <= 0) return PKV_ERR_SHAPE;

@@ -486,7 +486,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             half_sync(half);
             const float *f = quarters + c0 + col;
             const float all = (f[0] + f[R]) + (f[2 * R] + f[3 * R]), hi = top[c0 + col];
-            const bool seen = hi != -FLT_MAX;
+            const bool seen = all != 0.f;  // (NaN is something)
             const int64_t part = (int64_t)(2 * cta + (sg.t0 == 0)) * R;  // rows of the workspace
             if (quarter == 0 && lane < CW && c0 + lane < nrows) {
                 const float lse2 = seen ? hi + log2f(all) : -INFINITY;

@@ -168,8 +168,8 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
         for (int s = 0; s < S; ++s) sent[s] = use[s] = want[s] = 0;
         for (int k = 0; k < L::kBars; ++k) {
             const uint32_t bar = bar_full + 8 * k;
-            // weights: the softmax warps of both CTAs; zeroed rows: both CTAs
-            mbar_init(bar, bar == bar_p ? 2 * kPairSoftmaxWarps : bar == bar_tail + 8 ? 2 : 1);
+            // weights: the softmax warps of both CTAs; stages and zeroed rows: both CTAs
+            mbar_init(bar, bar == bar_p ? 2 * kPairSoftmaxWarps : k < S || bar == bar_tail + 8 ? 2 : 1);
         }
         fence_barrier_init();
     }
@@ -202,7 +202,9 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             int n = 0;           // stages so far
             uint32_t g = 0, q_loads = 0;
             bool ok = true, withheld = false;
-            // Stage n, once it is free; the first CTA's barrier is told what both will send.
+            // Stage n, once it is free; the first CTA's barrier is told what both will send.  The second CTA arrives there for
+            // every stage, also for one that it has nothing to send for: the MMAs could otherwise use and release the stage
+            // twice before this thread came to wait for the first time (a barrier tells only neighbouring uses apart).
             auto open = [&](int bytes_all, int bytes_own) {
                 const int s = n % S;
                 if (n >= S) ok = wait_one(bar_empty + 8 * s, (uint32_t)(((n / S) & 1) ^ 1));
@@ -211,6 +213,8 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                 if (rank == 0) {
                     want[s] = bytes_all;
                     mbar_arrive_expect_tx(bar_full + 8 * s, (uint32_t)bytes_all);
+                } else {
+                    pair_arrive(full_there + 8 * s);
                 }
             };
             int prev[L::kBlocks];
@@ -514,7 +518,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             quarter_at[64 * (side + 2 * h)] = l;
             half_sync(group);
             const float all = (quarter_at[0] + quarter_at[64]) + (quarter_at[128] + quarter_at[192]);
-            const bool seen = m != -FLT_MAX;
+            const bool seen = all != 0.f;  // (NaN is something)
             const float inv = seen ? 1.f / all : 0.f;
             const int64_t part = (int64_t)(2 * pair + (sg.t0 == 0)) * 128 + rank * L::kRows + r;  // row of the workspace
             const int64_t row = (int64_t)sg.b * p.rows + row0 + r;
@@ -563,25 +567,27 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
         if (warp == kPairLoadWarp && lane == 0) {
             // Every copy on its way, into either CTA, is counted here: it lands before they leave.  A barrier is told to
             // expect what was asked for, where one of the two stopped before the other.
-            auto settle = [&](uint32_t bar, int number, int own, int other_number, int other, int told) {
+            auto settle = [&](uint32_t bar, int number, int own, int other_number, int other, int told, bool both_arrive) {
                 if (number == 0 && other_number == 0) return;
                 const int last = max(number, other_number);
                 const int coming = (number == last ? own : 0) + (other_number == last ? other : 0);
                 if (number != last) {
                     mbar_arrive_expect_tx(bar, (uint32_t)coming);
-                } else if (told != coming) {
+                    return;
+                }
+                if (told != coming)
                     asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"((uint32_t)(told - coming))
                                  : "memory");
-                }
+                if (both_arrive && other_number != last) mbar_arrive(bar);
             };
             for (int s = 0; s < S; ++s) {
                 const int mine = use[s], theirs = load_word(use + s, 1);
-                settle(bar_full + 8 * s, mine, sent[s], theirs, load_word(sent + s, 1), want[s]);
+                settle(bar_full + 8 * s, mine, sent[s], theirs, load_word(sent + s, 1), want[s], true);
                 const int last = max(mine, theirs);
                 if (last > 0) mbar_wait_bounded(bar_full + 8 * s, (uint32_t)(((last - 1) / S) & 1), nullptr, kDrainLimitNs);
             }
             const int mine = *q_asked, theirs = load_word(q_asked, 1), last = max(mine, theirs);
-            settle(bar_qfull, mine, L::kQBytes, theirs, L::kQBytes, 2 * L::kQBytes);
+            settle(bar_qfull, mine, L::kQBytes, theirs, L::kQBytes, 2 * L::kQBytes, false);
             if (last > 0) mbar_wait_bounded(bar_qfull, (uint32_t)((last - 1) & 1), nullptr, kDrainLimitNs);
         }
     }

@@ -467,9 +467,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pools_kernel(const __grid_c
             const int pair = (int)(k / p.num_pools);
             pool = (int)(k - (int64_t)pair * p.num_pools);
             src = __ldcg(p.src_dst + 2 * (int64_t)pair), dst = __ldcg(p.src_dst + 2 * (int64_t)pair + 1);
-            if ((src | dst) != -1 && (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks)) {
-                if (tid < 32) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-                src = -1;
+            if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+                if (tid < 32 && (src != -1 || dst != -1)) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                src = dst = -1;
             }
         }
         unsigned todo = __ballot_sync(0xFFFFFFFFu, src >= 0 && src != dst);

@@ -555,6 +555,99 @@ class SparseDecodeStep:
         return [getattr(self, n) for n in self.input_names()]
 
 
+class LatentDecodeStep:
+    """A decode step over a latent cache (one row of 576 elements a token, shared by all heads):
+    ``pkv_latent_append_multi`` norms the T newest tokens' latent vectors, turns their rotary keys and writes both into
+    their slots, and turns the rotary parts of their queries into ``q``; ``pkv_decode_attn_latent`` attends.
+
+    kv_new bf16 [B, T, 576] (latent vector, rotary key), q_rope bf16 [B, T, N, 64] before the rotation (any strides with
+    contiguous elements, e.g. a slice of the query projection's output), q bf16 [B, T, N, 576] whose first 512 elements
+    a head hold the queries that the key projection was absorbed into; latent_cache [num_blocks, 16, 576], block_tables
+    [B, max_blocks] and context_lens [B] (which count the new tokens) in device memory; inv_freq float64 [32];
+    norm_weight bf16 [512] or None.  q[..., 512:], slot_mapping, out [B, T, N, 512] and lse are written."""
+
+    def __init__(self, kv_new, q_rope, q, latent_cache, block_tables, context_lens, scale, inv_freq, norm_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, err_flag=None):
+        self.kv_new, self.q_rope, self.q = kv_new, q_rope, q
+        self.latent_cache, self.block_tables, self.context_lens = latent_cache, block_tables, context_lens
+        self.scale, self.inv_freq, self.norm_weight = float(scale), inv_freq, norm_weight
+        self.eps, self.interleaved, self.err_flag = float(eps), bool(interleaved), err_flag
+        nseq, T, N, _ = q.shape
+        dev = latent_cache.device
+        self.plan = AttentionPlan("latent", 0, 0)
+        self.fused = True
+        self.slot_mapping = torch.empty(nseq, T, dtype=torch.int64, device=dev)
+        self.out = torch.empty(nseq, T, N, B.PKV_LATENT_DIM, dtype=q.dtype, device=dev)
+        self.lse = torch.empty(nseq, T, N, dtype=torch.float32, device=dev)
+        self.workspace = torch.empty(B.pkv_latent_workspace_bytes(nseq, T, N), dtype=torch.uint8, device=dev)
+
+    def run(self, stream=None) -> None:
+        B.check(B.pkv_latent_append_multi(self.kv_new, self.q_rope, self.block_tables, self.context_lens, self.inv_freq,
+                                          self.latent_cache, self.q, self.slot_mapping, self.norm_weight, self.eps,
+                                          self.interleaved, self.err_flag, stream))
+        B.check(B.pkv_decode_attn_latent(self.q, self.latent_cache, self.block_tables, self.context_lens, self.scale,
+                                         self.out, self.lse, self.workspace, self.err_flag, stream))
+
+    def launches_per_step(self) -> int:
+        return 3  # append, attention, the join of sequences that several CTAs attended to
+
+    def input_names(self):
+        return ("kv_new", "q_rope", "q", "block_tables", "context_lens")
+
+    def inputs(self):
+        return [getattr(self, n) for n in self.input_names()]
+
+
+class SequenceBlocks:
+    """The rows of a batch and the blocks they hold, kept on the device: ``block_tables`` int32 [num_seqs, max_blocks],
+    ``context_lens`` int32 [num_seqs] (what the steps take) and ``ref_counts`` int32 [num_blocks].  All rows start empty.
+
+    ``extend`` before a step makes room for its new tokens, ``fork`` after one lets rows take over others (beams, samples
+    of one prompt, sequences that end), ``compact`` moves blocks to the front of the pools.  ``pools`` are the tensors
+    [num_blocks, ...] of every layer that the tables speak of, in groups of one shape and type.  Nothing is read back: too few
+    free blocks, say, shows in ``err_flag`` and in the lengths that did not grow."""
+
+    def __init__(self, num_seqs: int, max_blocks: int, num_blocks: int, device="cuda", err_flag=None):
+        ints = dict(dtype=torch.int32, device=device)
+        self.block_tables = torch.full((num_seqs, max_blocks), -1, **ints)
+        self.context_lens = torch.zeros(num_seqs, **ints)
+        self.ref_counts = torch.zeros(num_blocks, **ints)
+        self.copies = torch.full((num_seqs, 2), -1, **ints)
+        self.moves = torch.full((max(1, num_blocks // 2), 2), -1, **ints)
+        self.num_moves = torch.zeros(1, **ints)
+        self.err_flag = err_flag
+        self.workspace = torch.empty(B.pkv_blocks_workspace_bytes(num_blocks), dtype=torch.uint8, device=device)
+        self._other = (torch.empty_like(self.block_tables), torch.empty_like(self.context_lens))
+
+    def _copy(self, pools, pairs, stream) -> None:
+        groups = {}
+        for p in pools:
+            groups.setdefault((p.shape, p.dtype), []).append(p)
+        for same in groups.values():
+            B.check(B.pkv_copy_blocks_pools(same, pairs, self.err_flag, stream))
+
+    def extend(self, num_new, pools=(), stream=None) -> None:
+        """Row b grows by num_new[b] (int32 [num_seqs]) tokens; shared last blocks are copied on write in ``pools``."""
+        B.check(B.pkv_extend_sequences(self.block_tables, self.context_lens, num_new, self.ref_counts, self.copies,
+                                       self.workspace, self.err_flag, stream))
+        self._copy(pools, self.copies, stream)
+
+    def fork(self, parents, stream=None) -> None:
+        """Row b becomes what row parents[b] (int32 [num_seqs]) was, or empty (-1).  The tensors ``block_tables`` and
+        ``context_lens`` change places with a second pair, so steps are given them anew."""
+        tables, lens = self._other
+        B.check(B.pkv_fork_sequences(self.block_tables, self.context_lens, parents, self.ref_counts, tables, lens,
+                                     self.err_flag, stream))
+        self._other = (self.block_tables, self.context_lens)
+        self.block_tables, self.context_lens = tables, lens
+
+    def compact(self, pools=(), stream=None) -> None:
+        """The used blocks become the pools' first ones."""
+        B.check(B.pkv_compact_blocks(self.block_tables, self.context_lens, self.ref_counts, self.moves, self.num_moves,
+                                     self.workspace, self.err_flag, stream))
+        self._copy(pools, self.moves, stream)
+
+
 class LayerStack:
     """One decode step of a model with several attention layers: the same sequences (block tables
     and context lengths) in every layer, each layer with its own pools and its own q, k_new and
