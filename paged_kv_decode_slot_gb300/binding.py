@@ -1113,6 +1113,11 @@ def pkv_latent_append(kv_new, q_rope, positions, inv_freq, slot_mapping, latent_
     of latent_cache bf16 [num_blocks, 16, 576]; q_rope bf16 [T, N, 64] (any token and head strides) turned into
     q [T, N, 576][..., 512:].  positions int32 [T], inv_freq float64 [32], norm_weight bf16 [512] or None."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.latent_append(kv_new, q_rope, positions, inv_freq, latent_cache, q, slot_mapping, norm_weight, eps, interleaved,
+                                      err_flag, stream, dev)
+        if status is not None:
+            return status
     n = _shape(kv_new, 2, "kv_new")[0]
     cp, desc = _latent_cache(latent_cache, dev)
     kp, rp, token, head, qp, N = _latent_rows(kv_new, q_rope, q, (n,), dev)
@@ -1131,6 +1136,11 @@ def pkv_latent_append_multi(kv_new, q_rope, block_tables, context_lens, inv_freq
     """pkv_latent_append of the T newest tokens of each sequence: kv_new [B, T, 576], q_rope [B, T, N, 64],
     q [B, T, N, 576]; slot_mapping int64 [B, T] (written)."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.latent_append_multi(kv_new, q_rope, block_tables, context_lens, inv_freq, latent_cache, q, slot_mapping,
+                                            norm_weight, eps, interleaved, err_flag, stream, dev)
+        if status is not None:
+            return status
     B, T = _shape(kv_new, 3, "kv_new")[:2]
     cp, desc = _latent_cache(latent_cache, dev)
     kp, rp, token, head, qp, N = _latent_rows(kv_new, q_rope, q, (B, T), dev)
@@ -1153,7 +1163,11 @@ def pkv_decode_attn_latent(q, latent_cache, block_tables, context_lens, scale: f
     """Decode attention of the T newest tokens of each sequence over a latent cache: q bf16 [B, T, N, 576], out bf16
     [B, T, N, 512], lse_out float32 [B, T, N]; workspace: pkv_latent_workspace_bytes(B, T, N) bytes."""
     dev = _current_device()
-    B, T, N, _ = qs = _shape(q, 4, "q")
+    if _calls is not None:
+        status = _calls.decode_attn_latent(q, latent_cache, block_tables, context_lens, scale, out, lse_out, workspace, err_flag, stream, dev)
+        if status is not None:
+            return status
+    B, T, N, _ = _shape(q, 4, "q")
     cp, desc = _latent_cache(latent_cache, dev)
     tp, width, lp = _table_args(block_tables, context_lens, B, dev)
     size = 0 if workspace is None else _shape(workspace, 1, "workspace")[0]
@@ -1180,6 +1194,10 @@ def pkv_fork_sequences(block_tables, context_lens, parents, ref_counts, block_ta
     """Row b of block_tables_out [B', W] and context_lens_out [B'] becomes row parents[b] of the old ones [B, W], [B], or
     empty (-1); ref_counts int32 [num_blocks] follows."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.fork_sequences(block_tables, context_lens, parents, ref_counts, block_tables_out, context_lens_out, err_flag, stream, dev)
+        if status is not None:
+            return status
     B, R = _shape(context_lens, 1, "context_lens")[0], _shape(parents, 1, "parents")[0]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
     nb = _shape(ref_counts, 1, "ref_counts")[0]
@@ -1202,6 +1220,10 @@ def pkv_extend_sequences(block_tables, context_lens, num_new, ref_counts, copies
     copies int32 [B, 2] (written): the copy on write of each row, or (-1, -1).  workspace:
     pkv_blocks_workspace_bytes(num_blocks) bytes."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag, stream, dev)
+        if status is not None:
+            return status
     B, nb = _shape(context_lens, 1, "context_lens")[0], _shape(ref_counts, 1, "ref_counts")[0]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
     size = _shape(workspace, 1, "workspace")[0]
@@ -1218,6 +1240,10 @@ def pkv_compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves,
     """Blocks moved towards the front: moves int32 [max_moves, 2] and num_moves int32 [1] (written), block_tables [B, W]
     and ref_counts [num_blocks] in place.  workspace: pkv_blocks_workspace_bytes(num_blocks) bytes."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves, workspace, err_flag, stream, dev)
+        if status is not None:
+            return status
     B, nb = _shape(context_lens, 1, "context_lens")[0], _shape(ref_counts, 1, "ref_counts")[0]
     tp, width, cp = _table_args(block_tables, context_lens, B, dev)
     size, most = _shape(workspace, 1, "workspace")[0], _shape(moves, 2, "moves")[0]
@@ -1232,6 +1258,10 @@ def pkv_copy_blocks_pools(pools, src_dst, err_flag=None, stream=None) -> int:
     """Block src_dst[i, 1] of every pool [num_blocks, ...] (of one shape and type) becomes a copy of block src_dst[i, 0];
     (-1, -1) is skipped."""
     dev = _current_device()
+    if _calls is not None:
+        status = _calls.copy_blocks_pools(pools, src_dst, err_flag, stream, dev)
+        if status is not None:
+            return status
     pools = list(pools)
     if not pools:
         raise ValueError("pools is empty")

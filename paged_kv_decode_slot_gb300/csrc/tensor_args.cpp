@@ -83,7 +83,14 @@ PyObject *set_refuse(PyObject *, PyObject *f)
     X(pkv_select_blocks)                                                                                                        \
     X(pkv_decode_attn_blocks)                                                                                                   \
     X(pkv_decode_attn_blocks_fp8)                                                                                               \
-    X(pkv_verify_draft)
+    X(pkv_verify_draft)                                                                                                         \
+    X(pkv_latent_append)                                                                                                        \
+    X(pkv_latent_append_multi)                                                                                                  \
+    X(pkv_decode_attn_latent)                                                                                                   \
+    X(pkv_fork_sequences)                                                                                                       \
+    X(pkv_extend_sequences)                                                                                                     \
+    X(pkv_compact_blocks)                                                                                                       \
+    X(pkv_copy_blocks_pools)
 struct Library {
 #define PKV_MEMBER(f) decltype(&::f) f = nullptr;
     PKV_ENTRIES(PKV_MEMBER)
@@ -373,6 +380,154 @@ PyObject *verify_draft(PyObject *, PyObject *const *a, Py_ssize_t n)
                   out, ctx, ctx_out, ws, (size_t)size.v, err, stream);
 }
 
+// latent_append(kv_new, q_rope, positions | (block_tables, context_lens), inv_freq, latent_cache, q, slot_mapping, norm_weight,
+//               eps, interleaved, err_flag, stream, dev)
+template <bool kTables>
+PyObject *latent_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c(a, n, 13 + kTables);
+    Dim B, T, N, width, nb, bs{16}, row{PKV_LATENT_DIM + PKV_LATENT_ROPE}, half{PKV_LATENT_ROPE / 2}, dim{PKV_LATENT_DIM};
+    if (!kTables) T.v = 1;
+    const pkv_bf16 *kv = kTables ? c.tensor<pkv_bf16>(at::kBFloat16, {&B, &T, &row}) : c.tensor<pkv_bf16>(at::kBFloat16, {&B, &row});
+    // the queries' rotary parts: contiguous elements, heads and tokens any strides apart
+    const pkv_bf16 *q_rope = nullptr;
+    int64_t token = 0, head = 0;
+    if (c.ok && (c.ok = THPVariable_Check(*c.next))) {
+        const at::Tensor &t = THPVariable_Unpack(*c.next++);
+        const int lead = kTables ? 2 : 1;
+        c.ok = t.scalar_type() == at::kBFloat16 && t.is_cuda() && t.get_device() == c.dev && t.dim() == lead + 2 && t.numel() > 0 &&
+               t.size(0) == B.v && (!kTables || t.size(1) == T.v) && t.size(lead + 1) == PKV_LATENT_ROPE && t.stride(lead + 1) == 1;
+        if (c.ok) {
+            N.v = t.size(lead);
+            head = t.stride(lead);
+            token = kTables && T.v == 1 ? t.stride(0) : t.stride(lead - 1);
+            if (kTables && B.v > 1 && t.stride(0) != T.v * token) c.ok = false;
+            q_rope = static_cast<const pkv_bf16 *>(t.data_ptr());
+        }
+    }
+    const int32_t *positions = nullptr, *tables = nullptr, *lens = nullptr;
+    if constexpr (kTables) {
+        tables = c.tensor<int32_t>(at::kInt, {&B, &width});
+        lens = c.tensor<int32_t>(at::kInt, {&B});
+    } else {
+        positions = c.tensor<int32_t>(at::kInt, {&B});
+    }
+    const double *inv_freq = c.tensor<double>(at::kDouble, {&half});
+    pkv_bf16 *cache = c.tensor<pkv_bf16>(at::kBFloat16, {&nb, &bs, &row});
+    pkv_bf16 *q = kTables ? c.tensor<pkv_bf16>(at::kBFloat16, {&B, &T, &N, &row}) : c.tensor<pkv_bf16>(at::kBFloat16, {&B, &N, &row});
+    int64_t *slots = kTables ? c.tensor<int64_t>(at::kLong, {&B, &T}) : c.tensor<int64_t>(at::kLong, {&B});
+    const pkv_bf16 *weight = c.maybe<pkv_bf16>(at::kBFloat16, {&dim});
+    const float eps = c.f32();
+    const int32_t interleaved = c.i32();
+    int32_t *err = c.flag();
+    const pkv_stream_t stream = c.stream();
+    const pkv_cache_desc d{nb, bs, 1, row};
+    if constexpr (kTables)
+        return launch(c, g_lib.pkv_latent_append_multi, kv, q_rope, token, head, tables, width, lens, inv_freq, interleaved, weight, eps, B, T,
+                      N, cache, q, slots, d, err, stream);
+    else
+        return launch(c, g_lib.pkv_latent_append, kv, q_rope, token, head, positions, inv_freq, interleaved, weight, eps, slots, B, N, cache, q,
+                      d, err, stream);
+}
+
+// decode_attn_latent(q, latent_cache, block_tables, context_lens, scale, out, lse_out, workspace, err_flag, stream, dev)
+PyObject *decode_attn_latent(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c(a, n, 11);
+    Dim B, T, N, width, nb, bs{16}, row{PKV_LATENT_DIM + PKV_LATENT_ROPE}, dim{PKV_LATENT_DIM}, size;
+    const pkv_bf16 *q = c.tensor<pkv_bf16>(at::kBFloat16, {&B, &T, &N, &row});
+    const pkv_bf16 *cache = c.tensor<pkv_bf16>(at::kBFloat16, {&nb, &bs, &row});
+    const int32_t *tables = c.tensor<int32_t>(at::kInt, {&B, &width}), *lens = c.tensor<int32_t>(at::kInt, {&B});
+    const float scale = c.f32();
+    pkv_bf16 *out = c.tensor<pkv_bf16>(at::kBFloat16, {&B, &T, &N, &dim});
+    float *lse = c.maybe<float>(at::kFloat, {&B, &T, &N});
+    void *ws = c.tensor(at::kByte, {&size});
+    int32_t *err = c.flag();
+    const pkv_stream_t stream = c.stream();
+    return launch(c, g_lib.pkv_decode_attn_latent, q, cache, tables, width, lens, B, T, N, scale, out, lse, pkv_cache_desc{nb, bs, 1, row}, ws,
+                  (size_t)size.v, err, stream);
+}
+
+// fork_sequences(block_tables, context_lens, parents, ref_counts, block_tables_out, context_lens_out, err_flag, stream, dev)
+PyObject *fork_sequences(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c(a, n, 9);
+    Dim B, R, width, nb;
+    const int32_t *tables = c.tensor<int32_t>(at::kInt, {&B, &width}), *lens = c.tensor<int32_t>(at::kInt, {&B});
+    const int32_t *parents = c.tensor<int32_t>(at::kInt, {&R});
+    int32_t *refs = c.tensor<int32_t>(at::kInt, {&nb});
+    int32_t *tables_out = c.tensor<int32_t>(at::kInt, {&R, &width}), *lens_out = c.tensor<int32_t>(at::kInt, {&R});
+    int32_t *err = c.flag();
+    const pkv_stream_t stream = c.stream();
+    if (nb.v > INT32_MAX || R.v > INT32_MAX) c.ok = false;
+    return launch(c, g_lib.pkv_fork_sequences, tables, width, lens, B, parents, R, refs, nb, tables_out, lens_out, err, stream);
+}
+
+// extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag, stream, dev)
+PyObject *extend_sequences(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c(a, n, 9);
+    Dim B, width, nb, two{2}, size;
+    int32_t *tables = c.tensor<int32_t>(at::kInt, {&B, &width}), *lens = c.tensor<int32_t>(at::kInt, {&B});
+    const int32_t *num_new = c.tensor<int32_t>(at::kInt, {&B});
+    int32_t *refs = c.tensor<int32_t>(at::kInt, {&nb}), *copies = c.tensor<int32_t>(at::kInt, {&B, &two});
+    void *ws = c.tensor(at::kByte, {&size});
+    int32_t *err = c.flag();
+    const pkv_stream_t stream = c.stream();
+    if (nb.v > INT32_MAX) c.ok = false;
+    return launch(c, g_lib.pkv_extend_sequences, tables, width, lens, num_new, B, refs, nb, copies, ws, (size_t)size.v, err, stream);
+}
+
+// compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves, workspace, err_flag, stream, dev)
+PyObject *compact_blocks(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c(a, n, 9);
+    Dim B, width, nb, most, one{1}, two{2}, size;
+    int32_t *tables = c.tensor<int32_t>(at::kInt, {&B, &width});
+    const int32_t *lens = c.tensor<int32_t>(at::kInt, {&B});
+    int32_t *refs = c.tensor<int32_t>(at::kInt, {&nb}), *moves = c.tensor<int32_t>(at::kInt, {&most, &two});
+    int32_t *num_moves = c.tensor<int32_t>(at::kInt, {&one});
+    void *ws = c.tensor(at::kByte, {&size});
+    int32_t *err = c.flag();
+    const pkv_stream_t stream = c.stream();
+    if (nb.v > INT32_MAX) c.ok = false;
+    return launch(c, g_lib.pkv_compact_blocks, tables, width, lens, B, refs, nb, moves, most, num_moves, ws, (size_t)size.v, err, stream);
+}
+
+// copy_blocks_pools(pools, src_dst, err_flag, stream, dev); pools: a list or tuple of tensors of one shape and type
+PyObject *copy_blocks_pools(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c(a, n, 5);
+    void *at[256];
+    int32_t count = 0;
+    int64_t blocks = 0, bytes = 0;
+    if (c.ok && (c.ok = PyList_Check(*c.next) || PyTuple_Check(*c.next))) {
+        PyObject *const list = *c.next++, *const *const items = PySequence_Fast_ITEMS(list);
+        const Py_ssize_t k = PySequence_Fast_GET_SIZE(list);
+        c.ok = k >= 1 && k <= 256;
+        const at::Tensor *first = nullptr;
+        for (Py_ssize_t i = 0; c.ok && i < k; ++i) {
+            if (!(c.ok = THPVariable_Check(items[i]))) break;
+            const at::Tensor &t = THPVariable_Unpack(items[i]);
+            c.ok = t.is_cuda() && t.get_device() == c.dev && t.is_contiguous() && t.dim() >= 2 && t.numel() > 0;
+            if (!c.ok) break;
+            if (!first) {
+                first = &t;
+                blocks = t.size(0);
+                bytes = t.numel() / blocks * (int64_t)t.element_size();
+                c.ok = blocks <= INT32_MAX;
+            }
+            c.ok &= t.scalar_type() == first->scalar_type() && t.sizes() == first->sizes();
+            at[count++] = t.data_ptr();
+        }
+    }
+    Dim pairs, two{2};
+    const int32_t *src_dst = c.tensor<int32_t>(at::kInt, {&pairs, &two});
+    int32_t *err = c.flag();
+    const pkv_stream_t stream = c.stream();
+    return launch(c, g_lib.pkv_copy_blocks_pools, (void *const *)at, count, bytes, (int32_t)blocks, src_dst, pairs, err, stream);
+}
+
 // A whole call; a tensor that throws (a fake one has no address) is not plain.
 template <PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyObject *whole(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -399,6 +554,13 @@ PyMethodDef methods[] = {
     PKV_METHOD("decode_attn_blocks", whole<decode_attn_blocks<false>>),
     PKV_METHOD("decode_attn_blocks_fp8", whole<decode_attn_blocks<true>>),
     PKV_METHOD("verify_draft", whole<verify_draft>),
+    PKV_METHOD("latent_append", whole<latent_append<false>>),
+    PKV_METHOD("latent_append_multi", whole<latent_append<true>>),
+    PKV_METHOD("decode_attn_latent", whole<decode_attn_latent>),
+    PKV_METHOD("fork_sequences", whole<fork_sequences>),
+    PKV_METHOD("extend_sequences", whole<extend_sequences>),
+    PKV_METHOD("compact_blocks", whole<compact_blocks>),
+    PKV_METHOD("copy_blocks_pools", whole<copy_blocks_pools>),
     {"set_refuse", set_refuse, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
