@@ -161,14 +161,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     uint8_t *const mem = smem_raw + (base - raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    LatentWalk<L::kTile> walk;
-    int64_t total;
-    int ctas;
-    // (the sums lie where the first tiles will)
-    if (!latent_deal<L::kTile, kLatThreads>(p, cta, reinterpret_cast<int64_t *>(mem), walk, total, ctas)) return;
-
     const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
     const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * NS, bar_qfull = bar_empty + 8 * kRing,
                    bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_tail = bar_pv + 8,
@@ -181,19 +173,32 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     float *const factor = top + R;                                               // [R]
     float *const quarters = factor + R;                                          // [4][R]
 
-    __syncthreads();  // the sums are read
+    // what needs nothing of the launch ahead comes before the wait for it
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int s = 0; s < NS + kRing + 9; ++s) mbar_init(bar_full + 8 * s, s == NS + kRing + 4 ? kLatSoftmaxWarps : 1);
-        fence_barrier_init();
+        prefetch_tensormap(&tm_c);
+        prefetch_tensormap(&tm_q);
     }
     if (warp == kLatMmaWarp) {
         tmem_alloc(smem_u32((const void *)tmem_slot), L::kCols);
         tmem_relinquish();
     }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    LatentWalk<L::kTile> walk;
+    int64_t total;
+    int ctas;
+    // (the sums lie where the first tiles will)
+    const bool work = latent_deal<L::kTile, kLatThreads>(p, cta, reinterpret_cast<int64_t *>(mem), walk, total, ctas);
+    if (threadIdx.x == 0) fence_barrier_init();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (!work) {
+        if (warp == kLatMmaWarp) tmem_dealloc(*tmem_slot, L::kCols);
+        return;
+    }
     const uint32_t tm_o = *tmem_slot, tm_s = tm_o + 4 * R;
 
     auto give_up = [&]() {
@@ -210,8 +215,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         // ------------------------------ loads: one thread ------------------------------
         issuer = elect_one();
         if (issuer) {
-            prefetch_tensormap(&tm_c);
-            prefetch_tensormap(&tm_q);
             bool ok = true, withheld = false;
             int slot = 0;
             uint32_t parity = 0;  // of the slot's uses
@@ -546,34 +549,35 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 }
 
 // ---- joining the parts of units that were cut -----------------------------------------------------
-// One CTA per row at a time, four elements a thread: out = sum_p e^(lse_p - lse) out_p, as in the other merges of partial
-// softmaxes.  It also writes the rows of sequences without tokens, which no CTA has.
-constexpr int kLatJoinThreads = kLatentDim / 4;
-
-__global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const LatentAttnParams p, int chunk_rows, int64_t all_rows)
+// One CTA per row at a time: out = sum_p e^(lse_p - lse) out_p, as in the other merges of partial softmaxes, four elements a
+// thread, several parts' loads under way at once.  It also writes the rows of sequences without tokens, which no CTA has.
+// Few rows are cut into many parts (one sequence over the whole GPU into up to 152): there four groups of threads take every
+// fourth part.  Rows of larger batches are cut into two or three if at all, and want many small CTAs: one group.  (One
+// sequence of 128K tokens 63 us with one group, 55 with four; 64 sequences of 128 rows 100 and 138.)
+template <int kLatJoinGroups>
+__global__ void __launch_bounds__(kLatJoinGroups * kLatentDim / 4) latent_join_kernel(const LatentAttnParams p, int chunk_rows, int64_t all_rows)
 {
     __shared__ float weight[kLatentMaxCtas];
     __shared__ float total_lse;
-    const int tid = threadIdx.x;
+    __shared__ float4 sums[kLatJoinGroups > 1 ? kLatJoinGroups - 1 : 1][kLatentDim / 4];
+    const int tid = threadIdx.x, group = tid / (kLatentDim / 4), e = tid % (kLatentDim / 4);
     pdl_wait_primary();
     pdl_launch_dependents();
     for (int64_t row = blockIdx.x; row < all_rows; row += gridDim.x) {
         const int b = (int)(row / p.rows), r = (int)(row - (int64_t)b * p.rows);
         const int chunk = r / chunk_rows, cr = r - chunk * chunk_rows;
-        uint2 *out = reinterpret_cast<uint2 *>(p.out + row * kLatentDim) + tid;
+        uint2 *out = reinterpret_cast<uint2 *>(p.out + row * kLatentDim) + e;
+        const int2 info = __ldcg(p.unit_parts + (int64_t)b * p.chunks + chunk);
         if (latent_ctx(p, b) <= 0) {
-            // (out is 4-byte aligned)
-            uint32_t *o = reinterpret_cast<uint32_t *>(out);
-            o[0] = 0u, o[1] = 0u;
+            if (group == 0) *out = make_uint2(0u, 0u);
             if (tid == 0 && p.lse_out) p.lse_out[row] = -INFINITY;
             continue;
         }
-        const int2 info = p.unit_parts[(int64_t)b * p.chunks + chunk];
         const int first = max(0, min(info.x, p.ctas - 1)), parts = max(0, min(info.y, p.ctas - first));
         if (parts <= 1) continue;
         // part k of the unit lies in the last part of the first CTA and in the first parts of those behind it
         auto place = [&](int k) { return (int64_t)(2 * (first + k) + (k == 0)) * chunk_rows + cr; };
-        __syncthreads();  // the last row's weights are read
+        __syncthreads();  // the last row's weights and sums are read
         if (tid < 32) {
             float hi = -INFINITY;
             for (int k = tid; k < parts; k += 32) hi = fmaxf(hi, weight[k] = __ldcg(p.part_lse + place(k)));
@@ -588,24 +592,48 @@ __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const Late
             for (int k = tid; k < parts; k += 32) weight[k] *= inv;
             if (tid == 0) total_lse = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
         }
-        __syncthreads();
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float w = weight[k];
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_out + place(k) * kLatentDim) + tid);
-            acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+        // the first parts' loads go out before the weights are known
+        constexpr int kAtOnce = kLatJoinGroups > 1 ? 6 : 4;
+        for (int k0 = group; k0 < parts; k0 += kAtOnce * kLatJoinGroups) {
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int k = k0 + j * kLatJoinGroups;
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < parts) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.part_out + place(k) * kLatentDim) + e);
+            }
+            if (k0 == group) __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int k = k0 + j * kLatJoinGroups;
+                const float w = k < parts ? weight[k] : 0.f;
+                acc.x += w * v[j].x, acc.y += w * v[j].y, acc.z += w * v[j].z, acc.w += w * v[j].w;
+            }
         }
-        uint32_t *o = reinterpret_cast<uint32_t *>(out);
-        o[0] = pack_bf16x2(acc.x, acc.y), o[1] = pack_bf16x2(acc.z, acc.w);
-        if (tid == 0 && p.lse_out) p.lse_out[row] = total_lse;
+        if (group >= parts) __syncthreads();
+        if (kLatJoinGroups > 1) {
+            if (group > 0) sums[group - 1][e] = acc;
+            __syncthreads();
+        }
+        if (group == 0) {
+#pragma unroll
+            for (int g = 0; g < kLatJoinGroups - 1; ++g) {
+                const float4 v = sums[g][e];
+                acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+            }
+            *out = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            if (tid == 0 && p.lse_out) p.lse_out[row] = total_lse;
+        }
     }
 }
 
 cudaError_t launch_latent_join(const LatentAttnParams &p, int chunk_rows, int sms, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)p.B * p.rows;
-    return launch_kernel(latent_join_kernel, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatJoinThreads), 0, stream, true, p,
+    if (rows <= 4 * (int64_t)sms)
+        return launch_kernel(latent_join_kernel<4>, dim3((unsigned)rows), dim3(kLatentDim), 0, stream, true, p, chunk_rows, rows);
+    return launch_kernel(latent_join_kernel<1>, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatentDim / 4), 0, stream, true, p,
                          chunk_rows, rows);
 }
 

@@ -141,14 +141,6 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)pair_rank(), pair = (int)blockIdx.x >> 1;
 
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    LatentWalk<L::kTile> walk;
-    int64_t total;
-    int pairs;
-    // (the sums lie where the queries will; both CTAs find the same)
-    if (!latent_deal<L::kTile, kPairThreads>(p, pair, reinterpret_cast<int64_t *>(mem), walk, total, pairs)) return;
-
     const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
     const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * S, bar_qfull = bar_empty + 8 * S,
                    bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_tail = bar_pv + 8,
@@ -161,7 +153,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     volatile int *const sent = tile_mask + 8, *const use = sent + S, *const want = use + S;
     float *const quarters = const_cast<float *>(reinterpret_cast<volatile float *>(want + S));  // [4][64]
 
-    __syncthreads();  // the sums are read
+    // what needs nothing of the launch ahead comes before the wait for it
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         *q_asked = 0;
@@ -171,16 +163,31 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             // weights: the softmax warps of both CTAs; stages and zeroed rows: both CTAs
             mbar_init(bar, bar == bar_p ? 2 * kPairSoftmaxWarps : k < S || bar == bar_tail + 8 ? 2 : 1);
         }
-        fence_barrier_init();
+        prefetch_tensormap(&maps.keys);
+        prefetch_tensormap(&maps.rope);
+        prefetch_tensormap(&maps.values);
+        prefetch_tensormap(&maps.queries);
     }
     if (warp == kPairMmaWarp) {
         tmem_alloc2(smem_u32((const void *)tmem_slot), L::kCols);
         tmem_relinquish2();
     }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    LatentWalk<L::kTile> walk;
+    int64_t total;
+    int pairs;
+    // (the sums lie where the queries will; both CTAs find the same)
+    const bool work = latent_deal<L::kTile, kPairThreads>(p, pair, reinterpret_cast<int64_t *>(mem), walk, total, pairs);
+    if (threadIdx.x == 0) fence_barrier_init();
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
+    if (!work) {
+        if (warp == kPairMmaWarp) tmem_dealloc2(*tmem_slot, L::kCols);
+        return;
+    }
     const uint32_t tm_o = *tmem_slot, tm_s = tm_o + 256;
 
     auto give_up = [&]() {
@@ -194,10 +201,6 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     if (warp == kPairLoadWarp) {
         // ------------------------------ loads: one thread ------------------------------
         if (elect_one()) {
-            prefetch_tensormap(&maps.keys);
-            prefetch_tensormap(&maps.rope);
-            prefetch_tensormap(&maps.values);
-            prefetch_tensormap(&maps.queries);
             const uint32_t full_there = pair_at(bar_full, 0), qfull_there = pair_at(bar_qfull, 0);
             int n = 0;           // stages so far
             uint32_t g = 0, q_loads = 0;
