@@ -125,6 +125,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&x)[32])
     for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(r[c / 16][c % 16]);
 }
 
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ int load_word(const volatile int *at, int rank)
 {
     return __float_as_int(load_cluster<float>(smem_u32((const void *)at), rank));
@@ -530,25 +537,42 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                 if (!sg.whole) p.part_lse[part] = lse2;
                 else if (p.lse_out) p.lse_out[row] = lse2 * 0.69314718055994530942f;
             }
+            // Outputs.  A thread has a row's elements, its lanes' rows lie 1 or 2 KB apart: 16 elements of 32 rows at a time go
+            // through the group's part of P (2 KB a warp, 16-byte units swizzled by row), so that a store covers whole sectors of
+            // eight rows (straight from the registers a cut unit's outputs took 10,500 clocks, this way XXXX).
             const int h0 = 256 * side + 128 * h;
+            const uint32_t stage = p_u32 + group * 4096 + side * L::kPChunk + h * 2048;
+            const int64_t part0 = part - lane, row_first = row - lane;
+            const int rows_here = min(32, p.rows - (row0 + 32 * group));
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                tmem_load32(lanes + tm_o + 128 * h + c, o);
-                if (!real) continue;
+            for (int c = 0; c < 128; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(lanes + tm_o + 128 * h + c, o);
+                tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = seen ? o[k] * inv : 0.f;
+                for (int k = 0; k < 16; ++k) o[k] = seen ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    st_shared_v4(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+                __syncwarp();
                 if (sg.whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kLatentDim + h0 + c);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                            pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                    for (int k = 0; k < 2; ++k) {
+                        const int rr = 16 * k + (lane >> 1), u = 2 * (lane & 1), x = (rr >> 1) & 3;
+                        const float4 a = ld_shared_f4(stage + rr * 64 + ((u ^ x) << 4)), b = ld_shared_f4(stage + rr * 64 + (((u + 1) ^ x) << 4));
+                        if (rr < rows_here)
+                            *reinterpret_cast<uint4 *>(p.out + (row_first + rr) * kLatentDim + h0 + c + 4 * u) =
+                                make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+                    }
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_out + part * kLatentDim + h0 + c);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int rr = 8 * k + (lane >> 2), u = lane & 3;
+                        const float4 v = ld_shared_f4(stage + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4));
+                        if (rr < rows_here) *reinterpret_cast<float4 *>(p.part_out + (part0 + rr) * kLatentDim + h0 + c + 4 * u) = v;
+                    }
                 }
+                __syncwarp();
             }
             tc_fence_before();
             half_sync(group);  // the sums are read
