@@ -875,7 +875,9 @@ namespace {
 
 int check_sequences(int32_t max_nb, int32_t num_seqs, int32_t num_blocks)
 {
-    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * 2048 || num_seqs < 0 || num_blocks <= 0) return PKV_ERR_SHAPE;
+    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * 2048 || num_seqs < 0 || num_blocks <= 0 ||
+        num_blocks > INT32_MAX - 16)
+        return PKV_ERR_SHAPE;
     return PKV_OK;
 }
 

@@ -549,92 +549,110 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 }
 
 // ---- joining the parts of units that were cut -----------------------------------------------------
-// One CTA per row at a time: out = sum_p e^(lse_p - lse) out_p, as in the other merges of partial softmaxes, four elements a
-// thread, several parts' loads under way at once.  It also writes the rows of sequences without tokens, which no CTA has.
-// Few rows are cut into many parts (one sequence over the whole GPU into up to 152): there four groups of threads take every
-// fourth part.  Rows of larger batches are cut into two or three if at all, and want many small CTAs: one group.  (One
-// sequence of 128K tokens 63 us with one group, 55 with four; 64 sequences of 128 rows 100 and 138.)
-template <int kLatJoinGroups>
-__global__ void __launch_bounds__(kLatJoinGroups * kLatentDim / 4) latent_join_kernel(const LatentAttnParams p, int chunk_rows, int64_t all_rows)
+// out = sum_p e^(lse_p - lse) out_p, as in the other merges of partial softmaxes.  A CTA takes kRows rows of a unit and leaves
+// at once where the unit was not cut; it also writes the rows of sequences without tokens, which no CTA of the attention has.
+// Warps compute the rows' weights, then 128 threads take a row's elements, four each, and kGroups such groups the rows, or
+// the parts of the one row.  Few rows are cut into many parts (one sequence over the whole GPU into up to 152): one row a
+// CTA, four groups that take every fourth part (one sequence of 128K tokens 63 -> 55 us against one group).  Rows of larger
+// batches are cut into two or three if at all: four rows a CTA (64 sequences of 128 rows 99 -> 94 us against a row a CTA at a time).
+template <int kRows, int kGroups>
+__global__ void __launch_bounds__(kGroups * kLatentDim / 4) latent_join_kernel(const LatentAttnParams p, int chunk_rows)
 {
-    __shared__ float weight[kLatentMaxCtas];
-    __shared__ float total_lse;
-    __shared__ float4 sums[kLatJoinGroups > 1 ? kLatJoinGroups - 1 : 1][kLatentDim / 4];
-    const int tid = threadIdx.x, group = tid / (kLatentDim / 4), e = tid % (kLatentDim / 4);
+    constexpr int kThreads = kGroups * kLatentDim / 4, kWarps = kThreads / 32;
+    constexpr bool kSplitParts = kRows == 1;  // the groups share the parts, else the rows
+    __shared__ float weight[kRows][kLatentMaxCtas];
+    __shared__ float lse_of[kRows];
+    __shared__ float4 sums[kSplitParts ? kGroups : 1][kLatentDim / 4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = tid / (kLatentDim / 4), e = tid % (kLatentDim / 4);
     pdl_wait_primary();
     pdl_launch_dependents();
-    for (int64_t row = blockIdx.x; row < all_rows; row += gridDim.x) {
-        const int b = (int)(row / p.rows), r = (int)(row - (int64_t)b * p.rows);
-        const int chunk = r / chunk_rows, cr = r - chunk * chunk_rows;
-        uint2 *out = reinterpret_cast<uint2 *>(p.out + row * kLatentDim) + e;
-        const int2 info = __ldcg(p.unit_parts + (int64_t)b * p.chunks + chunk);
-        if (latent_ctx(p, b) <= 0) {
-            if (group == 0) *out = make_uint2(0u, 0u);
-            if (tid == 0 && p.lse_out) p.lse_out[row] = -INFINITY;
-            continue;
-        }
-        const int first = max(0, min(info.x, p.ctas - 1)), parts = max(0, min(info.y, p.ctas - first));
-        if (parts <= 1) continue;
-        // part k of the unit lies in the last part of the first CTA and in the first parts of those behind it
-        auto place = [&](int k) { return (int64_t)(2 * (first + k) + (k == 0)) * chunk_rows + cr; };
-        __syncthreads();  // the last row's weights and sums are read
-        if (tid < 32) {
-            float hi = -INFINITY;
-            for (int k = tid; k < parts; k += 32) hi = fmaxf(hi, weight[k] = __ldcg(p.part_lse + place(k)));
+    const int pieces = (chunk_rows + kRows - 1) / kRows;
+    const int64_t unit = blockIdx.x / pieces;
+    const int cr = (int)(blockIdx.x - unit * pieces) * kRows;  // first row within the chunk
+    const int b = (int)(unit / p.chunks), r0 = (int)(unit - (int64_t)b * p.chunks) * chunk_rows + cr, rows = min(kRows, p.rows - r0);
+    const int2 info = __ldcg(p.unit_parts + unit);
+    const bool empty = latent_ctx(p, b) <= 0;
+    const int first = max(0, min(info.x, p.ctas - 1)), parts = empty ? 0 : max(0, min(info.y, p.ctas - first));
+    if (rows <= 0 || parts == 1) return;
+    const int64_t row0 = (int64_t)b * p.rows + r0;
+    // part k of the unit lies in the last part of the first CTA and in the first parts of those behind it
+    auto place = [&](int k, int row) { return (int64_t)(2 * (first + k) + (k == 0)) * chunk_rows + cr + row; };
+    for (int row = warp; row < rows; row += kWarps) {
+        float hi = -INFINITY;
+        for (int k = lane; k < parts; k += 32) hi = fmaxf(hi, weight[row][k] = __ldcg(p.part_lse + place(k, row)));
 #pragma unroll
-            for (int o = 16; o; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-            float sum = 0.f;
-            const float m = hi == -INFINITY ? 0.f : hi;
-            for (int k = tid; k < parts; k += 32) sum += weight[k] = exp2f(weight[k] - m);
+        for (int o = 16; o; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        float sum = 0.f;
+        const float m = hi == -INFINITY ? 0.f : hi;
+        for (int k = lane; k < parts; k += 32) sum += weight[row][k] = exp2f(weight[row][k] - m);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            const float inv = sum > 0.f ? 1.f / sum : sum;  // no key seen: 0; NaN stays
-            for (int k = tid; k < parts; k += 32) weight[k] *= inv;
-            if (tid == 0) total_lse = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
-        }
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float inv = sum > 0.f ? 1.f / sum : sum;  // no key seen: 0; NaN stays
+        for (int k = lane; k < parts; k += 32) weight[row][k] *= inv;
+        if (lane == 0) lse_of[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+    }
+    auto part_at = [&](int k, int row) { return __ldcg(reinterpret_cast<const float4 *>(p.part_out + place(k, row) * kLatentDim) + e); };
+    auto add = [](float4 &a, float w, const float4 &v) { a.x += w * v.x, a.y += w * v.y, a.z += w * v.z, a.w += w * v.w; };
+    auto write = [&](int row, const float4 &a) {
+        reinterpret_cast<uint2 *>(p.out + (row0 + row) * kLatentDim)[e] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        if (e == 0 && p.lse_out) p.lse_out[row0 + row] = lse_of[row];
+    };
+    if constexpr (kSplitParts) {
+        constexpr int kAtOnce = 6;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        // the first parts' loads go out before the weights are known
-        constexpr int kAtOnce = kLatJoinGroups > 1 ? 6 : 4;
-        for (int k0 = group; k0 < parts; k0 += kAtOnce * kLatJoinGroups) {
+        for (int k0 = group; k0 < parts; k0 += kAtOnce * kGroups) {
             float4 v[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const int k = k0 + j * kLatJoinGroups;
-                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k < parts) v[j] = __ldcg(reinterpret_cast<const float4 *>(p.part_out + place(k) * kLatentDim) + e);
-            }
-            if (k0 == group) __syncthreads();
+            for (int j = 0; j < kAtOnce; ++j)
+                v[j] = k0 + j * kGroups < parts ? part_at(k0 + j * kGroups, 0) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 == group) __syncthreads();  // the first parts' loads go out before the weights are known
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-                const int k = k0 + j * kLatJoinGroups;
-                const float w = k < parts ? weight[k] : 0.f;
-                acc.x += w * v[j].x, acc.y += w * v[j].y, acc.z += w * v[j].z, acc.w += w * v[j].w;
-            }
+            for (int j = 0; j < kAtOnce; ++j)
+                if (k0 + j * kGroups < parts) add(acc, weight[0][k0 + j * kGroups], v[j]);
         }
         if (group >= parts) __syncthreads();
-        if (kLatJoinGroups > 1) {
-            if (group > 0) sums[group - 1][e] = acc;
-            __syncthreads();
-        }
+        sums[group][e] = acc;
+        __syncthreads();
         if (group == 0) {
 #pragma unroll
-            for (int g = 0; g < kLatJoinGroups - 1; ++g) {
-                const float4 v = sums[g][e];
-                acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-            }
-            *out = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            if (tid == 0 && p.lse_out) p.lse_out[row] = total_lse;
+            for (int g = 1; g < kGroups; ++g) add(acc, 1.f, sums[g][e]);
+            write(0, acc);
         }
+    } else {
+        constexpr int kMine = kRows / kGroups;
+        float4 acc[kMine], v[2][kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto load = [&](int k, float4 (&to)[kMine]) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                to[i] = k < parts && group + i * kGroups < rows ? part_at(k, group + i * kGroups) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        load(0, v[0]);
+        load(1, v[1]);
+        __syncthreads();
+        for (int k = 0; k < parts; k += 2) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (k + j < parts && group + i * kGroups < rows) add(acc[i], weight[group + i * kGroups][k + j], v[j][i]);
+                load(k + j + 2, v[j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (group + i * kGroups < rows) write(group + i * kGroups, acc[i]);
     }
 }
 
 cudaError_t launch_latent_join(const LatentAttnParams &p, int chunk_rows, int sms, cudaStream_t stream)
 {
-    const int64_t rows = (int64_t)p.B * p.rows;
-    if (rows <= 4 * (int64_t)sms)
-        return launch_kernel(latent_join_kernel<4>, dim3((unsigned)rows), dim3(kLatentDim), 0, stream, true, p, chunk_rows, rows);
-    return launch_kernel(latent_join_kernel<1>, dim3((unsigned)min(rows, (int64_t)sms * 16)), dim3(kLatentDim / 4), 0, stream, true, p,
-                         chunk_rows, rows);
+    const int64_t units = (int64_t)p.B * p.chunks;
+    if (units * chunk_rows <= 4 * (int64_t)sms)
+        return launch_kernel(latent_join_kernel<1, 4>, dim3((unsigned)(units * chunk_rows)), dim3(kLatentDim), 0, stream, true, p, chunk_rows);
+    return launch_kernel(latent_join_kernel<4, 2>, dim3((unsigned)(units * (chunk_rows / 4))), dim3(kLatentDim / 2), 0, stream, true, p,
+                         chunk_rows);
 }
 
 template <int R>

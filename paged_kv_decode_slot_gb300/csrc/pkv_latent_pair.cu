@@ -539,7 +539,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             }
             // Outputs.  A thread has a row's elements, its lanes' rows lie 1 or 2 KB apart: 16 elements of 32 rows at a time go
             // through the group's part of P (2 KB a warp, 16-byte units swizzled by row), so that a store covers whole sectors of
-            // eight rows (straight from the registers a cut unit's outputs took 10,500 clocks, this way XXXX).
+            // eight rows (straight from the registers a unit's outputs took 10,500 clocks; a ragged batch of 64 with 128 heads 102 -> 99 us).
             const int h0 = 256 * side + 128 * h;
             const uint32_t stage = p_u32 + group * 4096 + side * L::kPChunk + h * 2048;
             const int64_t part0 = part - lane, row_first = row - lane;

@@ -8,6 +8,8 @@
 // What bounds these: a scan of the counts (4 bytes a block: 0.4 MB for 100,000 blocks) and the table entries that change,
 // both from L2; the rest is the latency of a launch and of a few barriers.  Scans run as one cluster of eight CTAs, whose
 // totals meet in shared memory, rather than as a grid that would have to be launched twice or count itself.
+#include <limits.h>
+
 #include "pkv_cluster.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -18,6 +20,7 @@ namespace pkv {
 // ---- forking --------------------------------------------------------------------------------------
 constexpr int kForkThreads = 256;
 constexpr int kForkEntries = 2048;  // table entries of a CTA
+constexpr int kForkEach = kForkEntries / kForkThreads;
 
 __device__ __forceinline__ int fork_blocks(const ForkParams &p, int row, bool report, int &ctx)
 {
@@ -50,8 +53,17 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p)
         if (from >= 0) nb = fork_blocks(p, from, false, ctx);
         const int32_t *src = p.block_tables + (int64_t)from * p.max_nb;
         int32_t *dst = p.tables_out + (int64_t)row * p.max_nb;
-#pragma unroll 4
-        for (int e = e0 + tid; e < e1; e += kForkThreads) dst[e] = e < nb ? __ldg(src + e) : -1;
+        int id[kForkEach];
+#pragma unroll
+        for (int k = 0; k < kForkEach; ++k) {
+            const int e = e0 + tid + k * kForkThreads;
+            id[k] = e < min(e1, nb) ? __ldg(src + e) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kForkEach; ++k) {
+            const int e = e0 + tid + k * kForkThreads;
+            if (e < e1) dst[e] = id[k];
+        }
         if (report) p.lens_out[row] = ctx;
         return;
     }
@@ -70,10 +82,19 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p)
     for (int w = 0; w < kForkThreads / 32; ++w) change += sums[w];
     if (change == 0) return;
     const int32_t *src = p.block_tables + (int64_t)row * p.max_nb;
-    for (int e = e0 + tid; e < nb; e += kForkThreads) {
-        const int id = __ldg(src + e);
-        if (id < 0 || id >= p.num_blocks) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-        else if (atomicAdd(p.ref_counts + id, change) + change < 0) set_flag(p.err_flag, PKV_FLAG_REF_RANGE);
+    // all of a thread's entries, then all of its additions, under way at once
+    int id[kForkEach], left[kForkEach];
+#pragma unroll
+    for (int k = 0; k < kForkEach; ++k) {
+        const int e = e0 + tid + k * kForkThreads;
+        id[k] = e < nb ? __ldg(src + e) : INT_MIN;
+    }
+#pragma unroll
+    for (int k = 0; k < kForkEach; ++k) left[k] = id[k] >= 0 && id[k] < p.num_blocks ? atomicAdd(p.ref_counts + id[k], change) + change : 0;
+#pragma unroll
+    for (int k = 0; k < kForkEach; ++k) {
+        if (id[k] != INT_MIN && (id[k] < 0 || id[k] >= p.num_blocks)) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+        if (left[k] < 0) set_flag(p.err_flag, PKV_FLAG_REF_RANGE);
     }
 }
 
@@ -92,15 +113,21 @@ struct PairList {
 };
 
 // ---- a cluster that scans the counts ----------------------------------------------------------------
-constexpr int kScanCtas = 8, kScanThreads = 1024, kScanWarps = kScanThreads / 32;
+constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
+constexpr int kScanCtas = 8;         // CTAs of the cluster ..
+// .. or one CTA, whose barriers cost less, where it reads the counts as fast as it needs them: extensions of up to this many
+// rows and blocks (64 rows over 21,797 blocks 9.9 -> 7.4 us; 250 over 68,943 15.8 -> 24.6), plans of moves, which read them
+// twice, in small pools (10,898 blocks 10.1 -> 12.2)
+constexpr int kOneCtaBlocks = 32768, kOneCtaRows = kScanThreads, kOneCtaPlan = 4096;
 
-// Warp w of the cluster's 256 takes the counts [w * per_warp, (w + 1) * per_warp), 128 a step.
+// Warp w of the kCtas * 32 takes the counts [w * per_warp, (w + 1) * per_warp), 128 a step.
 struct ScanRange {
     int begin, end;
 };
+template <int kCtas>
 __device__ __forceinline__ ScanRange scan_range(int num_blocks, int rank)
 {
-    const int warps = kScanCtas * kScanWarps, w = rank * kScanWarps + (threadIdx.x >> 5);
+    const int warps = kCtas * kScanWarps, w = rank * kScanWarps + (threadIdx.x >> 5);
     const int steps = (num_blocks + 127) / 128, per = (steps + warps - 1) / warps;
     const int64_t b = (int64_t)w * per * 128, e = b + (int64_t)per * 128;
     return ScanRange{(int)min((int64_t)num_blocks, b), (int)min((int64_t)num_blocks, e)};
@@ -158,21 +185,40 @@ __device__ __forceinline__ int cta_warps_before(int v, int *sums, int &all)
     return __shfl_sync(0xFFFFFFFFu, before, warp);
 }
 
-// The value that every CTA of the cluster published in `word`, summed before this one and over all.
+// A barrier of all CTAs: what they wrote before it, to global or their shared memory, is seen behind it.
+template <int kCtas>
+__device__ __forceinline__ void scan_sync()
+{
+    if constexpr (kCtas > 1) cluster_sync();
+    else __syncthreads();
+}
+
+// The value that every CTA published in `word` before a barrier, summed before this one and over all.  Whole warps; the CTAs'
+// words are read by a lane each (one after the other they take 0.1 us a word).
+template <int kCtas>
 __device__ __forceinline__ void cluster_before(const long long *word, int rank, long long &before, long long &all)
 {
-    before = all = 0;
-    for (int r = 0; r < kScanCtas; ++r) {
-        const long long v = load_cluster<long long>(smem_u32(word), r);
-        if (r < rank) before += v;
-        all += v;
+    if constexpr (kCtas == 1) {
+        before = 0, all = *word;
+    } else {
+        const int lane = threadIdx.x & 31;
+        all = lane < kCtas ? load_cluster<long long>(smem_u32(word), lane) : 0;
+        before = lane < rank ? all : 0;
+#pragma unroll
+        for (int o = kCtas / 2; o; o >>= 1) {
+            all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+            before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        }
+        all = __shfl_sync(0xFFFFFFFFu, all, 0);
+        before = __shfl_sync(0xFFFFFFFFu, before, 0);
     }
 }
 
+template <int kCtas>
 __device__ __forceinline__ int scan_rank()
 {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    uint32_t r = 0;
+    if constexpr (kCtas > 1) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return (int)r;
 }
 
@@ -183,9 +229,11 @@ __device__ __forceinline__ int scan_rank()
 // zero had no other holders, and its last row, found by an atomic minimum over -(row + 1) in the count itself, keeps the
 // block.  Then a scan over what the rows need says who gets which of the free blocks.
 //
-// Between the phases a row's state lies in its entry of `copies`: (block to copy, or one of the marks below; first rank of
-// its fresh blocks).
+// A thread keeps its row's state in registers (`per` is 1 up to 8,192 rows) or in the row's entry of `copies`, which also
+// tells the warps of rows with many fresh blocks: (block to copy, or one of the marks below; first rank of its fresh blocks).
 constexpr int kNoCopy = -1, kKeeps = -2, kIdle = -3;
+constexpr int kWaits = INT_MIN;  // + 1 + the block to copy: a row whose fresh blocks a warp hands out
+constexpr int kFewBlocks = 4;  // fresh blocks that a row's own thread writes; more are a warp's work
 
 struct GrowRow {
     int ctx, now, then;   // tokens, blocks before and after
@@ -200,26 +248,43 @@ __device__ __forceinline__ GrowRow grow_row(const ExtendParams &p, int row)
     return g;
 }
 
+// Gives row `row` its fresh blocks k0, k0 + step, .. of n, which replace or follow those up to entry `at` of its table.
+__device__ __forceinline__ void give_blocks(const ExtendParams &p, int row, int at, int n, int first, int k0, int step, int cow_of)
+{
+    int32_t *tbl = p.block_tables + (int64_t)row * p.max_nb + at;
+    for (int k = k0; k < n; k += step) {
+        const int id = __ldcg(p.free_ids + first + k);
+        if (id < 0 || id >= p.num_blocks) {  // only where counts and tables disagree
+            set_flag(p.err_flag, PKV_FLAG_REF_RANGE);
+            continue;
+        }
+        tbl[k] = id;
+        p.ref_counts[id] = 1;
+        if (k == 0 && cow_of >= 0) PairList{p.copies}.put(row, make_int2(cow_of, id));
+    }
+}
+
+template <int kCtas>
 __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendParams p)
 {
     __shared__ int sums[kScanWarps];
-    __shared__ long long free_here, need_here;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = scan_rank();
-    pdl_wait_primary();
-    pdl_launch_dependents();
+    __shared__ long long free_here, need_here, many_here;
+    __shared__ long long warp_need[kScanWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = scan_rank<kCtas>();
     const PairList state{p.copies};
     // this thread's rows
-    const int threads = kScanCtas * kScanThreads, per = (p.rows + threads - 1) / threads;
+    const int threads = kCtas * kScanThreads, per = (p.rows + threads - 1) / threads;
     const int64_t r0 = (int64_t)(rank * kScanThreads + tid) * per;
     const int rb = (int)min((int64_t)p.rows, r0), re = (int)min((int64_t)p.rows, r0 + per);
-
-    // free blocks
-    const ScanRange range = scan_range(p.num_blocks, rank);
-    const int mine = count_free(p.ref_counts, range);
-    int all;
-    const int free_in_cta = cta_warps_before(mine, sums, all);
-    if (tid == 0) free_here = all;
-    cluster_sync();  // every count is read before any changes
+    const bool one = per == 1;
+    int2 mine_state = make_int2(kIdle, 0);
+    GrowRow mine_row = {};
+    auto get = [&](int row) { return one ? mine_state : state.get(row); };
+    auto put = [&](int row, int2 s) { if (one) mine_state = s; else state.put(row, s); };
+    auto grow = [&](int row) { return one ? mine_row : grow_row(p, row); };
+    if (tid == 0) many_here = 0;
+    pdl_wait_primary();
+    pdl_launch_dependents();
 
     for (int row = rb; row < re; ++row) {
         const int t = p.num_new[row], ctx = p.context_lens[row];
@@ -228,6 +293,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
             set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
         } else if (t > 0) {
             s.x = kNoCopy;
+            mine_row = GrowRow{ctx, (ctx + kBlockSize - 1) / kBlockSize, (int)(((int64_t)ctx + t + kBlockSize - 1) / kBlockSize)};
             if (ctx % kBlockSize != 0) {
                 const int id = p.block_tables[(int64_t)row * p.max_nb + ctx / kBlockSize];
                 if (id < 0 || id >= p.num_blocks) {
@@ -239,27 +305,33 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
                 }
             }
         }
-        state.put(row, s);
+        put(row, s);
     }
-    cluster_sync();
+    scan_sync<kCtas>();
     for (int row = rb; row < re; ++row) {
-        const int id = state.first(row);
+        const int id = get(row).x;
         if (id >= 0 && __ldcg(p.ref_counts + id) <= 0) atomicMin(p.ref_counts + id, -(row + 1));
     }
-    cluster_sync();
+    scan_sync<kCtas>();
+    // every held block's count is above zero or, where all its holders grow, below: zero says free
+    const ScanRange range = scan_range<kCtas>(p.num_blocks, rank);
+    const int mine = count_free(p.ref_counts, range);
     long long need = 0;
     for (int row = rb; row < re; ++row) {
-        const int id = state.first(row);
+        const int id = get(row).x;
         if (id == kIdle) continue;
-        const GrowRow g = grow_row(p, row);
+        const GrowRow g = grow(row);
         need += g.then - g.now;
         if (id >= 0) {
-            if (__ldcg(p.ref_counts + id) == -(row + 1)) p.copies[2 * (int64_t)row] = kKeeps;
+            if (__ldcg(p.ref_counts + id) == -(row + 1)) put(row, make_int2(kKeeps, id));
             else ++need;
         }
+        if (g.then - g.now >= kFewBlocks) many_here = 1;
     }
+    int all;
+    const int free_in_cta = cta_warps_before(mine, sums, all);
+    if (tid == 0) free_here = all;
     // rows' needs: exclusive over the threads, 64-bit
-    __shared__ long long warp_need[kScanWarps];
     long long upto = need;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -278,30 +350,31 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
         warp_need[lane] = s - v;
         if (lane == 31) need_here = s;
     }
-    cluster_sync();  // (also this CTA's barrier) every row has decided; the totals are there
+    scan_sync<kCtas>();  // (also this CTA's barrier) every row has decided; the totals are there
     long long free_before, free_all, need_before, need_all;
-    cluster_before(&free_here, rank, free_before, free_all);
-    cluster_before(&need_here, rank, need_before, need_all);
+    cluster_before<kCtas>(&free_here, rank, free_before, free_all);
+    cluster_before<kCtas>(&need_here, rank, need_before, need_all);
+    long long many_before, many;
+    cluster_before<kCtas>(&many_here, rank, many_before, many);
     long long at = need_before + warp_need[warp] + upto - need;
     for (int row = rb; row < re; ++row) {
-        const int id = state.first(row);
-        if (id == kIdle) continue;
-        const GrowRow g = grow_row(p, row);
-        if (id == kKeeps) p.ref_counts[p.block_tables[(int64_t)row * p.max_nb + g.ctx / kBlockSize]] = 1;
-        const long long n = g.then - g.now + (id >= 0);
+        const int2 s = get(row);
+        if (s.x == kIdle) continue;
+        const GrowRow g = grow(row);
+        if (s.x == kKeeps) p.ref_counts[s.y] = 1;
+        const long long n = g.then - g.now + (s.x >= 0);
         if (at + n <= free_all) {
-            state.put(row, make_int2(id == kKeeps ? kNoCopy : id, (int)at));
+            put(row, make_int2(s.x == kKeeps ? kNoCopy : s.x, (int)at));
         } else {
             set_flag(p.err_flag, PKV_FLAG_NO_BLOCKS);
             // its block, if it was to leave it, has its holder back (behind the barrier: the keeper sets it to 1 here)
-            state.put(row, make_int2(id >= 0 ? id : kIdle, -1));
+            put(row, make_int2(s.x >= 0 ? s.x : kIdle, -1));
         }
         at += n;
     }
     // the free blocks that are needed, in order
     const long long wanted = need_all < free_all ? need_all : free_all;
     long long base = free_before + free_in_cta;
-    // (a row's own count changes only from above zero or back to it behind the barrier; counts that were zero are zero)
     for (int b = range.begin; b < range.end && base < wanted; b += 128) {
         unsigned free[4];
         scan_free(p.ref_counts, b, range.end, free);
@@ -312,64 +385,68 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
             base += __popc(free[j]);
         }
     }
-    cluster_sync();
-    // hand them out, a warp a row
-    for (int row = rank * kScanWarps + warp; row < p.rows; row += kScanCtas * kScanWarps) {
+    scan_sync<kCtas>();
+    // hand them out: few a row by its own thread ..
+    for (int row = rb; row < re; ++row) {
+        const int2 s = get(row);
+        if (s.x == kIdle || s.y < 0) {
+            if (s.x >= 0) atomicAdd(p.ref_counts + s.x, 1);
+            state.put(row, make_int2(-1, -1));
+            continue;
+        }
+        const GrowRow g = grow(row);
+        const int cow = s.x >= 0, n = g.then - g.now + cow;
+        if (n > kFewBlocks) {
+            state.put(row, make_int2(kWaits + 1 + s.x, s.y));
+        } else {
+            if (!cow) state.put(row, make_int2(-1, -1));
+            give_blocks(p, row, g.now - cow, n, s.y, 0, 1, s.x);
+            p.context_lens[row] = g.ctx + p.num_new[row];
+        }
+    }
+    if (many == 0) return;
+    scan_sync<kCtas>();
+    // .. many by a warp
+    for (int row = rank * kScanWarps + warp; row < p.rows; row += kCtas * kScanWarps) {
         const int2 s = state.get(row);
+        if (s.x >= kIdle) continue;
+        const int cow_of = s.x - kWaits - 1, cow = cow_of >= 0;
         const GrowRow g = grow_row(p, row);
         const int t = p.num_new[row];
         __syncwarp();
-        if (s.x == kIdle || s.y < 0) {
-            if (lane == 0) {
-                if (s.x >= 0) atomicAdd(p.ref_counts + s.x, 1);
-                state.put(row, make_int2(-1, -1));
-            }
-            continue;
-        }
-        const int cow = s.x >= 0;
-        int32_t *tbl = p.block_tables + (int64_t)row * p.max_nb + g.now - cow;
-        const int n = g.then - g.now + cow;
-        for (int k = lane; k < n; k += 32) {
-            const int id = __ldcg(p.free_ids + s.y + k);
-            if (id < 0 || id >= p.num_blocks) {  // only where a held block was counted as free
-                set_flag(p.err_flag, PKV_FLAG_REF_RANGE);
-                continue;
-            }
-            tbl[k] = id;
-            p.ref_counts[id] = 1;
-            if (k == 0 && cow) state.put(row, make_int2(s.x, id));
-        }
-        if (lane == 0) {
-            if (!cow) state.put(row, make_int2(-1, -1));
-            p.context_lens[row] = g.ctx + t;
-        }
+        if (lane == 0 && !cow) state.put(row, make_int2(-1, -1));
+        give_blocks(p, row, g.now - cow, g.then - g.now + cow, s.y, lane, 32, cow_of);
+        if (lane == 0) p.context_lens[row] = g.ctx + t;
     }
 }
 
 cudaError_t launch_extend_sequences(const ExtendParams &p, cudaStream_t stream)
 {
-    return launch_clusters(extend_kernel, dim3(kScanCtas), dim3(kScanThreads), dim3(kScanCtas, 1, 1), 0, stream, p);
+    if (p.num_blocks <= kOneCtaBlocks && p.rows <= kOneCtaRows)
+        return launch_kernel(extend_kernel<1>, dim3(1), dim3(kScanThreads), 0, stream, true, p);
+    return launch_clusters(extend_kernel<kScanCtas>, dim3(kScanCtas), dim3(kScanThreads), dim3(kScanCtas, 1, 1), 0, stream, p);
 }
 
 // ---- compacting -------------------------------------------------------------------------------------
 // With U blocks in use, those with ids from U on move to the free ids below U: the highest to the lowest.  A used block's
 // place in the moves is the number of used blocks above it, a free one's the number of free blocks below it, so the scan
 // writes both sides of the list directly.
+template <int kCtas>
 __global__ void __launch_bounds__(kScanThreads, 1) plan_moves_kernel(const CompactParams p)
 {
     __shared__ int sums[kScanWarps];
     __shared__ long long used_here, above_here;
-    const int tid = threadIdx.x, lane = tid & 31, rank = scan_rank();
+    const int tid = threadIdx.x, lane = tid & 31, rank = scan_rank<kCtas>();
     pdl_wait_primary();
     pdl_launch_dependents();
-    const ScanRange range = scan_range(p.num_blocks, rank);
+    const ScanRange range = scan_range<kCtas>(p.num_blocks, rank);
     const int mine = range.end - range.begin - count_free(p.ref_counts, range);
     int all;
     const int in_cta = cta_warps_before(mine, sums, all);
     if (tid == 0) used_here = all, above_here = 0;
-    cluster_sync();
+    scan_sync<kCtas>();
     long long before, used;
-    cluster_before(&used_here, rank, before, used);
+    cluster_before<kCtas>(&used_here, rank, before, used);
     long long base = before + in_cta;  // used blocks below this warp's range
     int above = 0;                     // used blocks from U on
     for (int b = range.begin; b < range.end; b += 128) {
@@ -395,12 +472,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) plan_moves_kernel(const Compa
     }
     above = __reduce_add_sync(0xFFFFFFFFu, above);
     if (lane == 0 && above) atomicAdd(reinterpret_cast<unsigned long long *>(&above_here), (unsigned long long)above);
-    cluster_sync();
+    scan_sync<kCtas>();
     long long unused, total;
-    cluster_before(&above_here, rank, unused, total);
+    cluster_before<kCtas>(&above_here, rank, unused, total);
     const int n = (int)min(total, (long long)p.max_moves);
     if (rank == 0 && tid == 0) *p.num_moves = n;
-    for (int k = rank * kScanThreads + tid; k < p.max_moves; k += kScanCtas * kScanThreads) {
+    for (int k = rank * kScanThreads + tid; k < p.max_moves; k += kCtas * kScanThreads) {
         if (k >= n) {
             PairList{p.moves}.put(k, make_int2(-1, -1));
             continue;
@@ -409,7 +486,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) plan_moves_kernel(const Compa
         p.ref_counts[dst] = p.ref_counts[src];
         p.ref_counts[src] = 0;
     }
-    cluster_sync();  // no CTA leaves while its totals are read
+    scan_sync<kCtas>();  // no CTA leaves while its totals are read
 }
 
 // Entries [y * kForkEntries, ..) of row x: a moved block's new id.
@@ -442,7 +519,9 @@ __global__ void __launch_bounds__(kForkThreads) move_entries_kernel(const Compac
 
 cudaError_t launch_compact_blocks(const CompactParams &p, cudaStream_t stream)
 {
-    cudaError_t e = launch_clusters(plan_moves_kernel, dim3(kScanCtas), dim3(kScanThreads), dim3(kScanCtas, 1, 1), 0, stream, p);
+    cudaError_t e = p.num_blocks <= kOneCtaPlan
+                        ? launch_kernel(plan_moves_kernel<1>, dim3(1), dim3(kScanThreads), 0, stream, true, p)
+                        : launch_clusters(plan_moves_kernel<kScanCtas>, dim3(kScanCtas), dim3(kScanThreads), dim3(kScanCtas, 1, 1), 0, stream, p);
     if (e != cudaSuccess || p.rows == 0) return e;
     return launch_kernel(move_entries_kernel, dim3((unsigned)p.rows, (unsigned)((p.max_nb + kForkEntries - 1) / kForkEntries)),
                          dim3(kForkThreads), 0, stream, true, p);
