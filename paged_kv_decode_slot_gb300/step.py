@@ -624,7 +624,8 @@ class SequenceBlocks:
         for p in pools:
             groups.setdefault((p.shape, p.dtype), []).append(p)
         for same in groups.values():
-            B.check(B.pkv_copy_blocks_pools(same, pairs, self.err_flag, stream))
+            for k in range(0, len(same), 256):  # pools a call
+                B.check(B.pkv_copy_blocks_pools(same[k:k + 256], pairs, self.err_flag, stream))
 
     def extend(self, num_new, pools=(), stream=None) -> None:
         """Row b grows by num_new[b] (int32 [num_seqs]) tokens; shared last blocks are copied on write in ``pools``."""
