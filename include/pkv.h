@@ -692,7 +692,10 @@ size_t pkv_latent_workspace_bytes(int32_t num_seqs, int32_t num_new, int32_t num
    log, nullable.  Any N.  The tiles of all sequences are dealt out evenly over the GPU, whatever the lengths: which parts a
    sequence is cut into, and so the last bits of its result, depend on the other sequences of the batch.  Softmax weights
    are rounded to bf16 before they multiply the values (they sum to one as rounded).  Two launches (the second joins what
-   was cut).  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left out. */
+   was cut).  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left out.  Whatever lies
+   behind a sequence's end in its last block is not read as a value, infinities and NaN included.  The num_new tokens themselves
+   multiply all rows of their sequence, those that do not see them with weight 0: an infinity or NaN in one of their latent
+   vectors makes its elements NaN in the rows before it too. */
 int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, const int32_t *block_tables,
                            int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, int32_t num_new,
                            int32_t num_q_heads, float scale, pkv_bf16 *out, float *lse_out, pkv_cache_desc cache,
@@ -702,7 +705,7 @@ int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, cons
  * ---- the life of a cache's blocks -----------------------------------------------------------------
  * ("Optimización de la inferencia", "Página Atención": pages anywhere in memory, shared ones copied on write.)  The state
  * of the sequences: block_tables int32 [num_seqs][max_blocks_per_seq], context_lens int32 [num_seqs], and ref_counts
- * int32 [num_blocks], for every physical block the number of table rows that hold it (entries j < ceil(ctx / 16) of a row
+ * int32 [num_blocks] (num_seqs and num_blocks up to 2^31 - 65,537), for every physical block the number of table rows that hold it (entries j < ceil(ctx / 16) of a row
  * count, those behind are not looked at).  A block with count 0 is free.  The calls below keep the counts; all results are
  * exact and follow from the arguments alone.  Where counts and tables disagree the result is void: disagreements that
  * a call meets set PKV_FLAG_REF_RANGE, nothing outside the given arrays is touched.  Blocks are blocks of every layer's
@@ -730,8 +733,8 @@ size_t pkv_blocks_workspace_bytes(int32_t num_blocks);
    copies[b] (int32 [num_seqs][2]) = (old, new), to be copied before the new tokens are written; otherwise copies[b] =
    (-1, -1).  (Rows that share it and grow in one call are taken in order: the last holder keeps the block.)  Once a row needs
    more blocks than are left, it and all growing rows behind it stay as they are and PKV_FLAG_NO_BLOCKS is set.  A negative
-   num_new, a context outside [0, 16 max_blocks_per_seq], or a row that would outgrow its table, sets PKV_FLAG_CTX_RANGE and that
-   row stays as it is. */
+   num_new, a context outside [0, 16 max_blocks_per_seq], or a row that would outgrow its table, sets PKV_FLAG_CTX_RANGE, a
+   partly filled block outside the pool PKV_FLAG_BLOCK_RANGE, and that row stays as it is. */
 int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *num_new,
                          int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks, int32_t *copies, void *workspace,
                          size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);

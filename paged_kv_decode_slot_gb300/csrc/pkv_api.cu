@@ -822,7 +822,8 @@ PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_
     int st = check_latent_desc(cache);
     if (st == PKV_OK) st = check_latent_sizes(num_seqs, num_new, num_q_heads);
     if (st != PKV_OK) return st;
-    if (max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * 16 > INT32_MAX) return PKV_ERR_SHAPE;
+    // positions are 32-bit, a tile past the end too
+    if (max_blocks_per_seq <= 0 || (int64_t)max_blocks_per_seq * 16 > INT32_MAX - 1024) return PKV_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(out, 16) || !aligned(lse_out, 4)) return PKV_ERR_ALIGN;
     const pkv::LatentPlan plan = pkv::latent_plan((int64_t)num_new * num_q_heads);
     const LatentWorkspace w = latent_workspace(num_seqs, plan);
@@ -873,10 +874,13 @@ PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_
 // ---- the life of a cache's blocks -----------------------------------------------------------------
 namespace {
 
+// Rows, blocks and pairs are counted in 32 bits, in steps of up to a cluster's threads past the end.
+constexpr int32_t kMaxCount = INT32_MAX - 65536;
+
 int check_sequences(int32_t max_nb, int32_t num_seqs, int32_t num_blocks)
 {
-    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * 2048 || num_seqs < 0 || num_blocks <= 0 ||
-        num_blocks > INT32_MAX - 16)
+    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * 2048 || num_seqs < 0 || num_seqs > kMaxCount ||
+        num_blocks <= 0 || num_blocks > kMaxCount)
         return PKV_ERR_SHAPE;
     return PKV_OK;
 }
@@ -899,7 +903,7 @@ PKV_EXPORT int pkv_fork_sequences(const int32_t *block_tables, int32_t max_block
         return PKV_ERR_NULL;
     int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
     if (st != PKV_OK) return st;
-    if (num_seqs_out < 0 || (int64_t)num_seqs + num_seqs_out > INT32_MAX) return PKV_ERR_SHAPE;
+    if (num_seqs_out < 0 || (int64_t)num_seqs + num_seqs_out > kMaxCount) return PKV_ERR_SHAPE;
     if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(parents, 4) || !aligned(ref_counts, 4) ||
         !aligned(block_tables_out, 4) || !aligned(context_lens_out, 4))
         return PKV_ERR_ALIGN;
@@ -944,7 +948,7 @@ PKV_EXPORT int pkv_compact_blocks(int32_t *block_tables, int32_t max_blocks_per_
     if ((num_seqs != 0 && (!block_tables || !context_lens)) || !ref_counts || !moves || !num_moves) return PKV_ERR_NULL;
     int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
     if (st != PKV_OK) return st;
-    if (max_moves <= 0) return PKV_ERR_SHAPE;
+    if (max_moves <= 0 || max_moves > kMaxCount) return PKV_ERR_SHAPE;
     if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(ref_counts, 4) || !aligned(moves, 4) ||
         !aligned(num_moves, 4))
         return PKV_ERR_ALIGN;

@@ -24,7 +24,7 @@ __device__ __forceinline__ constexpr int latent_unit_cost()
 
 __device__ __forceinline__ int latent_ctx(const LatentAttnParams &p, int b)
 {
-    const int ctx = __ldg(p.context_lens + b);
+    const int ctx = p.context_lens[b];
     return ctx < 0 || ctx > p.max_nb * kBlockSize ? 0 : ctx;
 }
 template <int kTile>
@@ -74,7 +74,7 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, 
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t cost = 0;
     for (int b = b0; b < b1; ++b) {
-        const int ctx = __ldg(p.context_lens + b);
+        const int ctx = p.context_lens[b];
         if (cta == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
         cost += latent_cost<kTile>(latent_ctx(p, b));
     }

@@ -232,7 +232,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 int next[NB];
                 auto ids_of = [&](int t) {
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) next[k] = t < sg.t1 && t * NB + k < nb ? __ldg(tbl + t * NB + k) : -1;
+                    for (int k = 0; k < NB; ++k) next[k] = t < sg.t1 && t * NB + k < nb ? tbl[t * NB + k] : -1;
                 };
                 ids_of(sg.t0);
                 for (int t = sg.t0; t < sg.t1 && ok; ++t) {

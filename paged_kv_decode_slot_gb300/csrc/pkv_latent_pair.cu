@@ -258,7 +258,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
 #pragma unroll
                     for (int k = 0; k < L::kBlocks; ++k) {
                         const int j = t * L::kBlocks + k;
-                        next[k] = t < sg.t1 && j < nb ? __ldg(tbl + j) : -1;
+                        next[k] = t < sg.t1 && j < nb ? tbl[j] : -1;
                     }
                 };
                 ids_of(sg.t0);

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p)
 #pragma unroll
         for (int k = 0; k < kForkEach; ++k) {
             const int e = e0 + tid + k * kForkThreads;
-            id[k] = e < min(e1, nb) ? __ldg(src + e) : -1;
+            id[k] = e < min(e1, nb) ? src[e] : -1;
         }
 #pragma unroll
         for (int k = 0; k < kForkEach; ++k) {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p)
     const int nb = min(e1, fork_blocks(p, row, tid == 0 && blockIdx.y == 0, ctx));
     if (nb <= e0) return;
     int mine = 0;
-    for (int r = tid; r < p.rows_out; r += kForkThreads) mine += __ldg(p.parents + r) == row;
+    for (int r = tid; r < p.rows_out; r += kForkThreads) mine += p.parents[r] == row;
     // heirs, a block-wide sum
     __shared__ int sums[kForkThreads / 32];
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p)
 #pragma unroll
     for (int k = 0; k < kForkEach; ++k) {
         const int e = e0 + tid + k * kForkThreads;
-        id[k] = e < nb ? __ldg(src + e) : INT_MIN;
+        id[k] = e < nb ? src[e] : INT_MIN;
     }
 #pragma unroll
     for (int k = 0; k < kForkEach; ++k) left[k] = id[k] >= 0 && id[k] < p.num_blocks ? atomicAdd(p.ref_counts + id[k], change) + change : 0;
@@ -107,7 +107,6 @@ cudaError_t launch_fork_sequences(const ForkParams &p, cudaStream_t stream)
 // A list of pairs of integers (4-byte aligned, as the caller's tensors are).
 struct PairList {
     int32_t *at;
-    __device__ __forceinline__ int first(int64_t i) const { return __ldcg(at + 2 * i); }
     __device__ __forceinline__ int2 get(int64_t i) const { return make_int2(__ldcg(at + 2 * i), __ldcg(at + 2 * i + 1)); }
     __device__ __forceinline__ void put(int64_t i, int2 v) const { at[2 * i] = v.x, at[2 * i + 1] = v.y; }
 };

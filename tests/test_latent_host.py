@@ -129,3 +129,26 @@ def test_references():
     assert f2.tolist() == [0, 0, 0, 2, 2]
     tab3, f3, moves, n = L.compact(tab2, c2, f2, 4)
     assert tab3[:2].tolist() == [[1, 0], [1, 0]] and moves[:n].tolist() == [[4, 0], [3, 1]] and f3.tolist() == [2, 2, 0, 0, 0]
+
+
+def test_counts_near_2_to_the_31_are_refused(lib):
+    """Loops over rows, blocks and pairs step past the end in 32 bits."""
+    most = 2 ** 31 - 1 - 65536
+    need = lib.pkv_blocks_workspace_bytes
+    need.argtypes = [I]
+    fork = caller(lib.pkv_fork_sequences, [("bt", P, None), ("nb", I, 1), ("ctx", P, None), ("B", I, 0), ("par", P, None), ("R", I, 0),
+                  ("ref", P, FAKE), ("blocks", I, 9), ("bo", P, None), ("co", P, None), ("err", P, None), ("stream", P, None)])
+    assert fork(blocks=most) == 0 and fork(blocks=most + 1) == -2
+    args = dict(bt=FAKE, ctx=FAKE, par=FAKE, bo=1 << 60, co=1 << 61)
+    assert fork(B=most + 1, **args) == -2 and fork(R=most + 1, **args) == -2 and fork(B=most, R=1, **args) == -2
+    extend = caller(lib.pkv_extend_sequences, [("bt", P, FAKE), ("nb", I, 4), ("ctx", P, FAKE), ("new", P, FAKE), ("B", I, 0), ("ref", P, FAKE),
+                    ("blocks", I, 9), ("copies", P, FAKE), ("ws", P, FAKE), ("bytes", Z, 1 << 40), ("err", P, None), ("stream", P, None)])
+    assert extend(blocks=most) == 0 and extend(blocks=most + 1) == -2 and extend(B=most + 1) == -2
+    compact = caller(lib.pkv_compact_blocks, [("bt", P, None), ("nb", I, 4), ("ctx", P, None), ("B", I, 0), ("ref", P, FAKE), ("blocks", I, 9),
+                     ("moves", P, FAKE), ("most", I, 4), ("n", P, FAKE), ("ws", P, FAKE), ("bytes", Z, 1 << 40), ("err", P, None),
+                     ("stream", P, None)])
+    assert compact(blocks=most + 1) == -2 and compact(most=most + 1) == -2
+    attend = caller(lib.pkv_decode_attn_latent, [("q", P, FAKE), ("cache", P, FAKE), ("bt", P, FAKE), ("nb", I, 4), ("ctx", P, FAKE),
+                    ("B", I, 0), ("T", I, 2), ("N", I, 8), ("scale", F, 1.0), ("out", P, FAKE), ("lse", P, None), ("d", Desc, GOOD),
+                    ("ws", P, FAKE), ("bytes", Z, 1 << 40), ("err", P, None), ("stream", P, None)])
+    assert attend(nb=(2 ** 31 - 1 - 1024) // 16) == 0 and attend(nb=(2 ** 31 - 1 - 1024) // 16 + 1) == -2
