@@ -316,3 +316,17 @@ def test_pool_past_2_to_the_32_bytes(pkv, N):
     kv, q = torch.randn(1, 576, device="cuda").bfloat16(), torch.zeros(1, N, 576, device="cuda").bfloat16()
     pkv.check(pkv.pkv_latent_append(kv, q[..., 512:], i32_dev([0]), torch.from_numpy(INV).cuda(), torch.tensor([16 * nb - 1], device="cuda"), big, q))
     assert same(big[-1, -1], kv[0])
+
+
+@pytest.mark.parametrize("N,T,ctx", [(1, 64, [70, 3, 200, 64, 0, 65]), (3, 64, [130, 64, 1, 900]), (128, 64, [300, 63]), (130, 33, [31, 257])], ids=str)
+def test_up_to_64_new_tokens(pkv, N, T, ctx):
+    """Many chunks of rows a sequence; lengths below the number of new tokens."""
+    c = Case(N, ctx, N, T).poison()
+    c.check(*c.run(pkv))
+
+
+@pytest.mark.parametrize("N", [1, 40])
+def test_a_large_batch_of_short_sequences(pkv, N):
+    r = np.random.default_rng(N)
+    c = Case(N, r.integers(0, 40, 5000), N, spread=0.5).poison()
+    c.check(*c.run(pkv))

@@ -182,3 +182,73 @@ def test_the_binding_names_what_is_wrong(pkv):  # noqa: F811
     assert pkv.pkv_decode_attn_latent(empty(0, 1, 8, 576), cache, i32(0, 2), i32(0), 0.1, empty(0, 1, 8, 512)) == 0
     assert pkv.pkv_copy_blocks_pools([cache], i32(0, 2)) == 0
     assert pkv.pkv_extend_sequences(i32(0, 2), i32(0), i32(0), i32(9), i32(0, 2), ws) == 0
+
+
+@pytest.mark.parametrize("N", [16, 128])
+def test_a_captured_tick_grows_its_sequences(pkv, N):  # noqa: F811
+    """Extension with copies, append and attention in one graph, each launch ahead of its predecessor's end, replayed over many
+    steps: what the same calls give one at a time, each after the end of the last."""
+    from paged_kv_decode_slot_gb300.step import LatentDecodeStep, SequenceBlocks, StepGraph
+    r = np.random.default_rng(N)
+    rows, blocks, ticks = 40, 400, 40
+    inv, new = torch.from_numpy(INV).cuda(), lambda *shape: bf16_dev(R.to_bf16(r.standard_normal(shape)))
+    base, q_rope, absorbed = new(blocks, 16, 576), new(rows, 1, N, 64), new(rows, 1, N, 576)
+    kv = new(ticks, rows, 1, 576)
+    parents = i32_dev(r.integers(0, 12, rows))
+
+    class Tick:
+        def __init__(self):
+            self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            self.seqs = SequenceBlocks(rows, 16, blocks, err_flag=self.err)
+            self.cache = base.clone()
+            first = np.zeros(rows, dtype=np.int32)
+            first[:12] = np.random.default_rng(1).integers(1, 100, 12)
+            self.seqs.extend(i32_dev(first), [self.cache])
+            self.seqs.fork(parents)
+            self.ones = torch.ones(rows, dtype=torch.int32, device="cuda")
+            self.step = LatentDecodeStep(kv[0].clone(), q_rope, absorbed.clone(), self.cache, self.seqs.block_tables, self.seqs.context_lens, 0.05,
+                                         inv, err_flag=self.err)
+            self.out = self.step.out
+
+        def run(self, stream=None):
+            self.seqs.extend(self.ones, [self.cache], stream)
+            self.step.run(stream)
+
+        def state(self):
+            return (self.seqs.block_tables, self.seqs.context_lens, self.seqs.ref_counts, self.seqs.copies, self.cache, self.step.q, self.step.out,
+                    self.step.lse, self.err)
+    one, other = Tick(), Tick()
+    saved = [t.clone() for t in one.state()]
+    graph = StepGraph(one)                                    # (runs the step while it warms up)
+    for t, s in zip(one.state(), saved):
+        t.copy_(s)
+    for k in range(ticks):
+        one.step.kv_new.copy_(kv[k])
+        graph.replay()
+        other.step.kv_new.copy_(kv[k])
+        torch.cuda.synchronize()
+        s = other.step
+        other.seqs.extend(other.ones, ())
+        torch.cuda.synchronize()
+        other.seqs._copy([other.cache], other.seqs.copies, None)
+        torch.cuda.synchronize()
+        pkv.check(pkv.pkv_latent_append_multi(s.kv_new, s.q_rope, s.block_tables, s.context_lens, inv, s.latent_cache, s.q, s.slot_mapping, None,
+                                              s.eps, False, s.err_flag))
+        torch.cuda.synchronize()
+        pkv.check(pkv.pkv_decode_attn_latent(s.q, s.latent_cache, s.block_tables, s.context_lens, s.scale, s.out, s.lse, s.workspace, s.err_flag))
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(one.state(), other.state())), f"tick {k}"
+    assert int(one.err) == 0 and int(one.seqs.context_lens.min()) > ticks
+
+
+def test_blocks_of_more_pools_than_one_call_takes(pkv):  # noqa: F811
+    from paged_kv_decode_slot_gb300.step import SequenceBlocks
+    seqs = SequenceBlocks(2, 2, 5)
+    pools = [torch.zeros(5, 16, 8, device="cuda") for _ in range(600)]
+    seqs.extend(i32_dev([7, 0]), pools)
+    for k, p in enumerate(pools):
+        p[0] = k + 1
+    seqs.fork(i32_dev([0, 0]))
+    seqs.extend(i32_dev([1, 1]), pools)
+    assert seqs.copies.tolist() == [[0, 1], [-1, -1]]
+    assert all(bool((p[:2] == k + 1).all()) and not p[2:].any() for k, p in enumerate(pools))
