@@ -1,4 +1,4 @@
-// pkv_latent_pair.cu - decode attention over a paged latent cache for sequences of more than 32 (token, head) rows; the
+// pkv_latent_pair.cu - decode attention over a paged latent cache for sequences of more than 48 (token, head) rows; the
 // mathematics is in pkv_latent_attn.cu.  Chunks of up to 128 rows, a cluster of two CTAs each.
 //
 // With 128 rows a cached row of 1,152 bytes takes 2 * 1088 * 128 operations, 242 a byte, about what the chip has for one
@@ -18,6 +18,14 @@
 // CTA = 11 warps: 0-7 softmax (warps w, w + 2, .. share rows 32 (w % 2) ..; of a tile's 128 tokens each thread has a row's 32:
 // half of them by lane, half by w / 4), 8 issues the MMAs (first CTA), 9 the loads, 10 zeroes what lies behind a sequence's
 // end.  QK^T of tile i + 1 is issued before P V of tile i, so the tensor cores work through the softmax of tile i.
+//
+// Bound by the tensor cores at half their rate: with 64 rows a CTA an MMA of M = 128 over the pair takes as long as one of
+// M = 256 would (61 clocks per N = 128, 122 per N = 256), 4,350 clocks a tile of which the period measured is 4,700.  152
+// sequences of 4,096 tokens and 128 heads take 170 us, 1.02 PFLOP/s; 64 of 512 to 8,192 tokens 94 us; one of 131,072 tokens 53.
+// The full rate needs the transposed products, M = 256 tokens or elements: built and measured at 134 us for the 64 sequences.
+// Both CTAs then need all tokens' weights for half of the rows (16 KB to the other CTA each tile, and common maxima), which
+// leaves six 16 KB stages, and a CTA's 278 KB a tile in loads of 2 KB boxes (100 clocks each to issue) come too slowly
+// through them.  Fetching tiles ahead into L2 gave nothing (100 to 113 us for 102, one to four tiles ahead).
 #include "pkv_cluster.cuh"
 #include "pkv_latent.cuh"
 

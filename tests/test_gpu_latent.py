@@ -330,3 +330,12 @@ def test_a_large_batch_of_short_sequences(pkv, N):
     r = np.random.default_rng(N)
     c = Case(N, r.integers(0, 40, 5000), N, spread=0.5).poison()
     c.check(*c.run(pkv))
+
+
+@pytest.mark.parametrize("N,T", [(48, 1), (16, 3), (24, 2), (47, 1), (11, 4), (49, 1), (60, 1)])
+def test_around_48_rows(pkv, N, T):
+    """The widest a CTA takes alone, and the first that a pair of CTAs shares."""
+    c = Case(N, CTX, N, T).poison()
+    c.check(*c.run(pkv))
+    c = Case(N, [9000, 70, 0, 3333], N, T).poison()
+    c.check(*c.run(pkv))

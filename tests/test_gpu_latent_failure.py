@@ -30,6 +30,8 @@ CASES = {
     "pairs": (128, 1, [900, 70, 3000]),
     "pairs, one of them with rows": (40, 1, [2000] * 100),
     "pairs, several chunks": (100, 3, [500, 129, 1000]),
+    "48 rows": (24, 2, [900, 70, 3000]),
+    "pairs, the second CTA without rows": (60, 1, [2000] * 100),
 }
 
 
