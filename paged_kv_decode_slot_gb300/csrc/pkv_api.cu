@@ -831,6 +831,7 @@ PKV_EXPORT int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_
     if (!aligned(workspace, 256)) return PKV_ERR_ALIGN;
     if (num_seqs == 0) return PKV_OK;
     pkv::LatentAttnParams p{};
+    p.cache = reinterpret_cast<const char *>(latent_cache);
     p.block_tables = block_tables, p.context_lens = context_lens, p.max_nb = max_blocks_per_seq;
     p.B = num_seqs, p.N = num_q_heads, p.T = num_new, p.num_blocks = cache.num_blocks;
     p.rows = num_new * num_q_heads, p.chunks = (int32_t)plan.chunks;

@@ -14,24 +14,26 @@ constexpr int kLatentDim = 512;   // the latent vector of a token
 constexpr int kLatentRope = 64;   // its rotary key
 constexpr int kLatentMaxCtas = 152;
 
-// How the (token, head) rows of a sequence are dealt out: chunks of chunk_rows rows, to a CTA (16, 32 or 48) or to a pair of
+// How the (token, head) rows of a sequence are dealt out: chunks of chunk_rows rows, to a CTA (16 or 32) or to a pair of
 // CTAs (128, 64 each).
 struct LatentPlan {
     int chunk_rows;
     int64_t chunks;
     int ctas() const { return chunk_rows == 128 ? 2 : 1; }
 };
-// The narrowest that holds a sequence's rows (64 sequences of 512 to 8,192 tokens and 48 rows: 71 us, by pairs 90; 16 rows in 32:
-// 66 for 63).
+// The narrowest that holds a sequence's rows (64 sequences of 512 to 8,192 tokens: 63 us with 16 rows, 66 with 32, 70 with 48 and
+// 71 with 64 by pairs).  A CTA has room for 48 rows too: no faster than a pair where there is work for all (three new tokens of
+// 16 heads over 20 sequences of up to 32,520 tokens 82 us for 76), 17 us for 21 over 5 short sequences, and not kept.
 inline LatentPlan latent_plan(int64_t rows)
 {
     LatentPlan p;
-    p.chunk_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 128;
+    p.chunk_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
     p.chunks = (rows + p.chunk_rows - 1) / p.chunk_rows;
     return p;
 }
 
 struct LatentAttnParams {
+    const char *cache;             // [num_blocks][16][576] bf16
     const int32_t *block_tables;   // [B][max_nb]
     const int32_t *context_lens;   // [B]
     int32_t max_nb, B, N, T, num_blocks;

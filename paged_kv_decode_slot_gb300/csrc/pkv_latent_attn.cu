@@ -3,19 +3,17 @@
 // the queries before and applied to the outputs after).
 //     s[r][j] = scale q[r] . c[j],  out[r] = sum_j softmax(s[r])_j c[j][:512],  r a (token, head) row of a sequence.
 //
-// This is the kernel for sequences of at most 48 rows (few heads, as one of several GPUs has them, or a few new tokens of
-// 16); more rows take pkv_latent_pair.cu.  All rows share the keys, so that even here the contraction is dense (30 operations a
-// byte with 16 rows) and goes to the tcgen05 tensor cores, both products transposed:
+// This is the kernel for sequences of at most 32 rows (few heads, as one of several GPUs has them); more rows take
+// pkv_latent_pair.cu.  All rows share the keys, so that even here the contraction is dense (30 operations a byte with 16 rows)
+// and goes to the tcgen05 tensor cores, both products transposed:
 //     S^T[64 tokens x R]  = C[64 x 576] . Q^T       A: the tile's rows as they lie (K-major), B: the queries
 //     O^T[512 x R]       += C^T[512 x 64] . P^T     A: the same bytes read MN-major (four M = 128 products), B: P
-// so that R = 16, 32 or 48 query rows a CTA is the N of the products, not a padded M: the 512 x R accumulator takes 4 R
-// of the 512 tensor-memory columns, and a tile is loaded once and read as keys and as values where it lies.  (48 rows are
-// what three tiles of 48 tokens leave room for.  With 64 rows two tiles remain, too few to load ahead: 90 to 104 us for 64
-// sequences of 512 to 8,192 tokens, where the pairs of CTAs take 90.)
+// so that R = 16 or 32 query rows a CTA is the N of the products, not a padded M: the 512 x R accumulator takes 4 R
+// of the 512 tensor-memory columns, and a tile is loaded once and read as keys and as values where it lies.
 //
 // Bound by memory, where there is enough of it: 152 sequences of 4,096 tokens and 16 rows take 116 us, 6.2 TB/s, 92% of a
-// copy's rate.  64 sequences of 512 to 8,192 tokens (325 MB) take 63 us with 16 rows, 66 with 32 and 71 with 48; one of 2,000
-// tokens 11 us, the launches and the dependent loads of lengths, tables and tiles.
+// copy's rate; 64 sequences of 512 to 8,192 tokens (325 MB) 63 us with 16 rows and 66 with 32.  One sequence of 2,000 tokens
+// takes 11 us: launches, and the dependent loads of lengths, tables and tiles.
 //
 // A block of 16 tokens is one TMA load of 18 KB, a box of (64 elements, 8 tokens, 9 chunks of elements, 2 halves): it
 // lands as [half][chunk][8 rows][128 bytes], swizzle atoms of 8 rows, so that the 8-row groups of consecutive blocks lie
@@ -41,14 +39,14 @@ constexpr int kLatThreads = 352;
 // R: query rows of a CTA.
 template <int R>
 struct LatentLayout {
-    static_assert(R == 16 || R == 32 || R == 48, "rows of a CTA");
+    static_assert(R == 16 || R == 32, "rows of a CTA");
     static constexpr int kBlocks = 3;                    // blocks of a tile (M = 64: at most four)
     static constexpr int kSlots = 3;                     // tiles in shared memory
     static constexpr int kTile = kBlocks * kBlockSize;   // tokens of a tile
     static constexpr int kRing = kSlots * kBlocks;
     static constexpr int kQChunk = R * 128;              // 64 elements of R queries, K-major, 128-byte swizzle
     static constexpr int kQBytes = kLatChunks * kQChunk;
-    static constexpr int kPLine = R == 48 ? 128 : R * 2; // bytes of one token's weights: a swizzle atom's row
+    static constexpr int kPLine = R * 2;                 // bytes of one token's weights: a swizzle atom's row
     static constexpr int kPBytes = kTile * kPLine;
     static constexpr int kRingOffset = 0;
     static constexpr int kQOffset = kRing * kLatBlock;
@@ -64,16 +62,16 @@ struct LatentLayout {
     static_assert(kQOffset % 1024 == 0 && kPOffset % 1024 == 0 && kSlots <= 4, "swizzle atoms are aligned");
     static_assert((kSlots - 1) * kBlocks * kLatBlock + 8 * kLatGroup <= kBytes, "M = 64 rows from any slot on lie inside the window");
     static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
-    static constexpr uint32_t kCols = R == 48 ? 512 : R == 32 ? 256 : 128;  // tensor memory: O^T 4 R, S^T 2 R
+    static constexpr uint32_t kCols = R == 32 ? 256 : 128;  // tensor memory: O^T 4 R, S^T 2 R
 };
 
 // ---- small pieces -------------------------------------------------------------------------------
-// Descriptor of P^T as an MN-major operand: the swizzle is as wide as a token's line (of 48 rows: 128 bytes, 96 in use).
+// Descriptor of P^T as an MN-major operand of R elements a row: the swizzle is as wide as the row.
 template <int R>
 __device__ __forceinline__ uint64_t latent_p_desc(uint32_t addr)
 {
-    constexpr uint64_t kMode = R == 48 ? 2 : R == 32 ? 4 : 6;
-    constexpr uint32_t kGroup = 8 * LatentLayout<R>::kPLine;  // eight tokens
+    constexpr uint64_t kMode = R == 32 ? 4 : 6;
+    constexpr uint32_t kGroup = 8 * R * 2;  // eight tokens
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kGroup >> 4) << 16) | ((uint64_t)(kGroup >> 4) << 32) | (1ull << 46) |
            (kMode << 61);
 }
@@ -82,11 +80,11 @@ __device__ __forceinline__ uint64_t latent_p_desc(uint32_t addr)
 template <int R>
 __device__ __forceinline__ uint32_t latent_p_at(int t, int u)
 {
-    const int x = R == 48 ? t & 7 : R == 32 ? (t >> 1) & 3 : (t >> 2) & 1;
-    return (uint32_t)(t * LatentLayout<R>::kPLine + ((u ^ x) << 4));
+    const int x = R == 32 ? (t >> 1) & 3 : (t >> 2) & 1;
+    return (uint32_t)(t * (R * 2) + ((u ^ x) << 4));
 }
 
-// C columns of a warp's 32 lanes (C = 8, 16 or 24).
+// C columns of a warp's 32 lanes (C = 8, 16 or 32).
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -102,51 +100,57 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 template <int C>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&x)[C])
 {
-    constexpr int kWide = C / 16 * 16;
-    uint32_t a[16], b[8];
-    if constexpr (kWide > 0) tmem_ld16(taddr, a);
-    if constexpr (C > kWide) tmem_ld8(taddr + kWide, b);
-    tmem_ld_wait();
+    if constexpr (C == 8) {
+        uint32_t r[8];
+        tmem_ld8(taddr, r);
+        tmem_ld_wait();
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = __uint_as_float(c < kWide ? a[c % 16] : b[c % 8]);
+        for (int c = 0; c < 8; ++c) x[c] = __uint_as_float(r[c]);
+    } else {
+        uint32_t r[C / 16][16];
+#pragma unroll
+        for (int k = 0; k < C / 16; ++k) tmem_ld16(taddr + 16 * k, r[k]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = __uint_as_float(r[c / 16][c % 16]);
+    }
 }
 template <int C>
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&x)[C])
 {
-    constexpr int kWide = C / 16 * 16;
-    uint32_t a[16], b[8];
+    if constexpr (C == 8) {
+        uint32_t r[8];
 #pragma unroll
-    for (int c = 0; c < C; ++c) (c < kWide ? a[c % 16] : b[c % 8]) = __float_as_uint(x[c]);
-    if constexpr (kWide > 0) tmem_st16(taddr, a);
-    if constexpr (C > kWide) tmem_st8(taddr + kWide, b);
+        for (int c = 0; c < 8; ++c) r[c] = __float_as_uint(x[c]);
+        tmem_st8(taddr, r);
+    } else {
+#pragma unroll
+        for (int k = 0; k < C / 16; ++k) {
+            uint32_t r[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(x[16 * k + c]);
+            tmem_st16(taddr + 16 * k, r);
+        }
+    }
 }
 
-// Reduce column c of a warp's 32 lanes for C columns at once; lane l receives column l % C (of 24, lanes 0 .. 23 theirs).  x is
-// used up.
+// Reduce column c of a warp's 32 lanes for C columns at once; lane l receives column l % C.  x is used up.
 template <int C, typename Op>
 __device__ __forceinline__ float reduce_columns(float (&x)[C], int lane, Op op)
 {
-    if constexpr (C == 24) {
-        float a[16], b[8];
 #pragma unroll
-        for (int c = 0; c < C; ++c) (c < 16 ? a[c % 16] : b[c % 8]) = x[c];
-        const float first = reduce_columns<16>(a, lane, op), rest = reduce_columns<8>(b, lane, op);
-        return lane < 16 ? first : rest;
-    } else {
+    for (int o = C / 2; o >= 1; o >>= 1) {
+        const bool up = lane & o;
 #pragma unroll
-        for (int o = C / 2; o >= 1; o >>= 1) {
-            const bool up = lane & o;
-#pragma unroll
-            for (int j = 0; j < o; ++j) {
-                const float give = up ? x[j] : x[j + o], keep = up ? x[j + o] : x[j];
-                x[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
-            }
+        for (int j = 0; j < o; ++j) {
+            const float give = up ? x[j] : x[j + o], keep = up ? x[j + o] : x[j];
+            x[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
         }
-        float v = x[0];
-#pragma unroll
-        for (int o = C; o < 32; o <<= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-        return v;
     }
+    float v = x[0];
+#pragma unroll
+    for (int o = C; o < 32; o <<= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
 }
 
 template <int R>
@@ -371,7 +375,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         const int quarter = warp & 3, half = warp >> 2, tok = 16 * quarter + lane, c0 = half * CW;
         const bool token = lane < 16 && quarter < NB;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const int col = lane % CW;  // the column this lane holds after a reduction
+        const int col = lane & (CW - 1);  // the column this lane holds after a reduction
         uint32_t g = 0;
         bool ok = true;
         LatentSegment sg;
@@ -380,7 +384,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             const int nrows = min(R, p.rows - row0);
             if (threadIdx.x == 0 && sg.t0 == 0) {
                 // for the joining launch: the first CTA of the unit's parts, and how many there are
-                const int64_t last = sg.start + sg.tiles + latent_unit_cost<L::kTile>() - 1;
+                const int64_t last = sg.start + sg.tiles + kLatentUnitCost - 1;
                 const int parts = sg.whole ? 1 : (int)(((last + 1) * ctas - 1) / total) - cta + 1;
                 p.unit_parts[(int64_t)sg.b * p.chunks + sg.chunk] = make_int2(cta, parts);
             }
@@ -679,9 +683,7 @@ static cudaError_t latent_attn_t(const CUtensorMap &tc, const CUtensorMap &tq, L
 cudaError_t launch_latent_attn(const CUtensorMap &tc, const CUtensorMap &tq, const LatentAttnParams &p, int cta_rows, int sms,
                                cudaStream_t stream)
 {
-    return cta_rows == 48   ? latent_attn_t<48>(tc, tq, p, sms, stream)
-           : cta_rows == 32 ? latent_attn_t<32>(tc, tq, p, sms, stream)
-                            : latent_attn_t<16>(tc, tq, p, sms, stream);
+    return cta_rows == 32 ? latent_attn_t<32>(tc, tq, p, sms, stream) : latent_attn_t<16>(tc, tq, p, sms, stream);
 }
 
 }  // namespace pkv

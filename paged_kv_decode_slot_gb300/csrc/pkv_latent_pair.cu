@@ -5,27 +5,33 @@
 // byte of DRAM, and 128 queries and a 128-token tile are 147 KB each: neither one CTA's shared memory (227 KB) nor its tensor
 // memory (128 x 512 sums fill it) holds the problem.  tcgen05.mma with cta_group::2 spreads it over two SMs, and no operand
 // is held twice:
-//     S[128 x 128 tokens] = Q . C^T        a CTA: its 64 rows of Q; the keys of 64 of the tokens
-//     O[128 x 512]       += P . C[:, :512] a CTA: its 64 rows of P; all tokens' values of its 256 elements
-// S and O lie in both tensor memories, each CTA's 64 rows: a row's first half of the columns in lane r, its second half in
-// lane 64 + r.  One thread of the first CTA issues all MMAs.
+//     S[128 x 128 tokens]  = Q . C^T            a CTA: its 64 rows of Q; the keys of 64 of the tokens
+//     O^T[512 x 128 rows] += C[:, :512]^T . P^T a CTA: all tokens' values of its 256 elements; its 64 rows of P
+// S is split by rows: a row's first half of the columns lies in lane r, its second half in lane 64 + r, so softmax stays within
+// a CTA, and its weights are, row by row, what the second product takes from this CTA.  O^T is split by elements, each CTA with
+// all rows.  That way P V runs as M = 256 at the full rate (as O += P V, M = 128, an MMA of the pair takes as long for half as
+// much); what it costs is that scaling a row's sums takes both CTAs.  They do so at the end, for 1 / sum, and where a logit
+// exceeds its row's reference (the maximum of its first tile) by 2^32, which weights and sums in 32-bit exponents bear: the
+// MMA thread then refuses that round of weights, both CTAs exchange factors, scale, and make the tile's weights again.
+// One thread of the first CTA issues all MMAs.
 //
-// The cache streams through a ring of 16 KB stages, a CTA's share of a tile first as keys (64 tokens x 128 elements, four and
-// a half stages), then, from L2, as values (32 tokens x 256 elements, four): 138 KB a tile and CTA, of which nothing waits
-// for the softmax, so that nearly the whole ring is always under way.  A box is one block's share of a stage, in swizzle
-// atoms of 8 rows, [half][chunk][8 rows][128 bytes].  Each CTA's loads are counted on the first CTA's barrier.
+// The cache streams through nine slots, four of 16 KB for a CTA's share of a tile as keys (64 tokens x 128 elements), half a
+// one for its rotary keys and four for its values (32 tokens x 256 elements, from L2): every tile uses every slot once, so
+// all addresses and parities of the MMA thread's code are known when it is compiled.  (Through a ring whose stages had to
+// be computed, that thread was what bounded the kernel: 4,700 clocks a tile, whatever the MMAs' rate.)  A box is one block's
+// share of a slot, in swizzle atoms of 8 rows, [half][chunk][8 rows][128 bytes].  Each CTA's loads are counted on the first
+// CTA's barrier.  The next tile's blocks are fetched into L2 meanwhile: a slot of keys is free again only when the last tile's
+// are multiplied (64 sequences of 512 to 8,192 tokens: 81 us, without 87, two tiles ahead 84).
 //
-// CTA = 11 warps: 0-7 softmax (warps w, w + 2, .. share rows 32 (w % 2) ..; of a tile's 128 tokens each thread has a row's 32:
-// half of them by lane, half by w / 4), 8 issues the MMAs (first CTA), 9 the loads, 10 zeroes what lies behind a sequence's
-// end.  QK^T of tile i + 1 is issued before P V of tile i, so the tensor cores work through the softmax of tile i.
+// CTA = 12 warps: 0-7 softmax (warps w, w + 2, .. share rows 32 (w % 2) ..; of a tile's 128 tokens each thread has a row's 32:
+// half of them by lane, half by w / 4) and outputs (each thread an element of all rows), 8 issues the MMAs (first CTA), 9 and 10
+// load keys and queries, 11 loads values and zeroes what lies behind a sequence's end.  QK^T of tile i + 1 is issued before P V of
+// tile i, so the tensor cores work through the softmax of tile i.
 //
-// Bound by the tensor cores at half their rate: with 64 rows a CTA an MMA of M = 128 over the pair takes as long as one of
-// M = 256 would (61 clocks per N = 128, 122 per N = 256), 4,350 clocks a tile of which the period measured is 4,700.  152
-// sequences of 4,096 tokens and 128 heads take 170 us, 1.02 PFLOP/s; 64 of 512 to 8,192 tokens 94 us; one of 131,072 tokens 53.
-// The full rate needs the transposed products, M = 256 tokens or elements: built and measured at 134 us for the 64 sequences.
-// Both CTAs then need all tokens' weights for half of the rows (16 KB to the other CTA each tile, and common maxima), which
-// leaves six 16 KB stages, and a CTA's 278 KB a tile in loads of 2 KB boxes (100 clocks each to issue) come too slowly
-// through them.  Fetching tiles ahead into L2 gave nothing (100 to 113 us for 102, one to four tiles ahead).
+// Bound by memory and by what a unit costs beside its tiles (prologue, exchange, outputs and join, about 20 us of the 77):
+// 152 sequences of 4,096 tokens and 128 heads take 139 us, 5.5 TB/s and 1.25 PFLOP/s; 64 of 512 to 8,192 tokens 77 us, with 64
+// heads 71; one of 131,072 tokens 46.  Tiles of 256 tokens with both products as M = 256 took 134 us for the 64 sequences: each CTA
+// then needs half of the other's weights in every tile, and 72 KB of queries leave 96 KB for 278 KB of loads a tile.
 #include "pkv_cluster.cuh"
 #include "pkv_latent.cuh"
 
@@ -34,23 +40,28 @@ namespace pkv {
 struct PairLayout {
     static constexpr int kTile = 128, kBlocks = kTile / kBlockSize;
     static constexpr int kRows = 64;                                   // of a CTA
-    static constexpr int kStages = 8, kStage = 16384;
+    static constexpr int kStages = 9, kStage = 16384, kRope = 8;       // slots: 4 of keys, 4 of values, the rotary keys (half a slot)
     static constexpr int kQChunk = kRows * 128, kQBytes = kLatChunks * kQChunk;
     static constexpr int kPChunk = kRows * 128, kPBytes = 2 * kPChunk;  // 64 tokens a chunk
     static constexpr int kQOffset = 0, kPOffset = kQBytes, kRingOffset = kPOffset + kPBytes;
-    static constexpr int kBarOffset = kRingOffset + kStages * kStage;
-    // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, tail[2], fin
-    static constexpr int kBars = 2 * kStages + 9;
+    static constexpr int kBarOffset = kRingOffset + 8 * kStage + kStage / 2;
+    // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, exchange, tail[2], fin
+    static constexpr int kBars = 2 * kStages + 10;
     static constexpr int kMiscOffset = (kBarOffset + kBars * 8 + 15) & ~15;
-    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, query loads, - */ + 3 * kStages /* sent, use, want */ + 4 * kRows;
+    static constexpr int kWords = 4 /* tile masks */ + 8 /* abort, tmem, query loads, raise, verdict, - */ + 3 * kStages + 1 /* sent, use, want, - */ +
+                                  4 * kRows /* of four warps */ + 2 * kRows /* factors */;
     static constexpr int kBytes = kMiscOffset + kWords * 4;
     static constexpr int kAlloc = kBytes + 1024;                       // room to align the window
     static_assert(kPOffset % 1024 == 0 && kRingOffset % 1024 == 0, "swizzle atoms are aligned");
     static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
-    static constexpr uint32_t kCols = 512;                             // tensor memory: O 256, S 2 x 64
+    static constexpr uint32_t kCols = 512;                             // tensor memory: O^T 2 x 128, S 2 x 64
 };
-constexpr int kPairSoftmaxWarps = 8, kPairMmaWarp = 8, kPairLoadWarp = 9, kPairTailWarp = 10;
-constexpr int kPairThreads = 352;
+constexpr int kPairSoftmaxWarps = 8, kPairMmaWarp = 8, kPairLoadWarp = 9, kPairValueWarp = 11;
+constexpr int kPairThreads = 384;
+constexpr int kBlockBytes = kBlockSize * (kLatentDim + kLatentRope) * 2;
+// A logit may exceed its row's reference by this much (log2) before the reference moves: weights and sums have 32-bit
+// exponents, so that only the far ends of the range matter, and moving it takes both CTAs.
+constexpr float kPairRescale = 32.f;
 
 // ---- cta_group::2 -------------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t ncols)
@@ -133,6 +144,10 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&x)[32])
     for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(r[c / 16][c % 16]);
 }
 
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
 {
     float4 v;
@@ -145,11 +160,32 @@ __device__ __forceinline__ int load_word(const volatile int *at, int rank)
     return __float_as_int(load_cluster<float>(smem_u32((const void *)at), rank));
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// An arrival, at a barrier of the cluster, that what this thread wrote to either CTA's shared memory comes before.
+__device__ __forceinline__ void pair_arrive_release(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *at, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
+// A barrier's phase that is complete: what was written before its arrivals is seen behind this.
+__device__ __forceinline__ void pair_acquired(uint32_t bar, uint32_t parity)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar), "r"(parity)
+                 : "memory");
+}
+// (2,000 clocks: where an exchange of the CTAs' shared memory needs it, not in every tile)
+__device__ __forceinline__ void pair_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 __global__ void __launch_bounds__(kPairThreads, 1)
 latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttnParams p)
 {
     using L = PairLayout;
-    constexpr int S = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const mem = smem_raw + (base - raw);
@@ -157,26 +193,29 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     const int rank = (int)pair_rank(), pair = (int)blockIdx.x >> 1;
 
     const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
-    const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * S, bar_qfull = bar_empty + 8 * S,
-                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_tail = bar_pv + 8,
-                   bar_fin = bar_tail + 16;
+    const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * L::kStages, bar_qfull = bar_empty + 8 * L::kStages,
+                   bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_x = bar_pv + 8,
+                   bar_tail = bar_x + 8, bar_fin = bar_tail + 16;
     volatile int *const tile_mask = reinterpret_cast<volatile int *>(mem + L::kMiscOffset);  // [4], by tile % 4: blocks there
     volatile int *const abort_flag = tile_mask + 4;
     volatile uint32_t *const tmem_slot = reinterpret_cast<volatile uint32_t *>(tile_mask + 5);
     volatile int *const q_asked = tile_mask + 6;
-    // of a stage's last use: bytes this CTA asked for, the use's number + 1, bytes the barrier was told (first CTA)
-    volatile int *const sent = tile_mask + 8, *const use = sent + S, *const want = use + S;
-    float *const quarters = const_cast<float *>(reinterpret_cast<volatile float *>(want + S));  // [4][64]
+    // of a slot's last use: bytes this CTA asked for, the use's number + 1, bytes the barrier was told (first CTA)
+    volatile int *const raise = tile_mask + 7;    // first CTA: a logit passed its reference by too much
+    volatile int *const verdict = tile_mask + 8;  // the last round of weights that is to be made again with new references
+    volatile int *const sent = tile_mask + 12, *const use = sent + L::kStages, *const want = use + L::kStages;
+    float *const quarters = const_cast<float *>(reinterpret_cast<volatile float *>(want + L::kStages + 1));  // [4][64]
+    float *const factor = quarters + 4 * L::kRows;                                              // [128] of both CTAs' rows
 
     // what needs nothing of the launch ahead comes before the wait for it
     if (threadIdx.x == 0) {
-        *abort_flag = 0;
-        *q_asked = 0;
-        for (int s = 0; s < S; ++s) sent[s] = use[s] = want[s] = 0;
+        *abort_flag = 0, *q_asked = 0, *raise = 0, *verdict = 0;
+        for (int s = 0; s < L::kStages; ++s) sent[s] = use[s] = want[s] = 0;
         for (int k = 0; k < L::kBars; ++k) {
             const uint32_t bar = bar_full + 8 * k;
-            // weights: the softmax warps of both CTAs; stages and zeroed rows: both CTAs
-            mbar_init(bar, bar == bar_p ? 2 * kPairSoftmaxWarps : k < S || bar == bar_tail + 8 ? 2 : 1);
+            // weights: the softmax warps of both CTAs; exchanges: two warps of the other CTA and, so that none can be a round
+            // behind, all eight of this one; stages and zeroed rows: both CTAs
+            mbar_init(bar, bar == bar_p ? 2 * kPairSoftmaxWarps : bar == bar_x ? 2 + kPairSoftmaxWarps : k < L::kStages || bar == bar_tail + 8 ? 2 : 1);
         }
         prefetch_tensormap(&maps.keys);
         prefetch_tensormap(&maps.rope);
@@ -211,167 +250,187 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     };
     auto wait_one = [&](uint32_t bar, uint32_t parity) { return latent_wait(bar, parity, abort_flag, p.wait_ns); };
     auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)); };
+    auto give_up_one = [&]() {
+        if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
+        *abort_flag = 1;
+    };
     bool issuer = false;  // the thread that issues the MMAs (a commit speaks of its thread's)
 
-    if (warp == kPairLoadWarp) {
-        // ------------------------------ loads: one thread ------------------------------
+    // Slot s for tile number gt, once it is free; the first CTA's barrier is told what both will send.  The second CTA arrives there
+    // also where it has nothing to send: the MMAs could otherwise use and release the slot twice before this thread came to
+    // wait for the first time (a barrier tells only neighbouring uses apart).
+    auto open = [&](int s, uint32_t gt, int bytes_all, int bytes_own) {
+        if (gt > 0 && !wait_one(bar_empty + 8 * s, (gt & 1) ^ 1)) return false;
+        sent[s] = bytes_own, use[s] = (int)gt + 1;
+        if (rank == 0) {
+            want[s] = bytes_all;
+            mbar_arrive_expect_tx(bar_full + 8 * s, (uint32_t)bytes_all);
+        } else {
+            pair_arrive(pair_at(bar_full + 8 * s, 0));
+        }
+        return true;
+    };
+    // The blocks of tile t of a segment (-1: none, or none of the pool).
+    auto ids_of = [&](const LatentSegment &sg, int t, int (&ids)[L::kBlocks]) {
+        const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
+        const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
+#pragma unroll
+        for (int k = 0; k < L::kBlocks; ++k) {
+            const int j = t * L::kBlocks + k;
+            ids[k] = t < sg.t1 && j < nb ? tbl[j] : -1;
+        }
+    };
+    auto mask_of = [&](const int (&ids)[L::kBlocks]) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int k = 0; k < L::kBlocks; ++k) mask |= (uint32_t)(ids[k] >= 0 && ids[k] < p.num_blocks) << k;
+        return mask;
+    };
+    if (warp == kPairLoadWarp || warp == kPairLoadWarp + 1) {
+        // ------------------------------ keys and queries: one thread of two warps ------------------------------
         if (elect_one()) {
+            const int me = warp - kPairLoadWarp;
             const uint32_t full_there = pair_at(bar_full, 0), qfull_there = pair_at(bar_qfull, 0);
-            int n = 0;           // stages so far
             uint32_t g = 0, q_loads = 0;
             bool ok = true, withheld = false;
-            // Stage n, once it is free; the first CTA's barrier is told what both will send.  The second CTA arrives there for
-            // every stage, also for one that it has nothing to send for: the MMAs could otherwise use and release the stage
-            // twice before this thread came to wait for the first time (a barrier tells only neighbouring uses apart).
-            auto open = [&](int bytes_all, int bytes_own) {
-                const int s = n % S;
-                if (n >= S) ok = wait_one(bar_empty + 8 * s, (uint32_t)(((n / S) & 1) ^ 1));
-                if (!ok) return;
-                sent[s] = bytes_own, use[s] = n + 1;
-                if (rank == 0) {
-                    want[s] = bytes_all;
-                    mbar_arrive_expect_tx(bar_full + 8 * s, (uint32_t)bytes_all);
-                } else {
-                    pair_arrive(full_there + 8 * s);
-                }
-            };
-            int prev[L::kBlocks];
-            uint32_t prev_mask = 0;
-            auto fill_v = [&](int nblk) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    if (2 * v >= nblk) break;
-                    const uint32_t two = (prev_mask >> (2 * v)) & 3u;
-                    open(2 * __popc(two) * 8192, __popc(two) * 8192);
-                    if (!ok) return;
-                    const uint32_t dst = ring + (n % S) * L::kStage, bar = full_there + 8 * (n % S);
-                    if (two & 1u) pair_load_5d(dst, &maps.values, bar, 0, 0, 4 * rank, 0, prev[2 * v]);
-                    if (two & 2u) pair_load_5d(dst + 8192, &maps.values, bar, 0, 0, 4 * rank, 0, prev[2 * v + 1]);
-                    ++n;
-                }
-            };
             LatentSegment sg;
             while (ok && walk.next(p, sg)) {
-                // the queries, once the last unit's are no longer needed
-                if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
-                if (!ok) break;
-                const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * 128 + rank * L::kRows;
-                *q_asked = (int)++q_loads;
-                if (rank == 0) mbar_arrive_expect_tx(bar_qfull, 2 * L::kQBytes);
-                for (int c = 0; c < kLatChunks; ++c) pair_load_3d(q_u32 + c * L::kQChunk, &maps.queries, qfull_there, 0, (int)row, c);
-                const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
-                const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
+                if (me == 0) {
+                    // the queries, once the last unit's are no longer needed
+                    if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
+                    if (!ok) break;
+                    const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * 128 + rank * L::kRows;
+                    *q_asked = (int)++q_loads;
+                    if (rank == 0) mbar_arrive_expect_tx(bar_qfull, 2 * L::kQBytes);
+                    for (int c = 0; c < kLatChunks; ++c) pair_load_3d(q_u32 + c * L::kQChunk, &maps.queries, qfull_there, 0, (int)row, c);
+                }
                 int next[L::kBlocks];
-                auto ids_of = [&](int t) {
-#pragma unroll
-                    for (int k = 0; k < L::kBlocks; ++k) {
-                        const int j = t * L::kBlocks + k;
-                        next[k] = t < sg.t1 && j < nb ? tbl[j] : -1;
-                    }
-                };
-                ids_of(sg.t0);
+                ids_of(sg, sg.t0, next);
                 for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
-                    const int nblk = min(L::kBlocks, nb - t * L::kBlocks);
-                    int ids[L::kBlocks];
-                    uint32_t mask = 0;
-#pragma unroll
-                    for (int k = 0; k < L::kBlocks; ++k) {
-                        ids[k] = next[k];
-                        mask |= (uint32_t)(ids[k] >= 0 && ids[k] < p.num_blocks) << k;
-                    }
-                    ids_of(t + 1);
                     if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
                         withheld = true, ok = false;
                         break;
                     }
-                    if (mask != (1u << nblk) - 1u && rank == 0) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
-                    tile_mask[g & 3] = (int)mask;
-                    const uint32_t own = (mask >> (4 * rank)) & 0xFu;
+                    const uint32_t mask = mask_of(next), own = (mask >> (4 * rank)) & 0xFu;
                     int mine[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mine[k] = rank ? ids[4 + k] : ids[k];
+                    for (int k = 0; k < 4; ++k) mine[k] = rank ? next[4 + k] : next[k];
+                    ids_of(sg, t + 1, next);
+                    if (me == 0 && rank == 0) {
+                        const int nblk = min(L::kBlocks, (sg.ctx + kBlockSize - 1) / kBlockSize - t * L::kBlocks);
+                        if (mask != (1u << nblk) - 1u) set_flag(p.err_flag, PKV_FLAG_BLOCK_RANGE);
+                    }
+                    tile_mask[g & 3] = (int)mask;  // (both threads write it, each before it fills a slot of the tile)
 #pragma unroll 1
-                    for (int c = 0; c < 5; ++c, ++n) {
-                        const int bytes = c < 4 ? 4096 : 2048;
-                        open(__popc(mask) * bytes, __popc(own) * bytes);
+                    for (int c = 2 * me; c < 2 + 3 * me; ++c) {
+                        const bool rope = c == 4;
+                        const int s = rope ? L::kRope : c, bytes = rope ? 2048 : 4096;
+                        ok = open(s, g, __popc(mask) * bytes, __popc(own) * bytes);
                         if (!ok) break;
-                        const CUtensorMap *const map = c < 4 ? &maps.keys : &maps.rope;
-                        const uint32_t dst = ring + (n % S) * L::kStage, bar = full_there + 8 * (n % S);
+                        const CUtensorMap *const map = rope ? &maps.rope : &maps.keys;
+                        const uint32_t dst = ring + s * L::kStage, bar = full_there + 8 * s;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if ((own >> k) & 1u) pair_load_5d(dst + k * bytes, map, bar, 0, 0, 2 * c, 0, mine[k]);
                     }
-                    if (t > sg.t0 && ok) fill_v(L::kBlocks);
-                    prev_mask = mask;
+                    if (me == 0) {
+                        // the next tile on its way into L2 meanwhile
 #pragma unroll
-                    for (int k = 0; k < L::kBlocks; ++k) prev[k] = ids[k];
+                        for (int k = 0; k < 4; ++k) {
+                            const int id = rank ? next[4 + k] : next[k];
+                            if (id >= 0 && id < p.num_blocks) prefetch_l2(p.cache + (int64_t)id * kBlockBytes, kBlockBytes);
+                        }
+                    }
                 }
-                if (ok) fill_v(min(L::kBlocks, nb - (sg.t1 - 1) * L::kBlocks));
             }
-            // every stage and the queries released: no arrival is on its way into this CTA any more
-            for (int k = max(0, n - S); k < n && ok; ++k) ok = wait_one(bar_empty + 8 * (k % S), (uint32_t)((k / S) & 1));
+            // the slots and the queries released: no arrival is on its way into this CTA any more
+            for (int c = 2 * me; c < 2 + 3 * me && ok && g > 0; ++c) ok = wait_one(bar_empty + 8 * (c == 4 ? L::kRope : c), (g - 1) & 1);
             if (ok && q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
-            if (!ok && !withheld) {
-                if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
-                *abort_flag = 1;
-            }
+            if (!ok && !withheld) give_up_one();
         }
         __syncwarp();
-    } else if (warp == kPairTailWarp) {
-        // ---------------- rows behind a sequence's end ----------------
-        // They may hold anything, and 0 x NaN is NaN: both CTAs zero them before P V reads them, when the MMA thread asks for it
-        // (asked and answered in turn, so that neither can be a use of the stage ahead of the other).
-        int n = 0;
-        uint32_t asked = 0;
-        bool ok = true;
+    } else if (warp == kPairValueWarp) {
+        // ------------------------------ values: one thread; rows behind a sequence's end: the warp ------------------------------
+        // Those may hold anything, and 0 x NaN is NaN: both CTAs zero them before P V reads them, when the MMA thread asks for it
+        // (asked and answered in turn, so that neither can be a use of the slot ahead of the other).
+        const bool leads = elect_one();
+        uint32_t g = 0, asked = 0;
+        bool ok = true, withheld = false;
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
-            const int count = sg.t1 - sg.t0, tail = sg.ctx % kBlockSize;
-            int last = 4;  // stages of the last tile's values
-            if (sg.t1 == sg.tiles) {
-                const int nblk = (sg.ctx + kBlockSize - 1) / kBlockSize - (sg.tiles - 1) * L::kBlocks;
-                last = (nblk + 1) / 2;
-                if (tail > 0) {
-                    ok = wait(bar_tail, asked++ & 1);
-                    if (!ok) break;
-                    const int k = n + 5 * count + 4 * (count - 1) + last - 1;
-                    const uint32_t blk = ring + (k % S) * L::kStage + ((nblk - 1) & 1) * 8192;
-                    for (int x = lane; x < (kBlockSize - tail) * 32; x += 32) {
-                        const int u = x & 31, row = tail + (x >> 5);
-                        st_shared_v4(blk + (row >> 3) * 4096 + (u >> 3) * 1024 + (row & 7) * 128 + (u & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+            if (leads) {
+                int next[L::kBlocks];
+                ids_of(sg, sg.t0, next);
+                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
+                    if (PKV_TILE_WITHHELD(p, t)) {
+                        withheld = true, ok = false;
+                        break;
                     }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) pair_arrive(pair_at(bar_tail + 8, 0));
+                    const uint32_t mask = mask_of(next);
+                    int ids[L::kBlocks];
+#pragma unroll
+                    for (int k = 0; k < L::kBlocks; ++k) ids[k] = next[k];
+                    ids_of(sg, t + 1, next);
+                    // (slots past the last block pass empty, so that all have a tile's parity)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const uint32_t two = (mask >> (2 * v)) & 3u;
+                        if (ok) ok = open(4 + v, g, 2 * __popc(two) * 8192, __popc(two) * 8192);
+                        if (!ok) break;
+                        const uint32_t dst = ring + (4 + v) * L::kStage, bar = pair_at(bar_full + 8 * (4 + v), 0);
+                        if (two & 1u) pair_load_5d(dst, &maps.values, bar, 0, 0, 4 * rank, 0, ids[2 * v]);
+                        if (two & 2u) pair_load_5d(dst + 8192, &maps.values, bar, 0, 0, 4 * rank, 0, ids[2 * v + 1]);
+                    }
                 }
             }
-            n += 5 * count + 4 * (count - 1) + last;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            const int tail = sg.ctx % kBlockSize;
+            if (!ok || sg.t1 != sg.tiles || tail == 0) continue;
+            ok = wait(bar_tail, asked++ & 1);
+            if (!ok) break;
+            const int j = sg.ctx / kBlockSize - (sg.tiles - 1) * L::kBlocks;
+            const uint32_t blk = ring + (4 + (j >> 1)) * L::kStage + (j & 1) * 8192;
+            for (int x = lane; x < (kBlockSize - tail) * 32; x += 32) {
+                const int u = x & 31, row = tail + (x >> 5);
+                st_shared_v4(blk + (row >> 3) * 4096 + (u >> 3) * 1024 + (row & 7) * 128 + (u & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) pair_arrive(pair_at(bar_tail + 8, 0));
         }
-        if (!ok) give_up();
+        if (leads)
+            for (int v = 0; v < 4 && ok && g > 0; ++v) ok = wait_one(bar_empty + 8 * (4 + v), (g - 1) & 1);
+        if (!__all_sync(0xFFFFFFFFu, ok || withheld) && !__any_sync(0xFFFFFFFFu, withheld)) give_up();
     } else if (warp == kPairMmaWarp) {
         // ------------------------------ MMAs: one thread of the first CTA ------------------------------
         issuer = elect_one() && rank == 0;
         if (issuer) {
-            constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0), kIdO = idesc_bf16_f32(128, 256, 0, 1);
-            // descriptors: an address moves the low word alone
-            const uint64_t k_desc = smem_desc_sw128(ring, 16, 2048), r_desc = smem_desc_sw128(ring, 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(ring, 1024, 4096);
+            constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0), kIdO = idesc_bf16_f32(256, 128, 1, 0);
+            const uint64_t k_desc = smem_desc_sw128(ring, 16, 2048), r_desc = smem_desc_sw128(ring + L::kRope * L::kStage, 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(ring + 4 * L::kStage, 1024, 4096);
             const uint64_t q_desc = smem_desc_sw128(q_u32, 16, 1024), p_desc = smem_desc_sw128(p_u32, 16, 1024);
-            const uint32_t ask_other = pair_at(bar_tail, 1);
-            int n = 0;
-            uint32_t g = 0, unit = 0, tails = 0;
+            const uint32_t ask_other = pair_at(bar_tail, 1), pv_other = pair_at(bar_pv, 1);
+            const uint32_t verdict_other = pair_at(smem_u32((const void *)verdict), 1);
+            uint32_t g = 0, unit = 0, tails = 0, rounds = 0;
             bool ok = true, started = false;
-            // P V of tile number gt; has_tail: its last block's end is zeroed first
-            auto pv = [&](uint32_t gt, int nblk, bool has_tail) {
-                ok = wait_one(bar_p, gt & 1);
-                if (!ok) return;
+            // P V of tile number gt; tail_of: the slot whose last block's end is zeroed first
+            auto pv = [&](uint32_t gt, int tail_of) {
+                for (;;) {
+                    ok = wait_one(bar_p, rounds & 1);
+                    pair_acquired(bar_p, rounds++ & 1);
+                    if (!ok) return;
+                    if (*raise == 0) break;
+                    *raise = 0;
+                    *verdict = (int)rounds;
+                    st_cluster_u32(verdict_other, rounds);
+                    pair_arrive_release(pv_other);
+                    mbar_arrive(bar_pv);
+                }
                 const uint32_t mask = (uint32_t)tile_mask[gt & 3];
-                const int stages = (nblk + 1) / 2;
-#pragma unroll 1
-                for (int v = 0; v < stages; ++v, ++n) {
-                    const int s = n % S;
-                    ok = wait_one(bar_full + 8 * s, (uint32_t)((n / S) & 1));
-                    if (ok && has_tail && v == stages - 1) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    ok = wait_one(bar_full + 8 * (4 + v), gt & 1);
+                    if (ok && v == tail_of) {
                         mbar_arrive(bar_tail);
                         pair_arrive(ask_other);
                         ok = wait_one(bar_tail + 8, tails++ & 1);
@@ -380,16 +439,16 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                     tc_fence_after();
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
+                        constexpr int kQuad = L::kPChunk >> 4;
                         const int blk = 2 * v + j;
                         if ((mask >> blk) & 1u) {
-                            const uint64_t a = p_desc + (uint32_t)((blk >> 2) * (L::kPChunk >> 4) + 2 * (blk & 3));
-                            const uint64_t b = v_desc + (uint32_t)((s * L::kStage + j * 8192) >> 4);
+                            const uint64_t a = v_desc + ((v * L::kStage + j * 8192) >> 4), b = p_desc + (blk >> 2) * kQuad + 2 * (blk & 3);
                             tc_mma_ss2(tm_o, a, b, kIdO, started);
-                            tc_mma_ss2(tm_o + 128, a, b + (2048 >> 4), kIdO, started);
+                            tc_mma_ss2(tm_o + 128, a + (2048 >> 4), b, kIdO, started);
                             started = true;
                         }
                     }
-                    tc_commit2_both(bar_empty + 8 * s);
+                    tc_commit2_both(bar_empty + 8 * (4 + v));
                 }
                 tc_commit2_both(bar_pv);
             };
@@ -397,40 +456,35 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             while (ok && walk.next(p, sg)) {
                 ok = wait_one(bar_qfull, unit & 1);
                 ++unit;
-                const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
                 for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
                     const uint32_t d = tm_s + 64 * (g & 1);
-#pragma unroll 1
-                    for (int c = 0; c < 5; ++c, ++n) {
-                        const int s = n % S;
-                        ok = wait_one(bar_full + 8 * s, (uint32_t)((n / S) & 1));
+#pragma unroll
+                    for (int c = 0; c < 4 && ok; ++c) {
+                        ok = wait_one(bar_full + 8 * c, g & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t at = (uint32_t)((s * L::kStage) >> 4);
-                        const uint64_t a = q_desc + (uint32_t)(2 * c * (L::kQChunk >> 4));
-                        if (c < 4) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                tc_mma_ss2(d, a + (k >> 2) * (L::kQChunk >> 4) + 2 * (k & 3), k_desc + at + (k >> 2) * (1024 >> 4) + 2 * (k & 3), kIdS,
-                                           c + k > 0);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) tc_mma_ss2(d, a + 2 * k, r_desc + at + 2 * k, kIdS, 1);
+                        for (int k = 0; k < 8; ++k) {
+                            const int q = ((2 * c + (k >> 2)) * L::kQChunk >> 4) + 2 * (k & 3), at = ((c * L::kStage + (k >> 2) * 1024) >> 4) + 2 * (k & 3);
+                            tc_mma_ss2(d, q_desc + q, k_desc + at, kIdS, c + k > 0);
                         }
-                        tc_commit2_both(bar_empty + 8 * s);
+                        tc_commit2_both(bar_empty + 8 * c);
                     }
+                    if (ok) ok = wait_one(bar_full + 8 * L::kRope, g & 1);
                     if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc_mma_ss2(d, q_desc + (8 * L::kQChunk >> 4) + 2 * k, r_desc + 2 * k, kIdS, 1);
+                    tc_commit2_both(bar_empty + 8 * L::kRope);
                     tc_commit2_both(bar_s + 8 * (g & 1));
                     if (t + 1 == sg.t1) tc_commit2_both(bar_qfree);
-                    if (t > sg.t0) pv(g - 1, L::kBlocks, false);
+                    if (t > sg.t0) pv(g - 1, -1);
                     else started = false;
                 }
-                if (ok) pv(g - 1, min(L::kBlocks, nb - (sg.t1 - 1) * L::kBlocks), sg.t1 == sg.tiles && sg.ctx % kBlockSize > 0);
+                const int blk_in_tile = sg.ctx / kBlockSize - (sg.tiles - 1) * L::kBlocks;
+                if (ok) pv(g - 1, sg.t1 == sg.tiles && sg.ctx % kBlockSize > 0 ? blk_in_tile >> 1 : -1);
             }
-            if (!ok) {
-                if (!*abort_flag) set_flag(p.err_flag, PKV_FLAG_TIMEOUT);
-                *abort_flag = 1;
-            }
+            if (!ok) give_up_one();
         }
         __syncwarp();
     } else {
@@ -439,95 +493,138 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
         const int r = 32 * group + lane;              // row of the CTA
         const int tok0 = 64 * side + 32 * h;          // this thread's tokens of a tile
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const uint32_t ready = pair_at(bar_p, 0);
+        const uint32_t ready = pair_at(bar_p, 0), raise_there = pair_at(smem_u32((const void *)raise), 0);
+        const uint32_t x_there = pair_at(bar_x, rank ^ 1), factor_there = pair_at(smem_u32(factor), rank ^ 1);
         const uint32_t p_row = p_u32 + side * L::kPChunk + r * 128;
         float *const quarter_at = quarters + r;
-        uint32_t g = 0;
+        uint32_t g = 0, rounds = 0, swaps = 0;
         bool ok = true;
+        auto wait_for = [&](uint32_t bar, uint32_t parity) {
+            if (ok) ok = wait(bar, parity);
+            if (!ok) give_up();
+        };
+        // A value for each row of this CTA into both CTAs' factors.
+        auto exchange = [&](float v) {
+            if (side + h == 0) {
+                factor[64 * rank + r] = v;
+                st_cluster_u32(factor_there + (64 * rank + r) * 4, __float_as_uint(v));
+                __syncwarp();
+                if (lane == 0) pair_arrive_release(x_there);
+            }
+            if (lane == 0) mbar_arrive(bar_x);
+            wait_for(bar_x, swaps & 1);
+            pair_acquired(bar_x, swaps++ & 1);
+        };
         LatentSegment sg;
         while (ok && walk.next(p, sg)) {
             const int row0 = sg.chunk * 128 + rank * L::kRows;  // first row of this CTA within the sequence
             const bool real = row0 + r < p.rows;
             if (threadIdx.x == 0 && rank == 0 && sg.t0 == 0) {
                 // for the joining launch: the first pair of the unit's parts, and how many there are
-                const int64_t last = sg.start + sg.tiles + latent_unit_cost<L::kTile>() - 1;
+                const int64_t last = sg.start + sg.tiles + kLatentUnitCost - 1;
                 const int parts = sg.whole ? 1 : (int)(((last + 1) * pairs - 1) / total) - pair + 1;
                 p.unit_parts[(int64_t)sg.b * p.chunks + sg.chunk] = make_int2(pair, parts);
             }
             const int limit = real ? sg.ctx - p.T + (row0 + r) / p.N + 1 : 0;  // tokens the row sees
-            float m = -FLT_MAX, l = 0.f;
-            // The barriers below count all four warps of a group, so a warp whose wait gave up leaves only where
-            // all four agree on it, at the votes that open a tile and the outputs.
-            bool left = false;
-            for (int t = sg.t0; t < sg.t1; ++t, ++g) {
-                if (ok) ok = wait(bar_s + 8 * (g & 1), (g >> 1) & 1);
-                if (!ok) give_up();
-                left = half_any(group, !ok);
-                if (left) break;
-                tc_fence_after();
-                float x[32];
-                tmem_load32(lanes + tm_s + 64 * (g & 1) + 32 * h, x);
-                const uint32_t mask = (uint32_t)tile_mask[g & 3];
-                if (mask == 0xFFu && sg.ctx - p.T + 1 >= (t + 1) * L::kTile) {  // every row sees the whole tile
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] *= p.scale_log2;
-                } else {
-                    const int left_of = limit - (t * L::kTile + tok0);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        x[c] = c < left_of && ((mask >> ((tok0 + c) / kBlockSize)) & 1u) ? x[c] * p.scale_log2 : -INFINITY;
+            // The first tile sets the rows' references.  Where a later one exceeds them by too much, the MMA thread refuses the
+            // round of weights: both CTAs then scale the sums of the rows concerned and make the tile's weights again.  That is
+            // learned with the wait for the product, so after the next tile's weights were made: those are dropped.
+            // The warps of a group leave together: one that gives up goes to a vote, and the others meet it at their next.
+            float m = -FLT_MAX, l = 0.f, l_here = 0.f, l_before = 0.f;  // l ahead of this tile, and of the last
+            bool left = false, first = true, redo = false, clear = true;
+            for (int t = sg.t0;;) {
+                if (t < sg.t1) wait_for(bar_s + 8 * (g & 1), (g >> 1) & 1);
+                if (first || redo || !ok) {
+                    left = half_any(group, !ok);
+                    if (left) break;
                 }
                 float hi = -INFINITY;
+                uint32_t w[16];
+                bool over = false;
+                if (t < sg.t1) {
+                    tc_fence_after();
+                    float x[32];
+                    tmem_load32(lanes + tm_s + 64 * (g & 1) + 32 * h, x);
+                    const uint32_t mask = (uint32_t)tile_mask[g & 3];
+                    if (mask == 0xFFu && sg.ctx - p.T + 1 >= (t + 1) * L::kTile) {  // every row sees the whole tile
 #pragma unroll
-                for (int c = 0; c < 32; ++c) hi = fmaxf(hi, x[c]);
-                if (half_any(group, hi - m > kLatRescale)) {
-                    quarter_at[64 * (side + 2 * h)] = hi;
-                    half_sync(group);
-                    hi = fmaxf(fmaxf(quarter_at[0], quarter_at[64]), fmaxf(quarter_at[128], quarter_at[192]));
-                    const bool up = hi - m > kLatRescale;
-                    const float factor = up ? exp2_sfu(m - hi) : 1.f;
-                    if (up) m = hi;
-                    l *= factor;
-                    if (t > sg.t0) {
-                        ok = wait(bar_pv, (g - 1) & 1);
-                        tc_fence_after();
+                        for (int c = 0; c < 32; ++c) x[c] *= p.scale_log2;
+                    } else {
+                        const int left_of = limit - (t * L::kTile + tok0);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            x[c] = c < left_of && ((mask >> ((tok0 + c) / kBlockSize)) & 1u) ? x[c] * p.scale_log2 : -INFINITY;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) hi = fmaxf(hi, x[c]);
+                    if (first || redo) {
+                        quarter_at[64 * (side + 2 * h)] = hi;
+                        half_sync(group);
+                        hi = fmaxf(fmaxf(quarter_at[0], quarter_at[64]), fmaxf(quarter_at[128], quarter_at[192]));
+                        const bool up = hi - m > kPairRescale;  // as the weights ask, or a round could end where it began
+                        const float f = up ? exp2_sfu(m - hi) : 1.f;
+                        if (up) m = hi;
+                        if (redo) {
+                            l = l_before * f;
+                            exchange(f);
+                            left = half_any(group, !ok);
+                            if (left) break;
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 128; c += 32) {
-                            float o[32];
-                            const uint32_t at = lanes + tm_o + 128 * h + c;
-                            tmem_load32(at, o);
-                            uint32_t w[2][16];
+                            for (int c = 0; c < 128 && t > sg.t0; c += 16) {
+                                uint32_t o[16];
+                                const uint32_t at = lanes + tm_o + 128 * h + c;
+                                tmem_ld16(at, o);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) w[k / 16][k % 16] = __float_as_uint(o[k] * factor);
-                            tmem_st16(at, w[0]);
-                            tmem_st16(at + 16, w[1]);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor[c + k]);
+                                tmem_st16(at, o);
+                            }
+                            tmem_st_wait();
                         }
-                        tmem_st_wait();
+                        first = redo = false;
+                    }
+                    over = hi - m > kPairRescale;
+                    // weights: rounded to bf16 for the product, summed as they are
+                    l_here = l;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float a = exp2_sfu(x[c] - m), b = exp2_sfu(x[c + 1] - m);
+                        w[c / 2] = pack_bf16x2(a, b);
+                        l += a + b;
                     }
                 }
-                // weights: rounded to bf16 for the product, summed as they are
-                uint32_t w[16];
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const float a = exp2_sfu(x[c] - m), b = exp2_sfu(x[c + 1] - m);
-                    w[c / 2] = pack_bf16x2(a, b);
-                    l += a + b;
+                if (!clear) {
+                    // the product of the last tile, unless its weights were refused
+                    wait_for(bar_pv, rounds & 1);
+                    pair_acquired(bar_pv, rounds++ & 1);
+                    if (!ok) {
+                        half_any(group, true);
+                        left = true;
+                        break;
+                    }
+                    if ((uint32_t)*verdict == rounds) {
+                        --t, --g;
+                        redo = clear = true;
+                        continue;
+                    }
                 }
-                if (g > 0) ok = wait(bar_pv, (g - 1) & 1) && ok;  // the last tile's weights are no longer needed
-                if (!ok) give_up();
+                if (t == sg.t1) break;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
                     st_shared_v4(p_row + (((4 * h + u) ^ (r & 7)) << 4), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
                 fence_proxy_async_shared();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) pair_arrive(ready);
+                if (__any_sync(0xFFFFFFFFu, over) && lane == 0) {
+                    st_cluster_u32(raise_there, 1u);
+                    pair_fence();
+                }
+                if (lane == 0) pair_arrive(ready);
+                l_before = l_here, clear = false;
+                ++t, ++g;
             }
-            if (!left) {
-                if (ok) ok = wait(bar_pv, (g - 1) & 1);
-                if (!ok) give_up();
-                left = half_any(group, !ok);
-            }
+            if (!left) left = half_any(group, false);
             if (left) {
                 ok = false;
                 break;
@@ -537,48 +634,52 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             half_sync(group);
             const float all = (quarter_at[0] + quarter_at[64]) + (quarter_at[128] + quarter_at[192]);
             const bool seen = all != 0.f;  // (NaN is something)
-            const float inv = seen ? 1.f / all : 0.f;
-            const int64_t part = (int64_t)(2 * pair + (sg.t0 == 0)) * 128 + rank * L::kRows + r;  // row of the workspace
-            const int64_t row = (int64_t)sg.b * p.rows + row0 + r;
+            const int64_t part = (int64_t)(2 * pair + (sg.t0 == 0)) * 128;  // rows of the workspace
+            const int64_t first_row = (int64_t)sg.b * p.rows + sg.chunk * 128;
+            exchange(seen ? 1.f / all : 0.f);
+            left = half_any(group, !ok);
+            if (left) {
+                ok = false;
+                break;
+            }
             if (side + h == 0 && real) {
                 const float lse2 = seen ? m + log2f(all) : -INFINITY;
-                if (!sg.whole) p.part_lse[part] = lse2;
-                else if (p.lse_out) p.lse_out[row] = lse2 * 0.69314718055994530942f;
+                if (!sg.whole) p.part_lse[part + rank * L::kRows + r] = lse2;
+                else if (p.lse_out) p.lse_out[first_row + rank * L::kRows + r] = lse2 * 0.69314718055994530942f;
             }
-            // Outputs.  A thread has a row's elements, its lanes' rows lie 1 or 2 KB apart: 16 elements of 32 rows at a time go
-            // through the group's part of P (2 KB a warp, 16-byte units swizzled by row), so that a store covers whole sectors of
-            // eight rows (straight from the registers a unit's outputs took 10,500 clocks; a ragged batch of 64 with 128 heads 102 -> 99 us).
-            const int h0 = 256 * side + 128 * h;
-            const uint32_t stage = p_u32 + group * 4096 + side * L::kPChunk + h * 2048;
-            const int64_t part0 = part - lane, row_first = row - lane;
-            const int rows_here = min(32, p.rows - (row0 + 32 * group));
+            // Outputs.  A lane has an element of all rows: 16 rows of 32 elements at a time go through 2 KB of P, so that
+            // a store covers whole lines.
+            const int h0 = 256 * rank + 128 * h + 32 * quarter, nrows = min(128, p.rows - sg.chunk * 128);
+            const uint32_t stage = p_u32 + group * 4096 + side * L::kPChunk + h * 2048;  // (the group's own)
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
+            for (int c = 0; c < nrows; c += 16) {
                 uint32_t o[16];
                 tmem_ld16(lanes + tm_o + 128 * h + c, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = seen ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(factor + c + k);
+                    const float inv[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    st_shared_v4(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+                    for (int e = 0; e < 4; ++e) o[k + e] = inv[e] == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k + e]) * inv[e]);
+                }
+                if (!sg.whole) {
+                    float *const to = p.part_out + (part + c) * kLatentDim + h0 + lane;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (c + k < nrows) to[k * kLatentDim] = __uint_as_float(o[k]);
+                    continue;
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) st_shared_u32(stage + k * 128 + lane * 4, o[k]);
                 __syncwarp();
-                if (sg.whole) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int rr = 16 * k + (lane >> 1), u = 2 * (lane & 1), x = (rr >> 1) & 3;
-                        const float4 a = ld_shared_f4(stage + rr * 64 + ((u ^ x) << 4)), b = ld_shared_f4(stage + rr * 64 + (((u + 1) ^ x) << 4));
-                        if (rr < rows_here)
-                            *reinterpret_cast<uint4 *>(p.out + (row_first + rr) * kLatentDim + h0 + c + 4 * u) =
-                                make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int rr = 8 * k + (lane >> 2), u = lane & 3;
-                        const float4 v = ld_shared_f4(stage + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4));
-                        if (rr < rows_here) *reinterpret_cast<float4 *>(p.part_out + (part0 + rr) * kLatentDim + h0 + c + 4 * u) = v;
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const int rr = 8 * k + (lane >> 2), e = 8 * (lane & 3);
+                    const float4 a = ld_shared_f4(stage + rr * 128 + e * 4), b = ld_shared_f4(stage + rr * 128 + e * 4 + 16);
+                    if (c + rr < nrows)
+                        *reinterpret_cast<uint4 *>(p.out + (first_row + c + rr) * kLatentDim + h0 + e) =
+                            make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
                 }
                 __syncwarp();
             }
@@ -615,11 +716,11 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                                  : "memory");
                 if (both_arrive && other_number != last) mbar_arrive(bar);
             };
-            for (int s = 0; s < S; ++s) {
+            for (int s = 0; s < L::kStages; ++s) {
                 const int mine = use[s], theirs = load_word(use + s, 1);
                 settle(bar_full + 8 * s, mine, sent[s], theirs, load_word(sent + s, 1), want[s], true);
                 const int last = max(mine, theirs);
-                if (last > 0) mbar_wait_bounded(bar_full + 8 * s, (uint32_t)(((last - 1) / S) & 1), nullptr, kDrainLimitNs);
+                if (last > 0) mbar_wait_bounded(bar_full + 8 * s, (uint32_t)((last - 1) & 1), nullptr, kDrainLimitNs);
             }
             const int mine = *q_asked, theirs = load_word(q_asked, 1), last = max(mine, theirs);
             settle(bar_qfull, mine, L::kQBytes, theirs, L::kQBytes, 2 * L::kQBytes, false);

@@ -339,3 +339,29 @@ def test_around_48_rows(pkv, N, T):
     c.check(*c.run(pkv))
     c = Case(N, [9000, 70, 0, 3333], N, T).poison()
     c.check(*c.run(pkv))
+
+
+@pytest.mark.parametrize("N,T", [(128, 1), (70, 1), (40, 5), (16, 1), (32, 1)])
+@pytest.mark.parametrize("ctx", [[5000, 700, 129, 40, 300], [257, 256, 384, 1], [12000]], ids=str)
+def test_logits_that_jump_far_above_the_maximum_so_far(pkv, N, T, ctx):
+    """Now and then a token's logits exceed all before it by hundreds, for some rows and not for others: sums already made are
+    scaled down, again and again, in the first tile, the last, and where a sequence is cut."""
+    c = Case(N + len(ctx), ctx, N, T, spread=0.02)
+    r = c.r
+    q, cache = R.bf16_values(c.q).copy(), R.bf16_values(c.cache).copy() * 0.5
+    q[..., 0] = r.choice([0.0, 1.0, 1.0, -1.0, 0.25], q.shape[:-1])
+    q[..., 1] = r.choice([0.0, 0.0, 1.0], q.shape[:-1])
+    for b, n in enumerate(ctx):
+        level, side = -400.0, -300.0
+        for j in range(n):
+            level += (r.random() < 0.01) * r.integers(20, 200)
+            side += (r.random() < 0.004) * r.integers(20, 200)
+            row = cache[c.tab[b, j // 16], j % 16]
+            row[0], row[1] = level, side
+        cache[c.tab[b, (n - 1) // 16], (n - 1) % 16, 0] = 2000.0           # the very last token above all
+    c.q, c.cache, c.scale = R.to_bf16(q), R.to_bf16(cache), 1.0
+    c.poison()
+    first = c.run(pkv)
+    c.check(*first)
+    again = c.run(pkv)
+    assert same(first[0], again[0]) and same(first[1], again[1])
