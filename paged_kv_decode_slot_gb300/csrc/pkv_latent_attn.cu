@@ -557,8 +557,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 // at once where the unit was not cut; it also writes the rows of sequences without tokens, which no CTA of the attention has.
 // Warps compute the rows' weights, then 128 threads take a row's elements, four each, and kGroups such groups the rows, or
 // the parts of the one row.  Few rows are cut into many parts (one sequence over the whole GPU into up to 152): one row a
-// CTA, four groups that take every fourth part (one sequence of 128K tokens 63 -> 55 us against one group).  Rows of larger
-// batches are cut into two or three if at all: four rows a CTA (64 sequences of 128 rows 99 -> 94 us against a row a CTA at a time).
+// CTA, eight groups that take every eighth part (one sequence of 128K tokens: one group 63 us, four 45.9, eight 43.8).  Rows of
+// larger batches are cut into two or three if at all: two rows a CTA while the CTAs run at once (5 short sequences of 128 heads
+// 23.8 us, four rows 26.6, eight 29.8), then eight, the fewest CTAs (152 sequences of 4,096 tokens 133.7 us, four rows 136.3, two
+// 141.8; 200 short ones 37.7, 41.0, 47.2).
 template <int kRows, int kGroups>
 __global__ void __launch_bounds__(kGroups * kLatentDim / 4) latent_join_kernel(const LatentAttnParams p, int chunk_rows)
 {
@@ -652,11 +654,13 @@ __global__ void __launch_bounds__(kGroups * kLatentDim / 4) latent_join_kernel(c
 
 cudaError_t launch_latent_join(const LatentAttnParams &p, int chunk_rows, int sms, cudaStream_t stream)
 {
-    const int64_t units = (int64_t)p.B * p.chunks;
-    if (units * chunk_rows <= 4 * (int64_t)sms)
-        return launch_kernel(latent_join_kernel<1, 4>, dim3((unsigned)(units * chunk_rows)), dim3(kLatentDim), 0, stream, true, p, chunk_rows);
-    return launch_kernel(latent_join_kernel<4, 2>, dim3((unsigned)(units * (chunk_rows / 4))), dim3(kLatentDim / 2), 0, stream, true, p,
-                         chunk_rows);
+    const int64_t rows = (int64_t)p.B * p.chunks * chunk_rows;
+    const auto launch = [&](auto kernel, int rows_a_cta, int groups) {
+        return launch_kernel(kernel, dim3((unsigned)(rows / rows_a_cta)), dim3(groups * kLatentDim / 4), 0, stream, true, p, chunk_rows);
+    };
+    if (rows <= 4 * (int64_t)sms) return launch(latent_join_kernel<1, 8>, 1, 8);
+    if (rows <= 32 * (int64_t)sms) return launch(latent_join_kernel<2, 2>, 2, 2);
+    return launch(latent_join_kernel<8, 2>, 8, 2);
 }
 
 template <int R>
