@@ -6,8 +6,11 @@
 // from its inputs alone, whatever ran before and however the work is split.  Everything is integers and exact.
 //
 // What bounds these: a scan of the counts (4 bytes a block: 0.4 MB for 100,000 blocks) and the table entries that change,
-// both from L2; the rest is the latency of a launch and of a few barriers.  Scans run as one cluster of eight CTAs, whose
-// totals meet in shared memory, rather than as a grid that would have to be launched twice or count itself.
+// both from L2; the rest is the latency of a launch, of dependent loads and of a few barriers.  Scans run as one CTA or, of many
+// blocks, as one cluster of eight, whose totals meet in shared memory, rather than as a grid that would have to be launched
+// twice or count itself.  Measured inside CUDA graphs: 64 rows extended over 21,797 blocks 7.4 us, 250 rows of up to 700 new
+// tokens over 68,943 blocks 15.8; 64 beams forked 4.8 us, 250 rows of 1,001 to 2,033 blocks 10.0;
+// the plan of 20 rows' moves among 10,898 blocks 10 us with the tables' entries; copies 6.0 TB/s, 88% of a plain copy's rate.
 #include <limits.h>
 
 #include "pkv_cluster.cuh"
