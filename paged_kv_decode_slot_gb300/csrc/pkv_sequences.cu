@@ -8,8 +8,8 @@
 // What bounds these: a scan of the counts (4 bytes a block: 0.4 MB for 100,000 blocks) and the table entries that change,
 // both from L2; the rest is the latency of a launch, of dependent loads and of a few barriers.  Scans run as one CTA or, of many
 // blocks, as one cluster of eight, whose totals meet in shared memory, rather than as a grid that would have to be launched
-// twice or count itself.  Measured inside CUDA graphs: 64 rows extended over 21,797 blocks 7.4 us, 250 rows of up to 700 new
-// tokens over 68,943 blocks 15.8; 64 beams forked 4.8 us, 250 rows of 1,001 to 2,033 blocks 10.0;
+// twice or count itself.  Measured inside CUDA graphs: 64 rows extended over 21,797 blocks 6.4 us, 250 rows of up to 700 new
+// tokens over 68,943 blocks 13.9; 64 beams forked 4.8 us, 250 rows of 1,001 to 2,033 blocks 10.0;
 // the plan of 20 rows' moves among 10,898 blocks 10 us with the tables' entries; copies 6.0 TB/s, 88% of a plain copy's rate.
 #include <limits.h>
 
@@ -195,24 +195,29 @@ __device__ __forceinline__ void scan_sync()
     else __syncthreads();
 }
 
-// The value that every CTA published in `word` before a barrier, summed before this one and over all.  Whole warps; the CTAs'
-// words are read by a lane each (one after the other they take 0.1 us a word).
-template <int kCtas>
-__device__ __forceinline__ void cluster_before(const long long *word, int rank, long long &before, long long &all)
+// The values that every CTA published in `words` before a barrier, each summed before this one and over all.  Whole warps; a
+// word's CTAs are read by a lane each (one after the other they take 0.1 us a word), the words' reads are under way at once.
+template <int kCtas, int kWords>
+__device__ __forceinline__ void cluster_before(const long long *words, int rank, long long (&before)[kWords], long long (&all)[kWords])
 {
     if constexpr (kCtas == 1) {
-        before = 0, all = *word;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) before[w] = 0, all[w] = words[w];
     } else {
         const int lane = threadIdx.x & 31;
-        all = lane < kCtas ? load_cluster<long long>(smem_u32(word), lane) : 0;
-        before = lane < rank ? all : 0;
 #pragma unroll
-        for (int o = kCtas / 2; o; o >>= 1) {
-            all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-            before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        for (int w = 0; w < kWords; ++w) all[w] = lane < kCtas ? load_cluster<long long>(smem_u32(words + w), lane) : 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            before[w] = lane < rank ? all[w] : 0;
+#pragma unroll
+            for (int o = kCtas / 2; o; o >>= 1) {
+                all[w] += __shfl_xor_sync(0xFFFFFFFFu, all[w], o);
+                before[w] += __shfl_xor_sync(0xFFFFFFFFu, before[w], o);
+            }
+            all[w] = __shfl_sync(0xFFFFFFFFu, all[w], 0);
+            before[w] = __shfl_sync(0xFFFFFFFFu, before[w], 0);
         }
-        all = __shfl_sync(0xFFFFFFFFu, all, 0);
-        before = __shfl_sync(0xFFFFFFFFu, before, 0);
     }
 }
 
@@ -233,6 +238,8 @@ __device__ __forceinline__ int scan_rank()
 //
 // A thread keeps its row's state in registers (`per` is 1 up to 8,192 rows) or in the row's entry of `copies`, which also
 // tells the warps of rows with many fresh blocks: (block to copy, or one of the marks below; first rank of its fresh blocks).
+// The last barrier is the one behind which free blocks are known: threads and warps then hand them out side by side (with
+// states in registers; 250 rows over 68,943 blocks 14.6 -> 13.9 us against one barrier more).
 constexpr int kNoCopy = -1, kKeeps = -2, kIdle = -3;
 constexpr int kWaits = INT_MIN;  // + 1 + the block to copy: a row whose fresh blocks a warp hands out
 constexpr int kFewBlocks = 4;  // fresh blocks that a row's own thread writes; more are a warp's work
@@ -270,7 +277,7 @@ template <int kCtas>
 __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendParams p)
 {
     __shared__ int sums[kScanWarps];
-    __shared__ long long free_here, need_here, many_here;
+    __shared__ long long here[3];  // free blocks of this CTA's range, blocks its rows need, whether one needs many
     __shared__ long long warp_need[kScanWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = scan_rank<kCtas>();
     const PairList state{p.copies};
@@ -284,10 +291,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
     auto get = [&](int row) { return one ? mine_state : state.get(row); };
     auto put = [&](int row, int2 s) { if (one) mine_state = s; else state.put(row, s); };
     auto grow = [&](int row) { return one ? mine_row : grow_row(p, row); };
-    if (tid == 0) many_here = 0;
+    if (tid == 0) here[2] = 0;
     pdl_wait_primary();
     pdl_launch_dependents();
 
+    // (of the first row whose blocks this warp may hand out, while there is time)
+    const int row0 = rank * kScanWarps + warp;
+    GrowRow first_row = {};
+    if (row0 < p.rows) first_row = grow_row(p, row0);
     for (int row = rb; row < re; ++row) {
         const int t = p.num_new[row], ctx = p.context_lens[row];
         int2 s = make_int2(kIdle, 0);
@@ -328,11 +339,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
             if (__ldcg(p.ref_counts + id) == -(row + 1)) put(row, make_int2(kKeeps, id));
             else ++need;
         }
-        if (g.then - g.now >= kFewBlocks) many_here = 1;
+        if (g.then - g.now >= kFewBlocks) here[2] = 1;
     }
     int all;
     const int free_in_cta = cta_warps_before(mine, sums, all);
-    if (tid == 0) free_here = all;
+    if (tid == 0) here[0] = all;
     // rows' needs: exclusive over the threads, 64-bit
     long long upto = need;
 #pragma unroll
@@ -350,33 +361,36 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
             if (lane >= o) s += up;
         }
         warp_need[lane] = s - v;
-        if (lane == 31) need_here = s;
+        if (lane == 31) here[1] = s;
     }
     scan_sync<kCtas>();  // (also this CTA's barrier) every row has decided; the totals are there
-    long long free_before, free_all, need_before, need_all;
-    cluster_before<kCtas>(&free_here, rank, free_before, free_all);
-    cluster_before<kCtas>(&need_here, rank, need_before, need_all);
-    long long many_before, many;
-    cluster_before<kCtas>(&many_here, rank, many_before, many);
-    long long at = need_before + warp_need[warp] + upto - need;
+    long long before_here[3], all_of[3];
+    cluster_before<kCtas>(here, rank, before_here, all_of);
+    const long long free_all = all_of[0], need_all = all_of[1];
+    long long at = before_here[1] + warp_need[warp] + upto - need;
     for (int row = rb; row < re; ++row) {
         const int2 s = get(row);
-        if (s.x == kIdle) continue;
-        const GrowRow g = grow(row);
-        if (s.x == kKeeps) p.ref_counts[s.y] = 1;
-        const long long n = g.then - g.now + (s.x >= 0);
-        if (at + n <= free_all) {
-            put(row, make_int2(s.x == kKeeps ? kNoCopy : s.x, (int)at));
-        } else {
-            set_flag(p.err_flag, PKV_FLAG_NO_BLOCKS);
-            // its block, if it was to leave it, has its holder back (behind the barrier: the keeper sets it to 1 here)
-            put(row, make_int2(s.x >= 0 ? s.x : kIdle, -1));
+        int2 now = make_int2(kIdle, 0);
+        if (s.x != kIdle) {
+            const GrowRow g = grow(row);
+            if (s.x == kKeeps) p.ref_counts[s.y] = 1;
+            const int cow_of = s.x >= 0 ? s.x : kNoCopy;
+            const long long n = g.then - g.now + (s.x >= 0);
+            if (at + n <= free_all) {
+                now = make_int2(n > kFewBlocks ? kWaits + 1 + cow_of : cow_of, (int)at);
+            } else {
+                set_flag(p.err_flag, PKV_FLAG_NO_BLOCKS);
+                // its block, if it was to leave it, has its holder back (behind the barrier: the keeper sets it to 1 here)
+                now = make_int2(s.x >= 0 ? s.x : kIdle, -1);
+            }
+            at += n;
+            put(row, now);
         }
-        at += n;
+        if (one) state.put(row, now.x < kIdle ? now : make_int2(-1, -1));  // (what the warps look for)
     }
     // the free blocks that are needed, in order
     const long long wanted = need_all < free_all ? need_all : free_all;
-    long long base = free_before + free_in_cta;
+    long long base = before_here[0] + free_in_cta;
     for (int b = range.begin; b < range.end && base < wanted; b += 128) {
         unsigned free[4];
         scan_free(p.ref_counts, b, range.end, free);
@@ -391,6 +405,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
     // hand them out: few a row by its own thread ..
     for (int row = rb; row < re; ++row) {
         const int2 s = get(row);
+        if (s.x < kIdle) continue;
         if (s.x == kIdle || s.y < 0) {
             if (s.x >= 0) atomicAdd(p.ref_counts + s.x, 1);
             state.put(row, make_int2(-1, -1));
@@ -398,22 +413,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
         }
         const GrowRow g = grow(row);
         const int cow = s.x >= 0, n = g.then - g.now + cow;
-        if (n > kFewBlocks) {
-            state.put(row, make_int2(kWaits + 1 + s.x, s.y));
-        } else {
-            if (!cow) state.put(row, make_int2(-1, -1));
-            give_blocks(p, row, g.now - cow, n, s.y, 0, 1, s.x);
-            p.context_lens[row] = g.ctx + p.num_new[row];
-        }
+        if (!cow) state.put(row, make_int2(-1, -1));
+        give_blocks(p, row, g.now - cow, n, s.y, 0, 1, s.x);
+        p.context_lens[row] = g.ctx + p.num_new[row];
     }
-    if (many == 0) return;
-    scan_sync<kCtas>();
+    if (all_of[2] == 0) return;
+    if (!one) scan_sync<kCtas>();  // a row's own thread still reads its state where a warp leaves the pair to copy
     // .. many by a warp
-    for (int row = rank * kScanWarps + warp; row < p.rows; row += kCtas * kScanWarps) {
+    for (int row = row0; row < p.rows; row += kCtas * kScanWarps) {
         const int2 s = state.get(row);
         if (s.x >= kIdle) continue;
         const int cow_of = s.x - kWaits - 1, cow = cow_of >= 0;
-        const GrowRow g = grow_row(p, row);
+        const GrowRow g = row == row0 ? first_row : grow_row(p, row);
         const int t = p.num_new[row];
         __syncwarp();
         if (lane == 0 && !cow) state.put(row, make_int2(-1, -1));
@@ -447,9 +458,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) plan_moves_kernel(const Compa
     const int in_cta = cta_warps_before(mine, sums, all);
     if (tid == 0) used_here = all, above_here = 0;
     scan_sync<kCtas>();
-    long long before, used;
-    cluster_before<kCtas>(&used_here, rank, before, used);
-    long long base = before + in_cta;  // used blocks below this warp's range
+    long long before[1], used_of[1];
+    cluster_before<kCtas>(&used_here, rank, before, used_of);
+    const long long used = used_of[0];
+    long long base = before[0] + in_cta;  // used blocks below this warp's range
     int above = 0;                     // used blocks from U on
     for (int b = range.begin; b < range.end; b += 128) {
         unsigned free[4];
@@ -475,9 +487,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) plan_moves_kernel(const Compa
     above = __reduce_add_sync(0xFFFFFFFFu, above);
     if (lane == 0 && above) atomicAdd(reinterpret_cast<unsigned long long *>(&above_here), (unsigned long long)above);
     scan_sync<kCtas>();
-    long long unused, total;
-    cluster_before<kCtas>(&above_here, rank, unused, total);
-    const int n = (int)min(total, (long long)p.max_moves);
+    long long total[1];
+    cluster_before<kCtas>(&above_here, rank, before, total);
+    const int n = (int)min(total[0], (long long)p.max_moves);
     if (rank == 0 && tid == 0) *p.num_moves = n;
     for (int k = rank * kScanThreads + tid; k < p.max_moves; k += kCtas * kScanThreads) {
         if (k >= n) {

@@ -258,3 +258,34 @@ def test_in_a_graph_on_another_stream_and_with_a_workspace_in_use_elsewhere(pkv)
     for a, b in mv[:k]:
         p[int(b)] = p[int(a)]
     assert torch.equal(p, pool)
+
+
+@pytest.mark.parametrize("new", [1, 100, 0])
+def test_extend_more_rows_than_threads(pkv, new):
+    """Several rows a thread: their states are kept in `copies` between the passes."""
+    r = np.random.default_rng(new)
+    rows, width, blocks = 9001, 9, 60000
+    tables, ctx, ref = L.random_rows(r, rows, width, blocks, 0.6)
+    num_new = np.minimum(r.integers(0, new + 1, rows), 16 * width - ctx).astype(np.int32)
+    now = [i32_dev(x) for x in (tables, ctx, ref)]
+    copies, err = torch.full((rows, 2), -2147483648, dtype=torch.int32, device="cuda"), flag()
+    pkv.check(pkv.pkv_extend_sequences(now[0], now[1], i32_dev(num_new), now[2], copies, workspace(pkv, blocks), err))
+    t, c, f, cp, refused = L.extend(tables, ctx, num_new, ref)
+    assert err_of(err) == (pkv.PKV_FLAG_NO_BLOCKS if refused else 0)
+    for g, w in zip((*now, copies), (t, c, f, cp)):
+        np.testing.assert_array_equal(host(g), w)
+
+
+def test_what_copies_held_before_does_not_matter(pkv):
+    """Values as the call itself leaves them meanwhile for its warps."""
+    r = np.random.default_rng(8)
+    tables, ctx, ref = L.random_rows(r, 60, 30, 4000, 0.5)
+    num_new = np.minimum(r.choice([0, 1, 3, 200], 60), 480 - ctx).astype(np.int32)
+    t, c, f, cp, _ = L.extend(tables, ctx, num_new, ref)
+    for fill in (-2147483648, -2147483648 + 5, -3, 0, 7):
+        now = [i32_dev(x) for x in (tables, ctx, ref)]
+        copies, err = torch.full((60, 2), fill, dtype=torch.int32, device="cuda"), flag()
+        pkv.check(pkv.pkv_extend_sequences(now[0], now[1], i32_dev(num_new), now[2], copies, workspace(pkv, 4000), err))
+        assert err_of(err) == 0
+        for g, w in zip((*now, copies), (t, c, f, cp)):
+            np.testing.assert_array_equal(host(g), w)
