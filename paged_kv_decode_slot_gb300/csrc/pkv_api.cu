@@ -880,7 +880,7 @@ constexpr int32_t kMaxCount = INT32_MAX - 65536;
 
 int check_sequences(int32_t max_nb, int32_t num_seqs, int32_t num_blocks)
 {
-    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * 2048 || num_seqs < 0 || num_seqs > kMaxCount ||
+    if (max_nb <= 0 || (int64_t)max_nb * 16 > INT32_MAX || max_nb > 65535 * pkv::kSequenceEntries || num_seqs < 0 || num_seqs > kMaxCount ||
         num_blocks <= 0 || num_blocks > kMaxCount)
         return PKV_ERR_SHAPE;
     return PKV_OK;

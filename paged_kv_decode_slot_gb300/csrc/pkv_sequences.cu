@@ -9,7 +9,7 @@
 // both from L2; the rest is the latency of a launch, of dependent loads and of a few barriers.  Scans run as one CTA or, of many
 // blocks, as one cluster of eight, whose totals meet in shared memory, rather than as a grid that would have to be launched
 // twice or count itself.  Measured inside CUDA graphs: 64 rows extended over 21,797 blocks 6.4 us, 250 rows of up to 700 new
-// tokens over 68,943 blocks 13.9; 64 beams forked 4.8 us, 250 rows of 1,001 to 2,033 blocks 10.0;
+// tokens over 68,943 blocks 13.9; 64 beams forked 4.2 us, 250 rows of 1,001 to 2,033 blocks 8.0;
 // the plan of 20 rows' moves among 10,898 blocks 10 us with the tables' entries; copies 6.0 TB/s, 88% of a plain copy's rate.
 #include <limits.h>
 
@@ -22,7 +22,7 @@ namespace pkv {
 
 // ---- forking --------------------------------------------------------------------------------------
 constexpr int kForkThreads = 256;
-constexpr int kForkEntries = 2048;  // table entries of a CTA
+constexpr int kForkEntries = kSequenceEntries;  // table entries of a CTA (250 rows of up to 2,033: 8.0 us with 512, 8.2 with 1,024, 10.1 with 2,048)
 constexpr int kForkEach = kForkEntries / kForkThreads;
 
 __device__ __forceinline__ int fork_blocks(const ForkParams &p, int row, bool report, int &ctx)

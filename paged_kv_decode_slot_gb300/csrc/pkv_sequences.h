@@ -9,6 +9,7 @@
 namespace pkv {
 
 constexpr int kMaxCopyPools = 256;
+constexpr int kSequenceEntries = 512;  // table entries of a CTA (forks, moved blocks); a row takes up to 65,535 CTAs
 
 struct ForkParams {
     const int32_t *block_tables;   // [rows_in][max_nb]

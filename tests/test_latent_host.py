@@ -152,3 +152,10 @@ def test_counts_near_2_to_the_31_are_refused(lib):
                     ("B", I, 0), ("T", I, 2), ("N", I, 8), ("scale", F, 1.0), ("out", P, FAKE), ("lse", P, None), ("d", Desc, GOOD),
                     ("ws", P, FAKE), ("bytes", Z, 1 << 40), ("err", P, None), ("stream", P, None)])
     assert attend(nb=(2 ** 31 - 1 - 1024) // 16) == 0 and attend(nb=(2 ** 31 - 1 - 1024) // 16 + 1) == -2
+
+
+def test_rows_wider_than_a_grid_are_refused(lib):
+    most = 65535 * 512
+    fork = caller(lib.pkv_fork_sequences, [("bt", P, None), ("nb", I, 1), ("ctx", P, None), ("B", I, 0), ("par", P, None), ("R", I, 0),
+                  ("ref", P, FAKE), ("blocks", I, 9), ("bo", P, None), ("co", P, None), ("err", P, None), ("stream", P, None)])
+    assert fork(nb=most) == 0 and fork(nb=most + 1) == -2
