@@ -712,7 +712,7 @@ int latent_append(pkv::LatentAppendParams &p, bool interleaved, const pkv_cache_
     if (st != PKV_OK) return st;
     if (num_q_heads <= 0 || tokens < 0 || !(p.eps >= 0.f)) return PKV_ERR_SHAPE;
     // warps of the grid, and offsets inside a token, are 32-bit
-    if (tokens > INT32_MAX / 2 || num_q_heads > INT32_MAX / 2048 || tokens * (num_q_heads / 32 + 1) > INT32_MAX) return PKV_ERR_SHAPE;
+    if (tokens > INT32_MAX / 2 || num_q_heads > INT32_MAX / 2048 || tokens * (num_q_heads / 16 + 1) > INT32_MAX) return PKV_ERR_SHAPE;
     if (p.q_rope_token < 0 || p.q_rope_head < 0) return PKV_ERR_SHAPE;
     if (p.q_rope_token % 8 != 0 || p.q_rope_head % 8 != 0 || !aligned(p.kv_new, 16) || !aligned(p.q_rope, 16) ||
         !aligned(p.q, 16) || !aligned(p.cache, 16) || !aligned(p.norm_weight, 16) || !aligned(p.inv_freq, 8) ||

@@ -6,9 +6,9 @@
 // The angle is the fraction of a turn position * inv_freq / 2 pi in 64-bit integers, as in pkv_rope.cu: off by 1e-10 of a
 // turn at position 10^6.  Sums of squares, norms and rotations in fp32, one rounding to bf16 at the end.
 //
-// Bound by memory: a token reads and writes 1,152 + 128 N bytes.  8,192 tokens of 16 heads take 9.3 us (5.7 TB/s), 5,001 of 40
-// heads 9.5 (6.6 TB/s, 98% of a copy's rate; both partly from L2), 64 of 128 heads 3.0, a launch and the chain of length, table and
-// position.  One warp takes a token's row and up to 32 of its heads
+// Bound by memory: a token reads and writes 1,152 + 128 N bytes.  From a cold L2 8,192 tokens of 16 heads take 11.8 us, 5,001 of
+// 40 heads 12.8 (4.9 TB/s, launch and a first wave's loads included; with CTAs of eight warps and fewer of them at once 14.8 and
+// 13.7), 64 of 128 heads 3.1, a launch and the chain of length, table and position.  One warp takes a token's row and up to 32 of its heads
 // (the key counts as one), so that lane j computes pair j's angle once for all of them and nothing waits for other
 // warps: loads (all of them before the slot, the position and the angles are known), two shuffles a pair of elements,
 // stores.  A head is four lanes' work of two 16-byte vectors, half a head apart.
@@ -18,7 +18,7 @@
 
 namespace pkv {
 
-constexpr int kLatAppendWarps = 8;
+constexpr int kLatAppendWarps = 4;                           // seven CTAs an SM: 72 registers
 constexpr int kLatAppendHeads = 32;                          // heads of a warp's job, the key among them
 constexpr int kLatAppendRounds = kLatAppendHeads * 4 / 32;   // of 32 lanes
 constexpr int kLatRow = kLatentDim + kLatentRope;
@@ -36,7 +36,7 @@ __device__ __forceinline__ uint4 latent_pack(const float (&x)[8])
 }
 
 template <bool kInter>
-__global__ void __launch_bounds__(kLatAppendWarps * 32) latent_append_kernel(const LatentAppendParams p, int parts, int per)
+__global__ void __launch_bounds__(kLatAppendWarps * 32, 7) latent_append_kernel(const LatentAppendParams p, int parts, int per)
 {
     __shared__ float2 angles[kLatAppendWarps][kLatentRope / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kLatAppendWarps * 32) latent_append_kernel(con
 
 cudaError_t launch_latent_append(const LatentAppendParams &p, bool interleaved, cudaStream_t stream)
 {
-    const int parts = (p.N + kLatAppendHeads) / kLatAppendHeads, per = (p.N + parts) / parts;
+    // where there are few, half as many a warp: 64 tokens of 128 heads 3.2 -> 3.1 us (250 of 128 3.9 -> 4.4)
+    const int heads = (int64_t)p.n * (p.N + 1) <= 16384 ? kLatAppendHeads / 2 : kLatAppendHeads;
+    const int parts = (p.N + heads) / heads, per = (p.N + parts) / parts;
     const int64_t jobs = (int64_t)p.n * parts;
     const unsigned grid = (unsigned)((jobs + kLatAppendWarps - 1) / kLatAppendWarps);
     return launch_kernel(interleaved ? latent_append_kernel<true> : latent_append_kernel<false>, dim3(grid),
