@@ -10,7 +10,7 @@
 // blocks, as one cluster of eight, whose totals meet in shared memory, rather than as a grid that would have to be launched
 // twice or count itself.  Measured inside CUDA graphs: 64 rows extended over 21,797 blocks 6.4 us, 250 rows of up to 700 new
 // tokens over 68,943 blocks 13.9; 64 beams forked 4.2 us, 250 rows of 1,001 to 2,033 blocks 8.0;
-// the plan of 20 rows' moves among 10,898 blocks 10 us with the tables' entries; copies 6.0 TB/s, 88% of a plain copy's rate.
+// the plan of 20 rows' moves among 10,898 blocks 10 us with the tables' entries; copies 6.5 TB/s, 96% of a plain copy's rate.
 #include <limits.h>
 
 #include "pkv_cluster.cuh"
@@ -544,8 +544,10 @@ cudaError_t launch_compact_blocks(const CompactParams &p, cudaStream_t stream)
 // ---- copies in many pools -----------------------------------------------------------------------------
 // Item k of pairs x pools (pools fastest) copies one block; CTA c takes items c, c + grid, ..  A warp's lanes read the pairs
 // of 32 of them at once, so that the many entries without a copy cost nothing.  Bound by memory: every copied block is read
-// and written once.
-constexpr int kCopyThreads = 256;
+// and written once, 18 KB (a latent cache's block) by one round of loads.  With more CTAs than run at once those that end
+// make room for others' loads: compacting eight pools (780 MB) 145.5 us with 8 CTAs of 256 threads an SM and rounds of 16
+// KB, 141.5 with rounds of 20, 137 with 16 CTAs, 134 with 64 of 128 threads, 152 with one for every block.
+constexpr int kCopyThreads = 128, kCopyAtOnce = 9, kCopyCtas = 64;  // threads, their vectors a round, CTAs an SM
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pools_kernel(const __grid_constant__ CopyPoolsParams p)
 {
@@ -571,22 +573,22 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pools_kernel(const __grid_c
             uint4 *const base = static_cast<uint4 *>(p.pools[__shfl_sync(0xFFFFFFFFu, pool, l)]);
             const uint4 *from = base + (int64_t)__shfl_sync(0xFFFFFFFFu, src, l) * p.vectors;
             uint4 *to = base + (int64_t)__shfl_sync(0xFFFFFFFFu, dst, l) * p.vectors;
-            int64_t x = tid;
-            for (; x + 3 * kCopyThreads < p.vectors; x += 4 * kCopyThreads) {
-                uint4 v[4];
+            for (int64_t x = tid; x < p.vectors; x += kCopyAtOnce * kCopyThreads) {
+                uint4 v[kCopyAtOnce];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = from[x + j * kCopyThreads];
+                for (int j = 0; j < kCopyAtOnce; ++j)
+                    if (x + j * kCopyThreads < p.vectors) v[j] = from[x + j * kCopyThreads];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) to[x + j * kCopyThreads] = v[j];
+                for (int j = 0; j < kCopyAtOnce; ++j)
+                    if (x + j * kCopyThreads < p.vectors) to[x + j * kCopyThreads] = v[j];
             }
-            for (; x < p.vectors; x += kCopyThreads) to[x] = from[x];
         }
     }
 }
 
 cudaError_t launch_copy_pools(const CopyPoolsParams &p, int sms, cudaStream_t stream)
 {
-    const int64_t items = (int64_t)p.pairs * p.num_pools, most = (int64_t)sms * 8;
+    const int64_t items = (int64_t)p.pairs * p.num_pools, most = (int64_t)sms * kCopyCtas;
     return launch_kernel(copy_pools_kernel, dim3((unsigned)(items < most ? items : most)), dim3(kCopyThreads), 0, stream, true, p);
 }
 
