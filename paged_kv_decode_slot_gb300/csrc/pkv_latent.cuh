@@ -61,23 +61,80 @@ struct LatentWalk {
     }
 };
 
+// x * n / d of work x in [0, ..] (64-bit divisions take as long as a load).
+__device__ __forceinline__ int64_t latent_share(int64_t x, int n, int d)
+{
+    return x < (1 << 24) && n <= 152 ? (int64_t)((uint32_t)x * (uint32_t)n / (uint32_t)d) : x * n / d;
+}
+
 // This CTA's (or cluster's: `cta` of p.ctas) run of the work, the same in every thread; false: nothing to do.  `sums` holds kThreads + 4 64-bit
 // words of shared memory.  Every thread calls it.
+// Up to 128 sequences each warp finds it by itself, four sequences a lane; with the CTA's barriers, as more need them, it took
+// 1.5 us of the prologue.
 template <int kTile, int kThreads>
 __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, int64_t *sums, LatentWalk<kTile> &w, int64_t &total,
                                             int &ctas)
 {
-    const int tid = threadIdx.x, per = (p.B + kThreads - 1) / kThreads;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const auto bad = [&](int ctx) { return ctx < 0 || ctx > p.max_nb * kBlockSize; };
+    if (p.B <= 128) {
+        const int per = (p.B + 31) / 32, b0 = lane * per;
+        int ctx[4], costs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ctx[k] = k < per && b0 + k < p.B ? p.context_lens[b0 + k] : 0;
+        int64_t cost = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (bad(ctx[k])) {
+                if (cta == 0 && tid < 32) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+                ctx[k] = 0;
+            }
+            cost += costs[k] = latent_cost<kTile>(ctx[k]);
+        }
+        int64_t upto = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += up;
+        }
+        total = __shfl_sync(0xFFFFFFFFu, upto, 31) * p.chunks;
+        // no more runs than units and tiles: a run then holds at least one of them
+        ctas = (int)min((int64_t)p.ctas, total);
+        if (cta >= ctas) return false;
+        w.lo = latent_share(total, cta, ctas);
+        w.hi = latent_share(total, cta + 1, ctas);
+        // the lane whose sequences hold its start
+        int64_t at = (upto - cost) * p.chunks;
+        const bool here = at <= w.lo && w.lo < upto * p.chunks;
+        int b = b0, c = 1;
+        if (here) {
+            bool found = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t all = (int64_t)costs[k] * p.chunks;
+                if (!found && w.lo < at + all) found = true, b = b0 + k, c = costs[k];
+                if (!found) at += all;
+            }
+        }
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+        at = __shfl_sync(0xFFFFFFFFu, at, from);
+        c = __shfl_sync(0xFFFFFFFFu, c, from);
+        w.b = __shfl_sync(0xFFFFFFFFu, b, from);
+        w.chunk = p.chunks == 1 ? 0 : (int)((w.lo - at) / c);
+        w.start = at + (int64_t)w.chunk * c;
+        return true;
+    }
+    const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t cost = 0;
     for (int b = b0; b < b1; ++b) {
         const int ctx = p.context_lens[b];
-        if (cta == 0 && (ctx < 0 || ctx > p.max_nb * kBlockSize)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
+        if (cta == 0 && bad(ctx)) set_flag(p.err_flag, PKV_FLAG_CTX_RANGE);
         cost += latent_cost<kTile>(latent_ctx(p, b));
     }
     sums[tid] = cost;
     __syncthreads();
-    if (tid < 32) {  // exclusive scan by one warp, ten entries a lane
+    if (tid < 32) {  // exclusive scan by one warp, kThreads / 32 entries a lane
         constexpr int kPer = kThreads / 32;
         int64_t mine = 0;
         for (int k = 0; k < kPer; ++k) mine += sums[tid * kPer + k];
@@ -96,13 +153,11 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, 
         }
     }
     __syncthreads();
-    const int64_t all = sums[kThreads];
-    total = all * p.chunks;
-    // no more runs than units and tiles: a run then holds at least one of them
+    total = sums[kThreads] * p.chunks;
     ctas = (int)min((int64_t)p.ctas, total);
     if (cta >= ctas) return false;
-    w.lo = total * cta / ctas;
-    w.hi = total * (cta + 1) / ctas;
+    w.lo = latent_share(total, cta, ctas);
+    w.hi = latent_share(total, cta + 1, ctas);
     int64_t at = sums[tid] * p.chunks;
     if (at <= w.lo && w.lo < (sums[tid] + cost) * p.chunks) {
         for (int b = b0; b < b1; ++b) {
@@ -121,6 +176,7 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, 
     w.b = (int)sums[kThreads + 1];
     w.chunk = (int)sums[kThreads + 2];
     w.start = sums[kThreads + 3];
+    __syncthreads();  // (the sums' place is someone else's from here on)
     return true;
 }
 

@@ -188,6 +188,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         tmem_alloc(smem_u32((const void *)tmem_slot), L::kCols);
         tmem_relinquish();
     }
+    if (threadIdx.x == 0) fence_barrier_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     pdl_wait_primary();
     pdl_launch_dependents();
     LatentWalk<L::kTile> walk;
@@ -195,10 +199,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     int ctas;
     // (the sums lie where the first tiles will)
     const bool work = latent_deal<L::kTile, kLatThreads>(p, cta, reinterpret_cast<int64_t *>(mem), walk, total, ctas);
-    if (threadIdx.x == 0) fence_barrier_init();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (!work) {
         if (warp == kLatMmaWarp) tmem_dealloc(*tmem_slot, L::kCols);
         return;
@@ -224,13 +224,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             uint32_t parity = 0;  // of the slot's uses
             LatentSegment sg;
             while (ok && walk.next(p, sg)) {
-                // the queries, once the last unit's are no longer needed
-                if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
-                if (!ok) break;
-                const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * R;
-                mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
-                for (int c = 0; c < kLatChunks; ++c) tma_load_3d(q_u32 + c * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, c);
-                ++q_loads;
                 const int nb = (sg.ctx + kBlockSize - 1) / kBlockSize;
                 const int32_t *tbl = p.block_tables + (size_t)sg.b * p.max_nb;
                 int next[NB];
@@ -239,6 +232,13 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     for (int k = 0; k < NB; ++k) next[k] = t < sg.t1 && t * NB + k < nb ? tbl[t * NB + k] : -1;
                 };
                 ids_of(sg.t0);
+                // the queries, once the last unit's are no longer needed
+                if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
+                if (!ok) break;
+                const int64_t row = (int64_t)sg.b * p.rows + (int64_t)sg.chunk * R;
+                mbar_arrive_expect_tx(bar_qfull, L::kQBytes);
+                for (int c = 0; c < kLatChunks; ++c) tma_load_3d(q_u32 + c * L::kQChunk, &tm_q, bar_qfull, 0, (int)row, c);
+                ++q_loads;
                 for (int t = sg.t0; t < sg.t1 && ok; ++t) {
                     const int nblk = min(NB, nb - t * NB);
                     int ids[NB];

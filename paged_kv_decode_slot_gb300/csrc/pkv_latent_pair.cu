@@ -228,6 +228,11 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
         tmem_alloc2(smem_u32((const void *)tmem_slot), L::kCols);
         tmem_relinquish2();
     }
+    if (threadIdx.x == 0) fence_barrier_init();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers and tensor memory are there
+    tc_fence_after();
     pdl_wait_primary();
     pdl_launch_dependents();
     LatentWalk<L::kTile> walk;
@@ -235,11 +240,6 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     int pairs;
     // (the sums lie where the queries will; both CTAs find the same)
     const bool work = latent_deal<L::kTile, kPairThreads>(p, pair, reinterpret_cast<int64_t *>(mem), walk, total, pairs);
-    if (threadIdx.x == 0) fence_barrier_init();
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // both CTAs' barriers and tensor memory are there
-    tc_fence_after();
     if (!work) {
         if (warp == kPairMmaWarp) tmem_dealloc2(*tmem_slot, L::kCols);
         return;
@@ -297,6 +297,8 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             bool ok = true, withheld = false;
             LatentSegment sg;
             while (ok && walk.next(p, sg)) {
+                int next[L::kBlocks];
+                ids_of(sg, sg.t0, next);
                 if (me == 0) {
                     // the queries, once the last unit's are no longer needed
                     if (q_loads > 0) ok = wait_one(bar_qfree, (q_loads - 1) & 1);
@@ -306,8 +308,6 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                     if (rank == 0) mbar_arrive_expect_tx(bar_qfull, 2 * L::kQBytes);
                     for (int c = 0; c < kLatChunks; ++c) pair_load_3d(q_u32 + c * L::kQChunk, &maps.queries, qfull_there, 0, (int)row, c);
                 }
-                int next[L::kBlocks];
-                ids_of(sg, sg.t0, next);
                 for (int t = sg.t0; t < sg.t1 && ok; ++t, ++g) {
                     if (PKV_TILE_WITHHELD(p, t)) {  // test builds: nothing is loaded or signalled from here on
                         withheld = true, ok = false;
