@@ -177,7 +177,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     float *const factor = top + R;                                               // [R]
     float *const quarters = factor + R;                                          // [4][R]
 
-    // what needs nothing of the launch ahead comes before the wait for it
+    // What needs nothing of the launch ahead comes before the wait for it.  (Tensor memory too: a CTA that still has to take its own
+    // does not fit beside this one's shared memory, so none of that launch waits for what is held here.)
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int s = 0; s < NS + kRing + 9; ++s) mbar_init(bar_full + 8 * s, s == NS + kRing + 4 ? kLatSoftmaxWarps : 1);

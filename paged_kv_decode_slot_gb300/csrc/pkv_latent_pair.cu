@@ -209,7 +209,8 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     float *const quarters = const_cast<float *>(reinterpret_cast<volatile float *>(want + L::kStages + 1));  // [4][64]
     float *const factor = quarters + 4 * L::kRows;                                              // [128] of both CTAs' rows
 
-    // what needs nothing of the launch ahead comes before the wait for it
+    // What needs nothing of the launch ahead comes before the wait for it.  (Tensor memory too: a CTA that still has to take its own
+    // does not fit beside this one's shared memory, so none of that launch waits for what is held here.)
     if (threadIdx.x == 0) {
         *abort_flag = 0, *q_asked = 0, *raise = 0, *verdict = 0;
         for (int s = 0; s < L::kStages; ++s) sent[s] = use[s] = want[s] = 0;
