@@ -12,8 +12,8 @@
 // of the 512 tensor-memory columns, and a tile is loaded once and read as keys and as values where it lies.
 //
 // Bound by memory, where there is enough of it: 152 sequences of 4,096 tokens and 16 rows take 116 us, 6.2 TB/s, 92% of a
-// copy's rate; 64 sequences of 512 to 8,192 tokens (325 MB) 63 us with 16 rows and 66 with 32.  One sequence of 2,000 tokens
-// takes 11 us: launches, and the dependent loads of lengths, tables and tiles.
+// copy's rate; 64 sequences of 512 to 8,192 tokens (325 MB) 62 us with 16 rows and 65 with 32.  One sequence of 2,000 tokens
+// takes 10 us: launches, and the dependent loads of lengths, tables and tiles.
 //
 // A block of 16 tokens is one TMA load of 18 KB, a box of (64 elements, 8 tokens, 9 chunks of elements, 2 halves): it
 // lands as [half][chunk][8 rows][128 bytes], swizzle atoms of 8 rows, so that the 8-row groups of consecutive blocks lie
