@@ -146,17 +146,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&x)[32])
     for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(r[c / 16][c % 16]);
 }
 
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ int load_word(const volatile int *at, int rank)
 {
     return __float_as_int(load_cluster<float>(smem_u32((const void *)at), rank));
@@ -650,11 +639,10 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                 if (!sg.whole) p.part_lse[part + rank * L::kRows + r] = lse2;
                 else if (p.lse_out) p.lse_out[first_row + rank * L::kRows + r] = lse2 * 0.69314718055994530942f;
             }
-            // Outputs.  A lane has an element of all rows: a part's row is one line of 32 elements a warp, bf16 outputs go through
-            // 2 KB of P, 16 rows of 32 elements at a time, so that a store covers whole sectors.  (Parts that went the same way
-            // took as long: with all CTAs at it, 19 MB in 2.6 us, it is the writes that bound it.)
+            // Outputs.  A lane has an element of all rows: a part's row is one line of 32 elements a warp; bf16 outputs pair up, two
+            // lanes for two rows.  (Through shared memory in 16-byte units: parts took as long, with all CTAs at it 19 MB in 2.6 us,
+            // it is the writes that bound it; bf16 outputs longer, 200 short sequences of 128 heads 37.4 us for 34.4.)
             const int h0 = 256 * rank + 128 * h + 32 * quarter, nrows = min(128, p.rows - sg.chunk * 128);
-            const uint32_t stage = p_u32 + group * 4096 + side * L::kPChunk + h * 2048;  // (the group's own)
 #pragma unroll 1
             for (int c = 0; c < nrows; c += 16) {
                 uint32_t o[16];
@@ -674,18 +662,14 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                         if (c + k < nrows) to[k * kLatentDim] = __uint_as_float(o[k]);
                     continue;
                 }
+                // two lanes, two rows: each takes one row's two elements
+                __nv_bfloat16 *const to = p.out + (first_row + c + (lane & 1)) * kLatentDim + h0 + (lane & ~1);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) st_shared_u32(stage + k * 128 + lane * 4, o[k]);
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int rr = 8 * k + (lane >> 2), e = 8 * (lane & 3);
-                    const float4 a = ld_shared_f4(stage + rr * 128 + e * 4), b = ld_shared_f4(stage + rr * 128 + e * 4 + 16);
-                    if (c + rr < nrows)
-                        *reinterpret_cast<uint4 *>(p.out + (first_row + c + rr) * kLatentDim + h0 + e) =
-                            make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+                for (int k = 0; k < 16; k += 2) {
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? o[k] : o[k + 1], 1);
+                    const float a = __uint_as_float(lane & 1 ? got : o[k]), b = __uint_as_float(lane & 1 ? o[k + 1] : got);
+                    if (c + k + (lane & 1) < nrows) *reinterpret_cast<uint32_t *>(to + k * kLatentDim) = pack_bf16x2(a, b);
                 }
-                __syncwarp();
             }
             tc_fence_before();
             half_sync(group);  // the sums are read
