@@ -1,4 +1,4 @@
-// pkv_latent_pair.cu - decode attention over a paged latent cache for sequences of more than 48 (token, head) rows; the
+// pkv_latent_pair.cu - decode attention over a paged latent cache for sequences of more than 32 (token, head) rows; the
 // mathematics is in pkv_latent_attn.cu.  Chunks of up to 128 rows, a cluster of two CTAs each.
 //
 // With 128 rows a cached row of 1,152 bytes takes 2 * 1088 * 128 operations, 242 a byte, about what the chip has for one
@@ -45,8 +45,8 @@ struct PairLayout {
     static constexpr int kStages = 9, kStage = 16384, kRope = 8;       // slots: 4 of keys, 4 of values, the rotary keys (half a slot)
     static constexpr int kQChunk = kRows * 128, kQBytes = kLatChunks * kQChunk;
     static constexpr int kPChunk = kRows * 128, kPBytes = 2 * kPChunk;  // 64 tokens a chunk
-    static constexpr int kQOffset = 0, kPOffset = kQBytes, kRingOffset = kPOffset + kPBytes;
-    static constexpr int kBarOffset = kRingOffset + 8 * kStage + kStage / 2;
+    static constexpr int kQOffset = 0, kPOffset = kQBytes, kSlotsOffset = kPOffset + kPBytes;
+    static constexpr int kBarOffset = kSlotsOffset + 8 * kStage + kStage / 2;
     // full[S], empty[S], q_full, q_free, s_full[2], p_ready, pv_done, exchange, tail[2], fin
     static constexpr int kBars = 2 * kStages + 10;
     static constexpr int kMiscOffset = (kBarOffset + kBars * 8 + 15) & ~15;
@@ -54,7 +54,7 @@ struct PairLayout {
                                   4 * kRows /* of four warps */ + 2 * kRows /* factors */;
     static constexpr int kBytes = kMiscOffset + kWords * 4;
     static constexpr int kAlloc = kBytes + 1024;                       // room to align the window
-    static_assert(kPOffset % 1024 == 0 && kRingOffset % 1024 == 0, "swizzle atoms are aligned");
+    static_assert(kPOffset % 1024 == 0 && kSlotsOffset % 1024 == 0, "swizzle atoms are aligned");
     static_assert(kAlloc <= 227 * 1024, "shared memory of a CTA");
     static constexpr uint32_t kCols = 512;                             // tensor memory: O^T 2 x 128, S 2 x 64
 };
@@ -170,7 +170,7 @@ __device__ __forceinline__ void pair_acquired(uint32_t bar, uint32_t parity)
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar), "r"(parity)
                  : "memory");
 }
-// (2,000 clocks: where an exchange of the CTAs' shared memory needs it, not in every tile)
+// (2,000 clocks: for a refused round alone, not in every tile)
 __device__ __forceinline__ void pair_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -183,7 +183,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)pair_rank(), pair = (int)blockIdx.x >> 1;
 
-    const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, ring = base + L::kRingOffset;
+    const uint32_t q_u32 = base + L::kQOffset, p_u32 = base + L::kPOffset, slots = base + L::kSlotsOffset;
     const uint32_t bar_full = base + L::kBarOffset, bar_empty = bar_full + 8 * L::kStages, bar_qfull = bar_empty + 8 * L::kStages,
                    bar_qfree = bar_qfull + 8, bar_s = bar_qfree + 8, bar_p = bar_s + 16, bar_pv = bar_p + 8, bar_x = bar_pv + 8,
                    bar_tail = bar_x + 8, bar_fin = bar_tail + 16;
@@ -320,7 +320,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                         ok = open(s, g, __popc(mask) * bytes, __popc(own) * bytes);
                         if (!ok) break;
                         const CUtensorMap *const map = rope ? &maps.rope : &maps.keys;
-                        const uint32_t dst = ring + s * L::kStage, bar = full_there + 8 * s;
+                        const uint32_t dst = slots + s * L::kStage, bar = full_there + 8 * s;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if ((own >> k) & 1u) pair_load_5d(dst + k * bytes, map, bar, 0, 0, 2 * c, 0, mine[k]);
@@ -369,7 +369,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                         const uint32_t two = (mask >> (2 * v)) & 3u;
                         if (ok) ok = open(4 + v, g, 2 * __popc(two) * 8192, __popc(two) * 8192);
                         if (!ok) break;
-                        const uint32_t dst = ring + (4 + v) * L::kStage, bar = pair_at(bar_full + 8 * (4 + v), 0);
+                        const uint32_t dst = slots + (4 + v) * L::kStage, bar = pair_at(bar_full + 8 * (4 + v), 0);
                         if (two & 1u) pair_load_5d(dst, &maps.values, bar, 0, 0, 4 * rank, 0, ids[2 * v]);
                         if (two & 2u) pair_load_5d(dst + 8192, &maps.values, bar, 0, 0, 4 * rank, 0, ids[2 * v + 1]);
                     }
@@ -381,7 +381,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             ok = wait(bar_tail, asked++ & 1);
             if (!ok) break;
             const int j = sg.ctx / kBlockSize - (sg.tiles - 1) * L::kBlocks;
-            const uint32_t blk = ring + (4 + (j >> 1)) * L::kStage + (j & 1) * 8192;
+            const uint32_t blk = slots + (4 + (j >> 1)) * L::kStage + (j & 1) * 8192;
             for (int x = lane; x < (kBlockSize - tail) * 32; x += 32) {
                 const int u = x & 31, row = tail + (x >> 5);
                 st_shared_v4(blk + (row >> 3) * 4096 + (u >> 3) * 1024 + (row & 7) * 128 + (u & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
@@ -398,8 +398,8 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
         issuer = elect_one() && rank == 0;
         if (issuer) {
             constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0), kIdO = idesc_bf16_f32(256, 128, 1, 0);
-            const uint64_t k_desc = smem_desc_sw128(ring, 16, 2048), r_desc = smem_desc_sw128(ring + L::kRope * L::kStage, 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(ring + 4 * L::kStage, 1024, 4096);
+            const uint64_t k_desc = smem_desc_sw128(slots, 16, 2048), r_desc = smem_desc_sw128(slots + L::kRope * L::kStage, 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(slots + 4 * L::kStage, 1024, 4096);
             const uint64_t q_desc = smem_desc_sw128(q_u32, 16, 1024), p_desc = smem_desc_sw128(p_u32, 16, 1024);
             const uint32_t ask_other = pair_at(bar_tail, 1), pv_other = pair_at(bar_pv, 1);
             const uint32_t verdict_other = pair_at(smem_u32((const void *)verdict), 1);
