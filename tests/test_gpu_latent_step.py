@@ -252,3 +252,44 @@ def test_blocks_of_more_pools_than_one_call_takes(pkv):  # noqa: F811
     seqs.extend(i32_dev([1, 1]), pools)
     assert seqs.copies.tolist() == [[0, 1], [-1, -1]]
     assert all(bool((p[:2] == k + 1).all()) and not p[2:].any() for k, p in enumerate(pools))
+
+
+def test_arguments_in_pinned_host_memory(pkv):  # noqa: F811
+    """What the kernels read and write with plain loads and stores may lie in pinned host memory: the same results."""
+    r = np.random.default_rng(4)
+    new = lambda *shape: bf16_dev(R.to_bf16(r.standard_normal(shape)))
+    pin = lambda t: t.cpu().pin_memory()
+    inv, w, ctx = torch.from_numpy(INV).cuda(), new(512), [700, 0, 33]
+    for N in (16, 128):
+        tab, pool = R.tables(r, ctx)
+        cache, q, kv, rope = new(pool, 16, 576), new(3, 1, N, 576), new(3, 1, 576), new(3, 1, N, 64)
+        results = []
+        for move in (lambda t: t, pin):
+            c, qq = cache.clone(), q.clone()
+            slots, out, lse = (move(torch.zeros(3, 1, dtype=torch.int64, device="cuda")), move(torch.zeros(3, 1, N, 512, device="cuda").bfloat16()),
+                               move(torch.zeros(3, 1, N, device="cuda")))
+            ws = torch.zeros(pkv.pkv_latent_workspace_bytes(3, 1, N), dtype=torch.uint8, device="cuda")
+            t, l = move(i32_dev(tab)), move(i32_dev(ctx))
+            pkv.check(pkv.pkv_latent_append_multi(move(kv), move(rope), t, l, move(inv), c, qq, slots, move(w), 1e-6, True))
+            pkv.check(pkv.pkv_decode_attn_latent(qq, c, t, l, 0.05, out, lse, ws))
+            torch.cuda.synchronize()
+            results.append([x.cpu() for x in (c, qq, slots, out, lse)])
+        assert all(same(a, b) for a, b in zip(*results))
+    tables, lens, ref = L.random_rows(r, 20, 12, 200, 0.5)
+    num_new = np.minimum(r.integers(0, 90, 20), 192 - lens).astype(np.int32)
+    results = []
+    for move in (lambda t: t, pin):
+        t, l, f = move(i32_dev(tables)), move(i32_dev(lens)), i32_dev(ref)
+        copies, moves, n = (move(torch.zeros(k, 2, dtype=torch.int32, device="cuda")) for k in (20, 100, 1))
+        to, lo = move(torch.zeros(30, 12, dtype=torch.int32, device="cuda")), move(torch.zeros(30, dtype=torch.int32, device="cuda"))
+        n = n.view(-1)[:1]
+        ws = torch.zeros(pkv.pkv_blocks_workspace_bytes(200), dtype=torch.uint8, device="cuda")
+        pool = torch.arange(200 * 16, device="cuda", dtype=torch.float32).view(200, 16).clone()
+        pkv.check(pkv.pkv_extend_sequences(t, l, move(i32_dev(num_new)), f, copies, ws))
+        pkv.check(pkv.pkv_copy_blocks_pools([pool], copies))
+        pkv.check(pkv.pkv_fork_sequences(t, l, move(i32_dev(np.arange(30) % 17)), f, to, lo))
+        pkv.check(pkv.pkv_compact_blocks(to, lo, f, moves, n, ws))
+        pkv.check(pkv.pkv_copy_blocks_pools([pool], moves))
+        torch.cuda.synchronize()
+        results.append([x.cpu() for x in (t, l, f, copies, to, lo, moves, n, pool)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
