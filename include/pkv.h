@@ -705,8 +705,9 @@ int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, cons
  * ---- the life of a cache's blocks -----------------------------------------------------------------
  * ("Optimización de la inferencia", "Página Atención": pages anywhere in memory, shared ones copied on write.)  The state
  * of the sequences: block_tables int32 [num_seqs][max_blocks_per_seq], context_lens int32 [num_seqs], and ref_counts
- * int32 [num_blocks] in device memory (num_seqs and num_blocks up to 2^31 - 65,537, max_blocks_per_seq up to 33,553,920), for every physical block the number of table rows that hold it (entries j < ceil(ctx / 16) of a row
- * count, those behind are not looked at).  A block with count 0 is free.  The calls below keep the counts; all results are
+ * int32 [num_blocks] in device memory, for every physical block the number of table rows that hold it (entries
+ * j < ceil(ctx / 16) of a row count, those behind are not looked at); num_seqs and num_blocks up to 2^31 - 65,537,
+ * max_blocks_per_seq up to 33,553,920.  A block with count 0 is free.  The calls below keep the counts; all results are
  * exact and follow from the arguments alone.  Where counts and tables disagree the result is void: disagreements that
  * a call meets set PKV_FLAG_REF_RANGE, nothing outside the given arrays is touched.  Blocks are blocks of every layer's
  * pools (of any kind: K and V, e4m3, latent); what has to be copied is told as pairs for pkv_copy_blocks_pools.
