@@ -56,7 +56,7 @@ struct LatentLayout {
     static constexpr int kBars = kSlots + kRing + 9;
     static constexpr int kMiscOffset = (kBarOffset + kBars * 8 + 15) & ~15;
     static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, - */ + 2 * 4 /* a slot's bytes */ + R /* limits */ +
-                                  R /* maxima */ + R /* factors */ + 4 * R /* of four warps */;
+                                  R /* maxima */ + R /* factors */ + 8 * R /* of four warps */;
     static constexpr int kBytes = kMiscOffset + kWords * 4;
     static constexpr int kAlloc = kBytes + 1024;  // room to align the window
     static_assert(kQOffset % 1024 == 0 && kPOffset % 1024 == 0 && kSlots <= 4, "swizzle atoms are aligned");
@@ -175,7 +175,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     int *const limit = const_cast<int *>(tile_mask + 16);                        // [R] tokens a row sees
     float *const top = reinterpret_cast<float *>(limit + R);                     // [R] running maxima (log2)
     float *const factor = top + R;                                               // [R]
-    float *const quarters = factor + R;                                          // [4][R]
+    float *const quarters = factor + R, *const quarters_n = quarters + 4 * R;    // [4][R]
 
     // What needs nothing of the launch ahead comes before the wait for it.  (Tensor memory too: a CTA that still has to take its own
     // does not fit beside this one's shared memory, so none of that launch waits for what is held here.)
@@ -395,9 +395,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 top[c0 + lane] = -FLT_MAX;
             }
             half_sync(half);
-            float l[CW];
+            float l[CW], norm[CW];  // sums of the weights, as they are and as the product has them
 #pragma unroll
-            for (int c = 0; c < CW; ++c) l[c] = 0.f;
+            for (int c = 0; c < CW; ++c) l[c] = norm[c] = 0.f;
             // The barriers below count all four warps of a half, so a warp whose wait gave up leaves only where
             // all four agree on it, at the votes that open a tile and the outputs.
             bool left = false;
@@ -446,7 +446,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                         if (up) top[c0 + lane] = hi;
                     }
                     half_sync(half);
-                    load_top();
                     if (g > 0) ok = wait(bar_pv, (g - 1) & 1);
                     tc_fence_after();
 #pragma unroll 1
@@ -458,9 +457,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int c = 0; c < CW; ++c) l[c] *= factor[c0 + c];
+                    for (int c = 0; c < CW; ++c) l[c] *= factor[c0 + c], norm[c] *= factor[c0 + c];
                 }
-                // weights: rounded to bf16 for the product, summed as they are
+                load_top();  // (again: held across the vote the maxima would not fit the registers of 32 rows)
+                // weights: bf16, as the product takes them.  Outputs are normalised by the sum of the rounded ones, or a token
+                // that counts for all would scale its row by its own rounding; lse is of the sum of the weights as they are
                 uint32_t w[CW / 2];
 #pragma unroll
                 for (int c = 0; c < CW; c += 2) {
@@ -468,6 +469,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     w[c / 2] = pack_bf16x2(a, b);
                     l[c] += a;
                     l[c + 1] += b;
+                    norm[c] += bf16x2_lo(w[c / 2]);
+                    norm[c + 1] += bf16x2_hi(w[c / 2]);
                 }
                 if (g > 0) ok = wait(bar_pv, (g - 1) & 1) && ok;  // the last tile's weights are no longer needed
                 if (!ok) give_up();
@@ -489,11 +492,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             }
             tc_fence_after();
             // sums over the tokens: of the warp, then of the four warps
-            const float sum = reduce_columns<CW>(l, lane, [](float a, float b) { return a + b; });
-            if (lane < CW) quarters[quarter * R + c0 + lane] = sum;
+            const auto add = [](float a, float b) { return a + b; };
+            const float sum = reduce_columns<CW>(l, lane, add), sum_n = reduce_columns<CW>(norm, lane, add);
+            if (lane < CW) quarters[quarter * R + c0 + lane] = sum, quarters_n[quarter * R + c0 + lane] = sum_n;
             half_sync(half);
-            const float *f = quarters + c0 + col;
-            const float all = (f[0] + f[R]) + (f[2 * R] + f[3 * R]), hi = top[c0 + col];
+            const float *f = quarters + c0 + col, *fn = quarters_n + c0 + col;
+            const float all = (f[0] + f[R]) + (f[2 * R] + f[3 * R]), all_n = (fn[0] + fn[R]) + (fn[2 * R] + fn[3 * R]), hi = top[c0 + col];
             const bool seen = all != 0.f;  // (NaN is something)
             const int64_t part = (int64_t)(2 * cta + (sg.t0 == 0)) * R;  // rows of the workspace
             if (quarter == 0 && lane < CW && c0 + lane < nrows) {
@@ -502,7 +506,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 if (!sg.whole) p.part_lse[part + c0 + lane] = lse2;
                 else if (p.lse_out) p.lse_out[row] = lse2 * 0.69314718055994530942f;
             }
-            if (quarter == 0 && lane < CW) factor[c0 + lane] = seen ? 1.f / all : 0.f;
+            if (quarter == 0 && lane < CW) factor[c0 + lane] = seen ? 1.f / all_n : 0.f;
             half_sync(half);
             float inv[CW];
 #pragma unroll

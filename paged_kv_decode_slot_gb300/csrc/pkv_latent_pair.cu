@@ -522,7 +522,8 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
             // round of weights: both CTAs then scale the sums of the rows concerned and make the tile's weights again.  That is
             // learned with the wait for the product, so after the next tile's weights were made: those are dropped.
             // The warps of a group leave together: one that gives up goes to a vote, and the others meet it at their next.
-            float m = -FLT_MAX, l = 0.f, l_here = 0.f, l_before = 0.f;  // l ahead of this tile, and of the last
+            // l, norm: sums of the weights, as they are and as the product has them; _here, _before: ahead of this tile, and of the last
+            float m = -FLT_MAX, l = 0.f, l_here = 0.f, l_before = 0.f, norm = 0.f, norm_here = 0.f, norm_before = 0.f;
             bool left = false, first = true, redo = false, clear = true;
             for (int t = sg.t0;;) {
                 if (t < sg.t1) wait_for(bar_s + 8 * (g & 1), (g >> 1) & 1);
@@ -557,7 +558,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                         const float f = up ? exp2_sfu(m - hi) : 1.f;
                         if (up) m = hi;
                         if (redo) {
-                            l = l_before * f;
+                            l = l_before * f, norm = norm_before * f;
                             exchange(f);
                             left = half_any(group, !ok);
                             if (left) break;
@@ -577,13 +578,15 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                         first = redo = false;
                     }
                     over = hi - m > kPairRescale;
-                    // weights: rounded to bf16 for the product, summed as they are
-                    l_here = l;
+                    // weights: bf16, as the product takes them.  Outputs are normalised by the sum of the rounded ones, or a token
+                    // that counts for all would scale its row by its own rounding; lse is of the sum of the weights as they are
+                    l_here = l, norm_here = norm;
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
                         const float a = exp2_sfu(x[c] - m), b = exp2_sfu(x[c + 1] - m);
                         w[c / 2] = pack_bf16x2(a, b);
                         l += a + b;
+                        norm += bf16x2_lo(w[c / 2]) + bf16x2_hi(w[c / 2]);
                     }
                 }
                 if (!clear) {
@@ -613,7 +616,7 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                     pair_fence();
                 }
                 if (lane == 0) pair_arrive(ready);
-                l_before = l_here, clear = false;
+                l_before = l_here, norm_before = norm_here, clear = false;
                 ++t, ++g;
             }
             if (!left) left = half_any(group, false);
@@ -622,18 +625,22 @@ latent_pair_kernel(const __grid_constant__ LatentPairMaps maps, const LatentAttn
                 break;
             }
             tc_fence_after();
-            quarter_at[64 * (side + 2 * h)] = l;
-            half_sync(group);
-            const float all = (quarter_at[0] + quarter_at[64]) + (quarter_at[128] + quarter_at[192]);
-            const bool seen = all != 0.f;  // (NaN is something)
+            const auto all_of = [&](float v) {
+                quarter_at[64 * (side + 2 * h)] = v;
+                half_sync(group);
+                return (quarter_at[0] + quarter_at[64]) + (quarter_at[128] + quarter_at[192]);
+            };
+            const float all_n = all_of(norm);
+            const bool seen = all_n != 0.f;  // (NaN is something)
             const int64_t part = (int64_t)(2 * pair + (sg.t0 == 0)) * 128;  // rows of the workspace
             const int64_t first_row = (int64_t)sg.b * p.rows + sg.chunk * 128;
-            exchange(seen ? 1.f / all : 0.f);
+            exchange(seen ? 1.f / all_n : 0.f);
             left = half_any(group, !ok);
             if (left) {
                 ok = false;
                 break;
             }
+            const float all = all_of(l);  // (behind the vote: the first sums are read)
             if (side + h == 0 && real) {
                 const float lse2 = seen ? m + log2f(all) : -INFINITY;
                 if (!sg.whole) p.part_lse[part + rank * L::kRows + r] = lse2;
