@@ -736,10 +736,19 @@ size_t pkv_blocks_workspace_bytes(int32_t num_blocks);
    (-1, -1).  (Rows that share it and grow in one call are taken in order: the last holder keeps the block.)  Once a row needs
    more blocks than are left, it and all growing rows behind it stay as they are and PKV_FLAG_NO_BLOCKS is set.  A negative
    num_new, a context outside [0, 16 max_blocks_per_seq], or a row that would outgrow its table, sets PKV_FLAG_CTX_RANGE, a
-   partly filled block outside the pool PKV_FLAG_BLOCK_RANGE, and that row stays as it is. */
+   partly filled block outside the pool PKV_FLAG_BLOCK_RANGE, and that row stays as it is.  A step that writes the newest
+   tokens of EVERY row must not be given these lengths where a row may not have grown (num_new 0, or refused): it would write
+   over that row's last tokens, which other rows may share.  pkv_extend_sequences_step tells it which rows to leave alone. */
 int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *num_new,
                          int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks, int32_t *copies, void *workspace,
                          size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
+
+/* The same, and the lengths for the step that writes the new tokens: step_lens int32 [num_seqs] (nullable; must not overlap
+   context_lens or num_new), the new length of a row that grew and 0 of one that did not: a step appends nothing to a row of
+   length 0 and gives out 0, lse -inf. */
+int pkv_extend_sequences_step(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens, const int32_t *num_new,
+                              int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks, int32_t *copies, int32_t *step_lens,
+                              void *workspace, size_t workspace_bytes, int32_t *err_flag, pkv_stream_t stream);
 
 /* Moves blocks towards the front of the pool: the highest used id to the lowest free one, the next highest to the next
    lowest, while that lies below it, at most max_moves times (num_blocks / 2 always suffices: then the used blocks are the

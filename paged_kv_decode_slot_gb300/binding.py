@@ -1185,6 +1185,7 @@ _lib.pkv_fork_sequences.argtypes = [_P, _I32, _P, _I32, _P, _I32, _P, _I32, _P, 
 _lib.pkv_blocks_workspace_bytes.argtypes = [_I32]
 _lib.pkv_blocks_workspace_bytes.restype = ctypes.c_size_t
 _lib.pkv_extend_sequences.argtypes = [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.pkv_extend_sequences_step.argtypes = [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _P, ctypes.c_size_t, _P, _P]
 _lib.pkv_compact_blocks.argtypes = [_P, _I32, _P, _I32, _P, _I32, _P, _I32, _P, _P, ctypes.c_size_t, _P, _P]
 _lib.pkv_copy_blocks_pools.argtypes = [_P, _I32, _I64, _I32, _P, _I32, _P, _P]
 
@@ -1215,13 +1216,15 @@ def pkv_blocks_workspace_bytes(num_blocks: int) -> int:
 
 
 def pkv_extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag=None,
-                         stream=None) -> int:
+                         stream=None, step_lens=None) -> int:
     """Row b grows by num_new[b] tokens: block_tables [B, W], context_lens [B] and ref_counts [num_blocks] in place,
-    copies int32 [B, 2] (written): the copy on write of each row, or (-1, -1).  workspace:
+    copies int32 [B, 2] (written): the copy on write of each row, or (-1, -1).  step_lens int32 [B] (written): the lengths
+    for the step that writes the new tokens, 0 for rows that did not grow.  workspace:
     pkv_blocks_workspace_bytes(num_blocks) bytes."""
     dev = _current_device()
     if _calls is not None:
-        status = _calls.extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag, stream, dev)
+        status = _calls.extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, step_lens, workspace, err_flag,
+                                         stream, dev)
         if status is not None:
             return status
     B, nb = _shape(context_lens, 1, "context_lens")[0], _shape(ref_counts, 1, "ref_counts")[0]
@@ -1229,10 +1232,12 @@ def pkv_extend_sequences(block_tables, context_lens, num_new, ref_counts, copies
     size = _shape(workspace, 1, "workspace")[0]
     if B == 0:
         return PKV_OK
-    return _lib.pkv_extend_sequences(tp, width, cp, _arg(num_new, _i32, (B,), "num_new", dev), B,
-                                     _arg(ref_counts, _i32, (nb,), "ref_counts", dev), nb,
-                                     _arg(copies, _i32, (B, 2), "copies", dev), _arg(workspace, _u8, (size,), "workspace", dev),
-                                     size, _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
+    return _lib.pkv_extend_sequences_step(tp, width, cp, _arg(num_new, _i32, (B,), "num_new", dev), B,
+                                          _arg(ref_counts, _i32, (nb,), "ref_counts", dev), nb,
+                                          _arg(copies, _i32, (B, 2), "copies", dev),
+                                          _maybe(step_lens, _i32, (B,), "step_lens", dev),
+                                          _arg(workspace, _u8, (size,), "workspace", dev), size,
+                                          _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
 
 
 def pkv_compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves, workspace, err_flag=None,

@@ -921,24 +921,35 @@ PKV_EXPORT int pkv_fork_sequences(const int32_t *block_tables, int32_t max_block
 
 PKV_EXPORT size_t pkv_blocks_workspace_bytes(int32_t num_blocks) { return num_blocks > 0 ? 4 * (size_t)num_blocks : 0; }
 
-PKV_EXPORT int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens,
-                                    const int32_t *num_new, int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks,
-                                    int32_t *copies, void *workspace, size_t workspace_bytes, int32_t *err_flag,
-                                    pkv_stream_t stream)
+PKV_EXPORT int pkv_extend_sequences_step(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens,
+                                         const int32_t *num_new, int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks,
+                                         int32_t *copies, int32_t *step_lens, void *workspace, size_t workspace_bytes,
+                                         int32_t *err_flag, pkv_stream_t stream)
 {
     if (!block_tables || !context_lens || !num_new || !ref_counts || !copies) return PKV_ERR_NULL;
     int st = check_sequences(max_blocks_per_seq, num_seqs, num_blocks);
     if (st != PKV_OK) return st;
     if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(num_new, 4) || !aligned(ref_counts, 4) ||
-        !aligned(copies, 4))
+        !aligned(copies, 4) || !aligned(step_lens, 4))
         return PKV_ERR_ALIGN;
+    const int64_t lens = 4 * (int64_t)num_seqs;
+    if (step_lens && (overlap(step_lens, lens, context_lens, lens) || overlap(step_lens, lens, num_new, lens))) return PKV_ERR_SHAPE;
     if (!workspace || workspace_bytes < pkv_blocks_workspace_bytes(num_blocks)) return PKV_ERR_WORKSPACE;
     if (!aligned(workspace, 4)) return PKV_ERR_ALIGN;
     if (num_seqs == 0) return PKV_OK;
     pkv::ExtendParams p{block_tables, context_lens, num_new, max_blocks_per_seq, num_seqs, num_blocks, ref_counts, copies,
-                        static_cast<int32_t *>(workspace), err_flag};
+                        step_lens, static_cast<int32_t *>(workspace), err_flag};
     cudaError_t e = pkv::launch_extend_sequences(p, stream);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e, "extend launch");
+}
+
+PKV_EXPORT int pkv_extend_sequences(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *context_lens,
+                                    const int32_t *num_new, int32_t num_seqs, int32_t *ref_counts, int32_t num_blocks,
+                                    int32_t *copies, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                                    pkv_stream_t stream)
+{
+    return pkv_extend_sequences_step(block_tables, max_blocks_per_seq, context_lens, num_new, num_seqs, ref_counts, num_blocks,
+                                     copies, nullptr, workspace, workspace_bytes, err_flag, stream);
 }
 
 PKV_EXPORT int pkv_compact_blocks(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,

@@ -402,6 +402,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
         }
     }
     scan_sync<kCtas>();
+    auto step_len = [&](int row, int len) { if (p.step_lens) p.step_lens[row] = len; };
     // hand them out: few a row by its own thread ..
     for (int row = rb; row < re; ++row) {
         const int2 s = get(row);
@@ -409,13 +410,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
         if (s.x == kIdle || s.y < 0) {
             if (s.x >= 0) atomicAdd(p.ref_counts + s.x, 1);
             state.put(row, make_int2(-1, -1));
+            step_len(row, 0);
             continue;
         }
         const GrowRow g = grow(row);
         const int cow = s.x >= 0, n = g.then - g.now + cow;
         if (!cow) state.put(row, make_int2(-1, -1));
         give_blocks(p, row, g.now - cow, n, s.y, 0, 1, s.x);
-        p.context_lens[row] = g.ctx + p.num_new[row];
+        step_len(row, p.context_lens[row] = g.ctx + p.num_new[row]);
     }
     if (all_of[2] == 0) return;
     if (!one) scan_sync<kCtas>();  // a row's own thread still reads its state where a warp leaves the pair to copy
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) extend_kernel(const ExtendPar
         __syncwarp();
         if (lane == 0 && !cow) state.put(row, make_int2(-1, -1));
         give_blocks(p, row, g.now - cow, g.then - g.now + cow, s.y, lane, 32, cow_of);
-        if (lane == 0) p.context_lens[row] = g.ctx + t;
+        if (lane == 0) step_len(row, p.context_lens[row] = g.ctx + t);
     }
 }
 

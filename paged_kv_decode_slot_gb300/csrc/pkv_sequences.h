@@ -29,6 +29,7 @@ struct ExtendParams {
     int32_t max_nb, rows, num_blocks;
     int32_t *ref_counts;           // [num_blocks]
     int32_t *copies;               // [rows][2]
+    int32_t *step_lens;            // [rows], nullable: new lengths of the rows that grew, else 0
     int32_t *free_ids;             // workspace [num_blocks]
     int32_t *err_flag;
 };

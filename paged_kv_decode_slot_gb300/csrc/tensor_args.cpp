@@ -88,7 +88,7 @@ PyObject *set_refuse(PyObject *, PyObject *f)
     X(pkv_latent_append_multi)                                                                                                  \
     X(pkv_decode_attn_latent)                                                                                                   \
     X(pkv_fork_sequences)                                                                                                       \
-    X(pkv_extend_sequences)                                                                                                     \
+    X(pkv_extend_sequences_step)                                                                                            \
     X(pkv_compact_blocks)                                                                                                       \
     X(pkv_copy_blocks_pools)
 struct Library {
@@ -463,19 +463,21 @@ PyObject *fork_sequences(PyObject *, PyObject *const *a, Py_ssize_t n)
     return launch(c, g_lib.pkv_fork_sequences, tables, width, lens, B, parents, R, refs, nb, tables_out, lens_out, err, stream);
 }
 
-// extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag, stream, dev)
+// extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, step_lens, workspace, err_flag, stream, dev)
 PyObject *extend_sequences(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    Call c(a, n, 9);
+    Call c(a, n, 10);
     Dim B, width, nb, two{2}, size;
     int32_t *tables = c.tensor<int32_t>(at::kInt, {&B, &width}), *lens = c.tensor<int32_t>(at::kInt, {&B});
     const int32_t *num_new = c.tensor<int32_t>(at::kInt, {&B});
     int32_t *refs = c.tensor<int32_t>(at::kInt, {&nb}), *copies = c.tensor<int32_t>(at::kInt, {&B, &two});
+    int32_t *step_lens = c.maybe<int32_t>(at::kInt, {&B});
     void *ws = c.tensor(at::kByte, {&size});
     int32_t *err = c.flag();
     const pkv_stream_t stream = c.stream();
     if (nb.v > INT32_MAX) c.ok = false;
-    return launch(c, g_lib.pkv_extend_sequences, tables, width, lens, num_new, B, refs, nb, copies, ws, (size_t)size.v, err, stream);
+    return launch(c, g_lib.pkv_extend_sequences_step, tables, width, lens, num_new, B, refs, nb, copies, step_lens, ws, (size_t)size.v, err,
+                  stream);
 }
 
 // compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves, workspace, err_flag, stream, dev)

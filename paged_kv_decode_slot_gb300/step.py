@@ -563,7 +563,8 @@ class LatentDecodeStep:
     kv_new bf16 [B, T, 576] (latent vector, rotary key), q_rope bf16 [B, T, N, 64] before the rotation (any strides with
     contiguous elements, e.g. a slice of the query projection's output), q bf16 [B, T, N, 576] whose first 512 elements
     a head hold the queries that the key projection was absorbed into; latent_cache [num_blocks, 16, 576], block_tables
-    [B, max_blocks] and context_lens [B] (which count the new tokens) in device memory; inv_freq float64 [32];
+    [B, max_blocks] and context_lens [B] (which count the new tokens; 0 for a sequence that has none, which is then left
+    alone) in device memory; inv_freq float64 [32];
     norm_weight bf16 [512] or None.  q[..., 512:], slot_mapping, out [B, T, N, 512] and lse are written."""
 
     def __init__(self, kv_new, q_rope, q, latent_cache, block_tables, context_lens, scale, inv_freq, norm_weight=None,
@@ -605,7 +606,11 @@ class SequenceBlocks:
     ``extend`` before a step makes room for its new tokens, ``fork`` after one lets rows take over others (beams, samples
     of one prompt, sequences that end), ``compact`` moves blocks to the front of the pools.  ``pools`` are the tensors
     [num_blocks, ...] of every layer that the tables speak of, in groups of one shape and type.  Nothing is read back: too few
-    free blocks, say, shows in ``err_flag`` and in the lengths that did not grow."""
+    free blocks, say, shows in ``err_flag`` and in the lengths that did not grow.
+
+    ``step_lens`` int32 [num_seqs] is what the step that writes an extension's tokens is given as its ``context_lens``: the
+    new length of every row that grew, 0 for those that did not (asked for no token, or refused).  With ``context_lens`` itself
+    it would write over the last tokens of such a row, which other rows may share."""
 
     def __init__(self, num_seqs: int, max_blocks: int, num_blocks: int, device="cuda", err_flag=None):
         ints = dict(dtype=torch.int32, device=device)
@@ -613,6 +618,7 @@ class SequenceBlocks:
         self.context_lens = torch.zeros(num_seqs, **ints)
         self.ref_counts = torch.zeros(num_blocks, **ints)
         self.copies = torch.full((num_seqs, 2), -1, **ints)
+        self.step_lens = torch.zeros(num_seqs, **ints)
         self.moves = torch.full((max(1, num_blocks // 2), 2), -1, **ints)
         self.num_moves = torch.zeros(1, **ints)
         self.err_flag = err_flag
@@ -628,9 +634,10 @@ class SequenceBlocks:
                 B.check(B.pkv_copy_blocks_pools(same[k:k + 256], pairs, self.err_flag, stream))
 
     def extend(self, num_new, pools=(), stream=None) -> None:
-        """Row b grows by num_new[b] (int32 [num_seqs]) tokens; shared last blocks are copied on write in ``pools``."""
+        """Row b grows by num_new[b] (int32 [num_seqs]) tokens; shared last blocks are copied on write in ``pools``;
+        ``step_lens`` says which rows grew."""
         B.check(B.pkv_extend_sequences(self.block_tables, self.context_lens, num_new, self.ref_counts, self.copies,
-                                       self.workspace, self.err_flag, stream))
+                                       self.workspace, self.err_flag, stream, self.step_lens))
         self._copy(pools, self.copies, stream)
 
     def fork(self, parents, stream=None) -> None:
