@@ -601,7 +601,8 @@ class LatentDecodeStep:
 
 class SequenceBlocks:
     """The rows of a batch and the blocks they hold, kept on the device: ``block_tables`` int32 [num_seqs, max_blocks],
-    ``context_lens`` int32 [num_seqs] (what the steps take) and ``ref_counts`` int32 [num_blocks].  All rows start empty.
+    ``context_lens`` int32 [num_seqs] (what the steps take) and ``ref_counts`` int32 [num_blocks].  All rows start empty.  These
+    tensors stay the same ones whatever is called, so steps and captured graphs made with them go on.
 
     ``extend`` before a step makes room for its new tokens, ``fork`` after one lets rows take over others (beams, samples
     of one prompt, sequences that end), ``compact`` moves blocks to the front of the pools.  ``pools`` are the tensors
@@ -624,6 +625,7 @@ class SequenceBlocks:
         self.err_flag = err_flag
         self.workspace = torch.empty(B.pkv_blocks_workspace_bytes(num_blocks), dtype=torch.uint8, device=device)
         self._other = (torch.empty_like(self.block_tables), torch.empty_like(self.context_lens))
+        self._same = torch.arange(num_seqs, **ints)
 
     def _copy(self, pools, pairs, stream) -> None:
         groups = {}
@@ -641,13 +643,12 @@ class SequenceBlocks:
         self._copy(pools, self.copies, stream)
 
     def fork(self, parents, stream=None) -> None:
-        """Row b becomes what row parents[b] (int32 [num_seqs]) was, or empty (-1).  The tensors ``block_tables`` and
-        ``context_lens`` change places with a second pair, so steps are given them anew."""
-        tables, lens = self._other
-        B.check(B.pkv_fork_sequences(self.block_tables, self.context_lens, parents, self.ref_counts, tables, lens,
+        """Row b becomes what row parents[b] (int32 [num_seqs]) was, or empty (-1)."""
+        tables, lens = self._other  # a fork is not in place: first every row moves there, each its own heir
+        B.check(B.pkv_fork_sequences(self.block_tables, self.context_lens, self._same, self.ref_counts, tables, lens,
                                      self.err_flag, stream))
-        self._other = (self.block_tables, self.context_lens)
-        self.block_tables, self.context_lens = tables, lens
+        B.check(B.pkv_fork_sequences(tables, lens, parents, self.ref_counts, self.block_tables, self.context_lens,
+                                     self.err_flag, stream))
 
     def compact(self, pools=(), stream=None) -> None:
         """The used blocks become the pools' first ones."""

@@ -75,3 +75,45 @@ def test_rows_that_do_not_grow_keep_their_tokens(pkv, N, T):  # noqa: F811
     tol = (2.0 ** -8 + 2 * 576 * 2.0 ** -23 * 0.07 * size[..., None] + 1e-4) * spread + 2.0 ** -7 * np.abs(ref) + 1e-30
     assert np.all(np.abs(out_f64(step.out) - ref) <= tol)
     assert bool((step.out[torch.from_numpy(~grew).cuda()] == 0).all())
+
+
+def test_a_captured_loop_with_beams(pkv):  # noqa: F811
+    """Beams that choose their parents, grow (with copies on write) and step, all in one graph over tensors and a step that were
+    there before: every replay starts from what the last one left."""
+    from paged_kv_decode_slot_gb300.step import LatentDecodeStep, SequenceBlocks
+    r = np.random.default_rng(11)
+    rows, width, blocks, N = 12, 6, 60, 8
+    err = flag()
+    cache = bf16_dev(R.to_bf16(r.standard_normal((blocks, 16, 576))))
+    SequenceBlocks(rows, width, blocks).fork(torch.zeros(rows, dtype=torch.int32, device="cuda"))   # (first use of the kernels)
+    seqs = SequenceBlocks(rows, width, blocks, err_flag=err)
+    kept = (seqs.block_tables, seqs.context_lens)
+    seqs.extend(i32_dev([37, 5, 16, 30] + [0] * 8), [cache])
+    parents, new = i32_dev(np.zeros(rows)), i32_dev(np.ones(rows))
+    fresh = lambda *s: bf16_dev(R.to_bf16(r.standard_normal(s)))
+    step = LatentDecodeStep(fresh(rows, 1, 576), fresh(rows, 1, N, 64), fresh(rows, 1, N, 576), cache, seqs.block_tables, seqs.step_lens, 0.07,
+                            torch.from_numpy(INV).cuda(), err_flag=err)
+    step.run()                                                         # (no row has a step yet: nothing is written)
+    tab, ctx, ref = (host(x).copy() for x in (seqs.block_tables, seqs.context_lens, seqs.ref_counts))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        seqs.fork(parents, stream)
+        seqs.extend(new, [cache], stream)
+        step.run(stream)
+    for k in range(8):
+        parents.copy_(i32_dev(r.integers(-1 if k else 0, rows if k else 4, rows)))
+        new.copy_(i32_dev(r.integers(0, 2, rows)))
+        step.kv_new.copy_(fresh(rows, 1, 576))
+        graph.replay()
+        torch.cuda.synchronize()
+        tab, ctx, ref = L.fork(tab, ctx, host(parents), blocks)
+        old = ctx
+        tab, ctx, ref, _, refused = L.extend(tab, ctx, host(new), ref)
+        assert not refused and err_of(err) == 0
+        for g, w in zip((seqs.block_tables, seqs.context_lens, seqs.ref_counts), (tab, ctx, ref)):
+            np.testing.assert_array_equal(host(g), w, f"replay {k}")
+        want, _, spread, size = L.attention(R.bf16_values(bf16_host(step.q)), out_f64(cache), tab, np.where(ctx > old, ctx, 0), 0.07)
+        tol = (2.0 ** -8 + 2 * 576 * 2.0 ** -23 * 0.07 * size[..., None] + 1e-4) * spread + 2.0 ** -7 * np.abs(want) + 1e-30
+        assert np.all(np.abs(out_f64(step.out) - want) <= tol), f"replay {k}"
+    assert kept[0] is seqs.block_tables and kept[1] is seqs.context_lens
