@@ -632,8 +632,9 @@ size_t pkv_verify_workspace_bytes(int32_t num_seqs, int32_t vocab_size);
    (nullable: T everywhere): the drafted tokens a sequence has, T' = draft_lens[b]; what lies behind them is
    not read.  accept_u, sample_u in [0, 1).  num_accepted int32 [num_seqs]; tokens_out int32
    [num_seqs][T + 1]: the accepted tokens, the drawn one, then -1.  context_lens / context_lens_out int32
-   [num_seqs] (both or neither; may be one array): a context that counts the T' drafted tokens becomes the
-   one that keeps the accepted ones, ctx - T' + num_accepted.  A drafted token outside the vocabulary is
+   [num_seqs] (both or neither; may be one array, but not where the blocks' counts are kept by pkv_extend_sequences and
+   its like, see there): a context that counts the T' drafted tokens becomes the one that keeps the accepted ones, ctx - T' +
+   num_accepted.  A drafted token outside the vocabulary is
    refused and sets PKV_FLAG_TOKEN_RANGE; a row without mass gives token -1 and PKV_FLAG_NO_MASS.
    vocab_size up to 2^19 - 1, num_draft 0 to 1024. */
 int pkv_verify_draft(const void *target_probs, int64_t target_stride, const void *draft_probs,
@@ -710,7 +711,10 @@ int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, cons
  * j < ceil(ctx / 16) of a row count, those behind are not looked at); num_seqs and num_blocks up to 2^31 - 65,537,
  * max_blocks_per_seq up to 33,553,920.  A block with count 0 is free.  The calls below keep the counts; all results are
  * exact and follow from the arguments alone.  Where counts and tables disagree the result is void: disagreements that
- * a call meets set PKV_FLAG_REF_RANGE, nothing outside the given arrays is touched.  Blocks are blocks of every layer's
+ * a call meets set PKV_FLAG_REF_RANGE, nothing outside the given arrays is touched.  Lengths lowered by anything else (a
+ * verification's context_lens_out over context_lens) are such a disagreement that no call meets: the blocks that a row no
+ * longer reaches keep their counts, and are lost.  Two forks shorten rows: one over the shorter lengths in which every row
+ * has two heirs (its blocks gain a holder), then one over the old lengths with num_seqs_out 0 (all their blocks lose one).  Blocks are blocks of every layer's
  * pools (of any kind: K and V, e4m3, latent); what has to be copied is told as pairs for pkv_copy_blocks_pools.
  */
 

@@ -604,8 +604,10 @@ class SequenceBlocks:
     ``context_lens`` int32 [num_seqs] (what the steps take) and ``ref_counts`` int32 [num_blocks].  All rows start empty.  These
     tensors stay the same ones whatever is called, so steps and captured graphs made with them go on.
 
-    ``extend`` before a step makes room for its new tokens, ``fork`` after one lets rows take over others (beams, samples
-    of one prompt, sequences that end), ``compact`` moves blocks to the front of the pools.  ``pools`` are the tensors
+    ``extend`` before a step makes room for its new tokens, ``shorten`` after one takes back those that a verification
+    refused, ``fork`` lets rows take over others (beams, samples of one prompt, sequences that end), ``compact`` moves blocks to
+    the front of the pools.  Nothing else may write the tensors: blocks that a row whose length was lowered no longer reaches
+    would keep their counts for good (``pkv_verify_draft`` writes its lengths elsewhere, and ``shorten`` takes them).  ``pools`` are the tensors
     [num_blocks, ...] of every layer that the tables speak of, in groups of one shape and type.  Nothing is read back: too few
     free blocks, say, shows in ``err_flag`` and in the lengths that did not grow.
 
@@ -624,8 +626,11 @@ class SequenceBlocks:
         self.num_moves = torch.zeros(1, **ints)
         self.err_flag = err_flag
         self.workspace = torch.empty(B.pkv_blocks_workspace_bytes(num_blocks), dtype=torch.uint8, device=device)
-        self._other = (torch.empty_like(self.block_tables), torch.empty_like(self.context_lens))
+        self._two = (torch.empty(2 * num_seqs, max_blocks, **ints), torch.empty(2 * num_seqs, **ints))  # room for every row twice
+        self._other = tuple(t[:num_seqs] for t in self._two)
+        self._none = tuple(t[:0] for t in self._two)
         self._same = torch.arange(num_seqs, **ints)
+        self._twice = torch.cat((self._same, self._same))
 
     def _copy(self, pools, pairs, stream) -> None:
         groups = {}
@@ -648,6 +653,23 @@ class SequenceBlocks:
         B.check(B.pkv_fork_sequences(self.block_tables, self.context_lens, self._same, self.ref_counts, tables, lens,
                                      self.err_flag, stream))
         B.check(B.pkv_fork_sequences(tables, lens, parents, self.ref_counts, self.block_tables, self.context_lens,
+                                     self.err_flag, stream))
+
+    def shorten(self, context_lens, stream=None) -> None:
+        """Row b keeps its first context_lens[b] (int32 [num_seqs], another tensor; at most what it has) tokens, as the
+        ``context_lens_out`` of a verification says; blocks that it needs no more it gives back.  A row that did not grow
+        (``step_lens`` 0) was given a draft length of 0 there, and keeps what it has.  (Longer than the row: its length is void;
+        negative: PKV_FLAG_CTX_RANGE, the row ends.)"""
+        if isinstance(context_lens, torch.Tensor) and context_lens.data_ptr() == self.context_lens.data_ptr():
+            raise ValueError("context_lens must be another tensor than the rows' own")
+        tables, lens = self._two
+        # Two heirs of what a row keeps, one more holder of these blocks; then none of what it had, one holder less.
+        B.check(B.pkv_fork_sequences(self.block_tables, context_lens, self._twice, self.ref_counts, tables, lens, self.err_flag,
+                                     stream))
+        B.check(B.pkv_fork_sequences(self.block_tables, self.context_lens, self._none[1], self.ref_counts, *self._none,
+                                     self.err_flag, stream))
+        tables, lens = self._other
+        B.check(B.pkv_fork_sequences(tables, lens, self._same, self.ref_counts, self.block_tables, self.context_lens,
                                      self.err_flag, stream))
 
     def compact(self, pools=(), stream=None) -> None:

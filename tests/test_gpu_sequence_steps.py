@@ -117,3 +117,108 @@ def test_a_captured_loop_with_beams(pkv):  # noqa: F811
         tol = (2.0 ** -8 + 2 * 576 * 2.0 ** -23 * 0.07 * size[..., None] + 1e-4) * spread + 2.0 ** -7 * np.abs(want) + 1e-30
         assert np.all(np.abs(out_f64(step.out) - want) <= tol), f"replay {k}"
     assert kept[0] is seqs.block_tables and kept[1] is seqs.context_lens
+
+
+def shortened(tab, kept, blocks):
+    tab = tab.copy()
+    for b, n in enumerate(kept):
+        tab[b, -(-int(n) // 16):] = -1
+    return tab, L.counts(tab, kept, blocks)
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("rows,width,blocks", SIZES)
+def test_shorten(pkv, rows, width, blocks, seed):  # noqa: F811
+    """Rows of every kind (some share blocks) keep all, some or none of their tokens."""
+    from paged_kv_decode_slot_gb300.step import SequenceBlocks
+    r = np.random.default_rng(seed)
+    tables, ctx, ref = L.random_rows(r, rows, width, blocks, 0.8)
+    kept = [ctx.copy(), np.zeros_like(ctx), r.integers(0, ctx + 1).astype(np.int32), np.maximum(0, ctx - r.integers(0, 20, rows)).astype(np.int32)][seed]
+    err = flag()
+    seqs = SequenceBlocks(rows, width, blocks, err_flag=err)
+    for t, x in ((seqs.block_tables, tables), (seqs.context_lens, ctx), (seqs.ref_counts, ref)):
+        t.copy_(i32_dev(x))
+    seqs.shorten(i32_dev(kept))
+    tab, counts = shortened(tables, kept, blocks)
+    assert err_of(err) == 0
+    for g, w in zip((seqs.block_tables, seqs.context_lens, seqs.ref_counts), (tab, kept, counts)):
+        np.testing.assert_array_equal(host(g), w)
+
+
+def test_shorten_refuses_the_rows_own_lengths(pkv):  # noqa: F811
+    from paged_kv_decode_slot_gb300.step import SequenceBlocks
+    seqs = SequenceBlocks(3, 2, 9)
+    with pytest.raises(ValueError, match="context_lens"):
+        seqs.shorten(seqs.context_lens)
+    for bad in (i32_dev([0, 0]), torch.zeros(3, dtype=torch.int64, device="cuda"), None):
+        with pytest.raises((TypeError, ValueError)):
+            seqs.shorten(bad)
+
+
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+def test_a_loop_of_drafts_and_verifications_loses_no_block(pkv, captured):  # noqa: F811
+    """Samples of one prompt each draft T tokens, step over all T + 1, and keep what the verification accepts, across block
+    borders and in shared last blocks: after every tick the counts are what the tables say, and no other row's token changed."""
+    from paged_kv_decode_slot_gb300.step import LatentDecodeStep, SequenceBlocks
+    r = np.random.default_rng(captured)
+    rows, width, blocks, N, T, V = 6, 12, 80, 4, 5, 40
+    err = flag()
+    cache = bf16_dev(R.to_bf16(r.standard_normal((blocks, 16, 576))))
+    seqs = SequenceBlocks(rows, width, blocks, err_flag=err)
+    seqs.extend(i32_dev([45, 0, 0, 30, 0, 0]), [cache])
+    seqs.fork(i32_dev([0, 0, 0, 3, 3, -1]))
+    fresh = lambda *s: bf16_dev(R.to_bf16(r.standard_normal(s)))
+    step = LatentDecodeStep(fresh(rows, T + 1, 576), fresh(rows, T + 1, N, 64), fresh(rows, T + 1, N, 576), cache, seqs.block_tables, seqs.step_lens,
+                            0.07, torch.from_numpy(INV).cuda(), err_flag=err)
+    ints = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    new, drafted, lens, kept = i32_dev([T + 1] * 5 + [0]), ints(rows, T), i32_dev([T] * 5 + [0]), ints(rows)
+    probs, u, s = torch.rand(rows, T + 1, V, device="cuda"), torch.rand(rows, T, device="cuda"), torch.rand(rows, device="cuda")
+    accepted, tokens, ws = ints(rows), ints(rows, T + 1), torch.zeros(pkv.pkv_verify_workspace_bytes(rows, V), dtype=torch.uint8, device="cuda")
+    u.fill_(0.3)
+
+    def tick(stream=None):
+        seqs.extend(new, [cache], stream)
+        step.run(stream)
+        pkv.check(pkv.pkv_verify_draft(probs, None, drafted, u, s, accepted, tokens, ws, draft_lens=lens, context_lens=seqs.context_lens,
+                                       context_lens_out=kept, err_flag=err, stream=stream))
+        seqs.shorten(kept, stream)
+    if captured:
+        state = (seqs.block_tables, seqs.context_lens, seqs.ref_counts, cache, step.q)
+        saved = [t.clone() for t in state]
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            tick(stream)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            tick(stream)
+        for t, x in zip(state, saved):
+            t.copy_(x)
+        torch.cuda.synchronize()
+    seen, most = set(), 0
+    for k in range(40):
+        tab, ctx, ref = (host(x).copy() for x in (seqs.block_tables, seqs.context_lens, seqs.ref_counts))
+        rows_of = lambda t, n: [bf16_host(cache)[t[b, :-(-int(n[b]) // 16)]].reshape(-1, 576)[:n[b]] for b in range(rows)]
+        old = rows_of(tab, ctx)
+        probs.copy_(torch.rand(rows, T + 1, V, device="cuda") ** 3)
+        drafted.copy_(torch.randint(0, V, (rows, T), device="cuda", dtype=torch.int32))
+        step.kv_new.copy_(fresh(rows, T + 1, 576))
+        graph.replay() if captured else tick()
+        torch.cuda.synchronize()
+        assert err_of(err) == 0
+        tab, ctx, ref, _, refused = L.extend(tab, ctx, host(new), ref)
+        kept_want = ctx - host(lens) + host(accepted)
+        tab, ref = shortened(tab, kept_want, blocks)
+        assert not refused
+        for g, w in zip((seqs.block_tables, seqs.context_lens, seqs.ref_counts), (tab, kept_want, ref)):
+            np.testing.assert_array_equal(host(g), w, f"tick {k}")
+        for b, now in enumerate(rows_of(tab, kept_want)):
+            np.testing.assert_array_equal(now[:len(old[b])], old[b])
+        seen |= set(host(accepted).tolist())
+        most = max(most, int(kept_want.max()))
+        if most > 16 * width - 2 * (T + 1):
+            break
+    assert len(seen) > 3 and most > 100
+    seqs.fork(i32_dev([-1] * rows))
+    assert not seqs.ref_counts.any()
