@@ -179,7 +179,9 @@ __device__ __forceinline__ bool latent_deal(const LatentAttnParams &p, int cta, 
     w.b = (int)sums[kThreads + 1];
     w.chunk = (int)sums[kThreads + 2];
     w.start = sums[kThreads + 3];
-    __syncthreads();  // (the sums' place is someone else's from here on)
+    // the sums' place is TMA's from here on: what threads read and wrote there comes before its writes
+    fence_proxy_async_shared();
+    __syncthreads();
     return true;
 }
 
