@@ -55,7 +55,7 @@ struct LatentLayout {
     // full[slots], empty[ring], q_full, q_free, s_full[2], p_ready, pv_done, tail[2], fin
     static constexpr int kBars = kSlots + kRing + 9;
     static constexpr int kMiscOffset = (kBarOffset + kBars * 8 + 15) & ~15;
-    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, - */ + 2 * 4 /* a slot's bytes */ + R /* limits */ +
+    static constexpr int kWords = 4 /* tile masks */ + 4 /* abort, tmem, tiles, - */ + 2 * 4 /* - */ + R /* limits */ +
                                   R /* maxima */ + R /* factors */ + 8 * R /* of four warps */;
     static constexpr int kBytes = kMiscOffset + kWords * 4;
     static constexpr int kAlloc = kBytes + 1024;  // room to align the window
@@ -172,6 +172,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     volatile int *const tile_mask = reinterpret_cast<volatile int *>(mem + L::kMiscOffset);  // [4], by tile % 4: blocks there
     volatile int *const abort_flag = tile_mask + 4;
     volatile uint32_t *const tmem_slot = reinterpret_cast<volatile uint32_t *>(tile_mask + 5);
+    volatile int *const tiles_begun = tile_mask + 6;                             // by the MMA thread
     int *const limit = const_cast<int *>(tile_mask + 16);                        // [R] tokens a row sees
     float *const top = reinterpret_cast<float *>(limit + R);                     // [R] running maxima (log2)
     float *const factor = top + R;                                               // [R]
@@ -180,7 +181,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     // What needs nothing of the launch ahead comes before the wait for it.  (Tensor memory too: a CTA that still has to take its own
     // does not fit beside this one's shared memory, so none of that launch waits for what is held here.)
     if (threadIdx.x == 0) {
-        *abort_flag = 0;
+        *abort_flag = 0, *tiles_begun = 0;
         for (int s = 0; s < NS + kRing + 9; ++s) mbar_init(bar_full + 8 * s, s == NS + kRing + 4 ? kLatSoftmaxWarps : 1);
         prefetch_tensormap(&tm_c);
         prefetch_tensormap(&tm_q);
@@ -291,8 +292,15 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             g += sg.t1 - sg.t0;
             const int tail = sg.ctx % kBlockSize;
             if (sg.t1 != sg.tiles || tail == 0) continue;
-            ok = wait(bar_tail, asked++ & 1);
+            // (the limit is of a step of the pipeline, and this wait goes over all tiles of the run up to here: it begins
+            // again while the MMA thread gets on)
+            int begun;
+            do {
+                begun = *tiles_begun;
+                ok = wait(bar_tail, asked & 1);
+            } while (!ok && __any_sync(0xFFFFFFFFu, *tiles_begun != begun) && __all_sync(0xFFFFFFFFu, !*abort_flag));
             if (!ok) break;
+            ++asked;
             const int j = (sg.ctx / kBlockSize) - (sg.tiles - 1) * NB;
             const uint32_t blk = ring + ((int)((g - 1) % NS) * NB + j) * kLatBlock;
             // 16-byte units of the values' eight chunks
@@ -349,6 +357,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     ok = wait_one(bar_full + 8 * slot, parity);
                     if (!ok) break;
                     tc_fence_after();
+                    *tiles_begun = (int)g + 1;
                     const uint32_t d = tm_s + R * (g & 1);
                     const uint64_t a = k_desc + (uint32_t)(slot * NB * (kLatBlock >> 4));
 #pragma unroll
