@@ -682,7 +682,7 @@ class SequenceBlocks:
 class LayerStack:
     """One decode step of a model with several attention layers: the same sequences (block tables
     and context lengths) in every layer, each layer with its own pools and its own q, k_new and
-    v_new.  ``run`` launches the layers' fused steps in order (one launch each, two with a
+    v_new (kv_new, q_rope and q over latent caches).  ``run`` launches the layers' fused steps in order (one launch each, two with a
     separate merge); captured in a CUDA graph (``StepGraph``) the whole multi-layer step replays
     as one graph launch.  Attribute names ``"<name>.<layer>"`` (``"q.3"``) reach one layer's
     inputs, ``block_tables`` / ``context_lens`` are shared, ``out`` / ``lse`` are the last
@@ -727,7 +727,10 @@ class LayerStack:
         return sum(layer.launches_per_step() for layer in self.layers)
 
     def input_names(self):
-        return self._SHARED + tuple(f"{n}.{i}" for i in range(len(self.layers)) for n in ("q", "k_new", "v_new"))
+        # (a step with q, k_new and v_new: those, not the groups of a shared prefix, which are the batch's)
+        own = lambda layer: [n for n in layer.input_names() if n not in self._SHARED]
+        return self._SHARED + tuple(f"{n}.{i}" for i, layer in enumerate(self.layers)
+                                    for n in (("q", "k_new", "v_new") if hasattr(layer, "k_new") else own(layer)))
 
     def inputs(self):
         return [getattr(self, n) for n in self.input_names()]
