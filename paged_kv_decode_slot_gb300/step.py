@@ -740,14 +740,17 @@ class StepGraph:
     """A step (or a LayerStack) captured once into a CUDA graph and replayed: the launches of all
     its kernels cost one graph launch.  The step is run once eagerly first (kernel attributes are
     set on first use, outside the capture); a decode step is idempotent for fixed inputs (the same
-    rows land in the same slots), so that run changes nothing the replay would not."""
+    rows land in the same slots), so that run changes nothing the replay would not.  One that is not
+    (rows that grow or fork in it, queries turned in place) would take that run as a step of its own:
+    the caller runs its first one eagerly, and ``warm_up`` False captures it without another."""
 
-    def __init__(self, step, stream=None):
+    def __init__(self, step, stream=None, warm_up: bool = True):
         dev = step.out.device
         self.step = step
         self.stream = stream or torch.cuda.Stream(dev)
-        with torch.cuda.stream(self.stream):
-            step.run(self.stream)
+        if warm_up:
+            with torch.cuda.stream(self.stream):
+                step.run(self.stream)
         torch.cuda.synchronize(dev)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph, stream=self.stream):

@@ -222,3 +222,36 @@ def test_a_loop_of_drafts_and_verifications_loses_no_block(pkv, captured):  # no
     assert len(seen) > 3 and most > 100
     seqs.fork(i32_dev([-1] * rows))
     assert not seqs.ref_counts.any()
+
+
+def test_a_step_that_grows_its_rows_is_captured_without_a_run(pkv):  # noqa: F811
+    """The first step run eagerly, the others replayed: what the same number of eager steps gives."""
+    from paged_kv_decode_slot_gb300.step import LatentDecodeStep, SequenceBlocks, StepGraph
+    r = np.random.default_rng(2)
+    fresh = lambda *s: bf16_dev(R.to_bf16(r.standard_normal(s)))
+    base, kv, rope, absorbed = fresh(40, 16, 576), fresh(4, 1, 576), fresh(4, 1, 8, 64), fresh(4, 1, 8, 576)
+
+    class Tick:
+        def __init__(self):
+            self.seqs, self.cache, self.ones = SequenceBlocks(4, 6, 40), base.clone(), i32_dev([1] * 4)
+            self.seqs.extend(i32_dev([5, 31, 0, 47]), [self.cache])
+            q = absorbed.clone()
+            q[..., 512:] = rope                                        # turned in place
+            self.step = LatentDecodeStep(kv, q[..., 512:], q, self.cache, self.seqs.block_tables, self.seqs.step_lens, 0.07, torch.from_numpy(INV).cuda())
+            self.out = self.step.out
+
+        def run(self, stream=None):
+            self.seqs.extend(self.ones, [self.cache], stream)
+            self.step.run(stream)
+    one, other = Tick(), Tick()
+    one.run()
+    graph = StepGraph(one, warm_up=False)
+    for _ in range(4):
+        graph.replay()
+    for _ in range(5):
+        other.run()
+    torch.cuda.synchronize()
+    assert one.seqs.context_lens.tolist() == [10, 36, 5, 52]
+    for a, b in ((one.seqs.block_tables, other.seqs.block_tables), (one.seqs.context_lens, other.seqs.context_lens),
+                 (one.seqs.ref_counts, other.seqs.ref_counts), (one.cache, other.cache), (one.step.q, other.step.q), (one.out, other.out)):
+        assert same(a, b)
