@@ -255,3 +255,22 @@ def test_a_step_that_grows_its_rows_is_captured_without_a_run(pkv):  # noqa: F81
     for a, b in ((one.seqs.block_tables, other.seqs.block_tables), (one.seqs.context_lens, other.seqs.context_lens),
                  (one.seqs.ref_counts, other.seqs.ref_counts), (one.cache, other.cache), (one.step.q, other.step.q), (one.out, other.out)):
         assert same(a, b)
+
+
+@pytest.mark.parametrize("count", [0, -1, -7])
+@pytest.mark.parametrize("blocks", [6, 40000], ids=["one CTA", "cluster"])
+def test_counts_too_low_are_flagged(pkv, count, blocks):  # noqa: F811
+    """A row that grows into a partly filled block whose count knows no holder; one that grows into a fresh block does not look at
+    its others' counts; a fork that gives up a block without holders."""
+    ref = np.zeros(blocks, dtype=np.int32)
+    ref[:3] = [1, count, 1]
+    tables = np.array([[0, -1], [1, -1], [2, -1]], dtype=np.int32)
+    for ctx, new, want in (([5, 5, 5], [1, 1, 1], pkv.PKV_FLAG_REF_RANGE), ([5, 5, 5], [1, 0, 1], 0), ([5, 16, 5], [1, 0, 1], 0)):
+        d, copies, err = [i32_dev(x) for x in (tables, ctx, new, ref)], torch.zeros(3, 2, dtype=torch.int32, device="cuda"), flag()
+        pkv.check(pkv.pkv_extend_sequences(*d, copies, workspace(pkv, blocks), err))
+        assert err_of(err) == want, (ctx, new)
+    out, lens = torch.zeros(3, 2, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    for parents, want in (([0, -1, 2], pkv.PKV_FLAG_REF_RANGE), ([0, 1, 2], 0)):
+        err = flag()
+        pkv.check(pkv.pkv_fork_sequences(i32_dev(tables), i32_dev([5, 5, 5]), i32_dev(parents), i32_dev(ref), out, lens, err))
+        assert err_of(err) == want, parents
