@@ -1240,6 +1240,12 @@ def pkv_extend_sequences(block_tables, context_lens, num_new, ref_counts, copies
                                           _maybe(err_flag, _i32, _FLAG, "err_flag", dev), _launch(stream, dev))
 
 
+def pkv_extend_sequences_step(block_tables, context_lens, num_new, ref_counts, copies, step_lens, workspace, err_flag=None,
+                              stream=None) -> int:
+    """pkv_extend_sequences with the lengths for the step, in the entry point's order."""
+    return pkv_extend_sequences(block_tables, context_lens, num_new, ref_counts, copies, workspace, err_flag, stream, step_lens)
+
+
 def pkv_compact_blocks(block_tables, context_lens, ref_counts, moves, num_moves, workspace, err_flag=None,
                        stream=None) -> int:
     """Blocks moved towards the front: moves int32 [max_moves, 2] and num_moves int32 [1] (written), block_tables [B, W]

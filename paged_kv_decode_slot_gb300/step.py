@@ -643,8 +643,8 @@ class SequenceBlocks:
     def extend(self, num_new, pools=(), stream=None) -> None:
         """Row b grows by num_new[b] (int32 [num_seqs]) tokens; shared last blocks are copied on write in ``pools``;
         ``step_lens`` says which rows grew."""
-        B.check(B.pkv_extend_sequences(self.block_tables, self.context_lens, num_new, self.ref_counts, self.copies,
-                                       self.workspace, self.err_flag, stream, self.step_lens))
+        B.check(B.pkv_extend_sequences_step(self.block_tables, self.context_lens, num_new, self.ref_counts, self.copies,
+                                            self.step_lens, self.workspace, self.err_flag, stream))
         self._copy(pools, self.copies, stream)
 
     def fork(self, parents, stream=None) -> None:

@@ -274,3 +274,14 @@ def test_counts_too_low_are_flagged(pkv, count, blocks):  # noqa: F811
         err = flag()
         pkv.check(pkv.pkv_fork_sequences(i32_dev(tables), i32_dev([5, 5, 5]), i32_dev(parents), i32_dev(ref), out, lens, err))
         assert err_of(err) == want, parents
+
+
+def test_the_binding_names_what_is_wrong_with_the_lengths_for_the_step(pkv):  # noqa: F811
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    tab, ctx, new, ref, copies, ws = i32(2, 4), i32(2), i32(2), i32(9), i32(2, 2), workspace(pkv, 9)
+    call = lambda lens: pkv.pkv_extend_sequences_step(tab, ctx, new, ref, copies, lens, ws)
+    assert call(i32(2)) == 0 and call(None) == 0 and call(torch.zeros(2, dtype=torch.int32).pin_memory()) == 0
+    assert call(ctx) == pkv.PKV_ERR_SHAPE and call(new) == pkv.PKV_ERR_SHAPE
+    for bad in (i32(3), i32(2, 1), i32(2).long(), torch.zeros(2, dtype=torch.int32), i32(4)[::2]):
+        with pytest.raises((TypeError, ValueError), match="step_lens"):
+            call(bad)
