@@ -694,7 +694,8 @@ size_t pkv_latent_workspace_bytes(int32_t num_seqs, int32_t num_new, int32_t num
    sequence is cut into, and so the last bits of its result, depend on the other sequences of the batch.  Softmax weights
    are rounded to bf16 before they multiply the values and sum to one as rounded: equal values come back as they are, and
    out is off by up to 2^-8 of sum softmax |c - out| beside its own rounding; lse_out is of the weights as they are.  Two
-   launches (the second joins what was cut).  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left out.  Whatever lies
+   launches (the second joins what was cut).  Sums are fp32 and relative to a logit up to 2^32 below the row's largest: latent
+   elements above 2^78 in magnitude may overflow.  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left out.  Whatever lies
    behind a sequence's end in its last block is not read as a value, infinities and NaN included.  The num_new tokens themselves
    multiply all rows of their sequence, those that do not see them with weight 0: an infinity or NaN in one of their latent
    vectors makes its elements NaN in the rows before it too. */

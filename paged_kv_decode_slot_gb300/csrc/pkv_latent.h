@@ -21,9 +21,9 @@ struct LatentPlan {
     int64_t chunks;
     int ctas() const { return chunk_rows == 128 ? 2 : 1; }
 };
-// The narrowest that holds a sequence's rows (64 sequences of 512 to 8,192 tokens: 62 us with 16 rows, 65 with 32, 68 with 48 and
-// 70 with 64 by pairs).  A CTA has room for 48 rows too: no faster than a pair (three new tokens of 16 heads over 20 sequences
-// of up to 32,520 tokens 82 us for 76, 5 short sequences 17 for 15), and not kept.
+// The narrowest that holds a sequence's rows (64 sequences of 512 to 8,192 tokens: 63 us with 16 rows, 66 with 32, by pairs 69
+// with 48 and 71 with 64).  48 rows by one CTA were no faster than by a pair (three new tokens of 16 heads over 20 sequences of
+// up to 32,520 tokens 82 us for 76, 5 short sequences 17 for 15).
 inline LatentPlan latent_plan(int64_t rows)
 {
     LatentPlan p;

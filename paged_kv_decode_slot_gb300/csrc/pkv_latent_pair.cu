@@ -30,8 +30,8 @@
 //
 // Bound by how soon a slot of keys is filled again (the MMA thread's own work takes 2,600 clocks a tile, the tiles 2,600 to
 // 3,700, with DRAM, L2 and the tensor pipe busy for half to two thirds of it) and by what a unit costs beside its tiles
-// (prologue, exchange, outputs and join, about 20 us of the 76): 152 sequences of 4,096 tokens and 128 heads take 135 to 140 us, 5.4
-// TB/s and 1.25 PFLOP/s; 64 of 512 to 8,192 tokens 76 us, with 64 heads 70; one of 131,072 tokens 43.  Tiles of 256 tokens with both
+// (prologue, exchange, outputs and join, about 20 us of the 77): 152 sequences of 4,096 tokens and 128 heads take 135 to 144 us, 5.2
+// TB/s and 1.2 PFLOP/s; 64 of 512 to 8,192 tokens 77 us, with 64 heads 71; one of 131,072 tokens 43.  Tiles of 256 tokens with both
 // products as M = 256 took 134 us for the 64 sequences: each CTA then needs half of the other's weights in every tile, and 72
 // KB of queries leave 96 KB for 278 KB of loads a tile.
 #include "pkv_cluster.cuh"
