@@ -633,8 +633,8 @@ size_t pkv_verify_workspace_bytes(int32_t num_seqs, int32_t vocab_size);
    not read.  accept_u, sample_u in [0, 1).  num_accepted int32 [num_seqs]; tokens_out int32
    [num_seqs][T + 1]: the accepted tokens, the drawn one, then -1.  context_lens / context_lens_out int32
    [num_seqs] (both or neither; may be one array, but not where the blocks' counts are kept by pkv_extend_sequences and
-   its like, see there): a context that counts the T' drafted tokens becomes the one that keeps the accepted ones, ctx - T' +
-   num_accepted.  A drafted token outside the vocabulary is
+   its like, see there): a context that counts the T' drafted tokens becomes the one that keeps the accepted ones,
+   ctx - T' + num_accepted.  A drafted token outside the vocabulary is
    refused and sets PKV_FLAG_TOKEN_RANGE; a row without mass gives token -1 and PKV_FLAG_NO_MASS.
    vocab_size up to 2^19 - 1, num_draft 0 to 1024. */
 int pkv_verify_draft(const void *target_probs, int64_t target_stride, const void *draft_probs,
@@ -695,8 +695,8 @@ size_t pkv_latent_workspace_bytes(int32_t num_seqs, int32_t num_new, int32_t num
    are rounded to bf16 before they multiply the values and sum to one as rounded: equal values come back as they are, and
    out is off by up to 2^-8 of sum softmax |c - out| beside its own rounding; lse_out is of the weights as they are.  Two
    launches (the second joins what was cut).  Sums are fp32 and relative to a logit up to 2^32 below the row's largest: latent
-   elements above 2^78 in magnitude may overflow.  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left out.  Whatever lies
-   behind a sequence's end in its last block is not read as a value, infinities and NaN included.  The num_new tokens themselves
+   elements above 2^78 in magnitude may overflow.  A block id outside the pool sets PKV_FLAG_BLOCK_RANGE, its tokens are left
+   out.  Whatever lies behind a sequence's end in its last block is not read as a value, infinities and NaN included.  The num_new tokens themselves
    multiply all rows of their sequence, those that do not see them with weight 0: an infinity or NaN in one of their latent
    vectors makes its elements NaN in the rows before it too. */
 int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, const int32_t *block_tables,
@@ -715,8 +715,8 @@ int pkv_decode_attn_latent(const pkv_bf16 *q, const pkv_bf16 *latent_cache, cons
  * a call meets set PKV_FLAG_REF_RANGE, nothing outside the given arrays is touched.  Lengths lowered by anything else (a
  * verification's context_lens_out over context_lens) are such a disagreement that no call meets: the blocks that a row no
  * longer reaches keep their counts, and are lost.  Two forks shorten rows: one over the shorter lengths in which every row
- * has two heirs (its blocks gain a holder), then one over the old lengths with num_seqs_out 0 (all their blocks lose one).  Blocks are blocks of every layer's
- * pools (of any kind: K and V, e4m3, latent); what has to be copied is told as pairs for pkv_copy_blocks_pools.
+ * has two heirs (its blocks gain a holder), then one over the old lengths with num_seqs_out 0 (all their blocks lose one).
+ * Blocks are blocks of every layer's pools (of any kind: K and V, e4m3, latent); what has to be copied is told as pairs for pkv_copy_blocks_pools.
  */
 
 /* Row b of a new batch takes over row parents[b] of the old one, or (-1) starts empty: forks (several rows with one

@@ -682,8 +682,8 @@ class SequenceBlocks:
 class LayerStack:
     """One decode step of a model with several attention layers: the same sequences (block tables
     and context lengths) in every layer, each layer with its own pools and its own q, k_new and
-    v_new (kv_new, q_rope and q over latent caches).  ``run`` launches the layers' fused steps in order (one launch each, two with a
-    separate merge); captured in a CUDA graph (``StepGraph``) the whole multi-layer step replays
+    v_new (kv_new, q_rope and q over latent caches).  ``run`` launches the layers' fused steps in
+    order (one launch each, two with a separate merge); captured in a CUDA graph (``StepGraph``) the whole multi-layer step replays
     as one graph launch.  Attribute names ``"<name>.<layer>"`` (``"q.3"``) reach one layer's
     inputs, ``block_tables`` / ``context_lens`` are shared, ``out`` / ``lse`` are the last
     layer's; so ``PackedInputs(stack, stack.input_names())`` packs every layer's inputs into one
